@@ -197,7 +197,7 @@ def prepare(case, seed):
         from exact_attention_72_gb300 import binding
         s["handle"] = binding.PagedKVCache(s["k"], s["v"], s.get("k_sz"), s.get("v_sz"))
         if case["op"] == "attend":
-            n = binding.attn_fwd_paged_workspace_bytes(case["B"], case["H"], case["Hkv"], case["Nq"], d)
+            n = binding.attn_fwd_paged_workspace_bytes(s["handle"], case["B"], case["H"], case["Nq"])
             s["workspace"] = torch.empty(n, dtype=torch.uint8, device="cuda")
     return s
 
