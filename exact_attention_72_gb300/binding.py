@@ -18,6 +18,9 @@ ATTN_DTYPE_BF16, ATTN_DTYPE_FP8_E4M3 = 0, 1
 STATUS_NAMES = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED", 3: "ATTN_ERR_CUDA",
                 4: "ATTN_ERR_TIMEOUT"}
 
+ATTN_CACHE_BF16, ATTN_CACHE_INT4 = 0, 1
+ATTN_INT4_GROUP = 64     # dims per (scale, zero) pair of a 4-bit cache
+
 _LIB = None
 
 
@@ -25,6 +28,14 @@ class AttnError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {STATUS_NAMES.get(status, status)}")
         self.status = status
+
+
+class _PagedCacheStruct(ctypes.Structure):
+    """attn_paged_cache_t"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_sz", "v_sz")] + \
+        [(n, ctypes.c_longlong) for n in ("page_stride", "token_stride", "head_stride", "sz_page_stride",
+                                          "sz_token_stride", "sz_head_stride")] + \
+        [(n, ctypes.c_int) for n in ("num_pages", "page_size", "Hkv", "d", "type")]
 
 
 def lib_path() -> str:
@@ -77,6 +88,22 @@ def lib() -> ctypes.CDLL:
     L.attn_fwd_splitkv_workspace_bytes.argtypes = [i, i, i, i, i]
     L.attn_fwd_host_workspace_bytes.restype = sz
     L.attn_fwd_host_workspace_bytes.argtypes = [i, i, i, i, i, i]
+    ll, cache = ctypes.c_longlong, ctypes.POINTER(_PagedCacheStruct)
+    L.attn_qk_norm_rope.restype = i
+    L.attn_qk_norm_rope.argtypes = [vp] * 4 + [i] * 4 + [ll] * 4 + [i, vp, vp, f, vp, vp, i, i, i, vp, i, vp]
+    L.attn_qk_norm_rope_bwd_workspace_bytes.restype = sz
+    L.attn_qk_norm_rope_bwd_workspace_bytes.argtypes = [i, i, i, i]
+    L.attn_qk_norm_rope_bwd.restype = i
+    L.attn_qk_norm_rope_bwd.argtypes = [vp] * 8 + [i] * 4 + [ll] * 4 + [i, vp, vp, f, vp, vp, i, i, i, vp, i, vp, sz,
+                                                                       vp]
+    L.attn_paged_append.restype = i
+    L.attn_paged_append.argtypes = [cache, vp, vp, ll, ll, ll, ll, vp, vp, vp, ll, i, i, i, vp, vp, i, i, i, vp]
+    L.attn_paged_gather.restype = i
+    L.attn_paged_gather.argtypes = [cache, vp, vp, vp, vp, ll, i, i, i, vp]
+    L.attn_fwd_paged_workspace_bytes.restype = sz
+    L.attn_fwd_paged_workspace_bytes.argtypes = [i, i, i, i, i, i]
+    L.attn_fwd_paged.restype = i
+    L.attn_fwd_paged.argtypes = [vp, cache, vp, vp, vp, ll, i, vp, i, i, i, f, i, vp, sz, vp]
     L.attn_get_status.restype = i
     L.attn_get_status.argtypes = [vp]
     L.attn_get_status_detail.restype = i
@@ -466,6 +493,331 @@ def attn_fwd_host(q, k, v, out, lse, causal: bool, workspace, scale: Optional[fl
 
 def attn_fwd_host_workspace_bytes(B: int, H: int, Hkv: int, N: int, d: int, dtype_code: int) -> int:
     return int(lib().attn_fwd_host_workspace_bytes(B, H, Hkv, N, d, dtype_code))
+
+
+def _on_current_device(tensors):
+    """Kernels launch on the current device: its tensors only."""
+    import torch
+    dev = None
+    for name, t in tensors:
+        if t is None:
+            continue
+        if t.is_cuda and dev is None:
+            dev = torch.cuda.current_device()
+        if not t.is_cuda or t.device.index != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on the current device")
+
+
+def _buffer(shape, dtype, device, stream):
+    """A tensor the call makes for itself, allocated for the stream that it runs on."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(name, t, heads=None, d=None):
+    """(tokens, token stride, head stride) of bf16 rows [T, heads, d] or [B, N, heads, d], last dim contiguous."""
+    import torch
+    if t.dtype != torch.bfloat16 or t.dim() not in (3, 4) or t.stride(-1) != 1:
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor [T, heads, d] or [B, N, heads, d] with contiguous rows")
+    if heads is not None and (t.shape[-2], t.shape[-1]) != (heads, d):
+        raise ValueError(f"{name} must have {heads} heads of {d} values")
+    if t.dim() == 3:
+        return t.shape[0], t.stride(0), t.stride(1)
+    B, N = t.shape[:2]
+    if N == 1:
+        return B, t.stride(0), t.stride(2)
+    if B > 1 and t.stride(0) != N * t.stride(1):
+        raise ValueError(f"the tokens of {name} must be evenly spaced over the batch")
+    return B * N, t.stride(1), t.stride(2)
+
+
+def _rope_args(cos, sin, d):
+    """(cos pointer, sin pointer, rope_dim, max_pos) of angle tables [max_pos, rope_dim / 2]."""
+    import torch
+    if cos is None and sin is None:
+        return 0, 0, 0, 0
+    for name, t in (("cos", cos), ("sin", sin)):
+        if t is None or t.dtype != torch.float32 or t.dim() != 2 or not t.is_contiguous() or t.shape != cos.shape:
+            raise ValueError(f"{name} must be a contiguous float32 CUDA tensor [max_pos, rope_dim / 2], as its partner")
+    return cos.data_ptr(), sin.data_ptr(), 2 * cos.shape[1], cos.shape[0]
+
+
+def _norm_rope_args(q, k, cos, sin, positions, wq, wk, norm):
+    """Checks that the forward and the backward share; (T, H, Hkv, d, strides, weights, rope, positions, seq_len)."""
+    import torch
+    H, d = q.shape[-2:]
+    Hkv = 0
+    T, q_st, q_sh = _rows("q", q)
+    k_st = k_sh = 0
+    if k is not None:
+        if k.shape[:-2] != q.shape[:-2]:
+            raise ValueError("q and k must hold the same tokens")
+        Hkv = k.shape[-2]
+        _, k_st, k_sh = _rows("k", k, Hkv, d)
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None and (w.dtype != torch.float32 or w.shape != (d,) or not w.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of d values")
+    if wk is not None and k is None:
+        raise ValueError("wk needs k")
+    if positions is not None and (positions.dtype != torch.int32 or positions.shape != q.shape[:-2] or
+                                  not positions.is_contiguous()):
+        raise ValueError("positions must be a contiguous int32 CUDA tensor, one per token")
+    _on_current_device((("q", q), ("k", k), ("cos", cos), ("sin", sin), ("positions", positions), ("wq", wq),
+                        ("wk", wk)))
+    c, s, rope_dim, max_pos = _rope_args(cos, sin, d)
+    seq_len = q.shape[1] if q.dim() == 4 else T
+    tail = (int(bool(norm)), wq.data_ptr() if wq is not None else None, wk.data_ptr() if wk is not None else None)
+    return T, H, Hkv, d, (q_st, q_sh, k_st, k_sh), tail, (c, s, rope_dim, max_pos), \
+        positions.data_ptr() if positions is not None else None, seq_len
+
+
+def _out_rows(name, t, like, stream):
+    """An output with the shape of ``like``, contiguous: ``t`` if given."""
+    import torch
+    if t is None:
+        return _buffer(tuple(like.shape), torch.bfloat16, like.device, stream)
+    if t.shape != like.shape or t.dtype != torch.bfloat16 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor of shape {tuple(like.shape)}")
+    _on_current_device(((name, t),))
+    return t
+
+
+def attn_qk_norm_rope(q, k=None, cos=None, sin=None, positions=None, wq=None, wk=None, eps: float = 1e-6,
+                      norm: bool = True, interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """RMS norm of every head of q and k, then the rotation by position, in one pass: (q_out, k_out).
+
+    q is bf16 [B, N, H, d] or [T, H, d] (k the same with its heads, or None); rows are contiguous, token
+    and head strides free, so both may be parts of a fused projection. ``cos`` and ``sin`` (float32
+    [max_pos, rope_dim / 2]; None: no rotation) give the angles of the pairs (i, i + rope_dim / 2), or
+    (2i, 2i + 1) with ``interleaved``. ``positions`` (int32, one per token) defaults to the index
+    in the sequence. ``wq`` and ``wk`` (float32 [d]) weigh the normalised values; ``norm=False`` only
+    rotates. Outputs are contiguous; each may be its own contiguous input.
+    """
+    T, H, Hkv, d, strides, tail, rope, pos, seq_len = _norm_rope_args(q, k, cos, sin, positions, wq, wk, norm)
+    if k is None and k_out is not None:
+        raise ValueError("k_out needs k")
+    q_out = _out_rows("q_out", q_out, q, stream)
+    if k is not None:
+        k_out = _out_rows("k_out", k_out, k, stream)
+    if T == 0:
+        return q_out, k_out
+    st = lib().attn_qk_norm_rope(q.data_ptr(), k.data_ptr() if k is not None else None, q_out.data_ptr(),
+                                 k_out.data_ptr() if k is not None else None, T, H, Hkv, d, *strides, *tail,
+                                 float(eps), *rope, int(bool(interleaved)), pos, seq_len, _stream_handle(stream))
+    _check(st, "attn_qk_norm_rope")
+    return q_out, k_out
+
+
+def attn_qk_norm_rope_bwd_workspace_bytes(T: int, H: int, Hkv: int, d: int) -> int:
+    return int(lib().attn_qk_norm_rope_bwd_workspace_bytes(T, H, Hkv, d))
+
+
+def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out=None, cos=None, sin=None, positions=None, wq=None, wk=None,
+                          eps: float = 1e-6, norm: bool = True, interleaved: bool = False, dq=None, dk=None, dwq=None,
+                          dwk=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dwq, dwk) of attn_qk_norm_rope for the gradients of its outputs (contiguous, e.g.
+    from attn_bwd); dwq and dwk are float32 [d], None without weights. dq and dk may be dq_out and dk_out."""
+    import torch
+    T, H, Hkv, d, strides, tail, rope, pos, seq_len = _norm_rope_args(q, k, cos, sin, positions, wq, wk, norm)
+    for name, g, x in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
+        if (g is None) != (x is None) or (g is not None and (g.shape != x.shape or g.dtype != torch.bfloat16 or
+                                                             not g.is_contiguous())):
+            raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor like its input")
+    if (dk is not None and k is None) or (dwq is not None and wq is None) or (dwk is not None and wk is None):
+        raise ValueError("dk needs k, dwq needs wq and dwk needs wk")
+    _on_current_device((("dq_out", dq_out), ("dk_out", dk_out)))
+    dq = _out_rows("dq", dq, q, stream)
+    if k is not None:
+        dk = _out_rows("dk", dk, k, stream)
+    ptrs = []
+    grads = []
+    for name, g, w in (("dwq", dwq, wq), ("dwk", dwk, wk)):
+        if w is not None and g is None:
+            g = _buffer((d,), torch.float32, q.device, stream)
+        elif g is not None:
+            if g.dtype != torch.float32 or g.shape != (d,) or not g.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of d values")
+            _on_current_device(((name, g),))
+        grads.append(g)
+        ptrs.append(None if g is None else g.data_ptr())
+    if T == 0:
+        for g in grads:
+            if g is not None:
+                with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+                    g.zero_()
+        return dq, dk, grads[0], grads[1]
+    if workspace is None:
+        if wq is not None or wk is not None:
+            workspace = _buffer((attn_qk_norm_rope_bwd_workspace_bytes(T, H, Hkv, d),), torch.uint8, q.device, stream)
+    else:
+        _on_current_device((("workspace", workspace),))
+    ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    st = lib().attn_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr() if k is not None else None, dq_out.data_ptr(),
+                                     dk_out.data_ptr() if k is not None else None, dq.data_ptr(),
+                                     dk.data_ptr() if k is not None else None, *ptrs, T, H, Hkv, d, *strides, *tail,
+                                     float(eps), *rope, int(bool(interleaved)), pos, seq_len, *ws,
+                                     _stream_handle(stream))
+    _check(st, "attn_qk_norm_rope_bwd")
+    return dq, dk, grads[0], grads[1]
+
+
+class PagedKVCache:
+    """A paged key/value cache over the caller's tensors.
+
+    bf16: k, v bfloat16 [num_pages, page_size, Hkv, d]. 4 bits: k, v uint8 [num_pages, page_size, Hkv, d / 2] and
+    k_sz, v_sz bfloat16 [num_pages, page_size, Hkv, d / 64, 2], (scale, zero) pairs. The first three dims may be
+    strided in any order (k as v, k_sz as v_sz); ``allocate`` keeps the rows of one page and head together. Pages
+    are used as the page tables of the calls say; page_size is a multiple of 16.
+    """
+
+    def __init__(self, k, v, k_sz=None, v_sz=None):
+        import torch
+        four = k_sz is not None
+        if four != (v_sz is not None):
+            raise ValueError("a 4-bit cache has both k_sz and v_sz")
+        want = torch.uint8 if four else torch.bfloat16
+        for name, t in (("k", k), ("v", v)):
+            if t.dtype != want or t.dim() != 4 or t.stride(-1) != 1 or t.shape != k.shape or t.stride() != k.stride() or \
+                    not t.is_cuda or t.device != k.device:
+                raise ValueError(f"{name} must be a {want} CUDA tensor [num_pages, page_size, Hkv, row] with contiguous "
+                                 "rows, k and v alike")
+        P, S, Hkv, row = k.shape
+        d = 2 * row if four else row
+        sz = (0, 0, 0)
+        if four:
+            for name, t in (("k_sz", k_sz), ("v_sz", v_sz)):
+                if t.dtype != torch.bfloat16 or t.shape != (P, S, Hkv, d // ATTN_INT4_GROUP, 2) or \
+                        t.stride() != k_sz.stride() or t.stride(-1) != 1 or \
+                        (t.shape[3] > 1 and t.stride(3) != 2) or t.device != k.device:
+                    raise ValueError(f"{name} must be a bfloat16 CUDA tensor [num_pages, page_size, Hkv, d / 64, 2] with "
+                                     "contiguous rows, k_sz and v_sz alike")
+            sz = k_sz.stride()[:3]
+        self.k, self.v, self.k_sz, self.v_sz = k, v, k_sz, v_sz
+        self.num_pages, self.page_size, self.Hkv, self.d = P, S, Hkv, d
+        self.type = ATTN_CACHE_INT4 if four else ATTN_CACHE_BF16
+        self.device = k.device
+        self._struct = _PagedCacheStruct(k.data_ptr(), v.data_ptr(), k_sz.data_ptr() if four else None,
+                                         v_sz.data_ptr() if four else None, *k.stride()[:3], *sz, P, S, Hkv, d,
+                                         self.type)
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def allocate(cls, num_pages: int, page_size: int, Hkv: int, d: int, cache_type: str = "bf16", device="cuda"):
+        """A cache of zeros, ``cache_type`` "bf16" or "int4"."""
+        import torch
+        if cache_type not in ("bf16", "int4"):
+            raise ValueError("cache_type must be 'bf16' or 'int4'")
+
+        def make(*row, dtype):
+            return torch.zeros((num_pages, Hkv, page_size, *row), dtype=dtype, device=device).transpose(1, 2)
+        if cache_type == "bf16":
+            return cls(make(d, dtype=torch.bfloat16), make(d, dtype=torch.bfloat16))
+        return cls(make(d // 2, dtype=torch.uint8), make(d // 2, dtype=torch.uint8),
+                   make(d // ATTN_INT4_GROUP, 2, dtype=torch.bfloat16),
+                   make(d // ATTN_INT4_GROUP, 2, dtype=torch.bfloat16))
+
+
+def _paged_args(cache, page_table, **vectors):
+    """Checks of a call on ``cache``: the page table and int32 vectors (name=(tensor, length or None)). The batch B."""
+    import torch
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1 and page_table.shape[1] > 1:
+        raise ValueError("page_table must be an int32 CUDA tensor [B, max_pages] with contiguous rows")
+    B = page_table.shape[0]
+    for name, (t, extra) in vectors.items():
+        if t.dtype != torch.int32 or t.shape != (B + extra,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {B + extra} values")
+    _on_current_device([("cache", cache.k), ("page_table", page_table)] + [(n, t) for n, (t, _) in vectors.items()])
+    return B
+
+
+def attn_paged_append(cache: PagedKVCache, k, v, cu_seqlens, cache_lens, page_table, cos=None, sin=None,
+                      interleaved: bool = False, stream=None) -> None:
+    """Stores new keys and values k, v (bf16 [total, Hkv, d], token and head strides free) in ``cache``.
+
+    Packed token cu_seqlens[b] + i becomes position cache_lens[b] + i of sequence b, on page
+    page_table[b, position // page_size]. Keys are rotated by the tables' angles at their position on the
+    way (cos and sin as in attn_qk_norm_rope; None: k is stored as it is). Tokens from cu_seqlens[B] on are
+    not stored. Lengths stay as they are: the caller advances cache_lens.
+    """
+    B = _paged_args(cache, page_table, cu_seqlens=(cu_seqlens, 1), cache_lens=(cache_lens, 0))
+    if k.dim() != 3 or v.dim() != 3 or k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must be [total, Hkv, d]")
+    total, k_st, k_sh = _rows("k", k, cache.Hkv, cache.d)
+    _, v_st, v_sh = _rows("v", v, cache.Hkv, cache.d)
+    _on_current_device((("k", k), ("v", v), ("cos", cos), ("sin", sin)))
+    c, s, rope_dim, max_pos = _rope_args(cos, sin, cache.d)
+    if total == 0 or B == 0:
+        return
+    st = lib().attn_paged_append(cache._ref, k.data_ptr(), v.data_ptr(), k_st, k_sh, v_st, v_sh, cu_seqlens.data_ptr(),
+                                 cache_lens.data_ptr(), page_table.data_ptr(), page_table.stride(0),
+                                 page_table.shape[1], B, total, c, s, rope_dim, max_pos, int(bool(interleaved)),
+                                 _stream_handle(stream))
+    _check(st, "attn_paged_append")
+
+
+def attn_paged_gather(cache: PagedKVCache, cu_seqlens, page_table, total: int, k=None, v=None, stream=None):
+    """(k, v), bf16 [total, Hkv, d]: positions 0 .. cu_seqlens[b + 1] - cu_seqlens[b] - 1 of every sequence read
+    out of the cache, packed as attn_fwd_varlen takes them. Rows from cu_seqlens[B] on are left as they were."""
+    import torch
+    B = _paged_args(cache, page_table, cu_seqlens=(cu_seqlens, 1))
+    shape = (total, cache.Hkv, cache.d)
+    outs = []
+    for name, t in (("k", k), ("v", v)):
+        if t is None:
+            t = _buffer(shape, torch.bfloat16, cache.device, stream)
+        elif t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor of shape {shape}")
+        outs.append(t)
+    _on_current_device((("k", outs[0]), ("v", outs[1])))
+    if total == 0 or B == 0:
+        return outs[0], outs[1]
+    st = lib().attn_paged_gather(cache._ref, outs[0].data_ptr(), outs[1].data_ptr(), cu_seqlens.data_ptr(),
+                                 page_table.data_ptr(), page_table.stride(0), page_table.shape[1], B, total,
+                                 _stream_handle(stream))
+    _check(st, "attn_paged_gather")
+    return outs[0], outs[1]
+
+
+def attn_fwd_paged_workspace_bytes(cache: PagedKVCache, B: int, H: int, Nq: int) -> int:
+    return int(lib().attn_fwd_paged_workspace_bytes(B, H, cache.Hkv, Nq, cache.d, cache.type))
+
+
+def attn_fwd_paged(q, cache: PagedKVCache, page_table, seqlens, causal: bool = True, scale: Optional[float] = None,
+                   workspace=None, out=None, lse=None, stream=None):
+    """Attention of q [B, Nq, H, d] (bf16) over the cache: (out bf16 [B, Nq, H, d], lse float32 [B, H, Nq]).
+
+    ``seqlens`` (int32 [B]) counts each sequence's keys, the Nq new tokens' own among them; with ``causal``
+    query i sees keys j <= i + seqlens[b] - Nq. Rows that see no key give 0 and -inf. ``workspace`` (CUDA
+    uint8, at least attn_fwd_paged_workspace_bytes(...)) is allocated here with torch if not given.
+    """
+    import torch
+    if q.dim() != 4 or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bfloat16 CUDA tensor [B, Nq, H, d]")
+    B, Nq, H, d = q.shape
+    if _paged_args(cache, page_table, seqlens=(seqlens, 0)) != B or d != cache.d or H % cache.Hkv != 0:
+        raise ValueError("q must be [B, Nq, H, d] with the page table's B, the cache's d and a multiple of its heads")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if workspace is None:
+        workspace = _buffer((max(attn_fwd_paged_workspace_bytes(cache, B, H, Nq), 1),), torch.uint8, q.device, stream)
+    if out is None:
+        out = _buffer((B, Nq, H, d), torch.bfloat16, q.device, stream)
+    elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
+        raise ValueError("out must be a contiguous bfloat16 CUDA tensor like q")
+    if lse is None:
+        lse = _buffer((B, H, Nq), torch.float32, q.device, stream)
+    elif lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 CUDA tensor [B, H, Nq]")
+    _on_current_device((("q", q), ("workspace", workspace), ("out", out), ("lse", lse)))
+    st = lib().attn_fwd_paged(q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(), page_table.data_ptr(),
+                              page_table.stride(0), page_table.shape[1], seqlens.data_ptr(), B, H, Nq, float(scale),
+                              int(bool(causal)), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                              _stream_handle(stream))
+    _check(st, "attn_fwd_paged")
+    return out, lse
 
 
 def attn_get_status(stream=None) -> tuple[int, int]:

@@ -13,6 +13,7 @@
 #include "attn.h"
 #include "context_id.h"
 #include "launch.h"
+#include "ops.h"
 
 // First failure recorded by any kernel of this library on the device (0 = none).
 static __device__ uint32_t g_attn_status;
@@ -288,9 +289,13 @@ cudaError_t dispatch_d(gb300::LaunchArgs& a, bool causal, bool fp8, cudaStream_t
 
 }  // namespace
 
-extern "C" {
-
-}  // extern "C"
+bool gb300::device_state(int* num_sms, uint32_t** status) {
+  DeviceInfo* di = device_info();
+  if (!di) return false;
+  *num_sms = di->num_sms;
+  *status = di->status;
+  return true;
+}
 
 namespace {
 

@@ -1,0 +1,11 @@
+// State of the current device that entry points outside attn_api.cu need.
+#pragma once
+#include <cstdint>
+
+namespace gb300 {
+
+// SM count and the device status word (first failure recorded by a kernel) of the current device.
+// False, with nothing written, when the device cannot be queried.
+bool device_state(int* num_sms, uint32_t** status);
+
+}  // namespace gb300

@@ -1,0 +1,353 @@
+// Filling a paged key/value cache and reading it back.
+//
+// attn_paged_append: token i of sequence b (row cu[b] + i of the packed k and v) goes to position
+// p = len[b] + i, that is row p % page_size of page table[b, p / page_size]. Keys are turned by their
+// position's angles on the way; rows are stored as bf16 or in the 4-bit format of paged.cuh.
+// attn_paged_gather: rows 0 .. n_b - 1 of every sequence into packed bf16 k and v, the layout the
+// ragged-batch forward reads.
+//
+// Both are bound by memory. d / 8 lanes hold a row, 8 neighbouring values (16 bytes) each. A lane
+// reads the 8 values its own are paired with from the same row (a second load of a line already in
+// L1) instead of exchanging them; a group of 64 values is 8 neighbouring lanes, so its least and
+// greatest value take three exchanges. Rotation and quantisation round every step as written here
+// (no contraction into fused multiply-adds): a code must not depend on how the compiler schedules,
+// or a value at a border between two codes would change with it.
+#include <algorithm>
+#include <climits>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "attn.h"
+#include "ops.h"
+#include "paged.cuh"
+#include "paged_host.h"
+
+namespace gb300 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 2;   // heads of one token a thread has in flight
+
+struct AppendParams {
+  PagedCache c;
+  const __nv_bfloat16 *k, *v;
+  long long k_st, k_sh, v_st, v_sh;
+  const int *cu, *len, *table;
+  long long table_stride;
+  const float *cos, *sin;
+  int B, total, max_pages, half, rope_dim, max_pos, parts;
+  uint32_t* status;
+};
+
+struct GatherParams {
+  PagedCache c;
+  __nv_bfloat16 *k, *v;
+  const int *cu, *table;
+  long long table_stride;
+  int B, total, max_pages, parts;
+  uint32_t* status;
+};
+
+__device__ __forceinline__ void unpack8(float (&x)[8], const uint4& w) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(u[i] << 16);
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    u[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// fp32 to the bf16 not above it (UP false) or not below it, as fp32.
+template <bool UP>
+__device__ __forceinline__ float bf16_toward(float x) {
+  const uint32_t bits = __float_as_uint(x), cut = bits & 0xffff0000u;
+  const bool away = cut != bits && ((bits >> 31) != 0) != UP;
+  return __uint_as_float(cut + (away ? 0x10000u : 0u));
+}
+
+// 8 of a group's 64 values (8 neighbouring lanes) as codes; sz: its (scale, zero) pair.
+__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t& sz) {
+  float lo = x[0], hi = x[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    lo = fminf(lo, x[i]);
+    hi = fmaxf(hi, x[i]);
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  const float zero = bf16_toward<false>(lo);
+  const float least = fmaxf(fmaxf(fabsf(lo), fabsf(hi)) * 0x1p-20f, 0x1p-100f);
+  const float scale = bf16_toward<true>(fmaxf(__fdiv_rn(__fsub_rn(hi, zero), 15.f), least));
+  sz = (__float_as_uint(scale) >> 16) | (__float_as_uint(zero) & 0xffff0000u);
+  uint32_t codes = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[i], zero), scale)), 0.f), 15.f);
+    codes |= (uint32_t)c << (4 * i);
+  }
+  return codes;
+}
+
+// Where position pos of sequence b lies, or false where the table does not lead into the pool.
+__device__ __forceinline__ bool find_row(const PagedCache& c, const int* __restrict__ table, long long table_stride,
+                                         int max_pages, int b, int pos, int& page, int& at) {
+  const int e = pos / c.page_size;
+  if (pos < 0 || e >= max_pages) return false;
+  page = table[b * table_stride + e];
+  at = pos - e * c.page_size;
+  return page >= 0 && page < c.num_pages;
+}
+
+template <int D, bool INT4, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendParams p) {
+  constexpr int LPR = D / 8;
+  const int l = threadIdx.x % LPR;
+  const unsigned task = blockIdx.x * (unsigned)(kThreads / LPR) + threadIdx.x / LPR;
+  const int t = min(task / p.parts, (unsigned)p.total - 1u), part = task % p.parts;
+  bool good = task / p.parts < (unsigned)p.total;
+  const bool is_v = part >= p.parts / 2;
+  const int h0 = (is_v ? part - p.parts / 2 : part) * kRows, heads = p.c.Hkv;
+  const __nv_bfloat16* x = is_v ? p.v + t * p.v_st : p.k + t * p.k_st;
+  const long long sh = is_v ? p.v_sh : p.k_sh;
+  // This lane's dims 8l .. 8l + 7 and, for keys, where the values they are paired with begin.
+  const bool turned = !is_v && p.cos && 8 * l < p.rope_dim;
+  const int mate = 8 * l < p.half ? 8 * l + p.half : 8 * l - p.half;
+  uint4 raw[kRows], raw_mate[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const __nv_bfloat16* row = x + min(h0 + i, heads - 1) * sh;
+    raw[i] = *reinterpret_cast<const uint4*>(row + 8 * l);
+    raw_mate[i] = make_uint4(0, 0, 0, 0);
+    if (!INTERLEAVED && turned) raw_mate[i] = *reinterpret_cast<const uint4*>(row + mate);
+  }
+  const int b = find_sequence<LPR>(p.cu, p.B, t);
+  int page = 0, at = 0, pos = 0;
+  if (b >= p.B) {
+    good = false;   // behind the last sequence: not stored
+  } else {
+    const int first = p.cu[b], past = p.len[b];
+    pos = past + (t - first);
+    const bool in = t >= first && t < p.cu[b + 1] && past >= 0 && pos >= 0 &&
+                    find_row(p.c, p.table, p.table_stride, p.max_pages, b, pos, page, at) &&
+                    (!p.cos || pos < p.max_pos);
+    if (good && !in && l == 0) atomicCAS(p.status, 0u, kStatusBadPage);
+    good = good && in;
+    if (!in) pos = 0;
+  }
+  float cs[8], sn[8];
+  if (turned) {
+    // pair of dim j: j mod half, or j / 2 when interleaved
+    const int pair = INTERLEAVED ? 4 * l : (8 * l < p.half ? 8 * l : 8 * l - p.half);
+    const float* ct = p.cos + (long long)pos * p.half + pair;
+    const float* st = p.sin + (long long)pos * p.half + pair;
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      if (INTERLEAVED && i) break;
+      const float4 c = *reinterpret_cast<const float4*>(ct + i), s = *reinterpret_cast<const float4*>(st + i);
+      cs[i] = c.x, cs[i + 1] = c.y, cs[i + 2] = c.z, cs[i + 3] = c.w;
+      sn[i] = s.x, sn[i + 1] = s.y, sn[i + 2] = s.z, sn[i + 3] = s.w;
+    }
+  }
+  const PagedCache& c = p.c;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    float y[8];
+    unpack8(y, raw[i]);
+    if (turned) {
+      if (INTERLEAVED) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float u = y[2 * j], v = y[2 * j + 1];
+          y[2 * j] = __fsub_rn(__fmul_rn(u, cs[j]), __fmul_rn(v, sn[j]));
+          y[2 * j + 1] = __fadd_rn(__fmul_rn(v, cs[j]), __fmul_rn(u, sn[j]));
+        }
+      } else {
+        float m[8];
+        unpack8(m, raw_mate[i]);
+        const bool first_half = 8 * l < p.half;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float u = __fmul_rn(y[j], cs[j]), v = __fmul_rn(m[j], sn[j]);
+          y[j] = first_half ? __fsub_rn(u, v) : __fadd_rn(u, v);
+        }
+      }
+    }
+    const bool store = good && h0 + i < heads;
+    const long long row = page * c.page_b + at * c.token_b + (h0 + i) * c.head_b;
+    uint8_t* base = is_v ? c.v : c.k;
+    if constexpr (INT4) {
+      uint32_t sz;
+      const uint32_t codes = quantise8(y, sz);
+      if (store) {
+        *reinterpret_cast<uint32_t*>(base + row + 4 * l) = codes;
+        if (l % 8 == 0) {
+          const long long sz_row = page * c.sz_page_b + at * c.sz_token_b + (h0 + i) * c.sz_head_b;
+          *reinterpret_cast<uint32_t*>((is_v ? c.v_sz : c.k_sz) + sz_row + l / 8 * 4) = sz;
+        }
+      }
+    } else if (store) {
+      // values no rotation touches keep their bits
+      *reinterpret_cast<uint4*>(base + row + 16 * l) = turned ? pack8(y) : raw[i];
+    }
+  }
+}
+
+constexpr int kGatherRows = 4;
+
+template <int D, bool INT4>
+__global__ void __launch_bounds__(kThreads) paged_gather_kernel(const GatherParams p) {
+  constexpr int LPR = D / 8;
+  const int l = threadIdx.x % LPR;
+  const unsigned task = blockIdx.x * (unsigned)(kThreads / LPR) + threadIdx.x / LPR;
+  const int t = min(task / p.parts, (unsigned)p.total - 1u), part = task % p.parts;
+  const bool mine = task / p.parts < (unsigned)p.total;
+  const bool is_v = part >= p.parts / 2;
+  const int h0 = (is_v ? part - p.parts / 2 : part) * kGatherRows, heads = p.c.Hkv;
+  const int b = find_sequence<LPR>(p.cu, p.B, t);
+  if (b >= p.B || !mine) return;   // behind the last sequence: left as it was
+  const int first = p.cu[b];
+  int page, at;
+  if (t < first || t >= p.cu[b + 1] ||
+      !find_row(p.c, p.table, p.table_stride, p.max_pages, b, t - first, page, at)) {
+    if (l == 0) atomicCAS(p.status, 0u, kStatusBadPage);
+    return;
+  }
+  const PagedCache& c = p.c;
+  const uint8_t* base = (is_v ? c.v : c.k) + page * c.page_b + at * c.token_b;
+  __nv_bfloat16* y = (is_v ? p.v : p.k) + ((long long)t * heads + h0) * D + 8 * l;
+  if constexpr (INT4) {
+    const uint8_t* sz_base = (is_v ? c.v_sz : c.k_sz) + page * c.sz_page_b + at * c.sz_token_b + l / 8 * 4;
+    uint32_t codes[kGatherRows], sz[kGatherRows];
+#pragma unroll
+    for (int i = 0; i < kGatherRows; ++i) {
+      const int h = min(h0 + i, heads - 1);
+      codes[i] = *reinterpret_cast<const uint32_t*>(base + h * c.head_b + 4 * l);
+      sz[i] = *reinterpret_cast<const uint32_t*>(sz_base + h * c.sz_head_b);
+    }
+#pragma unroll
+    for (int i = 0; i < kGatherRows; ++i) {
+      const float scale = __uint_as_float(sz[i] << 16), zero = __uint_as_float(sz[i] & 0xffff0000u);
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = fmaf(scale, (float)((codes[i] >> (4 * j)) & 15u), zero);
+      if (h0 + i < heads) *reinterpret_cast<uint4*>(y + i * D) = pack8(x);
+    }
+  } else {
+    uint4 raw[kGatherRows];
+#pragma unroll
+    for (int i = 0; i < kGatherRows; ++i)
+      raw[i] = *reinterpret_cast<const uint4*>(base + min(h0 + i, heads - 1) * c.head_b + 16 * l);
+#pragma unroll
+    for (int i = 0; i < kGatherRows; ++i)
+      if (h0 + i < heads) *reinterpret_cast<uint4*>(y + i * D) = raw[i];
+  }
+}
+
+template <int D, bool INT4>
+cudaError_t launch_append(const AppendParams& p, bool interleaved, cudaStream_t s) {
+  const unsigned rows = kThreads / (D / 8);
+  const unsigned grid = ((unsigned)p.total * p.parts + rows - 1) / rows;
+  if (interleaved) paged_append_kernel<D, INT4, true><<<grid, kThreads, 0, s>>>(p);
+  else paged_append_kernel<D, INT4, false><<<grid, kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D, bool INT4>
+cudaError_t launch_gather(const GatherParams& p, cudaStream_t s) {
+  const unsigned rows = kThreads / (D / 8);
+  paged_gather_kernel<D, INT4><<<((unsigned)p.total * p.parts + rows - 1) / rows, kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace gb300
+
+using namespace gb300;
+
+extern "C" attn_status_t attn_paged_append(const attn_paged_cache_t* cache, const void* k, const void* v,
+                                           long long k_stride_t, long long k_stride_h, long long v_stride_t,
+                                           long long v_stride_h, const int* cu_seqlens, const int* cache_lens,
+                                           const int* page_table, long long table_stride, int max_pages, int B,
+                                           int total, const float* cos, const float* sin, int rope_dim, int max_pos,
+                                           int interleaved, cudaStream_t stream) {
+  AppendParams p = {};
+  const attn_status_t st = paged_cache_args(cache, &p.c);
+  if (st != ATTN_OK) return st;
+  if (B < 1 || total < 0 || max_pages < 1 || table_stride < 0) return ATTN_ERR_INVALID_ARG;
+  if (!k || !v || !cu_seqlens || !cache_lens || !page_table) return ATTN_ERR_INVALID_ARG;
+  if (!is_aligned(k, 16) || !is_aligned(v, 16) || !is_aligned(cu_seqlens, 4) || !is_aligned(cache_lens, 4) ||
+      !is_aligned(page_table, 4))
+    return ATTN_ERR_INVALID_ARG;
+  for (const long long s : {k_stride_t, k_stride_h, v_stride_t, v_stride_h})
+    if (s < 0 || s % 8 || s > (1LL << 40)) return ATTN_ERR_INVALID_ARG;
+  if ((cos != nullptr) != (sin != nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (cos) {
+    if (!is_aligned(cos, 16) || !is_aligned(sin, 16) || max_pos < 1) return ATTN_ERR_INVALID_ARG;
+    if (rope_dim < 16 || rope_dim % 16 || rope_dim > cache->d) return ATTN_ERR_INVALID_ARG;
+  }
+  p.parts = 2 * ((cache->Hkv + kRows - 1) / kRows);
+  if ((long long)total * p.parts > INT_MAX) return ATTN_ERR_UNSUPPORTED;   // tasks are counted in 32 bits
+  if (total == 0) return ATTN_OK;
+  int sms;
+  if (!device_state(&sms, &p.status)) return ATTN_ERR_CUDA;
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.k_st = k_stride_t, p.k_sh = k_stride_h, p.v_st = v_stride_t, p.v_sh = v_stride_h;
+  p.cu = cu_seqlens, p.len = cache_lens, p.table = page_table, p.table_stride = table_stride;
+  p.cos = cos, p.sin = sin;
+  p.B = B, p.total = total, p.max_pages = max_pages, p.max_pos = max_pos;
+  p.rope_dim = cos ? rope_dim : 0, p.half = p.rope_dim / 2;
+  const bool int4 = cache->type == ATTN_CACHE_INT4, il = interleaved != 0;
+  cudaError_t e;
+  switch (cache->d) {
+    case 64: e = int4 ? launch_append<64, true>(p, il, stream) : launch_append<64, false>(p, il, stream); break;
+    case 128: e = int4 ? launch_append<128, true>(p, il, stream) : launch_append<128, false>(p, il, stream); break;
+    default: e = int4 ? launch_append<256, true>(p, il, stream) : launch_append<256, false>(p, il, stream); break;
+  }
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" attn_status_t attn_paged_gather(const attn_paged_cache_t* cache, void* k, void* v, const int* cu_seqlens,
+                                           const int* page_table, long long table_stride, int max_pages, int B,
+                                           int total, cudaStream_t stream) {
+  GatherParams p = {};
+  const attn_status_t st = paged_cache_args(cache, &p.c);
+  if (st != ATTN_OK) return st;
+  if (B < 1 || total < 0 || max_pages < 1 || table_stride < 0) return ATTN_ERR_INVALID_ARG;
+  if (!k || !v || !cu_seqlens || !page_table) return ATTN_ERR_INVALID_ARG;
+  if (!is_aligned(k, 16) || !is_aligned(v, 16) || !is_aligned(cu_seqlens, 4) || !is_aligned(page_table, 4))
+    return ATTN_ERR_INVALID_ARG;
+  const uintptr_t bytes = (uintptr_t)total * cache->Hkv * cache->d * 2, kb = (uintptr_t)k, vb = (uintptr_t)v;
+  if (kb < vb + bytes && vb < kb + bytes) return ATTN_ERR_INVALID_ARG;
+  p.parts = 2 * ((cache->Hkv + kGatherRows - 1) / kGatherRows);
+  if ((long long)total * p.parts > INT_MAX) return ATTN_ERR_UNSUPPORTED;
+  if (total == 0) return ATTN_OK;
+  int sms;
+  if (!device_state(&sms, &p.status)) return ATTN_ERR_CUDA;
+  p.k = static_cast<__nv_bfloat16*>(k);
+  p.v = static_cast<__nv_bfloat16*>(v);
+  p.cu = cu_seqlens, p.table = page_table, p.table_stride = table_stride;
+  p.B = B, p.total = total, p.max_pages = max_pages;
+  const bool int4 = cache->type == ATTN_CACHE_INT4;
+  cudaError_t e;
+  switch (cache->d) {
+    case 64: e = int4 ? launch_gather<64, true>(p, stream) : launch_gather<64, false>(p, stream); break;
+    case 128: e = int4 ? launch_gather<128, true>(p, stream) : launch_gather<128, false>(p, stream); break;
+    default: e = int4 ? launch_gather<256, true>(p, stream) : launch_gather<256, false>(p, stream); break;
+  }
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}

@@ -1,0 +1,511 @@
+// RMS norm of every head of q and k, then the rotation by position, in one pass; and its gradient.
+//
+// One row is one token of one head, x of d values:
+//   n = x r, r = (mean x^2 + eps)^(-1/2);   u = n w;   y = R u,
+// where R turns the pairs (a, b) of the first rope_dim values by the position's angles:
+//   y_a = u_a cos - u_b sin,   y_b = u_b cos + u_a sin.
+// Pairs are (i, i + rope_dim / 2), or (2i, 2i + 1) when interleaved. The gradient turns back
+// (R is orthogonal), du = R^T dy, and with g = du w:
+//   dw = sum over rows of du n,   dx = r (g - n mean(g n)).
+//
+// d / 8 lanes hold a row, 8 values each as two chunks of 4 that hold both members of their pairs, so
+// the rotation needs no exchange and only the row sums cross lanes. A task is one token and up to
+// 4 heads of q or of k: the angles and weights are loaded once per task, and the 4 rows' loads are in
+// flight together. Everything is fp32 between the bf16 loads and the one rounding at the store.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "attn.h"
+#include "ops.h"
+#include "paged.cuh"
+
+namespace gb300 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kHeads = 4;   // rows of a task
+
+struct NormRopeParams {
+  const __nv_bfloat16 *q, *k;      // inputs (or x of the backward)
+  const __nv_bfloat16 *dyq, *dyk;  // backward: gradients of the outputs, contiguous
+  __nv_bfloat16 *oq, *ok;          // outputs (or dx), contiguous
+  long long q_st, q_sh, k_st, k_sh;
+  const float *wq, *wk, *cos, *sin;
+  const int* positions;
+  float* part;                     // backward: [CTAs, d] sums of du n
+  float eps;
+  int T, H, Hkv, half, max_pos, seq_len, parts_q, parts_k, ctas_q;
+  uint32_t* status;
+};
+
+struct Chunks {
+  float a[4], b[4];
+};
+
+__device__ __forceinline__ void load4(float (&x)[4], const __nv_bfloat16* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  x[0] = __uint_as_float(w.x << 16);
+  x[1] = __uint_as_float(w.x & 0xffff0000u);
+  x[2] = __uint_as_float(w.y << 16);
+  x[3] = __uint_as_float(w.y & 0xffff0000u);
+}
+
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[4]) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
+  uint2 w;
+  w.x = *reinterpret_cast<const uint32_t*>(&lo);
+  w.y = *reinterpret_cast<const uint32_t*>(&hi);
+  *reinterpret_cast<uint2*>(p) = w;
+}
+
+// First dims of a lane's two chunks. half = rope_dim / 2; lanes behind the rotated dims hold 8
+// neighbouring values, as all lanes do when pairs are interleaved.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void chunk_dims(int l, int half, int& da, int& db) {
+  const bool split = !INTERLEAVED && 4 * l < half;
+  da = split ? 4 * l : 8 * l;
+  db = split ? half + 4 * l : 8 * l + 4;
+}
+
+// Angles of a lane's pairs at one position: pair i of the lane is (a[i], b[i]), or when interleaved
+// (a[0], a[1]), (a[2], a[3]), (b[0], b[1]), (b[2], b[3]).
+struct Angles {
+  float c[4], s[4];
+};
+
+template <bool INTERLEAVED>
+__device__ __forceinline__ void turn(Chunks& x, const Angles& r, float sign) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float& u = INTERLEAVED ? (i < 2 ? x.a[2 * i] : x.b[2 * i - 4]) : x.a[i];
+    float& v = INTERLEAVED ? (i < 2 ? x.a[2 * i + 1] : x.b[2 * i - 3]) : x.b[i];
+    const float s = sign * r.s[i], u0 = u;
+    u = u0 * r.c[i] - v * s;
+    v = v * r.c[i] + u0 * s;
+  }
+}
+
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Angles of token t; false (nothing to store) where its position lies outside the tables.
+__device__ __forceinline__ bool load_angles(const NormRopeParams& p, int t, int l, Angles& r) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.c[i] = 1.f, r.s[i] = 0.f;
+  if (!p.cos) return true;
+  const int pos = p.positions ? p.positions[t] : t % p.seq_len;
+  if (pos < 0 || pos >= p.max_pos) {
+    if (l == 0) atomicCAS(p.status, 0u, kStatusBadPosition);
+    return false;
+  }
+  if (4 * l < p.half) {
+    const long long at = (long long)pos * p.half + 4 * l;
+    const float4 c = *reinterpret_cast<const float4*>(p.cos + at), s = *reinterpret_cast<const float4*>(p.sin + at);
+    r.c[0] = c.x, r.c[1] = c.y, r.c[2] = c.z, r.c[3] = c.w;
+    r.s[0] = s.x, r.s[1] = s.y, r.s[2] = s.z, r.s[3] = s.w;
+  }
+  return true;
+}
+
+__device__ __forceinline__ void load_weights(const float* w, int da, int db, Chunks& x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x.a[i] = w ? w[da + i] : 1.f;
+    x.b[i] = w ? w[db + i] : 1.f;
+  }
+}
+
+template <int D, bool NORM, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormRopeParams p) {
+  constexpr int LPR = D / 8;
+  const int l = threadIdx.x % LPR;
+  const unsigned task = blockIdx.x * (unsigned)(kThreads / LPR) + threadIdx.x / LPR;
+  const unsigned parts = p.parts_q + p.parts_k;
+  const bool mine = task / parts < (unsigned)p.T;   // row sums take whole warps: no thread leaves early
+  const int t = mine ? task / parts : p.T - 1, part = task % parts;
+  const bool is_k = part >= p.parts_q;
+  const int h0 = (is_k ? part - p.parts_q : part) * kHeads, heads = is_k ? p.Hkv : p.H;
+  const __nv_bfloat16* x = is_k ? p.k + t * p.k_st : p.q + t * p.q_st;
+  const long long sh = is_k ? p.k_sh : p.q_sh;
+  __nv_bfloat16* y = (is_k ? p.ok : p.oq) + (long long)t * heads * D;
+  int da, db;
+  chunk_dims<INTERLEAVED>(l, p.half, da, db);
+  Chunks v[kHeads];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    if (h0 + i < heads) {
+      load4(v[i].a, x + (h0 + i) * sh + da);
+      load4(v[i].b, x + (h0 + i) * sh + db);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i].a[j] = v[i].b[j] = 0.f;
+    }
+  }
+  Angles r;
+  const bool good = load_angles(p, t, l, r) && mine;
+  Chunks w;
+  if (NORM) load_weights(is_k ? p.wk : p.wq, da, db, w);
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    if (NORM) {
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s += v[i].a[j] * v[i].a[j] + v[i].b[j] * v[i].b[j];
+      const float rs = rsqrtf(row_sum<LPR>(s) * (1.f / D) + p.eps);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[i].a[j] *= rs * w.a[j];
+        v[i].b[j] *= rs * w.b[j];
+      }
+    }
+    turn<INTERLEAVED>(v[i], r, 1.f);
+    if (good && h0 + i < heads) {
+      store4(y + (h0 + i) * D + da, v[i].a);
+      store4(y + (h0 + i) * D + db, v[i].b);
+    }
+  }
+}
+
+// The gradient. CTAs 0 .. ctas_q - 1 walk the tasks of q, the others those of k, so a thread sums the
+// weight gradient of its 8 dims in registers; a CTA adds its rows' sums in a fixed order and leaves
+// [d] in part, which dw_kernel adds up: the same bits every time.
+template <int D, bool NORM, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const NormRopeParams p) {
+  constexpr int LPR = D / 8, ROWS = kThreads / LPR;
+  const int l = threadIdx.x % LPR, slot = threadIdx.x / LPR;
+  const bool is_k = blockIdx.x >= (unsigned)p.ctas_q;
+  const int cta = is_k ? (int)blockIdx.x - p.ctas_q : blockIdx.x, ctas = is_k ? (int)gridDim.x - p.ctas_q : p.ctas_q;
+  const int heads = is_k ? p.Hkv : p.H, parts = is_k ? p.parts_k : p.parts_q;
+  const float* wp = is_k ? p.wk : p.wq;
+  int da, db;
+  chunk_dims<INTERLEAVED>(l, p.half, da, db);
+  Chunks w, dw;
+  if (NORM) load_weights(wp, da, db, w);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) dw.a[j] = dw.b[j] = 0.f;
+  const unsigned tasks = (unsigned)p.T * parts;
+  // Every thread of the CTA makes the same number of turns: row sums take whole warps.
+  for (unsigned t0 = (unsigned)cta * ROWS; t0 < tasks; t0 += (unsigned)ctas * ROWS) {
+    const unsigned task = t0 + slot;
+    const bool mine = task < tasks;
+    const int t = mine ? task / parts : 0, h0 = mine ? task % parts * kHeads : heads;
+    const __nv_bfloat16* x = NORM ? (is_k ? p.k + t * p.k_st : p.q + t * p.q_st) : nullptr;
+    const long long sh = is_k ? p.k_sh : p.q_sh;
+    const long long at = (long long)t * heads * D;
+    const __nv_bfloat16* dy = (is_k ? p.dyk : p.dyq) + at;
+    __nv_bfloat16* dx = (is_k ? p.ok : p.oq) + at;
+    Chunks v[kHeads], g[kHeads];
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      if (h0 + i < heads) {
+        if (NORM) {
+          load4(v[i].a, x + (h0 + i) * sh + da);
+          load4(v[i].b, x + (h0 + i) * sh + db);
+        }
+        load4(g[i].a, dy + (h0 + i) * D + da);
+        load4(g[i].b, dy + (h0 + i) * D + db);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i].a[j] = v[i].b[j] = g[i].a[j] = g[i].b[j] = 0.f;
+      }
+    }
+    Angles r;
+    const bool good = load_angles(p, t, l, r);
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const bool row = good && h0 + i < heads;
+      turn<INTERLEAVED>(g[i], r, -1.f);
+      if (NORM) {
+        float s = 0.f, m = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s += v[i].a[j] * v[i].a[j] + v[i].b[j] * v[i].b[j];
+          m += g[i].a[j] * w.a[j] * v[i].a[j] + g[i].b[j] * w.b[j] * v[i].b[j];
+        }
+        s = row_sum<LPR>(s);
+        m = row_sum<LPR>(m);
+        const float rs = rsqrtf(s * (1.f / D) + p.eps), c = m * (1.f / D) * rs * rs;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (row) {
+            dw.a[j] += g[i].a[j] * v[i].a[j] * rs;
+            dw.b[j] += g[i].b[j] * v[i].b[j] * rs;
+          }
+          g[i].a[j] = rs * (g[i].a[j] * w.a[j] - v[i].a[j] * c);
+          g[i].b[j] = rs * (g[i].b[j] * w.b[j] - v[i].b[j] * c);
+        }
+      }
+      if (row) {
+        store4(dx + (h0 + i) * D + da, g[i].a);
+        store4(dx + (h0 + i) * D + db, g[i].b);
+      }
+    }
+  }
+  if (NORM && wp) {
+    __shared__ float sums[ROWS][D];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      sums[slot][da + j] = dw.a[j];
+      sums[slot][db + j] = dw.b[j];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < D; i += kThreads) {
+      float s = 0.f;
+      for (int r = 0; r < ROWS; ++r) s += sums[r][i];
+      p.part[(long long)blockIdx.x * D + i] = s;
+    }
+  }
+}
+
+// dw[i] = sum over CTAs of part[cta][i]; block x is 32 dims of q's (y = 0) or k's (y = 1) weight.
+__global__ void __launch_bounds__(1024) dw_kernel(const float* __restrict__ part, float* dwq, float* dwk, int d,
+                                                  int ctas_q, int ctas) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float* dw = blockIdx.y ? dwk : dwq;
+  if (!dw) return;
+  const int first = blockIdx.y ? ctas_q : 0, last = blockIdx.y ? ctas : ctas_q;
+  const int i = blockIdx.x * 32 + threadIdx.x;
+  float s = 0.f;
+  for (int c = first + threadIdx.y; c < last; c += 32) s += part[(long long)c * d + i];
+  __shared__ float sums[32][33];
+  sums[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y == 0) {
+    s = 0.f;
+    for (int r = 0; r < 32; ++r) s += sums[r][threadIdx.x];
+    dw[i] = s;
+  }
+}
+
+template <int D>
+cudaError_t launch_forward(const NormRopeParams& p, bool norm, bool interleaved, cudaStream_t s) {
+  const long long tasks = (long long)p.T * (p.parts_q + p.parts_k), rows = kThreads / (D / 8);
+  const unsigned grid = (unsigned)((tasks + rows - 1) / rows);
+  if (norm) {
+    if (interleaved) qk_norm_rope_kernel<D, true, true><<<grid, kThreads, 0, s>>>(p);
+    else qk_norm_rope_kernel<D, true, false><<<grid, kThreads, 0, s>>>(p);
+  } else {
+    if (interleaved) qk_norm_rope_kernel<D, false, true><<<grid, kThreads, 0, s>>>(p);
+    else qk_norm_rope_kernel<D, false, false><<<grid, kThreads, 0, s>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_backward(const NormRopeParams& p, bool norm, bool interleaved, int grid, cudaStream_t s) {
+  if (norm) {
+    if (interleaved) qk_norm_rope_bwd_kernel<D, true, true><<<grid, kThreads, 0, s>>>(p);
+    else qk_norm_rope_bwd_kernel<D, true, false><<<grid, kThreads, 0, s>>>(p);
+  } else {
+    if (interleaved) qk_norm_rope_bwd_kernel<D, false, true><<<grid, kThreads, 0, s>>>(p);
+    else qk_norm_rope_bwd_kernel<D, false, false><<<grid, kThreads, 0, s>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+// CTAs of the backward: one wave of 4 a SM (1024 threads), shared between q and k by their tasks.
+constexpr int kBwdCtasPerSm = 4;
+
+struct BwdGrid {
+  int ctas_q, ctas;
+};
+
+BwdGrid bwd_grid(int T, int H, int Hkv, int d, int sms) {
+  const long long rows = kThreads / (d / 8);
+  const long long tq = (long long)T * ((H + kHeads - 1) / kHeads), tk = (long long)T * ((Hkv + kHeads - 1) / kHeads);
+  const long long need_q = (tq + rows - 1) / rows, need_k = (tk + rows - 1) / rows, cap = (long long)kBwdCtasPerSm * sms;
+  if (need_q + need_k <= cap) return {(int)need_q, (int)(need_q + need_k)};
+  long long cq = cap * tq / (tq + tk);
+  cq = std::max<long long>(1, std::min(cq, cap - (tk ? 1 : 0)));
+  return {(int)cq, (int)(tk ? cap : cq)};
+}
+
+struct Range {
+  uintptr_t b, e;
+};
+
+Range rows_range(const void* p, long long T, long long heads, long long st, long long sh, int d) {
+  const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+  return {b, b + 2 * ((uintptr_t)(T - 1) * st + (uintptr_t)(heads - 1) * sh + d)};
+}
+
+bool meet(const Range& a, const Range& b) { return a.b < b.e && b.b < a.e; }
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool aligned4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
+
+// Checks that the forward and the backward share; x are the strided inputs (null: not read).
+attn_status_t check(const void* xq, const void* xk, const void* oq, const void* ok, int T, int H, int Hkv, int d,
+                    long long q_st, long long q_sh, long long k_st, long long k_sh, int norm, const float* wq,
+                    const float* wk, float eps, const float* cos, const float* sin, int rope_dim, int max_pos,
+                    const int* positions, int seq_len) {
+  if (T < 1 || H < 1 || Hkv < 0 || d < 1) return ATTN_ERR_INVALID_ARG;
+  if (!oq || (Hkv > 0) != (ok != nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(xq) || !aligned16(xk) || !aligned16(oq) || !aligned16(ok)) return ATTN_ERR_INVALID_ARG;
+  if (q_st < 0 || q_sh < 0 || k_st < 0 || k_sh < 0 || q_st % 8 || q_sh % 8 || k_st % 8 || k_sh % 8)
+    return ATTN_ERR_INVALID_ARG;
+  if (q_st > (1LL << 40) || q_sh > (1LL << 40) || k_st > (1LL << 40) || k_sh > (1LL << 40)) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128 && d != 256) return ATTN_ERR_UNSUPPORTED;
+  if (norm && !(eps >= 0.f && std::isfinite(eps))) return ATTN_ERR_INVALID_ARG;
+  if (!norm && (wq || wk)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned4(wq) || !aligned4(wk)) return ATTN_ERR_INVALID_ARG;
+  if ((cos != nullptr) != (sin != nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (cos) {
+    if (!aligned16(cos) || !aligned16(sin) || max_pos < 1 || !aligned4(positions)) return ATTN_ERR_INVALID_ARG;
+    if (!positions && seq_len < 1) return ATTN_ERR_INVALID_ARG;
+    if (rope_dim < 16 || rope_dim % 16 || rope_dim > d) return ATTN_ERR_INVALID_ARG;
+  }
+  const long long parts = (H + (long long)kHeads - 1) / kHeads + (Hkv + (long long)kHeads - 1) / kHeads;
+  if (T * parts > INT_MAX) return ATTN_ERR_UNSUPPORTED;   // tasks are counted in 32 bits
+  return ATTN_OK;
+}
+
+}  // namespace
+}  // namespace gb300
+
+using namespace gb300;
+
+extern "C" attn_status_t attn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int T, int H,
+                                           int Hkv, int d, long long q_stride_t, long long q_stride_h,
+                                           long long k_stride_t, long long k_stride_h, int norm, const float* wq,
+                                           const float* wk, float eps, const float* cos, const float* sin,
+                                           int rope_dim, int max_pos, int interleaved, const int* positions,
+                                           int seq_len, cudaStream_t stream) {
+  const attn_status_t st = check(q, k, q_out, k_out, T, H, Hkv, d, q_stride_t, q_stride_h, k_stride_t, k_stride_h,
+                                 norm, wq, wk, eps, cos, sin, rope_dim, max_pos, positions, seq_len);
+  if (st != ATTN_OK) return st;
+  if (!q || (Hkv > 0) != (k != nullptr)) return ATTN_ERR_INVALID_ARG;
+  // An output may be its own contiguous input (a row is read before it is written); otherwise
+  // outputs meet neither the inputs nor each other.
+  const Range rq = rows_range(q, T, H, q_stride_t, q_stride_h, d), oq = rows_range(q_out, T, H, (long long)H * d, d, d);
+  const bool same_q = q == q_out && q_stride_h == d && q_stride_t == (long long)H * d;
+  if (!same_q && meet(oq, rq)) return ATTN_ERR_INVALID_ARG;
+  if (Hkv > 0) {
+    const Range rk = rows_range(k, T, Hkv, k_stride_t, k_stride_h, d),
+                ok = rows_range(k_out, T, Hkv, (long long)Hkv * d, d, d);
+    const bool same_k = k == k_out && k_stride_h == d && k_stride_t == (long long)Hkv * d;
+    if ((!same_k && meet(ok, rk)) || meet(oq, rk) || meet(ok, rq) || meet(oq, ok)) return ATTN_ERR_INVALID_ARG;
+  }
+  int sms;
+  uint32_t* status;
+  if (!device_state(&sms, &status)) return ATTN_ERR_CUDA;
+  NormRopeParams p = {};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.oq = static_cast<__nv_bfloat16*>(q_out);
+  p.ok = static_cast<__nv_bfloat16*>(k_out);
+  p.q_st = q_stride_t, p.q_sh = q_stride_h, p.k_st = k_stride_t, p.k_sh = k_stride_h;
+  p.wq = wq, p.wk = wk, p.cos = cos, p.sin = sin, p.positions = positions;
+  p.eps = eps;
+  p.T = T, p.H = H, p.Hkv = Hkv, p.half = cos ? rope_dim / 2 : 0, p.max_pos = max_pos, p.seq_len = seq_len;
+  p.parts_q = (H + kHeads - 1) / kHeads, p.parts_k = (Hkv + kHeads - 1) / kHeads;
+  p.status = status;
+  cudaError_t e;
+  switch (d) {
+    case 64: e = launch_forward<64>(p, norm != 0, interleaved != 0, stream); break;
+    case 128: e = launch_forward<128>(p, norm != 0, interleaved != 0, stream); break;
+    default: e = launch_forward<256>(p, norm != 0, interleaved != 0, stream); break;
+  }
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" size_t attn_qk_norm_rope_bwd_workspace_bytes(int T, int H, int Hkv, int d) {
+  if (T < 1 || H < 1 || Hkv < 0 || (d != 64 && d != 128 && d != 256)) return 0;
+  int sms = 152;
+  uint32_t* status;
+  device_state(&sms, &status);
+  return (size_t)bwd_grid(T, H, Hkv, d, sms).ctas * d * 4;
+}
+
+extern "C" attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                                               void* dq, void* dk, float* dwq, float* dwk, int T, int H, int Hkv,
+                                               int d, long long q_stride_t, long long q_stride_h,
+                                               long long k_stride_t, long long k_stride_h, int norm, const float* wq,
+                                               const float* wk, float eps, const float* cos, const float* sin,
+                                               int rope_dim, int max_pos, int interleaved, const int* positions,
+                                               int seq_len, void* workspace, size_t workspace_bytes,
+                                               cudaStream_t stream) {
+  const attn_status_t st = check(norm ? q : nullptr, norm ? k : nullptr, dq, dk, T, H, Hkv, d, q_stride_t, q_stride_h,
+                                 k_stride_t, k_stride_h, norm, wq, wk, eps, cos, sin, rope_dim, max_pos, positions,
+                                 seq_len);
+  if (st != ATTN_OK) return st;
+  if (!dq_out || (Hkv > 0) != (dk_out != nullptr) || (norm && (!q || (Hkv > 0) != (k != nullptr))))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(dq_out) || !aligned16(dk_out)) return ATTN_ERR_INVALID_ARG;
+  // weight gradients come with their weights
+  if ((dwq != nullptr) != (wq != nullptr) || (dwk != nullptr) != (wk != nullptr) || !aligned4(dwq) || !aligned4(dwk))
+    return ATTN_ERR_INVALID_ARG;
+  const size_t need = attn_qk_norm_rope_bwd_workspace_bytes(T, H, Hkv, d);
+  const bool dw = dwq || dwk;
+  if (dw && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
+  // Outputs: dq and dk may be the gradients they are made from, and nothing else.
+  Range outs[5], ins[4];
+  int no = 0, ni = 0;
+  auto bytes = [](const void* p, size_t n) { return Range{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + n}; };
+  const Range oq = rows_range(dq, T, H, (long long)H * d, d, d);
+  outs[no++] = oq;
+  if (Hkv > 0) outs[no++] = rows_range(dk, T, Hkv, (long long)Hkv * d, d, d);
+  if (dwq) outs[no++] = bytes(dwq, (size_t)d * 4);
+  if (dwk) outs[no++] = bytes(dwk, (size_t)d * 4);
+  if (dw) outs[no++] = bytes(workspace, need);
+  if (norm) {
+    ins[ni++] = rows_range(q, T, H, q_stride_t, q_stride_h, d);
+    if (Hkv > 0) ins[ni++] = rows_range(k, T, Hkv, k_stride_t, k_stride_h, d);
+  }
+  ins[ni++] = rows_range(dq_out, T, H, (long long)H * d, d, d);
+  if (Hkv > 0) ins[ni++] = rows_range(dk_out, T, Hkv, (long long)Hkv * d, d, d);
+  for (int i = 0; i < no; ++i) {
+    for (int j = i + 1; j < no; ++j)
+      if (meet(outs[i], outs[j])) return ATTN_ERR_INVALID_ARG;
+    for (int j = 0; j < ni; ++j) {
+      const bool in_place = (i == 0 && dq == dq_out && j == (norm ? (Hkv > 0 ? 2 : 1) : 0)) ||
+                            (i == 1 && Hkv > 0 && dk == dk_out && j == ni - 1);
+      if (!in_place && meet(outs[i], ins[j])) return ATTN_ERR_INVALID_ARG;
+    }
+  }
+  int sms;
+  uint32_t* status;
+  if (!device_state(&sms, &status)) return ATTN_ERR_CUDA;
+  const BwdGrid g = bwd_grid(T, H, Hkv, d, sms);
+  NormRopeParams p = {};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.dyq = static_cast<const __nv_bfloat16*>(dq_out);
+  p.dyk = static_cast<const __nv_bfloat16*>(dk_out);
+  p.oq = static_cast<__nv_bfloat16*>(dq);
+  p.ok = static_cast<__nv_bfloat16*>(dk);
+  p.q_st = q_stride_t, p.q_sh = q_stride_h, p.k_st = k_stride_t, p.k_sh = k_stride_h;
+  p.wq = wq, p.wk = wk, p.cos = cos, p.sin = sin, p.positions = positions;
+  p.part = static_cast<float*>(workspace);
+  p.eps = eps;
+  p.T = T, p.H = H, p.Hkv = Hkv, p.half = cos ? rope_dim / 2 : 0, p.max_pos = max_pos, p.seq_len = seq_len;
+  p.parts_q = (H + kHeads - 1) / kHeads, p.parts_k = (Hkv + kHeads - 1) / kHeads, p.ctas_q = g.ctas_q;
+  p.status = status;
+  cudaError_t e;
+  switch (d) {
+    case 64: e = launch_backward<64>(p, norm != 0, interleaved != 0, g.ctas, stream); break;
+    case 128: e = launch_backward<128>(p, norm != 0, interleaved != 0, g.ctas, stream); break;
+    default: e = launch_backward<256>(p, norm != 0, interleaved != 0, g.ctas, stream); break;
+  }
+  if (e == cudaSuccess && dw) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)d / 32, 2);
+    cfg.blockDim = dim3(32, 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, dw_kernel, (const float*)p.part, dwq, dwk, d, g.ctas_q, g.ctas);
+  }
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}

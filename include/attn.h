@@ -349,17 +349,163 @@ attn_status_t attn_fwd_splitkv_static(const void* q, const void* k, const void* 
                                       const float* descale_v, cudaStream_t stream);
 
 /*
+ * attn_qk_norm_rope — RMS norm of every head of the queries and keys, then the rotation by
+ * position, in one pass: the step between the projections and attn_fwd, attn_fwd_varlen,
+ * attn_paged_append or attn_fwd_paged. For each row x (one token of one head, d values):
+ *   u = x (mean(x^2) + eps)^(-1/2) w      (norm nonzero; else u = x)
+ *   y_a = u_a cos - u_b sin,  y_b = u_b cos + u_a sin   for the pairs (a, b) of the first rope_dim
+ *   values, the others unchanged.
+ * Computed in fp32, rounded once to bf16. The pages have no counterpart to this entry point.
+ *   q: DEVICE bf16, T tokens of H heads; row (t, h) begins at q + t * q_stride_t + h * q_stride_h
+ *      (elements, >= 0, multiples of 8), its d values are contiguous: q may be a part of a fused
+ *      projection. k likewise with Hkv heads; Hkv == 0 with k and k_out NULL for queries alone.
+ *   q_out [T, H, d], k_out [T, Hkv, d]: DEVICE bf16, contiguous. Each may be its own input if that is
+ *      contiguous too; otherwise outputs must not overlap the inputs or each other.
+ *   norm, wq, wk, eps: wq, wk DEVICE fp32 [d] or NULL (all ones); both NULL without norm. eps >= 0.
+ *   cos, sin: DEVICE fp32 [max_pos, rope_dim / 2], or both NULL for no rotation. rope_dim is a
+ *      multiple of 16, 16 <= rope_dim <= d. Pairs are (i, i + rope_dim / 2), or (2i, 2i + 1) when
+ *      interleaved is nonzero; pair i turns by the angle of column i.
+ *   positions: DEVICE int32 [T], the table row of each token; NULL: token t has position t % seq_len
+ *      (seq_len >= 1). A token whose position lies outside 0 .. max_pos - 1 is not written, and
+ *      attn_get_status reports ATTN_ERR_INVALID_ARG.
+ *   q, k, q_out, k_out, cos, sin 16-byte aligned; d in {64, 128, 256}.
+ * One kernel, asynchronous on stream, allocates nothing. INVALID_ARG for pointers, sizes, strides or
+ * overlaps against the above; UNSUPPORTED for other d or T (ceil(H / 4) + ceil(Hkv / 4)) >= 2^31.
+ */
+attn_status_t attn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int T, int H,
+                                int Hkv, int d, long long q_stride_t, long long q_stride_h,
+                                long long k_stride_t, long long k_stride_h, int norm,
+                                const float* wq, const float* wk, float eps, const float* cos,
+                                const float* sin, int rope_dim, int max_pos, int interleaved,
+                                const int* positions, int seq_len, cudaStream_t stream);
+
+/*
+ * attn_qk_norm_rope_bwd — gradients of attn_qk_norm_rope. With du the output's gradient turned
+ * back, r = (mean(x^2) + eps)^(-1/2), n = x r and g = du w:
+ *   dx = r (g - n mean(g n)),   dw = sum over tokens and heads of du n      (dx = du without norm).
+ *   q, k and their strides: the forward's inputs; not read, and may be NULL, without norm.
+ *   dq_out [T, H, d], dk_out [T, Hkv, d]: DEVICE bf16, contiguous, e.g. dq and dk of attn_bwd.
+ *   dq, dk: DEVICE bf16, contiguous, may be dq_out and dk_out themselves.
+ *   dwq, dwk: DEVICE fp32 [d], NULL exactly where wq, wk are.
+ *   workspace: DEVICE, 16-byte aligned, at least attn_qk_norm_rope_bwd_workspace_bytes(...) bytes, not
+ *      overlapping the rest; needed with weights only. Needs no initialisation; calls that may
+ *      overlap on the GPU (captured graphs included) need one each.
+ *   The rest as attn_qk_norm_rope (a token with a bad position adds nothing to dwq, dwk).
+ * One kernel, and with weights a second that adds the partial sums; no atomics, so the results are
+ * deterministic.
+ */
+size_t attn_qk_norm_rope_bwd_workspace_bytes(int T, int H, int Hkv, int d);
+attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out,
+                                    const void* dk_out, void* dq, void* dk, float* dwq, float* dwk,
+                                    int T, int H, int Hkv, int d, long long q_stride_t,
+                                    long long q_stride_h, long long k_stride_t, long long k_stride_h,
+                                    int norm, const float* wq, const float* wk, float eps,
+                                    const float* cos, const float* sin, int rope_dim, int max_pos,
+                                    int interleaved, const int* positions, int seq_len,
+                                    void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Paged key/value cache. "flash-attention-3" (ai.thesatyajit.com), "What is actually in the box", and
+ * "FlashAttention-3 Deep Dive" (mojostudio.in), FAQ on paged KV, name it: keys and values live in
+ * pages of page_size tokens, and a page table says which pages hold a sequence, in order.
+ *
+ * Logical layout [num_pages, page_size, Hkv, d] for k and for v, in any order of the first three
+ * dims: the strides say where row (page, token, head) begins, its d values are contiguous.
+ *   ATTN_CACHE_BF16: k, v bf16; strides in elements, multiples of 8.
+ *   ATTN_CACHE_INT4: k, v hold d / 2 bytes a row (dims 2i and 2i + 1 in the low and high half of byte
+ *     i); strides in bytes, multiples of 16. k_sz, v_sz: bf16 [num_pages, page_size, Hkv, d / 64, 2],
+ *     a (scale, zero) pair per 64 dims, with strides of their own in bf16 values, multiples of
+ *     2 (d / 64); aligned to d / 16 bytes. A value is zero + scale * code, code in 0 .. 15.
+ *     attn_paged_append writes zero = the group's least value rounded down to bf16, scale =
+ *     max((greatest - zero) / 15, 2^-20 max|.|, 2^-100) rounded up, code = (x - zero) / scale rounded
+ *     to nearest even: |x - value| <= scale / 2. Other writers need finite scales and zeros.
+ *   k and v (and k_sz and v_sz) share their strides. k, v 16-byte aligned; d in {64, 128, 256};
+ *   page_size a multiple of 16 (UNSUPPORTED otherwise).
+ * The struct is HOST memory, read during a call only.
+ *
+ * Page tables are DEVICE int32, row b of sequence b at page_table + b * table_stride, max_pages entries
+ * each; entries behind a sequence's last page are not read. An entry outside 0 .. num_pages - 1
+ * that a call would use, a length that max_pages cannot hold, or offsets that do not ascend never lead
+ * outside the cache: the rows concerned are not written (append, gather) or count as zeros (attention,
+ * where a length is cut to max_pages * page_size), and attn_get_status reports ATTN_ERR_INVALID_ARG.
+ */
+typedef enum { ATTN_CACHE_BF16 = 0, ATTN_CACHE_INT4 = 1 } attn_cache_type_t;
+
+typedef struct {
+  void *k, *v, *k_sz, *v_sz;                             /* k_sz, v_sz: ATTN_CACHE_INT4 only       */
+  long long page_stride, token_stride, head_stride;      /* of k and v                             */
+  long long sz_page_stride, sz_token_stride, sz_head_stride;
+  int num_pages, page_size, Hkv, d;
+  attn_cache_type_t type;
+} attn_paged_cache_t;
+
+/*
+ * attn_paged_append — stores new keys and values, keys turned by their position on the way.
+ * Packed token cu_seqlens[b] + i becomes position cache_lens[b] + i of sequence b.
+ *   k, v: DEVICE bf16 [total, Hkv, d] with token and head strides as in attn_qk_norm_rope, 16-byte
+ *      aligned, finite, not overlapping the cache.
+ *   cu_seqlens: DEVICE int32 [B + 1], ascending; tokens from cu_seqlens[B] on are not stored.
+ *   cache_lens: DEVICE int32 [B], tokens the cache holds already (the call does not change it).
+ *   cos, sin, rope_dim, max_pos, interleaved: as in attn_qk_norm_rope; NULL stores k as it is (keys that
+ *      attn_qk_norm_rope has turned). The rotated key is rounded to bf16 (bf16 cache), or quantised
+ *      from fp32 (4 bits).
+ *   No two tokens of a call may fall on one cache row (sequences that share a page they write to).
+ * One kernel, asynchronous on stream, allocates nothing; total == 0 returns ATTN_OK at once.
+ */
+attn_status_t attn_paged_append(const attn_paged_cache_t* cache, const void* k, const void* v,
+                                long long k_stride_t, long long k_stride_h, long long v_stride_t,
+                                long long v_stride_h, const int* cu_seqlens, const int* cache_lens,
+                                const int* page_table, long long table_stride, int max_pages, int B,
+                                int total, const float* cos, const float* sin, int rope_dim,
+                                int max_pos, int interleaved, cudaStream_t stream);
+
+/*
+ * attn_paged_gather — reads positions 0 .. cu_seqlens[b + 1] - cu_seqlens[b] - 1 of every sequence into
+ * packed k, v [total, Hkv, d] (DEVICE bf16, contiguous, 16-byte aligned, not overlapping each other or
+ * the cache): what attn_fwd_varlen reads, e.g. to prefill on top of a cached prefix. 4-bit values are
+ * rounded to bf16. Rows from cu_seqlens[B] on are left as they were. One kernel, as attn_paged_append.
+ */
+attn_status_t attn_paged_gather(const attn_paged_cache_t* cache, void* k, void* v,
+                                const int* cu_seqlens, const int* page_table, long long table_stride,
+                                int max_pages, int B, int total, cudaStream_t stream);
+
+/*
+ * attn_fwd_paged — attention of Nq query tokens a sequence (one when decoding, a few drafted ones) over
+ * the cache.
+ *   q, o: DEVICE bf16 [B, Nq, H, d], contiguous, 16-byte aligned; lse: DEVICE fp32 [B, H, Nq], natural
+ *      log. Query head h reads kv head h / (H / Hkv); H / Hkv may be any whole number.
+ *   seqlens: DEVICE int32 [B], keys of each sequence in the cache, the Nq new tokens' own among them.
+ *   causal: query i sees keys j <= i + seqlens[b] - Nq (bottom-right aligned, as attn_fwd_varlen);
+ *      otherwise all. Rows that see no key get O = 0, LSE = -inf, so a padded entry of the batch has
+ *      length 0.
+ *   scale as in attn_fwd (finite, nonzero).
+ *   workspace: DEVICE, 256-byte aligned, at least attn_fwd_paged_workspace_bytes(...) bytes, which do
+ *      not depend on the lengths; needs no initialisation. Calls that may overlap on the GPU (captured
+ *      graphs included) need one each. q, o, lse and workspace must not overlap.
+ * Lengths stay on the device: the call can be captured and replayed while they grow. Every call reads
+ * its keys and values ceil(Nq (H / Hkv) / R) times, R = 8 query rows, or 16 when there are more than 8
+ * and d <= 128. Deterministic. Two kernels, the second a programmatic dependent launch; allocates nothing.
+ */
+size_t attn_fwd_paged_workspace_bytes(int B, int H, int Hkv, int Nq, int d, attn_cache_type_t type);
+attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t* cache, void* o, float* lse,
+                             const int* page_table, long long table_stride, int max_pages,
+                             const int* seqlens, int B, int H, int Nq, float scale, int causal,
+                             void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * attn_get_status — synchronizes `stream`, then returns ATTN_ERR_TIMEOUT if any kernel of this
  * library on the current device gave up a bounded wait since the last attn_clear_status,
  * ATTN_ERR_INVALID_ARG if a varlen forward was handed a plan that does not match it (or that the
- * plan builder marked invalid), ATTN_ERR_CUDA if the synchronization failed, else ATTN_OK.
+ * plan builder marked invalid), or a paged-cache or rotation call met a page, position or offset out
+ * of range, ATTN_ERR_CUDA if the synchronization failed, else ATTN_OK.
  */
 attn_status_t attn_get_status(cudaStream_t stream);
 
 /*
  * attn_get_status_detail — attn_get_status that also stores the raw device status word in
- * `detail` (may be NULL): 0, 0x40000000 | the code of the wait site that gave up, or 0x2000000C
- * for a rejected varlen plan. 0 is stored when the synchronization fails.
+ * `detail` (may be NULL): 0, 0x40000000 | the code of the wait site that gave up, 0x2000000C
+ * for a rejected varlen plan, 0x2000000D for a page, length or offset of a paged-cache call out of
+ * range, or 0x2000000E for a rotation position outside its tables. 0 is stored when the synchronization fails.
  */
 attn_status_t attn_get_status_detail(cudaStream_t stream, uint32_t* detail);
 
