@@ -136,7 +136,9 @@ def _dtype_code(t) -> int:
 
 def _stream_handle(stream) -> int:
     import torch
-    if stream is None:
+    if stream is None:   # the current stream's handle without a stream object: called on every launch
+        if torch.cuda.is_initialized():
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream)
 
@@ -495,17 +497,14 @@ def attn_fwd_host_workspace_bytes(B: int, H: int, Hkv: int, N: int, d: int, dtyp
     return int(lib().attn_fwd_host_workspace_bytes(B, H, Hkv, N, d, dtype_code))
 
 
-def _on_current_device(tensors):
-    """Kernels launch on the current device: its tensors only."""
+def _on_current_device(*tensors):
+    """Kernels launch on the current device: its tensors only (None stands for one that is not given)."""
     import torch
-    dev = None
-    for name, t in tensors:
-        if t is None:
-            continue
-        if t.is_cuda and dev is None:
-            dev = torch.cuda.current_device()
-        if not t.is_cuda or t.device.index != dev:
-            raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("every tensor of a call must be a CUDA tensor on the current device, "
+                             f"got one on {t.device}")
 
 
 def _buffer(shape, dtype, device, stream):
@@ -520,68 +519,78 @@ def _buffer(shape, dtype, device, stream):
 def _rows(name, t, heads=None, d=None):
     """(tokens, token stride, head stride) of bf16 rows [T, heads, d] or [B, N, heads, d], last dim contiguous."""
     import torch
-    if t.dtype != torch.bfloat16 or t.dim() not in (3, 4) or t.stride(-1) != 1:
+    shape, stride = t.shape, t.stride()
+    dim = len(shape)
+    if t.dtype != torch.bfloat16 or (dim != 3 and dim != 4) or stride[-1] != 1:
         raise ValueError(f"{name} must be a bfloat16 CUDA tensor [T, heads, d] or [B, N, heads, d] with contiguous rows")
-    if heads is not None and (t.shape[-2], t.shape[-1]) != (heads, d):
+    if heads is not None and (shape[-2] != heads or shape[-1] != d):
         raise ValueError(f"{name} must have {heads} heads of {d} values")
-    if t.dim() == 3:
-        return t.shape[0], t.stride(0), t.stride(1)
-    B, N = t.shape[:2]
+    if dim == 3:
+        return shape[0], stride[0], stride[1]
+    B, N = shape[0], shape[1]
     if N == 1:
-        return B, t.stride(0), t.stride(2)
-    if B > 1 and t.stride(0) != N * t.stride(1):
+        return B, stride[0], stride[2]
+    if B > 1 and stride[0] != N * stride[1]:
         raise ValueError(f"the tokens of {name} must be evenly spaced over the batch")
-    return B * N, t.stride(1), t.stride(2)
+    return B * N, stride[1], stride[2]
 
 
-def _rope_args(cos, sin, d):
+def _rope_args(cos, sin):
     """(cos pointer, sin pointer, rope_dim, max_pos) of angle tables [max_pos, rope_dim / 2]."""
     import torch
     if cos is None and sin is None:
         return 0, 0, 0, 0
-    for name, t in (("cos", cos), ("sin", sin)):
-        if t is None or t.dtype != torch.float32 or t.dim() != 2 or not t.is_contiguous() or t.shape != cos.shape:
-            raise ValueError(f"{name} must be a contiguous float32 CUDA tensor [max_pos, rope_dim / 2], as its partner")
-    return cos.data_ptr(), sin.data_ptr(), 2 * cos.shape[1], cos.shape[0]
+    if cos is None or sin is None or cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.dim() != 2 or \
+            cos.shape != sin.shape or not cos.is_contiguous() or not sin.is_contiguous():
+        raise ValueError("cos and sin must be contiguous float32 CUDA tensors [max_pos, rope_dim / 2], both or neither")
+    max_pos, half = cos.shape
+    return cos.data_ptr(), sin.data_ptr(), 2 * half, max_pos
+
+
+def _weight(name, w, d):
+    """Pointer of a float32 [d] tensor, None for None."""
+    import torch
+    if w is None:
+        return None
+    if w.dtype != torch.float32 or w.shape != (d,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of d values")
+    return w.data_ptr()
 
 
 def _norm_rope_args(q, k, cos, sin, positions, wq, wk, norm):
-    """Checks that the forward and the backward share; (T, H, Hkv, d, strides, weights, rope, positions, seq_len)."""
+    """Checks that the forward and the backward share: sizes (T, H, Hkv, d) and the C arguments from the strides to wk
+    and from cos to max_pos, the positions and the sequence length."""
     import torch
-    H, d = q.shape[-2:]
-    Hkv = 0
+    shape = q.shape
     T, q_st, q_sh = _rows("q", q)
-    k_st = k_sh = 0
+    H, d = shape[-2:]
+    Hkv = k_st = k_sh = 0
     if k is not None:
-        if k.shape[:-2] != q.shape[:-2]:
+        if k.shape[:-2] != shape[:-2]:
             raise ValueError("q and k must hold the same tokens")
         Hkv = k.shape[-2]
         _, k_st, k_sh = _rows("k", k, Hkv, d)
-    for name, w in (("wq", wq), ("wk", wk)):
-        if w is not None and (w.dtype != torch.float32 or w.shape != (d,) or not w.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of d values")
-    if wk is not None and k is None:
+    elif wk is not None:
         raise ValueError("wk needs k")
-    if positions is not None and (positions.dtype != torch.int32 or positions.shape != q.shape[:-2] or
-                                  not positions.is_contiguous()):
-        raise ValueError("positions must be a contiguous int32 CUDA tensor, one per token")
-    _on_current_device((("q", q), ("k", k), ("cos", cos), ("sin", sin), ("positions", positions), ("wq", wq),
-                        ("wk", wk)))
-    c, s, rope_dim, max_pos = _rope_args(cos, sin, d)
-    seq_len = q.shape[1] if q.dim() == 4 else T
-    tail = (int(bool(norm)), wq.data_ptr() if wq is not None else None, wk.data_ptr() if wk is not None else None)
-    return T, H, Hkv, d, (q_st, q_sh, k_st, k_sh), tail, (c, s, rope_dim, max_pos), \
-        positions.data_ptr() if positions is not None else None, seq_len
+    pos = None
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.shape != shape[:-2] or not positions.is_contiguous():
+            raise ValueError("positions must be a contiguous int32 CUDA tensor, one per token")
+        pos = positions.data_ptr()
+    wp = _weight("wq", wq, d), _weight("wk", wk, d)
+    rope = _rope_args(cos, sin)
+    _on_current_device(q, k, cos, sin, positions, wq, wk)
+    return (T, H, Hkv, d), (q_st, q_sh, k_st, k_sh, 1 if norm else 0, *wp), rope, pos, shape[1] if len(shape) == 4 else T
 
 
 def _out_rows(name, t, like, stream):
     """An output with the shape of ``like``, contiguous: ``t`` if given."""
     import torch
     if t is None:
-        return _buffer(tuple(like.shape), torch.bfloat16, like.device, stream)
+        return _buffer(like.shape, torch.bfloat16, like.device, stream)
     if t.shape != like.shape or t.dtype != torch.bfloat16 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor of shape {tuple(like.shape)}")
-    _on_current_device(((name, t),))
+    _on_current_device(t)
     return t
 
 
@@ -596,17 +605,17 @@ def attn_qk_norm_rope(q, k=None, cos=None, sin=None, positions=None, wq=None, wk
     in the sequence. ``wq`` and ``wk`` (float32 [d]) weigh the normalised values; ``norm=False`` only
     rotates. Outputs are contiguous; each may be its own contiguous input.
     """
-    T, H, Hkv, d, strides, tail, rope, pos, seq_len = _norm_rope_args(q, k, cos, sin, positions, wq, wk, norm)
+    sizes, rows, rope, pos, seq_len = _norm_rope_args(q, k, cos, sin, positions, wq, wk, norm)
     if k is None and k_out is not None:
         raise ValueError("k_out needs k")
     q_out = _out_rows("q_out", q_out, q, stream)
     if k is not None:
         k_out = _out_rows("k_out", k_out, k, stream)
-    if T == 0:
+    if sizes[0] == 0:
         return q_out, k_out
     st = lib().attn_qk_norm_rope(q.data_ptr(), k.data_ptr() if k is not None else None, q_out.data_ptr(),
-                                 k_out.data_ptr() if k is not None else None, T, H, Hkv, d, *strides, *tail,
-                                 float(eps), *rope, int(bool(interleaved)), pos, seq_len, _stream_handle(stream))
+                                 k_out.data_ptr() if k is not None else None, *sizes, *rows, eps, *rope,
+                                 1 if interleaved else 0, pos, seq_len, _stream_handle(stream))
     _check(st, "attn_qk_norm_rope")
     return q_out, k_out
 
@@ -621,47 +630,39 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out=None, cos=None, sin=None, positio
     """Gradients (dq, dk, dwq, dwk) of attn_qk_norm_rope for the gradients of its outputs (contiguous, e.g.
     from attn_bwd); dwq and dwk are float32 [d], None without weights. dq and dk may be dq_out and dk_out."""
     import torch
-    T, H, Hkv, d, strides, tail, rope, pos, seq_len = _norm_rope_args(q, k, cos, sin, positions, wq, wk, norm)
+    sizes, rows, rope, pos, seq_len = _norm_rope_args(q, k, cos, sin, positions, wq, wk, norm)
+    T, d = sizes[0], sizes[3]
     for name, g, x in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
         if (g is None) != (x is None) or (g is not None and (g.shape != x.shape or g.dtype != torch.bfloat16 or
                                                              not g.is_contiguous())):
             raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor like its input")
     if (dk is not None and k is None) or (dwq is not None and wq is None) or (dwk is not None and wk is None):
         raise ValueError("dk needs k, dwq needs wq and dwk needs wk")
-    _on_current_device((("dq_out", dq_out), ("dk_out", dk_out)))
     dq = _out_rows("dq", dq, q, stream)
     if k is not None:
         dk = _out_rows("dk", dk, k, stream)
-    ptrs = []
-    grads = []
-    for name, g, w in (("dwq", dwq, wq), ("dwk", dwk, wk)):
-        if w is not None and g is None:
-            g = _buffer((d,), torch.float32, q.device, stream)
-        elif g is not None:
-            if g.dtype != torch.float32 or g.shape != (d,) or not g.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of d values")
-            _on_current_device(((name, g),))
-        grads.append(g)
-        ptrs.append(None if g is None else g.data_ptr())
+    need = attn_qk_norm_rope_bwd_workspace_bytes(*sizes) if wq is not None or wk is not None else 0
+    if (wq is not None and dwq is None) or (wk is not None and dwk is None):
+        own = _buffer((2, d), torch.float32, q.device, stream)
+        dwq = own[0] if wq is not None and dwq is None else dwq
+        dwk = own[1] if wk is not None and dwk is None else dwk
     if T == 0:
-        for g in grads:
-            if g is not None:
-                with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+            for g in (dwq, dwk):
+                if g is not None:
                     g.zero_()
-        return dq, dk, grads[0], grads[1]
-    if workspace is None:
-        if wq is not None or wk is not None:
-            workspace = _buffer((attn_qk_norm_rope_bwd_workspace_bytes(T, H, Hkv, d),), torch.uint8, q.device, stream)
-    else:
-        _on_current_device((("workspace", workspace),))
+        return dq, dk, dwq, dwk
+    if workspace is None and need:
+        workspace = _buffer((need,), torch.uint8, q.device, stream)
+    _on_current_device(dq_out, dk_out, dwq, dwk, workspace)
     ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     st = lib().attn_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr() if k is not None else None, dq_out.data_ptr(),
                                      dk_out.data_ptr() if k is not None else None, dq.data_ptr(),
-                                     dk.data_ptr() if k is not None else None, *ptrs, T, H, Hkv, d, *strides, *tail,
-                                     float(eps), *rope, int(bool(interleaved)), pos, seq_len, *ws,
-                                     _stream_handle(stream))
+                                     dk.data_ptr() if k is not None else None, _weight("dwq", dwq, d),
+                                     _weight("dwk", dwk, d), *sizes, *rows, eps, *rope, 1 if interleaved else 0, pos,
+                                     seq_len, *ws, _stream_handle(stream))
     _check(st, "attn_qk_norm_rope_bwd")
-    return dq, dk, grads[0], grads[1]
+    return dq, dk, dwq, dwk
 
 
 class PagedKVCache:
@@ -720,17 +721,18 @@ class PagedKVCache:
                    make(d // ATTN_INT4_GROUP, 2, dtype=torch.bfloat16))
 
 
-def _paged_args(cache, page_table, **vectors):
-    """Checks of a call on ``cache``: the page table and int32 vectors (name=(tensor, length or None)). The batch B."""
+def _paged_args(cache, page_table, *vectors):
+    """Checks of a call on ``cache``: the page table and int32 vectors (name, tensor, entries more than B). The C arguments
+    (page table, stride, max_pages, B)."""
     import torch
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1 and page_table.shape[1] > 1:
+    int32 = torch.int32
+    if page_table.dtype != int32 or page_table.dim() != 2 or (page_table.stride(1) != 1 and page_table.shape[1] > 1):
         raise ValueError("page_table must be an int32 CUDA tensor [B, max_pages] with contiguous rows")
-    B = page_table.shape[0]
-    for name, (t, extra) in vectors.items():
-        if t.dtype != torch.int32 or t.shape != (B + extra,) or not t.is_contiguous():
+    B, max_pages = page_table.shape
+    for name, t, extra in vectors:
+        if t.dtype != int32 or t.shape != (B + extra,) or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {B + extra} values")
-    _on_current_device([("cache", cache.k), ("page_table", page_table)] + [(n, t) for n, (t, _) in vectors.items()])
-    return B
+    return page_table.data_ptr(), page_table.stride(0), max_pages, B
 
 
 def attn_paged_append(cache: PagedKVCache, k, v, cu_seqlens, cache_lens, page_table, cos=None, sin=None,
@@ -742,18 +744,17 @@ def attn_paged_append(cache: PagedKVCache, k, v, cu_seqlens, cache_lens, page_ta
     way (cos and sin as in attn_qk_norm_rope; None: k is stored as it is). Tokens from cu_seqlens[B] on are
     not stored. Lengths stay as they are: the caller advances cache_lens.
     """
-    B = _paged_args(cache, page_table, cu_seqlens=(cu_seqlens, 1), cache_lens=(cache_lens, 0))
-    if k.dim() != 3 or v.dim() != 3 or k.shape[0] != v.shape[0]:
-        raise ValueError("k and v must be [total, Hkv, d]")
+    table = _paged_args(cache, page_table, ("cu_seqlens", cu_seqlens, 1), ("cache_lens", cache_lens, 0))
     total, k_st, k_sh = _rows("k", k, cache.Hkv, cache.d)
-    _, v_st, v_sh = _rows("v", v, cache.Hkv, cache.d)
-    _on_current_device((("k", k), ("v", v), ("cos", cos), ("sin", sin)))
-    c, s, rope_dim, max_pos = _rope_args(cos, sin, cache.d)
-    if total == 0 or B == 0:
+    v_total, v_st, v_sh = _rows("v", v, cache.Hkv, cache.d)
+    if total != v_total or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("k and v must be [total, Hkv, d]")
+    rope = _rope_args(cos, sin)
+    _on_current_device(cache.k, page_table, cu_seqlens, cache_lens, k, v, cos, sin)
+    if total == 0 or table[3] == 0:
         return
     st = lib().attn_paged_append(cache._ref, k.data_ptr(), v.data_ptr(), k_st, k_sh, v_st, v_sh, cu_seqlens.data_ptr(),
-                                 cache_lens.data_ptr(), page_table.data_ptr(), page_table.stride(0),
-                                 page_table.shape[1], B, total, c, s, rope_dim, max_pos, int(bool(interleaved)),
+                                 cache_lens.data_ptr(), *table, total, *rope, 1 if interleaved else 0,
                                  _stream_handle(stream))
     _check(st, "attn_paged_append")
 
@@ -762,23 +763,22 @@ def attn_paged_gather(cache: PagedKVCache, cu_seqlens, page_table, total: int, k
     """(k, v), bf16 [total, Hkv, d]: positions 0 .. cu_seqlens[b + 1] - cu_seqlens[b] - 1 of every sequence read
     out of the cache, packed as attn_fwd_varlen takes them. Rows from cu_seqlens[B] on are left as they were."""
     import torch
-    B = _paged_args(cache, page_table, cu_seqlens=(cu_seqlens, 1))
+    table = _paged_args(cache, page_table, ("cu_seqlens", cu_seqlens, 1))
     shape = (total, cache.Hkv, cache.d)
-    outs = []
+    if k is None:
+        k = _buffer(shape, torch.bfloat16, cache.device, stream)
+    if v is None:
+        v = _buffer(shape, torch.bfloat16, cache.device, stream)
     for name, t in (("k", k), ("v", v)):
-        if t is None:
-            t = _buffer(shape, torch.bfloat16, cache.device, stream)
-        elif t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous():
+        if t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor of shape {shape}")
-        outs.append(t)
-    _on_current_device((("k", outs[0]), ("v", outs[1])))
-    if total == 0 or B == 0:
-        return outs[0], outs[1]
-    st = lib().attn_paged_gather(cache._ref, outs[0].data_ptr(), outs[1].data_ptr(), cu_seqlens.data_ptr(),
-                                 page_table.data_ptr(), page_table.stride(0), page_table.shape[1], B, total,
+    _on_current_device(cache.k, page_table, cu_seqlens, k, v)
+    if total == 0 or table[3] == 0:
+        return k, v
+    st = lib().attn_paged_gather(cache._ref, k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), *table, total,
                                  _stream_handle(stream))
     _check(st, "attn_paged_gather")
-    return outs[0], outs[1]
+    return k, v
 
 
 def attn_fwd_paged_workspace_bytes(cache: PagedKVCache, B: int, H: int, Nq: int) -> int:
@@ -797,25 +797,25 @@ def attn_fwd_paged(q, cache: PagedKVCache, page_table, seqlens, causal: bool = T
     if q.dim() != 4 or q.dtype != torch.bfloat16 or not q.is_contiguous():
         raise ValueError("q must be a contiguous bfloat16 CUDA tensor [B, Nq, H, d]")
     B, Nq, H, d = q.shape
-    if _paged_args(cache, page_table, seqlens=(seqlens, 0)) != B or d != cache.d or H % cache.Hkv != 0:
+    table = _paged_args(cache, page_table, ("seqlens", seqlens, 0))
+    if table[3] != B or d != cache.d or H % cache.Hkv != 0:
         raise ValueError("q must be [B, Nq, H, d] with the page table's B, the cache's d and a multiple of its heads")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if workspace is None:
         workspace = _buffer((max(attn_fwd_paged_workspace_bytes(cache, B, H, Nq), 1),), torch.uint8, q.device, stream)
     if out is None:
-        out = _buffer((B, Nq, H, d), torch.bfloat16, q.device, stream)
+        out = _buffer(q.shape, torch.bfloat16, q.device, stream)
     elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError("out must be a contiguous bfloat16 CUDA tensor like q")
     if lse is None:
         lse = _buffer((B, H, Nq), torch.float32, q.device, stream)
     elif lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 CUDA tensor [B, H, Nq]")
-    _on_current_device((("q", q), ("workspace", workspace), ("out", out), ("lse", lse)))
-    st = lib().attn_fwd_paged(q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(), page_table.data_ptr(),
-                              page_table.stride(0), page_table.shape[1], seqlens.data_ptr(), B, H, Nq, float(scale),
-                              int(bool(causal)), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                              _stream_handle(stream))
+    _on_current_device(cache.k, page_table, seqlens, q, workspace, out, lse)
+    st = lib().attn_fwd_paged(q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(), *table[:3], seqlens.data_ptr(), B,
+                              H, Nq, scale, 1 if causal else 0, workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), _stream_handle(stream))
     _check(st, "attn_fwd_paged")
     return out, lse
 

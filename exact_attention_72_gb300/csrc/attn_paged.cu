@@ -76,6 +76,7 @@ struct Params {
   const int *table, *lens;
   long long table_stride;
   int B, H, G, Nq, max_pages, row_blocks, causal;
+  uint32_t div_mul, div_shift;   // 16-key block / (page_size / 16) by a product (page_of_block)
   float scale_log2;
   float* part_o;     // [2 CTAs, ROWS, D] normalised O of a cut unit's parts
   float* part_lse;   // [2 CTAs, ROWS] their log2-sum-exp2
@@ -110,6 +111,20 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 x;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a) : "memory");
   return x;
+}
+
+// The (scale, zero) pairs of a row.
+template <int N>
+__device__ __forceinline__ void load_pairs(uint32_t (&x)[N], uint32_t a) {
+  if constexpr (N == 1) {
+    x[0] = lds32(a);
+  } else if constexpr (N == 2) {
+    const uint2 w = lds64(a);
+    x[0] = w.x, x[1] = w.y;
+  } else {
+    const uint4 w = lds128(a);
+    x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+  }
 }
 
 template <bool F16>
@@ -159,6 +174,11 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
 
 // Key of the 16-key block that the MMA's row i stands for.
 __device__ __forceinline__ int key_of_row(int i) { return (i & 8) | ((i & 7) >> 1) | ((i & 1) << 2); }
+
+// Page of a sequence that its 16-key block lies in: block / (page_size / 16), for blocks below 2^31.
+__device__ __forceinline__ int page_of_block(const Params& p, uint32_t block) {
+  return (int)((__umulhi(p.div_mul, block) + block) >> p.div_shift);
+}
 
 // Keys that some row of sequence b sees at most, and its pieces of work (at least one: a unit without
 // keys still writes its zeros).
@@ -242,38 +262,47 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
     const uint8_t* vsz = p.c.v_sz + hkv * p.c.sz_head_b;
     const int* pages = p.table + b * p.table_stride;
 
-    // Page of a tile's 16-key block `lane`; the copies of a tile use it one tile later.
-    auto look_up = [&](int n) -> int {
+    // A tile's copies: lane i < KB finds where 16-key block i begins (bytes into k and v, and into the
+    // pairs; -1: nowhere), one tile ahead of the copies themselves.
+    struct Place {
+      long long row, sz;
+    };
+    const int blocks_per_page = p.c.page_size >> 4;
+    auto look_up = [&](int n) -> Place {
       const int key = key0 + n * C::SPLIT + lane * 16;
-      int page = -1;
+      Place at{-1, -1};
       if (lane < KB && n < tiles && key < keys) {
-        page = pages[key / p.c.page_size];
-        if (page < 0 || page >= p.c.num_pages) {
+        const int block = key >> 4, e = page_of_block(p, block), page = pages[e];
+        const int in_page = (block - e * blocks_per_page) << 4;
+        if (page >= 0 && page < p.c.num_pages) {
+          at.row = page * p.c.page_b + in_page * p.c.token_b;
+          if (INT4) at.sz = page * p.c.sz_page_b + in_page * p.c.sz_token_b;
+        } else {
           atomicCAS(p.status, 0u, kStatusBadPage);
-          page = -1;
         }
       }
-      return page;
+      return at;
     };
-    auto fetch = [&](int n, int page_of_block) {
+    constexpr int CH = C::ROWB / 16, RPI = 32 / CH;   // chunks of a row, rows of one copy instruction
+    const long long my_row = (lane / CH) * p.c.token_b + lane % CH * 16;
+    auto fetch = [&](int n, const Place& place) {
       if (n < tiles) {
         const uint32_t dst = buf + n % C::STAGES * C::STAGE;
-        const int key = key0 + n * C::SPLIT;
-        constexpr int CH = C::ROWB / 16;   // chunks of a row
+        const int valid = keys - (key0 + n * C::SPLIT);
 #pragma unroll
-        for (int i = 0; i < KT * CH / 32; ++i) {
-          const int r = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
-          const int page = __shfl_sync(0xffffffffu, page_of_block, r / 16);
-          const bool in = page >= 0 && key + r < keys;
-          const long long row = in ? page * p.c.page_b + (key + r) % p.c.page_size * p.c.token_b + ch * 16 : 0;
-          const uint32_t d = dst + chunk_at<C::ROWB>(r, ch);
+        for (int i = 0; i < KT / RPI; ++i) {
+          const int r = i * RPI + lane / CH;
+          const long long base = __shfl_sync(0xffffffffu, place.row, i * RPI / 16);
+          const bool in = base >= 0 && r < valid;
+          const long long row = in ? base + my_row + i * RPI % 16 * p.c.token_b : 0;
+          const uint32_t d = dst + chunk_at<C::ROWB>(r, lane % CH);
           copy16(d, kbase + row, in);
           copy16(d + C::V_OFF, vbase + row, in);
         }
         if constexpr (INT4) {
-          const int page = __shfl_sync(0xffffffffu, page_of_block, lane / 16);
-          const bool in = page >= 0 && key + lane < keys;
-          const long long row = in ? page * p.c.sz_page_b + (key + lane) % p.c.page_size * p.c.sz_token_b : 0;
+          const long long base = __shfl_sync(0xffffffffu, place.sz, lane / 16);
+          const bool in = base >= 0 && lane < valid;
+          const long long row = in ? base + lane % 16 * p.c.sz_token_b : 0;
           copy_small<C::SZB>(dst + C::KSZ_OFF + lane * C::SZB, ksz + row, in);
           copy_small<C::SZB>(dst + C::VSZ_OFF + lane * C::SZB, vsz + row, in);
         }
@@ -281,10 +310,10 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
       copies_commit();
     };
 
-    int page = look_up(0);
+    Place page = look_up(0);
 #pragma unroll
     for (int n = 0; n < C::STAGES - 1; ++n) {
-      const int next = look_up(n + 1);
+      const Place next = look_up(n + 1);
       fetch(n, page);
       page = next;
     }
@@ -292,8 +321,9 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
     // Query rows as the B operand: lane (g, t) holds row g's values that its K bytes are paired with.
     constexpr int QR = D / 16;
     uint32_t qf[NT][QR][2];
-    float mult[NT][2];            // S = mult * product, per column 2t, 2t + 1
-    float qsum[NT][GROUPS][2];    // 4 bits: scaled sums of q over a group
+    float mult[NT][2];            // S = mult * (what the products give), per column 2t, 2t + 1
+    float qsum[NT][GROUPS][2];    // 4 bits: sums of q over a group, in units of the products
+    float out[NT][2];             // what a masked product is set to, so that S is -inf
     int limit[NT][2];             // keys the column's row sees: key < limit
     int least = INT_MAX;
 #pragma unroll
@@ -347,8 +377,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
             }
           }
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            qsum[nt][gr][j] = __shfl_sync(0xffffffffu, sum[gr], (2 * t + j) * 4) * p.scale_log2;
+          for (int j = 0; j < 2; ++j) qsum[nt][gr][j] = __shfl_sync(0xffffffffu, sum[gr] * down * 0x1p-24f, (2 * t + j) * 4);
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) mult[nt][j] = __shfl_sync(0xffffffffu, up, (2 * t + j) * 4) * p.scale_log2 * 0x1p24f;
@@ -366,6 +395,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int c = row0 + nt * 8 + 2 * t + j;
+        if (mult[nt][j] == 0.f) mult[nt][j] = 0x1p-126f;   // 0 times the masked infinity would be NaN
+        out[nt][j] = mult[nt][j] < 0.f ? INFINITY : -INFINITY;
         limit[nt][j] = p.causal ? (c < rows ? keys - p.Nq + 1 + c / p.G : keys) : keys;
         least = min(least, limit[nt][j]);
       }
@@ -394,13 +425,14 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
       copies_wait<C::STAGES - 2>();
       __syncwarp();
       {
-        const int next = look_up(n + C::STAGES);
+        const Place next = look_up(n + C::STAGES);
         fetch(n + C::STAGES - 1, page);
         page = next;
       }
       const uint32_t tile = buf + n % C::STAGES * C::STAGE;
       const int tile_key = key0 + n * C::SPLIT;
       float s[KB][NT][4], ev[KB][2];
+      uint32_t vs[KB][2][GROUPS];   // (scale, zero) of my two values' rows
       // S^T = K q^T
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
@@ -410,43 +442,46 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[kb][nt][j] = 0.f;
         if constexpr (INT4) {
-          float e0 = kMinExp, e1 = kMinExp;
+          uint32_t ks[2][GROUPS];
+          load_pairs<GROUPS>(ks[0], tile + C::KSZ_OFF + r0 * C::SZB);
+          load_pairs<GROUPS>(ks[1], tile + C::KSZ_OFF + r1 * C::SZB);
+          load_pairs<GROUPS>(vs[kb][0], tile + C::VSZ_OFF + r0 * C::SZB);
+          load_pairs<GROUPS>(vs[kb][1], tile + C::VSZ_OFF + r1 * C::SZB);
 #pragma unroll
           for (int gr = 0; gr < GROUPS; ++gr) {
             const uint32_t place = (t & 1) * 8;
             const uint2 w0 = lds64(tile + chunk_at<C::ROWB>(r0, gr * 2 + (t >> 1)) + place);
             const uint2 w1 = lds64(tile + chunk_at<C::ROWB>(r1, gr * 2 + (t >> 1)) + place);
-            const uint32_t sz0 = lds32(tile + C::KSZ_OFF + r0 * C::SZB + gr * 4);
-            const uint32_t sz1 = lds32(tile + C::KSZ_OFF + r1 * C::SZB + gr * 4);
-            const uint32_t sv0 = lds32(tile + C::VSZ_OFF + r0 * C::SZB + gr * 4);
-            const uint32_t sv1 = lds32(tile + C::VSZ_OFF + r1 * C::SZB + gr * 4);
             float c[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int j = 0; j < 4; ++j) c[nt][j] = 0.f;
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-              const uint32_t x0 = (ks < 2 ? w0.x : w0.y) >> (ks % 2 * 8), x1 = (ks < 2 ? w1.x : w1.y) >> (ks % 2 * 8);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t x0 = (k < 2 ? w0.x : w0.y) >> (k % 2 * 8), x1 = (k < 2 ? w1.x : w1.y) >> (k % 2 * 8);
               const uint32_t a0 = x0 & 0x000f000fu, a1 = x1 & 0x000f000fu, a2 = x0 & 0x00f000f0u, a3 = x1 & 0x00f000f0u;
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma<true>(c[nt], a0, a1, a2, a3, qf[nt][gr * 4 + ks][0], qf[nt][gr * 4 + ks][1]);
+              for (int nt = 0; nt < NT; ++nt) mma<true>(c[nt], a0, a1, a2, a3, qf[nt][gr * 4 + k][0], qf[nt][gr * 4 + k][1]);
             }
-            const float sc0 = __uint_as_float(sz0 << 16), zr0 = __uint_as_float(sz0 & 0xffff0000u);
-            const float sc1 = __uint_as_float(sz1 << 16), zr1 = __uint_as_float(sz1 & 0xffff0000u);
+            const float sc0 = __uint_as_float(ks[0][gr] << 16), zr0 = __uint_as_float(ks[0][gr] & 0xffff0000u);
+            const float sc1 = __uint_as_float(ks[1][gr] << 16), zr1 = __uint_as_float(ks[1][gr] & 0xffff0000u);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                s[kb][nt][j] += c[nt][j] * mult[nt][j] * sc0 + zr0 * qsum[nt][gr][j];
-                s[kb][nt][2 + j] += c[nt][2 + j] * mult[nt][j] * sc1 + zr1 * qsum[nt][gr][j];
+                s[kb][nt][j] = fmaf(c[nt][j], sc0, fmaf(zr0, qsum[nt][gr][j], s[kb][nt][j]));
+                s[kb][nt][2 + j] = fmaf(c[nt][2 + j], sc1, fmaf(zr1, qsum[nt][gr][j], s[kb][nt][2 + j]));
               }
-            // exponent of the value scale, one more so that scale 2^-e < 1
-            e0 = fmaxf(e0, (float)((int)((sv0 >> 7) & 0xffu) - 126));
-            e1 = fmaxf(e1, (float)((int)((sv1 >> 7) & 0xffu) - 126));
           }
-          ev[kb][0] = e0;
-          ev[kb][1] = e1;
+          // exponent of the greatest value scale, one more so that scale 2^-e < 1
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t e = 0;
+#pragma unroll
+            for (int gr = 0; gr < GROUPS; ++gr) e = max(e, vs[kb][i][gr] & 0x7f80u);
+            ev[kb][i] = fmaxf(__uint_as_float(0x4b000000u | (e >> 7)) - (0x1p23f + 126.f), kMinExp);
+          }
         } else {
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
@@ -457,10 +492,6 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
               mma<false>(s[kb][nt], x0.z, x1.z, x0.w, x1.w, qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
             }
           }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[kb][nt][j] *= mult[nt][j & 1];
           ev[kb][0] = ev[kb][1] = 0.f;
         }
         if (tile_key + KT > least) {   // the same for the whole warp
@@ -468,8 +499,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              if (tile_key + r0 >= limit[nt][j]) s[kb][nt][j] = -INFINITY;
-              if (tile_key + r1 >= limit[nt][j]) s[kb][nt][2 + j] = -INFINITY;
+              if (tile_key + r0 >= limit[nt][j]) s[kb][nt][j] = out[nt][j];
+              if (tile_key + r1 >= limit[nt][j]) s[kb][nt][2 + j] = out[nt][j];
             }
         }
       }
@@ -481,7 +512,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
         for (int j = 0; j < 2; ++j) {
           float x = -INFINITY;
 #pragma unroll
-          for (int kb = 0; kb < KB; ++kb) x = fmaxf(x, fmaxf(s[kb][nt][j] + ev[kb][0], s[kb][nt][2 + j] + ev[kb][1]));
+          for (int kb = 0; kb < KB; ++kb)
+            x = fmaxf(x, fmaxf(fmaf(s[kb][nt][j], mult[nt][j], ev[kb][0]), fmaf(s[kb][nt][2 + j], mult[nt][j], ev[kb][1])));
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
           top[j] = fmaxf(x, m[nt][j]);
@@ -506,8 +538,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
           const float ref = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb) {
-            s[kb][nt][j] = exp2_fast(s[kb][nt][j] - ref);
-            s[kb][nt][2 + j] = exp2_fast(s[kb][nt][2 + j] - ref);
+            s[kb][nt][j] = exp2_fast(fmaf(s[kb][nt][j], mult[nt][j], -ref));
+            s[kb][nt][2 + j] = exp2_fast(fmaf(s[kb][nt][2 + j], mult[nt][j], -ref));
             l[nt][j] += s[kb][nt][j] + s[kb][nt][2 + j];
           }
         }
@@ -515,12 +547,11 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
       // O^T += V^T P^T
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
-        const int r0 = kb * 16 + key_of_row(g), r1 = r0 + 8, v0 = kb * 16 + t;
+        const int v0 = kb * 16 + t;
         if constexpr (INT4) {
 #pragma unroll
           for (int gr = 0; gr < GROUPS; ++gr) {
-            const uint32_t sv0 = lds32(tile + C::VSZ_OFF + r0 * C::SZB + gr * 4);
-            const uint32_t sv1 = lds32(tile + C::VSZ_OFF + r1 * C::SZB + gr * 4);
+            const uint32_t sv0 = vs[kb][0][gr], sv1 = vs[kb][1][gr];
             const float sc0 = __uint_as_float(sv0 << 16), zr0 = __uint_as_float(sv0 & 0xffff0000u);
             const float sc1 = __uint_as_float(sv1 << 16), zr1 = __uint_as_float(sv1 & 0xffff0000u);
             uint32_t b0[NT], b1[NT];
@@ -837,6 +868,10 @@ extern "C" attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t*
   p.B = B, p.H = H, p.G = H / Hkv, p.Nq = Nq, p.max_pages = max_pages, p.row_blocks = pl.row_blocks;
   p.causal = causal != 0;
   p.scale_log2 = scale * 1.4426950408889634f;
+  // q = n / v for n < 2^31: with s = ceil(log2 v), m = floor(2^32 (2^s - v) / v) + 1, q = (hi(m n) + n) >> s
+  const uint32_t v = (uint32_t)cache->page_size / 16;
+  while ((1ull << p.div_shift) < v) ++p.div_shift;
+  p.div_mul = (uint32_t)((((1ull << p.div_shift) - v) << 32) / v + 1);
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + n[0]);
   p.cut = reinterpret_cast<::int4*>(static_cast<uint8_t*>(workspace) + n[0] + n[1]);
