@@ -37,6 +37,7 @@
 #include <cuda_runtime.h>
 
 #include "attn.h"
+#include "fastdiv.cuh"
 #include "ops.h"
 #include "paged.cuh"
 #include "paged_host.h"
@@ -76,7 +77,7 @@ struct Params {
   const int *table, *lens;
   long long table_stride;
   int B, H, G, Nq, max_pages, row_blocks, causal;
-  uint32_t div_mul, div_shift;   // 16-key block / (page_size / 16) by a product (page_of_block)
+  FastDiv blocks_per_page;   // 16-key blocks
   float scale_log2;
   float* part_o;     // [2 CTAs, ROWS, D] normalised O of a cut unit's parts
   float* part_lse;   // [2 CTAs, ROWS] their log2-sum-exp2
@@ -175,11 +176,6 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
 // Key of the 16-key block that the MMA's row i stands for.
 __device__ __forceinline__ int key_of_row(int i) { return (i & 8) | ((i & 7) >> 1) | ((i & 1) << 2); }
 
-// Page of a sequence that its 16-key block lies in: block / (page_size / 16), for blocks below 2^31.
-__device__ __forceinline__ int page_of_block(const Params& p, uint32_t block) {
-  return (int)((__umulhi(p.div_mul, block) + block) >> p.div_shift);
-}
-
 // Keys that some row of sequence b sees at most, and its pieces of work (at least one: a unit without
 // keys still writes its zeros).
 __device__ __forceinline__ int sequence_keys(const Params& p, int b) {
@@ -267,13 +263,12 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
     struct Place {
       long long row, sz;
     };
-    const int blocks_per_page = p.c.page_size >> 4;
     auto look_up = [&](int n) -> Place {
       const int key = key0 + n * C::SPLIT + lane * 16;
       Place at{-1, -1};
       if (lane < KB && n < tiles && key < keys) {
-        const int block = key >> 4, e = page_of_block(p, block), page = pages[e];
-        const int in_page = (block - e * blocks_per_page) << 4;
+        const uint32_t block = key >> 4, e = block / p.blocks_per_page;
+        const int page = pages[e], in_page = (block - e * p.blocks_per_page.v) << 4;
         if (page >= 0 && page < p.c.num_pages) {
           at.row = page * p.c.page_b + in_page * p.c.token_b;
           if (INT4) at.sz = page * p.c.sz_page_b + in_page * p.c.sz_token_b;
@@ -868,10 +863,7 @@ extern "C" attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t*
   p.B = B, p.H = H, p.G = H / Hkv, p.Nq = Nq, p.max_pages = max_pages, p.row_blocks = pl.row_blocks;
   p.causal = causal != 0;
   p.scale_log2 = scale * 1.4426950408889634f;
-  // q = n / v for n < 2^31: with s = ceil(log2 v), m = floor(2^32 (2^s - v) / v) + 1, q = (hi(m n) + n) >> s
-  const uint32_t v = (uint32_t)cache->page_size / 16;
-  while ((1ull << p.div_shift) < v) ++p.div_shift;
-  p.div_mul = (uint32_t)((((1ull << p.div_shift) - v) << 32) / v + 1);
+  p.blocks_per_page = fast_div((uint32_t)cache->page_size / 16);
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + n[0]);
   p.cut = reinterpret_cast<::int4*>(static_cast<uint8_t*>(workspace) + n[0] + n[1]);

@@ -19,6 +19,7 @@
 #include <cuda_runtime.h>
 
 #include "attn.h"
+#include "fastdiv.cuh"
 #include "ops.h"
 #include "paged.cuh"
 #include "paged_host.h"
@@ -27,7 +28,7 @@ namespace gb300 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 2;   // heads of one token a thread has in flight
+constexpr int kRows = 4;   // heads of one token that a thread has in flight
 
 struct AppendParams {
   PagedCache c;
@@ -36,7 +37,8 @@ struct AppendParams {
   const int *cu, *len, *table;
   long long table_stride;
   const float *cos, *sin;
-  int B, total, max_pages, half, rope_dim, max_pos, parts;
+  int B, total, max_pages, half, rope_dim, max_pos;
+  FastDiv parts, page_size;   // tasks of a token
   uint32_t* status;
 };
 
@@ -45,7 +47,8 @@ struct GatherParams {
   __nv_bfloat16 *k, *v;
   const int *cu, *table;
   long long table_stride;
-  int B, total, max_pages, parts;
+  int B, total, max_pages;
+  FastDiv parts, page_size;
   uint32_t* status;
 };
 
@@ -93,20 +96,27 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t& sz)
   const float least = fmaxf(fmaxf(fabsf(lo), fabsf(hi)) * 0x1p-20f, 0x1p-100f);
   const float scale = bf16_toward<true>(fmaxf(__fdiv_rn(__fsub_rn(hi, zero), 15.f), least));
   sz = (__float_as_uint(scale) >> 16) | (__float_as_uint(zero) & 0xffff0000u);
+  // (x - zero) / scale, correctly rounded, from the correctly rounded reciprocal (Markstein, "Computation
+  // of elementary functions on the IBM RISC System/6000 processor"): the remainder of the first product
+  // is exact. 0 <= quotient <= 15, as scale >= (hi - zero) / 15; adding 2^23 rounds it to a whole number.
+  const float inv = __frcp_rn(scale);
   uint32_t codes = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[i], zero), scale)), 0.f), 15.f);
-    codes |= (uint32_t)c << (4 * i);
+  for (int i = 7; i >= 0; --i) {
+    const float y = __fsub_rn(x[i], zero), q = __fmul_rn(y, inv);
+    const float c = __fadd_rn(__fmaf_rn(__fmaf_rn(-q, scale, y), inv, q), 0x1p23f);
+    codes = codes << 4 | (__float_as_uint(c) & 15u);
   }
   return codes;
 }
 
 // Where position pos of sequence b lies, or false where the table does not lead into the pool.
-__device__ __forceinline__ bool find_row(const PagedCache& c, const int* __restrict__ table, long long table_stride,
-                                         int max_pages, int b, int pos, int& page, int& at) {
-  const int e = pos / c.page_size;
-  if (pos < 0 || e >= max_pages) return false;
+__device__ __forceinline__ bool find_row(const PagedCache& c, const FastDiv& page_size,
+                                         const int* __restrict__ table, long long table_stride, int max_pages, int b,
+                                         int pos, int& page, int& at) {
+  if (pos < 0) return false;
+  const int e = (uint32_t)pos / page_size;
+  if (e >= max_pages) return false;
   page = table[b * table_stride + e];
   at = pos - e * c.page_size;
   return page >= 0 && page < c.num_pages;
@@ -116,11 +126,11 @@ template <int D, bool INT4, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendParams p) {
   constexpr int LPR = D / 8;
   const int l = threadIdx.x % LPR;
-  const unsigned task = blockIdx.x * (unsigned)(kThreads / LPR) + threadIdx.x / LPR;
-  const int t = min(task / p.parts, (unsigned)p.total - 1u), part = task % p.parts;
-  bool good = task / p.parts < (unsigned)p.total;
-  const bool is_v = part >= p.parts / 2;
-  const int h0 = (is_v ? part - p.parts / 2 : part) * kRows, heads = p.c.Hkv;
+  const uint32_t task = blockIdx.x * (uint32_t)(kThreads / LPR) + threadIdx.x / LPR, token = task / p.parts;
+  const int t = min(token, (uint32_t)p.total - 1u), part = task - token * p.parts.v, k_parts = p.parts.v / 2;
+  bool good = token < (uint32_t)p.total;
+  const bool is_v = part >= k_parts;
+  const int h0 = (is_v ? part - k_parts : part) * kRows, heads = p.c.Hkv;
   const __nv_bfloat16* x = is_v ? p.v + t * p.v_st : p.k + t * p.k_st;
   const long long sh = is_v ? p.v_sh : p.k_sh;
   // This lane's dims 8l .. 8l + 7 and, for keys, where the values they are paired with begin.
@@ -142,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
     const int first = p.cu[b], past = p.len[b];
     pos = past + (t - first);
     const bool in = t >= first && t < p.cu[b + 1] && past >= 0 && pos >= 0 &&
-                    find_row(p.c, p.table, p.table_stride, p.max_pages, b, pos, page, at) &&
+                    find_row(p.c, p.page_size, p.table, p.table_stride, p.max_pages, b, pos, page, at) &&
                     (!p.cos || pos < p.max_pos);
     if (good && !in && l == 0) atomicCAS(p.status, 0u, kStatusBadPage);
     good = good && in;
@@ -212,17 +222,17 @@ template <int D, bool INT4>
 __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const GatherParams p) {
   constexpr int LPR = D / 8;
   const int l = threadIdx.x % LPR;
-  const unsigned task = blockIdx.x * (unsigned)(kThreads / LPR) + threadIdx.x / LPR;
-  const int t = min(task / p.parts, (unsigned)p.total - 1u), part = task % p.parts;
-  const bool mine = task / p.parts < (unsigned)p.total;
-  const bool is_v = part >= p.parts / 2;
-  const int h0 = (is_v ? part - p.parts / 2 : part) * kGatherRows, heads = p.c.Hkv;
+  const uint32_t task = blockIdx.x * (uint32_t)(kThreads / LPR) + threadIdx.x / LPR, token = task / p.parts;
+  const int t = min(token, (uint32_t)p.total - 1u), part = task - token * p.parts.v, k_parts = p.parts.v / 2;
+  const bool mine = token < (uint32_t)p.total;
+  const bool is_v = part >= k_parts;
+  const int h0 = (is_v ? part - k_parts : part) * kGatherRows, heads = p.c.Hkv;
   const int b = find_sequence<LPR>(p.cu, p.B, t);
   if (b >= p.B || !mine) return;   // behind the last sequence: left as it was
   const int first = p.cu[b];
   int page, at;
   if (t < first || t >= p.cu[b + 1] ||
-      !find_row(p.c, p.table, p.table_stride, p.max_pages, b, t - first, page, at)) {
+      !find_row(p.c, p.page_size, p.table, p.table_stride, p.max_pages, b, t - first, page, at)) {
     if (l == 0) atomicCAS(p.status, 0u, kStatusBadPage);
     return;
   }
@@ -243,7 +253,8 @@ __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const GatherPara
       const float scale = __uint_as_float(sz[i] << 16), zero = __uint_as_float(sz[i] & 0xffff0000u);
       float x[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = fmaf(scale, (float)((codes[i] >> (4 * j)) & 15u), zero);
+      for (int j = 0; j < 8; ++j)   // a code in the low bits of 2^23 is 2^23 + code
+        x[j] = fmaf(scale, __uint_as_float(((codes[i] >> (4 * j)) & 15u) | 0x4b000000u) - 0x1p23f, zero);
       if (h0 + i < heads) *reinterpret_cast<uint4*>(y + i * D) = pack8(x);
     }
   } else {
@@ -260,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const GatherPara
 template <int D, bool INT4>
 cudaError_t launch_append(const AppendParams& p, bool interleaved, cudaStream_t s) {
   const unsigned rows = kThreads / (D / 8);
-  const unsigned grid = ((unsigned)p.total * p.parts + rows - 1) / rows;
+  const unsigned grid = ((unsigned)p.total * p.parts.v + rows - 1) / rows;
   if (interleaved) paged_append_kernel<D, INT4, true><<<grid, kThreads, 0, s>>>(p);
   else paged_append_kernel<D, INT4, false><<<grid, kThreads, 0, s>>>(p);
   return cudaGetLastError();
@@ -269,7 +280,7 @@ cudaError_t launch_append(const AppendParams& p, bool interleaved, cudaStream_t 
 template <int D, bool INT4>
 cudaError_t launch_gather(const GatherParams& p, cudaStream_t s) {
   const unsigned rows = kThreads / (D / 8);
-  paged_gather_kernel<D, INT4><<<((unsigned)p.total * p.parts + rows - 1) / rows, kThreads, 0, s>>>(p);
+  paged_gather_kernel<D, INT4><<<((unsigned)p.total * p.parts.v + rows - 1) / rows, kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -299,8 +310,9 @@ extern "C" attn_status_t attn_paged_append(const attn_paged_cache_t* cache, cons
     if (!is_aligned(cos, 16) || !is_aligned(sin, 16) || max_pos < 1) return ATTN_ERR_INVALID_ARG;
     if (rope_dim < 16 || rope_dim % 16 || rope_dim > cache->d) return ATTN_ERR_INVALID_ARG;
   }
-  p.parts = 2 * ((cache->Hkv + kRows - 1) / kRows);
-  if ((long long)total * p.parts > INT_MAX) return ATTN_ERR_UNSUPPORTED;   // tasks are counted in 32 bits
+  p.parts = fast_div(2 * (uint32_t)(((long long)cache->Hkv + kRows - 1) / kRows));
+  p.page_size = fast_div((uint32_t)cache->page_size);
+  if ((long long)total * p.parts.v > INT_MAX) return ATTN_ERR_UNSUPPORTED;   // tasks are counted in 32 bits
   if (total == 0) return ATTN_OK;
   int sms;
   if (!device_state(&sms, &p.status)) return ATTN_ERR_CUDA;
@@ -333,8 +345,9 @@ extern "C" attn_status_t attn_paged_gather(const attn_paged_cache_t* cache, void
     return ATTN_ERR_INVALID_ARG;
   const uintptr_t bytes = (uintptr_t)total * cache->Hkv * cache->d * 2, kb = (uintptr_t)k, vb = (uintptr_t)v;
   if (kb < vb + bytes && vb < kb + bytes) return ATTN_ERR_INVALID_ARG;
-  p.parts = 2 * ((cache->Hkv + kGatherRows - 1) / kGatherRows);
-  if ((long long)total * p.parts > INT_MAX) return ATTN_ERR_UNSUPPORTED;
+  p.parts = fast_div(2 * (uint32_t)(((long long)cache->Hkv + kGatherRows - 1) / kGatherRows));
+  p.page_size = fast_div((uint32_t)cache->page_size);
+  if ((long long)total * p.parts.v > INT_MAX) return ATTN_ERR_UNSUPPORTED;
   if (total == 0) return ATTN_OK;
   int sms;
   if (!device_state(&sms, &p.status)) return ATTN_ERR_CUDA;

@@ -20,6 +20,7 @@
 #include <cuda_runtime.h>
 
 #include "attn.h"
+#include "fastdiv.cuh"
 #include "ops.h"
 #include "paged.cuh"
 
@@ -28,6 +29,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kHeads = 4;   // rows of a task
+constexpr int kFwdCtasPerSm = 3, kBwdCtasPerSm = 3;
 
 struct NormRopeParams {
   const __nv_bfloat16 *q, *k;      // inputs (or x of the backward)
@@ -38,7 +40,8 @@ struct NormRopeParams {
   const int* positions;
   float* part;                     // backward: [CTAs, d] sums of du n
   float eps;
-  int T, H, Hkv, half, max_pos, seq_len, parts_q, parts_k, ctas_q;
+  int T, H, Hkv, half, max_pos, seq_len, parts_q, parts_k, ctas_q, w_vec;
+  FastDiv parts, div_q, div_k;     // tasks of a token: all, of q, of k
   uint32_t* status;
 };
 
@@ -46,12 +49,27 @@ struct Chunks {
   float a[4], b[4];
 };
 
-__device__ __forceinline__ void load4(float (&x)[4], const __nv_bfloat16* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
+// A lane's values of a row as they lie in memory: held like this while other rows' loads are under way.
+struct Raw {
+  uint2 a, b;
+};
+
+__device__ __forceinline__ Raw load_raw(const __nv_bfloat16* row, int da, int db) {
+  return {*reinterpret_cast<const uint2*>(row + da), *reinterpret_cast<const uint2*>(row + db)};
+}
+
+__device__ __forceinline__ void unpack4(float (&x)[4], const uint2& w) {
   x[0] = __uint_as_float(w.x << 16);
   x[1] = __uint_as_float(w.x & 0xffff0000u);
   x[2] = __uint_as_float(w.y << 16);
   x[3] = __uint_as_float(w.y & 0xffff0000u);
+}
+
+__device__ __forceinline__ Chunks unpack(const Raw& r) {
+  Chunks x;
+  unpack4(x.a, r.a);
+  unpack4(x.b, r.b);
+  return x;
 }
 
 __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[4]) {
@@ -96,81 +114,112 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// Angles of token t; false (nothing to store) where its position lies outside the tables.
-__device__ __forceinline__ bool load_angles(const NormRopeParams& p, int t, int l, Angles& r) {
+// Position of token t; -1 (nothing to store) where it lies outside the tables.
+__device__ __forceinline__ int position(const NormRopeParams& p, int t, int l) {
+  if (!p.cos) return 0;
+  const int pos = p.positions ? p.positions[t] : t % p.seq_len;
+  if (pos >= 0 && pos < p.max_pos) return pos;
+  if (l == 0) atomicCAS(p.status, 0u, kStatusBadPosition);
+  return -1;
+}
+
+__device__ __forceinline__ Angles load_angles(const NormRopeParams& p, int pos, int l) {
+  Angles r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) r.c[i] = 1.f, r.s[i] = 0.f;
-  if (!p.cos) return true;
-  const int pos = p.positions ? p.positions[t] : t % p.seq_len;
-  if (pos < 0 || pos >= p.max_pos) {
-    if (l == 0) atomicCAS(p.status, 0u, kStatusBadPosition);
-    return false;
-  }
-  if (4 * l < p.half) {
+  if (4 * l < p.half && pos >= 0) {
     const long long at = (long long)pos * p.half + 4 * l;
     const float4 c = *reinterpret_cast<const float4*>(p.cos + at), s = *reinterpret_cast<const float4*>(p.sin + at);
     r.c[0] = c.x, r.c[1] = c.y, r.c[2] = c.z, r.c[3] = c.w;
     r.s[0] = s.x, r.s[1] = s.y, r.s[2] = s.z, r.s[3] = s.w;
   }
-  return true;
+  return r;
 }
 
-__device__ __forceinline__ void load_weights(const float* w, int da, int db, Chunks& x) {
+__device__ __forceinline__ void load_weights4(float (&x)[4], const float* w, bool vec) {
+  if (vec) {
+    const float4 y = *reinterpret_cast<const float4*>(w);
+    x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x.a[i] = w ? w[da + i] : 1.f;
-    x.b[i] = w ? w[db + i] : 1.f;
+    for (int i = 0; i < 4; ++i) x[i] = w[i];
   }
 }
 
+// vec: the weights are 16-byte aligned.
+__device__ __forceinline__ Chunks load_weights(const float* w, int da, int db, bool vec) {
+  Chunks x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x.a[i] = x.b[i] = 1.f;
+  if (w) {
+    load_weights4(x.a, w + da, vec);
+    load_weights4(x.b, w + db, vec);
+  }
+  return x;
+}
+
+// CTAs walk the tasks of all tokens, one wave of them; a thread has the rows of its next task on their
+// way while it turns those of this one, so that loads are always in flight.
 template <int D, bool NORM, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormRopeParams p) {
-  constexpr int LPR = D / 8;
+__global__ void __launch_bounds__(kThreads, kFwdCtasPerSm) qk_norm_rope_kernel(const NormRopeParams p) {
+  constexpr int LPR = D / 8, ROWS = kThreads / LPR;
   const int l = threadIdx.x % LPR;
-  const unsigned task = blockIdx.x * (unsigned)(kThreads / LPR) + threadIdx.x / LPR;
-  const unsigned parts = p.parts_q + p.parts_k;
-  const bool mine = task / parts < (unsigned)p.T;   // row sums take whole warps: no thread leaves early
-  const int t = mine ? task / parts : p.T - 1, part = task % parts;
-  const bool is_k = part >= p.parts_q;
-  const int h0 = (is_k ? part - p.parts_q : part) * kHeads, heads = is_k ? p.Hkv : p.H;
-  const __nv_bfloat16* x = is_k ? p.k + t * p.k_st : p.q + t * p.q_st;
-  const long long sh = is_k ? p.k_sh : p.q_sh;
-  __nv_bfloat16* y = (is_k ? p.ok : p.oq) + (long long)t * heads * D;
   int da, db;
   chunk_dims<INTERLEAVED>(l, p.half, da, db);
-  Chunks v[kHeads];
+  struct Task {
+    int t, h0, pos;
+    bool is_k;
+    Raw raw[kHeads];
+  };
+  const uint32_t tasks = (uint32_t)p.T * p.parts.v, stride = gridDim.x * ROWS;
+  auto load = [&](uint32_t id) {
+    Task w;
+    const uint32_t token = id / p.parts;
+    const int part = id - token * p.parts.v;
+    w.t = token;
+    w.pos = position(p, w.t, l);
+    w.is_k = part >= p.parts_q;
+    w.h0 = (w.is_k ? part - p.parts_q : part) * kHeads;
+    const __nv_bfloat16* x = w.is_k ? p.k + w.t * p.k_st : p.q + w.t * p.q_st;
+    const long long sh = w.is_k ? p.k_sh : p.q_sh;
+    const int last = (w.is_k ? p.Hkv : p.H) - 1;
 #pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    if (h0 + i < heads) {
-      load4(v[i].a, x + (h0 + i) * sh + da);
-      load4(v[i].b, x + (h0 + i) * sh + db);
-    } else {
+    for (int i = 0; i < kHeads; ++i) w.raw[i] = load_raw(x + min(w.h0 + i, last) * sh, da, db);   // the last row again
+    return w;
+  };
+  // Every thread of the CTA makes the same number of turns: row sums take whole warps.
+  const uint32_t slot = threadIdx.x / LPR;
+  uint32_t id = blockIdx.x * ROWS + slot;
+  Task now = load(min(id, tasks - 1));
+  for (uint32_t first = blockIdx.x * ROWS; first < tasks; first += stride, id += stride) {
+    Task next = now;
+    if (first + stride < tasks) next = load(min(id + stride, tasks - 1));
+    const Angles r = load_angles(p, now.pos, l);
+    Chunks w;
+    if (NORM) w = load_weights(now.is_k ? p.wk : p.wq, da, db, p.w_vec);
+    const int heads = now.is_k ? p.Hkv : p.H, last = id < tasks && now.pos >= 0 ? heads : 0;
+    __nv_bfloat16* y = (now.is_k ? p.ok : p.oq) + ((long long)now.t * heads + now.h0) * D;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[i].a[j] = v[i].b[j] = 0.f;
-    }
-  }
-  Angles r;
-  const bool good = load_angles(p, t, l, r) && mine;
-  Chunks w;
-  if (NORM) load_weights(is_k ? p.wk : p.wq, da, db, w);
+    for (int i = 0; i < kHeads; ++i) {
+      Chunks v = unpack(now.raw[i]);
+      if (NORM) {
+        float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    if (NORM) {
-      float s = 0.f;
+        for (int j = 0; j < 4; ++j) s += v.a[j] * v.a[j] + v.b[j] * v.b[j];
+        const float rs = rsqrtf(row_sum<LPR>(s) * (1.f / D) + p.eps);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s += v[i].a[j] * v[i].a[j] + v[i].b[j] * v[i].b[j];
-      const float rs = rsqrtf(row_sum<LPR>(s) * (1.f / D) + p.eps);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[i].a[j] *= rs * w.a[j];
-        v[i].b[j] *= rs * w.b[j];
+        for (int j = 0; j < 4; ++j) {
+          v.a[j] *= rs * w.a[j];
+          v.b[j] *= rs * w.b[j];
+        }
+      }
+      turn<INTERLEAVED>(v, r, 1.f);
+      if (now.h0 + i < last) {
+        store4(y + i * D + da, v.a);
+        store4(y + i * D + db, v.b);
       }
     }
-    turn<INTERLEAVED>(v[i], r, 1.f);
-    if (good && h0 + i < heads) {
-      store4(y + (h0 + i) * D + da, v[i].a);
-      store4(y + (h0 + i) * D + db, v[i].b);
-    }
+    now = next;
   }
 }
 
@@ -178,74 +227,70 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormRopePa
 // weight gradient of its 8 dims in registers; a CTA adds its rows' sums in a fixed order and leaves
 // [d] in part, which dw_kernel adds up: the same bits every time.
 template <int D, bool NORM, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kernel(const NormRopeParams p) {
   constexpr int LPR = D / 8, ROWS = kThreads / LPR;
   const int l = threadIdx.x % LPR, slot = threadIdx.x / LPR;
   const bool is_k = blockIdx.x >= (unsigned)p.ctas_q;
   const int cta = is_k ? (int)blockIdx.x - p.ctas_q : blockIdx.x, ctas = is_k ? (int)gridDim.x - p.ctas_q : p.ctas_q;
-  const int heads = is_k ? p.Hkv : p.H, parts = is_k ? p.parts_k : p.parts_q;
+  const int heads = is_k ? p.Hkv : p.H;
+  const FastDiv parts = is_k ? p.div_k : p.div_q;
   const float* wp = is_k ? p.wk : p.wq;
+  const long long sh = is_k ? p.k_sh : p.q_sh;
   int da, db;
   chunk_dims<INTERLEAVED>(l, p.half, da, db);
   Chunks w, dw;
-  if (NORM) load_weights(wp, da, db, w);
+  if (NORM) w = load_weights(wp, da, db, p.w_vec);
 #pragma unroll
   for (int j = 0; j < 4; ++j) dw.a[j] = dw.b[j] = 0.f;
-  const unsigned tasks = (unsigned)p.T * parts;
+  const uint32_t tasks = (uint32_t)p.T * parts.v;
   // Every thread of the CTA makes the same number of turns: row sums take whole warps.
-  for (unsigned t0 = (unsigned)cta * ROWS; t0 < tasks; t0 += (unsigned)ctas * ROWS) {
-    const unsigned task = t0 + slot;
-    const bool mine = task < tasks;
-    const int t = mine ? task / parts : 0, h0 = mine ? task % parts * kHeads : heads;
+  for (uint32_t t0 = (uint32_t)cta * ROWS; t0 < tasks; t0 += (uint32_t)ctas * ROWS) {
+    const uint32_t task = min(t0 + slot, tasks - 1), token = task / parts;
+    const int t = token, h0 = (task - token * parts.v) * kHeads, pos = position(p, t, l);
     const __nv_bfloat16* x = NORM ? (is_k ? p.k + t * p.k_st : p.q + t * p.q_st) : nullptr;
-    const long long sh = is_k ? p.k_sh : p.q_sh;
     const long long at = (long long)t * heads * D;
     const __nv_bfloat16* dy = (is_k ? p.dyk : p.dyq) + at;
     __nv_bfloat16* dx = (is_k ? p.ok : p.oq) + at;
-    Chunks v[kHeads], g[kHeads];
+    Raw rx[kHeads], rg[kHeads];
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
-      if (h0 + i < heads) {
-        if (NORM) {
-          load4(v[i].a, x + (h0 + i) * sh + da);
-          load4(v[i].b, x + (h0 + i) * sh + db);
-        }
-        load4(g[i].a, dy + (h0 + i) * D + da);
-        load4(g[i].b, dy + (h0 + i) * D + db);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[i].a[j] = v[i].b[j] = g[i].a[j] = g[i].b[j] = 0.f;
-      }
+      const int h = min(h0 + i, heads - 1);
+      if (NORM) rx[i] = load_raw(x + h * sh, da, db);
+      rg[i] = load_raw(dy + h * D, da, db);
     }
-    Angles r;
-    const bool good = load_angles(p, t, l, r);
+    const Angles r = load_angles(p, pos, l);
+    const int last = t0 + slot < tasks && pos >= 0 ? heads : 0;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
-      const bool row = good && h0 + i < heads;
-      turn<INTERLEAVED>(g[i], r, -1.f);
+      Chunks g = unpack(rg[i]);
+      turn<INTERLEAVED>(g, r, -1.f);
       if (NORM) {
+        const Chunks v = unpack(rx[i]);
         float s = 0.f, m = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          s += v[i].a[j] * v[i].a[j] + v[i].b[j] * v[i].b[j];
-          m += g[i].a[j] * w.a[j] * v[i].a[j] + g[i].b[j] * w.b[j] * v[i].b[j];
+          s += v.a[j] * v.a[j] + v.b[j] * v.b[j];
+          m += g.a[j] * w.a[j] * v.a[j] + g.b[j] * w.b[j] * v.b[j];
         }
         s = row_sum<LPR>(s);
         m = row_sum<LPR>(m);
         const float rs = rsqrtf(s * (1.f / D) + p.eps), c = m * (1.f / D) * rs * rs;
+        if (h0 + i < last) {   // not the repeated rows, nor a row without a position, which may hold anything
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            dw.a[j] += g.a[j] * v.a[j] * rs;
+            dw.b[j] += g.b[j] * v.b[j] * rs;
+          }
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (row) {
-            dw.a[j] += g[i].a[j] * v[i].a[j] * rs;
-            dw.b[j] += g[i].b[j] * v[i].b[j] * rs;
-          }
-          g[i].a[j] = rs * (g[i].a[j] * w.a[j] - v[i].a[j] * c);
-          g[i].b[j] = rs * (g[i].b[j] * w.b[j] - v[i].b[j] * c);
+          g.a[j] = rs * (g.a[j] * w.a[j] - v.a[j] * c);
+          g.b[j] = rs * (g.b[j] * w.b[j] - v.b[j] * c);
         }
       }
-      if (row) {
-        store4(dx + (h0 + i) * D + da, g[i].a);
-        store4(dx + (h0 + i) * D + db, g[i].b);
+      if (h0 + i < last) {
+        store4(dx + (h0 + i) * D + da, g.a);
+        store4(dx + (h0 + i) * D + db, g.b);
       }
     }
   }
@@ -286,9 +331,9 @@ __global__ void __launch_bounds__(1024) dw_kernel(const float* __restrict__ part
 }
 
 template <int D>
-cudaError_t launch_forward(const NormRopeParams& p, bool norm, bool interleaved, cudaStream_t s) {
+cudaError_t launch_forward(const NormRopeParams& p, bool norm, bool interleaved, int sms, cudaStream_t s) {
   const long long tasks = (long long)p.T * (p.parts_q + p.parts_k), rows = kThreads / (D / 8);
-  const unsigned grid = (unsigned)((tasks + rows - 1) / rows);
+  const unsigned grid = (unsigned)std::min<long long>((tasks + rows - 1) / rows, (long long)kFwdCtasPerSm * sms);
   if (norm) {
     if (interleaved) qk_norm_rope_kernel<D, true, true><<<grid, kThreads, 0, s>>>(p);
     else qk_norm_rope_kernel<D, true, false><<<grid, kThreads, 0, s>>>(p);
@@ -311,9 +356,7 @@ cudaError_t launch_backward(const NormRopeParams& p, bool norm, bool interleaved
   return cudaGetLastError();
 }
 
-// CTAs of the backward: one wave of 4 a SM (1024 threads), shared between q and k by their tasks.
-constexpr int kBwdCtasPerSm = 4;
-
+// CTAs of the backward: one wave, shared between q and k by their tasks.
 struct BwdGrid {
   int ctas_q, ctas;
 };
@@ -407,12 +450,14 @@ extern "C" attn_status_t attn_qk_norm_rope(const void* q, const void* k, void* q
   p.eps = eps;
   p.T = T, p.H = H, p.Hkv = Hkv, p.half = cos ? rope_dim / 2 : 0, p.max_pos = max_pos, p.seq_len = seq_len;
   p.parts_q = (H + kHeads - 1) / kHeads, p.parts_k = (Hkv + kHeads - 1) / kHeads;
+  p.parts = fast_div(p.parts_q + p.parts_k), p.div_q = fast_div(p.parts_q), p.div_k = fast_div(std::max(p.parts_k, 1));
+  p.w_vec = aligned16(wq) && aligned16(wk);
   p.status = status;
   cudaError_t e;
   switch (d) {
-    case 64: e = launch_forward<64>(p, norm != 0, interleaved != 0, stream); break;
-    case 128: e = launch_forward<128>(p, norm != 0, interleaved != 0, stream); break;
-    default: e = launch_forward<256>(p, norm != 0, interleaved != 0, stream); break;
+    case 64: e = launch_forward<64>(p, norm != 0, interleaved != 0, sms, stream); break;
+    case 128: e = launch_forward<128>(p, norm != 0, interleaved != 0, sms, stream); break;
+    default: e = launch_forward<256>(p, norm != 0, interleaved != 0, sms, stream); break;
   }
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
@@ -488,6 +533,8 @@ extern "C" attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, con
   p.eps = eps;
   p.T = T, p.H = H, p.Hkv = Hkv, p.half = cos ? rope_dim / 2 : 0, p.max_pos = max_pos, p.seq_len = seq_len;
   p.parts_q = (H + kHeads - 1) / kHeads, p.parts_k = (Hkv + kHeads - 1) / kHeads, p.ctas_q = g.ctas_q;
+  p.parts = fast_div(p.parts_q + p.parts_k), p.div_q = fast_div(p.parts_q), p.div_k = fast_div(std::max(p.parts_k, 1));
+  p.w_vec = aligned16(wq) && aligned16(wk);
   p.status = status;
   cudaError_t e;
   switch (d) {
