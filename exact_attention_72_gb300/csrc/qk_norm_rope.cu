@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kHeads = 4;   // rows of a task
-constexpr int kFwdCtasPerSm = 3, kBwdCtasPerSm = 3;
+constexpr int kFwdCtasPerSm = 3, kBwdCtasPerSm = 2;
 
 struct NormRopeParams {
   const __nv_bfloat16 *q, *k;      // inputs (or x of the backward)
@@ -242,30 +242,41 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kern
   if (NORM) w = load_weights(wp, da, db, p.w_vec);
 #pragma unroll
   for (int j = 0; j < 4; ++j) dw.a[j] = dw.b[j] = 0.f;
-  const uint32_t tasks = (uint32_t)p.T * parts.v;
-  // Every thread of the CTA makes the same number of turns: row sums take whole warps.
-  for (uint32_t t0 = (uint32_t)cta * ROWS; t0 < tasks; t0 += (uint32_t)ctas * ROWS) {
-    const uint32_t task = min(t0 + slot, tasks - 1), token = task / parts;
-    const int t = token, h0 = (task - token * parts.v) * kHeads, pos = position(p, t, l);
-    const __nv_bfloat16* x = NORM ? (is_k ? p.k + t * p.k_st : p.q + t * p.q_st) : nullptr;
-    const long long at = (long long)t * heads * D;
-    const __nv_bfloat16* dy = (is_k ? p.dyk : p.dyq) + at;
-    __nv_bfloat16* dx = (is_k ? p.ok : p.oq) + at;
-    Raw rx[kHeads], rg[kHeads];
+  struct Task {
+    int t, h0, pos;
+    Raw x[kHeads], g[kHeads];
+  };
+  auto load = [&](uint32_t id) {
+    Task w;
+    w.t = id / parts;
+    w.h0 = (id - w.t * parts.v) * kHeads;
+    w.pos = position(p, w.t, l);
+    const __nv_bfloat16* x = is_k ? p.k + w.t * p.k_st : p.q + w.t * p.q_st;
+    const __nv_bfloat16* dy = (is_k ? p.dyk : p.dyq) + (long long)w.t * heads * D;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
-      const int h = min(h0 + i, heads - 1);
-      if (NORM) rx[i] = load_raw(x + h * sh, da, db);
-      rg[i] = load_raw(dy + h * D, da, db);
+      const int h = min(w.h0 + i, heads - 1);   // the last row again
+      if (NORM) w.x[i] = load_raw(x + h * sh, da, db);
+      w.g[i] = load_raw(dy + h * D, da, db);
     }
-    const Angles r = load_angles(p, pos, l);
-    const int last = t0 + slot < tasks && pos >= 0 ? heads : 0;
+    return w;
+  };
+  const uint32_t tasks = (uint32_t)p.T * parts.v, stride = (uint32_t)ctas * ROWS;
+  uint32_t id = (uint32_t)cta * ROWS + slot;
+  Task now = load(min(id, tasks - 1));
+  // Every thread of the CTA makes the same number of turns: row sums take whole warps.
+  for (uint32_t first = (uint32_t)cta * ROWS; first < tasks; first += stride, id += stride) {
+    Task next = now;
+    if (first + stride < tasks) next = load(min(id + stride, tasks - 1));
+    const Angles r = load_angles(p, now.pos, l);
+    const int last = id < tasks && now.pos >= 0 ? heads : 0;
+    __nv_bfloat16* dx = (is_k ? p.ok : p.oq) + ((long long)now.t * heads + now.h0) * D;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
-      Chunks g = unpack(rg[i]);
+      Chunks g = unpack(now.g[i]);
       turn<INTERLEAVED>(g, r, -1.f);
       if (NORM) {
-        const Chunks v = unpack(rx[i]);
+        const Chunks v = unpack(now.x[i]);
         float s = 0.f, m = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -275,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kern
         s = row_sum<LPR>(s);
         m = row_sum<LPR>(m);
         const float rs = rsqrtf(s * (1.f / D) + p.eps), c = m * (1.f / D) * rs * rs;
-        if (h0 + i < last) {   // not the repeated rows, nor a row without a position, which may hold anything
+        if (now.h0 + i < last) {   // not the repeated rows, nor a row without a position, which may hold anything
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             dw.a[j] += g.a[j] * v.a[j] * rs;
@@ -288,11 +299,12 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kern
           g.b[j] = rs * (g.b[j] * w.b[j] - v.b[j] * c);
         }
       }
-      if (h0 + i < last) {
-        store4(dx + (h0 + i) * D + da, g.a);
-        store4(dx + (h0 + i) * D + db, g.b);
+      if (now.h0 + i < last) {
+        store4(dx + i * D + da, g.a);
+        store4(dx + i * D + db, g.b);
       }
     }
+    now = next;
   }
   if (NORM && wp) {
     __shared__ float sums[ROWS][D];
