@@ -18,19 +18,20 @@
 // 2^-9, both averaged over the keys. For p_j scale_j to stay within fp16 at any scale, the running
 // maximum is taken over S + log2 of the key's scale (its exponent) instead of S.
 //
-// Work: sequences are cut into pieces of SPLIT keys; all pieces of all (sequence, kv head, row block)
-// units in order are dealt to the CTAs in equal contiguous shares, so ragged batches load every SM
-// alike. A unit inside one share is finished there; one cut across CTAs leaves normalised parts with
-// their LSE, joined by a second, dependent launch. The shares follow from the lengths alone: the same
-// bits on every run, no atomics.
+// Work: a sequence's keys are cut into tiles of KT; a unit is the tiles of one (sequence, kv head, block of query rows). All
+// units in order, each OVERHEAD tiles longer than it is, are dealt to all warps in equal contiguous shares, so ragged
+// batches load every SM alike. A warp streams through its share alone: query rows, keys and values go through a ring of its
+// own in shared memory, filled by 16-byte asynchronous copies that run ahead across the ends of units. A unit inside one
+// share is finished by its warp. One that is cut leaves normalised parts with their LSE: what the warps of a CTA hold of
+// one unit when their shares end is joined there, the rest by a second, dependent launch. The shares follow from the
+// lengths alone: the same bits on every run, no atomics.
 //
-// In a CTA each of the 4 warps takes every fourth tile of KT keys through a ring of its own in shared
-// memory, filled by 16-byte asynchronous copies; warps meet only at the end of a unit. Keys are
-// assigned to the MMA's rows in the order 0 4 1 5 2 6 3 7 so that a lane's four V rows are 4 apart
-// and the loads of both products meet every bank once.
+// Matrix loads hand out the operands, those of V transposed: a 16-bit unit of them is one bf16 value or four codes.
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
+#include <utility>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,26 +48,34 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr float kMinExp = -100.f;   // least scale exponent that counts in the running maximum
+// Least scale that counts in the running maximum: a weight then stays below 2^84, sums of weights and of weight
+// times zero (at most 2^20 scales) far from overflow.
+constexpr float kLeastScale = 0x1p-70f;
+
+constexpr float kNone = -1e30f;     // running maximum before the first key
+constexpr float kHeadroom = 0x1p14f;   // weights times scale may grow to this before the maximum is moved
 
 template <int D_, bool INT4_, int NT_>
 struct Cfg {
   static constexpr int D = D_, NT = NT_;
   static constexpr bool INT4 = INT4_;
-  static constexpr int KT = INT4 ? 32 : 16;              // keys of a warp's tile
-  static constexpr int SPLIT = KT * kWarps;              // keys of a piece of work
+  static constexpr int KT = INT4 ? 32 : 16;              // keys of a tile
+  static constexpr int OVERHEAD = INT4 ? 1 : 2;          // what beginning and ending a unit costs, in tiles
   static constexpr int ROWS = 8 * NT;                    // query rows of a unit
   static constexpr int GROUPS = D / kInt4Group;
   static constexpr int ROWB = INT4 ? D / 2 : 2 * D;      // bytes of a key's row
   static constexpr int SZB = INT4 ? 4 * GROUPS : 0;      // bytes of its (scale, zero) pairs
-  static constexpr int V_OFF = KT * ROWB, KSZ_OFF = 2 * KT * ROWB, VSZ_OFF = KSZ_OFF + KT * SZB;
-  static constexpr int STAGE = VSZ_OFF + KT * SZB;
-  static constexpr int STAGES = 3;
-  static constexpr int WARP_BYTES = STAGES * STAGE;
+  // A slot of the ring: a tile's keys and values, or 8 query rows. At d = 256 in bf16 a tile takes two slots, keys then
+  // values: two CTAs of four warps would not fit otherwise.
+  static constexpr bool PAIR = INT4 || D < 256;
+  static constexpr int V_OFF = PAIR ? KT * ROWB : 0, SZ_OFF = V_OFF + KT * ROWB, SZV_OFF = SZ_OFF + KT * SZB;
+  static constexpr int SLOT = PAIR ? SZV_OFF + KT * SZB : KT * ROWB;
+  static constexpr int SLOTS = 3;
+  static constexpr int WARP_BYTES = SLOTS * SLOT;
   static constexpr int SMEM = kWarps * WARP_BYTES;
-  static constexpr int CTAS = std::min(D * NT >= 256 ? 2 : 4, 233472 / (SMEM + 1024 + 1600));
+  static constexpr int CTAS = std::min(D * NT >= 256 ? 2 : 3, 233472 / (SMEM + 1024 + 2048));
   static_assert(WARP_BYTES >= ROWS * D * 4, "a warp's part of O is joined in its ring");
-  static_assert(CTAS >= 1 && STAGE % 16 == 0, "ring");
+  static_assert(SLOT >= 16 * D && CTAS >= 1 && SLOT % 16 == 0, "ring");
 };
 
 struct Params {
@@ -77,35 +86,46 @@ struct Params {
   const int *table, *lens;
   long long table_stride;
   int B, H, G, Nq, max_pages, row_blocks, causal;
-  FastDiv blocks_per_page;   // 16-key blocks
+  FastDiv blocks_per_page, div_g;   // 16-key blocks; heads of a group
   float scale_log2;
-  float* part_o;     // [2 CTAs, ROWS, D] normalised O of a cut unit's parts
-  float* part_lse;   // [2 CTAs, ROWS] their log2-sum-exp2
-  int4* cut;         // [CTAs]: the unit that begins in this CTA and ends in a later one (z; -1: none)
+  // Parts of cut units, by warp w of the grid: 2w the one whose unit ends inside its share, 2w + 1 the one that the share
+  // ends in, joined over the warps of the CTA from w on that hold the same unit.
+  float* part_o;     // [2 warps, ROWS, D] normalised O
+  float* part_lse;   // [2 warps, ROWS] log2-sum-exp2
+  int4* cut;         // [warps]: (sequence, unit in it, warp with its last tile, whether that ends inside a share; -1: none)
   uint32_t* status;
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+// Copies to dst + OFF in shared memory; zeros instead where `in` is false (the address must be readable all the same).
+template <int OFF>
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0+%2], [%1], 16;" ::"r"(dst), "l"(src), "n"(OFF) : "memory");
 }
-template <int N>
+template <int OFF>
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0+%3], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0), "n"(OFF) : "memory");
+}
+template <int OFF, int N>
 __device__ __forceinline__ void copy_small(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(in ? N : 0) : "memory");
+  asm volatile("cp.async.ca.shared.global [%0+%4], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(in ? N : 0), "n"(OFF) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t x;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
-  return x;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 x;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(a) : "memory");
+// Four 8x8 matrices of 16-bit values at a + OFF; lanes 8i .. 8i + 7 give the rows of matrix i. Lane (g, t) gets values 2t,
+// 2t + 1 of row g, or with TRANS of column g.
+template <bool TRANS, int OFF>
+__device__ __forceinline__ uint4 load_matrices(uint32_t a) {
+  uint4 x;
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4+%5];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a), "n"(OFF) : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4+%5];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a), "n"(OFF) : "memory");
   return x;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -114,36 +134,52 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   return x;
 }
 
-// The (scale, zero) pairs of a row.
-template <int N>
+// The (scale, zero) pairs of a row at a + OFF.
+template <int OFF, int N>
 __device__ __forceinline__ void load_pairs(uint32_t (&x)[N], uint32_t a) {
-  if constexpr (N == 1) {
-    x[0] = lds32(a);
-  } else if constexpr (N == 2) {
-    const uint2 w = lds64(a);
-    x[0] = w.x, x[1] = w.y;
-  } else {
-    const uint4 w = lds128(a);
-    x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
-  }
+  if constexpr (N == 1)
+    asm volatile("ld.shared.b32 %0, [%1+%2];" : "=r"(x[0]) : "r"(a), "n"(OFF) : "memory");
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2+%3];" : "=r"(x[0]), "=r"(x[1]) : "r"(a), "n"(OFF) : "memory");
+  else
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4+%5];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(a), "n"(OFF) : "memory");
+}
+
+// Calls f with the constants 0 .. N - 1, for addresses that take them as immediates.
+template <class F, int... I>
+__device__ __forceinline__ void each_in(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each_of(F&& f) {
+  each_in(f, std::make_integer_sequence<int, N>{});
 }
 
 template <bool F16>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
   if constexpr (F16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same with nothing summed yet.
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 
@@ -162,19 +198,14 @@ __device__ __forceinline__ uint32_t pack_bf162(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Byte offset of 16-byte chunk c of row r in a tile of rows of ROWB bytes. A K load takes rows 0 4 1 5
-// (2 6 3 7) at one place, a V load rows 0 1 2 3 (4 5 6 7): rows whose lines coincide are moved by 32
-// or 64 bytes so that either set covers all banks.
+// Byte offset of 16-byte chunk c of row r in a tile of rows of ROWB bytes: one chunk of 8 neighbouring rows, what a
+// matrix load takes, meets every bank once.
 template <int ROWB>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
-  const int h = ((r >> 1) ^ (r >> 2)) & 1;
-  if constexpr (ROWB == 32) return (uint32_t)((r ^ ((r >> 1) & 2)) * 32 + c * 16);
-  else if constexpr (ROWB == 64) return (uint32_t)(r * 64 + ((c ^ (h << 1)) * 16));
-  else return (uint32_t)(r * ROWB + ((c ^ (((r & 1) << 1) | (h << 2))) * 16));
+  constexpr int LINE = ROWB < 128 ? 128 / ROWB : 1;               // rows of 128 bytes
+  constexpr int MASK = ROWB < 128 ? ROWB / 16 - 1 : 7;
+  return (uint32_t)(r * ROWB + ((c ^ (r / LINE & MASK)) * 16));
 }
-
-// Key of the 16-key block that the MMA's row i stands for.
-__device__ __forceinline__ int key_of_row(int i) { return (i & 8) | ((i & 7) >> 1) | ((i & 1) << 2); }
 
 // Keys that some row of sequence b sees at most, and its pieces of work (at least one: a unit without
 // keys still writes its zeros).
@@ -185,579 +216,733 @@ __device__ __forceinline__ int sequence_keys(const Params& p, int b) {
 }
 
 template <class C>
-__device__ __forceinline__ int pieces(int keys) { return max(1, (keys + C::SPLIT - 1) / C::SPLIT); }
+__device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + C::KT - 1) / C::KT); }
+
+struct Unit {   // what a warp has to do of one unit: tiles [t0, t1) of nt
+  int b, unit, t0, t1, nt, keys, end;
+};
 
 template <class C>
 __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Params p) {
-  constexpr int D = C::D, NT = C::NT, KT = C::KT, KB = KT / 16, GROUPS = C::GROUPS;
+  constexpr int D = C::D, NT = C::NT, KT = C::KT, KB = KT / 16, GROUPS = C::GROUPS, OV = C::OVERHEAD;
   constexpr bool INT4 = C::INT4;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ long long s_scan[kThreads];
-  __shared__ long long s_base;
-  __shared__ int s_first;
+  __shared__ int s_scan[kThreads];
+  __shared__ int s_base[kWarps], s_first[kWarps];
+  __shared__ Unit s_units[kWarps][4];     // units whose copies have begun, by turn
+  __shared__ int s_id[kWarps], s_open[kWarps];
   __shared__ float s_m[kWarps][C::ROWS], s_l[kWarps][C::ROWS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int per_seq = p.c.Hkv * p.row_blocks;   // units of a sequence
 
-  // My share of all pieces: total and, for its first piece, the sequence it lies in.
-  long long mine = 0;
+  // My share of all tiles: total and, for its beginning, the sequence it lies in.
+  int mine = 0;
   const int each = (p.B + kThreads - 1) / kThreads;
-  for (int b = tid * each; b < min(p.B, (tid + 1) * each); ++b) mine += (long long)pieces<C>(sequence_keys(p, b)) * per_seq;
+  for (int b = tid * each; b < min(p.B, (tid + 1) * each); ++b) mine += (tiles_of<C>(sequence_keys(p, b)) + OV) * per_seq;
   s_scan[tid] = mine;
   __syncthreads();
   for (int o = 1; o < kThreads; o <<= 1) {
-    const long long x = tid >= o ? s_scan[tid - o] : 0;
+    const int x = tid >= o ? s_scan[tid - o] : 0;
     __syncthreads();
     s_scan[tid] += x;
     __syncthreads();
   }
-  const long long total = s_scan[kThreads - 1];
-  const long long ctas = min((long long)gridDim.x, total);
-  const long long cta = blockIdx.x;
-  if (tid == 0) p.cut[cta] = make_int4(0, 0, -1, 0);
-  if (cta >= ctas) return;
-  const long long first = cta * total / ctas, last = (cta + 1) * total / ctas;
-  {
-    long long base = s_scan[tid] - mine;
+  const int total = s_scan[kThreads - 1], warps = min((int)gridDim.x * kWarps, total), me = blockIdx.x * kWarps + warp;
+  auto share = [&](int w) { return (int)((long long)w * total / warps); };   // where warp w's begins
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int first = share(min((int)blockIdx.x * kWarps + w, warps));
+    int base = s_scan[tid] - mine;
     if (mine > 0 && base <= first && first < base + mine) {
       int b = tid * each;
       for (;; ++b) {
-        const long long n = (long long)pieces<C>(sequence_keys(p, b)) * per_seq;
+        const int n = (tiles_of<C>(sequence_keys(p, b)) + OV) * per_seq;
         if (first < base + n) break;
         base += n;
       }
-      s_first = b;
-      s_base = base;
+      s_first[w] = b;
+      s_base[w] = base;
     }
   }
+  if (lane == 0) {
+    p.cut[me] = make_int4(0, 0, -1, 0);
+    s_id[warp] = -1;
+  }
   __syncthreads();
-  int b = s_first;
-  long long seq_base = s_base;
-  const uint32_t buf = smem_u32(ring) + warp * C::WARP_BYTES;
-  float* part_of_warp = reinterpret_cast<float*>(ring + warp * C::WARP_BYTES);
 
-  for (long long at = first; at < last;) {
-    // The unit that piece `at` belongs to, and my pieces [p0, p1) of it.
-    int keys = sequence_keys(p, b), np = pieces<C>(keys);
-    while (at >= seq_base + (long long)np * per_seq) {
-      seq_base += (long long)np * per_seq;
-      ++b;
-      keys = sequence_keys(p, b);
-      np = pieces<C>(keys);
-    }
-    if (keys < p.lens[b] || p.lens[b] < 0)
-      if (tid == 0) atomicCAS(p.status, 0u, kStatusBadPage);
-    const int unit = (int)((at - seq_base) / np);
-    const long long unit_base = seq_base + (long long)unit * np;
-    const int p0 = (int)(at - unit_base), p1 = (int)min((long long)np, last - unit_base);
-    const int hkv = unit / p.row_blocks, row0 = unit % p.row_blocks * C::ROWS, rows = p.Nq * p.G;
-    const int key0 = p0 * C::SPLIT + warp * KT, tiles = p1 - p0;
-    const uint8_t* kbase = p.c.k + hkv * p.c.head_b;
-    const uint8_t* vbase = p.c.v + hkv * p.c.head_b;
-    const uint8_t* ksz = p.c.k_sz + hkv * p.c.sz_head_b;
-    const uint8_t* vsz = p.c.v_sz + hkv * p.c.sz_head_b;
-    const int* pages = p.table + b * p.table_stride;
+  const uint32_t buf = smem_u32(ring) + warp * C::WARP_BYTES, ring_end = buf + C::WARP_BYTES;
+  if (me < warps) {
+    // ---- copies: units in turn; of each its query rows (a slot for every 8), then keys and values of every tile
+    const int last = share(me + 1);
+    int at = share(me), seq = s_first[warp], seq_base = s_base[warp];   // next tile to plan for, its sequence
+    int f_turn = 0;              // units entered
+    int f_q = NT, f_tile = 0, f_end = 0, f_keys = 0, f_new = 0, f_b = 0;   // query slots done; tile; its unit's last, keys
+    bool f_values = false, f_unit = false;
+    long long at_row = -1, at_sz = -1;   // lane i: 16-key block i % KB of tile i / KB of a batch (bytes; -1: nowhere)
+    int next_pages = -1;
+    long long q_row = 0;                 // first query row of the unit's heads, and row of its block
+    int f_row0 = 0;
+    constexpr int PER = 32 / KB, CH = C::ROWB / 16, RPI = 32 / CH;   // tiles of a batch; chunks of a row, rows of a copy
+    const long long my_row = (lane / CH) * p.c.token_b + lane % CH * 16, my_sz = lane % 16 * p.c.sz_token_b;
+    long long f_head = 0, f_head_sz = 0;
+    uint32_t fill = buf;                 // slot that the next copies go to
+    const uint32_t my_dst = chunk_at<C::ROWB>(lane / CH, lane % CH);
 
-    // A tile's copies: lane i < KB finds where 16-key block i begins (bytes into k and v, and into the
-    // pairs; -1: nowhere), one tile ahead of the copies themselves.
-    struct Place {
-      long long row, sz;
+    auto look_up = [&](int first) -> int {   // pages of a batch of tiles, read one batch ahead
+      const int tile = first + lane / KB, key = tile * KT + lane % KB * 16;
+      return tile < f_end && key < f_keys ? p.table[f_b * p.table_stride + (uint32_t)(key >> 4) / p.blocks_per_page] : -1;
     };
-    auto look_up = [&](int n) -> Place {
-      const int key = key0 + n * C::SPLIT + lane * 16;
-      Place at{-1, -1};
-      if (lane < KB && n < tiles && key < keys) {
-        const uint32_t block = key >> 4, e = block / p.blocks_per_page;
-        const int page = pages[e], in_page = (block - e * p.blocks_per_page.v) << 4;
+    auto next_batch = [&]() {
+      const int tile = f_tile + lane / KB, key = tile * KT + lane % KB * 16;
+      const int page = next_pages;
+      at_row = at_sz = -1;
+      if (tile < f_end && key < f_keys) {
+        const uint32_t block = key >> 4;
+        const int in_page = (block - block / p.blocks_per_page * p.blocks_per_page.v) << 4;
         if (page >= 0 && page < p.c.num_pages) {
-          at.row = page * p.c.page_b + in_page * p.c.token_b;
-          if (INT4) at.sz = page * p.c.sz_page_b + in_page * p.c.sz_token_b;
+          at_row = page * p.c.page_b + in_page * p.c.token_b;
+          if (INT4) at_sz = page * p.c.sz_page_b + in_page * p.c.sz_token_b;
         } else {
           atomicCAS(p.status, 0u, kStatusBadPage);
         }
       }
-      return at;
+      next_pages = look_up(f_tile + PER);
     };
-    constexpr int CH = C::ROWB / 16, RPI = 32 / CH;   // chunks of a row, rows of one copy instruction
-    const long long my_row = (lane / CH) * p.c.token_b + lane % CH * 16;
-    auto fetch = [&](int n, const Place& place) {
-      if (n < tiles) {
-        const uint32_t dst = buf + n % C::STAGES * C::STAGE;
-        const int valid = keys - (key0 + n * C::SPLIT);
+    // The next unit of my share that has tiles in it; f_unit false when there is none.
+    auto enter = [&]() {
+      f_unit = false;
+      if (at >= last) return;
+      int keys = sequence_keys(p, seq), nt = tiles_of<C>(keys);
+      while (at >= seq_base + (nt + OV) * per_seq) {
+        seq_base += (nt + OV) * per_seq;
+        ++seq;
+        keys = sequence_keys(p, seq);
+        nt = tiles_of<C>(keys);
+      }
+      const int n = p.lens[seq];
+      if (n != keys && lane == 0) atomicCAS(p.status, 0u, kStatusBadPage);
+      const int unit = (at - seq_base) / (nt + OV), base = seq_base + unit * (nt + OV) + OV;   // its first tile
+      const int t0 = max(at - base, 0), t1 = min(nt, last - base);
+      at = base + nt;
+      if (t1 <= t0) return;   // my share ends before the unit's first tile
+      f_unit = true;
+      f_b = seq, f_keys = keys, f_tile = t0, f_end = t1, f_q = 0, f_new = t0, f_values = false;
+      const int hkv = unit / p.row_blocks;
+      f_row0 = (unit - hkv * p.row_blocks) * C::ROWS;
+      q_row = (long long)seq * p.Nq * p.H + hkv * p.G;
+      f_head = hkv * p.c.head_b + my_row;
+      f_head_sz = hkv * p.c.sz_head_b + my_sz;
+      next_pages = look_up(t0);
+      if (lane == 0) s_units[warp][f_turn & 3] = Unit{seq, unit, t0, t1, nt, keys, base + nt};
+      ++f_turn;
+    };
+    auto step = [&]() {
+      if (f_unit) {
+        if (f_q < NT) {
+          constexpr int QCH = D / 8, QRPI = 32 / QCH;   // 16-byte chunks of a query row, rows of a copy
 #pragma unroll
-        for (int i = 0; i < KT / RPI; ++i) {
-          const int r = i * RPI + lane / CH;
-          const long long base = __shfl_sync(0xffffffffu, place.row, i * RPI / 16);
-          const bool in = base >= 0 && r < valid;
-          const long long row = in ? base + my_row + i * RPI % 16 * p.c.token_b : 0;
-          const uint32_t d = dst + chunk_at<C::ROWB>(r, lane % CH);
-          copy16(d, kbase + row, in);
-          copy16(d + C::V_OFF, vbase + row, in);
-        }
-        if constexpr (INT4) {
-          const long long base = __shfl_sync(0xffffffffu, place.sz, lane / 16);
-          const bool in = base >= 0 && lane < valid;
-          const long long row = in ? base + lane % 16 * p.c.sz_token_b : 0;
-          copy_small<C::SZB>(dst + C::KSZ_OFF + lane * C::SZB, ksz + row, in);
-          copy_small<C::SZB>(dst + C::VSZ_OFF + lane * C::SZB, vsz + row, in);
+          for (int i = 0; i < 8 / QRPI; ++i) {
+            const int r = i * QRPI + lane / QCH;
+            const uint32_t row = f_row0 + f_q * 8 + r, qi = row / p.div_g;
+            const bool in = row < (uint32_t)(p.Nq * p.G);
+            const long long from = in ? q_row + (long long)qi * p.H + (row - qi * p.G) : 0;
+            copy16<0>(fill + chunk_at<2 * D>(r, lane % QCH), p.q + from * D + lane % QCH * 8, in);
+          }
+          ++f_q;
+        } else {
+          const int rel = (f_tile - f_new) % PER;
+          if ((C::PAIR || !f_values) && rel == 0) next_batch();
+          const int valid = f_keys - f_tile * KT, from = rel * KB;
+          const uint8_t* src = (!C::PAIR && f_values ? p.c.v : p.c.k) + f_head;
+          const long long to_v = p.c.v - p.c.k;
+          const uint32_t dst = fill + my_dst;
+          long long base[KB];
+          bool full = valid >= KT;
+#pragma unroll
+          for (int i = 0; i < KB; ++i) {
+            base[i] = __shfl_sync(0xffffffffu, at_row, from + i);
+            full = full && base[i] >= 0;
+          }
+          // Copies of one place of chunk_at's 8-row pattern share an address but for a constant.
+          auto copy_rows = [&](auto copy) {
+            each_of<KT / RPI>([&](auto index) {
+              constexpr int I = decltype(index)::value, R = I * RPI, FIRST = R % 8;
+              const uint32_t to = FIRST == 0 ? dst : fill + (chunk_at<C::ROWB>(FIRST + lane / CH, lane % CH) - FIRST * C::ROWB);
+              copy(std::integral_constant<int, R>{}, std::integral_constant<int, R * C::ROWB>{}, to);
+            });
+          };
+          if (full) {   // the same for the whole warp
+            copy_rows([&](auto row, auto off, uint32_t to) {
+              constexpr int R = decltype(row)::value, OFF = decltype(off)::value;
+              const uint8_t* from = src + base[R / 16] + R % 16 * p.c.token_b;
+              copy16<OFF>(to, from);
+              if (C::PAIR) copy16<C::V_OFF + OFF>(to, from + to_v);
+            });
+          } else {      // rows behind the last key, or without a page, become zeros
+            copy_rows([&](auto row, auto off, uint32_t to) {
+              constexpr int R = decltype(row)::value, OFF = decltype(off)::value;
+              const bool in = base[R / 16] >= 0 && R + lane / CH < valid;
+              const uint8_t* from = src + (in ? base[R / 16] + R % 16 * p.c.token_b : -f_head);
+              copy16<OFF>(to, from, in);
+              if (C::PAIR) copy16<C::V_OFF + OFF>(to, from + to_v, in);
+            });
+          }
+          if constexpr (INT4) {
+            const long long base = __shfl_sync(0xffffffffu, at_sz, from + lane / 16);
+            const bool in = base >= 0 && lane < valid;
+            const uint8_t* sz = p.c.k_sz + (in ? f_head_sz + base : 0);
+            copy_small<C::SZ_OFF, C::SZB>(fill + lane * C::SZB, sz, in);
+            copy_small<C::SZV_OFF, C::SZB>(fill + lane * C::SZB, sz + (p.c.v_sz - p.c.k_sz), in);
+          }
+          if (!C::PAIR && !f_values) {
+            f_values = true;
+          } else {
+            f_values = false;
+            if (++f_tile == f_end) enter();
+          }
         }
       }
       copies_commit();
+      fill += C::SLOT;
+      if (fill == ring_end) fill = buf;
     };
+    enter();
+#pragma unroll 1
+    for (int i = 0; i < C::SLOTS - 1; ++i) step();
 
-    Place page = look_up(0);
-#pragma unroll
-    for (int n = 0; n < C::STAGES - 1; ++n) {
-      const Place next = look_up(n + 1);
-      fetch(n, page);
-      page = next;
-    }
-
-    // Query rows as the B operand: lane (g, t) holds row g's values that its K bytes are paired with.
-    constexpr int QR = D / 16;
-    uint32_t qf[NT][QR][2];
-    float mult[NT][2];            // S = mult * (what the products give), per column 2t, 2t + 1
-    float qsum[NT][GROUPS][2];    // 4 bits: sums of q over a group, in units of the products
-    float out[NT][2];             // what a masked product is set to, so that S is -inf
-    int limit[NT][2];             // keys the column's row sees: key < limit
-    int least = INT_MAX;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = row0 + nt * 8 + g;
-      const bool in = r < rows;
-      const __nv_bfloat16* src =
-          p.q + (((long long)b * p.Nq + (in ? r / p.G : 0)) * p.H + hkv * p.G + (in ? r % p.G : 0)) * D;
-      if constexpr (INT4) {
-        uint4 raw[GROUPS][2];
-        float top = 0.f, sum[GROUPS];
-#pragma unroll
-        for (int gr = 0; gr < GROUPS; ++gr) {
-          sum[gr] = 0.f;
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            raw[gr][w] = in ? *reinterpret_cast<const uint4*>(src + gr * 64 + 16 * t + 8 * w) : make_uint4(0, 0, 0, 0);
-            const uint32_t u[4] = {raw[gr][w].x, raw[gr][w].y, raw[gr][w].z, raw[gr][w].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float x = __uint_as_float(u[i] << 16), y = __uint_as_float(u[i] & 0xffff0000u);
-              sum[gr] += x + y;
-              top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
-            }
-          }
-        }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-#pragma unroll
-          for (int gr = 0; gr < GROUPS; ++gr) sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], o);
-        }
-        // q 2^-e has its greatest value in [2^11, 2^12): normal in fp16 down to 2^-21 of it after the 1/16
-        const int e = top > 0.f ? min(max((int)(__float_as_uint(top) >> 23) - 127 - 11, -120), 120) : 0;
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-        for (int gr = 0; gr < GROUPS; ++gr) {
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const uint32_t u[4] = {raw[gr][w].x, raw[gr][w].y, raw[gr][w].z, raw[gr][w].w};
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x[2 * i] = __uint_as_float(u[i] << 16) * down;
-              x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u) * down;
-            }
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {   // word's codes (0, 4), (1, 5) then (2, 6), (3, 7)
-              qf[nt][gr * 4 + 2 * w + s][0] = pack_half2(x[2 * s], x[2 * s + 4]);
-              qf[nt][gr * 4 + 2 * w + s][1] = pack_half2(x[2 * s + 1] * 0.0625f, x[2 * s + 5] * 0.0625f);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) qsum[nt][gr][j] = __shfl_sync(0xffffffffu, sum[gr] * down * 0x1p-24f, (2 * t + j) * 4);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) mult[nt][j] = __shfl_sync(0xffffffffu, up, (2 * t + j) * 4) * p.scale_log2 * 0x1p24f;
-      } else {
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          const uint4 x = in ? *reinterpret_cast<const uint4*>(src + 32 * j + 8 * t) : make_uint4(0, 0, 0, 0);
-          qf[nt][2 * j][0] = x.x;
-          qf[nt][2 * j][1] = x.y;
-          qf[nt][2 * j + 1][0] = x.z;
-          qf[nt][2 * j + 1][1] = x.w;
-        }
-        mult[nt][0] = mult[nt][1] = p.scale_log2;
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int c = row0 + nt * 8 + 2 * t + j;
-        if (mult[nt][j] == 0.f) mult[nt][j] = 0x1p-126f;   // 0 times the masked infinity would be NaN
-        out[nt][j] = mult[nt][j] < 0.f ? INFINITY : -INFINITY;
-        limit[nt][j] = p.causal ? (c < rows ? keys - p.Nq + 1 + c / p.G : keys) : keys;
-        least = min(least, limit[nt][j]);
-      }
-    }
-    least = min(least, __shfl_xor_sync(0xffffffffu, least, 1));
-    least = min(least, __shfl_xor_sync(0xffffffffu, least, 2));
-
-    float acc[NT][D / 16][4];
-    float m[NT][2], l[NT][2], z[NT][INT4 ? GROUPS : 1][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[nt][i][j] = 0.f;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        m[nt][j] = -INFINITY;
-        l[nt][j] = 0.f;
-#pragma unroll
-        for (int gr = 0; gr < (INT4 ? GROUPS : 1); ++gr) z[nt][gr][j] = 0.f;
-      }
-    }
-
-    for (int n = 0; n < tiles; ++n) {
-      copies_wait<C::STAGES - 2>();
+    // ---- products
+    uint32_t slot = buf;   // slot that is read
+    // Its copies are here, and the slot read before, which all lanes are past, takes the next ones.
+    auto turn_to = [&]() {
+      copies_wait<C::SLOTS - 2>();
       __syncwarp();
-      {
-        const Place next = look_up(n + C::STAGES);
-        fetch(n + C::STAGES - 1, page);
-        page = next;
-      }
-      const uint32_t tile = buf + n % C::STAGES * C::STAGE;
-      const int tile_key = key0 + n * C::SPLIT;
-      float s[KB][NT][4], ev[KB][2];
-      uint32_t vs[KB][2][GROUPS];   // (scale, zero) of my two values' rows
-      // S^T = K q^T
+      step();
+    };
+    auto leave = [&]() {
+      slot += C::SLOT;
+      if (slot == ring_end) slot = buf;
+    };
+    // Where this lane's row of a matrix load lies: lanes 0-7 and 8-15 rows 0-7 and 8-15 of a 16-row block's first
+    // chunk, lanes 16-31 of its second. Further pairs of chunks differ in bits 5 and up.
+    const uint32_t my_chunk = chunk_at<C::ROWB>(lane & 15, lane >> 4);
+    for (int turn = 0; turn < f_turn; ++turn) {
+      constexpr int QR = D / 16;
+      // Query rows as the B operand: lane (g, t) holds row g's values that its K bytes are paired with.
+      uint32_t qf[NT][QR][2];
+      float mult[NT][2];            // S = mult * (what the products give), per column 2t, 2t + 1
+      float qsum[NT][GROUPS][2];    // 4 bits: sums of q over a group, in units of the products
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        const int r0 = kb * 16 + key_of_row(g), r1 = r0 + 8;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[kb][nt][j] = 0.f;
+      for (int nt = 0; nt < NT; ++nt) {
+        turn_to();
         if constexpr (INT4) {
-          uint32_t ks[2][GROUPS];
-          load_pairs<GROUPS>(ks[0], tile + C::KSZ_OFF + r0 * C::SZB);
-          load_pairs<GROUPS>(ks[1], tile + C::KSZ_OFF + r1 * C::SZB);
-          load_pairs<GROUPS>(vs[kb][0], tile + C::VSZ_OFF + r0 * C::SZB);
-          load_pairs<GROUPS>(vs[kb][1], tile + C::VSZ_OFF + r1 * C::SZB);
+          uint4 raw[GROUPS][2];
+          float top = 0.f, sum[GROUPS];
 #pragma unroll
           for (int gr = 0; gr < GROUPS; ++gr) {
-            const uint32_t place = (t & 1) * 8;
-            const uint2 w0 = lds64(tile + chunk_at<C::ROWB>(r0, gr * 2 + (t >> 1)) + place);
-            const uint2 w1 = lds64(tile + chunk_at<C::ROWB>(r1, gr * 2 + (t >> 1)) + place);
-            float c[NT][4];
+            sum[gr] = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int w = 0; w < 2; ++w) {
+              raw[gr][w] = lds128(slot + chunk_at<2 * D>(g, gr * 8 + 4 * w + t));   // dims 64 gr + 32 w + 8 t
+              const uint32_t u[4] = {raw[gr][w].x, raw[gr][w].y, raw[gr][w].z, raw[gr][w].w};
 #pragma unroll
-              for (int j = 0; j < 4; ++j) c[nt][j] = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t x0 = (k < 2 ? w0.x : w0.y) >> (k % 2 * 8), x1 = (k < 2 ? w1.x : w1.y) >> (k % 2 * 8);
-              const uint32_t a0 = x0 & 0x000f000fu, a1 = x1 & 0x000f000fu, a2 = x0 & 0x00f000f0u, a3 = x1 & 0x00f000f0u;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma<true>(c[nt], a0, a1, a2, a3, qf[nt][gr * 4 + k][0], qf[nt][gr * 4 + k][1]);
+              for (int i = 0; i < 4; ++i) {
+                const float x = __uint_as_float(u[i] << 16), y = __uint_as_float(u[i] & 0xffff0000u);
+                sum[gr] += x + y;
+                top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
+              }
             }
-            const float sc0 = __uint_as_float(ks[0][gr] << 16), zr0 = __uint_as_float(ks[0][gr] & 0xffff0000u);
-            const float sc1 = __uint_as_float(ks[1][gr] << 16), zr1 = __uint_as_float(ks[1][gr] & 0xffff0000u);
+          }
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+            for (int gr = 0; gr < GROUPS; ++gr) sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], o);
+          }
+          // q 2^-e has its greatest value in [2^11, 2^12): normal in fp16 down to 2^-21 of it after the 1/16
+          const int e = top > 0.f ? min(max((int)(__float_as_uint(top) >> 23) - 127 - 11, -120), 120) : 0;
+          const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+          for (int gr = 0; gr < GROUPS; ++gr) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const uint32_t u[4] = {raw[gr][w].x, raw[gr][w].y, raw[gr][w].z, raw[gr][w].w};
+              float x[8];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __uint_as_float(u[i] << 16) * down;
+                x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u) * down;
+              }
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {   // word's codes (0, 4), (1, 5) then (2, 6), (3, 7)
+                qf[nt][gr * 4 + 2 * w + i][0] = pack_half2(x[2 * i], x[2 * i + 4]);
+                qf[nt][gr * 4 + 2 * w + i][1] = pack_half2(x[2 * i + 1] * 0.0625f, x[2 * i + 5] * 0.0625f);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) qsum[nt][gr][j] = __shfl_sync(0xffffffffu, sum[gr] * down * 0x1p-24f, (2 * t + j) * 4);
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) mult[nt][j] = __shfl_sync(0xffffffffu, up, (2 * t + j) * 4) * p.scale_log2 * 0x1p24f;
+        } else {
+#pragma unroll
+          for (int k = 0; k < QR; k += 2) {   // matrices: 8 rows of four neighbouring chunks
+            const uint4 x = load_matrices<false, 0>(slot + chunk_at<2 * D>(lane & 7, 2 * k + (lane >> 3)));
+            qf[nt][k][0] = x.x;
+            qf[nt][k][1] = x.y;
+            qf[nt][k + 1][0] = x.z;
+            qf[nt][k + 1][1] = x.w;
+          }
+          mult[nt][0] = mult[nt][1] = p.scale_log2;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (mult[nt][j] == 0.f) mult[nt][j] = 0x1p-126f;   // 0 times a masked key's infinity would be NaN
+        leave();
+      }
+      const volatile Unit& unit = s_units[warp][turn & 3];
+      const int keys = unit.keys, t1 = unit.t1, row0 = unit.unit % p.row_blocks * C::ROWS, rows = p.Nq * p.G;
+      int limit[NT][2], least = INT_MAX;   // the column's row sees keys < limit
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int c = row0 + nt * 8 + 2 * t + j;
+          limit[nt][j] = p.causal && c < rows ? keys - p.Nq + 1 + (int)((uint32_t)c / p.div_g) : keys;
+          least = min(least, limit[nt][j]);
+        }
+      least = min(least, __shfl_xor_sync(0xffffffffu, least, 1));
+      least = min(least, __shfl_xor_sync(0xffffffffu, least, 2));
+
+      float acc[NT][D / 16][4];
+      float m[NT][2], l[NT][2], z[NT][INT4 ? GROUPS : 1][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[nt][i][j] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          m[nt][j] = kNone;
+          l[nt][j] = 0.f;
+#pragma unroll
+          for (int gr = 0; gr < (INT4 ? GROUPS : 1); ++gr) z[nt][gr][j] = 0.f;
+        }
+      }
+#pragma unroll 1
+      for (int n = unit.t0; n < t1; ++n) {
+        turn_to();
+        const int tile_key = n * KT;
+        float s[KB][NT][4];
+        // S^T = K q^T
+        each_of<KB>([&](auto block) {
+          constexpr int kb = decltype(block)::value;
+          [[maybe_unused]] const uint32_t pairs = slot + g * C::SZB;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[kb][nt][j] = 0.f;
+          if constexpr (INT4) {
+            uint32_t ks[2][GROUPS];
+            load_pairs<C::SZ_OFF + kb * 16 * C::SZB>(ks[0], pairs);
+            load_pairs<C::SZ_OFF + (kb * 16 + 8) * C::SZB>(ks[1], pairs);
+#pragma unroll
+            for (int gr = 0; gr < GROUPS; ++gr) {
+              // rows g and g + 8: dims 8t .. 8t + 7 of the group's first 32, then of its second
+              const uint4 x = load_matrices<false, kb * 16 * C::ROWB>(slot + (my_chunk ^ gr * 32));
+              float c[NT][4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t x0 = (k < 2 ? x.x : x.z) >> (k % 2 * 8), x1 = (k < 2 ? x.y : x.w) >> (k % 2 * 8);
+                const uint32_t a0 = x0 & 0x000f000fu, a1 = x1 & 0x000f000fu, a2 = x0 & 0x00f000f0u, a3 = x1 & 0x00f000f0u;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  const uint32_t(&q)[2] = qf[nt][gr * 4 + k];
+                  if (k == 0) mma_first(c[nt], a0, a1, a2, a3, q[0], q[1]);
+                  else mma<true>(c[nt], a0, a1, a2, a3, q[0], q[1]);
+                }
+              }
+              const float sc0 = __uint_as_float(ks[0][gr] << 16), zr0 = __uint_as_float(ks[0][gr] & 0xffff0000u);
+              const float sc1 = __uint_as_float(ks[1][gr] << 16), zr1 = __uint_as_float(ks[1][gr] & 0xffff0000u);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  s[kb][nt][j] = fmaf(c[nt][j], sc0, fmaf(zr0, qsum[nt][gr][j], s[kb][nt][j]));
+                  s[kb][nt][2 + j] = fmaf(c[nt][2 + j], sc1, fmaf(zr1, qsum[nt][gr][j], s[kb][nt][2 + j]));
+                }
+            }
+          } else {
+            each_of<QR>([&](auto step) {
+              constexpr int k = decltype(step)::value;
+              const uint4 x = load_matrices<false, kb * 16 * C::ROWB + k / 4 * 128>(slot + (my_chunk ^ k % 4 * 32));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma<false>(s[kb][nt], x.x, x.y, x.z, x.w, qf[nt][k][0], qf[nt][k][1]);
+            });
+          }
+          if (tile_key + KT > least) {   // the same for the whole warp
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                s[kb][nt][j] = fmaf(c[nt][j], sc0, fmaf(zr0, qsum[nt][gr][j], s[kb][nt][j]));
-                s[kb][nt][2 + j] = fmaf(c[nt][2 + j], sc1, fmaf(zr1, qsum[nt][gr][j], s[kb][nt][2 + j]));
+                const float out = mult[nt][j] < 0.f ? INFINITY : -INFINITY;   // so that S is -inf
+                if (tile_key + kb * 16 + g >= limit[nt][j]) s[kb][nt][j] = out;
+                if (tile_key + kb * 16 + g + 8 >= limit[nt][j]) s[kb][nt][2 + j] = out;
               }
           }
-          // exponent of the greatest value scale, one more so that scale 2^-e < 1
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t e = 0;
-#pragma unroll
-            for (int gr = 0; gr < GROUPS; ++gr) e = max(e, vs[kb][i][gr] & 0x7f80u);
-            ev[kb][i] = fmaxf(__uint_as_float(0x4b000000u | (e >> 7)) - (0x1p23f + 126.f), kMinExp);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < D / 32; ++j) {
-            const uint4 x0 = lds128(tile + chunk_at<C::ROWB>(r0, 4 * j + t)), x1 = lds128(tile + chunk_at<C::ROWB>(r1, 4 * j + t));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma<false>(s[kb][nt], x0.x, x1.x, x0.y, x1.y, qf[nt][2 * j][0], qf[nt][2 * j][1]);
-              mma<false>(s[kb][nt], x0.z, x1.z, x0.w, x1.w, qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
-            }
-          }
-          ev[kb][0] = ev[kb][1] = 0.f;
+        });
+        if constexpr (!C::PAIR) {
+          leave();
+          turn_to();
         }
-        if (tile_key + KT > least) {   // the same for the whole warp
+        // Weights p = 2^(S - m). The maximum m of S + log2 scale moves only when a weight times scale outgrows fp16's
+        // room: rarely after the first tile, so that a tile costs a vote instead of the exchanges of a maximum.
+        uint32_t vs[KB][2][INT4 ? GROUPS : 1];   // (scale, zero) of my two values of a block
+        float top_scale[KB][2];
+        each_of<KB * 2>([&](auto index) {
+          constexpr int kb = decltype(index)::value / 2, i = decltype(index)::value % 2;
+          top_scale[kb][i] = 1.f;
+          if constexpr (INT4) {
+            load_pairs<C::SZV_OFF + (kb * 16 + i * 8) * C::SZB>(vs[kb][i], slot + g * C::SZB);
+            float x = kLeastScale;
+#pragma unroll
+            for (int gr = 0; gr < GROUPS; ++gr) x = fmaxf(x, fabsf(__uint_as_float(vs[kb][i][gr] << 16)));
+            top_scale[kb][i] = x;
+          }
+        });
+        float w[KB][NT][4], high = 0.f;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              w[kb][nt][j] = exp2_fast(fmaf(s[kb][nt][j], mult[nt][j & 1], -m[nt][j & 1]));
+              high = fmaxf(high, w[kb][nt][j] * top_scale[kb][j >> 1]);
+            }
+        if (__any_sync(0xffffffffu, high > kHeadroom)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              if (tile_key + r0 >= limit[nt][j]) s[kb][nt][j] = out[nt][j];
-              if (tile_key + r1 >= limit[nt][j]) s[kb][nt][2 + j] = out[nt][j];
+              float x = m[nt][j];
+#pragma unroll
+              for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  // exponent of the scale, one more so that scale 2^-e < 1 (1 for bf16: e = 1)
+                  const float e = (float)((int)(__float_as_uint(top_scale[kb][i]) >> 23) - 126);
+                  x = fmaxf(x, fmaf(s[kb][nt][2 * i + j], mult[nt][j], e));
+                }
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+              const float f = exp2_fast(m[nt][j] - x);
+              m[nt][j] = x;
+              l[nt][j] *= f;
+#pragma unroll
+              for (int gr = 0; gr < (INT4 ? GROUPS : 1); ++gr) z[nt][gr][j] *= f;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                acc[nt][i][j] *= f;
+                acc[nt][i][2 + j] *= f;
+              }
+#pragma unroll
+              for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) w[kb][nt][2 * i + j] = exp2_fast(fmaf(s[kb][nt][2 * i + j], mult[nt][j], -x));
             }
         }
-      }
-      // Running maximum of S + exponent, rescale of what was summed under an older one.
+        // O^T += V^T P^T
+        each_of<KB>([&](auto block) {
+          constexpr int kb = decltype(block)::value;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float top[2];
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float x = -INFINITY;
+            for (int j = 0; j < 2; ++j) l[nt][j] += w[kb][nt][j] + w[kb][nt][2 + j];
+          if constexpr (INT4) {
 #pragma unroll
-          for (int kb = 0; kb < KB; ++kb)
-            x = fmaxf(x, fmaxf(fmaf(s[kb][nt][j], mult[nt][j], ev[kb][0]), fmaf(s[kb][nt][2 + j], mult[nt][j], ev[kb][1])));
+            for (int gr = 0; gr < GROUPS; ++gr) {
+              const uint32_t sv0 = vs[kb][0][gr], sv1 = vs[kb][1][gr];
+              const float sc0 = __uint_as_float(sv0 << 16), zr0 = __uint_as_float(sv0 & 0xffff0000u);
+              const float sc1 = __uint_as_float(sv1 << 16), zr1 = __uint_as_float(sv1 & 0xffff0000u);
+              uint32_t b0[NT], b1[NT];
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-          top[j] = fmaxf(x, m[nt][j]);
-        }
-        if (__any_sync(0xffffffffu, top[0] != m[nt][0] || top[1] != m[nt][1])) {
+              for (int nt = 0; nt < NT; ++nt) {
+                const float(&q)[4] = w[kb][nt];
+                b0[nt] = transpose8x8(pack_half2(q[0] * sc0, q[1] * sc0));
+                b1[nt] = transpose8x8(pack_half2(q[2] * sc1, q[3] * sc1));
+                z[nt][gr][0] += q[0] * zr0 + q[2] * zr1;
+                z[nt][gr][1] += q[1] * zr0 + q[3] * zr1;
+              }
+              // lane (g, t): of keys 2t, 2t + 1 (and 8 further) dims 4g .. 4g + 3 of the group's two halves
+              const uint4 x = load_matrices<true, C::V_OFF + kb * 16 * C::ROWB>(slot + (my_chunk ^ gr * 32));
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float f = m[nt][j] == -INFINITY ? 0.f : exp2_fast(m[nt][j] - top[j]);
-            m[nt][j] = top[j];
-            l[nt][j] *= f;
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t x0 = (i < 2 ? x.x : x.z) >> (i % 2 * 8), x1 = (i < 2 ? x.y : x.w) >> (i % 2 * 8);
+                const uint32_t a0 = x0 & 0x000f000fu, a1 = x0 & 0x00f000f0u, a2 = x1 & 0x000f000fu, a3 = x1 & 0x00f000f0u;
 #pragma unroll
-            for (int gr = 0; gr < (INT4 ? GROUPS : 1); ++gr) z[nt][gr][j] *= f;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              acc[nt][i][j] *= f;
-              acc[nt][i][2 + j] *= f;
+                for (int nt = 0; nt < NT; ++nt) mma<true>(acc[nt][gr * 4 + i], a0, a1, a2, a3, b0[nt], b1[nt]);
+              }
             }
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float ref = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
-#pragma unroll
-          for (int kb = 0; kb < KB; ++kb) {
-            s[kb][nt][j] = exp2_fast(fmaf(s[kb][nt][j], mult[nt][j], -ref));
-            s[kb][nt][2 + j] = exp2_fast(fmaf(s[kb][nt][2 + j], mult[nt][j], -ref));
-            l[nt][j] += s[kb][nt][j] + s[kb][nt][2 + j];
-          }
-        }
-      }
-      // O^T += V^T P^T
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        const int v0 = kb * 16 + t;
-        if constexpr (INT4) {
-#pragma unroll
-          for (int gr = 0; gr < GROUPS; ++gr) {
-            const uint32_t sv0 = vs[kb][0][gr], sv1 = vs[kb][1][gr];
-            const float sc0 = __uint_as_float(sv0 << 16), zr0 = __uint_as_float(sv0 & 0xffff0000u);
-            const float sc1 = __uint_as_float(sv1 << 16), zr1 = __uint_as_float(sv1 & 0xffff0000u);
+          } else {
             uint32_t b0[NT], b1[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const float(&q)[4] = s[kb][nt];
-              b0[nt] = transpose8x8(pack_half2(q[0] * sc0, q[1] * sc0));
-              b1[nt] = transpose8x8(pack_half2(q[2] * sc1, q[3] * sc1));
-              z[nt][gr][0] += q[0] * zr0 + q[2] * zr1;
-              z[nt][gr][1] += q[1] * zr0 + q[3] * zr1;
+              b0[nt] = transpose8x8(pack_bf162(w[kb][nt][0], w[kb][nt][1]));
+              b1[nt] = transpose8x8(pack_bf162(w[kb][nt][2], w[kb][nt][3]));
             }
-            uint32_t w[4];
+            each_of<D / 16>([&](auto index) {
+              constexpr int i = decltype(index)::value;
+              const uint4 x = load_matrices<true, C::V_OFF + kb * 16 * C::ROWB + i / 4 * 128>(slot + (my_chunk ^ i % 4 * 32));
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = lds32(tile + C::V_OFF + chunk_at<C::ROWB>(v0 + 4 * i, gr * 2 + (g >> 2)) + (g & 3) * 4);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const uint32_t sel = half ? 0x7632u : 0x5410u;
-              const uint32_t x = __byte_perm(w[0], w[1], sel), y = __byte_perm(w[2], w[3], sel);
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint32_t xs = x >> (8 * k), ys = y >> (8 * k);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  mma<true>(acc[nt][gr * 4 + 2 * half + k], xs & 0x000f000fu, xs & 0x00f000f0u, ys & 0x000f000fu,
-                            ys & 0x00f000f0u, b0[nt], b1[nt]);
-              }
-            }
+              for (int nt = 0; nt < NT; ++nt) mma<false>(acc[nt][i], x.x, x.z, x.y, x.w, b0[nt], b1[nt]);
+            });
           }
-        } else {
-          uint32_t b0[NT], b1[NT];
+        });
+        leave();
+      }
+
+      // The unit is done, or my share is. Column sums over the lanes that hold its keys.
+      const bool head = unit.t0 == 0, tail = t1 == unit.nt;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            b0[nt] = transpose8x8(pack_bf162(s[kb][nt][0], s[kb][nt][1]));
-            b1[nt] = transpose8x8(pack_bf162(s[kb][nt][2], s[kb][nt][3]));
-          }
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            uint4 w[4];
+        for (int j = 0; j < 2; ++j) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = lds128(tile + C::V_OFF + chunk_at<C::ROWB>(v0 + 4 * i, 8 * j + g));
+          for (int o = 4; o < 32; o <<= 1) {
+            l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], o);
+            if constexpr (INT4) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t u0 = i == 0 ? w[0].x : i == 1 ? w[0].y : i == 2 ? w[0].z : w[0].w;
-              const uint32_t u1 = i == 0 ? w[1].x : i == 1 ? w[1].y : i == 2 ? w[1].z : w[1].w;
-              const uint32_t u2 = i == 0 ? w[2].x : i == 1 ? w[2].y : i == 2 ? w[2].z : w[2].w;
-              const uint32_t u3 = i == 0 ? w[3].x : i == 1 ? w[3].y : i == 2 ? w[3].z : w[3].w;
-              const uint32_t a0 = __byte_perm(u0, u1, 0x5410), a1 = __byte_perm(u0, u1, 0x7632);
-              const uint32_t a2 = __byte_perm(u2, u3, 0x5410), a3 = __byte_perm(u2, u3, 0x7632);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma<false>(acc[nt][j * 4 + i], a0, a1, a2, a3, b0[nt], b1[nt]);
+              for (int gr = 0; gr < GROUPS; ++gr) z[nt][gr][j] += __shfl_xor_sync(0xffffffffu, z[nt][gr][j], o);
             }
           }
         }
+      // O^T of column c, dims d(i) and d(i) + 1 (4 bits) or + 8: MMA rows g and g + 8 of tile i
+      auto value = [&](int nt, int i, int j) -> float2 {
+        const float x = acc[nt][i][j], y = acc[nt][i][2 + j];
+        if constexpr (INT4) return make_float2(x * 0x1p24f + z[nt][i / 4][j], y * 0x1p20f + z[nt][i / 4][j]);
+        else return make_float2(x, y);
+      };
+      auto dim = [&](int i) { return INT4 ? i / 2 * 32 + 4 * g + i % 2 * 2 : 16 * i + g; };
+      const bool whole = head && tail;
+      if (whole || turn + 1 < f_turn) {   // finished, or the last part of a unit that other warps have begun
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int c = nt * 8 + 2 * t + j, row = row0 + c;
+            const float inv = l[nt][j] > 0.f ? 1.f / l[nt][j] : 0.f;
+            const float lse2 = l[nt][j] > 0.f ? m[nt][j] + log2f(l[nt][j]) : -INFINITY;
+            if (!whole) {
+              float* to = p.part_o + ((long long)(2 * me) * C::ROWS + c) * D;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                const float2 x = value(nt, i, j);
+                if constexpr (INT4) *reinterpret_cast<float2*>(to + dim(i)) = make_float2(x.x * inv, x.y * inv);
+                else to[dim(i)] = x.x * inv, to[dim(i) + 8] = x.y * inv;
+              }
+              if (g == 0) p.part_lse[2 * me * C::ROWS + c] = lse2;
+            } else if (row < rows) {
+              const int qi = (uint32_t)row / p.div_g, h = unit.unit / p.row_blocks * p.G + row - qi * p.G;
+              __nv_bfloat16* to = p.o + (((long long)unit.b * p.Nq + qi) * p.H + h) * D;
+              if constexpr (INT4) {
+#pragma unroll
+                for (int i = 0; i < D / 16; i += 2) {
+                  const float2 x = value(nt, i, j), y = value(nt, i + 1, j);
+                  *reinterpret_cast<uint2*>(to + dim(i)) = make_uint2(pack_bf162(x.x * inv, x.y * inv), pack_bf162(y.x * inv, y.y * inv));
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                  const float2 x = value(nt, i, j);
+                  to[dim(i)] = __float2bfloat16_rn(x.x * inv), to[dim(i) + 8] = __float2bfloat16_rn(x.y * inv);
+                }
+              }
+              if (g == 0) p.lse[((long long)unit.b * p.H + h) * p.Nq + qi] = lse2 * 0.69314718055994531f;
+            }
+          }
+      } else {   // my share ends in this unit: joined with the CTA's other warps in it, below
+        copies_wait<0>();
+        __syncwarp();
+        float* part = reinterpret_cast<float*>(ring + warp * C::WARP_BYTES);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int c = nt * 8 + 2 * t + j;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              const float2 x = value(nt, i, j);
+              if constexpr (INT4) *reinterpret_cast<float2*>(part + c * D + dim(i)) = x;
+              else part[c * D + dim(i)] = x.x, part[c * D + dim(i) + 8] = x.y;
+            }
+            if (g == 0) {
+              s_m[warp][c] = m[nt][j];
+              s_l[warp][c] = l[nt][j];
+            }
+          }
+        if (lane == 0) {
+          s_units[warp][0] = Unit{unit.b, unit.unit, unit.t0, t1, unit.nt, keys, unit.end};
+          s_id[warp] = unit.end;   // no two units end at one place
+          s_open[warp] = (head ? 1 : 0) | (tail ? 2 : 0);
+        }
       }
-      __syncwarp();   // all lanes have read the tile before its slot is filled again
     }
     copies_wait<0>();
-    __syncthreads();
+  }
+  __syncthreads();
 
-    // Join the warps: each weighs its part by exp2(its maximum - the CTA's).
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], o);
-          if constexpr (INT4) {
-#pragma unroll
-            for (int gr = 0; gr < GROUPS; ++gr) z[nt][gr][j] += __shfl_xor_sync(0xffffffffu, z[nt][gr][j], o);
-          }
+  // Warps [w0, w1) of this CTA whose shares end in one unit.
+  for (int w0 = 0; w0 < kWarps;) {
+    int w1 = w0 + 1;
+    while (w1 < kWarps && s_id[w1] == s_id[w0]) ++w1;
+    if (s_id[w0] >= 0) {
+      const Unit unit = s_units[w0][0];
+      const int first = blockIdx.x * kWarps + w0, row0 = unit.unit % p.row_blocks * C::ROWS, rows = p.Nq * p.G;
+      const bool head = s_open[w0] & 1, whole = head && (s_open[w1 - 1] & 2);
+      for (int i = tid; i < C::ROWS * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), c = i % (D / 4) * 4, row = row0 + r;
+        float top = s_m[w0][r], sum = 0.f;
+        for (int w = w0 + 1; w < w1; ++w) top = fmaxf(top, s_m[w][r]);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = w0; w < w1; ++w) {
+          const float f = exp2_fast(s_m[w][r] - top);
+          const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(ring + w * C::WARP_BYTES) + r * D + c);
+          sum += s_l[w][r] * f;
+          x.x += y.x * f, x.y += y.y * f, x.z += y.z * f, x.w += y.w * f;
         }
-        if (g == 0) {
-          s_m[warp][nt * 8 + 2 * t + j] = m[nt][j];
-          s_l[warp][nt * 8 + 2 * t + j] = l[nt][j];
-        }
-      }
-    __syncthreads();
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int c = nt * 8 + 2 * t + j;
-        float top = s_m[0][c];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][c]);
-        const float f = m[nt][j] == -INFINITY ? 0.f : exp2_fast(m[nt][j] - top);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          float x = acc[nt][i][j], y = acc[nt][i][2 + j];
-          if constexpr (INT4) {
-            x = x * 0x1p24f + z[nt][i / 4][j];
-            y = y * 0x1p20f + z[nt][i / 4][j];
-          }
-          // MMA rows g, g + 8 of tile i are dims 64 (i / 4) + 8 g + 2 (i % 4) and the next
-          *reinterpret_cast<float2*>(part_of_warp + c * D + i / 4 * 64 + 8 * g + i % 4 * 2) = make_float2(x * f, y * f);
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
+        const float lse2 = sum > 0.f ? top + log2f(sum) : -INFINITY;
+        if (!whole) {
+          const long long to = (long long)(2 * first + 1) * C::ROWS + r;
+          *reinterpret_cast<float4*>(p.part_o + to * D + c) = x;
+          if (c == 0) p.part_lse[to] = lse2;
+        } else if (row < rows) {
+          const int qi = (uint32_t)row / p.div_g, h = unit.unit / p.row_blocks * p.G + row - qi * p.G;
+          *reinterpret_cast<uint2*>(p.o + (((long long)unit.b * p.Nq + qi) * p.H + h) * D + c) =
+              make_uint2(pack_bf162(x.x, x.y), pack_bf162(x.z, x.w));
+          if (c == 0) p.lse[((long long)unit.b * p.H + h) * p.Nq + qi] = lse2 * 0.69314718055994531f;
         }
       }
-    __syncthreads();
-    const bool whole = p0 == 0 && p1 == np;
-    const long long slot = 2 * cta + (p0 == 0 ? 1 : 0);
-    for (int i = tid; i < C::ROWS * (D / 4); i += kThreads) {
-      const int r = i / (D / 4), c = i % (D / 4) * 4;
-      float top = s_m[0][r], sum = 0.f;
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (s_m[w][r] > -INFINITY) sum += s_l[w][r] * exp2_fast(s_m[w][r] - top);
-        const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(ring + w * C::WARP_BYTES) + r * D + c);
-        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-      }
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
-      const float lse2 = sum > 0.f ? top + log2f(sum) : -INFINITY;
-      if (!whole) {
-        *reinterpret_cast<float4*>(p.part_o + (slot * C::ROWS + r) * D + c) = x;
-        if (c == 0) p.part_lse[slot * C::ROWS + r] = lse2;
-      } else if (row0 + r < rows) {
-        const int qi = (row0 + r) / p.G, h = hkv * p.G + (row0 + r) % p.G;
-        uint2 y;
-        y.x = pack_bf162(x.x, x.y);
-        y.y = pack_bf162(x.z, x.w);
-        *reinterpret_cast<uint2*>(p.o + (((long long)b * p.Nq + qi) * p.H + h) * D + c) = y;
-        if (c == 0) p.lse[((long long)b * p.H + h) * p.Nq + qi] = lse2 * 0.69314718055994531f;
+      if (head && !whole && tid == 0) {
+        // The warp with the unit's last tile, at unit.end - 1; whether it goes on to the tiles of a next unit.
+        const int end = unit.end - 1;
+        int w = (int)((long long)end * warps / total);
+        while (share(w + 1) <= end) ++w;
+        while (share(w) > end) --w;
+        p.cut[first] = make_int4(unit.b, unit.unit, w, share(w + 1) > unit.end + OV ? 1 : 0);
       }
     }
-    if (p0 == 0 && !whole && tid == 0) {
-      // the CTA that holds the unit's last piece: the last c with c total / ctas < its end
-      const long long end = unit_base + np - 1;
-      long long c = (end * ctas) / total;
-      while ((c + 1) * total / ctas <= end) ++c;
-      while (c * total / ctas > end) --c;
-      p.cut[cta] = make_int4(b, unit, (int)c, 0);
-    }
-    __syncthreads();   // the ring is free again
-    at = unit_base + p1;
+    w0 = w1;
   }
 }
 
-// Joins the parts of the units that were cut: CTA (c, r) takes row r of the unit that begins in CTA c.
+// Joins the parts of the units that were cut: CTA (c, r) takes row r of the units that begin in warps of CTA c, a warp
+// one of them if it has few parts, all four warps together otherwise.
 // LSE = log2 sum 2^LSE_i,  O = sum 2^(LSE_i - LSE) O_i.
+constexpr int kFewParts = 8;
+
 template <int D>
-__global__ void __launch_bounds__(128) attn_paged_join_kernel(const Params p, int rows_per_unit) {
+__global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params p, int rows_per_unit) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int LANES = D / 4, WAYS = 128 / LANES;
-  const int4 cut = p.cut[blockIdx.x];
-  const int r = blockIdx.y, hkv = cut.y / p.row_blocks, row = cut.y % p.row_blocks * rows_per_unit + r;
-  if (cut.z < 0 || row >= p.Nq * p.G) return;
-  const int parts = cut.z - (int)blockIdx.x + 1;
-  const int tid = threadIdx.x, c = tid % LANES * 4, way = tid / LANES;
-  // part 0 is slot 2c + 1 of CTA c, part i > 0 slot 2 (c + i)
-  auto at = [&](int i) -> long long {
-    return ((i == 0 ? 2LL * blockIdx.x + 1 : 2LL * (blockIdx.x + i)) * rows_per_unit + r);
+  constexpr int LANES = D / 4;                // lanes of a row
+  constexpr int STEP = LANES < 32 ? LANES : 32, V = LANES / STEP, WAYS = 32 / STEP;   // of a warp: values each, rows at once
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, c = lane % STEP * 4, way = lane / STEP, r = blockIdx.y;
+  auto cut_of = [&](int k) {
+    const int4 cut = p.cut[blockIdx.x * kWarps + k];
+    return cut.z >= 0 && cut.y % p.row_blocks * rows_per_unit + r < p.Nq * p.G ? cut : make_int4(0, 0, -1, 0);
   };
-  __shared__ float s_top[128], s_sum[WAYS];
-  __shared__ float4 s_x[128];
-  float top = -INFINITY;
-  for (int i = tid; i < parts; i += 128) top = fmaxf(top, p.part_lse[at(i)]);
-  s_top[tid] = top;
-  __syncthreads();
-  for (int o = 64; o > 0; o >>= 1) {
-    if (tid < o) s_top[tid] = fmaxf(s_top[tid], s_top[tid + o]);
-    __syncthreads();
-  }
-  top = s_top[0];
-  float sum = 0.f;
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (top > -INFINITY) {
+  // Parts of a unit that begins in warp k: slot 2 first + 1, one of each later CTA's first warp, and of the last warp its
+  // slot for a unit that ends inside a share (then the last CTA's first warp has one only if it is not that warp).
+  auto joined_of = [&](const int4& cut) { return max(cut.z / kWarps - (int)blockIdx.x - (cut.w && cut.z % kWarps == 0 ? 1 : 0), 0); };
+  // Parts first, first + stride, .. of a unit: their weighted sums for this lane, and the weights'.
+  struct Sum {
+    float top, sum;
+    float4 x[V];
+  };
+  auto gather = [&](const int4& cut, int k, int first, int stride) {
+    const int joined = joined_of(cut), parts = 1 + joined + cut.w, from = blockIdx.x * kWarps + k;
+    auto at = [&](int i) -> long long {
+      const long long slot = i == 0 ? 2LL * from + 1 : i <= joined ? 2LL * kWarps * (blockIdx.x + i) + 1 : 2LL * cut.z;
+      return slot * rows_per_unit + r;
+    };
+    Sum s{-INFINITY, 0.f, {}};
+    for (int i = lane; i < parts; i += 32) s.top = fmaxf(s.top, p.part_lse[at(i)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s.top = fmaxf(s.top, __shfl_xor_sync(0xffffffffu, s.top, o));
+    if (s.top == -INFINITY) return s;
 #pragma unroll 4
-    for (int i = way; i < parts; i += WAYS) {
-      const float f = exp2_fast(p.part_lse[at(i)] - top);
-      const float4 y = *reinterpret_cast<const float4*>(p.part_o + at(i) * D + c);
-      sum += f;
-      x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
+    for (int i = first * WAYS + way; i < parts; i += stride * WAYS) {
+      const float f = exp2_fast(p.part_lse[at(i)] - s.top);
+      s.sum += f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float4 y = *reinterpret_cast<const float4*>(p.part_o + at(i) * D + v * 128 + c);
+        s.x[v].x += f * y.x, s.x[v].y += f * y.y, s.x[v].z += f * y.z, s.x[v].w += f * y.w;
+      }
     }
-  }
-  s_x[tid] = x;
-  if (c == 0) s_sum[way] = sum;
-  __syncthreads();
-  if (way == 0) {
-    for (int w = 1; w < WAYS; ++w) {
-      const float4 y = s_x[w * LANES + tid];
-      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-      sum += s_sum[w];
+    if constexpr (WAYS > 1) {
+#pragma unroll
+      for (int o = STEP; o < 32; o <<= 1) {
+        s.sum += __shfl_xor_sync(0xffffffffu, s.sum, o);
+        s.x[0].x += __shfl_xor_sync(0xffffffffu, s.x[0].x, o);
+        s.x[0].y += __shfl_xor_sync(0xffffffffu, s.x[0].y, o);
+        s.x[0].z += __shfl_xor_sync(0xffffffffu, s.x[0].z, o);
+        s.x[0].w += __shfl_xor_sync(0xffffffffu, s.x[0].w, o);
+      }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int qi = row / p.G, h = hkv * p.G + row % p.G;
-    uint2 y;
-    y.x = pack_bf162(x.x * inv, x.y * inv);
-    y.y = pack_bf162(x.z * inv, x.w * inv);
-    *reinterpret_cast<uint2*>(p.o + (((long long)cut.x * p.Nq + qi) * p.H + h) * D + c) = y;
-    if (c == 0)
-      p.lse[((long long)cut.x * p.H + h) * p.Nq + qi] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+    return s;
+  };
+  auto store = [&](const int4& cut, const Sum& s) {
+    const int hkv = cut.y / p.row_blocks, row = (cut.y - hkv * p.row_blocks) * rows_per_unit + r;
+    const int qi = (uint32_t)row / p.div_g, h = hkv * p.G + row - qi * p.G;
+    const float inv = s.sum > 0.f ? 1.f / s.sum : 0.f;
+    if (way == 0) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        *reinterpret_cast<uint2*>(p.o + (((long long)cut.x * p.Nq + qi) * p.H + h) * D + v * 128 + c) =
+            make_uint2(pack_bf162(s.x[v].x * inv, s.x[v].y * inv), pack_bf162(s.x[v].z * inv, s.x[v].w * inv));
+    }
+    if (lane == 0)
+      p.lse[((long long)cut.x * p.H + h) * p.Nq + qi] = s.sum > 0.f ? (s.top + log2f(s.sum)) * 0.69314718055994531f : -INFINITY;
+  };
+  const int4 mine = cut_of(warp);
+  const bool many = mine.z >= 0 && 1 + joined_of(mine) + mine.w > kFewParts;
+  if (mine.z >= 0 && !many) store(mine, gather(mine, warp, 0, 1));
+  if (!__syncthreads_or(many)) return;
+  __shared__ Sum sums[kWarps][32];
+  for (int k = 0; k < kWarps; ++k) {
+    const int4 cut = cut_of(k);   // the same for the whole CTA
+    if (cut.z < 0 || 1 + joined_of(cut) + cut.w <= kFewParts) continue;
+    sums[warp][lane] = gather(cut, k, warp, kWarps);
+    __syncthreads();
+    if (warp == 0) {
+      Sum s = sums[0][lane];
+      for (int w = 1; w < kWarps; ++w) {
+        const Sum& y = sums[w][lane];
+        s.sum += y.sum;
+#pragma unroll
+        for (int v = 0; v < V; ++v) s.x[v].x += y.x[v].x, s.x[v].y += y.x[v].y, s.x[v].z += y.x[v].z, s.x[v].w += y.x[v].w;
+      }
+      store(cut, s);
+    }
+    __syncthreads();   // the sums are free again
   }
 }
 
 struct Plan {
-  int rows_per_unit, row_blocks, grid, split;
+  int rows_per_unit, row_blocks, grid, tile, overhead;
 };
 
-// Rows a unit holds (8, or 16 at d <= 128 when a call has more than 8: d = 256 has no registers for
-// them) and the CTAs that fill the device.
+// Rows a unit holds (8, or 16 at d <= 128 when a call has more: d = 256 has no registers for them) and the CTAs that fill
+// the device.
 template <int D, bool INT4>
 Plan plan_for(int rows, int sms) {
   constexpr int NT2 = D <= 128 ? 2 : 1;
-  const bool two = rows > 8 && NT2 == 2;
-  const int per = two ? 16 : 8;
-  return {per, (rows + per - 1) / per, sms * (two ? Cfg<D, INT4, NT2>::CTAS : Cfg<D, INT4, 1>::CTAS), Cfg<D, INT4, 1>::SPLIT};
+  const int per = rows > 8 ? 8 * NT2 : 8;
+  return {per, (rows + per - 1) / per, sms * (per == 16 ? Cfg<D, INT4, NT2>::CTAS : Cfg<D, INT4, 1>::CTAS),
+          Cfg<D, INT4, 1>::KT, Cfg<D, INT4, 1>::OVERHEAD};
 }
 
 Plan make_plan(int d, bool int4, int rows, int sms) {
@@ -777,7 +962,7 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t s) {
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, (unsigned)std::min(C::ROWS, p.Nq * p.G));
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -799,9 +984,10 @@ size_t pad(size_t x) { return (x + 255) / 256 * 256; }
 
 // Bytes of the parts, of their LSE, and of the cut units.
 void workspace_parts(const Plan& pl, int d, size_t (&n)[3]) {
-  n[0] = pad((size_t)2 * pl.grid * pl.rows_per_unit * d * 4);
-  n[1] = pad((size_t)2 * pl.grid * pl.rows_per_unit * 4);
-  n[2] = pad((size_t)pl.grid * sizeof(int4));
+  const size_t warps = (size_t)pl.grid * kWarps;
+  n[0] = pad(2 * warps * pl.rows_per_unit * d * 4);
+  n[1] = pad(2 * warps * pl.rows_per_unit * 4);
+  n[2] = pad(warps * sizeof(int4));
 }
 
 bool shape_ok(int B, int H, int Hkv, int Nq) { return B >= 1 && H >= 1 && Hkv >= 1 && Nq >= 1 && H % Hkv == 0; }
@@ -864,12 +1050,15 @@ extern "C" attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t*
   p.causal = causal != 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.blocks_per_page = fast_div((uint32_t)cache->page_size / 16);
+  p.div_g = fast_div((uint32_t)p.G);
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + n[0]);
   p.cut = reinterpret_cast<::int4*>(static_cast<uint8_t*>(workspace) + n[0] + n[1]);
-  // No more CTAs than pieces of work there can be.
-  const long long most = (long long)B * Hkv * pl.row_blocks * std::max<long long>(1, ((long long)max_pages * cache->page_size + pl.split - 1) / pl.split);
-  const int grid = (int)std::min<long long>(pl.grid, most);
+  // No more warps than tiles there can be; tiles are counted in 32 bits.
+  const long long most = (long long)B * Hkv * pl.row_blocks *
+                         (std::max<long long>(1, ((long long)max_pages * cache->page_size + pl.tile - 1) / pl.tile) + pl.overhead);
+  if (most > INT_MAX) return ATTN_ERR_UNSUPPORTED;
+  const int grid = (int)std::min<long long>(pl.grid, (most + kWarps - 1) / kWarps);
   cudaError_t e;
   switch (d) {
     case 64: e = bits4 ? launch_rows<64, true>(p, pl.rows_per_unit, grid, stream) : launch_rows<64, false>(p, pl.rows_per_unit, grid, stream); break;
