@@ -9,8 +9,8 @@
 //
 // 4-bit codes go to the tensor cores as they are. A code c in the low bits of a half is the
 // subnormal fp16 number c 2^-24, and 4 bits higher it is 16 c 2^-24: a pair of operands costs one AND.
-// For keys the factor 16 is taken out of the query's matching values; for values it falls on
-// separate output rows. Scale and zero stay outside the products, in fp32:
+// For keys the factor 16 is taken out of the query's matching values; for values a pair of rows sums
+// low codes and whole bytes, low + 16 high, whose difference is taken once at the end. Scale and zero stay outside the products, in fp32:
 //   q.k = sum over groups  scale (codes . q) + zero sum(q),
 //   O   = (sum_j (p_j scale_j) codes_j + sum_j p_j zero_j) / sum_j p_j.
 // q is scaled by a power of two per row, so fp16 holds it exactly where it counts (2^-25 of the row's
@@ -189,6 +189,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// Bytes 1 and 3 as two 16-bit values.
+__device__ __forceinline__ uint32_t high_bytes(uint32_t x) { return __byte_perm(x, 0, 0x4341); }
+__device__ __forceinline__ uint32_t subtract_half2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -218,6 +225,13 @@ __device__ __forceinline__ int sequence_keys(const Params& p, int b) {
 template <class C>
 __device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + C::KT - 1) / C::KT); }
 
+// Where a warp is in its share: the next tile to plan for, its sequence, what that begins with; of the unit that is being
+// copied the sequence, the first query row of its heads and of its block.
+struct Cursor {
+  int at, last, seq, seq_base, b, hkv, row0;
+  long long q_row;
+};
+
 struct Unit {   // what a warp has to do of one unit: tiles [t0, t1) of nt
   int b, unit, t0, t1, nt, keys, end;
 };
@@ -227,11 +241,13 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
   constexpr int D = C::D, NT = C::NT, KT = C::KT, KB = KT / 16, GROUPS = C::GROUPS, OV = C::OVERHEAD;
   constexpr bool INT4 = C::INT4;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ int s_scan[kThreads];
+  __shared__ int s_scan[kWarps];
   __shared__ int s_base[kWarps], s_first[kWarps];
   __shared__ Unit s_units[kWarps][4];     // units whose copies have begun, by turn
+  __shared__ Cursor s_cursor[kWarps];     // here, not in registers: needed once a unit
   __shared__ int s_id[kWarps], s_open[kWarps];
   __shared__ float s_m[kWarps][C::ROWS], s_l[kWarps][C::ROWS];
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // launched early: what it reads may be a previous kernel's
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int per_seq = p.c.Hkv * p.row_blocks;   // units of a sequence
 
@@ -239,22 +255,28 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
   int mine = 0;
   const int each = (p.B + kThreads - 1) / kThreads;
   for (int b = tid * each; b < min(p.B, (tid + 1) * each); ++b) mine += (tiles_of<C>(sequence_keys(p, b)) + OV) * per_seq;
-  s_scan[tid] = mine;
-  __syncthreads();
-  for (int o = 1; o < kThreads; o <<= 1) {
-    const int x = tid >= o ? s_scan[tid - o] : 0;
-    __syncthreads();
-    s_scan[tid] += x;
-    __syncthreads();
+  int upto = mine;   // of this warp's threads up to me
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
   }
-  const int total = s_scan[kThreads - 1], warps = min((int)gridDim.x * kWarps, total), me = blockIdx.x * kWarps + warp;
-  auto share = [&](int w) { return (int)((long long)w * total / warps); };   // where warp w's begins
+  if (lane == 31) s_scan[warp] = upto;
+  __syncthreads();
+  int total = 0, base0 = upto - mine;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) base0 += s_scan[w];
+    total += s_scan[w];
+  }
+  const int warps = min((int)gridDim.x * kWarps, total), me = blockIdx.x * kWarps + warp;
+  const int part = total / warps, more = total - part * warps;         // the first `more` shares have one tile more
+  auto share = [&](int w) { return w * part + min(w, more); };         // where warp w's begins
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     const int first = share(min((int)blockIdx.x * kWarps + w, warps));
-    int base = s_scan[tid] - mine;
-    if (mine > 0 && base <= first && first < base + mine) {
-      int b = tid * each;
+    if (base0 <= first && first < base0 + mine) {
+      int b = tid * each, base = base0;
       for (;; ++b) {
         const int n = (tiles_of<C>(sequence_keys(p, b)) + OV) * per_seq;
         if (first < base + n) break;
@@ -273,24 +295,22 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
   const uint32_t buf = smem_u32(ring) + warp * C::WARP_BYTES, ring_end = buf + C::WARP_BYTES;
   if (me < warps) {
     // ---- copies: units in turn; of each its query rows (a slot for every 8), then keys and values of every tile
-    const int last = share(me + 1);
-    int at = share(me), seq = s_first[warp], seq_base = s_base[warp];   // next tile to plan for, its sequence
+    volatile Cursor& cur = s_cursor[warp];
+    if (lane == 0) cur.at = share(me), cur.last = share(me + 1), cur.seq = s_first[warp], cur.seq_base = s_base[warp];
+    __syncwarp();
     int f_turn = 0;              // units entered
-    int f_q = NT, f_tile = 0, f_end = 0, f_keys = 0, f_new = 0, f_b = 0;   // query slots done; tile; its unit's last, keys
+    int f_q = NT, f_tile = 0, f_end = 0, f_keys = 0, f_rel = 0;   // query slots done; tile; its unit's last, keys; in a batch
     bool f_values = false, f_unit = false;
     long long at_row = -1, at_sz = -1;   // lane i: 16-key block i % KB of tile i / KB of a batch (bytes; -1: nowhere)
     int next_pages = -1;
-    long long q_row = 0;                 // first query row of the unit's heads, and row of its block
-    int f_row0 = 0;
     constexpr int PER = 32 / KB, CH = C::ROWB / 16, RPI = 32 / CH;   // tiles of a batch; chunks of a row, rows of a copy
     const long long my_row = (lane / CH) * p.c.token_b + lane % CH * 16, my_sz = lane % 16 * p.c.sz_token_b;
-    long long f_head = 0, f_head_sz = 0;
     uint32_t fill = buf;                 // slot that the next copies go to
     const uint32_t my_dst = chunk_at<C::ROWB>(lane / CH, lane % CH);
 
     auto look_up = [&](int first) -> int {   // pages of a batch of tiles, read one batch ahead
       const int tile = first + lane / KB, key = tile * KT + lane % KB * 16;
-      return tile < f_end && key < f_keys ? p.table[f_b * p.table_stride + (uint32_t)(key >> 4) / p.blocks_per_page] : -1;
+      return tile < f_end && key < f_keys ? p.table[cur.b * p.table_stride + (uint32_t)(key >> 4) / p.blocks_per_page] : -1;
     };
     auto next_batch = [&]() {
       const int tile = f_tile + lane / KB, key = tile * KT + lane % KB * 16;
@@ -298,10 +318,10 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
       at_row = at_sz = -1;
       if (tile < f_end && key < f_keys) {
         const uint32_t block = key >> 4;
-        const int in_page = (block - block / p.blocks_per_page * p.blocks_per_page.v) << 4;
+        const int in_page = (block - block / p.blocks_per_page * p.blocks_per_page.v) << 4, hkv = cur.hkv;
         if (page >= 0 && page < p.c.num_pages) {
-          at_row = page * p.c.page_b + in_page * p.c.token_b;
-          if (INT4) at_sz = page * p.c.sz_page_b + in_page * p.c.sz_token_b;
+          at_row = page * p.c.page_b + in_page * p.c.token_b + hkv * p.c.head_b;
+          if (INT4) at_sz = page * p.c.sz_page_b + in_page * p.c.sz_token_b + hkv * p.c.sz_head_b;
         } else {
           atomicCAS(p.status, 0u, kStatusBadPage);
         }
@@ -311,29 +331,29 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
     // The next unit of my share that has tiles in it; f_unit false when there is none.
     auto enter = [&]() {
       f_unit = false;
+      const int at = cur.at, last = cur.last;
       if (at >= last) return;
-      int keys = sequence_keys(p, seq), nt = tiles_of<C>(keys);
+      int seq = cur.seq, seq_base = cur.seq_base, keys = sequence_keys(p, seq), nt = tiles_of<C>(keys);
       while (at >= seq_base + (nt + OV) * per_seq) {
         seq_base += (nt + OV) * per_seq;
         ++seq;
         keys = sequence_keys(p, seq);
         nt = tiles_of<C>(keys);
       }
-      const int n = p.lens[seq];
-      if (n != keys && lane == 0) atomicCAS(p.status, 0u, kStatusBadPage);
+      if (p.lens[seq] != keys && lane == 0) atomicCAS(p.status, 0u, kStatusBadPage);
       const int unit = (at - seq_base) / (nt + OV), base = seq_base + unit * (nt + OV) + OV;   // its first tile
-      const int t0 = max(at - base, 0), t1 = min(nt, last - base);
-      at = base + nt;
+      const int t0 = max(at - base, 0), t1 = min(nt, last - base), hkv = unit / p.row_blocks;
+      __syncwarp();
+      if (lane == 0) {
+        cur.at = base + nt, cur.seq = seq, cur.seq_base = seq_base, cur.b = seq, cur.hkv = hkv;
+        cur.row0 = (unit - hkv * p.row_blocks) * C::ROWS, cur.q_row = (long long)seq * p.Nq * p.H + hkv * p.G;
+        s_units[warp][f_turn & 3] = Unit{seq, unit, t0, t1, nt, keys, base + nt};
+      }
+      __syncwarp();
       if (t1 <= t0) return;   // my share ends before the unit's first tile
       f_unit = true;
-      f_b = seq, f_keys = keys, f_tile = t0, f_end = t1, f_q = 0, f_new = t0, f_values = false;
-      const int hkv = unit / p.row_blocks;
-      f_row0 = (unit - hkv * p.row_blocks) * C::ROWS;
-      q_row = (long long)seq * p.Nq * p.H + hkv * p.G;
-      f_head = hkv * p.c.head_b + my_row;
-      f_head_sz = hkv * p.c.sz_head_b + my_sz;
+      f_keys = keys, f_tile = t0, f_end = t1, f_q = 0, f_rel = 0, f_values = false;
       next_pages = look_up(t0);
-      if (lane == 0) s_units[warp][f_turn & 3] = Unit{seq, unit, t0, t1, nt, keys, base + nt};
       ++f_turn;
     };
     auto step = [&]() {
@@ -343,17 +363,16 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
 #pragma unroll
           for (int i = 0; i < 8 / QRPI; ++i) {
             const int r = i * QRPI + lane / QCH;
-            const uint32_t row = f_row0 + f_q * 8 + r, qi = row / p.div_g;
+            const uint32_t row = cur.row0 + f_q * 8 + r, qi = row / p.div_g;
             const bool in = row < (uint32_t)(p.Nq * p.G);
-            const long long from = in ? q_row + (long long)qi * p.H + (row - qi * p.G) : 0;
+            const long long from = in ? cur.q_row + (long long)qi * p.H + (row - qi * p.G) : 0;
             copy16<0>(fill + chunk_at<2 * D>(r, lane % QCH), p.q + from * D + lane % QCH * 8, in);
           }
           ++f_q;
         } else {
-          const int rel = (f_tile - f_new) % PER;
-          if ((C::PAIR || !f_values) && rel == 0) next_batch();
-          const int valid = f_keys - f_tile * KT, from = rel * KB;
-          const uint8_t* src = (!C::PAIR && f_values ? p.c.v : p.c.k) + f_head;
+          if (f_rel == 0 && (C::PAIR || !f_values)) next_batch();
+          const int valid = f_keys - f_tile * KT, from = f_rel * KB;
+          const uint8_t* src = (!C::PAIR && f_values ? p.c.v : p.c.k) + my_row;
           const long long to_v = p.c.v - p.c.k;
           const uint32_t dst = fill + my_dst;
           long long base[KB];
@@ -382,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
             copy_rows([&](auto row, auto off, uint32_t to) {
               constexpr int R = decltype(row)::value, OFF = decltype(off)::value;
               const bool in = base[R / 16] >= 0 && R + lane / CH < valid;
-              const uint8_t* from = src + (in ? base[R / 16] + R % 16 * p.c.token_b : -f_head);
+              const uint8_t* from = src + (in ? base[R / 16] + R % 16 * p.c.token_b : -my_row);
               copy16<OFF>(to, from, in);
               if (C::PAIR) copy16<C::V_OFF + OFF>(to, from + to_v, in);
             });
@@ -390,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
           if constexpr (INT4) {
             const long long base = __shfl_sync(0xffffffffu, at_sz, from + lane / 16);
             const bool in = base >= 0 && lane < valid;
-            const uint8_t* sz = p.c.k_sz + (in ? f_head_sz + base : 0);
+            const uint8_t* sz = p.c.k_sz + (in ? my_sz + base : 0);
             copy_small<C::SZ_OFF, C::SZB>(fill + lane * C::SZB, sz, in);
             copy_small<C::SZV_OFF, C::SZB>(fill + lane * C::SZB, sz + (p.c.v_sz - p.c.k_sz), in);
           }
@@ -398,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
             f_values = true;
           } else {
             f_values = false;
+            f_rel = (f_rel + 1) % PER;
             if (++f_tile == f_end) enter();
           }
         }
@@ -553,8 +573,14 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
               float c[NT][4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const uint32_t x0 = (k < 2 ? x.x : x.z) >> (k % 2 * 8), x1 = (k < 2 ? x.y : x.w) >> (k % 2 * 8);
-                const uint32_t a0 = x0 & 0x000f000fu, a1 = x1 & 0x000f000fu, a2 = x0 & 0x00f000f0u, a3 = x1 & 0x00f000f0u;
+                const uint32_t x0 = k < 2 ? x.x : x.z, x1 = k < 2 ? x.y : x.w;
+                uint32_t a0, a1, a2, a3;   // low codes of both rows, high codes
+                if (k % 2 == 0) {
+                  a0 = x0 & 0x000f000fu, a1 = x1 & 0x000f000fu, a2 = x0 & 0x00f000f0u, a3 = x1 & 0x00f000f0u;
+                } else {
+                  const uint32_t y0 = high_bytes(x0), y1 = high_bytes(x1);
+                  a0 = y0 & 0x000f000fu, a1 = y1 & 0x000f000fu, a2 = subtract_half2(y0, a0), a3 = subtract_half2(y1, a1);
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                   const uint32_t(&q)[2] = qf[nt][gr * 4 + k];
@@ -610,17 +636,19 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
             top_scale[kb][i] = x;
           }
         });
-        float w[KB][NT][4], high = 0.f;
+        float w[KB][NT][4], high = 0.f, most = 0.f;
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+        for (int kb = 0; kb < KB; ++kb) {
+          most = fmaxf(most, fmaxf(top_scale[kb][0], top_scale[kb][1]));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               w[kb][nt][j] = exp2_fast(fmaf(s[kb][nt][j], mult[nt][j & 1], -m[nt][j & 1]));
-              high = fmaxf(high, w[kb][nt][j] * top_scale[kb][j >> 1]);
+              high = fmaxf(high, w[kb][nt][j]);
             }
-        if (__any_sync(0xffffffffu, high > kHeadroom)) {
+        }
+        if (__any_sync(0xffffffffu, high * most > kHeadroom)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -678,10 +706,11 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
               const uint4 x = load_matrices<true, C::V_OFF + kb * 16 * C::ROWB>(slot + (my_chunk ^ gr * 32));
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const uint32_t x0 = (i < 2 ? x.x : x.z) >> (i % 2 * 8), x1 = (i < 2 ? x.y : x.w) >> (i % 2 * 8);
-                const uint32_t a0 = x0 & 0x000f000fu, a1 = x0 & 0x00f000f0u, a2 = x1 & 0x000f000fu, a3 = x1 & 0x00f000f0u;
+                const uint32_t x0 = i < 2 ? x.x : x.z, x1 = i < 2 ? x.y : x.w;
+                const uint32_t y0 = i % 2 ? high_bytes(x0) : x0 & 0x00ff00ffu, y1 = i % 2 ? high_bytes(x1) : x1 & 0x00ff00ffu;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma<true>(acc[nt][gr * 4 + i], a0, a1, a2, a3, b0[nt], b1[nt]);
+                for (int nt = 0; nt < NT; ++nt)   // low codes, and low + 16 high
+                  mma<true>(acc[nt][gr * 4 + i], y0 & 0x000f000fu, y0, y1 & 0x000f000fu, y1, b0[nt], b1[nt]);
               }
             }
           } else {
@@ -720,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
       // O^T of column c, dims d(i) and d(i) + 1 (4 bits) or + 8: MMA rows g and g + 8 of tile i
       auto value = [&](int nt, int i, int j) -> float2 {
         const float x = acc[nt][i][j], y = acc[nt][i][2 + j];
-        if constexpr (INT4) return make_float2(x * 0x1p24f + z[nt][i / 4][j], y * 0x1p20f + z[nt][i / 4][j]);
+        if constexpr (INT4) return make_float2(x * 0x1p24f + z[nt][i / 4][j], (y - x) * 0x1p20f + z[nt][i / 4][j]);
         else return make_float2(x, y);
       };
       auto dim = [&](int i) { return INT4 ? i / 2 * 32 + 4 * g + i % 2 * 2 : 16 * i + g; };
@@ -790,6 +819,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
     }
     copies_wait<0>();
   }
+  // The joining kernel's CTAs may take the room that CTAs of this one leave; they wait for all of its results.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
 
   // Warps [w0, w1) of this CTA whose shares end in one unit.
@@ -802,10 +833,13 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
       const bool head = s_open[w0] & 1, whole = head && (s_open[w1 - 1] & 2);
       for (int i = tid; i < C::ROWS * (D / 4); i += kThreads) {
         const int r = i / (D / 4), c = i % (D / 4) * 4, row = row0 + r;
-        float top = s_m[w0][r], sum = 0.f;
-        for (int w = w0 + 1; w < w1; ++w) top = fmaxf(top, s_m[w][r]);
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, w >= w0 && w < w1 ? s_m[w][r] : -INFINITY);
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = w0; w < w1; ++w) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < w0 || w >= w1) continue;
           const float f = exp2_fast(s_m[w][r] - top);
           const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(ring + w * C::WARP_BYTES) + r * D + c);
           sum += s_l[w][r] * f;
@@ -826,11 +860,9 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
         }
       }
       if (head && !whole && tid == 0) {
-        // The warp with the unit's last tile, at unit.end - 1; whether it goes on to the tiles of a next unit.
-        const int end = unit.end - 1;
-        int w = (int)((long long)end * warps / total);
-        while (share(w + 1) <= end) ++w;
-        while (share(w) > end) --w;
+        // The warp with the unit's last tile; whether it goes on to the tiles of a next unit.
+        const int end = unit.end - 1, long_ones = more * (part + 1);
+        const int w = end < long_ones ? end / (part + 1) : more + (end - long_ones) / part;
         p.cut[first] = make_int4(unit.b, unit.unit, w, share(w + 1) > unit.end + OV ? 1 : 0);
       }
     }
@@ -907,9 +939,36 @@ __global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params 
     if (lane == 0)
       p.lse[((long long)cut.x * p.H + h) * p.Nq + qi] = s.sum > 0.f ? (s.top + log2f(s.sum)) * 0.69314718055994531f : -INFINITY;
   };
+  // A few parts: everything is loaded at once.
+  auto gather_few = [&](const int4& cut, int k) {
+    const int joined = joined_of(cut), parts = 1 + joined + cut.w, from = blockIdx.x * kWarps + k;
+    float lse[kFewParts];
+    float4 x[kFewParts][V];
+#pragma unroll
+    for (int i = 0; i < kFewParts; ++i) {
+      const long long slot = i == 0 ? 2LL * from + 1 : i <= joined ? 2LL * kWarps * (blockIdx.x + i) + 1 : 2LL * cut.z;
+      const long long at = slot * rows_per_unit + r;
+      lse[i] = i < parts ? p.part_lse[at] : -INFINITY;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        x[i][v] = i < parts ? *reinterpret_cast<const float4*>(p.part_o + at * D + v * 128 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    Sum s{lse[0], 0.f, {}};
+#pragma unroll
+    for (int i = 1; i < kFewParts; ++i) s.top = fmaxf(s.top, lse[i]);
+    if (s.top == -INFINITY) return s;
+#pragma unroll
+    for (int i = 0; i < kFewParts; ++i) {
+      const float f = exp2_fast(lse[i] - s.top);
+      s.sum += f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) s.x[v].x += f * x[i][v].x, s.x[v].y += f * x[i][v].y, s.x[v].z += f * x[i][v].z, s.x[v].w += f * x[i][v].w;
+    }
+    return s;
+  };
   const int4 mine = cut_of(warp);
   const bool many = mine.z >= 0 && 1 + joined_of(mine) + mine.w > kFewParts;
-  if (mine.z >= 0 && !many) store(mine, gather(mine, warp, 0, 1));
+  if (mine.z >= 0 && !many) store(mine, gather_few(mine, warp));
   if (!__syncthreads_or(many)) return;
   __shared__ Sum sums[kWarps][32];
   for (int k = 0; k < kWarps; ++k) {
@@ -958,17 +1017,20 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t s) {
   auto kernel = attn_paged_kernel<C>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, C::SMEM, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)std::min(C::ROWS, p.Nq * p.G));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
+  // Both are programmatic dependents: their CTAs are scheduled while the kernel before still runs, and wait for it.
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.dynamicSmemBytes = C::SMEM;
+  if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)std::min(C::ROWS, p.Nq * p.G));
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<C::D>, p, C::ROWS);
 }
 
