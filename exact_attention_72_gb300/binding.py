@@ -563,12 +563,13 @@ def _norm_rope_args(q, k, cos, sin, positions, wq, wk, norm):
     import torch
     shape = q.shape
     T, q_st, q_sh = _rows("q", q)
-    H, d = shape[-2:]
+    H, d = shape[-2], shape[-1]
     Hkv = k_st = k_sh = 0
     if k is not None:
-        if k.shape[:-2] != shape[:-2]:
+        k_shape = k.shape
+        Hkv = k_shape[-2]
+        if len(k_shape) != len(shape) or k_shape[0] != shape[0] or (len(shape) == 4 and k_shape[1] != shape[1]):
             raise ValueError("q and k must hold the same tokens")
-        Hkv = k.shape[-2]
         _, k_st, k_sh = _rows("k", k, Hkv, d)
     elif wk is not None:
         raise ValueError("wk needs k")
@@ -577,17 +578,20 @@ def _norm_rope_args(q, k, cos, sin, positions, wq, wk, norm):
         if positions.dtype != torch.int32 or positions.shape != shape[:-2] or not positions.is_contiguous():
             raise ValueError("positions must be a contiguous int32 CUDA tensor, one per token")
         pos = positions.data_ptr()
-    wp = _weight("wq", wq, d), _weight("wk", wk, d)
     rope = _rope_args(cos, sin)
     _on_current_device(q, k, cos, sin, positions, wq, wk)
-    return (T, H, Hkv, d), (q_st, q_sh, k_st, k_sh, 1 if norm else 0, *wp), rope, pos, shape[1] if len(shape) == 4 else T
+    return (T, H, Hkv, d), (q_st, q_sh, k_st, k_sh, 1 if norm else 0, None if wq is None else _weight("wq", wq, d),
+                            None if wk is None else _weight("wk", wk, d)), rope, pos, shape[1] if len(shape) == 4 else T
 
 
 def _out_rows(name, t, like, stream):
     """An output with the shape of ``like``, contiguous: ``t`` if given."""
     import torch
     if t is None:
-        return _buffer(like.shape, torch.bfloat16, like.device, stream)
+        if stream is None:
+            return torch.empty_like(like, memory_format=torch.contiguous_format)
+        with torch.cuda.stream(stream):
+            return torch.empty_like(like, memory_format=torch.contiguous_format)
     if t.shape != like.shape or t.dtype != torch.bfloat16 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor of shape {tuple(like.shape)}")
     _on_current_device(t)
@@ -642,10 +646,10 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out=None, cos=None, sin=None, positio
     if k is not None:
         dk = _out_rows("dk", dk, k, stream)
     need = attn_qk_norm_rope_bwd_workspace_bytes(*sizes) if wq is not None or wk is not None else 0
-    if (wq is not None and dwq is None) or (wk is not None and dwk is None):
-        own = _buffer((2, d), torch.float32, q.device, stream)
-        dwq = own[0] if wq is not None and dwq is None else dwq
-        dwk = own[1] if wk is not None and dwk is None else dwk
+    if wq is not None and dwq is None:
+        dwq = _buffer((d,), torch.float32, q.device, stream)
+    if wk is not None and dwk is None:
+        dwk = _buffer((d,), torch.float32, q.device, stream)
     if T == 0:
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
             for g in (dwq, dwk):
@@ -804,15 +808,12 @@ def attn_fwd_paged(q, cache: PagedKVCache, page_table, seqlens, causal: bool = T
         scale = 1.0 / math.sqrt(d)
     if workspace is None:
         workspace = _buffer((max(attn_fwd_paged_workspace_bytes(cache, B, H, Nq), 1),), torch.uint8, q.device, stream)
-    if out is None:
-        out = _buffer(q.shape, torch.bfloat16, q.device, stream)
-    elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
-        raise ValueError("out must be a contiguous bfloat16 CUDA tensor like q")
+    out = _out_rows("out", out, q, stream)
     if lse is None:
         lse = _buffer((B, H, Nq), torch.float32, q.device, stream)
     elif lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 CUDA tensor [B, H, Nq]")
-    _on_current_device(cache.k, page_table, seqlens, q, workspace, out, lse)
+    _on_current_device(cache.k, page_table, seqlens, q, workspace, lse)
     st = lib().attn_fwd_paged(q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(), *table[:3], seqlens.data_ptr(), B,
                               H, Nq, scale, 1 if causal else 0, workspace.data_ptr(),
                               workspace.numel() * workspace.element_size(), _stream_handle(stream))
