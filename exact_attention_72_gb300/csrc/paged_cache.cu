@@ -27,8 +27,8 @@
 namespace gb300 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRows = 4;   // heads of one token that a thread has in flight
+constexpr int kThreads = 128;
+constexpr int kRows = 2;   // heads of one token that a thread has in flight, keys and values
 
 struct AppendParams {
   PagedCache c;
@@ -38,7 +38,7 @@ struct AppendParams {
   long long table_stride;
   const float *cos, *sin;
   int B, total, max_pages, half, rope_dim, max_pos;
-  FastDiv parts, page_size;   // tasks of a token
+  FastDiv parts, page_size;   // parts: tasks of a token
   uint32_t* status;
 };
 
@@ -79,6 +79,13 @@ __device__ __forceinline__ float bf16_toward(float x) {
   return __uint_as_float(cut + (away ? 0x10000u : 0u));
 }
 
+// x / y, correctly rounded, from the correctly rounded reciprocal of y (Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor"): the remainder of the first product is exact.
+__device__ __forceinline__ float divide(float x, float y, float inv) {
+  const float q = __fmul_rn(x, inv);
+  return __fmaf_rn(__fmaf_rn(-q, y, x), inv, q);
+}
+
 // 8 of a group's 64 values (8 neighbouring lanes) as codes; sz: its (scale, zero) pair.
 __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t& sz) {
   float lo = x[0], hi = x[0];
@@ -94,20 +101,18 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t& sz)
   }
   const float zero = bf16_toward<false>(lo);
   const float least = fmaxf(fmaxf(fabsf(lo), fabsf(hi)) * 0x1p-20f, 0x1p-100f);
-  const float scale = bf16_toward<true>(fmaxf(__fdiv_rn(__fsub_rn(hi, zero), 15.f), least));
+  const float scale = bf16_toward<true>(fmaxf(divide(__fsub_rn(hi, zero), 15.f, 1.f / 15.f), least));
   sz = (__float_as_uint(scale) >> 16) | (__float_as_uint(zero) & 0xffff0000u);
-  // (x - zero) / scale, correctly rounded, from the correctly rounded reciprocal (Markstein, "Computation
-  // of elementary functions on the IBM RISC System/6000 processor"): the remainder of the first product
-  // is exact. 0 <= quotient <= 15, as scale >= (hi - zero) / 15; adding 2^23 rounds it to a whole number.
+  // 0 <= quotient <= 15, as scale >= (hi - zero) / 15. Adding 2^23 rounds it to a whole number, which then stands in the
+  // low bits; the exponents that the sum of the shifted words carries with it are taken off at the end.
   const float inv = __frcp_rn(scale);
-  uint32_t codes = 0;
+  uint32_t codes = 0, exponents = 0;
 #pragma unroll
   for (int i = 7; i >= 0; --i) {
-    const float y = __fsub_rn(x[i], zero), q = __fmul_rn(y, inv);
-    const float c = __fadd_rn(__fmaf_rn(__fmaf_rn(-q, scale, y), inv, q), 0x1p23f);
-    codes = codes << 4 | (__float_as_uint(c) & 15u);
+    codes = codes * 16 + __float_as_uint(__fadd_rn(divide(__fsub_rn(x[i], zero), scale, inv), 0x1p23f));
+    exponents = exponents * 16 + 0x4b000000u;
   }
-  return codes;
+  return codes - exponents;
 }
 
 // Where position pos of sequence b lies, or false where the table does not lead into the pool.
@@ -127,22 +132,20 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
   constexpr int LPR = D / 8;
   const int l = threadIdx.x % LPR;
   const uint32_t task = blockIdx.x * (uint32_t)(kThreads / LPR) + threadIdx.x / LPR, token = task / p.parts;
-  const int t = min(token, (uint32_t)p.total - 1u), part = task - token * p.parts.v, k_parts = p.parts.v / 2;
+  const int t = min(token, (uint32_t)p.total - 1u), h0 = (task - token * p.parts.v) * kRows, heads = p.c.Hkv;
   bool good = token < (uint32_t)p.total;
-  const bool is_v = part >= k_parts;
-  const int h0 = (is_v ? part - k_parts : part) * kRows, heads = p.c.Hkv;
-  const __nv_bfloat16* x = is_v ? p.v + t * p.v_st : p.k + t * p.k_st;
-  const long long sh = is_v ? p.v_sh : p.k_sh;
-  // This lane's dims 8l .. 8l + 7 and, for keys, where the values they are paired with begin.
-  const bool turned = !is_v && p.cos && 8 * l < p.rope_dim;
+  // This lane's dims 8l .. 8l + 7 and where the values they are paired with begin.
+  const bool turned = p.cos && 8 * l < p.rope_dim;
   const int mate = 8 * l < p.half ? 8 * l + p.half : 8 * l - p.half;
-  uint4 raw[kRows], raw_mate[kRows];
+  uint4 raw[2][kRows], raw_mate[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const __nv_bfloat16* row = x + min(h0 + i, heads - 1) * sh;
-    raw[i] = *reinterpret_cast<const uint4*>(row + 8 * l);
+    const long long h = min(h0 + i, heads - 1);
+    const __nv_bfloat16* row = p.k + t * p.k_st + h * p.k_sh;
+    raw[0][i] = *reinterpret_cast<const uint4*>(row + 8 * l);
     raw_mate[i] = make_uint4(0, 0, 0, 0);
     if (!INTERLEAVED && turned) raw_mate[i] = *reinterpret_cast<const uint4*>(row + mate);
+    raw[1][i] = *reinterpret_cast<const uint4*>(p.v + t * p.v_st + h * p.v_sh + 8 * l);
   }
   const int b = find_sequence<LPR>(p.cu, p.B, t);
   int page = 0, at = 0, pos = 0;
@@ -171,62 +174,75 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
       cs[i] = c.x, cs[i + 1] = c.y, cs[i + 2] = c.z, cs[i + 3] = c.w;
       sn[i] = s.x, sn[i + 1] = s.y, sn[i + 2] = s.z, sn[i + 3] = s.w;
     }
+    if (!INTERLEAVED && 8 * l < p.half) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
+    }
   }
   const PagedCache& c = p.c;
+  const long long row0 = page * c.page_b + at * c.token_b, sz0 = page * c.sz_page_b + at * c.sz_token_b;
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    float y[8];
-    unpack8(y, raw[i]);
-    if (turned) {
-      if (INTERLEAVED) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float u = y[2 * j], v = y[2 * j + 1];
-          y[2 * j] = __fsub_rn(__fmul_rn(u, cs[j]), __fmul_rn(v, sn[j]));
-          y[2 * j + 1] = __fadd_rn(__fmul_rn(v, cs[j]), __fmul_rn(u, sn[j]));
-        }
-      } else {
-        float m[8];
-        unpack8(m, raw_mate[i]);
-        const bool first_half = 8 * l < p.half;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float u = __fmul_rn(y[j], cs[j]), v = __fmul_rn(m[j], sn[j]);
-          y[j] = first_half ? __fsub_rn(u, v) : __fadd_rn(u, v);
-        }
-      }
-    }
     const bool store = good && h0 + i < heads;
-    const long long row = page * c.page_b + at * c.token_b + (h0 + i) * c.head_b;
-    uint8_t* base = is_v ? c.v : c.k;
-    if constexpr (INT4) {
-      uint32_t sz;
-      const uint32_t codes = quantise8(y, sz);
-      if (store) {
-        *reinterpret_cast<uint32_t*>(base + row + 4 * l) = codes;
-        if (l % 8 == 0) {
-          const long long sz_row = page * c.sz_page_b + at * c.sz_token_b + (h0 + i) * c.sz_head_b;
-          *reinterpret_cast<uint32_t*>((is_v ? c.v_sz : c.k_sz) + sz_row + l / 8 * 4) = sz;
+    const long long row = row0 + (h0 + i) * c.head_b;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      float y[8];
+      unpack8(y, raw[v][i]);
+      if (v == 0 && turned) {
+        if (INTERLEAVED) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float u = y[2 * j], w = y[2 * j + 1];
+            y[2 * j] = __fsub_rn(__fmul_rn(u, cs[j]), __fmul_rn(w, sn[j]));
+            y[2 * j + 1] = __fadd_rn(__fmul_rn(w, cs[j]), __fmul_rn(u, sn[j]));
+          }
+        } else {
+          float m[8];
+          unpack8(m, raw_mate[i]);
+          // the first half subtracts; a product with the sine's sign turned has the other sign, bit for bit
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = __fadd_rn(__fmul_rn(y[j], cs[j]), __fmul_rn(m[j], sn[j]));
         }
       }
-    } else if (store) {
-      // values no rotation touches keep their bits
-      *reinterpret_cast<uint4*>(base + row + 16 * l) = turned ? pack8(y) : raw[i];
+      uint8_t* base = v ? c.v : c.k;
+      if constexpr (INT4) {
+        uint32_t sz;
+        const uint32_t codes = quantise8(y, sz);
+        if (store) {
+          *reinterpret_cast<uint32_t*>(base + row + 4 * l) = codes;
+          if (l % 8 == 0) *reinterpret_cast<uint32_t*>((v ? c.v_sz : c.k_sz) + sz0 + (h0 + i) * c.sz_head_b + l / 8 * 4) = sz;
+        }
+      } else if (store) {
+        // values no rotation touches keep their bits
+        *reinterpret_cast<uint4*>(base + row + 16 * l) = v == 0 && turned ? pack8(y) : raw[v][i];
+      }
     }
   }
 }
 
-constexpr int kGatherRows = 4;
+constexpr int kGatherRows = 2;   // heads of one token, keys and values
+
+// The values of 8 codes as bf16. A code in the low bits of bf16 128 is 128 + code; scale * code + zero is rounded once.
+__device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t sz) {
+  const uint32_t scale = __byte_perm(sz, 0, 0x1010), zero = __byte_perm(sz, 0, 0x3232);
+  uint32_t x[4];   // codes (0, 4), (1, 5), (2, 6), (3, 7)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t c = ((codes >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    asm("{\n .reg .b32 c;\n sub.rn.bf16x2 c, %1, %2;\n fma.rn.bf16x2 %0, c, %3, %4;\n}" : "=r"(x[i]) : "r"(c), "r"(0x43004300u), "r"(scale), "r"(zero));
+  }
+  return make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[0], x[1], 0x7632),
+                    __byte_perm(x[2], x[3], 0x7632));
+}
 
 template <int D, bool INT4>
 __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const GatherParams p) {
   constexpr int LPR = D / 8;
   const int l = threadIdx.x % LPR;
   const uint32_t task = blockIdx.x * (uint32_t)(kThreads / LPR) + threadIdx.x / LPR, token = task / p.parts;
-  const int t = min(token, (uint32_t)p.total - 1u), part = task - token * p.parts.v, k_parts = p.parts.v / 2;
+  const int t = min(token, (uint32_t)p.total - 1u), h0 = (task - token * p.parts.v) * kGatherRows, heads = p.c.Hkv;
   const bool mine = token < (uint32_t)p.total;
-  const bool is_v = part >= k_parts;
-  const int h0 = (is_v ? part - k_parts : part) * kGatherRows, heads = p.c.Hkv;
   const int b = find_sequence<LPR>(p.cu, p.B, t);
   if (b >= p.B || !mine) return;   // behind the last sequence: left as it was
   const int first = p.cu[b];
@@ -237,34 +253,39 @@ __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const GatherPara
     return;
   }
   const PagedCache& c = p.c;
-  const uint8_t* base = (is_v ? c.v : c.k) + page * c.page_b + at * c.token_b;
-  __nv_bfloat16* y = (is_v ? p.v : p.k) + ((long long)t * heads + h0) * D + 8 * l;
+  const long long row0 = page * c.page_b + at * c.token_b, out = ((long long)t * heads + h0) * D + 8 * l;
   if constexpr (INT4) {
-    const uint8_t* sz_base = (is_v ? c.v_sz : c.k_sz) + page * c.sz_page_b + at * c.sz_token_b + l / 8 * 4;
-    uint32_t codes[kGatherRows], sz[kGatherRows];
+    const long long sz0 = page * c.sz_page_b + at * c.sz_token_b + l / 8 * 4;
+    uint32_t codes[2][kGatherRows], sz[2][kGatherRows];
 #pragma unroll
     for (int i = 0; i < kGatherRows; ++i) {
       const int h = min(h0 + i, heads - 1);
-      codes[i] = *reinterpret_cast<const uint32_t*>(base + h * c.head_b + 4 * l);
-      sz[i] = *reinterpret_cast<const uint32_t*>(sz_base + h * c.sz_head_b);
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        codes[v][i] = *reinterpret_cast<const uint32_t*>((v ? c.v : c.k) + row0 + h * c.head_b + 4 * l);
+        sz[v][i] = *reinterpret_cast<const uint32_t*>((v ? c.v_sz : c.k_sz) + sz0 + h * c.sz_head_b);
+      }
     }
 #pragma unroll
     for (int i = 0; i < kGatherRows; ++i) {
-      const float scale = __uint_as_float(sz[i] << 16), zero = __uint_as_float(sz[i] & 0xffff0000u);
-      float x[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)   // a code in the low bits of 2^23 is 2^23 + code
-        x[j] = fmaf(scale, __uint_as_float(((codes[i] >> (4 * j)) & 15u) | 0x4b000000u) - 0x1p23f, zero);
-      if (h0 + i < heads) *reinterpret_cast<uint4*>(y + i * D) = pack8(x);
+      if (h0 + i >= heads) break;
+      *reinterpret_cast<uint4*>(p.k + out + i * D) = values8(codes[0][i], sz[0][i]);
+      *reinterpret_cast<uint4*>(p.v + out + i * D) = values8(codes[1][i], sz[1][i]);
     }
   } else {
-    uint4 raw[kGatherRows];
+    uint4 raw[2][kGatherRows];
 #pragma unroll
-    for (int i = 0; i < kGatherRows; ++i)
-      raw[i] = *reinterpret_cast<const uint4*>(base + min(h0 + i, heads - 1) * c.head_b + 16 * l);
+    for (int i = 0; i < kGatherRows; ++i) {
+      const long long row = row0 + min(h0 + i, heads - 1) * c.head_b + 16 * l;
+      raw[0][i] = *reinterpret_cast<const uint4*>(c.k + row);
+      raw[1][i] = *reinterpret_cast<const uint4*>(c.v + row);
+    }
 #pragma unroll
-    for (int i = 0; i < kGatherRows; ++i)
-      if (h0 + i < heads) *reinterpret_cast<uint4*>(y + i * D) = raw[i];
+    for (int i = 0; i < kGatherRows; ++i) {
+      if (h0 + i >= heads) break;
+      *reinterpret_cast<uint4*>(p.k + out + i * D) = raw[0][i];
+      *reinterpret_cast<uint4*>(p.v + out + i * D) = raw[1][i];
+    }
   }
 }
 
@@ -310,7 +331,7 @@ extern "C" attn_status_t attn_paged_append(const attn_paged_cache_t* cache, cons
     if (!is_aligned(cos, 16) || !is_aligned(sin, 16) || max_pos < 1) return ATTN_ERR_INVALID_ARG;
     if (rope_dim < 16 || rope_dim % 16 || rope_dim > cache->d) return ATTN_ERR_INVALID_ARG;
   }
-  p.parts = fast_div(2 * (uint32_t)(((long long)cache->Hkv + kRows - 1) / kRows));
+  p.parts = fast_div((uint32_t)(((long long)cache->Hkv + kRows - 1) / kRows));
   p.page_size = fast_div((uint32_t)cache->page_size);
   if ((long long)total * p.parts.v > INT_MAX) return ATTN_ERR_UNSUPPORTED;   // tasks are counted in 32 bits
   if (total == 0) return ATTN_OK;
@@ -345,7 +366,7 @@ extern "C" attn_status_t attn_paged_gather(const attn_paged_cache_t* cache, void
     return ATTN_ERR_INVALID_ARG;
   const uintptr_t bytes = (uintptr_t)total * cache->Hkv * cache->d * 2, kb = (uintptr_t)k, vb = (uintptr_t)v;
   if (kb < vb + bytes && vb < kb + bytes) return ATTN_ERR_INVALID_ARG;
-  p.parts = fast_div(2 * (uint32_t)(((long long)cache->Hkv + kGatherRows - 1) / kGatherRows));
+  p.parts = fast_div((uint32_t)(((long long)cache->Hkv + kGatherRows - 1) / kGatherRows));
   p.page_size = fast_div((uint32_t)cache->page_size);
   if ((long long)total * p.parts.v > INT_MAX) return ATTN_ERR_UNSUPPORTED;
   if (total == 0) return ATTN_OK;

@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kern
     __syncthreads();
     for (int i = threadIdx.x; i < D; i += kThreads) {
       float s = 0.f;
+#pragma unroll
       for (int r = 0; r < ROWS; ++r) s += sums[r][i];
       p.part[(long long)blockIdx.x * D + i] = s;
     }
@@ -331,6 +332,7 @@ __global__ void __launch_bounds__(1024) dw_kernel(const float* __restrict__ part
   const int first = blockIdx.y ? ctas_q : 0, last = blockIdx.y ? ctas : ctas_q;
   const int i = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
+#pragma unroll 8
   for (int c = first + threadIdx.y; c < last; c += 32) s += part[(long long)c * d + i];
   __shared__ float sums[32][33];
   sums[threadIdx.y][threadIdx.x] = s;
