@@ -6,12 +6,10 @@
 // attn_paged_gather: rows 0 .. n_b - 1 of every sequence into packed bf16 k and v, the layout the
 // ragged-batch forward reads.
 //
-// Both are bound by memory. d / 8 lanes hold a row, 8 neighbouring values (16 bytes) each. A lane
-// reads the 8 values its own are paired with from the same row (a second load of a line already in
-// L1) instead of exchanging them; a group of 64 values is 8 neighbouring lanes, so its least and
-// greatest value take three exchanges. Rotation and quantisation round every step as written here
-// (no contraction into fused multiply-adds): a code must not depend on how the compiler schedules,
-// or a value at a border between two codes would change with it.
+// A lane reads the values that its own are paired with from the same row (a second load of a line already in L1) instead
+// of exchanging them, and a group of 64 values is 4 neighbouring lanes, so its least and greatest value take two
+// exchanges. Rotation and quantisation round every step as written here (no contraction into fused multiply-adds): a
+// code must not depend on how the compiler schedules, or a value at a border between two codes would change with it.
 #include <algorithm>
 #include <climits>
 
@@ -28,7 +26,6 @@ namespace gb300 {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRows = 2;   // heads of one token that a thread has in flight, keys and values
 
 struct AppendParams {
   PagedCache c;
@@ -86,16 +83,16 @@ __device__ __forceinline__ float divide(float x, float y, float inv) {
   return __fmaf_rn(__fmaf_rn(-q, y, x), inv, q);
 }
 
-// 8 of a group's 64 values (8 neighbouring lanes) as codes; sz: its (scale, zero) pair.
-__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t& sz) {
+// 16 of a group's 64 values (4 neighbouring lanes) as codes; sz: its (scale, zero) pair.
+__device__ __forceinline__ uint2 quantise16(const float (&x)[16], uint32_t& sz) {
   float lo = x[0], hi = x[0];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
+  for (int i = 1; i < 16; ++i) {
     lo = fminf(lo, x[i]);
     hi = fmaxf(hi, x[i]);
   }
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) {
+  for (int o = 2; o > 0; o >>= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
@@ -106,13 +103,15 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t& sz)
   // 0 <= quotient <= 15, as scale >= (hi - zero) / 15. Adding 2^23 rounds it to a whole number, which then stands in the
   // low bits; the exponents that the sum of the shifted words carries with it are taken off at the end.
   const float inv = __frcp_rn(scale);
-  uint32_t codes = 0, exponents = 0;
+  uint32_t codes[2] = {0, 0}, exponents = 0;
 #pragma unroll
   for (int i = 7; i >= 0; --i) {
-    codes = codes * 16 + __float_as_uint(__fadd_rn(divide(__fsub_rn(x[i], zero), scale, inv), 0x1p23f));
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      codes[s] = codes[s] * 16 + __float_as_uint(__fadd_rn(divide(__fsub_rn(x[8 * s + i], zero), scale, inv), 0x1p23f));
     exponents = exponents * 16 + 0x4b000000u;
   }
-  return codes - exponents;
+  return make_uint2(codes[0] - exponents, codes[1] - exponents);
 }
 
 // Where position pos of sequence b lies, or false where the table does not lead into the pool.
@@ -127,25 +126,26 @@ __device__ __forceinline__ bool find_row(const PagedCache& c, const FastDiv& pag
   return page >= 0 && page < c.num_pages;
 }
 
+// d / 16 lanes hold a row; a task is one head of one token, key and value.
 template <int D, bool INT4, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendParams p) {
-  constexpr int LPR = D / 8;
+  constexpr int LPR = D / 16;
   const int l = threadIdx.x % LPR;
   const uint32_t task = blockIdx.x * (uint32_t)(kThreads / LPR) + threadIdx.x / LPR, token = task / p.parts;
-  const int t = min(token, (uint32_t)p.total - 1u), h0 = (task - token * p.parts.v) * kRows, heads = p.c.Hkv;
+  const int t = min(token, (uint32_t)p.total - 1u), h = task - token * p.parts.v;
   bool good = token < (uint32_t)p.total;
-  // This lane's dims 8l .. 8l + 7 and where the values they are paired with begin.
-  const bool turned = p.cos && 8 * l < p.rope_dim;
-  const int mate = 8 * l < p.half ? 8 * l + p.half : 8 * l - p.half;
-  uint4 raw[2][kRows], raw_mate[kRows];
+  // This lane's dims in eights, 16l and 16l + 8, and for each where the values begin that they are paired with.
+  const __nv_bfloat16 *k = p.k + t * p.k_st + h * p.k_sh, *v = p.v + t * p.v_st + h * p.v_sh;
+  uint4 raw[2][2], raw_mate[2];
+  bool turned[2];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const long long h = min(h0 + i, heads - 1);
-    const __nv_bfloat16* row = p.k + t * p.k_st + h * p.k_sh;
-    raw[0][i] = *reinterpret_cast<const uint4*>(row + 8 * l);
-    raw_mate[i] = make_uint4(0, 0, 0, 0);
-    if (!INTERLEAVED && turned) raw_mate[i] = *reinterpret_cast<const uint4*>(row + mate);
-    raw[1][i] = *reinterpret_cast<const uint4*>(p.v + t * p.v_st + h * p.v_sh + 8 * l);
+  for (int s = 0; s < 2; ++s) {
+    const int d0 = 16 * l + 8 * s;
+    raw[0][s] = *reinterpret_cast<const uint4*>(k + d0);
+    raw[1][s] = *reinterpret_cast<const uint4*>(v + d0);
+    turned[s] = p.cos && d0 < p.rope_dim;
+    raw_mate[s] = make_uint4(0, 0, 0, 0);
+    if (!INTERLEAVED && turned[s]) raw_mate[s] = *reinterpret_cast<const uint4*>(k + (d0 < p.half ? d0 + p.half : d0 - p.half));
   }
   const int b = find_sequence<LPR>(p.cu, p.B, t);
   int page = 0, at = 0, pos = 0;
@@ -161,61 +161,63 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
     good = good && in;
     if (!in) pos = 0;
   }
-  float cs[8], sn[8];
-  if (turned) {
-    // pair of dim j: j mod half, or j / 2 when interleaved
-    const int pair = INTERLEAVED ? 4 * l : (8 * l < p.half ? 8 * l : 8 * l - p.half);
-    const float* ct = p.cos + (long long)pos * p.half + pair;
-    const float* st = p.sin + (long long)pos * p.half + pair;
+  float y[2][16];   // key, value
 #pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-      if (INTERLEAVED && i) break;
-      const float4 c = *reinterpret_cast<const float4*>(ct + i), s = *reinterpret_cast<const float4*>(st + i);
-      cs[i] = c.x, cs[i + 1] = c.y, cs[i + 2] = c.z, cs[i + 3] = c.w;
-      sn[i] = s.x, sn[i + 1] = s.y, sn[i + 2] = s.z, sn[i + 3] = s.w;
-    }
-    if (!INTERLEAVED && 8 * l < p.half) {
+  for (int s = 0; s < 2; ++s) {
+    float x[8], m[8], cs[8], sn[8];
+    unpack8(x, raw[1][s]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
+    for (int j = 0; j < 8; ++j) y[1][8 * s + j] = x[j];
+    unpack8(x, raw[0][s]);
+    if (turned[s]) {
+      // pair of dim j: j mod half, or j / 2 when interleaved
+      const int d0 = 16 * l + 8 * s, pair = INTERLEAVED ? d0 / 2 : (d0 < p.half ? d0 : d0 - p.half);
+      const float* ct = p.cos + (long long)pos * p.half + pair;
+      const float* st = p.sin + (long long)pos * p.half + pair;
+#pragma unroll
+      for (int i = 0; i < (INTERLEAVED ? 4 : 8); i += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(ct + i), b = *reinterpret_cast<const float4*>(st + i);
+        cs[i] = a.x, cs[i + 1] = a.y, cs[i + 2] = a.z, cs[i + 3] = a.w;
+        sn[i] = b.x, sn[i + 1] = b.y, sn[i + 2] = b.z, sn[i + 3] = b.w;
+      }
+      if (INTERLEAVED) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float u = x[2 * j], w = x[2 * j + 1];
+          x[2 * j] = __fsub_rn(__fmul_rn(u, cs[j]), __fmul_rn(w, sn[j]));
+          x[2 * j + 1] = __fadd_rn(__fmul_rn(w, cs[j]), __fmul_rn(u, sn[j]));
+        }
+      } else {
+        unpack8(m, raw_mate[s]);
+        // the first half subtracts: a product with the sine's sign turned has the other sign, bit for bit
+        const float sign = d0 < p.half ? -1.f : 1.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __fadd_rn(__fmul_rn(x[j], cs[j]), __fmul_rn(m[j], __fmul_rn(sn[j], sign)));
+      }
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[0][8 * s + j] = x[j];
   }
   const PagedCache& c = p.c;
-  const long long row0 = page * c.page_b + at * c.token_b, sz0 = page * c.sz_page_b + at * c.sz_token_b;
+  const long long row = page * c.page_b + at * c.token_b + h * c.head_b;
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const bool store = good && h0 + i < heads;
-    const long long row = row0 + (h0 + i) * c.head_b;
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      float y[8];
-      unpack8(y, raw[v][i]);
-      if (v == 0 && turned) {
-        if (INTERLEAVED) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float u = y[2 * j], w = y[2 * j + 1];
-            y[2 * j] = __fsub_rn(__fmul_rn(u, cs[j]), __fmul_rn(w, sn[j]));
-            y[2 * j + 1] = __fadd_rn(__fmul_rn(w, cs[j]), __fmul_rn(u, sn[j]));
-          }
-        } else {
-          float m[8];
-          unpack8(m, raw_mate[i]);
-          // the first half subtracts; a product with the sine's sign turned has the other sign, bit for bit
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = __fadd_rn(__fmul_rn(y[j], cs[j]), __fmul_rn(m[j], sn[j]));
-        }
+  for (int i = 0; i < 2; ++i) {
+    uint8_t* base = (i ? c.v : c.k) + row;
+    if constexpr (INT4) {
+      uint32_t sz;
+      const uint2 codes = quantise16(y[i], sz);
+      if (good) {
+        *reinterpret_cast<uint2*>(base + 8 * l) = codes;
+        if (l % 4 == 0)
+          *reinterpret_cast<uint32_t*>((i ? c.v_sz : c.k_sz) + page * c.sz_page_b + at * c.sz_token_b + h * c.sz_head_b + l) = sz;
       }
-      uint8_t* base = v ? c.v : c.k;
-      if constexpr (INT4) {
-        uint32_t sz;
-        const uint32_t codes = quantise8(y, sz);
-        if (store) {
-          *reinterpret_cast<uint32_t*>(base + row + 4 * l) = codes;
-          if (l % 8 == 0) *reinterpret_cast<uint32_t*>((v ? c.v_sz : c.k_sz) + sz0 + (h0 + i) * c.sz_head_b + l / 8 * 4) = sz;
-        }
-      } else if (store) {
-        // values no rotation touches keep their bits
-        *reinterpret_cast<uint4*>(base + row + 16 * l) = v == 0 && turned ? pack8(y) : raw[v][i];
+    } else if (good) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {   // values no rotation touches keep their bits
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = y[i][8 * s + j];
+        *reinterpret_cast<uint4*>(base + 32 * l + 16 * s) = i == 0 && turned[s] ? pack8(x) : raw[i][s];
       }
     }
   }
@@ -291,7 +293,7 @@ __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const GatherPara
 
 template <int D, bool INT4>
 cudaError_t launch_append(const AppendParams& p, bool interleaved, cudaStream_t s) {
-  const unsigned rows = kThreads / (D / 8);
+  const unsigned rows = kThreads / (D / 16);
   const unsigned grid = ((unsigned)p.total * p.parts.v + rows - 1) / rows;
   if (interleaved) paged_append_kernel<D, INT4, true><<<grid, kThreads, 0, s>>>(p);
   else paged_append_kernel<D, INT4, false><<<grid, kThreads, 0, s>>>(p);
@@ -331,7 +333,7 @@ extern "C" attn_status_t attn_paged_append(const attn_paged_cache_t* cache, cons
     if (!is_aligned(cos, 16) || !is_aligned(sin, 16) || max_pos < 1) return ATTN_ERR_INVALID_ARG;
     if (rope_dim < 16 || rope_dim % 16 || rope_dim > cache->d) return ATTN_ERR_INVALID_ARG;
   }
-  p.parts = fast_div((uint32_t)(((long long)cache->Hkv + kRows - 1) / kRows));
+  p.parts = fast_div((uint32_t)cache->Hkv);
   p.page_size = fast_div((uint32_t)cache->page_size);
   if ((long long)total * p.parts.v > INT_MAX) return ATTN_ERR_UNSUPPORTED;   // tasks are counted in 32 bits
   if (total == 0) return ATTN_OK;
