@@ -86,7 +86,8 @@ struct Params {
   const int *table, *lens;
   long long table_stride;
   int B, H, G, Nq, max_pages, row_blocks, causal;
-  FastDiv blocks_per_page, div_g;   // 16-key blocks; heads of a group
+  int table_lines;   // of 32 entries, of a sequence; 0 for tables of more than a line a thread, or 1 MB
+  FastDiv blocks_per_page, div_g, div_blocks;   // 16-key blocks; heads of a group; row blocks of a kv head
   float scale_log2;
   // Parts of cut units, by warp w of the grid: 2w the one whose unit ends inside its share, 2w + 1 the one that the share
   // ends in, joined over the warps of the CTA from w on that hold the same unit.
@@ -241,8 +242,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
   constexpr int D = C::D, NT = C::NT, KT = C::KT, KB = KT / 16, GROUPS = C::GROUPS, OV = C::OVERHEAD;
   constexpr bool INT4 = C::INT4;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ int s_scan[kWarps];
-  __shared__ int s_base[kWarps], s_first[kWarps];
+  __shared__ int s_upto[kThreads];        // tiles of this warp's threads' sequences, up to each
   __shared__ Unit s_units[kWarps][4];     // units whose copies have begun, by turn
   __shared__ Cursor s_cursor[kWarps];     // here, not in registers: needed once a unit
   __shared__ int s_id[kWarps], s_open[kWarps];
@@ -255,48 +255,50 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
   int mine = 0;
   const int each = (p.B + kThreads - 1) / kThreads;
   for (int b = tid * each; b < min(p.B, (tid + 1) * each); ++b) mine += (tiles_of<C>(sequence_keys(p, b)) + OV) * per_seq;
+  // The tables are read a little later, by single lanes one entry after the other: small ones go into L2 meanwhile.
+  const int line = blockIdx.x * kThreads + tid;
+  if (line < p.B * p.table_lines) {
+    const int b = line / p.table_lines;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + b * p.table_stride + (line - b * p.table_lines) * 32));
+  }
   int upto = mine;   // of this warp's threads up to me
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += x;
   }
-  if (lane == 31) s_scan[warp] = upto;
+  s_upto[tid] = upto;
+  if (lane == 0) s_id[warp] = -1;
   __syncthreads();
-  int total = 0, base0 = upto - mine;
+  int total = 0, before[kWarps];   // of the warps before each
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) base0 += s_scan[w];
-    total += s_scan[w];
+    before[w] = total;
+    total += s_upto[32 * w + 31];
   }
   const int warps = min((int)gridDim.x * kWarps, total), me = blockIdx.x * kWarps + warp;
   const int part = total / warps, more = total - part * warps;         // the first `more` shares have one tile more
   auto share = [&](int w) { return w * part + min(w, more); };         // where warp w's begins
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int first = share(min((int)blockIdx.x * kWarps + w, warps));
-    if (base0 <= first && first < base0 + mine) {
-      int b = tid * each, base = base0;
-      for (;; ++b) {
-        const int n = (tiles_of<C>(sequence_keys(p, b)) + OV) * per_seq;
-        if (first < base + n) break;
-        base += n;
-      }
-      s_first[w] = b;
-      s_base[w] = base;
-    }
-  }
-  if (lane == 0) {
-    p.cut[me] = make_int4(0, 0, -1, 0);
-    s_id[warp] = -1;
-  }
-  __syncthreads();
+  if (lane == 0) p.cut[me] = make_int4(0, 0, -1, 0);
 
   const uint32_t buf = smem_u32(ring) + warp * C::WARP_BYTES, ring_end = buf + C::WARP_BYTES;
   if (me < warps) {
     // ---- copies: units in turn; of each its query rows (a slot for every 8), then keys and values of every tile
     volatile Cursor& cur = s_cursor[warp];
-    if (lane == 0) cur.at = share(me), cur.last = share(me + 1), cur.seq = s_first[warp], cur.seq_base = s_base[warp];
+    {
+      // The thread above whose sequences hold the share's beginning, and the tiles before them.
+      const int first = share(me);
+      int owner = 0;
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) owner = first >= before[w] ? w : owner;
+      const int base = before[0] + (owner == 0 ? 0 : owner == 1 ? before[1] : owner == 2 ? before[2] : before[3]);
+      const uint32_t behind = __ballot_sync(0xffffffffu, base + s_upto[32 * owner + lane] <= first);
+      const int j = __popc(behind);   // lanes whose sequences all end before
+      if (lane == 0) {
+        cur.at = first, cur.last = share(me + 1), cur.seq = (32 * owner + j) * each;
+        cur.seq_base = base + (j > 0 ? s_upto[32 * owner + j - 1] : 0);
+      }
+    }
     __syncwarp();
     int f_turn = 0;              // units entered
     int f_q = NT, f_tile = 0, f_end = 0, f_keys = 0, f_rel = 0;   // query slots done; tile; its unit's last, keys; in a batch
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
       }
       if (p.lens[seq] != keys && lane == 0) atomicCAS(p.status, 0u, kStatusBadPage);
       const int unit = (at - seq_base) / (nt + OV), base = seq_base + unit * (nt + OV) + OV;   // its first tile
-      const int t0 = max(at - base, 0), t1 = min(nt, last - base), hkv = unit / p.row_blocks;
+      const int t0 = max(at - base, 0), t1 = min(nt, last - base), hkv = (uint32_t)unit / p.div_blocks;
       __syncwarp();
       if (lane == 0) {
         cur.at = base + nt, cur.seq = seq, cur.seq_base = seq_base, cur.b = seq, cur.hkv = hkv;
@@ -520,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
         leave();
       }
       const volatile Unit& unit = s_units[warp][turn & 3];
-      const int keys = unit.keys, t1 = unit.t1, row0 = unit.unit % p.row_blocks * C::ROWS, rows = p.Nq * p.G;
+      const int keys = unit.keys, t1 = unit.t1, row0 = (unit.unit - (uint32_t)unit.unit / p.div_blocks * p.row_blocks) * C::ROWS, rows = p.Nq * p.G;
       int limit[NT][2], least = INT_MAX;   // the column's row sees keys < limit
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -772,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
               }
               if (g == 0) p.part_lse[2 * me * C::ROWS + c] = lse2;
             } else if (row < rows) {
-              const int qi = (uint32_t)row / p.div_g, h = unit.unit / p.row_blocks * p.G + row - qi * p.G;
+              const int qi = (uint32_t)row / p.div_g, h = (uint32_t)unit.unit / p.div_blocks * p.G + row - qi * p.G;
               __nv_bfloat16* to = p.o + (((long long)unit.b * p.Nq + qi) * p.H + h) * D;
               if constexpr (INT4) {
 #pragma unroll
@@ -829,10 +831,11 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
     while (w1 < kWarps && s_id[w1] == s_id[w0]) ++w1;
     if (s_id[w0] >= 0) {
       const Unit unit = s_units[w0][0];
-      const int first = blockIdx.x * kWarps + w0, row0 = unit.unit % p.row_blocks * C::ROWS, rows = p.Nq * p.G;
+      const int first = blockIdx.x * kWarps + w0, row0 = (unit.unit - (uint32_t)unit.unit / p.div_blocks * p.row_blocks) * C::ROWS, rows = p.Nq * p.G;
       const bool head = s_open[w0] & 1, whole = head && (s_open[w1 - 1] & 2);
-      for (int i = tid; i < C::ROWS * (D / 4); i += kThreads) {
-        const int r = i / (D / 4), c = i % (D / 4) * 4, row = row0 + r;
+#pragma unroll
+      for (int n = 0; n < C::ROWS * (D / 4) / kThreads; ++n) {
+        const int i = n * kThreads + tid, r = i / (D / 4), c = i % (D / 4) * 4, row = row0 + r;
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, w >= w0 && w < w1 ? s_m[w][r] : -INFINITY);
@@ -853,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
           *reinterpret_cast<float4*>(p.part_o + to * D + c) = x;
           if (c == 0) p.part_lse[to] = lse2;
         } else if (row < rows) {
-          const int qi = (uint32_t)row / p.div_g, h = unit.unit / p.row_blocks * p.G + row - qi * p.G;
+          const int qi = (uint32_t)row / p.div_g, h = (uint32_t)unit.unit / p.div_blocks * p.G + row - qi * p.G;
           *reinterpret_cast<uint2*>(p.o + (((long long)unit.b * p.Nq + qi) * p.H + h) * D + c) =
               make_uint2(pack_bf162(x.x, x.y), pack_bf162(x.z, x.w));
           if (c == 0) p.lse[((long long)unit.b * p.H + h) * p.Nq + qi] = lse2 * 0.69314718055994531f;
@@ -1112,7 +1115,7 @@ extern "C" attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t*
   p.causal = causal != 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.blocks_per_page = fast_div((uint32_t)cache->page_size / 16);
-  p.div_g = fast_div((uint32_t)p.G);
+  p.div_g = fast_div((uint32_t)p.G), p.div_blocks = fast_div((uint32_t)pl.row_blocks);
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + n[0]);
   p.cut = reinterpret_cast<::int4*>(static_cast<uint8_t*>(workspace) + n[0] + n[1]);
@@ -1121,6 +1124,8 @@ extern "C" attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t*
                          (std::max<long long>(1, ((long long)max_pages * cache->page_size + pl.tile - 1) / pl.tile) + pl.overhead);
   if (most > INT_MAX) return ATTN_ERR_UNSUPPORTED;
   const int grid = (int)std::min<long long>(pl.grid, (most + kWarps - 1) / kWarps);
+  const long long lines = (max_pages + 31LL) / 32;
+  p.table_lines = lines * B <= std::min(8192, grid * kThreads) ? (int)lines : 0;
   cudaError_t e;
   switch (d) {
     case 64: e = bits4 ? launch_rows<64, true>(p, pl.rows_per_unit, grid, stream) : launch_rows<64, false>(p, pl.rows_per_unit, grid, stream); break;
