@@ -1,33 +1,42 @@
-// Attention over a paged key/value cache in bf16 or 4 bits, for few query rows a sequence (decode,
-// drafted tokens):  S = scale q k^T over the keys a row sees,  O = softmax(S) V,  LSE.
+// Attention over a paged key/value cache in bf16 or 4 bits, for few query rows a sequence (decode, drafted tokens):
+//   S = scale q k^T over the keys a row sees,  O = softmax(S) V,  LSE.
 //
-// The cache is read once and that bounds the call: 2 d / 2 + d / 4 bytes a key and kv head in 4 bits.
-// All query rows that share a kv head (Nq tokens x H / Hkv heads) are columns of one narrow product,
+// The cache is read once and that bounds the call: 4 d bytes a key and kv head in bf16, d + d / 8 in 4 bits. All query
+// rows that share a kv head (Nq tokens x H / Hkv heads) are columns of one narrow product,
 //   S^T [keys x rows] = K [keys x d] q^T,     O^T [d x rows] = V^T [d x keys] P^T,
-// with m16n8k16: the long dims (keys, d) fill the 16 and a call pads its rows only to 8. tcgen05 would
-// pad them to 128 and needs unpacked operands in shared memory, more traffic than the cache itself.
+// with m16n8k16: the long dims (keys, d) fill the 16 and a call pads its rows only to 8. tcgen05 would pad them to 128
+// and needs unpacked operands in shared memory, more traffic than the cache itself.
 //
-// 4-bit codes go to the tensor cores as they are. A code c in the low bits of a half is the
-// subnormal fp16 number c 2^-24, and 4 bits higher it is 16 c 2^-24: a pair of operands costs one AND.
-// For keys the factor 16 is taken out of the query's matching values; for values a pair of rows sums
-// low codes and whole bytes, low + 16 high, whose difference is taken once at the end. Scale and zero stay outside the products, in fp32:
+// 4-bit codes go to the tensor cores as they are. A code c in the low bits of a half is the subnormal fp16 number
+// c 2^-24, and 4 bits higher it is 16 c 2^-24: a pair of operands costs one AND. For keys the factor 16 is taken out of
+// the query's matching values; for values a pair of rows sums low codes and whole bytes, low + 16 high, whose difference
+// is taken once at the end. Scale and zero stay outside the products, in fp32:
 //   q.k = sum over groups  scale (codes . q) + zero sum(q),
 //   O   = (sum_j (p_j scale_j) codes_j + sum_j p_j zero_j) / sum_j p_j.
-// q is scaled by a power of two per row, so fp16 holds it exactly where it counts (2^-25 of the row's
-// greatest value); p_j scale_j is rounded to fp16, 2^-11 of itself. bf16 caches take p_j as a sum of two
-// bf16 numbers, 2^-16 off: in one, 2^-8 off, the weights would add as much to O's error as its own rounding
-// (0.0023 instead of 0.0017 of its norm), and the second product costs nothing beside the cache's bytes. For p_j scale_j to stay within fp16 at any scale, the running
-// maximum is taken over S + log2 of the key's scale (its exponent) instead of S.
+// Roundings: q is scaled by a power of two per row, so fp16 holds it exactly where it counts (2^-25 of the row's greatest
+// value); p_j scale_j is rounded to fp16, 2^-11 of itself. bf16 caches take p_j as a sum of two bf16 numbers, 2^-16 off:
+// in one, 2^-8 off, the weights would add as much to O's error as its own rounding (0.0023 instead of 0.0017 of its
+// norm), and the second product costs nothing beside the cache's bytes. For p_j scale_j to stay within fp16 at any scale,
+// the running maximum is taken over S + log2 of the key's scale (its exponent) instead of S.
 //
-// Work: a sequence's keys are cut into tiles of KT; a unit is the tiles of one (sequence, kv head, block of query rows). All
-// units in order, each OVERHEAD tiles longer than it is, are dealt to all warps in equal contiguous shares, so ragged
-// batches load every SM alike. A warp streams through its share alone: query rows, keys and values go through a ring of its
-// own in shared memory, filled by 16-byte asynchronous copies that run ahead across the ends of units. A unit inside one
-// share is finished by its warp. One that is cut leaves normalised parts with their LSE: what the warps of a CTA hold of
-// one unit when their shares end is joined there, the rest by a second, dependent launch. The shares follow from the
+// Work: a sequence's keys are cut into tiles of KT; a unit is the tiles of one (sequence, kv head, block of query rows).
+// All units in order, each OVERHEAD tiles longer than it is, are dealt to all warps in equal contiguous shares, so ragged
+// batches load every SM alike. A warp streams through its share alone: query rows, keys and values go through a ring of
+// its own in shared memory, filled by 16-byte asynchronous copies that run ahead across the ends of units. A unit inside
+// one share is finished by its warp. One that is cut leaves normalised parts with their LSE: what the warps of a CTA hold
+// of one unit when their shares end is joined there, the rest by a second, dependent launch. The shares follow from the
 // lengths alone: the same bits on every run, no atomics.
 //
 // Matrix loads hand out the operands, those of V transposed: a 16-bit unit of them is one bf16 value or four codes.
+//
+// Measured on a GB300 (us in a CUDA graph, share of the copy bandwidth; H 32, Hkv 8, d 128 if not said otherwise):
+//   bf16, B 8, 16384 keys                85    93%
+//   4 bits, B 8, 16384 keys              36    62%: about 5 us until the first tiles are there and 5 us to join the parts;
+//                                              between them the tiles stream at 99%
+//   4 bits, B 32, up to 32768 keys      102    82%
+//   bf16, d 256, B 13, up to 5000 keys, 12 rows (two blocks, the second out of L2)  34    52%
+// What it took, at B 8 and 16384 keys in 4 bits: tiles of one CTA with lane-wise operand loads 61; pages looked up once a
+// tile 48.6; matrix loads, shares by warp, a vote instead of the maximum's exchanges 40; one wave of shorter launches 36.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -53,6 +62,7 @@ constexpr int kThreads = 32 * kWarps;
 // times zero (at most 2^20 scales) far from overflow.
 constexpr float kLeastScale = 0x1p-70f;
 
+constexpr long long kMaxKeys = INT_MAX - 1023;   // keys a page table may hold: they are counted in 32 bits
 constexpr float kNone = -1e30f;     // running maximum before the first key
 constexpr float kHeadroom = 0x1p14f;   // weights times scale may grow to this before the maximum is moved
 
@@ -107,11 +117,13 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
 }
 template <int OFF>
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0+%3], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0), "n"(OFF) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0+%3], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0), "n"(OFF)
+               : "memory");
 }
 template <int OFF, int N>
 __device__ __forceinline__ void copy_small(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0+%4], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(in ? N : 0), "n"(OFF) : "memory");
+  asm volatile("cp.async.ca.shared.global [%0+%4], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(in ? N : 0), "n"(OFF)
+               : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -207,6 +219,10 @@ __device__ __forceinline__ uint32_t pack_bf162(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ void add(float4& x, float f, const float4& y) {
+  x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
+}
+
 // Byte offset of 16-byte chunk c of row r in a tile of rows of ROWB bytes: one chunk of 8 neighbouring rows, what a
 // matrix load takes, meets every bank once.
 template <int ROWB>
@@ -219,13 +235,17 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
 // Keys that some row of sequence b sees at most, and its pieces of work (at least one: a unit without
 // keys still writes its zeros).
 __device__ __forceinline__ int sequence_keys(const Params& p, int b) {
-  const long long cap = min((long long)p.max_pages * p.c.page_size, (long long)INT_MAX);
   const int n = p.lens[b];
-  return n < 0 ? 0 : (int)min((long long)n, cap);
+  return min(max(n, 0), p.max_pages * p.c.page_size);   // a call with more than kMaxKeys is refused
+}
+
+// Which block of query rows the unit of a sequence has.
+__device__ __forceinline__ int row_block(const Params& p, uint32_t unit) {
+  return unit - unit / p.div_blocks * p.row_blocks;
 }
 
 template <class C>
-__device__ __forceinline__ int tiles_of(int keys) { return max(1, (keys + C::KT - 1) / C::KT); }
+__device__ __forceinline__ int tiles_of(int keys) { return (keys - 1) / C::KT + 1; }   // at least 1
 
 // Where a warp is in its share: the next tile to plan for, its sequence, what that begins with; of the unit that is being
 // copied the sequence, the first query row of its heads and of its block.
@@ -313,7 +333,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
 
     auto look_up = [&](int first) -> int {   // pages of a batch of tiles, read one batch ahead
       const int tile = first + lane / KB, key = tile * KT + lane % KB * 16;
-      return tile < f_end && key < f_keys ? p.table[cur.b * p.table_stride + (uint32_t)(key >> 4) / p.blocks_per_page] : -1;
+      if (tile >= f_end || key >= f_keys) return -1;
+      return p.table[cur.b * p.table_stride + (uint32_t)(key >> 4) / p.blocks_per_page];
     };
     auto next_batch = [&]() {
       const int tile = f_tile + lane / KB, key = tile * KT + lane % KB * 16;
@@ -337,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
       const int at = cur.at, last = cur.last;
       if (at >= last) return;
       int seq = cur.seq, seq_base = cur.seq_base, keys = sequence_keys(p, seq), nt = tiles_of<C>(keys);
-      while (at >= seq_base + (nt + OV) * per_seq) {
+      while (seq + 1 < p.B && at >= seq_base + (nt + OV) * per_seq) {
         seq_base += (nt + OV) * per_seq;
         ++seq;
         keys = sequence_keys(p, seq);
@@ -389,7 +410,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
           auto copy_rows = [&](auto copy) {
             each_of<KT / RPI>([&](auto index) {
               constexpr int I = decltype(index)::value, R = I * RPI, FIRST = R % 8;
-              const uint32_t to = FIRST == 0 ? dst : fill + (chunk_at<C::ROWB>(FIRST + lane / CH, lane % CH) - FIRST * C::ROWB);
+              uint32_t to = dst;
+              if constexpr (FIRST != 0) to = fill + chunk_at<C::ROWB>(FIRST + lane / CH, lane % CH) - FIRST * C::ROWB;
               copy(std::integral_constant<int, R>{}, std::integral_constant<int, R * C::ROWB>{}, to);
             });
           };
@@ -523,7 +545,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
         leave();
       }
       const volatile Unit& unit = s_units[warp][turn & 3];
-      const int keys = unit.keys, t1 = unit.t1, row0 = (unit.unit - (uint32_t)unit.unit / p.div_blocks * p.row_blocks) * C::ROWS, rows = p.Nq * p.G;
+      const int keys = unit.keys, t1 = unit.t1, rows = p.Nq * p.G;
+      const int row0 = row_block(p, unit.unit) * C::ROWS;
       int limit[NT][2], least = INT_MAX;   // the column's row sees keys < limit
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -770,8 +793,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int c = nt * 8 + 2 * t + j, row = row0 + c;
-            const float inv = l[nt][j] > 0.f ? 1.f / l[nt][j] : 0.f;
-            const float lse2 = l[nt][j] > 0.f ? m[nt][j] + log2f(l[nt][j]) : -INFINITY;
+            const float inv = l[nt][j] != 0.f ? 1.f / l[nt][j] : 0.f;
+            const float lse2 = l[nt][j] != 0.f ? m[nt][j] + log2f(l[nt][j]) : -INFINITY;
             if (!whole) {
               float* to = p.part_o + ((long long)(2 * me) * C::ROWS + c) * D;
 #pragma unroll
@@ -788,7 +811,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
 #pragma unroll
                 for (int i = 0; i < D / 16; i += 2) {
                   const float2 x = value(nt, i, j), y = value(nt, i + 1, j);
-                  *reinterpret_cast<uint2*>(to + dim(i)) = make_uint2(pack_bf162(x.x * inv, x.y * inv), pack_bf162(y.x * inv, y.y * inv));
+                  *reinterpret_cast<uint2*>(to + dim(i)) =
+                      make_uint2(pack_bf162(x.x * inv, x.y * inv), pack_bf162(y.x * inv, y.y * inv));
                 }
               } else {
 #pragma unroll
@@ -839,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
     while (w1 < kWarps && s_id[w1] == s_id[w0]) ++w1;
     if (s_id[w0] >= 0) {
       const Unit unit = s_units[w0][0];
-      const int first = blockIdx.x * kWarps + w0, row0 = (unit.unit - (uint32_t)unit.unit / p.div_blocks * p.row_blocks) * C::ROWS, rows = p.Nq * p.G;
+      const int first = blockIdx.x * kWarps + w0, rows = p.Nq * p.G, row0 = row_block(p, unit.unit) * C::ROWS;
       const bool head = s_open[w0] & 1, whole = head && (s_open[w1 - 1] & 2);
 #pragma unroll
       for (int n = 0; n < C::ROWS * (D / 4) / kThreads; ++n) {
@@ -852,13 +876,13 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
         for (int w = 0; w < kWarps; ++w) {
           if (w < w0 || w >= w1) continue;
           const float f = exp2_fast(s_m[w][r] - top);
-          const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(ring + w * C::WARP_BYTES) + r * D + c);
+          const float4 y = *reinterpret_cast<const float4*>(ring + w * C::WARP_BYTES + (r * D + c) * 4);
           sum += s_l[w][r] * f;
-          x.x += y.x * f, x.y += y.y * f, x.z += y.z * f, x.w += y.w * f;
+          add(x, f, y);
         }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;
         x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
-        const float lse2 = sum > 0.f ? top + log2f(sum) : -INFINITY;
+        const float lse2 = sum != 0.f ? top + log2f(sum) : -INFINITY;
         if (!whole) {
           const long long to = (long long)(2 * first + 1) * C::ROWS + r;
           *reinterpret_cast<float4*>(p.part_o + to * D + c) = x;
@@ -898,7 +922,9 @@ __global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params 
   };
   // Parts of a unit that begins in warp k: slot 2 first + 1, one of each later CTA's first warp, and of the last warp its
   // slot for a unit that ends inside a share (then the last CTA's first warp has one only if it is not that warp).
-  auto joined_of = [&](const int4& cut) { return max(cut.z / kWarps - (int)blockIdx.x - (cut.w && cut.z % kWarps == 0 ? 1 : 0), 0); };
+  auto joined_of = [&](const int4& cut) {
+    return max(cut.z / kWarps - (int)blockIdx.x - (cut.w && cut.z % kWarps == 0 ? 1 : 0), 0);
+  };
   // Parts first, first + stride, .. of a unit: their weighted sums for this lane, and the weights'.
   struct Sum {
     float top, sum;
@@ -911,18 +937,22 @@ __global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params 
       return slot * rows_per_unit + r;
     };
     Sum s{-INFINITY, 0.f, {}};
-    for (int i = lane; i < parts; i += 32) s.top = fmaxf(s.top, p.part_lse[at(i)]);
+    bool any = false;   // a part that has keys, or is NaN
+    for (int i = lane; i < parts; i += 32) {
+      const float lse = p.part_lse[at(i)];
+      s.top = fmaxf(s.top, lse);
+      any = any || !(lse == -INFINITY);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s.top = fmaxf(s.top, __shfl_xor_sync(0xffffffffu, s.top, o));
-    if (s.top == -INFINITY) return s;
+    if (!__any_sync(0xffffffffu, any)) return s;
 #pragma unroll 4
     for (int i = first * WAYS + way; i < parts; i += stride * WAYS) {
       const float f = exp2_fast(p.part_lse[at(i)] - s.top);
       s.sum += f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float4 y = *reinterpret_cast<const float4*>(p.part_o + at(i) * D + v * 128 + c);
-        s.x[v].x += f * y.x, s.x[v].y += f * y.y, s.x[v].z += f * y.z, s.x[v].w += f * y.w;
+        add(s.x[v], f, *reinterpret_cast<const float4*>(p.part_o + at(i) * D + v * 128 + c));
       }
     }
     if constexpr (WAYS > 1) {
@@ -940,7 +970,7 @@ __global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params 
   auto store = [&](const int4& cut, const Sum& s) {
     const int hkv = cut.y / p.row_blocks, row = (cut.y - hkv * p.row_blocks) * rows_per_unit + r;
     const int qi = (uint32_t)row / p.div_g, h = hkv * p.G + row - qi * p.G;
-    const float inv = s.sum > 0.f ? 1.f / s.sum : 0.f;
+    const float inv = s.sum != 0.f ? 1.f / s.sum : 0.f;
     if (way == 0) {
 #pragma unroll
       for (int v = 0; v < V; ++v)
@@ -948,7 +978,7 @@ __global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params 
             make_uint2(pack_bf162(s.x[v].x * inv, s.x[v].y * inv), pack_bf162(s.x[v].z * inv, s.x[v].w * inv));
     }
     if (lane == 0)
-      p.lse[((long long)cut.x * p.H + h) * p.Nq + qi] = s.sum > 0.f ? (s.top + log2f(s.sum)) * 0.69314718055994531f : -INFINITY;
+      p.lse[((long long)cut.x * p.H + h) * p.Nq + qi] = s.sum != 0.f ? (s.top + log2f(s.sum)) * 0.69314718055994531f : -INFINITY;
   };
   // A few parts: everything is loaded at once.
   auto gather_few = [&](const int4& cut, int k) {
@@ -962,18 +992,22 @@ __global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params 
       lse[i] = i < parts ? p.part_lse[at] : -INFINITY;
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        x[i][v] = i < parts ? *reinterpret_cast<const float4*>(p.part_o + at * D + v * 128 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[i][v] = i < parts ? *reinterpret_cast<const float4*>(p.part_o + at * D + v * 128 + c) : float4{};
     }
-    Sum s{lse[0], 0.f, {}};
-#pragma unroll
-    for (int i = 1; i < kFewParts; ++i) s.top = fmaxf(s.top, lse[i]);
-    if (s.top == -INFINITY) return s;
+    Sum s{-INFINITY, 0.f, {}};
+    bool any = false;
 #pragma unroll
     for (int i = 0; i < kFewParts; ++i) {
-      const float f = exp2_fast(lse[i] - s.top);
+      s.top = fmaxf(s.top, lse[i]);
+      any = any || !(lse[i] == -INFINITY);
+    }
+    if (!any) return s;
+#pragma unroll
+    for (int i = 0; i < kFewParts; ++i) {
+      const float f = i < parts ? exp2_fast(lse[i] - s.top) : 0.f;
       s.sum += f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) s.x[v].x += f * x[i][v].x, s.x[v].y += f * x[i][v].y, s.x[v].z += f * x[i][v].z, s.x[v].w += f * x[i][v].w;
+      for (int v = 0; v < V; ++v) add(s.x[v], f, x[i][v]);
     }
     return s;
   };
@@ -993,7 +1027,7 @@ __global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params 
         const Sum& y = sums[w][lane];
         s.sum += y.sum;
 #pragma unroll
-        for (int v = 0; v < V; ++v) s.x[v].x += y.x[v].x, s.x[v].y += y.x[v].y, s.x[v].z += y.x[v].z, s.x[v].w += y.x[v].w;
+        for (int v = 0; v < V; ++v) add(s.x[v], 1.f, y.x[v]);
       }
       store(cut, s);
     }
@@ -1053,6 +1087,11 @@ cudaError_t launch_rows(const Params& p, int rows_per_unit, int grid, cudaStream
   return launch<Cfg<D, INT4, 1>>(p, grid, s);
 }
 
+template <int D>
+cudaError_t launch_dim(const Params& p, bool bits4, int rows_per_unit, int grid, cudaStream_t s) {
+  return bits4 ? launch_rows<D, true>(p, rows_per_unit, grid, s) : launch_rows<D, false>(p, rows_per_unit, grid, s);
+}
+
 size_t pad(size_t x) { return (x + 255) / 256 * 256; }
 
 // Bytes of the parts, of their LSE, and of the cut units.
@@ -1097,7 +1136,8 @@ extern "C" attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t*
     return ATTN_ERR_INVALID_ARG;
   if (scale == 0.f) return ATTN_ERR_UNSUPPORTED;   // as attn_fwd
   const long long rows = (long long)Nq * (H / Hkv);
-  if (rows > INT_MAX / 2 || (long long)B * H * Nq > INT_MAX) return ATTN_ERR_UNSUPPORTED;
+  if (rows > INT_MAX / 2 || (long long)B * H * Nq > INT_MAX || (long long)max_pages * cache->page_size > kMaxKeys)
+    return ATTN_ERR_UNSUPPORTED;
   int sms;
   if (!device_state(&sms, &p.status)) return ATTN_ERR_CUDA;
   const bool bits4 = cache->type == ATTN_CACHE_INT4;
@@ -1109,7 +1149,10 @@ extern "C" attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t*
   struct {
     const void* b;
     size_t n;
-  } x[4] = {{o, (size_t)B * Nq * H * d * 2}, {lse, (size_t)B * Nq * H * 4}, {workspace, n[0] + n[1] + n[2]}, {q, (size_t)B * Nq * H * d * 2}};
+  } x[4] = {{o, (size_t)B * Nq * H * d * 2},
+            {lse, (size_t)B * Nq * H * 4},
+            {workspace, n[0] + n[1] + n[2]},
+            {q, (size_t)B * Nq * H * d * 2}};
   for (int i = 0; i < 3; ++i)
     for (int j = i + 1; j < 4; ++j) {
       const uintptr_t a = (uintptr_t)x[i].b, b = (uintptr_t)x[j].b;
@@ -1129,16 +1172,13 @@ extern "C" attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t*
   p.cut = reinterpret_cast<::int4*>(static_cast<uint8_t*>(workspace) + n[0] + n[1]);
   // No more warps than tiles there can be; tiles are counted in 32 bits.
   const long long most = (long long)B * Hkv * pl.row_blocks *
-                         (std::max<long long>(1, ((long long)max_pages * cache->page_size + pl.tile - 1) / pl.tile) + pl.overhead);
+                         (((long long)max_pages * cache->page_size - 1) / pl.tile + 1 + pl.overhead);
   if (most > INT_MAX) return ATTN_ERR_UNSUPPORTED;
   const int grid = (int)std::min<long long>(pl.grid, (most + kWarps - 1) / kWarps);
   const long long lines = (max_pages + 31LL) / 32;
   p.table_lines = lines * B <= std::min(8192, grid * kThreads) ? (int)lines : 0;
-  cudaError_t e;
-  switch (d) {
-    case 64: e = bits4 ? launch_rows<64, true>(p, pl.rows_per_unit, grid, stream) : launch_rows<64, false>(p, pl.rows_per_unit, grid, stream); break;
-    case 128: e = bits4 ? launch_rows<128, true>(p, pl.rows_per_unit, grid, stream) : launch_rows<128, false>(p, pl.rows_per_unit, grid, stream); break;
-    default: e = bits4 ? launch_rows<256, true>(p, pl.rows_per_unit, grid, stream) : launch_rows<256, false>(p, pl.rows_per_unit, grid, stream); break;
-  }
+  const cudaError_t e = d == 64    ? launch_dim<64>(p, bits4, pl.rows_per_unit, grid, stream)
+                        : d == 128 ? launch_dim<128>(p, bits4, pl.rows_per_unit, grid, stream)
+                                   : launch_dim<256>(p, bits4, pl.rows_per_unit, grid, stream);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
     raw[1][s] = *reinterpret_cast<const uint4*>(v + d0);
     turned[s] = p.cos && d0 < p.rope_dim;
     raw_mate[s] = make_uint4(0, 0, 0, 0);
-    if (!INTERLEAVED && turned[s]) raw_mate[s] = *reinterpret_cast<const uint4*>(k + (d0 < p.half ? d0 + p.half : d0 - p.half));
+    if (!INTERLEAVED && turned[s])
+      raw_mate[s] = *reinterpret_cast<const uint4*>(k + (d0 < p.half ? d0 + p.half : d0 - p.half));
   }
   const int b = find_sequence<LPR>(p.cu, p.B, t);
   int page = 0, at = 0, pos = 0;
@@ -208,8 +209,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
       const uint2 codes = quantise16(y[i], sz);
       if (good) {
         *reinterpret_cast<uint2*>(base + 8 * l) = codes;
-        if (l % 4 == 0)
-          *reinterpret_cast<uint32_t*>((i ? c.v_sz : c.k_sz) + page * c.sz_page_b + at * c.sz_token_b + h * c.sz_head_b + l) = sz;
+        const long long sz_row = page * c.sz_page_b + at * c.sz_token_b + h * c.sz_head_b;
+        if (l % 4 == 0) *reinterpret_cast<uint32_t*>((i ? c.v_sz : c.k_sz) + sz_row + l) = sz;
       }
     } else if (good) {
 #pragma unroll
@@ -232,7 +233,9 @@ __device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t sz) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t c = ((codes >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    asm("{\n .reg .b32 c;\n sub.rn.bf16x2 c, %1, %2;\n fma.rn.bf16x2 %0, c, %3, %4;\n}" : "=r"(x[i]) : "r"(c), "r"(0x43004300u), "r"(scale), "r"(zero));
+    asm("{\n .reg .b32 c;\n sub.rn.bf16x2 c, %1, %2;\n fma.rn.bf16x2 %0, c, %3, %4;\n}"
+        : "=r"(x[i])
+        : "r"(c), "r"(0x43004300u), "r"(scale), "r"(zero));
   }
   return make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[0], x[1], 0x7632),
                     __byte_perm(x[2], x[3], 0x7632));
@@ -335,7 +338,7 @@ extern "C" attn_status_t attn_paged_append(const attn_paged_cache_t* cache, cons
   }
   p.parts = fast_div((uint32_t)cache->Hkv);
   p.page_size = fast_div((uint32_t)cache->page_size);
-  if ((long long)total * p.parts.v > INT_MAX) return ATTN_ERR_UNSUPPORTED;   // tasks are counted in 32 bits
+  if ((long long)total * p.parts.v > INT_MAX - kThreads) return ATTN_ERR_UNSUPPORTED;   // tasks are counted in 31 bits
   if (total == 0) return ATTN_OK;
   int sms;
   if (!device_state(&sms, &p.status)) return ATTN_ERR_CUDA;
@@ -370,7 +373,7 @@ extern "C" attn_status_t attn_paged_gather(const attn_paged_cache_t* cache, void
   if (kb < vb + bytes && vb < kb + bytes) return ATTN_ERR_INVALID_ARG;
   p.parts = fast_div((uint32_t)(((long long)cache->Hkv + kGatherRows - 1) / kGatherRows));
   p.page_size = fast_div((uint32_t)cache->page_size);
-  if ((long long)total * p.parts.v > INT_MAX) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)total * p.parts.v > INT_MAX - kThreads) return ATTN_ERR_UNSUPPORTED;
   if (total == 0) return ATTN_OK;
   int sms;
   if (!device_state(&sms, &p.status)) return ATTN_ERR_CUDA;

@@ -508,7 +508,9 @@ extern "C" attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, con
   // Outputs: dq and dk may be the gradients they are made from, and nothing else.
   Range outs[5], ins[4];
   int no = 0, ni = 0;
-  auto bytes = [](const void* p, size_t n) { return Range{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + n}; };
+  auto bytes = [](const void* p, size_t n) {
+    return Range{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + n};
+  };
   const Range oq = rows_range(dq, T, H, (long long)H * d, d, d);
   outs[no++] = oq;
   if (Hkv > 0) outs[no++] = rows_range(dk, T, Hkv, (long long)Hkv * d, d, d);

@@ -167,3 +167,9 @@ def test_binding_refuses_before_the_library():
         binding.attn_qk_norm_rope(q, positions=torch.zeros(4))
     with pytest.raises(ValueError):
         binding.PagedKVCache(q, q)
+
+
+def test_tables_for_more_keys_than_are_counted(lib):
+    """Keys are counted in 32 bits: a table that could hold more is refused, one that just fits is not this check's."""
+    assert attend(lib, cache(ps=1 << 20), mp=2048) == UNS
+    assert attend(lib, cache(ps=1 << 20), mp=1 << 30) == UNS

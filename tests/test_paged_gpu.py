@@ -521,3 +521,53 @@ def test_binding_checks():
     with pytest.raises(binding.AttnError):
         binding.attn_paged_append(binding.PagedKVCache.allocate(4, 24, 2, 128), k, k, i32([0, 3]), n, table)
     ok()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int4"])
+@pytest.mark.parametrize("n", [40, 20000])     # finished by one warp, and cut over many
+def test_a_bad_query_row_stays_one_row(kind, n):
+    table, pages = make_table([n], 16, 1)
+    cache = make_cache(kind, pages, 16, 1, 64)
+    keys, vals = fill(cache, table, [n], 4)
+    q = randn((1, 1, 8, 64), 5)
+    bad = q.clone()
+    bad[0, 0, 3, 7], bad[0, 0, 5, 0] = float("nan"), float("inf")
+    want, want_lse = attend(q, cache, table, [n])
+    o, lse = attend(bad, cache, table, [n])
+    good = [0, 1, 2, 4, 6, 7]
+    assert bool(torch.isnan(o[0, 0, 3]).all()) and bool(torch.isnan(lse[0, 3]).all())
+    assert bool(torch.isnan(o[0, 0, 5]).all())
+    # the running maximum of other rows may move at other tiles: the last bit of a weight
+    assert torch.allclose(o[0, 0, good].float(), want[0, 0, good].float(), rtol=2.0 ** -7, atol=2.0 ** -10)
+    assert torch.allclose(lse[0, good], want_lse[0, good], rtol=2.0 ** -19)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int4"])
+def test_many_parts_few_parts_and_whole_units_in_one_call(kind):
+    """One sequence over most warps (joined by four warps), some over a few (by one), some inside a share, empty ones
+    between them; every call the same bits."""
+    lens = [60000, 1, 0, 3000, 17, 0, 0, 900, 5000] + [5] * 40 + [2500]
+    table, pages = make_table(lens, 32, 3)
+    cache = make_cache(kind, pages, 32, 2, 128)
+    keys, vals = fill(cache, table, lens, 4)
+    q = randn((len(lens), 1, 6, 128), 5, 2.0)
+    o, lse = attend(q, cache, table, lens)
+    check(q, o, lse, keys, vals, 128 ** -0.5, True, kind)
+    for _ in range(5):
+        o2, lse2 = attend(q, cache, table, lens)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_every_number_of_keys_around_the_tiles():
+    """Lengths 1 .. 140, each as its own call and all in one batch, d = 64 with 2 kv heads."""
+    lens = list(range(1, 141))
+    table, pages = make_table(lens, 16, 3)
+    for kind in ("bf16", "int4"):
+        cache = make_cache(kind, pages, 16, 2, 64)
+        keys, vals = fill(cache, table, lens, 4)
+        q = randn((len(lens), 2, 4, 64), 5, 2.0)
+        o, lse = attend(q, cache, table, lens)
+        check(q, o, lse, keys, vals, 0.125, True, kind)
+        for b in range(0, 140, 13):
+            o1, lse1 = attend(q[b:b + 1], cache, table[b:b + 1], lens[b:b + 1])
+            check(q[b:b + 1], o1, lse1, keys[b:b + 1], vals[b:b + 1], 0.125, True, kind)
