@@ -516,23 +516,21 @@ def _buffer(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _rows(name, t, heads=None, d=None):
-    """(tokens, token stride, head stride) of bf16 rows [T, heads, d] or [B, N, heads, d], last dim contiguous."""
+def _rows(name, t):
+    """(shape, tokens, token stride, head stride) of bf16 rows [T, heads, d] or [B, N, heads, d], last dim contiguous."""
     import torch
     shape, stride = t.shape, t.stride()
     dim = len(shape)
     if t.dtype != torch.bfloat16 or (dim != 3 and dim != 4) or stride[-1] != 1:
         raise ValueError(f"{name} must be a bfloat16 CUDA tensor [T, heads, d] or [B, N, heads, d] with contiguous rows")
-    if heads is not None and (shape[-2] != heads or shape[-1] != d):
-        raise ValueError(f"{name} must have {heads} heads of {d} values")
     if dim == 3:
-        return shape[0], stride[0], stride[1]
+        return shape, shape[0], stride[0], stride[1]
     B, N = shape[0], shape[1]
     if N == 1:
-        return B, stride[0], stride[2]
+        return shape, B, stride[0], stride[2]
     if B > 1 and stride[0] != N * stride[1]:
         raise ValueError(f"the tokens of {name} must be evenly spaced over the batch")
-    return B * N, stride[1], stride[2]
+    return shape, B * N, stride[1], stride[2]
 
 
 def _rope_args(cos, sin):
@@ -561,16 +559,15 @@ def _norm_rope_args(q, k, cos, sin, positions, wq, wk, norm):
     """Checks that the forward and the backward share: sizes (T, H, Hkv, d) and the C arguments from the strides to wk
     and from cos to max_pos, the positions and the sequence length."""
     import torch
-    shape = q.shape
-    T, q_st, q_sh = _rows("q", q)
-    H, d = shape[-2], shape[-1]
+    shape, T, q_st, q_sh = _rows("q", q)
+    H, d = shape[-2:]
+    four = len(shape) == 4
     Hkv = k_st = k_sh = 0
     if k is not None:
-        k_shape = k.shape
+        k_shape, k_T, k_st, k_sh = _rows("k", k)
         Hkv = k_shape[-2]
-        if len(k_shape) != len(shape) or k_shape[0] != shape[0] or (len(shape) == 4 and k_shape[1] != shape[1]):
-            raise ValueError("q and k must hold the same tokens")
-        _, k_st, k_sh = _rows("k", k, Hkv, d)
+        if k_T != T or k_shape[-1] != d or len(k_shape) != len(shape) or (four and k_shape[1] != shape[1]):
+            raise ValueError("q and k must hold the same tokens and values of one size")
     elif wk is not None:
         raise ValueError("wk needs k")
     pos = None
@@ -580,8 +577,8 @@ def _norm_rope_args(q, k, cos, sin, positions, wq, wk, norm):
         pos = positions.data_ptr()
     rope = _rope_args(cos, sin)
     _on_current_device(q, k, cos, sin, positions, wq, wk)
-    return (T, H, Hkv, d), (q_st, q_sh, k_st, k_sh, 1 if norm else 0, None if wq is None else _weight("wq", wq, d),
-                            None if wk is None else _weight("wk", wk, d)), rope, pos, shape[1] if len(shape) == 4 else T
+    return (T, H, Hkv, d), (q_st, q_sh, k_st, k_sh, 1 if norm else 0, _weight("wq", wq, d), _weight("wk", wk, d)), rope, \
+        pos, shape[1] if four else T
 
 
 def _out_rows(name, t, like, stream):
@@ -749,10 +746,10 @@ def attn_paged_append(cache: PagedKVCache, k, v, cu_seqlens, cache_lens, page_ta
     not stored. Lengths stay as they are: the caller advances cache_lens.
     """
     table = _paged_args(cache, page_table, ("cu_seqlens", cu_seqlens, 1), ("cache_lens", cache_lens, 0))
-    total, k_st, k_sh = _rows("k", k, cache.Hkv, cache.d)
-    v_total, v_st, v_sh = _rows("v", v, cache.Hkv, cache.d)
-    if total != v_total or k.dim() != 3 or v.dim() != 3:
-        raise ValueError("k and v must be [total, Hkv, d]")
+    shape, total, k_st, k_sh = _rows("k", k)
+    v_shape, _, v_st, v_sh = _rows("v", v)
+    if shape != (total, cache.Hkv, cache.d) or v_shape != shape:
+        raise ValueError("k and v must be [total, Hkv, d] with the cache's heads")
     rope = _rope_args(cos, sin)
     _on_current_device(cache.k, page_table, cu_seqlens, cache_lens, k, v, cos, sin)
     if total == 0 or table[3] == 0:
