@@ -880,7 +880,7 @@ attn_status_t attn_get_status_detail(cudaStream_t stream, uint32_t* detail) {
   if (cudaMemcpyFromSymbol(&v, g_attn_status, sizeof(v)) != cudaSuccess) return ATTN_ERR_CUDA;
   if (detail) *detail = v;
   if (!v) return ATTN_OK;
-  return (v & 0x40000000u) ? ATTN_ERR_TIMEOUT : ATTN_ERR_INVALID_ARG;   // 0x20000000: bad varlen plan
+  return (v & 0x40000000u) ? ATTN_ERR_TIMEOUT : ATTN_ERR_INVALID_ARG;   // 0x20000000: bad plan, page or position
 }
 
 attn_status_t attn_clear_status(void) {

@@ -10,6 +10,10 @@
 // of exchanging them, and a group of 64 values is 4 neighbouring lanes, so its least and greatest value take two
 // exchanges. Rotation and quantisation round every step as written here (no contraction into fused multiply-adds): a
 // code must not depend on how the compiler schedules, or a value at a border between two codes would change with it.
+//
+// Measured on a GB300, 8 kv heads, d 128, 4 bits: append of 12.4k tokens 24.5 us (66 MB; arithmetic and the chain of
+// offsets, page and angles; 49 us with IEEE divisions and 8 values a lane), gather of 29.4k tokens 24.4 us (154 MB, 93% of
+// the copy bandwidth; 29.5 us with values converted one by one).
 #include <algorithm>
 #include <climits>
 

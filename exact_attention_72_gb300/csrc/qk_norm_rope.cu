@@ -11,7 +11,12 @@
 // d / 8 lanes hold a row, 8 values each as two chunks of 4 that hold both members of their pairs, so
 // the rotation needs no exchange and only the row sums cross lanes. A task is one token and up to
 // 4 heads of q or of k: the angles and weights are loaded once per task, and the 4 rows' loads are in
-// flight together. Everything is fp32 between the bf16 loads and the one rounding at the store.
+// flight together, those of the next task behind them. Everything is fp32 between the bf16 loads and the
+// one rounding at the store.
+//
+// Memory bounds both. At B 2, N 8192, 32 + 8 heads, d 128 on a GB300 (share of the copy bandwidth): forward 56.7 us
+// (88%; 102 with rows unpacked at the load and a CTA per 16 tasks, 70 with rows held packed), backward
+// 92.2 us (81%; 155 at first; with 2 heads a task 114).
 #include <algorithm>
 #include <climits>
 #include <cmath>

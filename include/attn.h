@@ -424,10 +424,12 @@ attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq
  * The struct is HOST memory, read during a call only.
  *
  * Page tables are DEVICE int32, row b of sequence b at page_table + b * table_stride, max_pages entries
- * each; entries behind a sequence's last page are not read. An entry outside 0 .. num_pages - 1
+ * each; entries behind a sequence's last page are not used. An entry outside 0 .. num_pages - 1
  * that a call would use, a length that max_pages cannot hold, or offsets that do not ascend never lead
  * outside the cache: the rows concerned are not written (append, gather) or count as zeros (attention,
  * where a length is cut to max_pages * page_size), and attn_get_status reports ATTN_ERR_INVALID_ARG.
+ * Rows behind a sequence's length may hold anything; rows within it have to be finite (a masked key's weight is 0,
+ * and 0 times an infinity is NaN).
  */
 typedef enum { ATTN_CACHE_BF16 = 0, ATTN_CACHE_INT4 = 1 } attn_cache_type_t;
 
@@ -481,10 +483,12 @@ attn_status_t attn_paged_gather(const attn_paged_cache_t* cache, void* k, void* 
  *   scale as in attn_fwd (finite, nonzero).
  *   workspace: DEVICE, 256-byte aligned, at least attn_fwd_paged_workspace_bytes(...) bytes, which do
  *      not depend on the lengths; needs no initialisation. Calls that may overlap on the GPU (captured
- *      graphs included) need one each. q, o, lse and workspace must not overlap.
+ *      graphs included) need one each. q, o, lse and workspace must not overlap each other or the cache.
  * Lengths stay on the device: the call can be captured and replayed while they grow. Every call reads
  * its keys and values ceil(Nq (H / Hkv) / R) times, R = 8 query rows, or 16 when there are more than 8
- * and d <= 128. Deterministic. Two kernels, the second a programmatic dependent launch; allocates nothing.
+ * and d <= 128. Deterministic. Two programmatic dependent launches; allocates nothing.
+ * UNSUPPORTED as for the cache, for scale == 0, and for max_pages * page_size >= 2^31 - 1023 or
+ * B * Hkv * row blocks * tiles of 16 keys (32 in 4 bits) >= 2^31.
  */
 size_t attn_fwd_paged_workspace_bytes(int B, int H, int Hkv, int Nq, int d, attn_cache_type_t type);
 attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t* cache, void* o, float* lse,
