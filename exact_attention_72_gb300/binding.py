@@ -136,9 +136,7 @@ def _dtype_code(t) -> int:
 
 def _stream_handle(stream) -> int:
     import torch
-    if stream is None:   # the current stream's handle without a stream object: called on every launch
-        if torch.cuda.is_initialized():
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if stream is None:
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream)
 
@@ -497,14 +495,17 @@ def attn_fwd_host_workspace_bytes(B: int, H: int, Hkv: int, N: int, d: int, dtyp
     return int(lib().attn_fwd_host_workspace_bytes(B, H, Hkv, N, d, dtype_code))
 
 
-def _on_current_device(*tensors):
-    """Kernels launch on the current device: its tensors only (None stands for one that is not given)."""
+def _launch_stream(stream, *tensors):
+    """The stream handle of a call. Kernels launch on the current device: its tensors only (None: one not given)."""
     import torch
-    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+    dev = tensors[0].get_device()
+    if dev >= 0 and dev != torch._C._cuda_getDevice():
+        dev = -1
     for t in tensors:
-        if t is not None and t.get_device() != dev:
+        if t is not None and (dev < 0 or t.get_device() != dev):
             raise ValueError("every tensor of a call must be a CUDA tensor on the current device, "
                              f"got one on {t.device}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
 
 
 def _buffer(shape, dtype, device, stream):
@@ -576,7 +577,6 @@ def _norm_rope_args(q, k, cos, sin, positions, wq, wk, norm):
             raise ValueError("positions must be a contiguous int32 CUDA tensor, one per token")
         pos = positions.data_ptr()
     rope = _rope_args(cos, sin)
-    _on_current_device(q, k, cos, sin, positions, wq, wk)
     return (T, H, Hkv, d), (q_st, q_sh, k_st, k_sh, 1 if norm else 0, _weight("wq", wq, d), _weight("wk", wk, d)), rope, \
         pos, shape[1] if four else T
 
@@ -591,7 +591,6 @@ def _out_rows(name, t, like, stream):
             return torch.empty_like(like, memory_format=torch.contiguous_format)
     if t.shape != like.shape or t.dtype != torch.bfloat16 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor of shape {tuple(like.shape)}")
-    _on_current_device(t)
     return t
 
 
@@ -609,15 +608,18 @@ def attn_qk_norm_rope(q, k=None, cos=None, sin=None, positions=None, wq=None, wk
     sizes, rows, rope, pos, seq_len = _norm_rope_args(q, k, cos, sin, positions, wq, wk, norm)
     if k is None and k_out is not None:
         raise ValueError("k_out needs k")
+    handle = _launch_stream(stream, q, k, cos, sin, positions, wq, wk, q_out, k_out)
     q_out = _out_rows("q_out", q_out, q, stream)
+    kp = k_out_p = None
     if k is not None:
         k_out = _out_rows("k_out", k_out, k, stream)
+        kp, k_out_p = k.data_ptr(), k_out.data_ptr()
     if sizes[0] == 0:
         return q_out, k_out
-    st = lib().attn_qk_norm_rope(q.data_ptr(), k.data_ptr() if k is not None else None, q_out.data_ptr(),
-                                 k_out.data_ptr() if k is not None else None, *sizes, *rows, eps, *rope,
-                                 1 if interleaved else 0, pos, seq_len, _stream_handle(stream))
-    _check(st, "attn_qk_norm_rope")
+    st = lib().attn_qk_norm_rope(q.data_ptr(), kp, q_out.data_ptr(), k_out_p, *sizes, *rows, eps, *rope,
+                                 1 if interleaved else 0, pos, seq_len, handle)
+    if st != ATTN_OK:
+        _check(st, "attn_qk_norm_rope")
     return q_out, k_out
 
 
@@ -639,9 +641,12 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out=None, cos=None, sin=None, positio
             raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor like its input")
     if (dk is not None and k is None) or (dwq is not None and wq is None) or (dwk is not None and wk is None):
         raise ValueError("dk needs k, dwq needs wq and dwk needs wk")
+    handle = _launch_stream(stream, q, k, dq_out, dk_out, cos, sin, positions, wq, wk, dq, dk, dwq, dwk, workspace)
     dq = _out_rows("dq", dq, q, stream)
+    kp = dk_out_p = dk_p = None
     if k is not None:
         dk = _out_rows("dk", dk, k, stream)
+        kp, dk_out_p, dk_p = k.data_ptr(), dk_out.data_ptr(), dk.data_ptr()
     need = attn_qk_norm_rope_bwd_workspace_bytes(*sizes) if wq is not None or wk is not None else 0
     if wq is not None and dwq is None:
         dwq = _buffer((d,), torch.float32, q.device, stream)
@@ -655,14 +660,12 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out=None, cos=None, sin=None, positio
         return dq, dk, dwq, dwk
     if workspace is None and need:
         workspace = _buffer((need,), torch.uint8, q.device, stream)
-    _on_current_device(dq_out, dk_out, dwq, dwk, workspace)
     ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = lib().attn_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr() if k is not None else None, dq_out.data_ptr(),
-                                     dk_out.data_ptr() if k is not None else None, dq.data_ptr(),
-                                     dk.data_ptr() if k is not None else None, _weight("dwq", dwq, d),
-                                     _weight("dwk", dwk, d), *sizes, *rows, eps, *rope, 1 if interleaved else 0, pos,
-                                     seq_len, *ws, _stream_handle(stream))
-    _check(st, "attn_qk_norm_rope_bwd")
+    st = lib().attn_qk_norm_rope_bwd(q.data_ptr(), kp, dq_out.data_ptr(), dk_out_p, dq.data_ptr(), dk_p,
+                                     _weight("dwq", dwq, d), _weight("dwk", dwk, d), *sizes, *rows, eps, *rope,
+                                     1 if interleaved else 0, pos, seq_len, *ws, handle)
+    if st != ATTN_OK:
+        _check(st, "attn_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
 
@@ -751,13 +754,13 @@ def attn_paged_append(cache: PagedKVCache, k, v, cu_seqlens, cache_lens, page_ta
     if shape != (total, cache.Hkv, cache.d) or v_shape != shape:
         raise ValueError("k and v must be [total, Hkv, d] with the cache's heads")
     rope = _rope_args(cos, sin)
-    _on_current_device(cache.k, page_table, cu_seqlens, cache_lens, k, v, cos, sin)
+    handle = _launch_stream(stream, cache.k, page_table, cu_seqlens, cache_lens, k, v, cos, sin)
     if total == 0 or table[3] == 0:
         return
     st = lib().attn_paged_append(cache._ref, k.data_ptr(), v.data_ptr(), k_st, k_sh, v_st, v_sh, cu_seqlens.data_ptr(),
-                                 cache_lens.data_ptr(), *table, total, *rope, 1 if interleaved else 0,
-                                 _stream_handle(stream))
-    _check(st, "attn_paged_append")
+                                 cache_lens.data_ptr(), *table, total, *rope, 1 if interleaved else 0, handle)
+    if st != ATTN_OK:
+        _check(st, "attn_paged_append")
 
 
 def attn_paged_gather(cache: PagedKVCache, cu_seqlens, page_table, total: int, k=None, v=None, stream=None):
@@ -766,19 +769,19 @@ def attn_paged_gather(cache: PagedKVCache, cu_seqlens, page_table, total: int, k
     import torch
     table = _paged_args(cache, page_table, ("cu_seqlens", cu_seqlens, 1))
     shape = (total, cache.Hkv, cache.d)
+    for name, t in (("k", k), ("v", v)):
+        if t is not None and (t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor of shape {shape}")
+    handle = _launch_stream(stream, cache.k, page_table, cu_seqlens, k, v)
     if k is None:
         k = _buffer(shape, torch.bfloat16, cache.device, stream)
     if v is None:
         v = _buffer(shape, torch.bfloat16, cache.device, stream)
-    for name, t in (("k", k), ("v", v)):
-        if t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor of shape {shape}")
-    _on_current_device(cache.k, page_table, cu_seqlens, k, v)
     if total == 0 or table[3] == 0:
         return k, v
-    st = lib().attn_paged_gather(cache._ref, k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), *table, total,
-                                 _stream_handle(stream))
-    _check(st, "attn_paged_gather")
+    st = lib().attn_paged_gather(cache._ref, k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), *table, total, handle)
+    if st != ATTN_OK:
+        _check(st, "attn_paged_gather")
     return k, v
 
 
@@ -801,20 +804,19 @@ def attn_fwd_paged(q, cache: PagedKVCache, page_table, seqlens, causal: bool = T
     table = _paged_args(cache, page_table, ("seqlens", seqlens, 0))
     if table[3] != B or d != cache.d or H % cache.Hkv != 0:
         raise ValueError("q must be [B, Nq, H, d] with the page table's B, the cache's d and a multiple of its heads")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+    if lse is not None and (lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 CUDA tensor [B, H, Nq]")
+    handle = _launch_stream(stream, cache.k, page_table, seqlens, q, workspace, out, lse)
     if workspace is None:
         workspace = _buffer((max(attn_fwd_paged_workspace_bytes(cache, B, H, Nq), 1),), torch.uint8, q.device, stream)
     out = _out_rows("out", out, q, stream)
     if lse is None:
         lse = _buffer((B, H, Nq), torch.float32, q.device, stream)
-    elif lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous float32 CUDA tensor [B, H, Nq]")
-    _on_current_device(cache.k, page_table, seqlens, q, workspace, lse)
     st = lib().attn_fwd_paged(q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(), *table[:3], seqlens.data_ptr(), B,
-                              H, Nq, scale, 1 if causal else 0, workspace.data_ptr(),
-                              workspace.numel() * workspace.element_size(), _stream_handle(stream))
-    _check(st, "attn_fwd_paged")
+                              H, Nq, d ** -0.5 if scale is None else scale, 1 if causal else 0, workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), handle)
+    if st != ATTN_OK:
+        _check(st, "attn_fwd_paged")
     return out, lse
 
 
