@@ -1,4 +1,5 @@
-"""ctypes binding of libattn_gb300.so (argument marshalling only; all compute runs in the library).
+"""Binding of libattn_gb300.so (argument marshalling only; all compute runs in the library), by ctypes; the calls whose
+kernels take a few microseconds (norm and rotation, paged cache) are marshalled by _calls.so (csrc/calls.cpp).
 
 The Python names mirror the C ABI in include/attn.h. ``attn_fwd`` takes torch CUDA tensors
 (PyTorch is used for device memory and streams only) and raises ``AttnError`` on any non-OK
@@ -495,103 +496,28 @@ def attn_fwd_host_workspace_bytes(B: int, H: int, Hkv: int, N: int, d: int, dtyp
     return int(lib().attn_fwd_host_workspace_bytes(B, H, Hkv, N, d, dtype_code))
 
 
-def _launch_stream(stream, *tensors):
-    """The stream handle of a call. Kernels launch on the current device: its tensors only (None: one not given)."""
-    import torch
-    dev = tensors[0].get_device()
-    if dev >= 0 and dev != torch._C._cuda_getDevice():
-        dev = -1
-    for t in tensors:
-        if t is not None and (dev < 0 or t.get_device() != dev):
-            raise ValueError("every tensor of a call must be a CUDA tensor on the current device, "
-                             f"got one on {t.device}")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
+_CALLS = None
 
 
-def _buffer(shape, dtype, device, stream):
-    """A tensor the call makes for itself, allocated for the stream that it runs on."""
+def _calls():
+    """The compiled calls (csrc/calls.cpp), loaded with the library they link to."""
+    global _CALLS
+    if _CALLS is None:
+        import torch  # noqa: F401  (its libraries first)
+        lib()
+        if not os.path.exists(_build.CALLS_PATH):
+            raise RuntimeError("_calls.so is not built; call exact_attention_72_gb300.build.build()")
+        from . import _calls as module
+        module.set_error(AttnError)
+        _CALLS = module
+    return _CALLS
+
+
+def _on(stream, call, *args):
+    """call(*args) on a stream of the caller's: what it allocates belongs to that stream too."""
     import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _rows(name, t):
-    """(shape, tokens, token stride, head stride) of bf16 rows [T, heads, d] or [B, N, heads, d], last dim contiguous."""
-    import torch
-    shape, stride = t.shape, t.stride()
-    dim = len(shape)
-    if t.dtype != torch.bfloat16 or (dim != 3 and dim != 4) or stride[-1] != 1:
-        raise ValueError(f"{name} must be a bfloat16 CUDA tensor [T, heads, d] or [B, N, heads, d] with contiguous rows")
-    if dim == 3:
-        return shape, shape[0], stride[0], stride[1]
-    B, N = shape[0], shape[1]
-    if N == 1:
-        return shape, B, stride[0], stride[2]
-    if B > 1 and stride[0] != N * stride[1]:
-        raise ValueError(f"the tokens of {name} must be evenly spaced over the batch")
-    return shape, B * N, stride[1], stride[2]
-
-
-def _rope_args(cos, sin):
-    """(cos pointer, sin pointer, rope_dim, max_pos) of angle tables [max_pos, rope_dim / 2]."""
-    import torch
-    if cos is None and sin is None:
-        return 0, 0, 0, 0
-    if cos is None or sin is None or cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.dim() != 2 or \
-            cos.shape != sin.shape or not cos.is_contiguous() or not sin.is_contiguous():
-        raise ValueError("cos and sin must be contiguous float32 CUDA tensors [max_pos, rope_dim / 2], both or neither")
-    max_pos, half = cos.shape
-    return cos.data_ptr(), sin.data_ptr(), 2 * half, max_pos
-
-
-def _weight(name, w, d):
-    """Pointer of a float32 [d] tensor, None for None."""
-    import torch
-    if w is None:
-        return None
-    if w.dtype != torch.float32 or w.shape != (d,) or not w.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of d values")
-    return w.data_ptr()
-
-
-def _norm_rope_args(q, k, cos, sin, positions, wq, wk, norm):
-    """Checks that the forward and the backward share: sizes (T, H, Hkv, d) and the C arguments from the strides to wk
-    and from cos to max_pos, the positions and the sequence length."""
-    import torch
-    shape, T, q_st, q_sh = _rows("q", q)
-    H, d = shape[-2:]
-    four = len(shape) == 4
-    Hkv = k_st = k_sh = 0
-    if k is not None:
-        k_shape, k_T, k_st, k_sh = _rows("k", k)
-        Hkv = k_shape[-2]
-        if k_T != T or k_shape[-1] != d or len(k_shape) != len(shape) or (four and k_shape[1] != shape[1]):
-            raise ValueError("q and k must hold the same tokens and values of one size")
-    elif wk is not None:
-        raise ValueError("wk needs k")
-    pos = None
-    if positions is not None:
-        if positions.dtype != torch.int32 or positions.shape != shape[:-2] or not positions.is_contiguous():
-            raise ValueError("positions must be a contiguous int32 CUDA tensor, one per token")
-        pos = positions.data_ptr()
-    rope = _rope_args(cos, sin)
-    return (T, H, Hkv, d), (q_st, q_sh, k_st, k_sh, 1 if norm else 0, _weight("wq", wq, d), _weight("wk", wk, d)), rope, \
-        pos, shape[1] if four else T
-
-
-def _out_rows(name, t, like, stream):
-    """An output with the shape of ``like``, contiguous: ``t`` if given."""
-    import torch
-    if t is None:
-        if stream is None:
-            return torch.empty_like(like, memory_format=torch.contiguous_format)
-        with torch.cuda.stream(stream):
-            return torch.empty_like(like, memory_format=torch.contiguous_format)
-    if t.shape != like.shape or t.dtype != torch.bfloat16 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor of shape {tuple(like.shape)}")
-    return t
+        return call(*args)
 
 
 def attn_qk_norm_rope(q, k=None, cos=None, sin=None, positions=None, wq=None, wk=None, eps: float = 1e-6,
@@ -605,22 +531,10 @@ def attn_qk_norm_rope(q, k=None, cos=None, sin=None, positions=None, wq=None, wk
     in the sequence. ``wq`` and ``wk`` (float32 [d]) weigh the normalised values; ``norm=False`` only
     rotates. Outputs are contiguous; each may be its own contiguous input.
     """
-    sizes, rows, rope, pos, seq_len = _norm_rope_args(q, k, cos, sin, positions, wq, wk, norm)
-    if k is None and k_out is not None:
-        raise ValueError("k_out needs k")
-    handle = _launch_stream(stream, q, k, cos, sin, positions, wq, wk, q_out, k_out)
-    q_out = _out_rows("q_out", q_out, q, stream)
-    kp = k_out_p = None
-    if k is not None:
-        k_out = _out_rows("k_out", k_out, k, stream)
-        kp, k_out_p = k.data_ptr(), k_out.data_ptr()
-    if sizes[0] == 0:
-        return q_out, k_out
-    st = lib().attn_qk_norm_rope(q.data_ptr(), kp, q_out.data_ptr(), k_out_p, *sizes, *rows, eps, *rope,
-                                 1 if interleaved else 0, pos, seq_len, handle)
-    if st != ATTN_OK:
-        _check(st, "attn_qk_norm_rope")
-    return q_out, k_out
+    call = (_CALLS or _calls()).qk_norm_rope
+    if stream is not None:
+        return _on(stream, call, q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, q_out, k_out)
+    return call(q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, q_out, k_out)
 
 
 def attn_qk_norm_rope_bwd_workspace_bytes(T: int, H: int, Hkv: int, d: int) -> int:
@@ -632,41 +546,11 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out=None, cos=None, sin=None, positio
                           dwk=None, workspace=None, stream=None):
     """Gradients (dq, dk, dwq, dwk) of attn_qk_norm_rope for the gradients of its outputs (contiguous, e.g.
     from attn_bwd); dwq and dwk are float32 [d], None without weights. dq and dk may be dq_out and dk_out."""
-    import torch
-    sizes, rows, rope, pos, seq_len = _norm_rope_args(q, k, cos, sin, positions, wq, wk, norm)
-    T, d = sizes[0], sizes[3]
-    for name, g, x in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
-        if (g is None) != (x is None) or (g is not None and (g.shape != x.shape or g.dtype != torch.bfloat16 or
-                                                             not g.is_contiguous())):
-            raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor like its input")
-    if (dk is not None and k is None) or (dwq is not None and wq is None) or (dwk is not None and wk is None):
-        raise ValueError("dk needs k, dwq needs wq and dwk needs wk")
-    handle = _launch_stream(stream, q, k, dq_out, dk_out, cos, sin, positions, wq, wk, dq, dk, dwq, dwk, workspace)
-    dq = _out_rows("dq", dq, q, stream)
-    kp = dk_out_p = dk_p = None
-    if k is not None:
-        dk = _out_rows("dk", dk, k, stream)
-        kp, dk_out_p, dk_p = k.data_ptr(), dk_out.data_ptr(), dk.data_ptr()
-    need = attn_qk_norm_rope_bwd_workspace_bytes(*sizes) if wq is not None or wk is not None else 0
-    if wq is not None and dwq is None:
-        dwq = _buffer((d,), torch.float32, q.device, stream)
-    if wk is not None and dwk is None:
-        dwk = _buffer((d,), torch.float32, q.device, stream)
-    if T == 0:
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
-            for g in (dwq, dwk):
-                if g is not None:
-                    g.zero_()
-        return dq, dk, dwq, dwk
-    if workspace is None and need:
-        workspace = _buffer((need,), torch.uint8, q.device, stream)
-    ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = lib().attn_qk_norm_rope_bwd(q.data_ptr(), kp, dq_out.data_ptr(), dk_out_p, dq.data_ptr(), dk_p,
-                                     _weight("dwq", dwq, d), _weight("dwk", dwk, d), *sizes, *rows, eps, *rope,
-                                     1 if interleaved else 0, pos, seq_len, *ws, handle)
-    if st != ATTN_OK:
-        _check(st, "attn_qk_norm_rope_bwd")
-    return dq, dk, dwq, dwk
+    call = (_CALLS or _calls()).qk_norm_rope_bwd
+    if stream is not None:
+        return _on(stream, call, q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, dq_out, dk_out, dq, dk, dwq, dwk,
+                   workspace)
+    return call(q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, dq_out, dk_out, dq, dk, dwq, dwk, workspace)
 
 
 class PagedKVCache:
@@ -707,7 +591,7 @@ class PagedKVCache:
         self._struct = _PagedCacheStruct(k.data_ptr(), v.data_ptr(), k_sz.data_ptr() if four else None,
                                          v_sz.data_ptr() if four else None, *k.stride()[:3], *sz, P, S, Hkv, d,
                                          self.type)
-        self._ref = ctypes.byref(self._struct)
+        self._address, self._index = ctypes.addressof(self._struct), k.get_device()   # what the calls take
 
     @classmethod
     def allocate(cls, num_pages: int, page_size: int, Hkv: int, d: int, cache_type: str = "bf16", device="cuda"):
@@ -725,20 +609,6 @@ class PagedKVCache:
                    make(d // ATTN_INT4_GROUP, 2, dtype=torch.bfloat16))
 
 
-def _paged_args(cache, page_table, *vectors):
-    """Checks of a call on ``cache``: the page table and int32 vectors (name, tensor, entries more than B). The C arguments
-    (page table, stride, max_pages, B)."""
-    import torch
-    int32 = torch.int32
-    if page_table.dtype != int32 or page_table.dim() != 2 or (page_table.stride(1) != 1 and page_table.shape[1] > 1):
-        raise ValueError("page_table must be an int32 CUDA tensor [B, max_pages] with contiguous rows")
-    B, max_pages = page_table.shape
-    for name, t, extra in vectors:
-        if t.dtype != int32 or t.shape != (B + extra,) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {B + extra} values")
-    return page_table.data_ptr(), page_table.stride(0), max_pages, B
-
-
 def attn_paged_append(cache: PagedKVCache, k, v, cu_seqlens, cache_lens, page_table, cos=None, sin=None,
                       interleaved: bool = False, stream=None) -> None:
     """Stores new keys and values k, v (bf16 [total, Hkv, d], token and head strides free) in ``cache``.
@@ -748,41 +618,19 @@ def attn_paged_append(cache: PagedKVCache, k, v, cu_seqlens, cache_lens, page_ta
     way (cos and sin as in attn_qk_norm_rope; None: k is stored as it is). Tokens from cu_seqlens[B] on are
     not stored. Lengths stay as they are: the caller advances cache_lens.
     """
-    table = _paged_args(cache, page_table, ("cu_seqlens", cu_seqlens, 1), ("cache_lens", cache_lens, 0))
-    shape, total, k_st, k_sh = _rows("k", k)
-    v_shape, _, v_st, v_sh = _rows("v", v)
-    if shape != (total, cache.Hkv, cache.d) or v_shape != shape:
-        raise ValueError("k and v must be [total, Hkv, d] with the cache's heads")
-    rope = _rope_args(cos, sin)
-    handle = _launch_stream(stream, cache.k, page_table, cu_seqlens, cache_lens, k, v, cos, sin)
-    if total == 0 or table[3] == 0:
-        return
-    st = lib().attn_paged_append(cache._ref, k.data_ptr(), v.data_ptr(), k_st, k_sh, v_st, v_sh, cu_seqlens.data_ptr(),
-                                 cache_lens.data_ptr(), *table, total, *rope, 1 if interleaved else 0, handle)
-    if st != ATTN_OK:
-        _check(st, "attn_paged_append")
+    call = (_CALLS or _calls()).paged_append
+    if stream is not None:
+        return _on(stream, call, cache._address, cache._index, k, v, cu_seqlens, cache_lens, page_table, cos, sin, interleaved)
+    return call(cache._address, cache._index, k, v, cu_seqlens, cache_lens, page_table, cos, sin, interleaved)
 
 
 def attn_paged_gather(cache: PagedKVCache, cu_seqlens, page_table, total: int, k=None, v=None, stream=None):
     """(k, v), bf16 [total, Hkv, d]: positions 0 .. cu_seqlens[b + 1] - cu_seqlens[b] - 1 of every sequence read
     out of the cache, packed as attn_fwd_varlen takes them. Rows from cu_seqlens[B] on are left as they were."""
-    import torch
-    table = _paged_args(cache, page_table, ("cu_seqlens", cu_seqlens, 1))
-    shape = (total, cache.Hkv, cache.d)
-    for name, t in (("k", k), ("v", v)):
-        if t is not None and (t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor of shape {shape}")
-    handle = _launch_stream(stream, cache.k, page_table, cu_seqlens, k, v)
-    if k is None:
-        k = _buffer(shape, torch.bfloat16, cache.device, stream)
-    if v is None:
-        v = _buffer(shape, torch.bfloat16, cache.device, stream)
-    if total == 0 or table[3] == 0:
-        return k, v
-    st = lib().attn_paged_gather(cache._ref, k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), *table, total, handle)
-    if st != ATTN_OK:
-        _check(st, "attn_paged_gather")
-    return k, v
+    call = (_CALLS or _calls()).paged_gather
+    if stream is not None:
+        return _on(stream, call, cache._address, cache._index, cu_seqlens, page_table, total, k, v)
+    return call(cache._address, cache._index, cu_seqlens, page_table, total, k, v)
 
 
 def attn_fwd_paged_workspace_bytes(cache: PagedKVCache, B: int, H: int, Nq: int) -> int:
@@ -797,27 +645,10 @@ def attn_fwd_paged(q, cache: PagedKVCache, page_table, seqlens, causal: bool = T
     query i sees keys j <= i + seqlens[b] - Nq. Rows that see no key give 0 and -inf. ``workspace`` (CUDA
     uint8, at least attn_fwd_paged_workspace_bytes(...)) is allocated here with torch if not given.
     """
-    import torch
-    if q.dim() != 4 or q.dtype != torch.bfloat16 or not q.is_contiguous():
-        raise ValueError("q must be a contiguous bfloat16 CUDA tensor [B, Nq, H, d]")
-    B, Nq, H, d = q.shape
-    table = _paged_args(cache, page_table, ("seqlens", seqlens, 0))
-    if table[3] != B or d != cache.d or H % cache.Hkv != 0:
-        raise ValueError("q must be [B, Nq, H, d] with the page table's B, the cache's d and a multiple of its heads")
-    if lse is not None and (lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous float32 CUDA tensor [B, H, Nq]")
-    handle = _launch_stream(stream, cache.k, page_table, seqlens, q, workspace, out, lse)
-    if workspace is None:
-        workspace = _buffer((max(attn_fwd_paged_workspace_bytes(cache, B, H, Nq), 1),), torch.uint8, q.device, stream)
-    out = _out_rows("out", out, q, stream)
-    if lse is None:
-        lse = _buffer((B, H, Nq), torch.float32, q.device, stream)
-    st = lib().attn_fwd_paged(q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(), *table[:3], seqlens.data_ptr(), B,
-                              H, Nq, d ** -0.5 if scale is None else scale, 1 if causal else 0, workspace.data_ptr(),
-                              workspace.numel() * workspace.element_size(), handle)
-    if st != ATTN_OK:
-        _check(st, "attn_fwd_paged")
-    return out, lse
+    call = (_CALLS or _calls()).fwd_paged
+    if stream is not None:
+        return _on(stream, call, cache._address, cache._index, q, page_table, seqlens, causal, scale, workspace, out, lse)
+    return call(cache._address, cache._index, q, page_table, seqlens, causal, scale, workspace, out, lse)
 
 
 def attn_get_status(stream=None) -> tuple[int, int]:

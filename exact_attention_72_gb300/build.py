@@ -1,4 +1,5 @@
-"""Builds libattn_gb300.so from csrc/ with nvcc for sm_103a (in-tree, no setuptools).
+"""Builds libattn_gb300.so from csrc/ with nvcc for sm_103a (in-tree, no setuptools), and _calls.so, the compiled part
+of the Python binding (csrc/calls.cpp, against torch's headers), beside it.
 
 Each .cu file compiles in its own nvcc process (in parallel); the objects are linked into one
 shared library next to this file. The CUDA runtime is linked statically and the driver's
@@ -9,10 +10,12 @@ from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -21,6 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_NAME = "libattn_gb300.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
+CALLS_PATH = os.path.join(PKG_DIR, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
@@ -37,15 +41,21 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _torch_dir() -> str:
+    return list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+
+
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))) + \
-        sorted(glob.glob(os.path.join(INCLUDE, "*.h"))) + [os.path.abspath(__file__)]
+    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
+                               glob.glob(os.path.join(CSRC, "*.cpp"))) + \
+        sorted(glob.glob(os.path.join(INCLUDE, "*.h"))) + \
+        [os.path.abspath(__file__), os.path.join(_torch_dir(), "version.py")]   # _calls.so is bound to one torch
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -60,6 +70,21 @@ def _compile(nvcc: str, src: str, verbose: bool) -> str:
     return obj
 
 
+def _run(cmd, what: str) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_calls(nvcc: str) -> str:
+    obj = os.path.join(BUILD_DIR, "calls.o")
+    includes = [os.path.join(_torch_dir(), "include"), sysconfig.get_paths()["include"],
+                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"), INCLUDE]
+    _run(["g++", "-O2", "-std=c++17", "-fPIC"] + ["-I" + p for p in includes] +
+         ["-c", os.path.join(CSRC, "calls.cpp"), "-o", obj], "g++ for calls.cpp")
+    return obj
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compiles (if needed) and returns the path of the shared library."""
     if not force and up_to_date():
@@ -67,14 +92,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = _sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        calls = ex.submit(_compile_calls, nvcc)
         objs = list(ex.map(lambda s: _compile(nvcc, s, verbose), srcs))
+        calls_obj = calls.result()
     tmp = LIB_PATH + ".tmp"
-    cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([nvcc] + ARCH + ["-shared", "-Xlinker", "-soname=" + LIB_NAME, "-o", tmp] + objs, "link")
     os.replace(tmp, LIB_PATH)
+    # finds the library beside itself, and torch's where they were when it was built
+    torch_lib = os.path.join(_torch_dir(), "lib")
+    tmp = CALLS_PATH + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, calls_obj, "-L" + PKG_DIR, "-l:" + LIB_NAME, "-L" + torch_lib, "-ltorch_python",
+          "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib], "link of _calls.so")
+    os.replace(tmp, CALLS_PATH)
     return LIB_PATH
 
 

@@ -173,3 +173,21 @@ def test_tables_for_more_keys_than_are_counted(lib):
     """Keys are counted in 32 bits: a table that could hold more is refused, one that just fits is not this check's."""
     assert attend(lib, cache(ps=1 << 20), mp=2048) == UNS
     assert attend(lib, cache(ps=1 << 20), mp=1 << 30) == UNS
+
+
+def test_compiled_calls_turn_errors_into_exceptions():
+    calls = binding._calls()
+    with pytest.raises(TypeError):
+        calls.qk_norm_rope(torch.zeros(1, 1, 64, dtype=torch.bfloat16))                  # the number of arguments
+    with pytest.raises(TypeError, match="q must be a torch tensor"):
+        binding.attn_qk_norm_rope([[0.0]])
+    with pytest.raises(TypeError, match="cos must be a torch tensor"):
+        binding.attn_qk_norm_rope(torch.zeros(1, 1, 64, dtype=torch.bfloat16), cos=1.0)
+    with pytest.raises(TypeError):
+        binding.attn_qk_norm_rope(torch.zeros(1, 1, 64, dtype=torch.bfloat16), eps="x")
+    with pytest.raises((ValueError, RuntimeError)):                                       # a tensor without rows
+        binding.attn_qk_norm_rope(torch.zeros(1, 1, 64, dtype=torch.bfloat16).to_sparse())
+    with pytest.raises(ValueError, match="CUDA tensor on the current device"):
+        binding.attn_qk_norm_rope(torch.zeros(1, 1, 64, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="CUDA tensor on the current device"):
+        binding.attn_qk_norm_rope(torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="meta"))
