@@ -103,7 +103,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     torch_lib = os.path.join(_torch_dir(), "lib")
     tmp = CALLS_PATH + ".tmp"
     _run(["g++", "-shared", "-o", tmp, calls_obj, "-L" + PKG_DIR, "-l:" + LIB_NAME, "-L" + torch_lib, "-ltorch_python",
-          "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib], "link of _calls.so")
+          "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib], "link of _calls.so")
     os.replace(tmp, CALLS_PATH)
     return LIB_PATH
 
