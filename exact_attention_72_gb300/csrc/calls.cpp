@@ -2,9 +2,9 @@
 //
 // These kernels take 2 to 10 us at decode sizes. Marshalled in Python through ctypes their calls took 10 to 36 us of
 // the host (tens of attribute reads and a conversion for each of up to 37 arguments). Everything here is that
-// marshalling (3 to 11 us now, 2.2 us of them each launch); all compute runs in libattn_gb300.so, which this module links to. Functions take their arguments by
-// position, None for one that is not given, and launch on the current stream of the current device. binding.py holds the
-// signatures, defaults and documentation.
+// marshalling (3 to 11 us now, 2.2 us of them each launch); all compute runs in libattn_gb300.so, which this module
+// links to. Functions take their arguments by position, None for one that is not given, and launch on the current
+// stream of the current device. binding.py holds the signatures, defaults and documentation.
 #include <Python.h>
 
 #include <algorithm>

@@ -25,6 +25,7 @@
 #include "ops.h"
 #include "paged.cuh"
 #include "paged_host.h"
+#include "ptx.cuh"
 
 namespace gb300 {
 namespace {
@@ -53,23 +54,37 @@ struct GatherParams {
   uint32_t* status;
 };
 
-__device__ __forceinline__ void unpack8(float (&x)[8], const uint4& w) {
+// Two values in a register pair: the arithmetic below works on two at a time (FFMA2 and its kin, half the issue slots).
+__device__ __forceinline__ void unpack8(uint64_t* x, const uint4& w) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  for (int i = 0; i < 4; ++i) x[i] = f2_pack(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+}
+
+__device__ __forceinline__ void load8(uint64_t (&x)[4], const float* from) {
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(from + 2 * i);
+    x[i] = a.x, x[i + 1] = a.y;
   }
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+__device__ __forceinline__ uint4 pack8(const uint64_t* x) {
   uint32_t u[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    float lo, hi;
+    f2_unpack(x[i], lo, hi);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     u[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // fp32 to the bf16 not above it (UP false) or not below it, as fp32.
@@ -87,35 +102,69 @@ __device__ __forceinline__ float divide(float x, float y, float inv) {
   return __fmaf_rn(__fmaf_rn(-q, y, x), inv, q);
 }
 
-// 16 of a group's 64 values (4 neighbouring lanes) as codes; sz: its (scale, zero) pair.
-__device__ __forceinline__ uint2 quantise16(const float (&x)[16], uint32_t& sz) {
-  float lo = x[0], hi = x[0];
+// A lane's 16 values of a row as codes, dims 8l .. 8l + 7 in codes[0] and D / 2 on in codes[1]; sz: a (scale, zero) pair.
+// d = 64: one group in 4 lanes. Above: the two eights lie in two groups of 8 lanes; lanes 0 to 3 of the eight finish the
+// first one's least and greatest value, scale and reciprocal, lanes 4 to 7 the second's, and they swap what they found.
+template <int D>
+__device__ __forceinline__ void quantise16(const uint64_t (&x)[8], uint32_t (&codes)[2], uint32_t& sz) {
+  constexpr bool TWO = D > 64;
+  float lo[2], hi[2];
 #pragma unroll
-  for (int i = 1; i < 16; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
+  for (int s = 0; s < 2; ++s) {
+    float a, b;
+    f2_unpack(x[4 * s], a, b);
+    lo[s] = fminf(a, b), hi[s] = fmaxf(a, b);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+      f2_unpack(x[4 * s + i], a, b);
+      lo[s] = fmin3(lo[s], a, b), hi[s] = fmax3(hi[s], a, b);
+    }
+  }
+  const bool second = TWO && (threadIdx.x & 4);
+  float least, greatest;
+  if (TWO) {
+    least = fminf(second ? lo[1] : lo[0], __shfl_xor_sync(0xffffffffu, second ? lo[0] : lo[1], 4));
+    greatest = fmaxf(second ? hi[1] : hi[0], __shfl_xor_sync(0xffffffffu, second ? hi[0] : hi[1], 4));
+  } else {
+    least = fminf(lo[0], lo[1]), greatest = fmaxf(hi[0], hi[1]);
   }
 #pragma unroll
   for (int o = 2; o > 0; o >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+    greatest = fmaxf(greatest, __shfl_xor_sync(0xffffffffu, greatest, o));
   }
-  const float zero = bf16_toward<false>(lo);
-  const float least = fmaxf(fmaxf(fabsf(lo), fabsf(hi)) * 0x1p-20f, 0x1p-100f);
-  const float scale = bf16_toward<true>(fmaxf(divide(__fsub_rn(hi, zero), 15.f, 1.f / 15.f), least));
-  sz = (__float_as_uint(scale) >> 16) | (__float_as_uint(zero) & 0xffff0000u);
-  // 0 <= quotient <= 15, as scale >= (hi - zero) / 15. Adding 2^23 rounds it to a whole number, which then stands in the
-  // low bits; the exponents that the sum of the shifted words carries with it are taken off at the end.
+  const float zero = bf16_toward<false>(least);
+  const float floor = fmaxf(fmaxf(fabsf(least), fabsf(greatest)) * 0x1p-20f, 0x1p-100f);
+  const float scale = bf16_toward<true>(fmaxf(divide(__fsub_rn(greatest, zero), 15.f, 1.f / 15.f), floor));
   const float inv = __frcp_rn(scale);
-  uint32_t codes[2] = {0, 0}, exponents = 0;
-#pragma unroll
-  for (int i = 7; i >= 0; --i) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-      codes[s] = codes[s] * 16 + __float_as_uint(__fadd_rn(divide(__fsub_rn(x[8 * s + i], zero), scale, inv), 0x1p23f));
-    exponents = exponents * 16 + 0x4b000000u;
+  sz = (__float_as_uint(scale) >> 16) | (__float_as_uint(zero) & 0xffff0000u);
+  uint32_t sz_of[2] = {sz, sz};
+  float inv_of[2] = {inv, inv};
+  if (TWO) {
+    const uint32_t o_sz = __shfl_xor_sync(0xffffffffu, sz, 4);
+    const float o_inv = __shfl_xor_sync(0xffffffffu, inv, 4);
+    sz_of[0] = second ? o_sz : sz, sz_of[1] = second ? sz : o_sz;
+    inv_of[0] = second ? o_inv : inv, inv_of[1] = second ? inv : o_inv;
   }
-  return make_uint2(codes[0] - exponents, codes[1] - exponents);
+  // 0 <= quotient <= 15, as scale >= (greatest - zero) / 15. Adding 2^23 rounds it to a whole number, which then stands in
+  // the low bits; the exponents that the sum of the shifted words carries with it are taken off at the end.
+  const uint64_t whole2 = f2_pack(0x1p23f, 0x1p23f);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const float z = __uint_as_float(sz_of[s] & 0xffff0000u), m = -__uint_as_float(sz_of[s] << 16);
+    const uint64_t zero2 = f2_pack(z, z), inv2 = f2_pack(inv_of[s], inv_of[s]), minus_scale2 = f2_pack(m, m);
+    uint32_t word = 0, exponents = 0;
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+      // divide() by the scale, two at a time: the remainder is x - q scale = q (-scale) + x
+      const uint64_t n = f2_sub(x[4 * s + i], zero2), q = f2_mul(n, inv2);
+      float even, odd;
+      f2_unpack(f2_add(f2_fma(f2_fma(q, minus_scale2, n), inv2, q), whole2), even, odd);
+      word = (word * 16 + __float_as_uint(odd)) * 16 + __float_as_uint(even);
+      exponents = (exponents * 16 + 0x4b000000u) * 16 + 0x4b000000u;
+    }
+    codes[s] = word - exponents;
+  }
 }
 
 // Where position pos of sequence b lies, or false where the table does not lead into the pool.
@@ -130,26 +179,28 @@ __device__ __forceinline__ bool find_row(const PagedCache& c, const FastDiv& pag
   return page >= 0 && page < c.num_pages;
 }
 
-// d / 16 lanes hold a row; a task is one head of one token, key and value.
-template <int D, bool INT4, bool INTERLEAVED>
+enum Rope { kNone, kFull, kPart, kInterleaved };   // rotation: none, of half-split pairs over the row or a part, of neighbours
+
+// d / 16 lanes hold a row, dims 8l .. 8l + 7 and d / 2 on each (the pairs of a fully turned row, and loads and stores of
+// whole sectors); a task is one head of one token, key and value.
+template <int D, bool INT4, int ROPE>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendParams p) {
   constexpr int LPR = D / 16;
   const int l = threadIdx.x % LPR;
   const uint32_t task = blockIdx.x * (uint32_t)(kThreads / LPR) + threadIdx.x / LPR, token = task / p.parts;
   const int t = min(token, (uint32_t)p.total - 1u), h = task - token * p.parts.v;
   bool good = token < (uint32_t)p.total;
-  // This lane's dims in eights, 16l and 16l + 8, and for each where the values begin that they are paired with.
   const __nv_bfloat16 *k = p.k + t * p.k_st + h * p.k_sh, *v = p.v + t * p.v_st + h * p.v_sh;
   uint4 raw[2][2], raw_mate[2];
   bool turned[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    const int d0 = 16 * l + 8 * s;
+    const int d0 = 8 * l + s * (D / 2);
     raw[0][s] = *reinterpret_cast<const uint4*>(k + d0);
     raw[1][s] = *reinterpret_cast<const uint4*>(v + d0);
-    turned[s] = p.cos && d0 < p.rope_dim;
+    turned[s] = ROPE != kNone && (ROPE == kFull || d0 < p.rope_dim);
     raw_mate[s] = make_uint4(0, 0, 0, 0);
-    if (!INTERLEAVED && turned[s])
+    if (ROPE == kPart && turned[s])
       raw_mate[s] = *reinterpret_cast<const uint4*>(k + (d0 < p.half ? d0 + p.half : d0 - p.half));
   }
   const int b = find_sequence<LPR>(p.cu, p.B, t);
@@ -166,42 +217,52 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
     good = good && in;
     if (!in) pos = 0;
   }
-  float y[2][16];   // key, value
+  uint64_t y[2][8];   // key, value
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    float x[8], m[8], cs[8], sn[8];
-    unpack8(x, raw[1][s]);
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[1][8 * s + j] = x[j];
-    unpack8(x, raw[0][s]);
-    if (turned[s]) {
-      // pair of dim j: j mod half, or j / 2 when interleaved
-      const int d0 = 16 * l + 8 * s, pair = INTERLEAVED ? d0 / 2 : (d0 < p.half ? d0 : d0 - p.half);
+    for (int s = 0; s < 2; ++s) unpack8(y[i] + 4 * s, raw[i][s]);
+  if constexpr (ROPE == kFull) {
+    uint64_t cs[4], sn[4];
+    load8(cs, p.cos + (long long)pos * (D / 2) + 8 * l);
+    load8(sn, p.sin + (long long)pos * (D / 2) + 8 * l);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t a = y[0][j], b = y[0][4 + j];
+      y[0][j] = f2_sub(f2_mul(a, cs[j]), f2_mul(b, sn[j]));
+      y[0][4 + j] = f2_add(f2_mul(b, cs[j]), f2_mul(a, sn[j]));
+    }
+  } else if constexpr (ROPE != kNone) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (!turned[s]) continue;
+      // x cos -+ mate sin. Pair of dim j: j mod half, or j / 2 when interleaved
+      const int d0 = 8 * l + s * (D / 2), pair = ROPE == kInterleaved ? d0 / 2 : (d0 < p.half ? d0 : d0 - p.half);
       const float* ct = p.cos + (long long)pos * p.half + pair;
       const float* st = p.sin + (long long)pos * p.half + pair;
-#pragma unroll
-      for (int i = 0; i < (INTERLEAVED ? 4 : 8); i += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(ct + i), b = *reinterpret_cast<const float4*>(st + i);
-        cs[i] = a.x, cs[i + 1] = a.y, cs[i + 2] = a.z, cs[i + 3] = a.w;
-        sn[i] = b.x, sn[i + 1] = b.y, sn[i + 2] = b.z, sn[i + 3] = b.w;
-      }
-      if (INTERLEAVED) {
+      uint64_t* x = y[0] + 4 * s;
+      uint64_t m[4], cs[4], sn[4], sign;
+      if constexpr (ROPE == kInterleaved) {
+        const float4 a = *reinterpret_cast<const float4*>(ct), b = *reinterpret_cast<const float4*>(st);
+        const float ca[4] = {a.x, a.y, a.z, a.w}, sa[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float u = x[2 * j], w = x[2 * j + 1];
-          x[2 * j] = __fsub_rn(__fmul_rn(u, cs[j]), __fmul_rn(w, sn[j]));
-          x[2 * j + 1] = __fadd_rn(__fmul_rn(w, cs[j]), __fmul_rn(u, sn[j]));
+          float u, w;
+          f2_unpack(x[j], u, w);
+          m[j] = f2_pack(w, u), cs[j] = f2_pack(ca[j], ca[j]), sn[j] = f2_pack(sa[j], sa[j]);
         }
+        sign = f2_pack(-1.f, 1.f);
       } else {
+        load8(cs, ct);
+        load8(sn, st);
         unpack8(m, raw_mate[s]);
-        // the first half subtracts: a product with the sine's sign turned has the other sign, bit for bit
-        const float sign = d0 < p.half ? -1.f : 1.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __fadd_rn(__fmul_rn(x[j], cs[j]), __fmul_rn(m[j], __fmul_rn(sn[j], sign)));
+        const float first = d0 < p.half ? -1.f : 1.f;
+        sign = f2_pack(first, first);
       }
-    }
+      // both products rounded, then their sum or difference (a product with +-1 is exact)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[0][8 * s + j] = x[j];
+      for (int j = 0; j < 4; ++j) x[j] = f2_fma(f2_mul(m[j], sn[j]), sign, f2_mul(x[j], cs[j]));
+    }
   }
   const PagedCache& c = p.c;
   const long long row = page * c.page_b + at * c.token_b + h * c.head_b;
@@ -209,21 +270,19 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
   for (int i = 0; i < 2; ++i) {
     uint8_t* base = (i ? c.v : c.k) + row;
     if constexpr (INT4) {
-      uint32_t sz;
-      const uint2 codes = quantise16(y[i], sz);
+      uint32_t sz, codes[2];
+      quantise16<D>(y[i], codes, sz);
       if (good) {
-        *reinterpret_cast<uint2*>(base + 8 * l) = codes;
+        *reinterpret_cast<uint32_t*>(base + 4 * l) = codes[0];
+        *reinterpret_cast<uint32_t*>(base + D / 4 + 4 * l) = codes[1];
         const long long sz_row = page * c.sz_page_b + at * c.sz_token_b + h * c.sz_head_b;
-        if (l % 4 == 0) *reinterpret_cast<uint32_t*>((i ? c.v_sz : c.k_sz) + sz_row + l) = sz;
+        const int group = D == 64 ? 0 : l / 8 + (l & 4 ? D / 128 : 0);
+        if (l % 4 == 0) *reinterpret_cast<uint32_t*>((i ? c.v_sz : c.k_sz) + sz_row + 4 * group) = sz;
       }
     } else if (good) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {   // values no rotation touches keep their bits
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = y[i][8 * s + j];
-        *reinterpret_cast<uint4*>(base + 32 * l + 16 * s) = i == 0 && turned[s] ? pack8(x) : raw[i][s];
-      }
+      for (int s = 0; s < 2; ++s)   // values no rotation touches keep their bits
+        *reinterpret_cast<uint4*>(base + D * s + 16 * l) = i == 0 && turned[s] ? pack8(y[i] + 4 * s) : raw[i][s];
     }
   }
 }
@@ -302,8 +361,10 @@ template <int D, bool INT4>
 cudaError_t launch_append(const AppendParams& p, bool interleaved, cudaStream_t s) {
   const unsigned rows = kThreads / (D / 16);
   const unsigned grid = ((unsigned)p.total * p.parts.v + rows - 1) / rows;
-  if (interleaved) paged_append_kernel<D, INT4, true><<<grid, kThreads, 0, s>>>(p);
-  else paged_append_kernel<D, INT4, false><<<grid, kThreads, 0, s>>>(p);
+  if (!p.cos) paged_append_kernel<D, INT4, kNone><<<grid, kThreads, 0, s>>>(p);
+  else if (interleaved) paged_append_kernel<D, INT4, kInterleaved><<<grid, kThreads, 0, s>>>(p);
+  else if (p.rope_dim == D) paged_append_kernel<D, INT4, kFull><<<grid, kThreads, 0, s>>>(p);
+  else paged_append_kernel<D, INT4, kPart><<<grid, kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
