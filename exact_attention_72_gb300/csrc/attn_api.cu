@@ -289,11 +289,12 @@ cudaError_t dispatch_d(gb300::LaunchArgs& a, bool causal, bool fp8, cudaStream_t
 
 }  // namespace
 
-bool gb300::device_state(int* num_sms, uint32_t** status) {
+bool gb300::device_state(int* num_sms, uint32_t** status, unsigned long long* context) {
   DeviceInfo* di = device_info();
   if (!di) return false;
   *num_sms = di->num_sms;
   *status = di->status;
+  if (context) *context = di->ctx;
   return true;
 }
 

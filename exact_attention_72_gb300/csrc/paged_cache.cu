@@ -6,14 +6,16 @@
 // attn_paged_gather: rows 0 .. n_b - 1 of every sequence into packed bf16 k and v, the layout the
 // ragged-batch forward reads.
 //
-// A lane reads the values that its own are paired with from the same row (a second load of a line already in L1) instead
-// of exchanging them, and a group of 64 values is 4 neighbouring lanes, so its least and greatest value take two
-// exchanges. Rotation and quantisation round every step as written here (no contraction into fused multiply-adds): a
-// code must not depend on how the compiler schedules, or a value at a border between two codes would change with it.
+// A lane holds 8 values of a row's first half and the 8 half a row on: the pairs of a fully turned row lie in one lane,
+// and loads and stores are whole sectors (16 neighbouring values a lane took 14.1 instead of 11.8 us for 12.4k bf16 tokens).
+// Rows turned in part read the paired values a second time, out of L1. Rotation and quantisation round every step as
+// written here (no contraction into fused multiply-adds): a code must not depend on how the compiler schedules, or a value
+// at a border between two codes would change with it.
 //
-// Measured on a GB300, 8 kv heads, d 128, 4 bits: append of 12.4k tokens 24.5 us (66 MB; arithmetic and the chain of
-// offsets, page and angles; 49 us with IEEE divisions and 8 values a lane), gather of 29.4k tokens 24.4 us (154 MB, 93% of
-// the copy bandwidth; 29.5 us with values converted one by one).
+// Measured on a GB300, 8 kv heads, d 128, 4 bits: append of 12.4k tokens 20 us (66 MB; arithmetic, 60% of the issue slots,
+// and the chain of offsets, page and angles; 49 us with IEEE divisions, 24.5 us one value an instruction), gather of 29.4k
+// tokens 24.4 us (154 MB, 93% of the copy bandwidth; 29.5 us with values converted one by one). Two heads a lane, sharing
+// the look-ups, are no faster (45.3 against 44.7 us for both), nor are more CTAs an SM.
 #include <algorithm>
 #include <climits>
 
