@@ -53,6 +53,7 @@
 #include "ops.h"
 #include "paged.cuh"
 #include "paged_host.h"
+#include "ptx.cuh"
 
 namespace gb300 {
 namespace {
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
   __shared__ Cursor s_cursor[kWarps];     // here, not in registers: needed once a unit
   __shared__ int s_id[kWarps], s_open[kWarps];
   __shared__ float s_m[kWarps][C::ROWS], s_l[kWarps][C::ROWS];
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // launched early: what it reads may be a previous kernel's
+  griddep_wait();   // launched early: what it reads may be a previous kernel's
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int per_seq = p.c.Hkv * p.row_blocks;   // units of a sequence
 
@@ -855,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
     copies_wait<0>();
   }
   // The joining kernel's CTAs may take the room that CTAs of this one leave; they wait for all of its results.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  griddep_launch_dependents();
   __syncthreads();
 
   // Warps [w0, w1) of this CTA whose shares end in one unit.
@@ -913,7 +914,7 @@ constexpr int kFewParts = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params p, int rows_per_unit) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  griddep_wait();
   constexpr int LANES = D / 4;                // lanes of a row
   constexpr int STEP = LANES < 32 ? LANES : 32, V = LANES / STEP, WAYS = 32 / STEP;   // of a warp: values each, rows at once
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, c = lane % STEP * 4, way = lane / STEP, r = blockIdx.y;
@@ -1068,21 +1069,9 @@ cudaError_t launch(const Params& p, int grid, unsigned long long context, cudaSt
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
     set_for.store(context, std::memory_order_relaxed);
   }
-  // Both are programmatic dependents: their CTAs are scheduled while the kernel before still runs, and wait for it.
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.dynamicSmemBytes = C::SMEM;
-  if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)std::min(C::ROWS, p.Nq * p.G));
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<C::D>, p, C::ROWS);
+  if ((e = launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreads), C::SMEM, s, p)) != cudaSuccess) return e;
+  return launch_dependent(attn_paged_join_kernel<C::D>, dim3((unsigned)grid, (unsigned)std::min(C::ROWS, p.Nq * p.G)),
+                          dim3(kThreads), 0, s, p, (int)C::ROWS);
 }
 
 template <int D, bool INT4>

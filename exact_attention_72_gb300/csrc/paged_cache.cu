@@ -187,6 +187,8 @@ enum Rope { kNone, kFull, kPart, kInterleaved };   // rotation: none, of half-sp
 // whole sectors); a task is one head of one token, key and value.
 template <int D, bool INT4, int ROPE>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendParams p) {
+  griddep_wait();
+  griddep_launch_dependents();   // of the next kernel only the launch may overlap: it waits for this one's end
   constexpr int LPR = D / 16;
   const int l = threadIdx.x % LPR;
   const uint32_t task = blockIdx.x * (uint32_t)(kThreads / LPR) + threadIdx.x / LPR, token = task / p.parts;
@@ -308,6 +310,8 @@ __device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t sz) {
 
 template <int D, bool INT4>
 __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const GatherParams p) {
+  griddep_wait();
+  griddep_launch_dependents();   // of the next kernel only the launch may overlap: it waits for this one's end
   constexpr int LPR = D / 8;
   const int l = threadIdx.x % LPR;
   const uint32_t task = blockIdx.x * (uint32_t)(kThreads / LPR) + threadIdx.x / LPR, token = task / p.parts;
@@ -363,18 +367,18 @@ template <int D, bool INT4>
 cudaError_t launch_append(const AppendParams& p, bool interleaved, cudaStream_t s) {
   const unsigned rows = kThreads / (D / 16);
   const unsigned grid = ((unsigned)p.total * p.parts.v + rows - 1) / rows;
-  if (!p.cos) paged_append_kernel<D, INT4, kNone><<<grid, kThreads, 0, s>>>(p);
-  else if (interleaved) paged_append_kernel<D, INT4, kInterleaved><<<grid, kThreads, 0, s>>>(p);
-  else if (p.rope_dim == D) paged_append_kernel<D, INT4, kFull><<<grid, kThreads, 0, s>>>(p);
-  else paged_append_kernel<D, INT4, kPart><<<grid, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  auto kernel = !p.cos          ? paged_append_kernel<D, INT4, kNone>
+                : interleaved     ? paged_append_kernel<D, INT4, kInterleaved>
+                : p.rope_dim == D ? paged_append_kernel<D, INT4, kFull>
+                                  : paged_append_kernel<D, INT4, kPart>;
+  return launch_dependent(kernel, dim3(grid), dim3(kThreads), 0, s, p);
 }
 
 template <int D, bool INT4>
 cudaError_t launch_gather(const GatherParams& p, cudaStream_t s) {
   const unsigned rows = kThreads / (D / 8);
-  paged_gather_kernel<D, INT4><<<((unsigned)p.total * p.parts.v + rows - 1) / rows, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  const unsigned grid = ((unsigned)p.total * p.parts.v + rows - 1) / rows;
+  return launch_dependent(paged_gather_kernel<D, INT4>, dim3(grid), dim3(kThreads), 0, s, p);
 }
 
 }  // namespace

@@ -28,6 +28,7 @@
 #include "fastdiv.cuh"
 #include "ops.h"
 #include "paged.cuh"
+#include "ptx.cuh"
 
 namespace gb300 {
 namespace {
@@ -167,6 +168,8 @@ __device__ __forceinline__ Chunks load_weights(const float* w, int da, int db, b
 // way while it turns those of this one, so that loads are always in flight.
 template <int D, bool NORM, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, kFwdCtasPerSm) qk_norm_rope_kernel(const NormRopeParams p) {
+  griddep_wait();
+  griddep_launch_dependents();   // of the next kernel only the launch may overlap: it waits for this one's end
   constexpr int LPR = D / 8, ROWS = kThreads / LPR;
   const int l = threadIdx.x % LPR;
   int da, db;
@@ -233,6 +236,8 @@ __global__ void __launch_bounds__(kThreads, kFwdCtasPerSm) qk_norm_rope_kernel(c
 // [d] in part, which dw_kernel adds up: the same bits every time.
 template <int D, bool NORM, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kernel(const NormRopeParams p) {
+  griddep_wait();
+  griddep_launch_dependents();   // of the next kernel only the launch may overlap: it waits for this one's end
   constexpr int LPR = D / 8, ROWS = kThreads / LPR;
   const int l = threadIdx.x % LPR, slot = threadIdx.x / LPR;
   const bool is_k = blockIdx.x >= (unsigned)p.ctas_q;
@@ -331,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kern
 // dw[i] = sum over CTAs of part[cta][i]; block x is 32 dims of q's (y = 0) or k's (y = 1) weight.
 __global__ void __launch_bounds__(1024) dw_kernel(const float* __restrict__ part, float* dwq, float* dwk, int d,
                                                   int ctas_q, int ctas) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  griddep_wait();
   float* dw = blockIdx.y ? dwk : dwq;
   if (!dw) return;
   const int first = blockIdx.y ? ctas_q : 0, last = blockIdx.y ? ctas : ctas_q;
@@ -353,26 +358,16 @@ template <int D>
 cudaError_t launch_forward(const NormRopeParams& p, bool norm, bool interleaved, int sms, cudaStream_t s) {
   const long long tasks = (long long)p.T * (p.parts_q + p.parts_k), rows = kThreads / (D / 8);
   const unsigned grid = (unsigned)std::min<long long>((tasks + rows - 1) / rows, (long long)kFwdCtasPerSm * sms);
-  if (norm) {
-    if (interleaved) qk_norm_rope_kernel<D, true, true><<<grid, kThreads, 0, s>>>(p);
-    else qk_norm_rope_kernel<D, true, false><<<grid, kThreads, 0, s>>>(p);
-  } else {
-    if (interleaved) qk_norm_rope_kernel<D, false, true><<<grid, kThreads, 0, s>>>(p);
-    else qk_norm_rope_kernel<D, false, false><<<grid, kThreads, 0, s>>>(p);
-  }
-  return cudaGetLastError();
+  auto kernel = norm ? (interleaved ? qk_norm_rope_kernel<D, true, true> : qk_norm_rope_kernel<D, true, false>)
+                     : (interleaved ? qk_norm_rope_kernel<D, false, true> : qk_norm_rope_kernel<D, false, false>);
+  return launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, p);
 }
 
 template <int D>
 cudaError_t launch_backward(const NormRopeParams& p, bool norm, bool interleaved, int grid, cudaStream_t s) {
-  if (norm) {
-    if (interleaved) qk_norm_rope_bwd_kernel<D, true, true><<<grid, kThreads, 0, s>>>(p);
-    else qk_norm_rope_bwd_kernel<D, true, false><<<grid, kThreads, 0, s>>>(p);
-  } else {
-    if (interleaved) qk_norm_rope_bwd_kernel<D, false, true><<<grid, kThreads, 0, s>>>(p);
-    else qk_norm_rope_bwd_kernel<D, false, false><<<grid, kThreads, 0, s>>>(p);
-  }
-  return cudaGetLastError();
+  auto kernel = norm ? (interleaved ? qk_norm_rope_bwd_kernel<D, true, true> : qk_norm_rope_bwd_kernel<D, true, false>)
+                     : (interleaved ? qk_norm_rope_bwd_kernel<D, false, true> : qk_norm_rope_bwd_kernel<D, false, false>);
+  return launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, p);
 }
 
 // CTAs of the backward: one wave, shared between q and k by their tasks.
@@ -564,16 +559,8 @@ extern "C" attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, con
     default: e = launch_backward<256>(p, norm != 0, interleaved != 0, g.ctas, stream); break;
   }
   if (e == cudaSuccess && dw) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)d / 32, 2);
-    cfg.blockDim = dim3(32, 32);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, dw_kernel, (const float*)p.part, dwq, dwk, d, g.ctas_q, g.ctas);
+    e = launch_dependent(dw_kernel, dim3((unsigned)d / 32, 2), dim3(32, 32), 0, stream, (const float*)p.part, dwq, dwk, d,
+                         g.ctas_q, g.ctas);
   }
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
