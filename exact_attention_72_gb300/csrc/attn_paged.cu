@@ -31,10 +31,10 @@
 //
 // Measured on a GB300 (us in a CUDA graph, share of the copy bandwidth; H 32, Hkv 8, d 128 if not said otherwise):
 //   bf16, B 8, 16384 keys                85    93%
-//   4 bits, B 8, 16384 keys              36    62%: about 5 us until the first tiles are there and 5 us to join the parts;
+//   4 bits, B 8, 16384 keys              35    63%: about 5 us until the first tiles are there and 5 us to join the parts;
 //                                              between them the tiles stream at 99%
 //   4 bits, B 32, up to 32768 keys      102    82%
-//   bf16, d 256, B 13, up to 5000 keys, 12 rows (two blocks, the second out of L2)  34    52%
+//   bf16, d 256, B 13, up to 5000 keys, 12 rows (two blocks, the second out of L2)  35    51%
 // What it took, at B 8 and 16384 keys in 4 bits: tiles of one CTA with lane-wise operand loads 61; pages looked up once a
 // tile 48.6; matrix loads, shares by warp, a vote instead of the maximum's exchanges 40; one wave of shorter launches 36.
 #include <algorithm>
@@ -907,37 +907,45 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
   }
 }
 
-// Joins the parts of the units that were cut: CTA (c, r) takes row r of the units that begin in warps of CTA c, a warp
-// one of them if it has few parts, all four warps together otherwise.
+// Joins the parts of the units that were cut: CTA (c, r) takes row r of the units that begin in warps c span to
+// (c + 1) span - 1 of the grid before. With a unit a warp or so (span = kWarps, "alone") a warp takes one if it has few
+// parts; otherwise the four warps share the parts of one after the other.
 // LSE = log2 sum 2^LSE_i,  O = sum 2^(LSE_i - LSE) O_i.
 constexpr int kFewParts = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params p, int rows_per_unit) {
+__global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params p, int rows_per_unit, int span, int records) {
   griddep_wait();
   constexpr int LANES = D / 4;                // lanes of a row
   constexpr int STEP = LANES < 32 ? LANES : 32, V = LANES / STEP, WAYS = 32 / STEP;   // of a warp: values each, rows at once
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, c = lane % STEP * 4, way = lane / STEP, r = blockIdx.y;
-  auto cut_of = [&](int k) {
-    const int4 cut = p.cut[blockIdx.x * kWarps + k];
-    return cut.z >= 0 && cut.y % p.row_blocks * rows_per_unit + r < p.Nq * p.G ? cut : make_int4(0, 0, -1, 0);
+  struct Cut {
+    int4 cut;
+    int from;   // the warp that it begins in
   };
-  // Parts of a unit that begins in warp k: slot 2 first + 1, one of each later CTA's first warp, and of the last warp its
+  __shared__ Cut cuts[kThreads];   // units left to the whole CTA, in order
+  __shared__ int counts[kWarps];
+  const bool alone = span == kWarps;   // a record a warp
+  Cut own{make_int4(0, 0, -1, 0), (int)(blockIdx.x * span + (alone ? warp : threadIdx.x))};
+  if ((alone || (int)threadIdx.x < span) && own.from < records) own.cut = p.cut[own.from];
+  bool mine = own.cut.z >= 0 && own.cut.y % p.row_blocks * rows_per_unit + r < p.Nq * p.G;
+  // Parts of a unit that begins in warp `from`: slot 2 from + 1, one of each later CTA's first warp, and of the last warp its
   // slot for a unit that ends inside a share (then the last CTA's first warp has one only if it is not that warp).
-  auto joined_of = [&](const int4& cut) {
-    return max(cut.z / kWarps - (int)blockIdx.x - (cut.w && cut.z % kWarps == 0 ? 1 : 0), 0);
+  auto joined_of = [&](const Cut& x) {
+    return max(x.cut.z / kWarps - x.from / kWarps - (x.cut.w && x.cut.z % kWarps == 0 ? 1 : 0), 0);
+  };
+  auto parts_of = [&](const Cut& x) { return 1 + joined_of(x) + x.cut.w; };
+  auto slot_of = [&](const Cut& x, int joined, int i) -> long long {
+    return i == 0 ? 2LL * x.from + 1 : i <= joined ? 2LL * kWarps * (x.from / kWarps + i) + 1 : 2LL * x.cut.z;
   };
   // Parts first, first + stride, .. of a unit: their weighted sums for this lane, and the weights'.
   struct Sum {
     float top, sum;
     float4 x[V];
   };
-  auto gather = [&](const int4& cut, int k, int first, int stride) {
-    const int joined = joined_of(cut), parts = 1 + joined + cut.w, from = blockIdx.x * kWarps + k;
-    auto at = [&](int i) -> long long {
-      const long long slot = i == 0 ? 2LL * from + 1 : i <= joined ? 2LL * kWarps * (blockIdx.x + i) + 1 : 2LL * cut.z;
-      return slot * rows_per_unit + r;
-    };
+  auto gather = [&](const Cut& x, int first, int stride) {
+    const int joined = joined_of(x), parts = parts_of(x);
+    auto at = [&](int i) -> long long { return slot_of(x, joined, i) * rows_per_unit + r; };
     Sum s{-INFINITY, 0.f, {}};
     bool any = false;   // a part that has keys, or is NaN
     for (int i = lane; i < parts; i += 32) {
@@ -983,14 +991,13 @@ __global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params 
       p.lse[((long long)cut.x * p.H + h) * p.Nq + qi] = s.sum != 0.f ? (s.top + log2f(s.sum)) * 0.69314718055994531f : -INFINITY;
   };
   // A few parts: everything is loaded at once.
-  auto gather_few = [&](const int4& cut, int k) {
-    const int joined = joined_of(cut), parts = 1 + joined + cut.w, from = blockIdx.x * kWarps + k;
+  auto gather_few = [&](const Cut& cut) {
+    const int joined = joined_of(cut), parts = parts_of(cut);
     float lse[kFewParts];
     float4 x[kFewParts][V];
 #pragma unroll
     for (int i = 0; i < kFewParts; ++i) {
-      const long long slot = i == 0 ? 2LL * from + 1 : i <= joined ? 2LL * kWarps * (blockIdx.x + i) + 1 : 2LL * cut.z;
-      const long long at = slot * rows_per_unit + r;
+      const long long at = slot_of(cut, joined, i) * rows_per_unit + r;
       lse[i] = i < parts ? p.part_lse[at] : -INFINITY;
 #pragma unroll
       for (int v = 0; v < V; ++v)
@@ -1013,15 +1020,28 @@ __global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params 
     }
     return s;
   };
-  const int4 mine = cut_of(warp);
-  const bool many = mine.z >= 0 && 1 + joined_of(mine) + mine.w > kFewParts;
-  if (mine.z >= 0 && !many) store(mine, gather_few(mine, warp));
-  if (!__syncthreads_or(many)) return;
+  if (alone) {
+    if (mine && parts_of(own) <= kFewParts) {
+      store(own.cut, gather_few(own));
+      mine = false;
+    }
+    mine = mine && lane == 0;
+  }
+  const uint32_t ballot = __ballot_sync(0xffffffffu, mine);
+  if (lane == 0) counts[warp] = __popc(ballot);
+  if (!__syncthreads_or(mine)) return;
+  int n = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    before += w < warp ? counts[w] : 0;
+    n += counts[w];
+  }
+  if (mine) cuts[before + __popc(ballot & ((1u << lane) - 1u))] = own;
+  __syncthreads();
   __shared__ Sum sums[kWarps][32];
-  for (int k = 0; k < kWarps; ++k) {
-    const int4 cut = cut_of(k);   // the same for the whole CTA
-    if (cut.z < 0 || 1 + joined_of(cut) + cut.w <= kFewParts) continue;
-    sums[warp][lane] = gather(cut, k, warp, kWarps);
+  for (int i = 0; i < n; ++i) {   // the same for the whole CTA
+    const Cut x = cuts[i];
+    sums[warp][lane] = gather(x, warp, kWarps);
     __syncthreads();
     if (warp == 0) {
       Sum s = sums[0][lane];
@@ -1031,7 +1051,7 @@ __global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params 
 #pragma unroll
         for (int v = 0; v < V; ++v) add(s.x[v], 1.f, y.x[v]);
       }
-      store(cut, s);
+      store(x.cut, s);
     }
     __syncthreads();   // the sums are free again
   }
@@ -1070,8 +1090,15 @@ cudaError_t launch(const Params& p, int grid, unsigned long long context, cudaSt
     set_for.store(context, std::memory_order_relaxed);
   }
   if ((e = launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreads), C::SMEM, s, p)) != cudaSuccess) return e;
-  return launch_dependent(attn_paged_join_kernel<C::D>, dim3((unsigned)grid, (unsigned)std::min(C::ROWS, p.Nq * p.G)),
-                          dim3(kThreads), 0, s, p, (int)C::ROWS);
+  // At most a unit a CTA, as a rule: with few units most warps begin none, and CTAs that find nothing cost more than a look at
+  // more warps does (B 4, one kv head, 12 rows, 6161 keys: 13.5 us with 4 warps a CTA always, 11.3 so; twice or four times
+  // as many warps a CTA leave some with two units, one after the other, 1 us more at B 2).
+  const int records = grid * kWarps;
+  const long long units = (long long)p.B * p.c.Hkv * p.row_blocks;
+  const int span = (int)std::clamp<long long>(records / (4 * units), kWarps, kThreads);
+  return launch_dependent(attn_paged_join_kernel<C::D>,
+                          dim3((unsigned)((records + span - 1) / span), (unsigned)std::min(C::ROWS, p.Nq * p.G)),
+                          dim3(kThreads), 0, s, p, (int)C::ROWS, span, records);
 }
 
 template <int D, bool INT4>
