@@ -81,15 +81,17 @@ Rows rows_of(const at::Tensor& t, const char* name) {
   if (t.scalar_type() != at::kBFloat16 || (n != 3 && n != 4) || t.stride(n - 1) != 1)
     refuse(std::string(name) + " must be a bfloat16 CUDA tensor [T, heads, d] or [B, N, heads, d] with contiguous rows");
   Rows r;
-  r.heads = t.size(n - 2), r.d = t.size(n - 1), r.sh = t.stride(n - 2);
+  r.heads = t.size(n - 2), r.d = t.size(n - 1);
+  r.sh = r.heads > 1 ? t.stride(n - 2) : r.d;   // a stride of one head or one token says nothing
   if (n == 3) {
     r.T = r.N = t.size(0), r.st = t.stride(0);
-    return r;
+  } else {
+    const int64_t B = t.size(0);
+    r.N = t.size(1), r.T = B * r.N, r.st = r.N == 1 ? t.stride(0) : t.stride(1);
+    if (r.N > 1 && B > 1 && t.stride(0) != r.N * t.stride(1))
+      refuse(std::string("the tokens of ") + name + " must be evenly spaced over the batch");
   }
-  const int64_t B = t.size(0);
-  r.N = t.size(1), r.T = B * r.N, r.st = r.N == 1 ? t.stride(0) : t.stride(1);
-  if (r.N != 1 && B > 1 && t.stride(0) != r.N * t.stride(1))
-    refuse(std::string("the tokens of ") + name + " must be evenly spaced over the batch");
+  if (r.T == 1) r.st = r.heads * r.d;
   return r;
 }
 

@@ -571,3 +571,68 @@ def test_every_number_of_keys_around_the_tiles():
         for b in range(0, 140, 13):
             o1, lse1 = attend(q[b:b + 1], cache, table[b:b + 1], lens[b:b + 1])
             check(q[b:b + 1], o1, lse1, keys[b:b + 1], vals[b:b + 1], 0.125, True, kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int4"])
+@pytest.mark.parametrize("d,H,Nq,lens", [
+    (128, 8, 1, [30000, 33, 500, 70, 900, 0, 40, 1200]),    # one over nearly all warps, several cut in the rest
+    (64, 4, 3, [9000, 700, 2, 650]),                        # 12 rows
+    (256, 3, 1, [5000, 4000, 17, 3000]),
+    (64, 20, 1, [4000]),                                    # two units
+])
+def test_few_units_of_any_length(kind, d, H, Nq, lens):
+    """One kv head: few units for all warps, so a CTA of the joining kernel looks through many of them, and may find several."""
+    table, pages = make_table(lens, 16, 13)
+    cache = make_cache(kind, pages, 16, 1, d)
+    keys, vals = fill(cache, table, lens, 14)
+    q = randn((len(lens), Nq, H, d), 15, 2.0)
+    o, lse = attend(q, cache, table, lens)
+    check(q, o, lse, keys, vals, d ** -0.5, True, kind)
+
+
+def test_calls_of_two_threads_at_once():
+    """Each on a stream of its own, with its own cache; the results are those of calls one after the other."""
+    import threading
+    lens = [700, 45, 3000]
+    table, pages = make_table(lens, 16, 3)
+    jobs = []
+    for seed in (1, 2):
+        cache = make_cache("int4", pages, 16, 2, 128)
+        fill(cache, table, lens, seed)
+        q = randn((3, 1, 8, 128), seed + 5)
+        jobs.append((cache, q, attend(q, cache, table, lens)))
+    tab, n = i32(table), i32(lens)
+    torch.cuda.synchronize()
+    wrong, errors = [], []
+
+    def run(cache, q, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    got = binding.attn_fwd_paged(q, cache, tab, n)
+                    if not all(torch.equal(x, y) for x, y in zip(got, want)):
+                        wrong.append(1)
+        except Exception as e:   # shown in the main thread
+            errors.append(e)
+    threads = [threading.Thread(target=run, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors and not wrong
+    ok()
+
+
+def test_strides_of_single_tokens_and_heads_do_not_count():
+    """A dimension of one entry may have any stride (exchange formats set it to 1)."""
+    lens = [5]
+    table, pages = make_table(lens, 16, 3)
+    cache = make_cache("bf16", pages, 16, 1, 64)
+    k, v = randn((1, 1, 64), 1), randn((1, 1, 64), 2)
+    odd = [torch.as_strided(x, x.shape, (1, 1, 1)) for x in (k, v)]
+    binding.attn_paged_append(cache, *odd, i32([0, 1]), i32([0]), i32(table))
+    got = binding.attn_paged_gather(cache, i32([0, 1]), i32(table), 1)
+    assert torch.equal(got[0], k) and torch.equal(got[1], v)
+    y, _ = binding.attn_qk_norm_rope(odd[0])
+    assert torch.equal(y, binding.attn_qk_norm_rope(k)[0])
+    ok()

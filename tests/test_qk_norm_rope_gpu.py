@@ -266,3 +266,14 @@ def test_training_step_through_the_attention():
                       (dwq, ws[0].grad), (dwk, ws[1].grad)):
         diff = got.cpu().double() - want.detach()
         assert float(diff.norm() / want.detach().norm()) <= 2e-2
+
+
+def test_batches_without_tokens():
+    w = torch.ones(64, device="cuda")
+    for shape in ((2, 0, 4, 64), (0, 5, 4, 64), (0, 4, 64)):
+        q = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+        y, z = binding.attn_qk_norm_rope(q, q[..., :2, :], wq=w, wk=w)
+        assert y.shape == q.shape and z.shape == (*shape[:-2], 2, 64)
+        dq, _, dwq, dwk = binding.attn_qk_norm_rope_bwd(q, None, q, wq=w)
+        assert dq.shape == q.shape and bool((dwq == 0).all()) and dwk is None
+    ok()
