@@ -14,9 +14,11 @@
 // flight together, those of the next task behind them. Everything is fp32 between the bf16 loads and the
 // one rounding at the store.
 //
-// Memory bounds both. At B 2, N 8192, 32 + 8 heads, d 128 on a GB300 (share of the copy bandwidth): forward 56.7 us
-// (88%; 102 with rows unpacked at the load and a CTA per 16 tasks, 70 with rows held packed), backward
-// 92.2 us (81%; 155 at first; with 2 heads a task 114).
+// Memory bounds both. At B 2, N 8192, 32 + 8 heads, d 128 on a GB300 (share of the copy bandwidth): forward 55.8 us
+// (90%; 102 with rows unpacked at the load and a CTA per 16 tasks, 70 with rows held packed, 56.7 one value an
+// instruction), backward 89.7 us (83%; 155 at first; 114 with 2 heads a task, 92.2 one value an instruction). Angles
+// loaded before the next task's rows cost 2 to 5 us, a ring of asynchronous copies in shared memory 24: 8-byte copies, what
+// a half-split pair leaves a lane, take more of the load unit than 8-byte loads.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -48,11 +50,14 @@ struct NormRopeParams {
   float eps;
   int T, H, Hkv, half, max_pos, seq_len, parts_q, parts_k, ctas_q, w_vec;
   FastDiv parts, div_q, div_k;     // tasks of a token: all, of q, of k
+  FastDiv div_seq;
   uint32_t* status;
 };
 
+// A lane's 8 values of a row: pairs of neighbours, 0 and 1 of its first chunk, 2 and 3 of its second. The arithmetic works
+// on a register pair at a time (FFMA2 and its kin).
 struct Chunks {
-  float a[4], b[4];
+  uint64_t v[4];
 };
 
 // A lane's values of a row as they lie in memory: held like this while other rows' loads are under way.
@@ -64,26 +69,30 @@ __device__ __forceinline__ Raw load_raw(const __nv_bfloat16* row, int da, int db
   return {*reinterpret_cast<const uint2*>(row + da), *reinterpret_cast<const uint2*>(row + db)};
 }
 
-__device__ __forceinline__ void unpack4(float (&x)[4], const uint2& w) {
-  x[0] = __uint_as_float(w.x << 16);
-  x[1] = __uint_as_float(w.x & 0xffff0000u);
-  x[2] = __uint_as_float(w.y << 16);
-  x[3] = __uint_as_float(w.y & 0xffff0000u);
+__device__ __forceinline__ uint64_t unpack2(uint32_t w) {
+  return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
 __device__ __forceinline__ Chunks unpack(const Raw& r) {
-  Chunks x;
-  unpack4(x.a, r.a);
-  unpack4(x.b, r.b);
-  return x;
+  return {{unpack2(r.a.x), unpack2(r.a.y), unpack2(r.b.x), unpack2(r.b.y)}};
 }
 
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[4]) {
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
-  uint2 w;
-  w.x = *reinterpret_cast<const uint32_t*>(&lo);
-  w.y = *reinterpret_cast<const uint32_t*>(&hi);
-  *reinterpret_cast<uint2*>(p) = w;
+__device__ __forceinline__ uint32_t pack2(uint64_t x) {
+  float lo, hi;
+  f2_unpack(x, lo, hi);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void store4(__nv_bfloat16* p, uint64_t x, uint64_t y) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(x), pack2(y));
+}
+
+__device__ __forceinline__ uint64_t twice(float x) { return f2_pack(x, x); }
+__device__ __forceinline__ float sum2(uint64_t x) {
+  float lo, hi;
+  f2_unpack(x, lo, hi);
+  return lo + hi;
 }
 
 // First dims of a lane's two chunks. half = rope_dim / 2; lanes behind the rotated dims hold 8
@@ -95,21 +104,29 @@ __device__ __forceinline__ void chunk_dims(int l, int half, int& da, int& db) {
   db = split ? half + 4 * l : 8 * l + 4;
 }
 
-// Angles of a lane's pairs at one position: pair i of the lane is (a[i], b[i]), or when interleaved
-// (a[0], a[1]), (a[2], a[3]), (b[0], b[1]), (b[2], b[3]).
+// Angles of a lane's pairs at one position, as turn() multiplies with them: cosines, sines for the second member of a pair
+// and, with the sign turned, for the first. When interleaved a register pair is a rotated pair: (cos, cos), (-sin, sin).
+template <bool INTERLEAVED>
 struct Angles {
-  float c[4], s[4];
+  uint64_t c[INTERLEAVED ? 4 : 2], s[INTERLEAVED ? 4 : 2], n[INTERLEAVED ? 1 : 2];
 };
 
 template <bool INTERLEAVED>
-__device__ __forceinline__ void turn(Chunks& x, const Angles& r, float sign) {
+__device__ __forceinline__ void turn(Chunks& x, const Angles<INTERLEAVED>& r) {
+  if constexpr (INTERLEAVED) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float& u = INTERLEAVED ? (i < 2 ? x.a[2 * i] : x.b[2 * i - 4]) : x.a[i];
-    float& v = INTERLEAVED ? (i < 2 ? x.a[2 * i + 1] : x.b[2 * i - 3]) : x.b[i];
-    const float s = sign * r.s[i], u0 = u;
-    u = u0 * r.c[i] - v * s;
-    v = v * r.c[i] + u0 * s;
+    for (int i = 0; i < 4; ++i) {
+      float u, w;
+      f2_unpack(x.v[i], u, w);
+      x.v[i] = f2_fma(x.v[i], r.c[i], f2_mul(f2_pack(w, u), r.s[i]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t a = x.v[i], b = x.v[2 + i];
+      x.v[i] = f2_fma(a, r.c[i], f2_mul(b, r.n[i]));
+      x.v[2 + i] = f2_fma(b, r.c[i], f2_mul(a, r.s[i]));
+    }
   }
 }
 
@@ -123,43 +140,47 @@ __device__ __forceinline__ float row_sum(float x) {
 // Position of token t; -1 (nothing to store) where it lies outside the tables.
 __device__ __forceinline__ int position(const NormRopeParams& p, int t, int l) {
   if (!p.cos) return 0;
-  const int pos = p.positions ? p.positions[t] : t % p.seq_len;
+  const int pos = p.positions ? p.positions[t] : t - (int)((uint32_t)t / p.div_seq) * p.seq_len;
   if (pos >= 0 && pos < p.max_pos) return pos;
   if (l == 0) atomicCAS(p.status, 0u, kStatusBadPosition);
   return -1;
 }
 
-__device__ __forceinline__ Angles load_angles(const NormRopeParams& p, int pos, int l) {
-  Angles r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r.c[i] = 1.f, r.s[i] = 0.f;
+// Angles of position pos; back: for the turn back.
+template <bool INTERLEAVED>
+__device__ __forceinline__ Angles<INTERLEAVED> load_angles(const NormRopeParams& p, int pos, int l, bool back) {
+  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (4 * l < p.half && pos >= 0) {
     const long long at = (long long)pos * p.half + 4 * l;
-    const float4 c = *reinterpret_cast<const float4*>(p.cos + at), s = *reinterpret_cast<const float4*>(p.sin + at);
-    r.c[0] = c.x, r.c[1] = c.y, r.c[2] = c.z, r.c[3] = c.w;
-    r.s[0] = s.x, r.s[1] = s.y, r.s[2] = s.z, r.s[3] = s.w;
+    c = *reinterpret_cast<const float4*>(p.cos + at), s = *reinterpret_cast<const float4*>(p.sin + at);
+  }
+  if (back) s = make_float4(-s.x, -s.y, -s.z, -s.w);
+  Angles<INTERLEAVED> r;
+  if constexpr (INTERLEAVED) {
+    const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.c[i] = twice(cs[i]), r.s[i] = f2_pack(-sn[i], sn[i]);
+  } else {
+    r.c[0] = f2_pack(c.x, c.y), r.c[1] = f2_pack(c.z, c.w);
+    r.s[0] = f2_pack(s.x, s.y), r.s[1] = f2_pack(s.z, s.w);
+    r.n[0] = f2_pack(-s.x, -s.y), r.n[1] = f2_pack(-s.z, -s.w);
   }
   return r;
 }
 
-__device__ __forceinline__ void load_weights4(float (&x)[4], const float* w, bool vec) {
-  if (vec) {
-    const float4 y = *reinterpret_cast<const float4*>(w);
-    x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = w[i];
-  }
+__device__ __forceinline__ void load_weights4(uint64_t* x, const float* w, bool vec) {
+  const float4 y = vec ? *reinterpret_cast<const float4*>(w) : make_float4(w[0], w[1], w[2], w[3]);
+  x[0] = f2_pack(y.x, y.y), x[1] = f2_pack(y.z, y.w);
 }
 
 // vec: the weights are 16-byte aligned.
 __device__ __forceinline__ Chunks load_weights(const float* w, int da, int db, bool vec) {
   Chunks x;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x.a[i] = x.b[i] = 1.f;
+  for (int i = 0; i < 4; ++i) x.v[i] = twice(1.f);
   if (w) {
-    load_weights4(x.a, w + da, vec);
-    load_weights4(x.b, w + db, vec);
+    load_weights4(x.v, w + da, vec);
+    load_weights4(x.v + 2, w + db, vec);
   }
   return x;
 }
@@ -202,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtasPerSm) qk_norm_rope_kernel(c
   for (uint32_t first = blockIdx.x * ROWS; first < tasks; first += stride, id += stride) {
     Task next = now;
     if (first + stride < tasks) next = load(min(id + stride, tasks - 1));
-    const Angles r = load_angles(p, now.pos, l);
+    const Angles<INTERLEAVED> r = load_angles<INTERLEAVED>(p, now.pos, l, false);
     Chunks w;
     if (NORM) w = load_weights(now.is_k ? p.wk : p.wq, da, db, p.w_vec);
     const int heads = now.is_k ? p.Hkv : p.H, last = id < tasks && now.pos >= 0 ? heads : 0;
@@ -211,20 +232,17 @@ __global__ void __launch_bounds__(kThreads, kFwdCtasPerSm) qk_norm_rope_kernel(c
     for (int i = 0; i < kHeads; ++i) {
       Chunks v = unpack(now.raw[i]);
       if (NORM) {
-        float s = 0.f;
+        uint64_t s = f2_mul(v.v[0], v.v[0]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s += v.a[j] * v.a[j] + v.b[j] * v.b[j];
-        const float rs = rsqrtf(row_sum<LPR>(s) * (1.f / D) + p.eps);
+        for (int j = 1; j < 4; ++j) s = f2_fma(v.v[j], v.v[j], s);
+        const uint64_t rs = twice(rsqrtf(row_sum<LPR>(sum2(s)) * (1.f / D) + p.eps));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v.a[j] *= rs * w.a[j];
-          v.b[j] *= rs * w.b[j];
-        }
+        for (int j = 0; j < 4; ++j) v.v[j] = f2_mul(f2_mul(v.v[j], rs), w.v[j]);
       }
-      turn<INTERLEAVED>(v, r, 1.f);
+      turn<INTERLEAVED>(v, r);
       if (now.h0 + i < last) {
-        store4(y + i * D + da, v.a);
-        store4(y + i * D + db, v.b);
+        store4(y + i * D + da, v.v[0], v.v[1]);
+        store4(y + i * D + db, v.v[2], v.v[3]);
       }
     }
     now = next;
@@ -251,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kern
   Chunks w, dw;
   if (NORM) w = load_weights(wp, da, db, p.w_vec);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) dw.a[j] = dw.b[j] = 0.f;
+  for (int j = 0; j < 4; ++j) dw.v[j] = twice(0.f);
   struct Task {
     int t, h0, pos;
     Raw x[kHeads], g[kHeads];
@@ -278,40 +296,36 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kern
   for (uint32_t first = (uint32_t)cta * ROWS; first < tasks; first += stride, id += stride) {
     Task next = now;
     if (first + stride < tasks) next = load(min(id + stride, tasks - 1));
-    const Angles r = load_angles(p, now.pos, l);
+    const Angles<INTERLEAVED> r = load_angles<INTERLEAVED>(p, now.pos, l, true);
     const int last = id < tasks && now.pos >= 0 ? heads : 0;
     __nv_bfloat16* dx = (is_k ? p.ok : p.oq) + ((long long)now.t * heads + now.h0) * D;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
       Chunks g = unpack(now.g[i]);
-      turn<INTERLEAVED>(g, r, -1.f);
+      turn<INTERLEAVED>(g, r);
       if (NORM) {
         const Chunks v = unpack(now.x[i]);
-        float s = 0.f, m = 0.f;
+        Chunks gw;
+        uint64_t s2 = 0, m2 = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          s += v.a[j] * v.a[j] + v.b[j] * v.b[j];
-          m += g.a[j] * w.a[j] * v.a[j] + g.b[j] * w.b[j] * v.b[j];
+          gw.v[j] = f2_mul(g.v[j], w.v[j]);
+          s2 = j ? f2_fma(v.v[j], v.v[j], s2) : f2_mul(v.v[j], v.v[j]);
+          m2 = j ? f2_fma(gw.v[j], v.v[j], m2) : f2_mul(gw.v[j], v.v[j]);
         }
-        s = row_sum<LPR>(s);
-        m = row_sum<LPR>(m);
+        const float s = row_sum<LPR>(sum2(s2)), m = row_sum<LPR>(sum2(m2));
         const float rs = rsqrtf(s * (1.f / D) + p.eps), c = m * (1.f / D) * rs * rs;
+        const uint64_t rs2 = twice(rs), c2 = twice(-c);
         if (now.h0 + i < last) {   // not the repeated rows, nor a row without a position, which may hold anything
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            dw.a[j] += g.a[j] * v.a[j] * rs;
-            dw.b[j] += g.b[j] * v.b[j] * rs;
-          }
+          for (int j = 0; j < 4; ++j) dw.v[j] = f2_fma(g.v[j], f2_mul(v.v[j], rs2), dw.v[j]);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          g.a[j] = rs * (g.a[j] * w.a[j] - v.a[j] * c);
-          g.b[j] = rs * (g.b[j] * w.b[j] - v.b[j] * c);
-        }
+        for (int j = 0; j < 4; ++j) g.v[j] = f2_mul(f2_fma(v.v[j], c2, gw.v[j]), rs2);
       }
       if (now.h0 + i < last) {
-        store4(dx + i * D + da, g.a);
-        store4(dx + i * D + db, g.b);
+        store4(dx + i * D + da, g.v[0], g.v[1]);
+        store4(dx + i * D + db, g.v[2], g.v[3]);
       }
     }
     now = next;
@@ -320,8 +334,8 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kern
     __shared__ float sums[ROWS][D];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      sums[slot][da + j] = dw.a[j];
-      sums[slot][db + j] = dw.b[j];
+      const int at = (j < 2 ? da : db) + j % 2 * 2;
+      f2_unpack(dw.v[j], sums[slot][at], sums[slot][at + 1]);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < D; i += kThreads) {
@@ -464,7 +478,7 @@ extern "C" attn_status_t attn_qk_norm_rope(const void* q, const void* k, void* q
   p.eps = eps;
   p.T = T, p.H = H, p.Hkv = Hkv, p.half = cos ? rope_dim / 2 : 0, p.max_pos = max_pos, p.seq_len = seq_len;
   p.parts_q = (H + kHeads - 1) / kHeads, p.parts_k = (Hkv + kHeads - 1) / kHeads;
-  p.parts = fast_div(p.parts_q + p.parts_k), p.div_q = fast_div(p.parts_q), p.div_k = fast_div(std::max(p.parts_k, 1));
+  p.parts = fast_div(p.parts_q + p.parts_k), p.div_q = fast_div(p.parts_q), p.div_k = fast_div(std::max(p.parts_k, 1)), p.div_seq = fast_div(std::max(seq_len, 1));
   p.w_vec = aligned16(wq) && aligned16(wk);
   p.status = status;
   cudaError_t e;
@@ -549,7 +563,7 @@ extern "C" attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, con
   p.eps = eps;
   p.T = T, p.H = H, p.Hkv = Hkv, p.half = cos ? rope_dim / 2 : 0, p.max_pos = max_pos, p.seq_len = seq_len;
   p.parts_q = (H + kHeads - 1) / kHeads, p.parts_k = (Hkv + kHeads - 1) / kHeads, p.ctas_q = g.ctas_q;
-  p.parts = fast_div(p.parts_q + p.parts_k), p.div_q = fast_div(p.parts_q), p.div_k = fast_div(std::max(p.parts_k, 1));
+  p.parts = fast_div(p.parts_q + p.parts_k), p.div_q = fast_div(p.parts_q), p.div_k = fast_div(std::max(p.parts_k, 1)), p.div_seq = fast_div(std::max(seq_len, 1));
   p.w_vec = aligned16(wq) && aligned16(wk);
   p.status = status;
   cudaError_t e;
