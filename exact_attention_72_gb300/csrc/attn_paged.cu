@@ -909,13 +909,15 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
 
 // Joins the parts of the units that were cut: CTA (c, r) takes row r of the units that begin in warps c span to
 // (c + 1) span - 1 of the grid before. With a unit a warp or so (span = kWarps, "alone") a warp takes one if it has few
-// parts; otherwise the four warps share the parts of one after the other.
+// parts; otherwise all warps share the parts of one after the other.
 // LSE = log2 sum 2^LSE_i,  O = sum 2^(LSE_i - LSE) O_i.
 constexpr int kFewParts = 8;
+constexpr int kManyWarps = 16;   // of a CTA when units have many parts
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params p, int rows_per_unit, int span, int records) {
+template <int D, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) attn_paged_join_kernel(const Params p, int rows_per_unit, int span, int records) {
   griddep_wait();
+  const bool alone = WARPS == kWarps && span == kWarps;   // a record a warp
   constexpr int LANES = D / 4;                // lanes of a row
   constexpr int STEP = LANES < 32 ? LANES : 32, V = LANES / STEP, WAYS = 32 / STEP;   // of a warp: values each, rows at once
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, c = lane % STEP * 4, way = lane / STEP, r = blockIdx.y;
@@ -923,9 +925,8 @@ __global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params 
     int4 cut;
     int from;   // the warp that it begins in
   };
-  __shared__ Cut cuts[kThreads];   // units left to the whole CTA, in order
-  __shared__ int counts[kWarps];
-  const bool alone = span == kWarps;   // a record a warp
+  __shared__ Cut cuts[32 * WARPS];   // units left to the whole CTA, in order
+  __shared__ int counts[WARPS];
   Cut own{make_int4(0, 0, -1, 0), (int)(blockIdx.x * span + (alone ? warp : threadIdx.x))};
   if ((alone || (int)threadIdx.x < span) && own.from < records) own.cut = p.cut[own.from];
   bool mine = own.cut.z >= 0 && own.cut.y % p.row_blocks * rows_per_unit + r < p.Nq * p.G;
@@ -938,24 +939,15 @@ __global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params 
   auto slot_of = [&](const Cut& x, int joined, int i) -> long long {
     return i == 0 ? 2LL * x.from + 1 : i <= joined ? 2LL * kWarps * (x.from / kWarps + i) + 1 : 2LL * x.cut.z;
   };
-  // Parts first, first + stride, .. of a unit: their weighted sums for this lane, and the weights'.
   struct Sum {
     float top, sum;
     float4 x[V];
   };
-  auto gather = [&](const Cut& x, int first, int stride) {
+  // Parts first, first + stride, .. of a unit: their weighted sums for this lane, and the weights'.
+  auto gather = [&](const Cut& x, float top, int first, int stride) {
     const int joined = joined_of(x), parts = parts_of(x);
     auto at = [&](int i) -> long long { return slot_of(x, joined, i) * rows_per_unit + r; };
-    Sum s{-INFINITY, 0.f, {}};
-    bool any = false;   // a part that has keys, or is NaN
-    for (int i = lane; i < parts; i += 32) {
-      const float lse = p.part_lse[at(i)];
-      s.top = fmaxf(s.top, lse);
-      any = any || !(lse == -INFINITY);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s.top = fmaxf(s.top, __shfl_xor_sync(0xffffffffu, s.top, o));
-    if (!__any_sync(0xffffffffu, any)) return s;
+    Sum s{top, 0.f, {}};
 #pragma unroll 4
     for (int i = first * WAYS + way; i < parts; i += stride * WAYS) {
       const float f = exp2_fast(p.part_lse[at(i)] - s.top);
@@ -1032,20 +1024,35 @@ __global__ void __launch_bounds__(kThreads) attn_paged_join_kernel(const Params 
   if (!__syncthreads_or(mine)) return;
   int n = 0, before = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     before += w < warp ? counts[w] : 0;
     n += counts[w];
   }
   if (mine) cuts[before + __popc(ballot & ((1u << lane) - 1u))] = own;
   __syncthreads();
-  __shared__ Sum sums[kWarps][32];
+  __shared__ Sum sums[WARPS][32];
+  __shared__ float tops[WARPS];
   for (int i = 0; i < n; ++i) {   // the same for the whole CTA
     const Cut x = cuts[i];
-    sums[warp][lane] = gather(x, warp, kWarps);
+    const int joined = joined_of(x), parts = parts_of(x);
+    float top = -INFINITY;
+    bool any = false;   // a part that has keys, or is NaN
+    for (int j = threadIdx.x; j < parts; j += 32 * WARPS) {
+      const float lse = p.part_lse[slot_of(x, joined, j) * rows_per_unit + r];
+      top = fmaxf(top, lse);
+      any = any || !(lse == -INFINITY);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) tops[warp] = top;
+    const bool some = __syncthreads_or(any);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) top = fmaxf(top, tops[w]);
+    sums[warp][lane] = some ? gather(x, top, warp, WARPS) : Sum{-INFINITY, 0.f, {}};
     __syncthreads();
     if (warp == 0) {
       Sum s = sums[0][lane];
-      for (int w = 1; w < kWarps; ++w) {
+      for (int w = 1; w < WARPS; ++w) {
         const Sum& y = sums[w][lane];
         s.sum += y.sum;
 #pragma unroll
@@ -1096,9 +1103,12 @@ cudaError_t launch(const Params& p, int grid, unsigned long long context, cudaSt
   const int records = grid * kWarps;
   const long long units = (long long)p.B * p.c.Hkv * p.row_blocks;
   const int span = (int)std::clamp<long long>(records / (4 * units), kWarps, kThreads);
-  return launch_dependent(attn_paged_join_kernel<C::D>,
-                          dim3((unsigned)((records + span - 1) / span), (unsigned)std::min(C::ROWS, p.Nq * p.G)),
-                          dim3(kThreads), 0, s, p, (int)C::ROWS, span, records);
+  // 32 parts a unit and more: 16 warps (one sequence of 60871 keys, d 256 in bf16, one kv head: 25.5 us, with 4 warps 32.4;
+  // at 16 parts, B 28 of up to 1166 keys, 17 against 10.4).
+  const bool many = grid >= 32 * units;
+  auto join = many ? attn_paged_join_kernel<C::D, kManyWarps> : attn_paged_join_kernel<C::D, kWarps>;
+  return launch_dependent(join, dim3((unsigned)((records + span - 1) / span), (unsigned)std::min(C::ROWS, p.Nq * p.G)),
+                          dim3(many ? 32 * kManyWarps : kThreads), 0, s, p, (int)C::ROWS, span, records);
 }
 
 template <int D, bool INT4>
