@@ -15,6 +15,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/Allocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -127,6 +128,16 @@ void check_like(const at::Tensor* t, const char* name, const at::Tensor& like) {
 at::Tensor make(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor& like) {
   return at::Tensor(at::detail::empty_cuda(sizes, type, like.device(), std::nullopt));
 }
+
+// Memory of the call's own on the current stream: the tensor given, or an allocation that lives as long as this.
+struct Workspace {
+  c10::DataPtr made;
+  void* ptr;
+  size_t bytes;
+  Workspace(const at::Tensor* given, size_t need) : ptr(pointer(given)), bytes(given ? given->nbytes() : need) {
+    if (!given && need) made = c10::GetAllocator(c10::kCUDA)->allocate(need), ptr = made.get();
+  }
+};
 
 // An output: the tensor given, or a new one.
 struct Out {
@@ -298,7 +309,7 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     vector_of(dwq, "dwq", x.d), vector_of(dwk, "dwk", x.d);
     const cudaStream_t s = launch_stream({&x.q, x.k, x.cos, x.sin, x.positions, x.wq, x.wk, &gq, gk, dq, dk, dwq, dwk, ws});
     Out o_q(a[12], dq, x.q.sizes(), at::kBFloat16, x.q);
-    at::Tensor made_k, made_wq, made_wk, made_ws;
+    at::Tensor made_k, made_wq, made_wk;
     if (x.k && !dk) made_k = make(x.k->sizes(), at::kBFloat16, x.q), dk = &made_k;
     if (x.wq && !dwq) made_wq = make({x.d}, at::kFloat, x.q), dwq = &made_wq;
     if (x.wk && !dwk) made_wk = make({x.d}, at::kFloat, x.q), dwk = &made_wk;
@@ -306,16 +317,13 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (dwq) dwq->zero_();
       if (dwk) dwk->zero_();
     } else {
-      if (!ws && (dwq || dwk)) {
-        made_ws = make({(int64_t)attn_qk_norm_rope_bwd_workspace_bytes(x.T, x.H, x.Hkv, x.d)}, at::kByte, x.q);
-        ws = &made_ws;
-      }
+      const Workspace work(ws, dwq || dwk ? attn_qk_norm_rope_bwd_workspace_bytes(x.T, x.H, x.Hkv, x.d) : 0);
       check_status(launch([&] {
         return attn_qk_norm_rope_bwd(x.q.data_ptr(), pointer(x.k), gq.data_ptr(), pointer(gk), o_q.ptr, pointer(dk),
                                      (float*)pointer(dwq), (float*)pointer(dwk), x.T, x.H, x.Hkv, x.d, x.rq.st, x.rq.sh,
                                      x.rk.st, x.rk.sh, x.norm, x.wqp, x.wkp, x.eps, x.rope.cos, x.rope.sin, x.rope.dim,
-                                     x.rope.max_pos, x.interleaved, (const int*)pointer(x.positions), x.N, pointer(ws),
-                                     ws ? ws->nbytes() : 0, s);
+                                     x.rope.max_pos, x.interleaved, (const int*)pointer(x.positions), x.N, work.ptr, work.bytes,
+                                     s);
       }), "attn_qk_norm_rope_bwd");
     }
     auto object = [&](PyObject* given, const at::Tensor* t, at::Tensor& made) {
@@ -421,15 +429,11 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int causal = truth(a[5]);
     const float scale = a[6] == Py_None ? (float)(1.0 / std::sqrt((double)d)) : (float)number(a[6]);
     const cudaStream_t s = p.stream({&p.table, &q, &lens, ws, out, lse});
-    at::Tensor made;
-    if (!ws) {
-      const size_t need = attn_fwd_paged_workspace_bytes(p.B, H, p.cache->Hkv, Nq, d, p.cache->type);
-      made = make({(int64_t)std::max<size_t>(need, 1)}, at::kByte, q), ws = &made;
-    }
+    const Workspace work(ws, ws ? 0 : attn_fwd_paged_workspace_bytes(p.B, H, p.cache->Hkv, Nq, d, p.cache->type));
     Out o(a[8], out, q.sizes(), at::kBFloat16, q), l(a[9], lse, {p.B, H, Nq}, at::kFloat, q);
     check_status(launch([&] {
       return attn_fwd_paged(q.data_ptr(), p.cache, o.ptr, (float*)l.ptr, (const int*)p.table.data_ptr(), p.stride, p.max_pages,
-                            lenp, p.B, H, Nq, scale, causal, ws->data_ptr(), ws->nbytes(), s);
+                            lenp, p.B, H, Nq, scale, causal, work.ptr, work.bytes, s);
     }), "attn_fwd_paged");
     return tuple({o.object(), l.object()});
   });
