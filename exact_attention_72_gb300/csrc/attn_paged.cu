@@ -31,12 +31,14 @@
 //
 // Measured on a GB300 (us in a CUDA graph, share of the copy bandwidth; H 32, Hkv 8, d 128 if not said otherwise):
 //   bf16, B 8, 16384 keys                85    93%
-//   4 bits, B 8, 16384 keys              35    63%: about 5 us until the first tiles are there and 5 us to join the parts;
+//   4 bits, B 8, 16384 keys              35    64%: about 5 us until the first tiles are there and 5 us to join the parts;
 //                                              between them the tiles stream at 99%
-//   4 bits, B 32, up to 32768 keys      102    82%
+//   4 bits, B 32, up to 32768 keys       99    85%
 //   bf16, d 256, B 13, up to 5000 keys, 12 rows (two blocks, the second out of L2)  35    51%
 // What it took, at B 8 and 16384 keys in 4 bits: tiles of one CTA with lane-wise operand loads 61; pages looked up once a
 // tile 48.6; matrix loads, shares by warp, a vote instead of the maximum's exchanges 40; one wave of shorter launches 36.
+// OVERHEAD sets how even the shares are where units are short: a warp that got a sequence's empty units at one tile each held
+// up a batch of 16 (4 bits, H 96, 165 to 20539 keys, one empty: 99 us, 72 at 4 tiles; the same sizes at equal lengths 74).
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -73,7 +75,7 @@ struct Cfg {
   static constexpr int D = D_, NT = NT_;
   static constexpr bool INT4 = INT4_;
   static constexpr int KT = INT4 ? 32 : 16;              // keys of a tile
-  static constexpr int OVERHEAD = INT4 ? 1 : 2;          // what beginning and ending a unit costs, in tiles
+  static constexpr int OVERHEAD = INT4 ? 4 : 8;          // what beginning and ending a unit costs, in tiles
   static constexpr int ROWS = 8 * NT;                    // query rows of a unit
   static constexpr int GROUPS = D / kInt4Group;
   static constexpr int ROWB = INT4 ? D / 2 : 2 * D;      // bytes of a key's row

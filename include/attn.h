@@ -488,7 +488,7 @@ attn_status_t attn_paged_gather(const attn_paged_cache_t* cache, void* k, void* 
  * its keys and values ceil(Nq (H / Hkv) / R) times, R = 8 query rows, or 16 when there are more than 8
  * and d <= 128. Deterministic. Two programmatic dependent launches; allocates nothing.
  * UNSUPPORTED as for the cache, for scale == 0, and for max_pages * page_size >= 2^31 - 1023 or
- * B * Hkv * row blocks * tiles of 16 keys (32 in 4 bits) >= 2^31.
+ * B * Hkv * row blocks * (tiles of 16 keys + 8; in 4 bits, of 32 keys + 4) >= 2^31.
  */
 size_t attn_fwd_paged_workspace_bytes(int B, int H, int Hkv, int Nq, int d, attn_cache_type_t type);
 attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t* cache, void* o, float* lse,
