@@ -15,7 +15,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
-#include <c10/core/Allocator.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -135,7 +135,7 @@ struct Workspace {
   void* ptr;
   size_t bytes;
   Workspace(const at::Tensor* given, size_t need) : ptr(pointer(given)), bytes(given ? given->nbytes() : need) {
-    if (!given && need) made = c10::GetAllocator(c10::kCUDA)->allocate(need), ptr = made.get();
+    if (!given && need) made = c10::cuda::CUDACachingAllocator::get()->allocate(need), ptr = made.get();
   }
 };
 

@@ -636,3 +636,27 @@ def test_strides_of_single_tokens_and_heads_do_not_count():
     y, _ = binding.attn_qk_norm_rope(odd[0])
     assert torch.equal(y, binding.attn_qk_norm_rope(k)[0])
     ok()
+
+
+def test_captured_without_a_workspace_of_the_callers():
+    """What a captured call allocates for itself stays with the graph: replays between other calls and allocations."""
+    lens = [4000, 9, 700]
+    table, pages = make_table(lens, 16, 3)
+    cache = make_cache("int4", pages, 16, 2, 64)
+    fill(cache, table, lens, 4)
+    q, tab, n = randn((3, 1, 8, 64), 5), i32(table), i32(lens)
+    want = attend(q, cache, table, lens)
+    w = torch.ones(64, device="cuda")
+    grads = binding.attn_qk_norm_rope_bwd(q, None, q, wq=w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = binding.attn_fwd_paged(q, cache, tab, n)
+        again = binding.attn_qk_norm_rope_bwd(q, None, q, wq=w)
+    for i in range(4):
+        graph.replay()
+        other = torch.full((1 << 22,), float(i), device="cuda")
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        assert torch.equal(again[0], grads[0]) and torch.equal(again[2], grads[2])
+        assert all(torch.equal(x, y) for x, y in zip(attend(q, cache, table, lens), want))
+        del other
+    ok()
