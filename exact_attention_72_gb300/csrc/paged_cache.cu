@@ -15,7 +15,7 @@
 // Measured on a GB300, 8 kv heads, d 128, 4 bits: append of 12.4k tokens 20 us (66 MB; arithmetic, 60% of the issue slots,
 // and the chain of offsets, page and angles; 49 us with IEEE divisions, 24.5 us one value an instruction), gather of 29.4k
 // tokens 24.4 us (154 MB, 93% of the copy bandwidth; 29.5 us with values converted one by one). Two heads a lane, sharing
-// the look-ups, are no faster (45.3 against 44.7 us for both), nor are more CTAs an SM.
+// the look-ups, are no faster (45.3 against 45.0 us for both), nor are more CTAs an SM.
 #include <algorithm>
 #include <climits>
 
@@ -43,6 +43,7 @@ struct AppendParams {
   const float *cos, *sin;
   int B, total, max_pages, half, rope_dim, max_pos;
   FastDiv parts, page_size;   // parts: tasks of a token
+  uint64_t one, minus_one;    // pairs of them, where the compiler does not see the value
   uint32_t* status;
 };
 
@@ -221,6 +222,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
     good = good && in;
     if (!in) pos = 0;
   }
+  // Rotation rounds both products, then their sum or difference: an addition of a product in a register pair may be fused
+  // with it even where both are written with a rounding of their own, a product with +-1 out of memory may not (and is exact).
   uint64_t y[2][8];   // key, value
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -233,8 +236,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint64_t a = y[0][j], b = y[0][4 + j];
-      y[0][j] = f2_sub(f2_mul(a, cs[j]), f2_mul(b, sn[j]));
-      y[0][4 + j] = f2_add(f2_mul(b, cs[j]), f2_mul(a, sn[j]));
+      y[0][j] = f2_fma(f2_mul(b, sn[j]), p.minus_one, f2_mul(a, cs[j]));
+      y[0][4 + j] = f2_fma(f2_mul(a, sn[j]), p.one, f2_mul(b, cs[j]));
     }
   } else if constexpr (ROPE != kNone) {
 #pragma unroll
@@ -255,15 +258,16 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
           f2_unpack(x[j], u, w);
           m[j] = f2_pack(w, u), cs[j] = f2_pack(ca[j], ca[j]), sn[j] = f2_pack(sa[j], sa[j]);
         }
-        sign = f2_pack(-1.f, 1.f);
+        float plus, minus, unused;
+        f2_unpack(p.one, plus, unused);
+        f2_unpack(p.minus_one, minus, unused);
+        sign = f2_pack(minus, plus);
       } else {
         load8(cs, ct);
         load8(sn, st);
         unpack8(m, raw_mate[s]);
-        const float first = d0 < p.half ? -1.f : 1.f;
-        sign = f2_pack(first, first);
+        sign = d0 < p.half ? p.minus_one : p.one;
       }
-      // both products rounded, then their sum or difference (a product with +-1 is exact)
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[j] = f2_fma(f2_mul(m[j], sn[j]), sign, f2_mul(x[j], cs[j]));
     }
@@ -420,6 +424,7 @@ extern "C" attn_status_t attn_paged_append(const attn_paged_cache_t* cache, cons
   p.cos = cos, p.sin = sin;
   p.B = B, p.total = total, p.max_pages = max_pages, p.max_pos = max_pos;
   p.rope_dim = cos ? rope_dim : 0, p.half = p.rope_dim / 2;
+  p.one = 0x3f8000003f800000u, p.minus_one = 0xbf800000bf800000u;
   const bool int4 = cache->type == ATTN_CACHE_INT4, il = interleaved != 0;
   cudaError_t e;
   switch (cache->d) {

@@ -660,3 +660,25 @@ def test_captured_without_a_workspace_of_the_callers():
         assert all(torch.equal(x, y) for x, y in zip(attend(q, cache, table, lens), want))
         del other
     ok()
+
+
+@pytest.mark.parametrize("d,rd,il", [(128, 128, False), (64, 64, False), (256, 256, False), (128, 64, False), (128, 128, True),
+                                     (64, 32, True)])
+def test_rotation_rounds_both_products(d, rd, il):
+    """Pairs (a, a) and (a, -a) turned by cos = sin: one of the two sums is of equal products and has to be 0 exactly. A fused
+    multiply-add would leave the product's rounding error there."""
+    n, half = 64, rd // 2
+    a = randn((n, 2, half), 3)
+    sign = torch.where(torch.arange(half, device="cuda") % 2 == 0, 1.0, -1.0).bfloat16()
+    k = randn((n, 2, d), 4)
+    first, second = (slice(0, rd, 2), slice(1, rd, 2)) if il else (slice(0, half), slice(half, rd))
+    k[..., first], k[..., second] = a, a * sign
+    t = torch.rand((n, half), generator=torch.Generator().manual_seed(5)).cuda() + 0.3
+    table, pages = make_table([n], 16, 3)
+    cache = make_cache("bf16", pages, 16, 2, d)
+    binding.attn_paged_append(cache, k, k, i32([0, n]), i32([0]), i32(table), cos=t, sin=t, interleaved=il)
+    got, _ = binding.attn_paged_gather(cache, i32([0, n]), i32(table), n)
+    ok()
+    assert bool((got[..., first][..., sign > 0] == 0).all()) and bool((got[..., second][..., sign < 0] == 0).all())
+    want = a.float() * t[:, None] * 2
+    assert torch.allclose(got[..., second][..., sign > 0].float(), want[..., sign > 0], rtol=2 ** -8 + 2 ** -22, atol=0)
