@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
+#include <optional>
 #include <stdexcept>
 #include <string>
 
@@ -275,23 +276,15 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (x.k) check_like(ko, "k_out", *x.k);
     const cudaStream_t s = launch_stream({&x.q, x.k, x.cos, x.sin, x.positions, x.wq, x.wk, qo, ko});
     Out q_out(a[10], qo, x.q.sizes(), at::kBFloat16, x.q);
-    if (!x.k) {
-      if (x.T > 0)
-        check_status(launch([&] {
-          return attn_qk_norm_rope(x.q.data_ptr(), nullptr, q_out.ptr, nullptr, x.T, x.H, 0, x.d, x.rq.st, x.rq.sh, 0, 0, x.norm,
-                                   x.wqp, nullptr, x.eps, x.rope.cos, x.rope.sin, x.rope.dim, x.rope.max_pos,
-                                   x.interleaved, (const int*)pointer(x.positions), x.N, s);
-        }), "attn_qk_norm_rope");
-      return tuple({q_out.object(), none()});
-    }
-    Out k_out(a[11], ko, x.k->sizes(), at::kBFloat16, x.q);
+    std::optional<Out> k_out;
+    if (x.k) k_out.emplace(a[11], ko, x.k->sizes(), at::kBFloat16, x.q);
     if (x.T > 0)
       check_status(launch([&] {
-        return attn_qk_norm_rope(x.q.data_ptr(), x.k->data_ptr(), q_out.ptr, k_out.ptr, x.T, x.H, x.Hkv, x.d, x.rq.st, x.rq.sh,
-                                 x.rk.st, x.rk.sh, x.norm, x.wqp, x.wkp, x.eps, x.rope.cos, x.rope.sin, x.rope.dim,
-                                 x.rope.max_pos, x.interleaved, (const int*)pointer(x.positions), x.N, s);
+        return attn_qk_norm_rope(x.q.data_ptr(), pointer(x.k), q_out.ptr, k_out ? k_out->ptr : nullptr, x.T, x.H, x.Hkv, x.d,
+                                 x.rq.st, x.rq.sh, x.rk.st, x.rk.sh, x.norm, x.wqp, x.wkp, x.eps, x.rope.cos, x.rope.sin,
+                                 x.rope.dim, x.rope.max_pos, x.interleaved, (const int*)pointer(x.positions), x.N, s);
       }), "attn_qk_norm_rope");
-    return tuple({q_out.object(), k_out.object()});
+    return tuple({q_out.object(), k_out ? k_out->object() : none()});
   });
 }
 
@@ -402,10 +395,12 @@ PyObject* paged_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (t && (t->sizes() != at::IntArrayRef(shape, 3) || t->scalar_type() != at::kBFloat16 || !t->is_contiguous()))
         refuse("k and v must be contiguous bfloat16 CUDA tensors [total, Hkv, d]");
     const cudaStream_t s = p.stream({&p.table, &cu, k, v});
-    Out ko(a[5], k, at::IntArrayRef(shape, 3), at::kBFloat16, p.table), vo(a[6], v, at::IntArrayRef(shape, 3), at::kBFloat16, p.table);
+    Out ko(a[5], k, at::IntArrayRef(shape, 3), at::kBFloat16, p.table);
+    Out vo(a[6], v, at::IntArrayRef(shape, 3), at::kBFloat16, p.table);
     if (total > 0 && p.B > 0)
       check_status(launch([&] {
-        return attn_paged_gather(p.cache, ko.ptr, vo.ptr, cup, (const int*)p.table.data_ptr(), p.stride, p.max_pages, p.B, total, s);
+        return attn_paged_gather(p.cache, ko.ptr, vo.ptr, cup, (const int*)p.table.data_ptr(), p.stride, p.max_pages, p.B,
+                                 total, s);
       }), "attn_paged_gather");
     return tuple({ko.object(), vo.object()});
   });
@@ -424,13 +419,14 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (q.size(0) != p.B || q.size(3) != d || p.cache->Hkv <= 0 || H % p.cache->Hkv != 0)
       refuse("q must be [B, Nq, H, d] with the page table's B, the cache's d and a multiple of its heads");
     check_like(out, "out", q);
-    if (lse && (lse->sizes() != at::IntArrayRef({(int64_t)p.B, (int64_t)H, (int64_t)Nq}) || lse->scalar_type() != at::kFloat || !lse->is_contiguous()))
+    const int64_t rows[3] = {p.B, H, Nq};
+    if (lse && (lse->sizes() != at::IntArrayRef(rows, 3) || lse->scalar_type() != at::kFloat || !lse->is_contiguous()))
       refuse("lse must be a contiguous float32 CUDA tensor [B, H, Nq]");
     const int causal = truth(a[5]);
     const float scale = a[6] == Py_None ? (float)(1.0 / std::sqrt((double)d)) : (float)number(a[6]);
     const cudaStream_t s = p.stream({&p.table, &q, &lens, ws, out, lse});
     const Workspace work(ws, ws ? 0 : attn_fwd_paged_workspace_bytes(p.B, H, p.cache->Hkv, Nq, d, p.cache->type));
-    Out o(a[8], out, q.sizes(), at::kBFloat16, q), l(a[9], lse, {p.B, H, Nq}, at::kFloat, q);
+    Out o(a[8], out, q.sizes(), at::kBFloat16, q), l(a[9], lse, at::IntArrayRef(rows, 3), at::kFloat, q);
     check_status(launch([&] {
       return attn_fwd_paged(q.data_ptr(), p.cache, o.ptr, (float*)l.ptr, (const int*)p.table.data_ptr(), p.stride, p.max_pages,
                             lenp, p.B, H, Nq, scale, causal, work.ptr, work.bytes, s);

@@ -478,7 +478,8 @@ extern "C" attn_status_t attn_qk_norm_rope(const void* q, const void* k, void* q
   p.eps = eps;
   p.T = T, p.H = H, p.Hkv = Hkv, p.half = cos ? rope_dim / 2 : 0, p.max_pos = max_pos, p.seq_len = seq_len;
   p.parts_q = (H + kHeads - 1) / kHeads, p.parts_k = (Hkv + kHeads - 1) / kHeads;
-  p.parts = fast_div(p.parts_q + p.parts_k), p.div_q = fast_div(p.parts_q), p.div_k = fast_div(std::max(p.parts_k, 1)), p.div_seq = fast_div(std::max(seq_len, 1));
+  p.parts = fast_div(p.parts_q + p.parts_k), p.div_q = fast_div(p.parts_q), p.div_k = fast_div(std::max(p.parts_k, 1));
+  p.div_seq = fast_div(std::max(seq_len, 1));
   p.w_vec = aligned16(wq) && aligned16(wk);
   p.status = status;
   cudaError_t e;
@@ -563,7 +564,8 @@ extern "C" attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, con
   p.eps = eps;
   p.T = T, p.H = H, p.Hkv = Hkv, p.half = cos ? rope_dim / 2 : 0, p.max_pos = max_pos, p.seq_len = seq_len;
   p.parts_q = (H + kHeads - 1) / kHeads, p.parts_k = (Hkv + kHeads - 1) / kHeads, p.ctas_q = g.ctas_q;
-  p.parts = fast_div(p.parts_q + p.parts_k), p.div_q = fast_div(p.parts_q), p.div_k = fast_div(std::max(p.parts_k, 1)), p.div_seq = fast_div(std::max(seq_len, 1));
+  p.parts = fast_div(p.parts_q + p.parts_k), p.div_q = fast_div(p.parts_q), p.div_k = fast_div(std::max(p.parts_k, 1));
+  p.div_seq = fast_div(std::max(seq_len, 1));
   p.w_vec = aligned16(wq) && aligned16(wk);
   p.status = status;
   cudaError_t e;
