@@ -14,9 +14,14 @@
 //   q.k = sum over groups  scale (codes . q) + zero sum(q),
 //   O   = (sum_j (p_j scale_j) codes_j + sum_j p_j zero_j) / sum_j p_j.
 // Roundings: q is scaled by a power of two per row, so fp16 holds it exactly where it counts (2^-25 of the row's greatest
-// value); p_j scale_j is rounded to fp16, 2^-11 of itself. bf16 caches take p_j as a sum of two bf16 numbers, 2^-16 off:
-// in one, 2^-8 off, the weights would add as much to O's error as its own rounding (0.0023 instead of 0.0017 of its
-// norm), and the second product costs nothing beside the cache's bytes. For p_j scale_j to stay within fp16 at any scale,
+// value). Weights go into the second product as a sum of two numbers. In one bf16 number, 2^-8 off, p_j would add as much to
+// O's error as its own rounding (0.0023 instead of 0.0017 of its norm); two are 2^-16 off, and the second product costs
+// nothing beside the cache's bytes. p_j scale_j in one fp16 number, 2^-11 off, moves O by 0.0011 of its norm (codes are
+// summed with their offset apart, so that a weight's rounding counts twice the value's size) and by any share of it where
+// zero and codes cancel; two are 2^-22 off and cost 12% with 5 to 8 rows, 19% with more. With at most 4 rows they cost 2%:
+// half the columns would be padding, so that columns c and c + 4 take one query row, and the first takes the weights'
+// first number, the second the other (B 8, 16384 keys, 4 rows: 34.8 us in one number, 35.5 so, 38.7 with two products;
+// B 32, up to 32768 keys: 98.7, 100.2, 112.4). For p_j scale_j to stay within fp16 at any scale,
 // the running maximum is taken over S + log2 of the key's scale (its exponent) instead of S.
 //
 // Work: a sequence's keys are cut into tiles of KT; a unit is the tiles of one (sequence, kv head, block of query rows).
@@ -70,10 +75,10 @@ constexpr long long kMaxKeys = INT_MAX - 1023;   // keys a page table may hold: 
 constexpr float kNone = -1e30f;     // running maximum before the first key
 constexpr float kHeadroom = 0x1p14f;   // weights times scale may grow to this before the maximum is moved
 
-template <int D_, bool INT4_, int NT_>
+template <int D_, bool INT4_, int NT_, bool TWIN_ = false>
 struct Cfg {
   static constexpr int D = D_, NT = NT_;
-  static constexpr bool INT4 = INT4_;
+  static constexpr bool INT4 = INT4_, TWIN = TWIN_;      // TWIN: columns c and c + 4 hold one query row (at most 4 rows)
   static constexpr int KT = INT4 ? 32 : 16;              // keys of a tile
   static constexpr int OVERHEAD = INT4 ? 4 : 8;          // what beginning and ending a unit costs, in tiles
   static constexpr int ROWS = 8 * NT;                    // query rows of a unit
@@ -217,6 +222,15 @@ __device__ __forceinline__ uint32_t subtract_half2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_half2(uint64_t x) {
+  float a, b;
+  f2_unpack(x, a, b);
+  return pack_half2(a, b);
+}
+__device__ __forceinline__ uint64_t unpack_half2(uint32_t x) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+  return f2_pack(f.x, f.y);
 }
 __device__ __forceinline__ uint32_t pack_bf162(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -391,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
 #pragma unroll
           for (int i = 0; i < 8 / QRPI; ++i) {
             const int r = i * QRPI + lane / QCH;
-            const uint32_t row = cur.row0 + f_q * 8 + r, qi = row / p.div_g;
+            const uint32_t row = cur.row0 + f_q * 8 + (C::TWIN ? r & 3 : r), qi = row / p.div_g;
             const bool in = row < (uint32_t)(p.Nq * p.G);
             const long long from = in ? cur.q_row + (long long)qi * p.H + (row - qi * p.G) : 0;
             copy16<0>(fill + chunk_at<2 * D>(r, lane % QCH), p.q + from * D + lane % QCH * 8, in);
@@ -473,6 +487,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
     };
     // Where this lane's row of a matrix load lies: lanes 0-7 and 8-15 rows 0-7 and 8-15 of a 16-row block's first
     // chunk, lanes 16-31 of its second. Further pairs of chunks differ in bits 5 and up.
+    [[maybe_unused]] const uint64_t minus_hi = t < 2 ? f2_pack(0.f, 0.f) : f2_pack(-1.f, -1.f);   // of twin columns
     const uint32_t my_chunk = chunk_at<C::ROWB>(lane & 15, lane >> 4);
     for (int turn = 0; turn < f_turn; ++turn) {
       constexpr int QR = D / 16;
@@ -556,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int c = row0 + nt * 8 + 2 * t + j;
+          const int c = row0 + nt * 8 + (C::TWIN ? 2 * t & 3 : 2 * t) + j;
           limit[nt][j] = p.causal && c < rows ? keys - p.Nq + 1 + (int)((uint32_t)c / p.div_g) : keys;
           least = min(least, limit[nt][j]);
         }
@@ -564,7 +579,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
       least = min(least, __shfl_xor_sync(0xffffffffu, least, 2));
 
       float acc[NT][D / 16][4];
-      float m[NT][2], l[NT][2], z[NT][INT4 ? GROUPS : 1][2];
+      float m[NT][2], l[NT][2];
+      uint64_t z[NT][INT4 ? GROUPS : 1];    // 4 bits: sums of weight times zero, a pair of columns
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -576,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
           m[nt][j] = kNone;
           l[nt][j] = 0.f;
 #pragma unroll
-          for (int gr = 0; gr < (INT4 ? GROUPS : 1); ++gr) z[nt][gr][j] = 0.f;
+          for (int gr = 0; gr < (INT4 ? GROUPS : 1); ++gr) z[nt][gr] = f2_pack(0.f, 0.f);
         }
       }
 #pragma unroll 1
@@ -698,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
               m[nt][j] = x;
               l[nt][j] *= f;
 #pragma unroll
-              for (int gr = 0; gr < (INT4 ? GROUPS : 1); ++gr) z[nt][gr][j] *= f;
+              for (int gr = 0; gr < (INT4 ? GROUPS : 1); ++gr) z[nt][gr] = f2_mul(z[nt][gr], j ? f2_pack(1.f, f) : f2_pack(f, 1.f));
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
                 acc[nt][i][j] *= f;
@@ -720,27 +736,42 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
           if constexpr (INT4) {
 #pragma unroll
             for (int gr = 0; gr < GROUPS; ++gr) {
-              const uint32_t sv0 = vs[kb][0][gr], sv1 = vs[kb][1][gr];
-              const float sc0 = __uint_as_float(sv0 << 16), zr0 = __uint_as_float(sv0 & 0xffff0000u);
-              const float sc1 = __uint_as_float(sv1 << 16), zr1 = __uint_as_float(sv1 & 0xffff0000u);
-              uint32_t b0[NT], b1[NT];
+              uint64_t sc[2], zr[2];
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const float(&q)[4] = w[kb][nt];
-                b0[nt] = transpose8x8(pack_half2(q[0] * sc0, q[1] * sc0));
-                b1[nt] = transpose8x8(pack_half2(q[2] * sc1, q[3] * sc1));
-                z[nt][gr][0] += q[0] * zr0 + q[2] * zr1;
-                z[nt][gr][1] += q[1] * zr0 + q[3] * zr1;
+              for (int i = 0; i < 2; ++i) {
+                const float a = __uint_as_float(vs[kb][i][gr] << 16), b = __uint_as_float(vs[kb][i][gr] & 0xffff0000u);
+                sc[i] = f2_pack(a, a), zr[i] = f2_pack(b, b);
               }
+              // Weights times scale rounded to fp16, and what that left; of twin columns the first takes one, the second the other.
+              uint32_t hi[2][NT];
+              [[maybe_unused]] uint32_t lo[2][NT];
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const uint64_t q = f2_pack(w[kb][nt][2 * i], w[kb][nt][2 * i + 1]), x = f2_mul(q, sc[i]);
+                  const uint32_t h = pack_half2(x);
+                  if constexpr (C::TWIN) {
+                    hi[i][nt] = transpose8x8(pack_half2(f2_fma(unpack_half2(h), minus_hi, x)));
+                  } else {
+                    hi[i][nt] = transpose8x8(h);
+                    lo[i][nt] = transpose8x8(pack_half2(f2_sub(x, unpack_half2(h))));
+                  }
+                  z[nt][gr] = f2_fma(q, zr[i], z[nt][gr]);
+                }
               // lane (g, t): of keys 2t, 2t + 1 (and 8 further) dims 4g .. 4g + 3 of the group's two halves
               const uint4 x = load_matrices<true, C::V_OFF + kb * 16 * C::ROWB>(slot + (my_chunk ^ gr * 32));
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const uint32_t x0 = i < 2 ? x.x : x.z, x1 = i < 2 ? x.y : x.w;
                 const uint32_t y0 = i % 2 ? high_bytes(x0) : x0 & 0x00ff00ffu, y1 = i % 2 ? high_bytes(x1) : x1 & 0x00ff00ffu;
+                const uint32_t c0 = y0 & 0x000f000fu, c1 = y1 & 0x000f000fu;   // low codes, and low + 16 high
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)   // low codes, and low + 16 high
-                  mma<true>(acc[nt][gr * 4 + i], y0 & 0x000f000fu, y0, y1 & 0x000f000fu, y1, b0[nt], b1[nt]);
+                for (int nt = 0; nt < NT; ++nt) mma<true>(acc[nt][gr * 4 + i], c0, y0, c1, y1, hi[0][nt], hi[1][nt]);
+                if constexpr (!C::TWIN) {
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) mma<true>(acc[nt][gr * 4 + i], c0, y0, c1, y1, lo[0][nt], lo[1][nt]);
+                }
               }
             }
           } else {
@@ -779,14 +810,25 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
             l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], o);
             if constexpr (INT4) {
 #pragma unroll
-              for (int gr = 0; gr < GROUPS; ++gr) z[nt][gr][j] += __shfl_xor_sync(0xffffffffu, z[nt][gr][j], o);
+              for (int gr = 0; gr < GROUPS; ++gr)
+                if (j == 0) z[nt][gr] = f2_add(z[nt][gr], __shfl_xor_sync(0xffffffffu, (unsigned long long)z[nt][gr], o));
             }
           }
         }
+      if constexpr (C::TWIN) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[0][i][j] += __shfl_xor_sync(0xffffffffu, acc[0][i][j], 2);
+      }
       // O^T of column c, dims d(i) and d(i) + 1 (4 bits) or + 8: MMA rows g and g + 8 of tile i
       auto value = [&](int nt, int i, int j) -> float2 {
         const float x = acc[nt][i][j], y = acc[nt][i][2 + j];
-        if constexpr (INT4) return make_float2(x * 0x1p24f + z[nt][i / 4][j], (y - x) * 0x1p20f + z[nt][i / 4][j]);
+        if constexpr (INT4) {
+          float z0, z1;
+          f2_unpack(z[nt][i / 4], z0, z1);
+          return make_float2(x * 0x1p24f + (j ? z1 : z0), (y - x) * 0x1p20f + (j ? z1 : z0));
+        }
         else return make_float2(x, y);
       };
       auto dim = [&](int i) { return INT4 ? i / 2 * 32 + 4 * g + i % 2 * 2 : 16 * i + g; };
@@ -1117,6 +1159,9 @@ template <int D, bool INT4>
 cudaError_t launch_rows(const Params& p, int rows_per_unit, int grid, unsigned long long context, cudaStream_t s) {
   if constexpr (D <= 128) {
     if (rows_per_unit == 16) return launch<Cfg<D, INT4, 2>>(p, grid, context, s);
+  }
+  if constexpr (INT4) {
+    if (p.Nq * p.G <= 4) return launch<Cfg<D, true, 1, true>>(p, grid, context, s);
   }
   return launch<Cfg<D, INT4, 1>>(p, grid, context, s);
 }
