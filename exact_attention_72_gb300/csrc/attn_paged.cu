@@ -22,7 +22,9 @@
 // half the columns would be padding, so that columns c and c + 4 take one query row, and the first takes the weights'
 // first number, the second the other (B 8, 16384 keys, 4 rows: 34.8 us in one number, 35.5 so, 38.7 with two products;
 // B 32, up to 32768 keys: 98.7, 100.2, 112.4). For p_j scale_j to stay within fp16 at any scale,
-// the running maximum is taken over S + log2 of the key's scale (its exponent) instead of S.
+// the running maximum is taken over S + log2 of the key's scale (its exponent) instead of S; with several groups of dims, each
+// has a power of two of its own that follows its own scales, so that a group keeps its bits beside one far larger (5% with 4
+// rows, 35.6 -> 37.2 and 100.3 -> 106 us, 1% with more; one factor for all lost the codes of a group 2^-14 as large).
 //
 // Work: a sequence's keys are cut into tiles of KT; a unit is the tiles of one (sequence, kv head, block of query rows).
 // All units in order, each OVERHEAD tiles longer than it is, are dealt to all warps in equal contiguous shares, so ragged
@@ -73,7 +75,10 @@ constexpr float kLeastScale = 0x1p-70f;
 
 constexpr long long kMaxKeys = INT_MAX - 1023;   // keys a page table may hold: they are counted in 32 bits
 constexpr float kNone = -1e30f;     // running maximum before the first key
-constexpr float kHeadroom = 0x1p14f;   // weights times scale may grow to this before the maximum is moved
+constexpr float kHeadroom = 0x1p14f;   // weights of a bf16 cache may grow to this before the maximum is moved
+// 4 bits: a move sets the greatest weight times scale below 2^6 (a group's own, where there are several); it may grow to
+// 2^15 before the next. fp16 may lose 2^-25 of each: 2^-29 of the greatest, which is 2^4 at least.
+constexpr float kTop = 6.f, kScaledHeadroom = 0x1p15f;
 
 template <int D_, bool INT4_, int NT_, bool TWIN_ = false>
 struct Cfg {
@@ -83,6 +88,7 @@ struct Cfg {
   static constexpr int OVERHEAD = INT4 ? 4 : 8;          // what beginning and ending a unit costs, in tiles
   static constexpr int ROWS = 8 * NT;                    // query rows of a unit
   static constexpr int GROUPS = D / kInt4Group;
+  static constexpr bool UP = INT4 && GROUPS > 1;         // groups have powers of two of their own
   static constexpr int ROWB = INT4 ? D / 2 : 2 * D;      // bytes of a key's row
   static constexpr int SZB = INT4 ? 4 * GROUPS : 0;      // bytes of its (scale, zero) pairs
   // A slot of the ring: a tile's keys and values, or 8 query rows. At d = 256 in bf16 a tile takes two slots, keys then
@@ -580,7 +586,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
 
       float acc[NT][D / 16][4];
       float m[NT][2], l[NT][2];
-      uint64_t z[NT][INT4 ? GROUPS : 1];    // 4 bits: sums of weight times zero, a pair of columns
+      uint64_t z[NT][INT4 ? GROUPS : 1];    // 4 bits, a pair of columns: sums of weight times zero,
+      [[maybe_unused]] uint64_t up[NT][C::UP ? GROUPS : 1];   // and what a group's weights times scale are multiplied with
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -593,6 +600,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
           l[nt][j] = 0.f;
 #pragma unroll
           for (int gr = 0; gr < (INT4 ? GROUPS : 1); ++gr) z[nt][gr] = f2_pack(0.f, 0.f);
+#pragma unroll
+          for (int gr = 0; gr < (C::UP ? GROUPS : 1); ++gr) up[nt][gr] = f2_pack(1.f, 1.f);
         }
       }
 #pragma unroll 1
@@ -667,58 +676,113 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
           leave();
           turn_to();
         }
-        // Weights p = 2^(S - m). The maximum m of S + log2 scale moves only when a weight times scale outgrows fp16's
-        // room: rarely after the first tile, so that a tile costs a vote instead of the exchanges of a maximum.
-        uint32_t vs[KB][2][INT4 ? GROUPS : 1];   // (scale, zero) of my two values of a block
-        float top_scale[KB][2];
-        each_of<KB * 2>([&](auto index) {
-          constexpr int kb = decltype(index)::value / 2, i = decltype(index)::value % 2;
-          top_scale[kb][i] = 1.f;
-          if constexpr (INT4) {
-            load_pairs<C::SZV_OFF + (kb * 16 + i * 8) * C::SZB>(vs[kb][i], slot + g * C::SZB);
-            float x = kLeastScale;
+        // Weights p = 2^(S - m). The maximum m moves only when a weight outgrows its room: rarely after the first tile, so
+        // that a tile costs a vote instead of the exchanges of a maximum. In 4 bits a weight times scale has to stay within
+        // fp16. With one group of dims m is taken over S + log2 scale (its exponent). With several it is taken over S, and each
+        // group of a column has a power of two that its weights times scale are multiplied with: one factor for all would
+        // follow the greatest scale and lose the codes of a group 2^-14 as large, or less beside one early key's.
+        [[maybe_unused]] uint32_t vs[KB][2][INT4 ? GROUPS : 1];   // (scale, zero) of my two values of a block
+        float w[KB][NT][4], high[NT][2];
 #pragma unroll
-            for (int gr = 0; gr < GROUPS; ++gr) x = fmaxf(x, fabsf(__uint_as_float(vs[kb][i][gr] << 16)));
-            top_scale[kb][i] = x;
+        for (int nt = 0; nt < NT; ++nt) {
+          high[nt][0] = high[nt][1] = 0.f;
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[kb][nt][j] = exp2_fast(fmaf(s[kb][nt][j], mult[nt][j & 1], -m[nt][j & 1]));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) high[nt][j] = fmax3(high[nt][j], w[kb][nt][j], w[kb][nt][2 + j]);
           }
-        });
-        float w[KB][NT][4], high = 0.f, most = 0.f;
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          most = fmaxf(most, fmaxf(top_scale[kb][0], top_scale[kb][1]));
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              w[kb][nt][j] = exp2_fast(fmaf(s[kb][nt][j], mult[nt][j & 1], -m[nt][j & 1]));
-              high = fmaxf(high, w[kb][nt][j]);
-            }
         }
-        if (__any_sync(0xffffffffu, high * most > kHeadroom)) {
+        float most = 0.f;
+        if constexpr (!INT4 || C::UP) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) most = fmax3(most, high[nt][0], high[nt][1]);
+        }
+        if constexpr (INT4) {
+          each_of<KB * 2>([&](auto index) {
+            constexpr int kb = decltype(index)::value / 2, i = decltype(index)::value % 2;
+            load_pairs<C::SZV_OFF + (kb * 16 + i * 8) * C::SZB>(vs[kb][i], slot + g * C::SZB);
+          });
+          most *= 0x1p-25f;   // with several groups: weights themselves stay far from overflow
+#pragma unroll
+          for (int gr = 0; gr < GROUPS; ++gr) {
+            float top = kLeastScale;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) top = fmaxf(top, fabsf(__uint_as_float(vs[kb][i][gr] << 16)));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float a = high[nt][0] * top, b = high[nt][1] * top;
+              if constexpr (C::UP) f2_unpack(f2_mul(f2_pack(a, b), up[nt][gr]), a, b);
+              most = fmax3(most, a, b);
+            }
+          }
+        }
+        if (__any_sync(0xffffffffu, most > (INT4 ? kScaledHeadroom : kHeadroom))) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               float x = m[nt][j];
+              [[maybe_unused]] float y[C::UP ? GROUPS : 1];   // the same of S + log2 scale
+#pragma unroll
+              for (int gr = 0; gr < (C::UP ? GROUPS : 1); ++gr) y[gr] = -INFINITY;
 #pragma unroll
               for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  // exponent of the scale, one more so that scale 2^-e < 1 (1 for bf16: e = 1)
-                  const float e = (float)((int)(__float_as_uint(top_scale[kb][i]) >> 23) - 126);
-                  x = fmaxf(x, fmaf(s[kb][nt][2 * i + j], mult[nt][j], e));
+                  // exponent of the scale, one more so that scale 2^-e < 1
+                  auto exponent = [&](int gr) {
+                    const float sc = fmaxf(fabsf(__uint_as_float(vs[kb][i][gr] << 16)), kLeastScale);
+                    return (float)((int)(__float_as_uint(sc) >> 23) - 126);
+                  };
+                  const float score = s[kb][nt][2 * i + j];
+                  if constexpr (C::UP) {
+                    x = fmaxf(x, score * mult[nt][j]);
+#pragma unroll
+                    for (int gr = 0; gr < GROUPS; ++gr) y[gr] = fmaxf(y[gr], fmaf(score, mult[nt][j], exponent(gr)));
+                  } else {
+                    x = fmaxf(x, fmaf(score, mult[nt][j], INT4 ? exponent(0) - kTop : 1.f));
+                  }
                 }
 #pragma unroll
-              for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-              const float f = exp2_fast(m[nt][j] - x);
+              for (int o = 4; o < 32; o <<= 1) {
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                if constexpr (C::UP) {
+#pragma unroll
+                  for (int gr = 0; gr < GROUPS; ++gr) y[gr] = fmaxf(y[gr], __shfl_xor_sync(0xffffffffu, y[gr], o));
+                }
+              }
+              const float down = m[nt][j] - x, f = exp2_fast(down);
               m[nt][j] = x;
               l[nt][j] *= f;
 #pragma unroll
               for (int gr = 0; gr < (INT4 ? GROUPS : 1); ++gr) z[nt][gr] = f2_mul(z[nt][gr], j ? f2_pack(1.f, f) : f2_pack(f, 1.f));
+              if constexpr (C::UP) {
 #pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
-                acc[nt][i][j] *= f;
-                acc[nt][i][2 + j] *= f;
+                for (int gr = 0; gr < GROUPS; ++gr) {
+                  float u[2];
+                  f2_unpack(up[nt][gr], u[0], u[1]);
+                  const int was = (int)(__float_as_uint(u[j]) >> 23) - 127;
+                  // as far up as this tile allows, and what is summed already (its greatest stays where it was)
+                  const int now = (int)fmaxf(fminf(fminf(floorf(kTop + x - y[gr]), was + floorf(-down)), 125.f), -125.f);
+                  u[j] = __uint_as_float((uint32_t)(now + 127) << 23);
+                  up[nt][gr] = f2_pack(u[0], u[1]);
+                  const float fg = exp2_fast(down + (float)(now - was));
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    acc[nt][gr * 4 + i][j] *= fg;
+                    acc[nt][gr * 4 + i][2 + j] *= fg;
+                  }
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                  acc[nt][i][j] *= f;
+                  acc[nt][i][2 + j] *= f;
+                }
               }
 #pragma unroll
               for (int kb = 0; kb < KB; ++kb)
@@ -749,7 +813,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  const uint64_t q = f2_pack(w[kb][nt][2 * i], w[kb][nt][2 * i + 1]), x = f2_mul(q, sc[i]);
+                  const uint64_t q = f2_pack(w[kb][nt][2 * i], w[kb][nt][2 * i + 1]);
+                  const uint64_t x = f2_mul(C::UP ? f2_mul(q, up[nt][gr]) : q, sc[i]);
                   const uint32_t h = pack_half2(x);
                   if constexpr (C::TWIN) {
                     hi[i][nt] = transpose8x8(pack_half2(f2_fma(unpack_half2(h), minus_hi, x)));
@@ -825,9 +890,14 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
       auto value = [&](int nt, int i, int j) -> float2 {
         const float x = acc[nt][i][j], y = acc[nt][i][2 + j];
         if constexpr (INT4) {
-          float z0, z1;
+          float z0, z1, back = 1.f;
           f2_unpack(z[nt][i / 4], z0, z1);
-          return make_float2(x * 0x1p24f + (j ? z1 : z0), (y - x) * 0x1p20f + (j ? z1 : z0));
+          if constexpr (C::UP) {
+            float u0, u1;
+            f2_unpack(up[nt][i / 4], u0, u1);
+            back = __uint_as_float((254u << 23) - __float_as_uint(j ? u1 : u0));   // 1 / u, a power of two
+          }
+          return make_float2(x * back * 0x1p24f + (j ? z1 : z0), (y - x) * back * 0x1p20f + (j ? z1 : z0));
         }
         else return make_float2(x, y);
       };
