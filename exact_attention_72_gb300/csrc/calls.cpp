@@ -130,6 +130,13 @@ at::Tensor make(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor& li
   return at::Tensor(at::detail::empty_cuda(sizes, type, like.device(), std::nullopt));
 }
 
+// A workspace argument; null for None. Its bytes are its values' only where it is contiguous.
+const at::Tensor* workspace(PyObject* o) {
+  const at::Tensor* t = tensor(o, "workspace");
+  if (t && !t->is_contiguous()) refuse("workspace must be a contiguous CUDA tensor");
+  return t;
+}
+
 // Memory of the call's own on the current stream: the tensor given, or an allocation that lives as long as this.
 struct Workspace {
   c10::DataPtr made;
@@ -294,7 +301,7 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const NormRope x(a);
     const at::Tensor &gq = needed(a[10], "dq_out"), *gk = tensor(a[11], "dk_out"), *dq = tensor(a[12], "dq"),
                      *dk = tensor(a[13], "dk"), *dwq = tensor(a[14], "dwq"), *dwk = tensor(a[15], "dwk"),
-                     *ws = tensor(a[16], "workspace");
+                     *ws = workspace(a[16]);
     if ((gk != nullptr) != (x.k != nullptr)) refuse("dk_out is given exactly with k");
     if ((dk && !x.k) || (dwq && !x.wq) || (dwk && !x.wk)) refuse("dk needs k, dwq needs wq and dwk needs wk");
     check_like(&gq, "dq_out", x.q), check_like(dq, "dq", x.q);
@@ -410,7 +417,7 @@ PyObject* paged_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 10, [&] {
     const Paged p(a[0], a[1], a[3]);
-    const at::Tensor &q = needed(a[2], "q"), &lens = needed(a[4], "seqlens"), *ws = tensor(a[7], "workspace"),
+    const at::Tensor &q = needed(a[2], "q"), &lens = needed(a[4], "seqlens"), *ws = workspace(a[7]),
                      *out = tensor(a[8], "out"), *lse = tensor(a[9], "lse");
     const int* lenp = p.ints(lens, "seqlens", 0);
     if (q.dim() != 4 || q.scalar_type() != at::kBFloat16 || !q.is_contiguous())

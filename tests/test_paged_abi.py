@@ -191,3 +191,16 @@ def test_compiled_calls_turn_errors_into_exceptions():
         binding.attn_qk_norm_rope(torch.zeros(1, 1, 64, dtype=torch.bfloat16))
     with pytest.raises(ValueError, match="CUDA tensor on the current device"):
         binding.attn_qk_norm_rope(torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="meta"))
+
+
+def test_a_workspace_has_the_bytes_that_its_size_says():
+    """Expanded or cut with gaps: fewer or other bytes than numel() counts. Refused before anything else is looked at."""
+    calls = binding._calls()
+    c = cache()
+    q, table, lens = torch.zeros(1, 1, 8, 128, dtype=torch.bfloat16), torch.zeros(1, 2, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    x, w = torch.zeros(4, 8, 128, dtype=torch.bfloat16), torch.ones(128)
+    for ws in (torch.empty(1, dtype=torch.uint8).expand(1 << 24), torch.empty(1 << 10, 2, dtype=torch.uint8)[:, 0]):
+        with pytest.raises(ValueError, match="workspace must be a contiguous"):
+            calls.fwd_paged(ctypes.addressof(c), 0, q, table, lens, True, None, ws, None, None)
+        with pytest.raises(ValueError, match="workspace must be a contiguous"):
+            binding.attn_qk_norm_rope_bwd(x, None, x, wq=w, workspace=ws)
