@@ -22,6 +22,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -95,11 +96,15 @@ __device__ __forceinline__ float sum2(uint64_t x) {
   return lo + hi;
 }
 
+// Whether a lane holds rotated pairs. The others' values stay as they are, rather than turned by 0: 0 times an infinite one
+// would make its neighbour NaN.
+__device__ __forceinline__ bool turns(int l, int half) { return 4 * l < half; }
+
 // First dims of a lane's two chunks. half = rope_dim / 2; lanes behind the rotated dims hold 8
 // neighbouring values, as all lanes do when pairs are interleaved.
 template <bool INTERLEAVED>
 __device__ __forceinline__ void chunk_dims(int l, int half, int& da, int& db) {
-  const bool split = !INTERLEAVED && 4 * l < half;
+  const bool split = !INTERLEAVED && turns(l, half);
   da = split ? 4 * l : 8 * l;
   db = split ? half + 4 * l : 8 * l + 4;
 }
@@ -130,6 +135,17 @@ __device__ __forceinline__ void turn(Chunks& x, const Angles<INTERLEAVED>& r) {
   }
 }
 
+// Of a lane whose values are rotated. PART: some lanes' are not, in a row that is rotated in part or not at all. They choose
+// rather than branch, which would keep the rows of a task apart (half of each row rotated, B 2, N 8192: forward 57.7 us, with a
+// branch 60.1, with values turned by 0 56.5; whole rows, that do not ask, 55.9, with a branch 59.2).
+template <bool INTERLEAVED, bool PART>
+__device__ __forceinline__ void turn_lane(Chunks& x, const Angles<INTERLEAVED>& r, bool rotated) {
+  Chunks y = x;
+  turn<INTERLEAVED>(y, r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x.v[i] = !PART || rotated ? y.v[i] : x.v[i];
+}
+
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x) {
 #pragma unroll
@@ -150,7 +166,7 @@ __device__ __forceinline__ int position(const NormRopeParams& p, int t, int l) {
 template <bool INTERLEAVED>
 __device__ __forceinline__ Angles<INTERLEAVED> load_angles(const NormRopeParams& p, int pos, int l, bool back) {
   float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (4 * l < p.half && pos >= 0) {
+  if (turns(l, p.half) && pos >= 0) {
     const long long at = (long long)pos * p.half + 4 * l;
     c = *reinterpret_cast<const float4*>(p.cos + at), s = *reinterpret_cast<const float4*>(p.sin + at);
   }
@@ -187,7 +203,7 @@ __device__ __forceinline__ Chunks load_weights(const float* w, int da, int db, b
 
 // CTAs walk the tasks of all tokens, one wave of them; a thread has the rows of its next task on their
 // way while it turns those of this one, so that loads are always in flight.
-template <int D, bool NORM, bool INTERLEAVED>
+template <int D, bool NORM, bool INTERLEAVED, bool PART>
 __global__ void __launch_bounds__(kThreads, kFwdCtasPerSm) qk_norm_rope_kernel(const NormRopeParams p) {
   griddep_wait();
   griddep_launch_dependents();   // of the next kernel only the launch may overlap: it waits for this one's end
@@ -239,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtasPerSm) qk_norm_rope_kernel(c
 #pragma unroll
         for (int j = 0; j < 4; ++j) v.v[j] = f2_mul(f2_mul(v.v[j], rs), w.v[j]);
       }
-      turn<INTERLEAVED>(v, r);
+      turn_lane<INTERLEAVED, PART>(v, r, turns(l, p.half));
       if (now.h0 + i < last) {
         store4(y + i * D + da, v.v[0], v.v[1]);
         store4(y + i * D + db, v.v[2], v.v[3]);
@@ -252,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtasPerSm) qk_norm_rope_kernel(c
 // The gradient. CTAs 0 .. ctas_q - 1 walk the tasks of q, the others those of k, so a thread sums the
 // weight gradient of its 8 dims in registers; a CTA adds its rows' sums in a fixed order and leaves
 // [d] in part, which dw_kernel adds up: the same bits every time.
-template <int D, bool NORM, bool INTERLEAVED>
+template <int D, bool NORM, bool INTERLEAVED, bool PART>
 __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kernel(const NormRopeParams p) {
   griddep_wait();
   griddep_launch_dependents();   // of the next kernel only the launch may overlap: it waits for this one's end
@@ -302,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kern
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
       Chunks g = unpack(now.g[i]);
-      turn<INTERLEAVED>(g, r);
+      turn_lane<INTERLEAVED, PART>(g, r, turns(l, p.half));
       if (NORM) {
         const Chunks v = unpack(now.x[i]);
         Chunks gw;
@@ -368,20 +384,29 @@ __global__ void __launch_bounds__(1024) dw_kernel(const float* __restrict__ part
   }
 }
 
+// f with the constants of the kernel that p and the flags ask for.
+template <int D, class F>
+cudaError_t with_kind(const NormRopeParams& p, bool norm, bool interleaved, F&& f) {
+  const bool part = 2 * p.half != D;
+  auto go = [&](auto n, auto i) { return part ? f(n, i, std::true_type{}) : f(n, i, std::false_type{}); };
+  if (norm) return interleaved ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
+  return interleaved ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
+}
+
 template <int D>
 cudaError_t launch_forward(const NormRopeParams& p, bool norm, bool interleaved, int sms, cudaStream_t s) {
   const long long tasks = (long long)p.T * (p.parts_q + p.parts_k), rows = kThreads / (D / 8);
   const unsigned grid = (unsigned)std::min<long long>((tasks + rows - 1) / rows, (long long)kFwdCtasPerSm * sms);
-  auto kernel = norm ? (interleaved ? qk_norm_rope_kernel<D, true, true> : qk_norm_rope_kernel<D, true, false>)
-                     : (interleaved ? qk_norm_rope_kernel<D, false, true> : qk_norm_rope_kernel<D, false, false>);
-  return launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, p);
+  return with_kind<D>(p, norm, interleaved, [&](auto n, auto i, auto part) {
+    return launch_dependent(qk_norm_rope_kernel<D, n(), i(), part()>, dim3(grid), dim3(kThreads), 0, s, p);
+  });
 }
 
 template <int D>
 cudaError_t launch_backward(const NormRopeParams& p, bool norm, bool interleaved, int grid, cudaStream_t s) {
-  auto kernel = norm ? (interleaved ? qk_norm_rope_bwd_kernel<D, true, true> : qk_norm_rope_bwd_kernel<D, true, false>)
-                     : (interleaved ? qk_norm_rope_bwd_kernel<D, false, true> : qk_norm_rope_bwd_kernel<D, false, false>);
-  return launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, p);
+  return with_kind<D>(p, norm, interleaved, [&](auto n, auto i, auto part) {
+    return launch_dependent(qk_norm_rope_bwd_kernel<D, n(), i(), part()>, dim3((unsigned)grid), dim3(kThreads), 0, s, p);
+  });
 }
 
 // CTAs of the backward: one wave, shared between q and k by their tasks.

@@ -277,3 +277,25 @@ def test_batches_without_tokens():
         dq, _, dwq, dwk = binding.attn_qk_norm_rope_bwd(q, None, q, wq=w)
         assert dq.shape == q.shape and bool((dwq == 0).all()) and dwk is None
     ok()
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan"), -0.0])
+@pytest.mark.parametrize("d,rd,il", [(64, 0, False), (64, 32, False), (128, 64, False), (128, 0, False), (128, 32, True),
+                                     (256, 16, False), (256, 240, True)])
+def test_values_behind_the_rotated_ones_are_unchanged(d, rd, il, value):
+    """Without the norm every value behind rope_dim comes out as it is, whatever stands beside it: each of them once infinite,
+    NaN or -0 in a row of its own. The same of the gradient."""
+    T = d - rd
+    q, _, _, _, _ = make(T, 3, 0, d, 11, fused=False)
+    cos, sin = tables(T, rd // 2) if rd else (None, None)
+    kw = dict(cos=cos, sin=sin, norm=False, interleaved=il)
+    want = binding.attn_qk_norm_rope(q, **kw)[0], binding.attn_qk_norm_rope_bwd(q, None, q, **kw)[0]
+    x = q.clone()
+    rows = torch.arange(T, device="cuda")
+    x[rows, 1, rd + rows] = value
+    got = binding.attn_qk_norm_rope(x, **kw)[0], binding.attn_qk_norm_rope_bwd(x, None, x, **kw)[0]
+    ok()
+    for y, w in zip(got, want):
+        w[..., rd:] = x[..., rd:]
+        same = y.view(torch.int16) == w.view(torch.int16)
+        assert bool((same | (y.isnan() & w.isnan())).all())
