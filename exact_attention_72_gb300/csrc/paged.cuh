@@ -19,8 +19,8 @@
 namespace gb300 {
 
 constexpr int kInt4Group = 64;
-constexpr uint32_t kStatusBadPage = 0x20000000u | 13u;       // page, position or offsets out of range
-constexpr uint32_t kStatusBadPosition = 0x20000000u | 14u;   // rotation position outside the tables
+constexpr uint32_t kStatusBadPage = 0x20000000u | 13u;       // paged cache: page, position (angles too) or offsets
+constexpr uint32_t kStatusBadPosition = 0x20000000u | 14u;   // norm and rotation: position outside the tables
 
 // Cache of one layer, in bytes: row (page, token in page, kv head) of k starts at
 // k + page * page_b + token * token_b + head * head_b; its (scale, zero) pairs at k_sz + ...

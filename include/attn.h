@@ -450,7 +450,7 @@ typedef struct {
  *   cache_lens: DEVICE int32 [B], tokens the cache holds already (the call does not change it).
  *   cos, sin, rope_dim, max_pos, interleaved: as in attn_qk_norm_rope; NULL stores k as it is (keys that
  *      attn_qk_norm_rope has turned). The rotated key is rounded to bf16 (bf16 cache), or quantised
- *      from fp32 (4 bits).
+ *      from fp32 (4 bits). A token whose position lies beyond the tables is not stored, and reported as above.
  *   No two tokens of a call may fall on one cache row (sequences that share a page they write to).
  * One kernel, asynchronous on stream, allocates nothing; total == 0 returns ATTN_OK at once.
  */
@@ -508,8 +508,9 @@ attn_status_t attn_get_status(cudaStream_t stream);
 /*
  * attn_get_status_detail — attn_get_status that also stores the raw device status word in
  * `detail` (may be NULL): 0, 0x40000000 | the code of the wait site that gave up, 0x2000000C
- * for a rejected varlen plan, 0x2000000D for a page, length or offset of a paged-cache call out of
- * range, or 0x2000000E for a rotation position outside its tables. 0 is stored when the synchronization fails.
+ * for a rejected varlen plan, 0x2000000D for a page, length, offset or position of a paged-cache call out of
+ * range (attn_paged_append: the tables of angles included), or 0x2000000E for a position of attn_qk_norm_rope or
+ * attn_qk_norm_rope_bwd outside their tables. 0 is stored when the synchronization fails.
  */
 attn_status_t attn_get_status_detail(cudaStream_t stream, uint32_t* detail);
 
