@@ -1,5 +1,6 @@
-"""Builds libattn_gb300.so from csrc/ with nvcc for sm_103a (in-tree, no setuptools), and _calls.so, the compiled part
-of the Python binding (csrc/calls.cpp, against torch's headers), beside it.
+"""Builds libattn_gb300.so from csrc/ with nvcc for sm_103a (in-tree, no setuptools), and beside it the compiled part of
+the Python binding (csrc/calls.cpp, against torch's headers). The library needs neither torch nor that part: without torch it
+is built alone, and it is linked before a failing compilation of calls.cpp is reported.
 
 Each .cu file compiles in its own nvcc process (in parallel); the objects are linked into one
 shared library next to this file. The CUDA runtime is linked statically and the driver's
@@ -16,6 +17,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+from typing import Optional
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -41,22 +43,42 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _torch_dir() -> str:
-    return list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+def _torch_dir() -> Optional[str]:
+    """Where torch is installed; None without torch."""
+    spec = importlib.util.find_spec("torch")
+    return list(spec.submodule_search_locations)[0] if spec else None
+
+
+def has_torch() -> bool:
+    return _torch_dir() is not None
+
+
+def _headers():
+    return glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
-                               glob.glob(os.path.join(CSRC, "*.cpp"))) + \
-        sorted(glob.glob(os.path.join(INCLUDE, "*.h"))) + \
-        [os.path.abspath(__file__), os.path.join(_torch_dir(), "version.py")]   # _calls.so is bound to one torch
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + _headers()
+
+
+def _newer(path: str, deps) -> bool:
+    if not os.path.exists(path):
+        return False
+    t = os.path.getmtime(path)
+    return all(os.path.getmtime(p) <= t for p in deps)
+
+
+def _library_up_to_date() -> bool:
+    return _newer(LIB_PATH, _deps())
+
+
+def _calls_up_to_date() -> bool:
+    version = os.path.join(_torch_dir(), "version.py")   # the calls are bound to one torch
+    return _newer(CALLS_PATH, [os.path.join(CSRC, "calls.cpp"), version] + _headers())
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _library_up_to_date() and (not has_torch() or _calls_up_to_date())
 
 
 def _compile(nvcc: str, src: str, verbose: bool) -> str:
@@ -85,26 +107,37 @@ def _compile_calls(nvcc: str) -> str:
     return obj
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compiles (if needed) and returns the path of the shared library."""
-    if not force and up_to_date():
-        return LIB_PATH
-    nvcc = _nvcc()
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs = _sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
-        calls = ex.submit(_compile_calls, nvcc)
-        objs = list(ex.map(lambda s: _compile(nvcc, s, verbose), srcs))
-        calls_obj = calls.result()
+def _link_library(nvcc: str, objs) -> None:
     tmp = LIB_PATH + ".tmp"
     _run([nvcc] + ARCH + ["-shared", "-Xlinker", "-soname=" + LIB_NAME, "-o", tmp] + objs, "link")
     os.replace(tmp, LIB_PATH)
+
+
+def _link_calls(obj: str) -> None:
     # finds the library beside itself, and torch's where they were when it was built
-    torch_lib = os.path.join(_torch_dir(), "lib")
-    tmp = CALLS_PATH + ".tmp"
-    _run(["g++", "-shared", "-o", tmp, calls_obj, "-L" + PKG_DIR, "-l:" + LIB_NAME, "-L" + torch_lib, "-ltorch_python",
-          "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib], "link of _calls.so")
+    torch_lib, tmp = os.path.join(_torch_dir(), "lib"), CALLS_PATH + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L" + PKG_DIR, "-l:" + LIB_NAME, "-L" + torch_lib, "-ltorch_python",
+          "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib],
+         "link of the compiled calls")
     os.replace(tmp, CALLS_PATH)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compiles (what is not up to date) and returns the path of the shared library."""
+    library = force or not _library_up_to_date()
+    calls = has_torch() and (force or not _calls_up_to_date())
+    if not library and not calls:
+        return LIB_PATH
+    nvcc = _nvcc()
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    srcs = _sources() if library else []
+    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        calls_obj = ex.submit(_compile_calls, nvcc) if calls else None
+        objs = list(ex.map(lambda s: _compile(nvcc, s, verbose), srcs))
+    if library:
+        _link_library(nvcc, objs)
+    if calls:
+        _link_calls(calls_obj.result())
     return LIB_PATH
 
 
