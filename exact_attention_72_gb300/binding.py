@@ -1,5 +1,5 @@
 """Binding of libattn_gb300.so (argument marshalling only; all compute runs in the library), by ctypes; the calls whose
-kernels take a few microseconds (norm and rotation, paged cache) are marshalled by _calls.so (csrc/calls.cpp).
+kernels take a few microseconds (norm and rotation, paged cache) are marshalled by the compiled module _calls (csrc/calls.cpp).
 
 The Python names mirror the C ABI in include/attn.h. ``attn_fwd`` takes torch CUDA tensors
 (PyTorch is used for device memory and streams only) and raises ``AttnError`` on any non-OK
@@ -506,7 +506,10 @@ def _calls():
         import torch  # noqa: F401  (its libraries first)
         lib()
         if not os.path.exists(_build.CALLS_PATH):
-            raise RuntimeError("_calls.so is not built; call exact_attention_72_gb300.build.build()")
+            raise RuntimeError(os.path.basename(_build.CALLS_PATH) + " is not built; call exact_attention_72_gb300.build.build()")
+        if not _build.calls_fit():
+            raise RuntimeError(os.path.basename(_build.CALLS_PATH) + " was built for another Python or torch; call "
+                               "exact_attention_72_gb300.build.build() again")
         from . import _calls as module
         module.set_error(AttnError)
         _CALLS = module

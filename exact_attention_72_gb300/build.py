@@ -26,7 +26,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_NAME = "libattn_gb300.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
-CALLS_PATH = os.path.join(PKG_DIR, "_calls.so")
+EXT_SUFFIX = sysconfig.get_config_var("EXT_SUFFIX")
+CALLS_PATH = os.path.join(PKG_DIR, "_calls" + EXT_SUFFIX)
+CALLS_STAMP = os.path.join(BUILD_DIR, "calls.txt")   # the environment that CALLS_PATH was built for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
@@ -73,12 +75,26 @@ def _library_up_to_date() -> bool:
 
 
 def _calls_up_to_date() -> bool:
-    version = os.path.join(_torch_dir(), "version.py")   # the calls are bound to one torch
-    return _newer(CALLS_PATH, [os.path.join(CSRC, "calls.cpp"), version] + _headers())
+    return _newer(CALLS_PATH, [os.path.join(CSRC, "calls.cpp")] + _headers()) and calls_fit()
 
 
 def up_to_date() -> bool:
     return _library_up_to_date() and (not has_torch() or _calls_up_to_date())
+
+
+def _environment() -> str:
+    """What the compiled calls are bound to: the interpreter's ABI, and one torch by its place and version."""
+    torch_dir = _torch_dir()
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        return "\n".join([EXT_SUFFIX, torch_dir, f.read()])
+
+
+def calls_fit() -> bool:
+    """Whether the compiled calls were built for the interpreter and torch that run now."""
+    if not os.path.exists(CALLS_STAMP):
+        return False
+    with open(CALLS_STAMP) as f:
+        return f.read() == _environment()
 
 
 def _compile(nvcc: str, src: str, verbose: bool) -> str:
@@ -115,11 +131,14 @@ def _link_library(nvcc: str, objs) -> None:
 
 def _link_calls(obj: str) -> None:
     # finds the library beside itself, and torch's where they were when it was built
-    torch_lib, tmp = os.path.join(_torch_dir(), "lib"), CALLS_PATH + ".tmp"
+    torch_lib, tmp, stamp = os.path.join(_torch_dir(), "lib"), CALLS_PATH + ".tmp", CALLS_STAMP + ".tmp"
     _run(["g++", "-shared", "-o", tmp, obj, "-L" + PKG_DIR, "-l:" + LIB_NAME, "-L" + torch_lib, "-ltorch_python",
           "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib],
          "link of the compiled calls")
+    with open(stamp, "w") as f:
+        f.write(_environment())
     os.replace(tmp, CALLS_PATH)
+    os.replace(stamp, CALLS_STAMP)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

@@ -62,3 +62,26 @@ def test_a_failing_compilation_of_the_calls_leaves_the_library(made, monkeypatch
     with pytest.raises(RuntimeError, match="calls.cpp failed"):
         build.build()
     assert os.path.exists(build.LIB_PATH) and not os.path.exists(build.CALLS_PATH)
+
+
+def test_the_calls_are_made_for_one_python_and_one_torch(made, monkeypatch, tmp_path):
+    """Another torch counts whatever the age of its files, another interpreter by its ABI, and neither's module is loaded."""
+    from exact_attention_72_gb300 import binding
+    assert os.path.basename(build.CALLS_PATH) == "_calls" + build.EXT_SUFFIX
+    assert not build.calls_fit()                       # nothing built yet
+    build.build()
+    assert build.calls_fit() and build.up_to_date()
+    torch = tmp_path / "other" / "torch"
+    torch.mkdir(parents=True)
+    (torch / "version.py").write_text("__version__ = '0'\n")
+    os.utime(torch / "version.py", (0, 0))             # older than the module
+    with monkeypatch.context() as m:
+        m.setattr(build, "_torch_dir", lambda: str(torch))
+        assert not build.calls_fit() and not build.up_to_date()
+        m.setattr(binding, "_CALLS", None)
+        m.setattr(binding, "lib", lambda: None)
+        with pytest.raises(RuntimeError, match="another Python or torch"):
+            binding._calls()
+    assert build.up_to_date()
+    monkeypatch.setattr(build, "EXT_SUFFIX", ".cpython-399-other.so")
+    assert not build.calls_fit()
