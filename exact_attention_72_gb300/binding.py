@@ -503,7 +503,7 @@ def _calls():
     """The compiled calls (csrc/calls.cpp), loaded with the library they link to."""
     global _CALLS
     if _CALLS is None:
-        import torch  # noqa: F401  (its libraries first)
+        import torch   # its libraries first
         lib()
         if not os.path.exists(_build.CALLS_PATH):
             raise RuntimeError(os.path.basename(_build.CALLS_PATH) + " is not built; call exact_attention_72_gb300.build.build()")
@@ -511,7 +511,7 @@ def _calls():
             raise RuntimeError(os.path.basename(_build.CALLS_PATH) + " was built for another Python or torch; call "
                                "exact_attention_72_gb300.build.build() again")
         from . import _calls as module
-        module.set_error(AttnError)
+        module.set_errors(AttnError, torch.OutOfMemoryError)
         _CALLS = module
     return _CALLS
 

@@ -25,7 +25,7 @@
 
 namespace {
 
-PyObject* g_attn_error = nullptr;   // binding.AttnError
+PyObject *g_attn_error = nullptr, *g_out_of_memory = nullptr;   // binding.AttnError, torch.OutOfMemoryError
 
 struct Refused : std::runtime_error {   // ValueError
   using std::runtime_error::runtime_error;
@@ -224,7 +224,7 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F&& f) {
   } catch (const WrongType& e) {
     PyErr_SetString(PyExc_TypeError, e.what());
   } catch (const c10::OutOfMemoryError& e) {
-    PyErr_SetString(PyExc_MemoryError, e.what_without_backtrace());
+    PyErr_SetString(g_out_of_memory, e.what_without_backtrace());   // as torch's own allocations do
   } catch (const c10::Error& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
   } catch (const std::exception& e) {
@@ -442,10 +442,14 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-PyObject* set_error(PyObject*, PyObject* e) {
-  Py_INCREF(e);
-  Py_XSETREF(g_attn_error, e);
-  return none();
+// AttnError, torch.OutOfMemoryError: once, before the first call.
+PyObject* set_errors(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 2, [&] {
+    Py_INCREF(a[0]), Py_INCREF(a[1]);
+    Py_XSETREF(g_attn_error, a[0]);
+    Py_XSETREF(g_out_of_memory, a[1]);
+    return none();
+  });
 }
 
 #define FAST(f) (PyCFunction)(void (*)())(f), METH_FASTCALL
@@ -454,7 +458,7 @@ PyMethodDef methods[] = {{"qk_norm_rope", FAST(qk_norm_rope), nullptr},
                          {"paged_append", FAST(paged_append), nullptr},
                          {"paged_gather", FAST(paged_gather), nullptr},
                          {"fwd_paged", FAST(fwd_paged), nullptr},
-                         {"set_error", set_error, METH_O, nullptr},
+                         {"set_errors", FAST(set_errors), nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -682,3 +682,11 @@ def test_rotation_rounds_both_products(d, rd, il):
     assert bool((got[..., first][..., sign > 0] == 0).all()) and bool((got[..., second][..., sign < 0] == 0).all())
     want = a.float() * t[:, None] * 2
     assert torch.allclose(got[..., second][..., sign > 0].float(), want[..., sign > 0], rtol=2 ** -8 + 2 ** -22, atol=0)
+
+
+def test_no_room_for_an_output_is_torchs_error():
+    """What torch.empty raises there, as in the rest of the binding: what a caller's retry catches. Nothing is launched."""
+    cache, cu, table = binding.PagedKVCache.allocate(1, 16, 64, 256), i32([0, 1 << 28]), i32([[0]])
+    with pytest.raises(torch.OutOfMemoryError):     # 2^28 rows of 64 * 256 bf16 values: 8 TB
+        binding.attn_paged_gather(cache, cu, table, 1 << 28)
+    ok()
