@@ -645,7 +645,8 @@ def attn_fwd_paged(q, cache: PagedKVCache, page_table, seqlens, causal: bool = T
     """Attention of q [B, Nq, H, d] (bf16) over the cache: (out bf16 [B, Nq, H, d], lse float32 [B, H, Nq]).
 
     ``seqlens`` (int32 [B]) counts each sequence's keys, the Nq new tokens' own among them; with ``causal``
-    query i sees keys j <= i + seqlens[b] - Nq. Rows that see no key give 0 and -inf. ``workspace`` (CUDA
+    query i sees keys j <= i + seqlens[b] - Nq. Rows that see no key give 0 and -inf; a batch without sequences or
+    queries gives tensors without values, like the other calls (the C entry takes B, Nq >= 1). ``workspace`` (CUDA
     uint8, at least attn_fwd_paged_workspace_bytes(...)) is allocated here with torch if not given.
     """
     call = (_CALLS or _calls()).fwd_paged

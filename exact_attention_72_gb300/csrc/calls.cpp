@@ -432,12 +432,14 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int causal = truth(a[5]);
     const float scale = a[6] == Py_None ? (float)(1.0 / std::sqrt((double)d)) : (float)number(a[6]);
     const cudaStream_t s = p.stream({&p.table, &q, &lens, ws, out, lse});
-    const Workspace work(ws, ws ? 0 : attn_fwd_paged_workspace_bytes(p.B, H, p.cache->Hkv, Nq, d, p.cache->type));
+    const bool any_rows = p.B > 0 && Nq > 0;   // nothing to launch for otherwise
+    const Workspace work(ws, ws || !any_rows ? 0 : attn_fwd_paged_workspace_bytes(p.B, H, p.cache->Hkv, Nq, d, p.cache->type));
     Out o(a[8], out, q.sizes(), at::kBFloat16, q), l(a[9], lse, at::IntArrayRef(rows, 3), at::kFloat, q);
-    check_status(launch([&] {
-      return attn_fwd_paged(q.data_ptr(), p.cache, o.ptr, (float*)l.ptr, (const int*)p.table.data_ptr(), p.stride, p.max_pages,
-                            lenp, p.B, H, Nq, scale, causal, work.ptr, work.bytes, s);
-    }), "attn_fwd_paged");
+    if (any_rows)
+      check_status(launch([&] {
+        return attn_fwd_paged(q.data_ptr(), p.cache, o.ptr, (float*)l.ptr, (const int*)p.table.data_ptr(), p.stride, p.max_pages,
+                              lenp, p.B, H, Nq, scale, causal, work.ptr, work.bytes, s);
+      }), "attn_fwd_paged");
     return tuple({o.object(), l.object()});
   });
 }

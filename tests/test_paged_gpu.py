@@ -690,3 +690,22 @@ def test_no_room_for_an_output_is_torchs_error():
     with pytest.raises(torch.OutOfMemoryError):     # 2^28 rows of 64 * 256 bf16 values: 8 TB
         binding.attn_paged_gather(cache, cu, table, 1 << 28)
     ok()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int4"])
+def test_batches_without_sequences_or_tokens(kind):
+    """Every call of a decoding step takes them, as the norm does, and leaves the cache as it was."""
+    cache = binding.PagedKVCache.allocate(4, 16, 2, 128, kind)
+    for B, Nq in ((0, 1), (0, 3), (2, 0), (0, 0)):
+        q = torch.empty((B, Nq, 8, 128), dtype=torch.bfloat16, device="cuda")
+        table, lens = torch.zeros((B, 2), dtype=torch.int32, device="cuda"), torch.full((B,), 5, dtype=torch.int32, device="cuda")
+        for ws in (None, torch.empty(256, dtype=torch.uint8, device="cuda")):
+            o, lse = binding.attn_fwd_paged(q, cache, table, lens, workspace=ws)
+            assert o.shape == (B, Nq, 8, 128) and o.dtype == torch.bfloat16 and lse.shape == (B, 8, Nq) and lse.dtype == torch.float32
+        out = torch.empty_like(q)
+        assert binding.attn_fwd_paged(q, cache, table, lens, out=out)[0] is out
+        k, cu = torch.empty((0, 2, 128), dtype=torch.bfloat16, device="cuda"), torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+        binding.attn_paged_append(cache, k, k, cu, lens, table)
+        assert binding.attn_paged_gather(cache, cu, table, 0)[0].shape == (0, 2, 128)
+    ok()
+    assert not bool(cache.k.any()) and not bool(cache.v.any())
