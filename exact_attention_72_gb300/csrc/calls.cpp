@@ -102,12 +102,14 @@ struct Rope {   // angle tables [max_pos, rope_dim / 2]
   int dim = 0, max_pos = 0;
 };
 
-Rope rope_of(const at::Tensor* cos, const at::Tensor* sin) {
+// For tokens of them: a table without entries has no address, and would read as none given.
+Rope rope_of(const at::Tensor* cos, const at::Tensor* sin, long long tokens) {
   Rope r;
   if (!cos && !sin) return r;
   if (!cos || !sin || cos->scalar_type() != at::kFloat || sin->scalar_type() != at::kFloat || cos->dim() != 2 ||
       cos->sizes() != sin->sizes() || !cos->is_contiguous() || !sin->is_contiguous())
     refuse("cos and sin must be contiguous float32 CUDA tensors [max_pos, rope_dim / 2], both or neither");
+  if (tokens > 0 && cos->numel() == 0) refuse("cos and sin hold no angles");
   r.cos = (const float*)cos->data_ptr(), r.sin = (const float*)sin->data_ptr();
   r.dim = as_int(2 * cos->size(1), "rope_dim"), r.max_pos = as_int(cos->size(0), "max_pos");
   return r;
@@ -267,7 +269,7 @@ struct NormRope {
     if (positions && (positions->scalar_type() != at::kInt || positions->sizes() != q.sizes().slice(0, q.dim() - 2) ||
                       !positions->is_contiguous()))
       refuse("positions must be a contiguous int32 CUDA tensor, one per token");
-    rope = rope_of(cos, sin);
+    rope = rope_of(cos, sin, rq.T);
     wqp = vector_of(wq, "wq", rq.d), wkp = vector_of(wk, "wk", rq.d);
     T = as_int(rq.T, "the number of tokens"), H = as_int(rq.heads, "heads"), Hkv = as_int(rk.heads, "heads");
     d = as_int(rq.d, "d"), N = as_int(rq.N, "the number of tokens");
@@ -377,7 +379,7 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Rows rk = rows_of(k, "k"), rv = rows_of(v, "v");
     if (k.dim() != 3 || v.sizes() != k.sizes() || rk.heads != p.cache->Hkv || rk.d != p.cache->d)
       refuse("k and v must be [total, Hkv, d] with the cache's heads");
-    const Rope rope = rope_of(cos, sin);
+    const Rope rope = rope_of(cos, sin, rk.T);
     const int total = as_int(rk.T, "the number of tokens"), interleaved = truth(a[9]);
     const cudaStream_t s = p.stream({&p.table, &k, &v, &cu, &lens, cos, sin});
     if (total > 0 && p.B > 0)

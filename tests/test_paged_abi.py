@@ -204,3 +204,20 @@ def test_a_workspace_has_the_bytes_that_its_size_says():
             calls.fwd_paged(ctypes.addressof(c), 0, q, table, lens, True, None, ws, None, None)
         with pytest.raises(ValueError, match="workspace must be a contiguous"):
             binding.attn_qk_norm_rope_bwd(x, None, x, wq=w, workspace=ws)
+
+
+@pytest.mark.parametrize("shape", [(0, 64), (50, 0), (0, 0)])
+def test_tables_without_angles_are_no_rotation_left_out(shape):
+    """cos[:n] with n = 0 is a mistake of the caller's, not a call without rotation; refused before the tensors' device counts."""
+    t = torch.zeros(shape)
+    x = torch.zeros(4, 8, 128, dtype=torch.bfloat16)
+    ints = [torch.zeros(n, dtype=torch.int32) for n in (2, 1)]
+    with pytest.raises(ValueError, match="no angles"):
+        binding.attn_qk_norm_rope(x, cos=t, sin=t)
+    with pytest.raises(ValueError, match="no angles"):
+        binding.attn_qk_norm_rope_bwd(x, None, x, cos=t, sin=t)
+    c = cache(Hkv=8)
+    with pytest.raises(ValueError, match="no angles"):
+        binding._calls().paged_append(ctypes.addressof(c), 0, x, x, *ints, torch.zeros(1, 2, dtype=torch.int32), t, t, False)
+    with pytest.raises(ValueError, match="on the current device"):     # without tokens there is nothing to turn
+        binding.attn_qk_norm_rope(x[:0], cos=t, sin=t)
