@@ -571,8 +571,11 @@ class PagedKVCache:
         if four != (v_sz is not None):
             raise ValueError("a 4-bit cache has both k_sz and v_sz")
         want = torch.uint8 if four else torch.bfloat16
+
+        def strides(t):     # of page, token and head; that of a single one says nothing
+            return [t.stride(i) if t.size(i) > 1 else 0 for i in range(3)]
         for name, t in (("k", k), ("v", v)):
-            if t.dtype != want or t.dim() != 4 or t.stride(-1) != 1 or t.shape != k.shape or t.stride() != k.stride() or \
+            if t.dtype != want or t.dim() != 4 or t.stride(-1) != 1 or t.shape != k.shape or strides(t) != strides(k) or \
                     not t.is_cuda or t.device != k.device:
                 raise ValueError(f"{name} must be a {want} CUDA tensor [num_pages, page_size, Hkv, row] with contiguous "
                                  "rows, k and v alike")
@@ -582,17 +585,17 @@ class PagedKVCache:
         if four:
             for name, t in (("k_sz", k_sz), ("v_sz", v_sz)):
                 if t.dtype != torch.bfloat16 or t.shape != (P, S, Hkv, d // ATTN_INT4_GROUP, 2) or \
-                        t.stride() != k_sz.stride() or t.stride(-1) != 1 or \
+                        strides(t) != strides(k_sz) or t.stride(-1) != 1 or \
                         (t.shape[3] > 1 and t.stride(3) != 2) or t.device != k.device:
                     raise ValueError(f"{name} must be a bfloat16 CUDA tensor [num_pages, page_size, Hkv, d / 64, 2] with "
                                      "contiguous rows, k_sz and v_sz alike")
-            sz = k_sz.stride()[:3]
+            sz = strides(k_sz)
         self.k, self.v, self.k_sz, self.v_sz = k, v, k_sz, v_sz
         self.num_pages, self.page_size, self.Hkv, self.d = P, S, Hkv, d
         self.type = ATTN_CACHE_INT4 if four else ATTN_CACHE_BF16
         self.device = k.device
         self._struct = _PagedCacheStruct(k.data_ptr(), v.data_ptr(), k_sz.data_ptr() if four else None,
-                                         v_sz.data_ptr() if four else None, *k.stride()[:3], *sz, P, S, Hkv, d,
+                                         v_sz.data_ptr() if four else None, *strides(k), *sz, P, S, Hkv, d,
                                          self.type)
         self._address, self._index = ctypes.addressof(self._struct), k.get_device()   # what the calls take
 

@@ -709,3 +709,21 @@ def test_batches_without_sequences_or_tokens(kind):
         assert binding.attn_paged_gather(cache, cu, table, 0)[0].shape == (0, 2, 128)
     ok()
     assert not bool(cache.k.any()) and not bool(cache.v.any())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int4"])
+def test_strides_of_single_pages_and_heads_of_a_cache_do_not_count(kind):
+    """As those of single tokens: k's and v's may differ there, and need not be multiples of a row's pieces."""
+    plain = binding.PagedKVCache.allocate(1, 16, 1, 64, kind)
+    other = binding.PagedKVCache.allocate(1, 16, 1, 64, kind)
+
+    def odd(t, page, head):
+        return None if t is None else torch.as_strided(t, t.shape, (page, t.stride(1), head, *t.stride()[3:]))
+    cache = binding.PagedKVCache(odd(other.k, 1, 1), odd(other.v, 3, 5), odd(other.k_sz, 1, 1), odd(other.v_sz, 7, 3))
+    k, v, q = randn((9, 1, 64), 1), randn((9, 1, 64), 2), randn((1, 1, 4, 64), 3)
+    got = []
+    for c in (plain, cache):
+        binding.attn_paged_append(c, k, v, i32([0, 9]), i32([0]), i32([[0]]))
+        got.append((*binding.attn_fwd_paged(q, c, i32([[0]]), i32([9])), *binding.attn_paged_gather(c, i32([0, 9]), i32([[0]]), 9)))
+    ok()
+    assert all(torch.equal(x, y) for x, y in zip(*got))
