@@ -299,3 +299,97 @@ def test_values_behind_the_rotated_ones_are_unchanged(d, rd, il, value):
         w[..., rd:] = x[..., rd:]
         same = y.view(torch.int16) == w.view(torch.int16)
         assert bool((same | (y.isnan() & w.isnan())).all())
+
+
+def plain64(x, pos, w, cos, sin, norm, il, dy=None, eps=1e-5):
+    """The forward, or with dy (dx, dw, sum |du n|), in 64 bits on the GPU."""
+    x, d, half = x.double(), x.shape[-1], 0 if cos is None else cos.shape[1]
+    first, second = (slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if il else (slice(0, half), slice(half, 2 * half))
+
+    def turn(u, sign):
+        y = u.clone()
+        if half:
+            c, s = cos.double()[pos.long()][:, None], sign * sin.double()[pos.long()][:, None]
+            y[..., first], y[..., second] = u[..., first] * c - u[..., second] * s, u[..., second] * c + u[..., first] * s
+        return y
+    n, r = x, 1.0
+    if norm:
+        r = 1 / (x.square().mean(-1, keepdim=True) + eps).sqrt()
+        n = x * r
+    wd = 1.0 if w is None else w.double()
+    if dy is None:
+        return turn(n * wd, 1.0)
+    du = turn(dy.double(), -1.0)
+    if not norm:
+        return du, None, None
+    g = du * wd
+    return r * (g - n * (g * n).mean(-1, keepdim=True)), (du * n).sum((0, 1)), (du * n).abs().sum((0, 1))
+
+
+LONG = [
+    # more tasks than threads take in one round, and no multiple of it
+    (6001, 12, 4, 128, 128, True, True, False, True),       # T, H, Hkv, d, rope_dim, norm, weights, interleaved, fused
+    (3001, 9, 3, 256, 128, True, True, True, True),
+    (9003, 8, 2, 64, 32, True, True, False, False),
+    (5003, 13, 0, 128, 64, False, False, False, False),
+    (4999, 7, 7, 128, 0, True, True, False, True),
+]
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("case", LONG, ids=str)
+def test_threads_with_several_tasks(case, in_place):
+    """Rows of the next task are loaded while those of one are turned. Bounds as above; a thread adds the terms of at most 6
+    tasks, 24, a CTA at most 32 threads, the last kernel 10 sums and 32 of those: still below 128 roundings. Two tokens have
+    positions outside the tables, one in the last round: not written, and not in the weights' gradients."""
+    T, H, Hkv, d, rd, norm, weights, il, fused = case
+    q, k, w, dy, pos = make(T, H, Hkv, d, 21, fused and not in_place)
+    kw = kwargs(case, w, pos)
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    if rd:
+        pos[5], pos[T - 2] = 50, -1
+        keep[5] = keep[T - 2] = False
+    outs = [x.clone() if in_place and x is not None else None for x in (q, k)]
+    args = outs if in_place else [q, k]
+    plain = lambda x, wx, g=None: plain64(x[keep], pos[keep], wx, kw["cos"], kw["sin"], norm, il, None if g is None else g[keep])
+    try:
+        got = binding.attn_qk_norm_rope(*args, **kw, q_out=outs[0], k_out=outs[1])
+        g = [x.clone() for x in dy]
+        grads = binding.attn_qk_norm_rope_bwd(q, k, g[0], g[1] if Hkv else None, **kw, dq=g[0] if in_place else None,
+                                              dk=g[1] if in_place and Hkv else None)
+        st = binding.attn_get_status()
+        assert st == ((binding.ATTN_ERR_INVALID_ARG, 0x2000000E) if rd else (binding.ATTN_OK, 0))
+    finally:
+        binding.attn_clear_status()
+    for i, (x, wx) in enumerate(((q, kw["wq"]), (k, kw["wk"]))):
+        if x is None:
+            continue
+        ref = plain(x, wx)
+        top = ref.abs().amax(-1, keepdim=True) * 2 ** 0.5
+        assert bool(((got[i][keep].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 32 * 2.0 ** -24 * top).all())
+        dx, dw, size = plain(x, wx, dy[i])
+        du = plain64(x[keep], pos[keep], wx, kw["cos"], kw["sin"], False, il, dy[i][keep])[0]
+        room = du.abs().amax(-1, keepdim=True) * 2
+        if norm:
+            r = 1 / (x[keep].double().square().mean(-1, keepdim=True) + 1e-5).sqrt()
+            n, gw = x[keep].double() * r, du * (1 if wx is None else wx.double())
+            room = r * (gw.abs().amax(-1, keepdim=True) * 2 + n.abs().amax(-1, keepdim=True) * (gw * n).abs().mean(-1, keepdim=True))
+        assert bool(((grads[i][keep].double() - dx).abs() <= 2.0 ** -8 * dx.abs() + 64 * 2.0 ** -24 * room).all())
+        if wx is not None:
+            assert bool(((grads[2 + i].double() - dw).abs() <= 128 * 2.0 ** -24 * size).all())
+        if in_place:      # rows without a position are as they were
+            assert torch.equal(got[i][~keep], x[~keep]) and torch.equal(grads[i][~keep], dy[i][~keep])
+
+
+def test_the_plain_form_is_the_oracles():
+    q, _, w, dy, pos = make(9, 3, 1, 64, 22)
+    cos, sin = tables(50, 16)
+    for norm, il in ((True, False), (True, True), (False, True)):
+        wx = w[0] if norm else None
+        okw = dict(w=None if wx is None else f64(wx), eps=1e-5, norm=norm, cos=f64(cos), sin=f64(sin), interleaved=il)
+        p = f64(pos).astype(int)
+        y = plain64(q, pos, wx, cos, sin, norm, il)
+        dx, dw, _ = plain64(q, pos, wx, cos, sin, norm, il, dy[0])
+        ref_dx, ref_dw = oracle.norm_rope_backward(f64(q), f64(dy[0]), p, **okw)
+        for a, b in ((y, oracle.norm_rope(f64(q), p, **okw)), (dx, ref_dx), (dw, ref_dw if norm else None)):
+            assert b is None or np.abs(a.cpu().numpy() - b).max() <= 1e-12 * (1 + np.abs(b).max())
