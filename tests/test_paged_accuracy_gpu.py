@@ -1,13 +1,14 @@
 """Attention over the paged cache, value by value: what the kernels' arithmetic allows, not a share of the greatest value.
 
 check_each, with t the terms a value is summed from (bf16: v; 4 bits: scale * code and zero apart) and A = sum_j P_j |t_j|:
-  scores: fp32 sums of d exact products and a few operations: dS = 32 * 2^-23 of scale * sum|q||k| (4 bits: of |q| times
+  scores: fp32 sums of d exact products. A matrix product may cut each of the 16 terms it adds, and the sum so far, at 24 bits of
+      the greatest: with 8 further roundings dS = (17 d / 16 + 8) * 2^-23 of scale * sum|q||k| (4 bits: of |q| times
       |zero| + scale * code), the greatest over the keys; a weight moves by dS of itself, and so does their sum: 2 dS A.
   weights: two bf16 numbers, 2^-8 * 2^-8, or (times scale) two fp16 numbers, 2^-11 * 2^-11, of themselves. The second fp16
       number is 2^-25 off at least, where the group's greatest weight times scale is 2^3 or more (2^4 when it is set, at most
       one bit less after a move): 2^-28 of the group's greatest, 15 codes, for each key.
-  sums: 64 fp32 roundings; a matrix product may cut each of the 16 terms it adds, and the sum so far, at 24 bits of the greatest,
-      17 * 2^-23. The calls here have so few keys that a warp's share holds at most two tiles of 32 (16) keys: 8 products.
+  sums: 64 fp32 roundings, and 17 * 2^-23 a product. The calls here have so few keys that a warp's share holds at most two
+      tiles of 32 (16) keys: 8 products.
   output: bf16, 2^-8 of the value. LSE: dS and 2^-19 (1 + |LSE|).
 """
 import numpy as np
@@ -15,7 +16,8 @@ import pytest
 import torch
 
 from oracle import paged
-from test_paged_gpu import attend, make_cache, make_table, np32, randn
+from exact_attention_72_gb300 import binding
+from test_paged_gpu import attend, i32, make_cache, make_table, np32, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -73,7 +75,7 @@ def check_each(q, o, lse, held, scale, causal=True):
                 top = S.max()
                 L = top + np.log(np.exp(S - top).sum())
                 P = np.exp(S - L)
-                dS = 32 * 2.0 ** -23 * abs(scale) * (ksize[:m, j] @ np.abs(qn[b, i, h])).max()
+                dS = (17 * d / 16 + 8) * 2.0 ** -23 * abs(scale) * (ksize[:m, j] @ np.abs(qn[b, i, h])).max()
                 want, A = P @ vals[:m, j], P @ vsize[:m, j]
                 rel = 2.0 ** -22 if four else 2.0 ** -16
                 room = 2.0 ** -8 * np.abs(want) + (rel + 2 * dS + (64 + 8 * 17) * 2.0 ** -23) * A
@@ -127,3 +129,78 @@ def test_a_small_group_keeps_its_bits_beside_a_large_one(d, H, bits, early):
         q = torch.tensor(q).bfloat16().cuda()
         o, lse = attend(q, cache, table, [n])
         check_each(q, o, lse, held, d ** -0.5)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int4"])
+@pytest.mark.parametrize("d,H,Hkv,Nq", [(64, 4, 2, 1), (128, 8, 1, 1), (128, 4, 2, 3), (128, 16, 1, 1), (64, 12, 1, 1),
+                                        (256, 4, 2, 1), (256, 12, 1, 1)])
+def test_every_value(kind, d, H, Hkv, Nq):
+    """Lengths from one token to units that are cut, each row by its own bound: a long sequence's small values, and what the
+    second number of each weight leaves, show beside a short one's."""
+    lens = [1, 33, 0, 6000, 200, 2, 900]
+    table, pages = make_table(lens, 16, 4)
+    cache = make_cache(kind, pages, 16, Hkv, d)
+    r = np.random.default_rng(5)
+    held = write(cache, table, [(normal(r, n, Hkv, d), normal(r, n, Hkv, d)) for n in lens])
+    q = randn((len(lens), Nq, H, d), 6, 2.0)
+    o, lse = attend(q, cache, table, lens)
+    check_each(q, o, lse, held, d ** -0.5)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int4"])
+def test_every_row_of_prefill_and_decode_lies_where_it_belongs(kind):
+    """Prompts, then tokens one at a time out of a captured graph: each row of the cache is the one that norm, rotation and (4
+    bits) the oracle's quantisation give for its token, bit for bit, and what the last step attends to is those rows."""
+    B, H, Hkv, d, ps, steps = 3, 6, 2, 128, 16, 19
+    prompts = [37, 90, 0]
+    table, pages = make_table([n + steps + 1 for n in prompts], ps, 4)
+    cache = make_cache(kind, pages, ps, Hkv, d)
+    a = np.arange(200)[:, None] * 10000.0 ** (-np.arange(d // 2) / (d // 2))
+    cos, sin = (torch.tensor(f(a), dtype=torch.float32).cuda() for f in (np.cos, np.sin))
+    w = [torch.ones(d, device="cuda") * 1.5, torch.ones(d, device="cuda") * 0.75]
+    total = sum(prompts)
+    x = randn((total, H + 2 * Hkv, d), 5)
+    pos = i32(np.concatenate([np.arange(n) for n in prompts]))
+    _, k = binding.attn_qk_norm_rope(x[:, :H], x[:, H:H + Hkv], cos, sin, pos, *w)
+    tab, lens, cu1 = i32(table), i32(prompts), i32([0, 1, 2, 3])
+    binding.attn_paged_append(cache, k, x[:, H + Hkv:], i32(np.concatenate(([0], np.cumsum(prompts)))), i32([0, 0, 0]), tab)
+    x1 = torch.empty((B, H + 2 * Hkv, d), dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        q1, k1 = binding.attn_qk_norm_rope(x1[:, :H], x1[:, H:H + Hkv], cos, sin, lens, *w)
+        binding.attn_paged_append(cache, k1, x1[:, H + Hkv:], cu1, lens, tab)
+        lens.add_(1)
+        return q1, *binding.attn_fwd_paged(q1.unsqueeze(1), cache, tab, lens)
+    news = [randn((B, H + 2 * Hkv, d), 100 + i) for i in range(steps)]
+    x1.copy_(news[0])
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q1, o, lse = step()
+    for new in news[1:]:
+        x1.copy_(new)
+        graph.replay()
+    ends = [n + steps for n in prompts]
+    assert lens.tolist() == ends
+    got = binding.attn_paged_gather(cache, i32(np.concatenate(([0], np.cumsum(ends)))), tab, sum(ends))
+    assert binding.attn_get_status()[0] == binding.ATTN_OK
+    rows = [[np32(y[sum(prompts[:b]):sum(prompts[:b + 1])]) for b in range(B)] for y in (k, x[:, H + Hkv:])]
+    for i, new in enumerate(news):
+        _, k1 = binding.attn_qk_norm_rope(new[:, :H], new[:, H:H + Hkv], cos, sin, i32([n + i for n in prompts]), *w)
+        for j, y in enumerate((k1, new[:, H + Hkv:])):
+            rows[j] = [np.concatenate((old, np32(y[b:b + 1]))) for b, old in enumerate(rows[j])]
+    held = []
+    for b in range(B):
+        one = []
+        for j in range(2):
+            here = np32(got[j][sum(ends[:b]):sum(ends[:b + 1])])
+            if kind == "bf16":
+                assert np.array_equal(here, rows[j][b]), (b, j)
+                one.append((np.float64(rows[j][b]), np.abs(np.float64(rows[j][b])), np.zeros(rows[j][b].shape)))
+            else:
+                codes, scale, zero = paged.quantise(rows[j][b])
+                value = paged.values(codes, scale, zero)
+                assert np.array_equal(here, paged.bf16_nearest(np.float32(value))), (b, j)
+                one.append((value, paged.values(codes, np.abs(scale), np.abs(zero)), np.repeat(15 * np.float64(scale), 64, -1)))
+        held.append((one[0][0], one[1][0], one[0][1], one[1][1], one[1][2]))
+    check_each(q1.unsqueeze(1), o, lse, held, d ** -0.5)
