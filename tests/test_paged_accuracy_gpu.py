@@ -204,3 +204,21 @@ def test_every_row_of_prefill_and_decode_lies_where_it_belongs(kind):
                 one.append((value, paged.values(codes, np.abs(scale), np.abs(zero)), np.repeat(15 * np.float64(scale), 64, -1)))
         held.append((one[0][0], one[1][0], one[0][1], one[1][1], one[1][2]))
     check_each(q1.unsqueeze(1), o, lse, held, d ** -0.5)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [40, 20000])     # finished by one warp, and cut over many
+def test_a_bad_query_row_among_few_stays_one_row(d, n):
+    """With at most 4 rows each holds two columns of the products."""
+    table, pages = make_table([n], 16, 1)
+    cache = make_cache("int4", pages, 16, 1, d)
+    r = np.random.default_rng(8)
+    held = write(cache, table, [(normal(r, n, 1, d), normal(r, n, 1, d))])
+    q = randn((1, 1, 4, d), 5)
+    bad = q.clone()
+    bad[0, 0, 2, 7] = float("nan")
+    o, lse = attend(bad, cache, table, [n])
+    assert bool(torch.isnan(o[0, 0, 2]).all()) and bool(torch.isnan(lse[0, 2]).all())
+    good, all_lse = attend(q, cache, table, [n])
+    o[0, 0, 2], lse[0, 2] = good[0, 0, 2], all_lse[0, 2]
+    check_each(q, o, lse, held, d ** -0.5)
