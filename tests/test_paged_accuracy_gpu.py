@@ -222,3 +222,40 @@ def test_a_bad_query_row_among_few_stays_one_row(d, n):
     good, all_lse = attend(q, cache, table, [n])
     o[0, 0, 2], lse[0, 2] = good[0, 0, 2], all_lse[0, 2]
     check_each(q, o, lse, held, d ** -0.5)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int4"])
+@pytest.mark.parametrize("d,H,Hkv", [(128, 32, 8), (64, 32, 8), (128, 16, 2), (64, 24, 2), (256, 8, 4)])
+def test_long_sums_do_not_drift(kind, d, H, Hkv):
+    """Hundreds of tiles in every warp's share: 64 sequences of 65536 keys, 4096 of them over and over. Two
+    neighbours have the same key, so the same weight, and the same values with the sign turned (4 bits: zero is -7.5 scale, codes c
+    and 15 - c): O is 0, what is there is the sums' error. Round to nearest errs up as often as down: over N sums of size A it is
+    sqrt(N) 2^-24 A in the mean square, and 4 times that is allowed. A cut towards 0 at each sum would be N 2^-25 A."""
+    n, times, B = 4096, 16, 64
+    table, pages = make_table([n], 64, 4, spare=0)
+    cache = make_cache(kind, pages, 64, Hkv, d)
+    r = np.random.default_rng(9)
+    v = normal(r, n, Hkv, d)
+    v[1::2] = -v[::2]
+    k = normal(r, n, Hkv, d)
+    k[1::2] = k[::2]
+    held = write(cache, table, [(k, v)])[0]
+    size = np.abs(v).mean(0)
+    if kind == "int4":
+        codes = torch.randint(0, 256, (n // 2, Hkv, d // 2), generator=torch.Generator().manual_seed(1), dtype=torch.uint8)
+        scale = torch.randint(9, 16, (n // 2, Hkv, d // 64), generator=torch.Generator().manual_seed(2)) / 32
+        pg, at = (torch.tensor(x).cuda() for x in np.array([paged.place(table[0], p, 64) for p in range(n)]).T)
+        cache.v[pg, at] = torch.stack((codes, 255 - codes), 1).flatten(0, 1).cuda()
+        cache.v_sz[pg, at] = torch.stack((scale, -7.5 * scale), -1).bfloat16().repeat_interleave(2, 0).cuda()
+        size = np.full((Hkv, d), 15 * float(scale.mean()))      # zero and codes, 7.5 scale each; 4 bits of scale: both exact
+    q = randn((B, 1, H, d), 6, 0.5)
+    o, lse = attend(q, cache, np.tile(table, (B, times)), [n * times] * B)
+    sums = B * Hkv * n * times / 16 / 1000      # at least 1000 warps; a sum for every 16 keys
+    rows = np.float64(np32(o)).reshape(B, Hkv, H // Hkv, d)
+    room = 4 * sums ** 0.5 * 2.0 ** -24 * np.sqrt((size ** 2).mean(-1))
+    assert np.all(np.sqrt((rows ** 2).mean(-1)) <= room[None, :, None]), float((np.sqrt((rows ** 2).mean(-1)) / room[None, :, None]).max())
+    for b, h in ((0, 0), (B - 1, H - 1)):
+        S = d ** -0.5 * (held[0][:, h // (H // Hkv)] @ np.float64(np32(q[b, 0, h])))
+        L = S.max() + np.log(np.exp(S - S.max()).sum()) + np.log(times)
+        dS = (17 * d / 16 + 8) * 2.0 ** -23 * d ** -0.5 * (held[2][:, h // (H // Hkv)] @ np.abs(np.float64(np32(q[b, 0, h])))).max()
+        assert abs(float(lse[b, h, 0]) - L) <= dS + 2.0 ** -19 * (1 + abs(L))
