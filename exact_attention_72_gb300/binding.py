@@ -89,6 +89,7 @@ def lib() -> ctypes.CDLL:
     L.attn_fwd_splitkv_workspace_bytes.argtypes = [i, i, i, i, i]
     L.attn_fwd_host_workspace_bytes.restype = sz
     L.attn_fwd_host_workspace_bytes.argtypes = [i, i, i, i, i, i]
+    # The launching entries from here on are for callers of the C ABI (the refusal tests): the functions below go through _calls().
     ll, cache = ctypes.c_longlong, ctypes.POINTER(_PagedCacheStruct)
     L.attn_qk_norm_rope.restype = i
     L.attn_qk_norm_rope.argtypes = [vp] * 4 + [i] * 4 + [ll] * 4 + [i, vp, vp, f, vp, vp, i, i, i, vp, i, vp]

@@ -39,12 +39,12 @@
 // Matrix loads hand out the operands, those of V transposed: a 16-bit unit of them is one bf16 value or four codes.
 //
 // Measured on a GB300 (us in a CUDA graph, share of the copy bandwidth; H 32, Hkv 8, d 128 if not said otherwise):
-//   bf16, B 8, 16384 keys                85    93%
-//   4 bits, B 8, 16384 keys              35    64%: about 5 us until the first tiles are there and 5 us to join the parts;
-//                                              between them the tiles stream at 99%
-//   4 bits, B 32, up to 32768 keys       99    85%
-//   bf16, d 256, B 13, up to 5000 keys, 12 rows (two blocks, the second out of L2)  35    51%
-// What it took, at B 8 and 16384 keys in 4 bits: tiles of one CTA with lane-wise operand loads 61; pages looked up once a
+//   bf16, B 8, 16384 keys                85.5  93%
+//   4 bits, B 8, 16384 keys              37.5  59%: about 5 us until the first tiles are there and 5 us to join the parts
+//   4 bits, B 32, up to 32768 keys       106   79%: issue slots 60%, ALU 53%; three warps a scheduler wait for their own results
+//   4 bits, B 16, H 96 (12 rows), 13400 keys  92    40%: two warps a scheduler, 254 registers
+//   bf16, d 256, B 13, up to 5000 keys, 12 rows (two blocks, the second out of L2)  35    52%
+// What it took before weights came in two numbers, at B 8 and 16384 keys in 4 bits: tiles of one CTA with lane-wise operand loads 61; pages looked up once a
 // tile 48.6; matrix loads, shares by warp, a vote instead of the maximum's exchanges 40; one wave of shorter launches 36.
 // OVERHEAD sets how even the shares are where units are short: a warp that got a sequence's empty units at one tile each held
 // up a batch of 16 (4 bits, H 96, 165 to 20539 keys, one empty: 99 us, 72 at 4 tiles; the same sizes at equal lengths 74).

@@ -476,6 +476,8 @@ attn_status_t attn_paged_gather(const attn_paged_cache_t* cache, void* k, void* 
  * the cache.
  *   q, o: DEVICE bf16 [B, Nq, H, d], contiguous, 16-byte aligned; lse: DEVICE fp32 [B, H, Nq], natural
  *      log. Query head h reads kv head h / (H / Hkv); H / Hkv may be any whole number.
+ *      Over 4-bit caches a query row is held in fp16 times a power of two: exact, but for values below 2^-24 of the row's
+ *      greatest.
  *   seqlens: DEVICE int32 [B], keys of each sequence in the cache, the Nq new tokens' own among them.
  *   causal: query i sees keys j <= i + seqlens[b] - Nq (bottom-right aligned, as attn_fwd_varlen);
  *      otherwise all. Rows that see no key get O = 0, LSE = -inf, so a padded entry of the batch has
