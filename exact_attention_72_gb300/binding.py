@@ -136,6 +136,13 @@ def _dtype_code(t) -> int:
     raise TypeError(f"q/k/v must be bfloat16 or float8_e4m3fn, got {t.dtype}")
 
 
+def _bytes(t, name: str) -> int:
+    """Bytes of a caller's workspace or plan: those its values span only where it is contiguous."""
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return t.numel() * t.element_size()
+
+
 def _stream_handle(stream) -> int:
     import torch
     if stream is None:
@@ -238,7 +245,7 @@ def attn_varlen_plan(cu_seqlens_q, cu_seqlens_k, H: int, total_q: int, total_k: 
     if plan is None:
         plan = torch.empty(max(need, 16), dtype=torch.uint8, device=cu_seqlens_q.device)
     st = lib().attn_varlen_plan(cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, H, total_q, total_k, d,
-                                int(bool(causal)), plan.data_ptr(), plan.numel() * plan.element_size(),
+                                int(bool(causal)), plan.data_ptr(), _bytes(plan, "plan"),
                                 _stream_handle(stream))
     _check(st, "attn_varlen_plan")
     return plan
@@ -277,7 +284,7 @@ def attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, plan, causal: bool, sca
             ptrs[idx] = t.data_ptr()
     st = lib().attn_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                                cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), plan.data_ptr(),
-                               plan.numel() * plan.element_size(), B, H, Hkv,
+                               _bytes(plan, "plan"), B, H, Hkv,
                                total_q, total_k, d, float(scale), int(bool(causal)), code, ptrs[0] or None,
                                ptrs[1] or None, ptrs[2] or None, _stream_handle(stream))
     _check(st, "attn_fwd_varlen")
@@ -311,7 +318,7 @@ def attn_bwd(q, k, v, o, lse, dout, causal: bool, scale: Optional[float] = None,
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     st = lib().attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(),
                         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Hkv, N, d, float(scale),
-                        int(bool(causal)), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                        int(bool(causal)), workspace.data_ptr(), _bytes(workspace, "workspace"),
                         _stream_handle(stream))
     _check(st, "attn_bwd")
     return dq, dk, dv
@@ -436,7 +443,7 @@ def attn_fwd_splitkv(q, k, v, num_splits: int, scale: Optional[float] = None, de
             ptrs[idx] = t.data_ptr()
     st = lib().attn_fwd_splitkv(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv,
                                 Nq, Nk, d, float(scale), int(num_splits), code, ptrs[0], ptrs[1], ptrs[2],
-                                workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                workspace.data_ptr(), _bytes(workspace, "workspace"),
                                 _stream_handle(stream))
     _check(st, "attn_fwd_splitkv")
     return out, lse
@@ -488,7 +495,7 @@ def attn_fwd_host(q, k, v, out, lse, causal: bool, workspace, scale: Optional[fl
                              d, float(scale), int(bool(causal)), code,
                              ctypes.addressof(dq) if fp8 else None, ctypes.addressof(dk) if fp8 else None,
                              ctypes.addressof(dv) if fp8 else None, workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), _stream_handle(stream))
+                             _bytes(workspace, "workspace"), _stream_handle(stream))
     _check(st, "attn_fwd_host")
     return out, lse
 

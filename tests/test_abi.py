@@ -246,3 +246,14 @@ def test_tail_units(lib):
     bounds = sorted((t - 304) * 64 + j for t, j in units)
     assert bounds == [s for s in (c * 13312 // 152 for c in range(1, 152)) if s % 64]
     assert binding.attn_fwd_tail_units(2, 32, 8192, 128, True) == []
+
+def test_a_workspace_or_plan_has_the_bytes_that_its_size_says():
+    """Expanded or cut with gaps: fewer or other bytes than numel() counts. Refused before the library is called."""
+    import torch
+    x, out, lse = (torch.zeros(1, 64, 2, 64, dtype=torch.bfloat16) for _ in range(3))
+    assert binding._bytes(torch.empty(3, 5, dtype=torch.float32), "workspace") == 60
+    for t in (torch.empty(1, dtype=torch.uint8).expand(1 << 20), torch.empty(64, 2, dtype=torch.uint8)[:, 0]):
+        with pytest.raises(ValueError, match="workspace must be a contiguous"):
+            binding.attn_fwd_host(x, x, x, out, lse, False, t)
+        with pytest.raises(ValueError, match="plan must be a contiguous"):
+            binding._bytes(t, "plan")
