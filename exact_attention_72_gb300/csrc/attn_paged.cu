@@ -21,12 +21,13 @@
 // zero and codes cancel; two are 2^-22 off and cost 12% with 5 to 8 rows, 19% with more. With at most 4 rows they cost 2%:
 // half the columns would be padding, so that columns c and c + 4 take one query row, and the first takes the weights'
 // first number, the second the other (B 8, 16384 keys, 4 rows: 34.8 us in one number, 35.5 so, 38.7 with two products;
-// B 32, up to 32768 keys: 98.7, 100.2, 112.4). For p_j scale_j to stay within fp16 at any scale,
-// the running maximum is taken over S + log2 of the key's scale (its exponent) instead of S; with several groups of dims, each
-// has a power of two of its own that follows its own scales, so that a group keeps its bits beside one far larger (5% with 4
-// rows, 35.6 -> 37.2 and 100.3 -> 106 us, 1% with more; one factor for all lost the codes of a group 2^-14 as large).
-// Products of 16 keys are added up outside the tensor cores: chained, they left an error of 0.0065 of O's norm at 48 sequences of
-// 32768 keys and 0.026 at 64 of 65536, added 0.0016 (at most 4 rows 1% slower, 8 rows 39.7 -> 42.4 us, 12 rows 68.5 -> 72.5).
+// B 32, up to 32768 keys: 98.7, 100.2, 112.4).
+// For p_j scale_j to stay within fp16 at any scale, the running maximum is taken over S + log2 of the key's scale (its exponent)
+// instead of S; with several groups of dims, each has a power of two of its own that follows its own scales, so that a group
+// keeps its bits beside one far larger (5% with 4 rows, 35.6 -> 37.2 and 100.3 -> 106 us, 1% with more; one factor for all
+// lost the codes of a group 2^-14 as large).
+// Products of 16 keys are added up outside the tensor cores: chained, they left an error of 0.0065 of O's norm at 48 sequences
+// of 32768 keys and 0.026 at 64 of 65536, added 0.0016 (at most 4 rows 1% slower, 8 rows 39.7 -> 42.4 us, 12 rows 68.5 -> 72.5).
 //
 // Work: a sequence's keys are cut into tiles of KT; a unit is the tiles of one (sequence, kv head, block of query rows).
 // All units in order, each OVERHEAD tiles longer than it is, are dealt to all warps in equal contiguous shares, so ragged
@@ -44,8 +45,9 @@
 //   4 bits, B 32, up to 32768 keys       106   79%: issue slots 60%, ALU 53%; three warps a scheduler wait for their own results
 //   4 bits, B 16, H 96 (12 rows), 13400 keys  92    40%: two warps a scheduler, 254 registers
 //   bf16, d 256, B 13, up to 5000 keys, 12 rows (two blocks, the second out of L2)  35    52%
-// What it took before weights came in two numbers, at B 8 and 16384 keys in 4 bits: tiles of one CTA with lane-wise operand loads 61; pages looked up once a
-// tile 48.6; matrix loads, shares by warp, a vote instead of the maximum's exchanges 40; one wave of shorter launches 36.
+// What it took before weights came in two numbers, at B 8 and 16384 keys in 4 bits: tiles of one CTA with lane-wise operand
+// loads 61; pages looked up once a tile 48.6; matrix loads, shares by warp, a vote instead of the maximum's exchanges 40; one
+// wave of shorter launches 36.
 // OVERHEAD sets how even the shares are where units are short: a warp that got a sequence's empty units at one tile each held
 // up a batch of 16 (4 bits, H 96, 165 to 20539 keys, one empty: 99 us, 72 at 4 tiles; the same sizes at equal lengths 74).
 #include <algorithm>
@@ -498,9 +500,10 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
       slot += C::SLOT;
       if (slot == ring_end) slot = buf;
     };
+    // Twin columns: the second ones' weights are without their first number.
+    [[maybe_unused]] const uint64_t minus_hi = t < 2 ? f2_pack(0.f, 0.f) : f2_pack(-1.f, -1.f);
     // Where this lane's row of a matrix load lies: lanes 0-7 and 8-15 rows 0-7 and 8-15 of a 16-row block's first
     // chunk, lanes 16-31 of its second. Further pairs of chunks differ in bits 5 and up.
-    [[maybe_unused]] const uint64_t minus_hi = t < 2 ? f2_pack(0.f, 0.f) : f2_pack(-1.f, -1.f);   // of twin columns
     const uint32_t my_chunk = chunk_at<C::ROWB>(lane & 15, lane >> 4);
     for (int turn = 0; turn < f_turn; ++turn) {
       constexpr int QR = D / 16;
@@ -813,7 +816,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
                 const float a = __uint_as_float(vs[kb][i][gr] << 16), b = __uint_as_float(vs[kb][i][gr] & 0xffff0000u);
                 sc[i] = f2_pack(a, a), zr[i] = f2_pack(b, b);
               }
-              // Weights times scale rounded to fp16, and what that left; of twin columns the first takes one, the second the other.
+              // Weights times scale rounded to fp16, and what that left; of twin columns the first takes one, the second
+              // the other.
               uint32_t hi[2][NT];
               [[maybe_unused]] uint32_t lo[2][NT];
 #pragma unroll
@@ -838,8 +842,8 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
                 const uint32_t x0 = i < 2 ? x.x : x.z, x1 = i < 2 ? x.y : x.w;
                 const uint32_t y0 = i % 2 ? high_bytes(x0) : x0 & 0x00ff00ffu, y1 = i % 2 ? high_bytes(x1) : x1 & 0x00ff00ffu;
                 const uint32_t c0 = y0 & 0x000f000fu, c1 = y1 & 0x000f000fu;   // low codes, and low + 16 high
-                // A matrix product cuts what it adds up, towards 0. In a chain over all keys that is a drift of the codes' offset,
-                // which is hundreds of times O where many keys share the weight: products start from 0, sums round to nearest.
+                // A matrix product cuts what it adds up, towards 0. In a chain over all keys that is a drift of the codes'
+                // offset, hundreds of times O where many keys share the weight: products start from 0, sums round to nearest.
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                   float p[4];
