@@ -106,6 +106,10 @@ def lib() -> ctypes.CDLL:
     L.attn_fwd_paged_workspace_bytes.argtypes = [i, i, i, i, i, i]
     L.attn_fwd_paged.restype = i
     L.attn_fwd_paged.argtypes = [vp, cache, vp, vp, vp, ll, i, vp, i, i, i, f, i, vp, sz, vp]
+    L.attn_fwd_paged_varlen_workspace_bytes.restype = sz
+    L.attn_fwd_paged_varlen_workspace_bytes.argtypes = [i, i, i, i, i, i]
+    L.attn_fwd_paged_varlen.restype = i
+    L.attn_fwd_paged_varlen.argtypes = [vp, cache, vp, vp, vp, ll, i, vp, vp, i, i, i, f, i, vp, sz, vp]
     L.attn_get_status.restype = i
     L.attn_get_status.argtypes = [vp]
     L.attn_get_status_detail.restype = i
@@ -664,6 +668,28 @@ def attn_fwd_paged(q, cache: PagedKVCache, page_table, seqlens, causal: bool = T
     if stream is not None:
         return _on(stream, call, cache._address, cache._index, q, page_table, seqlens, causal, scale, workspace, out, lse)
     return call(cache._address, cache._index, q, page_table, seqlens, causal, scale, workspace, out, lse)
+
+
+def attn_fwd_paged_varlen_workspace_bytes(cache: PagedKVCache, B: int, H: int, total_q: int) -> int:
+    return int(lib().attn_fwd_paged_varlen_workspace_bytes(B, H, cache.Hkv, total_q, cache.d, cache.type))
+
+
+def attn_fwd_paged_varlen(q, cache: PagedKVCache, page_table, cu_seqlens_q, seqlens, causal: bool = True,
+                          scale: Optional[float] = None, workspace=None, out=None, lse=None, stream=None):
+    """Attention of chunks of new tokens over the cache: q bf16 [total_q, H, d], sequence b's rows cu_seqlens_q[b] ..
+    cu_seqlens_q[b + 1] - 1; (out bf16 [total_q, H, d], lse float32 [H, total_q]).
+
+    ``seqlens`` (int32 [B]) counts each sequence's keys, its new tokens' own among them (append them first); with
+    ``causal`` query i of n sees keys j <= i + seqlens[b] - n. Chunks may have any length, one token (a decoding
+    sequence) or none. Rows that see no key give 0 and -inf; rows from cu_seqlens_q[B] on are left as they were.
+    ``workspace`` (CUDA uint8, at least attn_fwd_paged_varlen_workspace_bytes(...)) is allocated here with torch if not
+    given; where every chunk is one or a few tokens of a short row, attn_fwd_paged is faster.
+    """
+    call = (_CALLS or _calls()).fwd_paged_varlen
+    if stream is not None:
+        return _on(stream, call, cache._address, cache._index, q, page_table, cu_seqlens_q, seqlens, causal, scale, workspace, out,
+                   lse)
+    return call(cache._address, cache._index, q, page_table, cu_seqlens_q, seqlens, causal, scale, workspace, out, lse)
 
 
 def attn_get_status(stream=None) -> tuple[int, int]:

@@ -1,0 +1,1010 @@
+// Attention of chunks of new tokens over a paged key/value cache in bf16 or 4 bits, any ragged batch:
+//   S = scale q k^T over the keys a row sees,  O = softmax(S) V,  LSE,
+// with the queries of sequence b packed from row cu[b] on and its keys, the new ones among them, in pages.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "attn_fwd_kernel.cuh"
+#include "fastdiv.cuh"
+#include "ops.h"
+#include "paged.cuh"
+
+namespace gb300 {
+
+struct PagedVarlenParams {
+  PagedCache c;
+  const __nv_bfloat16* q;   // [total_q, H, D]
+  __nv_bfloat16* o;
+  float* lse;               // [H, total_q]
+  const int *table, *cu, *lens;
+  long long table_stride;
+  int B, H, G, P;           // G query heads a kv head, P = 128 / G positions a Q tile
+  int total_q, max_pages, box_rows, causal;
+  FastDiv div_g, div_page;  // by G and by the page size
+  float scale_log2;         // |scale| log2(e)
+  uint32_t qk_negate;       // as AttnParams
+  // Parts of cut units: slot 2c the one that CTA c continues, 2c + 1 the one that it begins and does not end.
+  float* part_o;            // [2 CTAs, ROWS, D] normalised O
+  float* part_lse;          // [2 CTAs, ROWS] log2-sum-exp2
+  int4* cut;                // [CTAs, 2]: (first packed row, kv head, positions, parts) of the unit that CTA c begins; parts 0: none
+  int o_v8;                 // rows of o are 32-byte aligned
+  uint32_t* status;
+  unsigned long long timeout_ns;
+  int debug_skip_load;
+};
+
+// A unit: the P * NQ positions of one (sequence, kv head) whose G heads fill the CTA's Q tiles; a piece: what one CTA does
+// of it, KV tiles t0 .. t0 + max(n0, n1) - 1.
+struct Piece {
+  int work;                 // 0: no more pieces
+  int q_row, n_pos;         // first packed row of the unit, its positions
+  int kvh, b;
+  int vis;                  // keys that its first query sees, less one (causal)
+  int nk;                   // keys of the sequence
+  int t0, n0, n1;           // first KV tile; tiles that Q tile 0 and 1 visit from there
+  int slot;                 // of its part; -1: the piece is the whole unit
+  int pad;
+};
+
+template <int D_, bool INT4_>
+struct PagedVarlenCfg {
+  static constexpr int D = D_;
+  static constexpr bool INT4 = INT4_, FP8 = false;
+  static constexpr int NQ = D <= 128 ? 2 : 1;             // 128-row Q tiles of a CTA
+  static constexpr int ROWS = 128 * NQ;                   // rows of a unit
+  // Operands: 16-bit, K-major (V: MN-major) tiles of 128 rows in chunks of 64 columns with the 128-byte swizzle.
+  static constexpr int SWZ = 128, SBO = 1024, CHUNK_BYTES = 128 * 128, NCH = D / 64;
+  static constexpr int TILE_BYTES = NCH * CHUNK_BYTES;
+  static constexpr int KSTEPS_QK = D / 16, KSTEPS_PV = 8, PV_ROWS = 16;
+  static constexpr int EXT_BYTES = INT4 ? 128 * 32 : 0;   // 16 more columns of Q and K for the zeros of 4-bit keys
+  static constexpr int NK = D == 64 ? 4 : D == 128 ? 2 : 1, NV = NK;   // stages of K and of V
+  static constexpr int Q_BYTES = NQ * TILE_BYTES;
+  static constexpr int SMEM_BYTES = Q_BYTES + NQ * EXT_BYTES + NK * (TILE_BYTES + EXT_BYTES) + NV * TILE_BYTES + 1024;
+  // TMEM: S buffers, then a P area and an O tile of each Q tile.
+  static constexpr int NSB = D == 64 ? 2 : 1;
+  static constexpr int P_COL = 128 * NSB, P_COLS = 64, O_COL = D == 64 ? 384 : 256, TMEM_COLS = 512;
+  static_assert(P_COL + NQ * P_COLS <= O_COL && O_COL + NQ * D <= TMEM_COLS, "TMEM budget");
+  static constexpr uint32_t FMT = INT4 ? kFmtF16 : kFmtBF16;
+  static constexpr uint32_t IDESC_QK = make_idesc(FMT, 128, 128, false, false);
+  static constexpr uint32_t IDESC_PV = make_idesc(FMT, 128, D, false, true);
+  // Warps: softmax (a warpgroup for each Q tile), then a warpgroup of PV issuers, scheduler / loader and S issuer, then
+  // (4 bits) a warpgroup that unpacks keys and values.
+  static constexpr int SOFTMAX_WARPS = 4 * NQ, WARP_PV = SOFTMAX_WARPS, WARP_LOAD = WARP_PV + 2, WARP_S = WARP_PV + 3;
+  static constexpr int WARP_UNPACK = WARP_PV + 4;
+  static constexpr int THREADS = 32 * (WARP_UNPACK + (INT4 ? 4 : 0));
+  static constexpr bool REG_SPLIT = THREADS > 256;
+  static constexpr uint32_t REGS_SOFTMAX = 200, REGS_ROLES = INT4 ? (NQ == 2 ? 48 : 64) : 96, REGS_UNPACK = NQ == 2 ? 64 : 128;
+  static constexpr int REGS_NEEDED = SOFTMAX_WARPS * 32 * REGS_SOFTMAX + 128 * REGS_ROLES + (INT4 ? 128 * REGS_UNPACK : 0);
+  static constexpr int PIECES = 4;                        // pieces that the scheduler may be ahead
+  static constexpr int CONSUMERS = SOFTMAX_WARPS + NQ + 1 + (INT4 ? 4 : 0);
+};
+
+constexpr int kUnitOverhead = 2 * 128;     // what beginning and ending a unit costs, in keys
+constexpr long long kLeastShare = 3 * 128;   // of a CTA, in keys
+
+// Descriptor of an operand without swizzle: 8 x 16-byte core matrices, lbo apart along K, sbo along the rows.
+__device__ __forceinline__ uint64_t make_sdesc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return make_sdesc_swz(saddr, lbo, sbo, 64u) & ~((uint64_t)7 << 61);
+}
+
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void sts128(uint32_t a, uint4 x) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+
+// Keys (in 128ths of a tile) that the units of one (sequence, kv head) cost, RP positions each, off = nk - nq: unit m needs the
+// keys that its last query sees and kUnitOverhead. The sum over units 0 .. k - 1:
+struct SeqCost {
+  int nq, nk, M, RP, causal;
+  __device__ int keys(int m) const {
+    if (!causal) return nk;
+    const long long last = (long long)min((long long)(m + 1) * RP, (long long)nq) + nk - nq;
+    return last > 0 ? (int)last : 0;
+  }
+  __device__ long long upto(int k) const {
+    long long s = (long long)k * kUnitOverhead;
+    if (!causal) return s + (long long)k * nk;
+    if (k == M && M > 0) {   // the last unit ends with the last query, which sees all keys
+      s += nk;
+      --k;
+    }
+    const long long off = (long long)nk - nq;
+    const long long m0 = off >= 0 ? 0 : -off / RP;   // units before see nothing
+    if (k > m0) s += (k - m0) * off + RP * ((long long)k * (k + 1) / 2 - m0 * (m0 + 1) / 2);
+    return s;
+  }
+};
+
+// Wait sites of this kernel besides those of the forward (SITE_*).
+enum : uint32_t { SITE_PIECE_FULL = 16, SITE_PIECE_EMPTY = 17 };
+
+// 2^e of a float's exponent bits: 1 <= bits <= 254.
+__device__ __forceinline__ float power_of_bits(uint32_t bits) { return __uint_as_float(bits << 23); }
+__device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t half2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float half_round(float x) { return __half2float(__float2half_rn(x)); }
+
+// The 4-bit cache's operands. Thread r of the warpgroup has query row r of each Q tile and key r of each KV tile.
+//
+// Keys: zero + scale c = scale (c - 8) + zero', zero' = zero + 8 scale. The first term has 11 bits (8 of scale, 3 of c - 8), so
+// fp16 holds it; the second is one value a group of dims, which S takes in as a product of 16 more columns,
+//   zero' sum(q) = (zh + zl) (Qh + Ql),    zh + zl and Qh + Ql the two values in 22 bits each.
+// So S is what fp32 would give. In bf16 the keys would be 2^-8 off, and LSE with them (2e-5 of it over 1000 keys).
+// Values: zero + scale c rounded once to fp16, 2^-11 off, as P is; in bf16 the two would add as much to O's error as its own
+// rounding.
+// fp16's range: every 32 keys (a warp's) of a tile are divided by a power of two that brings the greatest of them below 2^15, a
+// query row by one that brings its greatest value into [2^7, 2^8). Full precision is left to values 2^-29 of the greatest of
+// their 32 keys (query rows: 2^-21), others are off by 2^-40 (2^-33) of it. The softmax puts the keys' power back into the
+// scores, and the values' into the weights' exponents: the running maximum is over weights times those powers, and the weights
+// are summed without them.
+template <class C, class F>
+__device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int r, int PG, uint32_t sQ, uint32_t sQx, uint32_t sK,
+                                            uint32_t sKx, uint32_t sV, uint64_t* bar_q_full, uint64_t* bar_q_empty,
+                                            uint64_t* bar_k_full, uint64_t* bar_k_empty, uint64_t* bar_v_full,
+                                            uint64_t* bar_v_empty, float4* s_kf, float4* s_ve, float* s_qf, const WaitCtl& ctl,
+                                            F& piece_of_warp) {
+  constexpr int D = C::D, NQ = C::NQ, NK = C::NK, NV = C::NV, GROUPS = D / kInt4Group;
+  constexpr int WORDS = D >= 128 ? 16 : 8;      // 8 codes each, of a step
+  constexpr int HALVES = D / 8 / WORDS;         // steps of a row
+  const int lane = r & 31, w = r >> 5;
+  const uint32_t swz = (uint32_t)(r & 7), row_at = (uint32_t)r * 128, ext_at = (uint32_t)(r >> 3) * 256 + (r & 7) * 16;
+  const int pos_r = (uint32_t)r / p.div_g, g_r = r - pos_r * p.G;
+  uint32_t n_q = 0, n_k = 0;
+  Piece pc;
+  for (uint32_t it = 0; piece_of_warp(it, pc); ++it) {
+    const int n = max(pc.n0, pc.n1);
+    if (n == 0) continue;
+    // My key's row: of its page in the page table, and where its codes and pairs begin (-1: nowhere).
+    auto look_up = [&](int t) {
+      const int key = t * 128 + r;
+      return key < pc.nk ? __ldg(p.table + pc.b * p.table_stride + (uint32_t)key / p.div_page) : -1;
+    };
+    long long at = -1, at_sz = -1;
+    auto locate = [&](int t, int page) {
+      const int key = t * 128 + r;
+      at = at_sz = -1;
+      if (key >= pc.nk) return;
+      if (page < 0 || page >= p.c.num_pages) {
+        atomicCAS(p.status, 0u, kStatusBadPage);
+        return;
+      }
+      const int tok = key - (int)((uint32_t)key / p.div_page) * p.c.page_size;
+      at = page * p.c.page_b + tok * p.c.token_b + pc.kvh * p.c.head_b;
+      at_sz = page * p.c.sz_page_b + tok * p.c.sz_token_b + pc.kvh * p.c.sz_head_b;
+    };
+    uint32_t buf[2][WORDS];
+    auto fetch = [&](uint32_t (&x)[WORDS], const uint8_t* base, int half) {
+#pragma unroll
+      for (int i = 0; i < WORDS / 4; ++i) {
+        const uint4 u = at < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                               : __ldg(reinterpret_cast<const uint4*>(base + at + half * (WORDS * 4)) + i);
+        x[4 * i] = u.x, x[4 * i + 1] = u.y, x[4 * i + 2] = u.z, x[4 * i + 3] = u.w;
+      }
+    };
+    auto fetch_pairs = [&](uint32_t (&x)[GROUPS], const uint8_t* base) {
+      if constexpr (GROUPS == 1) {
+        x[0] = at < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t*>(base + at_sz));
+      } else if constexpr (GROUPS == 2) {
+        const uint2 u = at < 0 ? make_uint2(0u, 0u) : __ldg(reinterpret_cast<const uint2*>(base + at_sz));
+        x[0] = u.x, x[1] = u.y;
+      } else {
+        const uint4 u = at < 0 ? make_uint4(0u, 0u, 0u, 0u) : __ldg(reinterpret_cast<const uint4*>(base + at_sz));
+        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+      }
+    };
+    uint32_t ksz[GROUPS], vsz[GROUPS];
+    int page = look_up(pc.t0);
+    locate(pc.t0, page);
+    fetch(buf[0], p.c.k, 0);
+    fetch_pairs(ksz, p.c.k_sz);
+    fetch_pairs(vsz, p.c.v_sz);
+    page = n > 1 ? look_up(pc.t0 + 1) : -1;
+
+    // Query rows, once the S products of the last piece have read theirs.
+    bool ok = n_q == 0 || mbar_wait(smem_addr(bar_q_empty), (n_q - 1) & 1, ctl, SITE_Q_EMPTY);
+    if (!__all_sync(0xffffffffu, ok)) return;
+    for (int q = 0; q < NQ; ++q) {
+      if ((q ? pc.n1 : pc.n0) == 0) continue;
+      const int pos = q * p.P + pos_r;
+      const bool valid = r < PG && pos < pc.n_pos;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + ((long long)(pc.q_row + (valid ? pos : 0)) * p.H + pc.kvh * p.G + (valid ? g_r : 0)) * D);
+      uint32_t most = 0;
+#pragma unroll 8
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 u = __ldg(src + i);
+        most = max_u16x2(max_u16x2(most, u.x & 0x7fff7fffu), max_u16x2(u.y & 0x7fff7fffu, max_u16x2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
+      }
+      const uint32_t bits = max(max(most & 0xffffu, most >> 16) >> 7, 8u);   // exponent of the greatest
+      const float f = valid ? power_of_bits(261u - bits) : 0.f;
+      s_qf[n_q % (C::NSB + 1) * C::ROWS + q * 128 + r] = power_of_bits(bits - 7u);
+      uint32_t ext[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ext[i] = 0u;
+#pragma unroll
+      for (int ch = 0; ch < C::NCH; ++ch) {
+        float sum = 0.f;
+#pragma unroll
+        for (int u8 = 0; u8 < 8; ++u8) {
+          const uint4 u = valid ? __ldg(src + ch * 8 + u8) : make_uint4(0u, 0u, 0u, 0u);
+          const float d0 = __uint_as_float(u.x << 16) * f, d1 = __uint_as_float(u.x & 0xffff0000u) * f;
+          const float d2 = __uint_as_float(u.y << 16) * f, d3 = __uint_as_float(u.y & 0xffff0000u) * f;
+          const float d4 = __uint_as_float(u.z << 16) * f, d5 = __uint_as_float(u.z & 0xffff0000u) * f;
+          const float d6 = __uint_as_float(u.w << 16) * f, d7 = __uint_as_float(u.w & 0xffff0000u) * f;
+          sum += ((d0 + d1) + (d2 + d3)) + ((d4 + d5) + (d6 + d7));
+          sts128(sQ + (q * C::NCH + ch) * C::CHUNK_BYTES + row_at + ((u8 ^ swz) << 4),
+                 make_uint4(f16x2_pack(d0, d4), f16x2_pack(d1, d5), f16x2_pack(d2, d6), f16x2_pack(d3, d7)));
+        }
+        const float hi = half_round(sum), lo = sum - hi;
+        ext[2 * ch] = f16x2_pack(hi, hi), ext[2 * ch + 1] = f16x2_pack(lo, lo);
+      }
+      sts128(sQx + q * C::EXT_BYTES + ext_at, make_uint4(ext[0], ext[1], ext[2], ext[3]));
+      sts128(sQx + q * C::EXT_BYTES + ext_at + 128, make_uint4(ext[4], ext[5], ext[6], ext[7]));
+    }
+    fence_async_proxy();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(bar_q_full));
+    ++n_q;
+
+    for (int j = 0; j < n; ++j, ++n_k) {
+      const uint32_t ks = n_k % NK, vs = n_k % NV;
+      uint32_t s2[GROUPS], z2[GROUPS];   // scales (and zeros) as pairs
+#pragma unroll
+      for (int step = 0; step < 2 * HALVES; ++step) {
+        const bool is_v = step >= HALVES;
+        const int half = step % HALVES;
+        // The next step's codes, on their way while this one's are unpacked.
+        if (step + 1 < 2 * HALVES) {
+          fetch(buf[(step + 1) & 1], step + 1 >= HALVES ? p.c.v : p.c.k, (step + 1) % HALVES);
+        } else if (j + 1 < n) {
+          locate(pc.t0 + j + 1, page);
+          fetch(buf[0], p.c.k, 0);
+          fetch_pairs(ksz, p.c.k_sz);
+          fetch_pairs(vsz, p.c.v_sz);
+          if (j + 2 < n) page = look_up(pc.t0 + j + 2);
+        }
+        if (half == 0) {
+          if (!is_v) {
+            // Powers of two of my warp's keys and values.
+            uint32_t mk = 0, mv = 0;
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) {
+              const float scale = __uint_as_float(ksz[g] << 16), zero = __uint_as_float(ksz[g] & 0xffff0000u);
+              mk = max(mk, __float_as_uint(fmaxf(fabsf(scale) * 8.f, fabsf(fmaf(8.f, scale, zero)))));
+              const float vscale = __uint_as_float(vsz[g] << 16), vzero = __uint_as_float(vsz[g] & 0xffff0000u);
+              mv = max(mv, __float_as_uint(fmaf(15.f, fabsf(vscale), fabsf(vzero))));
+            }
+            const uint32_t bk = min(max(__reduce_max_sync(0xffffffffu, mk) >> 23, 15u), 254u);
+            // Not below 2^-80: weights without their powers are summed in fp32.
+            const uint32_t bv = min(max(__reduce_max_sync(0xffffffffu, mv) >> 23, 61u), 254u);
+            const float nk = power_of_bits(268u - bk), nv = power_of_bits(268u - bv);
+            uint32_t ext[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ext[i] = 0u;
+            const uint32_t meta = n_k % (2 * NK);
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) {
+              const float scale = __uint_as_float(ksz[g] << 16), zero = __uint_as_float(ksz[g] & 0xffff0000u);
+              const float z = fmaf(8.f, scale, zero) * nk, hi = half_round(z);
+              s2[g] = f16x2_pack(scale * nk, scale * nk);
+              ext[2 * g] = ext[2 * g + 1] = f16x2_pack(hi, z - hi);
+              // The values' pairs, as they are needed in the next steps.
+              const float vscale = __uint_as_float(vsz[g] << 16) * nv, vzero = __uint_as_float(vsz[g] & 0xffff0000u) * nv;
+              z2[g] = f16x2_pack(vscale, vzero);
+            }
+            ok = n_k < (uint32_t)NK || mbar_wait(smem_addr(&bar_k_empty[ks]), (n_k / NK - 1) & 1, ctl, SITE_KV_EMPTY);
+            if (!__all_sync(0xffffffffu, ok)) return;
+            if (lane == 0) {
+              reinterpret_cast<float*>(s_kf + meta)[w] = power_of_bits(bk - 14u);
+              reinterpret_cast<float*>(s_ve + meta)[w] = (float)((int)bv - 141);
+            }
+            sts128(sKx + ks * C::EXT_BYTES + ext_at, make_uint4(ext[0], ext[1], ext[2], ext[3]));
+            sts128(sKx + ks * C::EXT_BYTES + ext_at + 128, make_uint4(ext[4], ext[5], ext[6], ext[7]));
+          } else {
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) s2[g] = __byte_perm(z2[g], 0, 0x1010), z2[g] = __byte_perm(z2[g], 0, 0x3232);
+            ok = n_k < (uint32_t)NV || mbar_wait(smem_addr(&bar_v_empty[vs]), (n_k / NV - 1) & 1, ctl, SITE_KV_EMPTY);
+            if (!__all_sync(0xffffffffu, ok)) return;
+          }
+        }
+        const uint32_t tile = (is_v ? sV + vs * C::TILE_BYTES : sK + ks * C::TILE_BYTES) + row_at;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+          const int word = half * WORDS + i, ch = word / 8, u8 = word % 8;
+          const uint32_t x = buf[step & 1][i];
+          uint32_t y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {   // codes k and k + 4 as 1024 + c
+            const uint32_t c = ((x >> (4 * k)) & 0x000f000fu) | 0x64006400u;
+            y[k] = is_v ? half2_fma(half2_sub(c, 0x64006400u), s2[ch], z2[ch]) : half2_mul(half2_sub(c, 0x64086408u), s2[ch]);
+          }
+          sts128(tile + ch * C::CHUNK_BYTES + ((u8 ^ swz) << 4), make_uint4(y[0], y[1], y[2], y[3]));
+        }
+        if (half == HALVES - 1) {
+          fence_async_proxy();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(is_v ? &bar_v_full[vs] : &bar_k_full[ks]));
+        }
+      }
+    }
+  }
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedVarlenParams p) {
+  constexpr int D = C::D, NQ = C::NQ, NCH = C::NCH, NK = C::NK, NV = C::NV, NSB = C::NSB;
+  constexpr bool INT4 = C::INT4;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bar_q_full, bar_q_empty, bar_k_full[NK], bar_k_empty[NK], bar_v_full[NV], bar_v_empty[NV];
+  __shared__ __align__(8) uint64_t bar_s_full[NQ * NSB], bar_s_free[NSB], bar_p_half[NQ][2], bar_o_done[NQ], bar_o_full[NQ];
+  __shared__ __align__(8) uint64_t bar_piece_full[C::PIECES], bar_piece_empty[C::PIECES], bar_patch, bar_drain[NQ + 1];
+  __shared__ Piece s_pieces[C::PIECES];
+  // 4 bits: powers of two of the keys (as factors of S) and values (as exponents) of every 32 keys of a tile, and of the
+  // query rows. A tile's are overwritten two rounds of the K stages later, when its softmax has long read them: K_{j + 2 NK}
+  // waits for S_{j + NK}, which comes after the softmax has taken S_j from its buffer.
+  __shared__ float4 s_kf[INT4 ? 2 * NK : 1], s_ve[INT4 ? 2 * NK : 1];
+  __shared__ float s_qf[INT4 ? (NSB + 1) * C::ROWS : 1];   // a piece's are read before its first S leaves its buffer
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile uint32_t abort_flag;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t smem_base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sQ = smem_base, sK = sQ + C::Q_BYTES, sV = sK + NK * C::TILE_BYTES;
+  const uint32_t sQx = sV + NV * C::TILE_BYTES, sKx = sQx + NQ * C::EXT_BYTES;
+  const WaitCtl ctl{&abort_flag, p.status, p.timeout_ns};
+
+  if (tid == 0) {
+    abort_flag = 0u;
+    mbar_init(smem_addr(&bar_q_full), INT4 ? 4 : 1);
+    mbar_init(smem_addr(&bar_q_empty), 1);
+    for (int i = 0; i < NK; ++i) mbar_init(smem_addr(&bar_k_full[i]), INT4 ? 4 : 1), mbar_init(smem_addr(&bar_k_empty[i]), 1);
+    for (int i = 0; i < NV; ++i) mbar_init(smem_addr(&bar_v_full[i]), INT4 ? 4 : 1), mbar_init(smem_addr(&bar_v_empty[i]), NQ);
+    for (int i = 0; i < NQ * NSB; ++i) mbar_init(smem_addr(&bar_s_full[i]), 1);
+    for (int i = 0; i < NSB; ++i) mbar_init(smem_addr(&bar_s_free[i]), 4);
+    for (int i = 0; i < NQ; ++i) {
+      mbar_init(smem_addr(&bar_p_half[i][0]), 4);
+      mbar_init(smem_addr(&bar_p_half[i][1]), 4);
+      mbar_init(smem_addr(&bar_o_done[i]), 1);
+      mbar_init(smem_addr(&bar_o_full[i]), 1);
+    }
+    for (int i = 0; i < C::PIECES; ++i) {
+      mbar_init(smem_addr(&bar_piece_full[i]), 1);
+      mbar_init(smem_addr(&bar_piece_empty[i]), C::CONSUMERS);
+    }
+    mbar_init(smem_addr(&bar_patch), 1);
+    for (int i = 0; i < NQ + 1; ++i) mbar_init(smem_addr(&bar_drain[i]), 1);
+    fence_mbar_init();
+  }
+  if (warp == C::WARP_PV) {
+    tmem_alloc(smem_addr(&tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (!INT4 && p.P * p.G < 128) {   // rows of the Q tiles that no load writes
+    for (int i = tid; i < C::Q_BYTES / 16; i += C::THREADS) sts128(sQ + 16 * i, make_uint4(0u, 0u, 0u, 0u));
+    fence_async_proxy();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_wait();   // launched early: what it reads may be a previous kernel's
+  const uint32_t tmem = tmem_slot;
+  const int PG = p.P * p.G, RP = p.P * NQ;
+
+  // Pieces as their consumers see them; `it` counts those taken. A single lane's and a whole warp's way to take one.
+  auto piece_of_lane = [&](uint32_t it, Piece& pc) {
+    const uint32_t i = it % C::PIECES;
+    if (!mbar_wait(smem_addr(&bar_piece_full[i]), (it / C::PIECES) & 1, ctl, SITE_PIECE_FULL)) return false;
+    pc = s_pieces[i];
+    mbar_arrive(smem_addr(&bar_piece_empty[i]));
+    return pc.work != 0;
+  };
+  auto piece_of_warp = [&](uint32_t it, Piece& pc) {
+    const uint32_t i = it % C::PIECES;
+    const bool w = mbar_wait(smem_addr(&bar_piece_full[i]), (it / C::PIECES) & 1, ctl, SITE_PIECE_FULL);
+    if (!__all_sync(0xffffffffu, w)) return false;
+    pc = s_pieces[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&bar_piece_empty[i]));
+    return pc.work != 0;
+  };
+
+  if (warp == C::WARP_LOAD) {
+    // ------------------------------------------------------------------ scheduler, and TMA producer over a bf16 cache
+    if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REGS_ROLES>();
+    if (!INT4 && lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    uint32_t n_pieces = 0, n_k = 0, n_q = 0, n_patch = 0;   // published, K (and V) tiles, Q loads, patched V tiles
+    bool ok = true;
+    // Publishes a piece; its consumers are at most PIECES behind.
+    auto publish = [&](const Piece& pc) {
+      const uint32_t i = n_pieces % C::PIECES;
+      if (n_pieces >= (uint32_t)C::PIECES) {
+        const bool w = mbar_wait(smem_addr(&bar_piece_empty[i]), (n_pieces / C::PIECES - 1) & 1, ctl, SITE_PIECE_EMPTY);
+        if (!__all_sync(0xffffffffu, w)) return false;
+      }
+      if (lane == 0) {
+        s_pieces[i] = pc;
+        mbar_arrive(smem_addr(&bar_piece_full[i]));
+      }
+      __syncwarp();
+      ++n_pieces;
+      return true;
+    };
+    // Loads of a piece.
+    auto load = [&](const Piece& pc) {
+      if constexpr (!INT4) {
+        const int n = max(pc.n0, pc.n1);
+        if (n == 0) return true;
+        bool w = n_q == 0 || mbar_wait(smem_addr(&bar_q_empty), (n_q - 1) & 1, ctl, SITE_Q_EMPTY);
+        if (!__all_sync(0xffffffffu, w)) return false;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(smem_addr(&bar_q_full), ((pc.n0 > 0) + (pc.n1 > 0)) * NCH * PG * 128);
+          for (int q = 0; q < NQ; ++q) {
+            if ((q ? pc.n1 : pc.n0) == 0) continue;
+            for (int ch = 0; ch < NCH; ++ch)
+              tma_load_4d(sQ + (q * NCH + ch) * C::CHUNK_BYTES, &tm_q, smem_addr(&bar_q_full), ch * 64, 0,
+                          pc.q_row + q * p.P, pc.kvh);
+          }
+        }
+        ++n_q;
+        // Lane i copies 64 columns of box_rows neighbouring keys: chunk i % NCH of the tile's piece i / NCH.
+        const int rows = p.box_rows, at = lane / NCH * rows;
+        const bool mine = lane < 128 / rows * NCH;
+        const uint32_t dst = lane % NCH * C::CHUNK_BYTES + at * 128;
+        auto look_up = [&](int t) {
+          const int key = t * 128 + at;
+          return mine && key < pc.nk ? __ldg(p.table + pc.b * p.table_stride + (uint32_t)key / p.div_page) : -1;
+        };
+        int page = look_up(pc.t0);
+        for (int j = 0; j < n; ++j) {
+          const int key0 = (pc.t0 + j) * 128, key = key0 + at, tok = key - (int)((uint32_t)key / p.div_page) * p.c.page_size;
+          if (mine && key < pc.nk && (page < 0 || page >= p.c.num_pages)) {
+            atomicCAS(p.status, 0u, kStatusBadPage);
+            page = -1;   // outside the map: zeros, as for keys behind the last
+          }
+          const int from = page;
+          if (j + 1 < n) page = look_up(pc.t0 + j + 1);
+          const uint32_t ks = n_k % NK, vs = n_k % NV;
+          w = n_k < (uint32_t)NK || mbar_wait(smem_addr(&bar_k_empty[ks]), (n_k / NK - 1) & 1, ctl, SITE_KV_EMPTY);
+          if (!__all_sync(0xffffffffu, w)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(smem_addr(&bar_k_full[ks]), C::TILE_BYTES);
+          __syncwarp();
+          if (mine) tma_load_4d(sK + ks * C::TILE_BYTES + dst, &tm_k, smem_addr(&bar_k_full[ks]), lane % NCH * 64, tok, pc.kvh, from);
+          w = n_k < (uint32_t)NV || mbar_wait(smem_addr(&bar_v_empty[vs]), (n_k / NV - 1) & 1, ctl, SITE_KV_EMPTY);
+          ++n_k;
+          if (!__all_sync(0xffffffffu, w)) return false;
+          if (p.debug_skip_load && blockIdx.x == 0 && n_k == 1) continue;
+          // Rows of the last page behind the sequence's end may hold anything, and 0 times NaN is NaN: they are cleared.
+          const bool patch = pc.nk - key0 < 128 && pc.nk % rows != 0;
+          const uint32_t bar = smem_addr(patch ? &bar_patch : &bar_v_full[vs]);
+          if (lane == 0) mbar_arrive_expect_tx(bar, C::TILE_BYTES);
+          __syncwarp();
+          const uint32_t tile = sV + vs * C::TILE_BYTES;
+          if (mine) tma_load_4d(tile + dst, &tm_v, bar, lane % NCH * 64, tok, pc.kvh, from);
+          if (patch) {
+            ++n_patch;
+            w = mbar_wait(bar, (n_patch - 1) & 1, ctl, SITE_KV_FULL);
+            if (!__all_sync(0xffffffffu, w)) return false;
+            const int r0 = pc.nk - key0, n_rows = (r0 + rows - 1) / rows * rows - r0;
+            for (int i = lane; i < n_rows * 8 * NCH; i += 32) {
+              const int r = i / (8 * NCH), c = i % (8 * NCH);
+              sts128(tile + c / 8 * C::CHUNK_BYTES + (r0 + r) * 128 + c % 8 * 16, make_uint4(0u, 0u, 0u, 0u));
+            }
+            fence_async_proxy();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&bar_v_full[vs]));
+          }
+        }
+      }
+      return true;
+    };
+
+    // Sequence b as far as the offsets and lengths are sound; nq = 0 otherwise.
+    auto sequence = [&](int b, int& q_base) {
+      SeqCost s{0, 0, 0, RP, p.causal};
+      q_base = 0;
+      if (b < p.B) {
+        const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), n = __ldg(p.lens + b);
+        const int nk = min(max(n, 0), p.max_pages * p.c.page_size);   // the host refuses tables of more
+        const bool good = c0 >= 0 && c1 >= c0 && c1 <= p.total_q;
+        if (!good || nk != n) atomicCAS(p.status, 0u, kStatusBadPage);
+        if (good) q_base = c0, s.nq = c1 - c0, s.nk = nk, s.M = (s.nq + RP - 1) / RP;
+      }
+      return s;
+    };
+    // Costs of 32 sequences from b0 on: mine, and of all of them up to mine.
+    auto costs = [&](int b0, long long& mine) {
+      int q_base;
+      const SeqCost s = sequence(b0 + lane, q_base);
+      mine = p.c.Hkv * s.upto(s.M);
+      long long upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      return upto;
+    };
+    // All costs, dealt to the CTAs in equal contiguous shares: mine is [x0, x1).
+    long long W = 0, mine, x0 = 0, x1 = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) W += __shfl_sync(0xffffffffu, costs(b0, mine), 31);
+    const int shares = (int)max(1LL, min((long long)gridDim.x, W / kLeastShare)), me = blockIdx.x;
+    int4 cut0 = make_int4(0, 0, 0, 0);
+    if (me < shares && W > 0) {
+      x0 = me * W / shares;
+      x1 = (me + 1) * W / shares;
+      // The sequence, kv head and unit that x0 lies in.
+      int b = 0, kvh = 0, m = 0, q_base = 0;
+      long long before = 0;
+      for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const long long upto = costs(b0, mine), all = __shfl_sync(0xffffffffu, upto, 31);
+        if (before + all > x0) {
+          const int i = __popc(__ballot_sync(0xffffffffu, before + upto <= x0));
+          b = b0 + i;
+          before += __shfl_sync(0xffffffffu, upto - mine, i);
+          break;
+        }
+        before += all;
+      }
+      SeqCost s = sequence(b, q_base);
+      {
+        const long long per = s.upto(s.M), rest = x0 - before;
+        kvh = (int)(rest / per);
+        const long long in = rest - kvh * per;
+        int n = s.M;   // the last unit that begins at `in` or before
+        while (n > 1) {
+          const int step = (n + 31) / 32, i = m + lane * step;
+          const uint32_t ballot = __ballot_sync(0xffffffffu, lane * step < n && s.upto(i) <= in);
+          const int k = __popc(ballot) - 1;
+          m += k * step;
+          n = min(step, n - k * step);
+        }
+        before += kvh * per + s.upto(m);
+      }
+      while (ok && before < x1) {
+        const int keys = s.keys(m), n = (keys + 127) / 128;
+        // The tile that place x of all costs lies at.
+        auto tile_at = [&](long long x) {
+          const long long r = x - before - kUnitOverhead + 64;
+          return r <= 0 ? 0 : (int)min((long long)n, r >> 7);
+        };
+        const long long end = before + kUnitOverhead + keys;
+        const int t0 = x0 > before ? tile_at(x0) : 0, t1 = x1 >= end ? n : tile_at(x1);
+        if (t1 > t0 || (n == 0 && before >= x0)) {
+          const bool whole = t0 == 0 && t1 == n;
+          Piece pc = {};
+          pc.work = 1;
+          pc.q_row = q_base + m * RP;
+          pc.n_pos = min(RP, s.nq - m * RP);
+          pc.kvh = kvh, pc.b = b, pc.nk = s.nk, pc.t0 = t0;
+          pc.vis = m * RP + s.nk - s.nq;
+          auto tiles_of = [&](int q) {
+            const int last = min((q + 1) * p.P, pc.n_pos);   // positions up to the end of Q tile q
+            if (last <= q * p.P) return 0;
+            const int seen = p.causal ? pc.vis + last : s.nk;
+            return seen <= 0 ? 0 : max(min((seen + 127) / 128, t1) - t0, 0);
+          };
+          pc.n0 = tiles_of(0);
+          pc.n1 = NQ == 2 ? tiles_of(1) : 0;
+          pc.slot = whole ? -1 : t0 > 0 ? 2 * me : 2 * me + 1;
+          if (t0 == 0 && !whole) {
+            // Parts: mine, and one of each CTA whose share begins before the place where the last tile is reached.
+            const long long place = min(end, before + kUnitOverhead + 128LL * n - 64);
+            const int last = (int)((place * shares + W - 1) / W) - 1;
+            cut0 = make_int4(pc.q_row, pc.kvh, pc.n_pos, last - me + 1);
+          }
+          ok = publish(pc) && load(pc);
+        }
+        before = end;
+        if (++m == s.M) {
+          m = 0;
+          if (++kvh == p.c.Hkv) {
+            kvh = 0;
+            // The next sequence with queries.
+            int b0 = b + 1;
+            b = p.B;
+            for (; b0 < p.B; b0 += 32) {
+              const int i = b0 + lane;
+              const bool any = i < p.B && __ldg(p.cu + i + 1) > __ldg(p.cu + i);
+              const uint32_t ballot = __ballot_sync(0xffffffffu, any);
+              if (ballot) {
+                b = b0 + __ffs(ballot) - 1;
+                s = sequence(b, q_base);
+                if (s.M > 0) break;
+                b0 = b - 31;   // unsound: on behind it
+                b = p.B;
+              }
+            }
+            if (b == p.B) break;
+          }
+        }
+      }
+    }
+    if (lane == 0) p.cut[me] = cut0;
+    if (ok) {
+      Piece none = {};
+      publish(none);
+    } else if (!INT4) {
+      // Unwinding: let every copy still in flight land before the CTA exits.
+      auto land = [&](uint64_t* bar, uint32_t phase) {
+        const uint64_t t = global_timer_ns();
+        while (!mbar_try_wait(smem_addr(bar), phase & 1) && global_timer_ns() - t < p.timeout_ns) {}
+      };
+      for (uint32_t i = n_k > (uint32_t)NK ? n_k - NK : 0u; i < n_k; ++i) land(&bar_k_full[i % NK], i / NK);
+      for (uint32_t i = n_k > (uint32_t)NV ? n_k - NV : 0u; i < n_k; ++i) land(&bar_v_full[i % NV], i / NV);
+      if (n_q > 0) land(&bar_q_full, n_q - 1);
+      if (n_patch > 0) land(&bar_patch, n_patch - 1);
+    }
+  } else if (warp >= C::WARP_PV && warp < C::WARP_PV + NQ) {
+    // ------------------------------------------------------------------ PV issuer, one per Q tile
+    if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REGS_ROLES>();
+    if (lane == 0) {
+      const int q = warp - C::WARP_PV;
+      const uint32_t d_o = tmem + C::O_COL + q * D, a_p = tmem + C::P_COL + C::P_COLS * q;
+      uint32_t n_v = 0, g = 0;   // V tiles of the CTA, products of this Q tile
+      bool ok = true;
+      Piece pc;
+      for (uint32_t it = 0; ok && piece_of_lane(it, pc); ++it) {
+        const int n = q ? pc.n1 : pc.n0, n_all = max(pc.n0, pc.n1);
+        for (int j = 0; ok && j < n_all; ++j, ++n_v) {
+          const uint32_t vs = n_v % NV;
+          if (!mbar_wait(smem_addr(&bar_v_full[vs]), (n_v / NV) & 1, ctl, SITE_KV_FULL)) { ok = false; break; }
+          if (j < n) {
+            const uint32_t b_v = sV + vs * C::TILE_BYTES;
+            if (!mbar_wait(smem_addr(&bar_p_half[q][0]), g & 1, ctl, SITE_P_FULL)) { ok = false; break; }
+            tc_fence_after();
+            issue_pv_half<C, 0>(d_o, a_p, b_v, j > 0);
+            if (!mbar_wait(smem_addr(&bar_p_half[q][1]), g & 1, ctl, SITE_P_FULL)) { ok = false; break; }
+            tc_fence_after();
+            issue_pv_half<C, 1>(d_o, a_p, b_v, true);
+            tc_commit(smem_addr(&bar_o_done[q]));
+            if (j + 1 == n) tc_commit(smem_addr(&bar_o_full[q]));
+            tc_commit(smem_addr(&bar_v_empty[vs]));
+            ++g;
+          } else {
+            mbar_arrive(smem_addr(&bar_v_empty[vs]));
+          }
+        }
+      }
+      // Every MMA this warp issued must finish before TMEM is released.
+      tc_commit(smem_addr(&bar_drain[q]));
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(smem_addr(&bar_drain[q]), 0) && global_timer_ns() - t0 < p.timeout_ns) {}
+    }
+  } else if (warp == C::WARP_S) {
+    // ------------------------------------------------------------------ S issuer
+    if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REGS_ROLES>();
+    if (lane == 0) {
+      uint32_t n_k = 0, n_q = 0, k = 0, g0 = 0, g1 = 0;   // K tiles, Q loads, S products of the CTA and of each Q tile
+      bool ok = true;
+      Piece pc;
+      for (uint32_t it = 0; ok && piece_of_lane(it, pc); ++it) {
+        const int n_all = max(pc.n0, pc.n1);
+        if (n_all == 0) continue;
+        if (!mbar_wait(smem_addr(&bar_q_full), n_q & 1, ctl, SITE_Q_FULL)) { ok = false; break; }
+        ++n_q;
+        for (int j = 0; ok && j < n_all; ++j, ++n_k) {
+          const uint32_t ks = n_k % NK;
+          if (!mbar_wait(smem_addr(&bar_k_full[ks]), (n_k / NK) & 1, ctl, SITE_KV_FULL)) { ok = false; break; }
+          for (int q = 0; ok && q < NQ; ++q) {
+            if (j >= (q ? pc.n1 : pc.n0)) continue;
+            const uint32_t b = k % NSB;
+            if (k >= (uint32_t)NSB && !mbar_wait(smem_addr(&bar_s_free[b]), (k / NSB - 1) & 1, ctl, SITE_S_FREE)) { ok = false; break; }
+            tc_fence_after();
+            issue_qk<C>(tmem + b * 128u, sQ + q * C::TILE_BYTES, sK + ks * C::TILE_BYTES, C::IDESC_QK | p.qk_negate);
+            if constexpr (INT4)
+              mma_f16_ss(tmem + b * 128u, make_sdesc_plain(sQx + q * C::EXT_BYTES, 128, 256),
+                         make_sdesc_plain(sKx + ks * C::EXT_BYTES, 128, 256), C::IDESC_QK | p.qk_negate, 1u);
+            uint32_t& g = q ? g1 : g0;
+            tc_commit(smem_addr(&bar_s_full[q * NSB + g % NSB]));
+            ++g;
+            ++k;
+          }
+          if (!ok) break;
+          tc_commit(smem_addr(&bar_k_empty[ks]));
+          if (j + 1 == n_all) tc_commit(smem_addr(&bar_q_empty));
+        }
+      }
+      tc_commit(smem_addr(&bar_drain[NQ]));
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(smem_addr(&bar_drain[NQ]), 0) && global_timer_ns() - t0 < p.timeout_ns) {}
+    }
+  } else if (INT4 && warp >= C::WARP_UNPACK) {
+    // ------------------------------------------------------------------ 4 bits: query rows, keys and values to fp16
+    if constexpr (INT4) {
+      if constexpr (C::REG_SPLIT) {
+        if constexpr (C::REGS_UNPACK > 65536 / C::THREADS) setmaxnreg_inc<C::REGS_UNPACK>();
+        else setmaxnreg_dec<C::REGS_UNPACK>();
+      }
+      unpack_role<C>(p, tid - 32 * C::WARP_UNPACK, PG, sQ, sQx, sK, sKx, sV, &bar_q_full, &bar_q_empty, bar_k_full, bar_k_empty,
+                     bar_v_full, bar_v_empty, s_kf, s_ve, s_qf, ctl, piece_of_warp);
+    }
+  } else if (warp < C::SOFTMAX_WARPS) {
+    // ------------------------------------------------------------------ softmax + epilogue
+    if constexpr (C::REG_SPLIT) setmaxnreg_inc<C::REGS_SOFTMAX>();
+    const int qt = warp >> 2, r = ((warp & 3) << 5) + lane;   // Q tile; row in it == TMEM lane
+    const int pos_r = (uint32_t)r / p.div_g, g_r = r - pos_r * p.G;
+    const uint32_t lane_base = (uint32_t)((warp & 3) << 5) << 16;
+    const uint32_t tP = tmem + lane_base + C::P_COL + C::P_COLS * qt, tO = tmem + lane_base + C::O_COL + qt * D;
+    // S products of the CTA, of this tile; KV tiles; pieces with work, of the CTA and of this tile
+    uint32_t sbase = 0, g = 0, n_kv = 0, n_q = 0, done = 0;
+    bool ok = true;
+    Piece pc;
+    // P is 2^kUp times larger over 4-bit caches: fp16 then loses 2^-32 of a row's greatest weight times value at most.
+    constexpr float kUp = INT4 ? 7.0f : 0.0f;
+    for (uint32_t it = 0; ok && piece_of_warp(it, pc); ++it) {
+      const int n0 = pc.n0, n1 = pc.n1, n = qt ? n1 : n0;
+      const uint32_t sb = sbase, gb = g, kvb = n_kv;
+      sbase += (uint32_t)(n0 + n1);
+      g += (uint32_t)n;
+      n_kv += (uint32_t)max(n0, n1);
+      const int pos = qt * p.P + pos_r;                    // position in the unit
+      const bool valid = r < PG && pos < pc.n_pos;
+      const int seen = p.causal ? min(pc.nk, pc.vis + pos + 1) : pc.nk;   // keys that this row sees: the first so many
+      const bool empty = seen <= pc.t0 * 128;              // none in this piece
+      float s = p.scale_log2;
+      if (INT4 && n > 0) {
+        // The rows' powers of two come with the query rows.
+        const bool w = mbar_wait(smem_addr(&bar_s_full[qt * NSB + gb % NSB]), (gb / NSB) & 1, ctl, SITE_S_FULL);
+        if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+        s *= s_qf[n_q % (NSB + 1) * C::ROWS + qt * 128 + r];
+      }
+      n_q += n0 > 0 || n1 > 0;
+      float m = -INFINITY;   // running max (log2 units), the exponents' shift
+      float l = 0.0f;        // running sum of exp2(s x - m)
+      for (int j = 0; j < n; ++j) {
+        const uint32_t gj = gb + j;
+        bool w = mbar_wait(smem_addr(&bar_s_full[qt * NSB + gj % NSB]), (gj / NSB) & 1, ctl, SITE_S_FULL);
+        if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+        const int key0 = (pc.t0 + j) * 128;
+        const bool masked = key0 + 128 > pc.nk || (p.causal && key0 + 127 > pc.vis + qt * p.P);
+        tc_fence_after();
+        const uint32_t sbuf = NSB == 1 ? 0u : s_number(sb, qt, j, n0, n1) % NSB;
+        const uint32_t tS = tmem + lane_base + sbuf * 128u;
+        uint32_t sr[128];
+        float mq[4];   // maxima of 32 columns each, taken on the way: the row's of an unmasked tile
+        tmem_ld_32cols_max(tS, sr, mq[0]);
+        tmem_ld_32cols_max(tS + 32, sr + 32, mq[1]);
+        tmem_ld_32cols_max(tS + 64, sr + 64, mq[2]);
+        tmem_ld_32cols_max(tS + 96, sr + 96, mq[3]);
+        float sc[4], ve[4];   // 4 bits: scale of the scores and exponent of the values, of 32 keys each
+        if constexpr (INT4) {
+          const float4 f = s_kf[(kvb + j) % (2 * NK)], e = s_ve[(kvb + j) % (2 * NK)];
+          // never 0, which would make NaN of a masked score; scores that small are 0 either way
+          constexpr float kLeast = 0x1p-126f;
+          sc[0] = fmaxf(s * f.x, kLeast), sc[1] = fmaxf(s * f.y, kLeast), sc[2] = fmaxf(s * f.z, kLeast), sc[3] = fmaxf(s * f.w, kLeast);
+          ve[0] = e.x, ve[1] = e.y, ve[2] = e.z, ve[3] = e.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[i] = s, ve[i] = 0.f;
+        }
+        tmem_ld_wait();
+        reg_fence32(sr);
+        reg_fence32(sr + 32);
+        reg_fence32(sr + 64);
+        reg_fence32(sr + 96);
+        asm volatile("" : "+f"(mq[0]), "+f"(mq[1]), "+f"(mq[2]), "+f"(mq[3]));
+        // S is in registers: its buffer may take the next.
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&bar_s_free[sbuf]));
+        float x[128];
+#pragma unroll
+        for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(sr[c]);
+        if (masked) {
+          const int lim = seen - key0;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= lim) x[c] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float* y = x + 32 * i;
+            float a[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) a[c] = fmax3(y[c], y[c + 4], y[c + 8]);
+#pragma unroll
+            for (int c = 12; c + 8 <= 32; c += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) a[k] = fmax3(a[k], y[c + k], y[c + 4 + k]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) a[c] = fmaxf(a[c], y[28 + c]);
+            mq[i] = fmaxf(fmax3(a[0], a[1], a[2]), a[3]);
+          }
+        }
+        // P = exp2(s x + ve - m) in two halves of 64 keys, handed to the PV issuer one by one. The first is computed with the
+        // row's shift so far, and again where that moves (always on the first tile).
+        auto exp_half = [&](int h, float shift, uint32_t* pk) {
+          float sum = 0.f;
+          if constexpr (INT4) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int c0 = h * 64 + i * 32;
+              const float add = ve[2 * h + i] - shift + kUp;
+              const uint64_t s2 = f2_pack(sc[2 * h + i], sc[2 * h + i]), a2 = f2_pack(add, add);
+              uint64_t acc0 = 0, acc1 = 0;
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                float t0, t1, t2, t3;
+                f2_unpack(f2_fma(f2_pack(x[c0 + c], x[c0 + c + 1]), s2, a2), t0, t1);
+                f2_unpack(f2_fma(f2_pack(x[c0 + c + 2], x[c0 + c + 3]), s2, a2), t2, t3);
+                const float p0 = ex2(t0), p1 = ex2(t1), p2 = ex2(t2), p3 = ex2(t3);
+                acc0 = c ? f2_add(acc0, f2_pack(p0, p1)) : f2_pack(p0, p1);
+                acc1 = c ? f2_add(acc1, f2_pack(p2, p3)) : f2_pack(p2, p3);
+                pk[i * 16 + (c >> 1)] = f16x2_pack(p0, p1);
+                pk[i * 16 + (c >> 1) + 1] = f16x2_pack(p2, p3);
+              }
+              float l0, l1;
+              f2_unpack(f2_add(acc0, acc1), l0, l1);
+              sum = fmaf(l0 + l1, ex2(-ve[2 * h + i]), sum);
+            }
+          } else {
+            const uint64_t s2 = f2_pack(s, s), a2 = f2_pack(-shift, -shift);
+            uint64_t acc0 = 0, acc1 = 0;
+#pragma unroll
+            for (int c = 0; c < 64; c += 4) {
+              const int cc = h * 64 + c;
+              float t0, t1, t2, t3;
+              f2_unpack(f2_fma(f2_pack(x[cc], x[cc + 1]), s2, a2), t0, t1);
+              f2_unpack(f2_fma(f2_pack(x[cc + 2], x[cc + 3]), s2, a2), t2, t3);
+              const float p0 = ex2(t0), p1 = ex2(t1), p2 = ex2(t2), p3 = ex2(t3);
+              acc0 = f2_add(acc0, f2_pack(p0, p1));
+              acc1 = f2_add(acc1, f2_pack(p2, p3));
+              pk[c >> 1] = pack_bf16x2(p0, p1);
+              pk[(c >> 1) + 1] = pack_bf16x2(p2, p3);
+            }
+            float l0, l1;
+            f2_unpack(f2_add(acc0, acc1), l0, l1);
+            sum = l0 + l1;
+          }
+          return sum;
+        };
+        auto store_half = [&](int h, const uint32_t* pk) {
+          tmem_st_32cols(tP + h * 32, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&bar_p_half[qt][h]));
+        };
+        uint32_t pk[32];
+        float sum = exp_half(0, m, pk);
+        float m_tile;
+        if constexpr (INT4)
+          m_tile = fmaxf(fmaxf(fmaf(mq[0], sc[0], ve[0]), fmaf(mq[1], sc[1], ve[1])),
+                         fmaxf(fmaf(mq[2], sc[2], ve[2]), fmaf(mq[3], sc[3], ve[3])));
+        else
+          m_tile = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * s;
+        if (j > 0) {
+          // PV_{j-1} reads the last P, and adds to O, which a rescale changes.
+          w = mbar_wait(smem_addr(&bar_o_done[qt]), (gj - 1) & 1, ctl, SITE_O_DONE);
+          if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+        }
+        float alpha = 1.0f;
+        bool rescale = false;
+        if (m_tile > m + 8.0f) {
+          alpha = ex2(m - m_tile);   // 0 on the first tile
+          m = m_tile;
+          rescale = true;
+        }
+        if (__any_sync(0xffffffffu, rescale)) {
+          if (j > 0) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t ov[32];
+              tmem_ld_32cols(tO + c0, ov);
+              tmem_ld_wait();
+              reg_fence32(ov);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha);
+              tmem_st_32cols(tO + c0, ov);
+            }
+          }
+          sum = exp_half(0, m, pk);
+        }
+        store_half(0, pk);
+        sum += exp_half(1, m, pk);
+        store_half(1, pk);
+        l = l * alpha + sum;
+      }
+      if (!ok) break;
+      // Epilogue: O / l, LSE. A row that sees no key of the piece gives 0 and -inf; its accumulator holds nothing.
+      if (n > 0) {
+        const bool w = mbar_wait(smem_addr(&bar_o_full[qt]), done & 1, ctl, SITE_O_FULL);
+        if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+        ++done;
+        tc_fence_after();
+      }
+      const bool none = empty || n == 0;
+      const float inv_l = 1.0f / l, lse2 = none ? -INFINITY : m + log2f(l) - kUp;
+      // Column of dim i of a group of 8: 4-bit codes are unpacked in the order 0 4 1 5 2 6 3 7.
+      auto col = [](int c) { return INT4 ? (c & ~7) | ((c & 3) << 1) | ((c >> 2) & 1) : c; };
+      if (pc.slot < 0) {
+        const long long row = ((long long)(pc.q_row + pos) * p.H + pc.kvh * p.G + g_r);
+        __nv_bfloat16* orow = p.o + row * D;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 64) {
+          uint32_t pk[32];
+          if (n > 0) {   // the same for the whole warp
+            uint32_t ov[64];
+            tmem_ld_32cols(tO + c0, ov);
+            tmem_ld_32cols(tO + c0 + 32, ov + 32);
+            tmem_ld_wait();
+            reg_fence32(ov);
+            reg_fence32(ov + 32);
+#pragma unroll
+            for (int c = 0; c < 64; c += 2)
+              pk[c >> 1] = none ? 0u
+                                : pack_bf16x2(__uint_as_float(ov[col(c)]) * inv_l, __uint_as_float(ov[col(c + 1)]) * inv_l);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) pk[c] = 0u;
+          }
+          if (valid) {
+            if (p.o_v8) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) st_global_v8(orow + c0 + 16 * i, pk + 8 * i);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(orow + c0);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+            }
+          }
+        }
+        if (valid) p.lse[(long long)(pc.kvh * p.G + g_r) * p.total_q + pc.q_row + pos] = lse2 * 0.69314718055994531f;
+      } else {
+        const long long row = (long long)pc.slot * C::ROWS + qt * 128 + r;
+        float* orow = p.part_o + row * D;
+        if (n > 0) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t ov[32], out[32];
+            tmem_ld_32cols(tO + c0, ov);
+            tmem_ld_wait();
+            reg_fence32(ov);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) out[c] = __float_as_uint(__uint_as_float(ov[col(c)]) * inv_l);
+            if (valid && !none) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) st_global_v8(orow + c0 + 8 * i, out + 8 * i);
+            }
+          }
+        }
+        if (valid) p.part_lse[row] = lse2;
+      }
+      tc_fence_before();
+    }
+  } else {
+    if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REGS_ROLES>();
+  }
+
+  __syncwarp();
+  griddep_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == C::WARP_PV) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+}  // namespace gb300

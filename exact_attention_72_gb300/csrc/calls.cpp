@@ -446,6 +446,38 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// cache address, device, q, page_table, cu_seqlens_q, seqlens, causal, scale (None: 1 / sqrt(d)), workspace, out, lse
+PyObject* fwd_paged_varlen(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&] {
+    const Paged p(a[0], a[1], a[3]);
+    const at::Tensor &q = needed(a[2], "q"), &cu = needed(a[4], "cu_seqlens_q"), &lens = needed(a[5], "seqlens"),
+                     *ws = workspace(a[8]), *out = tensor(a[9], "out"), *lse = tensor(a[10], "lse");
+    const int* cup = p.ints(cu, "cu_seqlens_q", 1);
+    const int* lenp = p.ints(lens, "seqlens", 0);
+    if (q.dim() != 3 || q.scalar_type() != at::kBFloat16 || !q.is_contiguous())
+      refuse("q must be a contiguous bfloat16 CUDA tensor [total_q, H, d]");
+    const int total = as_int(q.size(0), "total_q"), H = as_int(q.size(1), "H"), d = p.cache->d;
+    if (q.size(2) != d || p.cache->Hkv <= 0 || H < 1 || H % p.cache->Hkv != 0)
+      refuse("q must be [total_q, H, d] with the cache's d and a multiple of its heads");
+    check_like(out, "out", q);
+    const int64_t rows[2] = {H, total};
+    if (lse && (lse->sizes() != at::IntArrayRef(rows, 2) || lse->scalar_type() != at::kFloat || !lse->is_contiguous()))
+      refuse("lse must be a contiguous float32 CUDA tensor [H, total_q]");
+    const int causal = truth(a[6]);
+    const float scale = a[7] == Py_None ? (float)(1.0 / std::sqrt((double)d)) : (float)number(a[7]);
+    const cudaStream_t s = p.stream({&p.table, &q, &cu, &lens, ws, out, lse});
+    const bool any_rows = p.B > 0 && total > 0;   // nothing to launch for otherwise
+    const Workspace work(ws, ws || !any_rows ? 0 : attn_fwd_paged_varlen_workspace_bytes(p.B, H, p.cache->Hkv, total, d, p.cache->type));
+    Out o(a[9], out, q.sizes(), at::kBFloat16, q), l(a[10], lse, at::IntArrayRef(rows, 2), at::kFloat, q);
+    if (any_rows)
+      check_status(launch([&] {
+        return attn_fwd_paged_varlen(q.data_ptr(), p.cache, o.ptr, (float*)l.ptr, (const int*)p.table.data_ptr(), p.stride,
+                                     p.max_pages, cup, lenp, p.B, H, total, scale, causal, work.ptr, work.bytes, s);
+      }), "attn_fwd_paged_varlen");
+    return tuple({o.object(), l.object()});
+  });
+}
+
 // AttnError, torch.OutOfMemoryError: once, before the first call.
 PyObject* set_errors(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 2, [&] {
@@ -462,6 +494,7 @@ PyMethodDef methods[] = {{"qk_norm_rope", FAST(qk_norm_rope), nullptr},
                          {"paged_append", FAST(paged_append), nullptr},
                          {"paged_gather", FAST(paged_gather), nullptr},
                          {"fwd_paged", FAST(fwd_paged), nullptr},
+                         {"fwd_paged_varlen", FAST(fwd_paged_varlen), nullptr},
                          {"set_errors", FAST(set_errors), nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

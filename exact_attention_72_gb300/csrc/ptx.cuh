@@ -197,6 +197,7 @@ __host__ __device__ constexpr uint32_t make_idesc(uint32_t ab_format, int M, int
 }
 // Bit 13 of the instruction descriptor negates the A operand (floating-point kinds).
 constexpr uint32_t kIdescNegateA = 1u << 13;
+constexpr uint32_t kFmtF16 = 0;
 constexpr uint32_t kFmtBF16 = 1;
 constexpr uint32_t kFmtE4M3 = 0;
 

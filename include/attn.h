@@ -499,6 +499,35 @@ attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t* cache, voi
                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * attn_fwd_paged_varlen — attention of a chunk of new tokens of each sequence over the cache: prompts computed piece by
+ * piece on top of what is cached of them, decoding sequences (chunks of one token) in the same batch.
+ *   q, o: DEVICE bf16 [total_q, H, d], contiguous, 16-byte aligned; sequence b owns rows cu_seqlens_q[b] ..
+ *      cu_seqlens_q[b + 1] - 1 (it may own none). lse: DEVICE fp32 [H, total_q], natural log. Query head h reads kv head
+ *      h / (H / Hkv); H / Hkv may be any whole number up to 128.
+ *   cu_seqlens_q: DEVICE int32 [B + 1], ascending; rows from cu_seqlens_q[B] on are left as they were.
+ *   seqlens: DEVICE int32 [B], keys of each sequence in the cache, its new tokens' own among them (attn_paged_append).
+ *   causal: query i of n sees keys j <= i + seqlens[b] - n (bottom-right aligned, as attn_fwd_varlen); otherwise all.
+ *      Rows that see no key get O = 0, LSE = -inf.
+ *   scale as in attn_fwd (finite, nonzero).
+ *   workspace: DEVICE, 256-byte aligned, at least attn_fwd_paged_varlen_workspace_bytes(...) bytes (which depend on d and
+ *      the device alone); needs no initialisation. Calls that may overlap on the GPU (captured graphs included) need one
+ *      each. q, o, lse and workspace must not overlap each other or the cache.
+ * Offsets and lengths stay on the device: the call can be captured and replayed with others. A sequence whose offsets do
+ * not ascend or pass total_q has no rows; pages and lengths out of range as above; each is reported by attn_get_status.
+ * Over 4-bit caches q, keys and values are held in fp16 times powers of two (of a query row; of 32 neighbouring keys):
+ * below 2^-21 of a row's, or 2^-29 of 32 keys', greatest value they lose bits. Deterministic. Two programmatic dependent
+ * launches; allocates nothing; total_q == 0 returns ATTN_OK at once.
+ * UNSUPPORTED as for the cache, for scale == 0, H / Hkv > 128, total_q or max_pages * page_size >= 2^31 - 1023, strides
+ * of a bf16 cache that tensor maps do not take (2^40 bytes and more, or 0 between two rows), and for more than 2^52 / Hkv
+ * keys over all blocks of queries.
+ */
+size_t attn_fwd_paged_varlen_workspace_bytes(int B, int H, int Hkv, int total_q, int d, attn_cache_type_t type);
+attn_status_t attn_fwd_paged_varlen(const void* q, const attn_paged_cache_t* cache, void* o, float* lse,
+                                    const int* page_table, long long table_stride, int max_pages,
+                                    const int* cu_seqlens_q, const int* seqlens, int B, int H, int total_q, float scale,
+                                    int causal, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * attn_get_status — synchronizes `stream`, then returns ATTN_ERR_TIMEOUT if any kernel of this
  * library on the current device gave up a bounded wait since the last attn_clear_status,
  * ATTN_ERR_INVALID_ARG if a varlen forward was handed a plan that does not match it (or that the
