@@ -98,6 +98,11 @@ def lib() -> ctypes.CDLL:
     L.attn_qk_norm_rope_bwd.restype = i
     L.attn_qk_norm_rope_bwd.argtypes = [vp] * 8 + [i] * 4 + [ll] * 4 + [i, vp, vp, f, vp, vp, i, i, i, vp, i, vp, sz,
                                                                        vp]
+    axes = [i, vp, vp, f, vp, vp, i, i, i, vp, ll, i, ctypes.c_char_p]
+    L.attn_qk_norm_rope_axes.restype = i
+    L.attn_qk_norm_rope_axes.argtypes = [vp] * 4 + [i] * 4 + [ll] * 4 + axes + [vp]
+    L.attn_qk_norm_rope_axes_bwd.restype = i
+    L.attn_qk_norm_rope_axes_bwd.argtypes = [vp] * 8 + [i] * 4 + [ll] * 4 + axes + [vp, sz, vp]
     L.attn_paged_append.restype = i
     L.attn_paged_append.argtypes = [cache, vp, vp, ll, ll, ll, ll, vp, vp, vp, ll, i, i, i, vp, vp, i, i, i, vp]
     L.attn_paged_gather.restype = i
@@ -548,8 +553,8 @@ def attn_qk_norm_rope(q, k=None, cos=None, sin=None, positions=None, wq=None, wk
     """
     call = (_CALLS or _calls()).qk_norm_rope
     if stream is not None:
-        return _on(stream, call, q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, q_out, k_out)
-    return call(q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, q_out, k_out)
+        return _on(stream, call, q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, None, q_out, k_out)
+    return call(q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, None, q_out, k_out)
 
 
 def attn_qk_norm_rope_bwd_workspace_bytes(T: int, H: int, Hkv: int, d: int) -> int:
@@ -563,9 +568,44 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out=None, cos=None, sin=None, positio
     from attn_bwd); dwq and dwk are float32 [d], None without weights. dq and dk may be dq_out and dk_out."""
     call = (_CALLS or _calls()).qk_norm_rope_bwd
     if stream is not None:
-        return _on(stream, call, q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, dq_out, dk_out, dq, dk, dwq, dwk,
-                   workspace)
-    return call(q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, dq_out, dk_out, dq, dk, dwq, dwk, workspace)
+        return _on(stream, call, q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, None, dq_out, dk_out, dq, dk, dwq,
+                   dwk, workspace)
+    return call(q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, None, dq_out, dk_out, dq, dk, dwq, dwk, workspace)
+
+
+def rope_pair_axes(sections, turns: bool = False) -> bytes:
+    """``pair_axis`` of axes that own sections[a] pairs each: in blocks, or (``turns``) one after the other while they have
+    pairs left (0 1 2 0 1 2 ... 0 0)."""
+    if not turns:
+        return bytes(a for a, n in enumerate(sections) for _ in range(n))
+    return bytes(a for i in range(max(sections, default=0)) for a, n in enumerate(sections) if i < n)
+
+
+def attn_qk_norm_rope_axes(q, k, cos, sin, positions, pair_axis, wq=None, wk=None, eps: float = 1e-6, norm: bool = True,
+                           interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """attn_qk_norm_rope with positions on several axes (time, height, width): (q_out, k_out).
+
+    ``positions`` is int32 [axes, B, N] or [axes, T], 1 to 4 axes. ``pair_axis`` (bytes, or a sequence of whole numbers)
+    holds the axis of every pair: pair i turns by cos, sin[positions[pair_axis[i]], i]. rope_pair_axes makes it of the number
+    of pairs of each axis. The rest as attn_qk_norm_rope; k may be None.
+    """
+    call = (_CALLS or _calls()).qk_norm_rope
+    axes = pair_axis if type(pair_axis) is bytes else bytes(pair_axis)
+    if stream is not None:
+        return _on(stream, call, q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, axes, q_out, k_out)
+    return call(q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, axes, q_out, k_out)
+
+
+def attn_qk_norm_rope_axes_bwd(q, k, dq_out, dk_out, cos, sin, positions, pair_axis, wq=None, wk=None, eps: float = 1e-6,
+                               norm: bool = True, interleaved: bool = False, dq=None, dk=None, dwq=None, dwk=None,
+                               workspace=None, stream=None):
+    """Gradients (dq, dk, dwq, dwk) of attn_qk_norm_rope_axes, as attn_qk_norm_rope_bwd gives them."""
+    call = (_CALLS or _calls()).qk_norm_rope_bwd
+    axes = pair_axis if type(pair_axis) is bytes else bytes(pair_axis)
+    if stream is not None:
+        return _on(stream, call, q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, axes, dq_out, dk_out, dq, dk, dwq,
+                   dwk, workspace)
+    return call(q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, axes, dq_out, dk_out, dq, dk, dwq, dwk, workspace)
 
 
 class PagedKVCache:

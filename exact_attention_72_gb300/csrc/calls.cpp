@@ -244,7 +244,8 @@ attn_status_t launch(F&& f) {   // other Python threads run while a launch waits
   return st;
 }
 
-// What the norm's forward and backward share: q, k, cos, sin, positions, wq, wk, eps, norm, interleaved.
+// What the norm's forward and backward share: q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, pair_axis (bytes, the
+// axis of every pair; positions then hold one more dim, the axes; None: one axis).
 struct NormRope {
   const at::Tensor &q, *k, *cos, *sin, *positions, *wq, *wk;
   float eps;
@@ -253,6 +254,8 @@ struct NormRope {
   Rope rope;
   const float *wqp, *wkp;
   int T, H, Hkv, d, N;
+  int axes = 0;                            // 0: the entries with one axis
+  const unsigned char* pair_axis = nullptr;
 
   explicit NormRope(PyObject* const* a)
       : q(needed(a[0], "q")), k(tensor(a[1], "k")), cos(tensor(a[2], "cos")), sin(tensor(a[3], "sin")),
@@ -266,9 +269,20 @@ struct NormRope {
     } else if (wk) {
       refuse("wk needs k");
     }
-    if (positions && (positions->scalar_type() != at::kInt || positions->sizes() != q.sizes().slice(0, q.dim() - 2) ||
-                      !positions->is_contiguous()))
+    if (a[10] != Py_None) {
+      if (!PyBytes_Check(a[10])) throw WrongType("pair_axis must be bytes");
+      pair_axis = (const unsigned char*)PyBytes_AS_STRING(a[10]);
+      const int64_t n = q.dim() - 2;
+      if (!positions || !cos || positions->scalar_type() != at::kInt || positions->dim() != n + 1 ||
+          positions->sizes().slice(1) != q.sizes().slice(0, n) || !positions->is_contiguous())
+        refuse("positions must be a contiguous int32 CUDA tensor [axes, ...], one per axis and token, with cos and sin");
+      axes = as_int(positions->size(0), "the number of axes");
+      if (axes < 1 || axes > 4 || cos->dim() != 2 || PyBytes_GET_SIZE(a[10]) != cos->size(1))
+        refuse("pair_axis must hold the axis of every pair (a column of cos), of 1 to 4 axes");
+    } else if (positions && (positions->scalar_type() != at::kInt || positions->sizes() != q.sizes().slice(0, q.dim() - 2) ||
+                             !positions->is_contiguous())) {
       refuse("positions must be a contiguous int32 CUDA tensor, one per token");
+    }
     rope = rope_of(cos, sin, rq.T);
     wqp = vector_of(wq, "wq", rq.d), wkp = vector_of(wk, "wk", rq.d);
     T = as_int(rq.T, "the number of tokens"), H = as_int(rq.heads, "heads"), Hkv = as_int(rk.heads, "heads");
@@ -277,40 +291,45 @@ struct NormRope {
 };
 
 PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 12, [&] {
+  return guarded(n, 13, [&] {
     const NormRope x(a);
-    const at::Tensor *qo = tensor(a[10], "q_out"), *ko = tensor(a[11], "k_out");
+    const at::Tensor *qo = tensor(a[11], "q_out"), *ko = tensor(a[12], "k_out");
     if (ko && !x.k) refuse("k_out needs k");
     check_like(qo, "q_out", x.q);
     if (x.k) check_like(ko, "k_out", *x.k);
     const cudaStream_t s = launch_stream({&x.q, x.k, x.cos, x.sin, x.positions, x.wq, x.wk, qo, ko});
-    Out q_out(a[10], qo, x.q.sizes(), at::kBFloat16, x.q);
+    Out q_out(a[11], qo, x.q.sizes(), at::kBFloat16, x.q);
     std::optional<Out> k_out;
-    if (x.k) k_out.emplace(a[11], ko, x.k->sizes(), at::kBFloat16, x.q);
+    if (x.k) k_out.emplace(a[12], ko, x.k->sizes(), at::kBFloat16, x.q);
     if (x.T > 0)
       check_status(launch([&] {
+        if (x.axes)
+          return attn_qk_norm_rope_axes(x.q.data_ptr(), pointer(x.k), q_out.ptr, k_out ? k_out->ptr : nullptr, x.T, x.H, x.Hkv,
+                                        x.d, x.rq.st, x.rq.sh, x.rk.st, x.rk.sh, x.norm, x.wqp, x.wkp, x.eps, x.rope.cos,
+                                        x.rope.sin, x.rope.dim, x.rope.max_pos, x.interleaved, (const int*)pointer(x.positions),
+                                        x.T, x.axes, x.pair_axis, s);
         return attn_qk_norm_rope(x.q.data_ptr(), pointer(x.k), q_out.ptr, k_out ? k_out->ptr : nullptr, x.T, x.H, x.Hkv, x.d,
                                  x.rq.st, x.rq.sh, x.rk.st, x.rk.sh, x.norm, x.wqp, x.wkp, x.eps, x.rope.cos, x.rope.sin,
                                  x.rope.dim, x.rope.max_pos, x.interleaved, (const int*)pointer(x.positions), x.N, s);
-      }), "attn_qk_norm_rope");
+      }), x.axes ? "attn_qk_norm_rope_axes" : "attn_qk_norm_rope");
     return tuple({q_out.object(), k_out ? k_out->object() : none()});
   });
 }
 
-// The ten shared arguments, then dq_out, dk_out, dq, dk, dwq, dwk, workspace.
+// The eleven shared arguments, then dq_out, dk_out, dq, dk, dwq, dwk, workspace.
 PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 17, [&] {
+  return guarded(n, 18, [&] {
     const NormRope x(a);
-    const at::Tensor &gq = needed(a[10], "dq_out"), *gk = tensor(a[11], "dk_out"), *dq = tensor(a[12], "dq"),
-                     *dk = tensor(a[13], "dk"), *dwq = tensor(a[14], "dwq"), *dwk = tensor(a[15], "dwk"),
-                     *ws = workspace(a[16]);
+    const at::Tensor &gq = needed(a[11], "dq_out"), *gk = tensor(a[12], "dk_out"), *dq = tensor(a[13], "dq"),
+                     *dk = tensor(a[14], "dk"), *dwq = tensor(a[15], "dwq"), *dwk = tensor(a[16], "dwk"),
+                     *ws = workspace(a[17]);
     if ((gk != nullptr) != (x.k != nullptr)) refuse("dk_out is given exactly with k");
     if ((dk && !x.k) || (dwq && !x.wq) || (dwk && !x.wk)) refuse("dk needs k, dwq needs wq and dwk needs wk");
     check_like(&gq, "dq_out", x.q), check_like(dq, "dq", x.q);
     if (x.k) check_like(gk, "dk_out", *x.k), check_like(dk, "dk", *x.k);
     vector_of(dwq, "dwq", x.d), vector_of(dwk, "dwk", x.d);
     const cudaStream_t s = launch_stream({&x.q, x.k, x.cos, x.sin, x.positions, x.wq, x.wk, &gq, gk, dq, dk, dwq, dwk, ws});
-    Out o_q(a[12], dq, x.q.sizes(), at::kBFloat16, x.q);
+    Out o_q(a[13], dq, x.q.sizes(), at::kBFloat16, x.q);
     at::Tensor made_k, made_wq, made_wk;
     if (x.k && !dk) made_k = make(x.k->sizes(), at::kBFloat16, x.q), dk = &made_k;
     if (x.wq && !dwq) made_wq = make({x.d}, at::kFloat, x.q), dwq = &made_wq;
@@ -321,18 +340,24 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else {
       const Workspace work(ws, dwq || dwk ? attn_qk_norm_rope_bwd_workspace_bytes(x.T, x.H, x.Hkv, x.d) : 0);
       check_status(launch([&] {
+        if (x.axes)
+          return attn_qk_norm_rope_axes_bwd(x.q.data_ptr(), pointer(x.k), gq.data_ptr(), pointer(gk), o_q.ptr, pointer(dk),
+                                            (float*)pointer(dwq), (float*)pointer(dwk), x.T, x.H, x.Hkv, x.d, x.rq.st, x.rq.sh,
+                                            x.rk.st, x.rk.sh, x.norm, x.wqp, x.wkp, x.eps, x.rope.cos, x.rope.sin, x.rope.dim,
+                                            x.rope.max_pos, x.interleaved, (const int*)pointer(x.positions), x.T, x.axes,
+                                            x.pair_axis, work.ptr, work.bytes, s);
         return attn_qk_norm_rope_bwd(x.q.data_ptr(), pointer(x.k), gq.data_ptr(), pointer(gk), o_q.ptr, pointer(dk),
                                      (float*)pointer(dwq), (float*)pointer(dwk), x.T, x.H, x.Hkv, x.d, x.rq.st, x.rq.sh,
                                      x.rk.st, x.rk.sh, x.norm, x.wqp, x.wkp, x.eps, x.rope.cos, x.rope.sin, x.rope.dim,
                                      x.rope.max_pos, x.interleaved, (const int*)pointer(x.positions), x.N, work.ptr, work.bytes,
                                      s);
-      }), "attn_qk_norm_rope_bwd");
+      }), x.axes ? "attn_qk_norm_rope_axes_bwd" : "attn_qk_norm_rope_bwd");
     }
     auto object = [&](PyObject* given, const at::Tensor* t, at::Tensor& made) {
       if (!t) return none();
       return made.defined() ? THPVariable_Wrap(std::move(made)) : (Py_INCREF(given), given);
     };
-    return tuple({o_q.object(), object(a[13], dk, made_k), object(a[14], dwq, made_wq), object(a[15], dwk, made_wk)});
+    return tuple({o_q.object(), object(a[14], dk, made_k), object(a[15], dwq, made_wq), object(a[16], dwk, made_wk)});
   });
 }
 

@@ -14,6 +14,11 @@
 // flight together, those of the next task behind them. Everything is fp32 between the bf16 loads and the
 // one rounding at the store.
 //
+// With several axes (time, height and width of images and video) a token has a position on each, and pair i turns by the angle
+// of column i at its axis' position: cos[pos[axis(i)], i]. The axes of the pairs are 2 bits each in the launch's parameters. A
+// lane's 4 columns come as one 16-byte load where their positions agree (one axis' block of columns, or text, whose axes
+// agree), and as 4-byte loads otherwise (axes that take turns).
+//
 // Memory bounds both. At B 2, N 8192, 32 + 8 heads, d 128 on a GB300 (share of the copy bandwidth): forward 55.8 us
 // (90%; 102 with rows unpacked at the load and a CTA per 16 tasks, 70 with rows held packed, 56.7 one value an
 // instruction), backward 89.7 us (83%; 155 at first; 114 with 2 heads a task, 92.2 one value an instruction). Angles
@@ -53,6 +58,9 @@ struct NormRopeParams {
   FastDiv parts, div_q, div_k;     // tasks of a token: all, of q, of k
   FastDiv div_seq;
   uint32_t* status;
+  // Several axes: positions [axes, T], axis_st apart, and the axis of every pair in 2 bits.
+  long long axis_st;
+  uint32_t axes, axis_of[8];       // axes: those that some pair turns by, a bit each
 };
 
 // A lane's 8 values of a row: pairs of neighbours, 0 and 1 of its first chunk, 2 and 3 of its second. The arithmetic works
@@ -153,8 +161,23 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// Position of token t; -1 (nothing to store) where it lies outside the tables.
+// Position of token t; -1 (nothing to store) where it lies outside the tables. AXES: of its positions some that its pairs use,
+// -1 where one of those lies outside.
+template <bool AXES>
 __device__ __forceinline__ int position(const NormRopeParams& p, int t, int l) {
+  if constexpr (AXES) {
+    int pos = 0;
+    bool good = true;
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+      if (p.axes >> a & 1) {
+        pos = p.positions[a * p.axis_st + t];
+        good = good && pos >= 0 && pos < p.max_pos;
+      }
+    if (good) return pos;
+    if (l == 0) atomicCAS(p.status, 0u, kStatusBadPosition);
+    return -1;
+  }
   if (!p.cos) return 0;
   const int pos = p.positions ? p.positions[t] : t - (int)((uint32_t)t / p.div_seq) * p.seq_len;
   if (pos >= 0 && pos < p.max_pos) return pos;
@@ -162,13 +185,32 @@ __device__ __forceinline__ int position(const NormRopeParams& p, int t, int l) {
   return -1;
 }
 
-// Angles of position pos; back: for the turn back.
-template <bool INTERLEAVED>
-__device__ __forceinline__ Angles<INTERLEAVED> load_angles(const NormRopeParams& p, int pos, int l, bool back) {
+// Angles of position pos (AXES: of token t's, if pos says that they lie in the tables); back: for the turn back. mine: the axes
+// of this lane's 4 pairs.
+template <bool INTERLEAVED, bool AXES>
+__device__ __forceinline__ Angles<INTERLEAVED> load_angles(const NormRopeParams& p, int pos, int t, uint32_t mine, int l, bool back) {
   float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (turns(l, p.half) && pos >= 0) {
-    const long long at = (long long)pos * p.half + 4 * l;
-    c = *reinterpret_cast<const float4*>(p.cos + at), s = *reinterpret_cast<const float4*>(p.sin + at);
+    bool same = true;
+    int at4[4];
+    if constexpr (AXES) {   // read before, to be checked: they are in the L1 cache
+#pragma unroll
+      for (int i = 0; i < 4; ++i) at4[i] = p.positions[(mine >> (2 * i) & 3u) * p.axis_st + t];
+      pos = at4[0];
+      same = at4[1] == pos && at4[2] == pos && at4[3] == pos;
+    }
+    if (same) {
+      const long long at = (long long)pos * p.half + 4 * l;
+      c = *reinterpret_cast<const float4*>(p.cos + at), s = *reinterpret_cast<const float4*>(p.sin + at);
+    } else if constexpr (AXES) {
+      float cs[4], sn[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const long long at = (long long)at4[i] * p.half + 4 * l + i;
+        cs[i] = p.cos[at], sn[i] = p.sin[at];
+      }
+      c = make_float4(cs[0], cs[1], cs[2], cs[3]), s = make_float4(sn[0], sn[1], sn[2], sn[3]);
+    }
   }
   if (back) s = make_float4(-s.x, -s.y, -s.z, -s.w);
   Angles<INTERLEAVED> r;
@@ -203,12 +245,13 @@ __device__ __forceinline__ Chunks load_weights(const float* w, int da, int db, b
 
 // CTAs walk the tasks of all tokens, one wave of them; a thread has the rows of its next task on their
 // way while it turns those of this one, so that loads are always in flight.
-template <int D, bool NORM, bool INTERLEAVED, bool PART>
+template <int D, bool NORM, bool INTERLEAVED, bool PART, bool AXES>
 __global__ void __launch_bounds__(kThreads, kFwdCtasPerSm) qk_norm_rope_kernel(const NormRopeParams p) {
   griddep_wait();
   griddep_launch_dependents();   // of the next kernel only the launch may overlap: it waits for this one's end
   constexpr int LPR = D / 8, ROWS = kThreads / LPR;
   const int l = threadIdx.x % LPR;
+  const uint32_t axes = AXES ? p.axis_of[l / 4] >> (8 * (l % 4)) : 0u;
   int da, db;
   chunk_dims<INTERLEAVED>(l, p.half, da, db);
   struct Task {
@@ -222,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtasPerSm) qk_norm_rope_kernel(c
     const uint32_t token = id / p.parts;
     const int part = id - token * p.parts.v;
     w.t = token;
-    w.pos = position(p, w.t, l);
+    w.pos = position<AXES>(p, w.t, l);
     w.is_k = part >= p.parts_q;
     w.h0 = (w.is_k ? part - p.parts_q : part) * kHeads;
     const __nv_bfloat16* x = w.is_k ? p.k + w.t * p.k_st : p.q + w.t * p.q_st;
@@ -239,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtasPerSm) qk_norm_rope_kernel(c
   for (uint32_t first = blockIdx.x * ROWS; first < tasks; first += stride, id += stride) {
     Task next = now;
     if (first + stride < tasks) next = load(min(id + stride, tasks - 1));
-    const Angles<INTERLEAVED> r = load_angles<INTERLEAVED>(p, now.pos, l, false);
+    const Angles<INTERLEAVED> r = load_angles<INTERLEAVED, AXES>(p, now.pos, now.t, axes, l, false);
     Chunks w;
     if (NORM) w = load_weights(now.is_k ? p.wk : p.wq, da, db, p.w_vec);
     const int heads = now.is_k ? p.Hkv : p.H, last = id < tasks && now.pos >= 0 ? heads : 0;
@@ -268,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtasPerSm) qk_norm_rope_kernel(c
 // The gradient. CTAs 0 .. ctas_q - 1 walk the tasks of q, the others those of k, so a thread sums the
 // weight gradient of its 8 dims in registers; a CTA adds its rows' sums in a fixed order and leaves
 // [d] in part, which dw_kernel adds up: the same bits every time.
-template <int D, bool NORM, bool INTERLEAVED, bool PART>
+template <int D, bool NORM, bool INTERLEAVED, bool PART, bool AXES>
 __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kernel(const NormRopeParams p) {
   griddep_wait();
   griddep_launch_dependents();   // of the next kernel only the launch may overlap: it waits for this one's end
@@ -280,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kern
   const FastDiv parts = is_k ? p.div_k : p.div_q;
   const float* wp = is_k ? p.wk : p.wq;
   const long long sh = is_k ? p.k_sh : p.q_sh;
+  const uint32_t axes = AXES ? p.axis_of[l / 4] >> (8 * (l % 4)) : 0u;
   int da, db;
   chunk_dims<INTERLEAVED>(l, p.half, da, db);
   Chunks w, dw;
@@ -294,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kern
     Task w;
     w.t = id / parts;
     w.h0 = (id - w.t * parts.v) * kHeads;
-    w.pos = position(p, w.t, l);
+    w.pos = position<AXES>(p, w.t, l);
     const __nv_bfloat16* x = is_k ? p.k + w.t * p.k_st : p.q + w.t * p.q_st;
     const __nv_bfloat16* dy = (is_k ? p.dyk : p.dyq) + (long long)w.t * heads * D;
 #pragma unroll
@@ -312,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kern
   for (uint32_t first = (uint32_t)cta * ROWS; first < tasks; first += stride, id += stride) {
     Task next = now;
     if (first + stride < tasks) next = load(min(id + stride, tasks - 1));
-    const Angles<INTERLEAVED> r = load_angles<INTERLEAVED>(p, now.pos, l, true);
+    const Angles<INTERLEAVED> r = load_angles<INTERLEAVED, AXES>(p, now.pos, now.t, axes, l, true);
     const int last = id < tasks && now.pos >= 0 ? heads : 0;
     __nv_bfloat16* dx = (is_k ? p.ok : p.oq) + ((long long)now.t * heads + now.h0) * D;
 #pragma unroll
@@ -388,7 +432,10 @@ __global__ void __launch_bounds__(1024) dw_kernel(const float* __restrict__ part
 template <int D, class F>
 cudaError_t with_kind(const NormRopeParams& p, bool norm, bool interleaved, F&& f) {
   const bool part = 2 * p.half != D;
-  auto go = [&](auto n, auto i) { return part ? f(n, i, std::true_type{}) : f(n, i, std::false_type{}); };
+  auto go = [&](auto n, auto i) {
+    if (p.axes) return part ? f(n, i, std::true_type{}, std::true_type{}) : f(n, i, std::false_type{}, std::true_type{});
+    return part ? f(n, i, std::true_type{}, std::false_type{}) : f(n, i, std::false_type{}, std::false_type{});
+  };
   if (norm) return interleaved ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
   return interleaved ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
 }
@@ -397,15 +444,15 @@ template <int D>
 cudaError_t launch_forward(const NormRopeParams& p, bool norm, bool interleaved, int sms, cudaStream_t s) {
   const long long tasks = (long long)p.T * (p.parts_q + p.parts_k), rows = kThreads / (D / 8);
   const unsigned grid = (unsigned)std::min<long long>((tasks + rows - 1) / rows, (long long)kFwdCtasPerSm * sms);
-  return with_kind<D>(p, norm, interleaved, [&](auto n, auto i, auto part) {
-    return launch_dependent(qk_norm_rope_kernel<D, n(), i(), part()>, dim3(grid), dim3(kThreads), 0, s, p);
+  return with_kind<D>(p, norm, interleaved, [&](auto n, auto i, auto part, auto axes) {
+    return launch_dependent(qk_norm_rope_kernel<D, n(), i(), part(), axes()>, dim3(grid), dim3(kThreads), 0, s, p);
   });
 }
 
 template <int D>
 cudaError_t launch_backward(const NormRopeParams& p, bool norm, bool interleaved, int grid, cudaStream_t s) {
-  return with_kind<D>(p, norm, interleaved, [&](auto n, auto i, auto part) {
-    return launch_dependent(qk_norm_rope_bwd_kernel<D, n(), i(), part()>, dim3((unsigned)grid), dim3(kThreads), 0, s, p);
+  return with_kind<D>(p, norm, interleaved, [&](auto n, auto i, auto part, auto axes) {
+    return launch_dependent(qk_norm_rope_bwd_kernel<D, n(), i(), part(), axes()>, dim3((unsigned)grid), dim3(kThreads), 0, s, p);
   });
 }
 
@@ -464,21 +511,45 @@ attn_status_t check(const void* xq, const void* xk, const void* oq, const void* 
   return ATTN_OK;
 }
 
+// Positions on several axes: what an _axes entry is given besides.
+struct Axes {
+  long long stride;
+  int n;
+  const unsigned char* of;   // host, of every pair
+};
+
+// Checks them (the tables and rope_dim have passed check) and puts them into p.
+attn_status_t put_axes(const Axes& a, int T, const float* cos, int rope_dim, const int* positions, NormRopeParams& p) {
+  if (!cos || !positions || !a.of || a.n < 1 || a.n > 4) return ATTN_ERR_INVALID_ARG;
+  if (a.n > 1 && (a.stride < T || a.stride > (1LL << 40))) return ATTN_ERR_INVALID_ARG;
+  p.axis_st = a.n > 1 ? a.stride : 0;
+  for (int i = 0; i < rope_dim / 2; ++i) {
+    if (a.of[i] >= a.n) return ATTN_ERR_INVALID_ARG;
+    p.axes |= 1u << a.of[i];
+    p.axis_of[i / 16] |= (uint32_t)a.of[i] << (2 * (i % 16));
+  }
+  return ATTN_OK;
+}
+
 }  // namespace
 }  // namespace gb300
 
 using namespace gb300;
 
-extern "C" attn_status_t attn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int T, int H,
-                                           int Hkv, int d, long long q_stride_t, long long q_stride_h,
-                                           long long k_stride_t, long long k_stride_h, int norm, const float* wq,
-                                           const float* wk, float eps, const float* cos, const float* sin,
-                                           int rope_dim, int max_pos, int interleaved, const int* positions,
-                                           int seq_len, cudaStream_t stream) {
+static attn_status_t norm_rope(const void* q, const void* k, void* q_out, void* k_out, int T, int H, int Hkv, int d,
+                               long long q_stride_t, long long q_stride_h, long long k_stride_t, long long k_stride_h,
+                               int norm, const float* wq, const float* wk, float eps, const float* cos, const float* sin,
+                               int rope_dim, int max_pos, int interleaved, const int* positions, int seq_len,
+                               const Axes* axes, cudaStream_t stream) {
   const attn_status_t st = check(q, k, q_out, k_out, T, H, Hkv, d, q_stride_t, q_stride_h, k_stride_t, k_stride_h,
                                  norm, wq, wk, eps, cos, sin, rope_dim, max_pos, positions, seq_len);
   if (st != ATTN_OK) return st;
   if (!q || (Hkv > 0) != (k != nullptr)) return ATTN_ERR_INVALID_ARG;
+  NormRopeParams p = {};
+  if (axes) {
+    const attn_status_t sa = put_axes(*axes, T, cos, rope_dim, positions, p);
+    if (sa != ATTN_OK) return sa;
+  }
   // An output may be its own contiguous input (a row is read before it is written); otherwise
   // outputs meet neither the inputs nor each other.
   const Range rq = rows_range(q, T, H, q_stride_t, q_stride_h, d), oq = rows_range(q_out, T, H, (long long)H * d, d, d);
@@ -493,7 +564,6 @@ extern "C" attn_status_t attn_qk_norm_rope(const void* q, const void* k, void* q
   int sms;
   uint32_t* status;
   if (!device_state(&sms, &status)) return ATTN_ERR_CUDA;
-  NormRopeParams p = {};
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k = static_cast<const __nv_bfloat16*>(k);
   p.oq = static_cast<__nv_bfloat16*>(q_out);
@@ -516,6 +586,28 @@ extern "C" attn_status_t attn_qk_norm_rope(const void* q, const void* k, void* q
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+extern "C" attn_status_t attn_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int T, int H,
+                                           int Hkv, int d, long long q_stride_t, long long q_stride_h,
+                                           long long k_stride_t, long long k_stride_h, int norm, const float* wq,
+                                           const float* wk, float eps, const float* cos, const float* sin,
+                                           int rope_dim, int max_pos, int interleaved, const int* positions,
+                                           int seq_len, cudaStream_t stream) {
+  return norm_rope(q, k, q_out, k_out, T, H, Hkv, d, q_stride_t, q_stride_h, k_stride_t, k_stride_h, norm, wq, wk, eps, cos,
+                   sin, rope_dim, max_pos, interleaved, positions, seq_len, nullptr, stream);
+}
+
+extern "C" attn_status_t attn_qk_norm_rope_axes(const void* q, const void* k, void* q_out, void* k_out, int T, int H,
+                                                int Hkv, int d, long long q_stride_t, long long q_stride_h,
+                                                long long k_stride_t, long long k_stride_h, int norm, const float* wq,
+                                                const float* wk, float eps, const float* cos, const float* sin,
+                                                int rope_dim, int max_pos, int interleaved, const int* positions,
+                                                long long axis_stride, int axes, const unsigned char* pair_axis,
+                                                cudaStream_t stream) {
+  const Axes a{axis_stride, axes, pair_axis};
+  return norm_rope(q, k, q_out, k_out, T, H, Hkv, d, q_stride_t, q_stride_h, k_stride_t, k_stride_h, norm, wq, wk, eps, cos,
+                   sin, rope_dim, max_pos, interleaved, positions, 1, &a, stream);
+}
+
 extern "C" size_t attn_qk_norm_rope_bwd_workspace_bytes(int T, int H, int Hkv, int d) {
   if (T < 1 || H < 1 || Hkv < 0 || (d != 64 && d != 128 && d != 256)) return 0;
   int sms = 152;
@@ -524,14 +616,12 @@ extern "C" size_t attn_qk_norm_rope_bwd_workspace_bytes(int T, int H, int Hkv, i
   return (size_t)bwd_grid(T, H, Hkv, d, sms).ctas * d * 4;
 }
 
-extern "C" attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
-                                               void* dq, void* dk, float* dwq, float* dwk, int T, int H, int Hkv,
-                                               int d, long long q_stride_t, long long q_stride_h,
-                                               long long k_stride_t, long long k_stride_h, int norm, const float* wq,
-                                               const float* wk, float eps, const float* cos, const float* sin,
-                                               int rope_dim, int max_pos, int interleaved, const int* positions,
-                                               int seq_len, void* workspace, size_t workspace_bytes,
-                                               cudaStream_t stream) {
+static attn_status_t norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                                   float* dwq, float* dwk, int T, int H, int Hkv, int d, long long q_stride_t,
+                                   long long q_stride_h, long long k_stride_t, long long k_stride_h, int norm,
+                                   const float* wq, const float* wk, float eps, const float* cos, const float* sin,
+                                   int rope_dim, int max_pos, int interleaved, const int* positions, int seq_len,
+                                   const Axes* axes, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   const attn_status_t st = check(norm ? q : nullptr, norm ? k : nullptr, dq, dk, T, H, Hkv, d, q_stride_t, q_stride_h,
                                  k_stride_t, k_stride_h, norm, wq, wk, eps, cos, sin, rope_dim, max_pos, positions,
                                  seq_len);
@@ -539,6 +629,11 @@ extern "C" attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, con
   if (!dq_out || (Hkv > 0) != (dk_out != nullptr) || (norm && (!q || (Hkv > 0) != (k != nullptr))))
     return ATTN_ERR_INVALID_ARG;
   if (!aligned16(dq_out) || !aligned16(dk_out)) return ATTN_ERR_INVALID_ARG;
+  NormRopeParams p = {};
+  if (axes) {
+    const attn_status_t sa = put_axes(*axes, T, cos, rope_dim, positions, p);
+    if (sa != ATTN_OK) return sa;
+  }
   // weight gradients come with their weights
   if ((dwq != nullptr) != (wq != nullptr) || (dwk != nullptr) != (wk != nullptr) || !aligned4(dwq) || !aligned4(dwk))
     return ATTN_ERR_INVALID_ARG;
@@ -576,7 +671,6 @@ extern "C" attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, con
   uint32_t* status;
   if (!device_state(&sms, &status)) return ATTN_ERR_CUDA;
   const BwdGrid g = bwd_grid(T, H, Hkv, d, sms);
-  NormRopeParams p = {};
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k = static_cast<const __nv_bfloat16*>(k);
   p.dyq = static_cast<const __nv_bfloat16*>(dq_out);
@@ -604,4 +698,32 @@ extern "C" attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, con
                          g.ctas_q, g.ctas);
   }
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                                               void* dq, void* dk, float* dwq, float* dwk, int T, int H, int Hkv,
+                                               int d, long long q_stride_t, long long q_stride_h,
+                                               long long k_stride_t, long long k_stride_h, int norm, const float* wq,
+                                               const float* wk, float eps, const float* cos, const float* sin,
+                                               int rope_dim, int max_pos, int interleaved, const int* positions,
+                                               int seq_len, void* workspace, size_t workspace_bytes,
+                                               cudaStream_t stream) {
+  return norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, dwq, dwk, T, H, Hkv, d, q_stride_t, q_stride_h, k_stride_t, k_stride_h,
+                       norm, wq, wk, eps, cos, sin, rope_dim, max_pos, interleaved, positions, seq_len, nullptr, workspace,
+                       workspace_bytes, stream);
+}
+
+extern "C" attn_status_t attn_qk_norm_rope_axes_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                                                    void* dq, void* dk, float* dwq, float* dwk, int T, int H, int Hkv,
+                                                    int d, long long q_stride_t, long long q_stride_h,
+                                                    long long k_stride_t, long long k_stride_h, int norm,
+                                                    const float* wq, const float* wk, float eps, const float* cos,
+                                                    const float* sin, int rope_dim, int max_pos, int interleaved,
+                                                    const int* positions, long long axis_stride, int axes,
+                                                    const unsigned char* pair_axis, void* workspace,
+                                                    size_t workspace_bytes, cudaStream_t stream) {
+  const Axes a{axis_stride, axes, pair_axis};
+  return norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, dwq, dwk, T, H, Hkv, d, q_stride_t, q_stride_h, k_stride_t, k_stride_h,
+                       norm, wq, wk, eps, cos, sin, rope_dim, max_pos, interleaved, positions, 1, &a, workspace,
+                       workspace_bytes, stream);
 }

@@ -405,6 +405,34 @@ attn_status_t attn_qk_norm_rope_bwd(const void* q, const void* k, const void* dq
                                     void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * attn_qk_norm_rope_axes, attn_qk_norm_rope_axes_bwd — the same with positions on several axes, as tokens of images and
+ * video have them (time, height, width; text has the same position on each). Pair i of token t turns by the angle of
+ * column i at its axis' position: cos, sin[positions[pair_axis[i] * axis_stride + t]][i]. The column says the frequency, so
+ * axes may have frequencies of their own.
+ *   cos, sin: as above, not NULL. positions: DEVICE int32, axis a's of token t at positions + a * axis_stride + t,
+ *      axis_stride >= T (with one axis it is not looked at). axes: 1 .. 4.
+ *   pair_axis: HOST [rope_dim / 2], each below axes, read during the call only. Axes that no pair has are not read.
+ * A token with a position outside the tables on an axis that some pair has is not written (and adds nothing to dwq, dwk), and
+ * attn_get_status reports ATTN_ERR_INVALID_ARG. Everything else, the workspace too, as attn_qk_norm_rope and its gradient.
+ */
+attn_status_t attn_qk_norm_rope_axes(const void* q, const void* k, void* q_out, void* k_out, int T, int H,
+                                     int Hkv, int d, long long q_stride_t, long long q_stride_h,
+                                     long long k_stride_t, long long k_stride_h, int norm, const float* wq,
+                                     const float* wk, float eps, const float* cos, const float* sin,
+                                     int rope_dim, int max_pos, int interleaved, const int* positions,
+                                     long long axis_stride, int axes, const unsigned char* pair_axis,
+                                     cudaStream_t stream);
+attn_status_t attn_qk_norm_rope_axes_bwd(const void* q, const void* k, const void* dq_out,
+                                         const void* dk_out, void* dq, void* dk, float* dwq, float* dwk,
+                                         int T, int H, int Hkv, int d, long long q_stride_t,
+                                         long long q_stride_h, long long k_stride_t, long long k_stride_h,
+                                         int norm, const float* wq, const float* wk, float eps,
+                                         const float* cos, const float* sin, int rope_dim, int max_pos,
+                                         int interleaved, const int* positions, long long axis_stride, int axes,
+                                         const unsigned char* pair_axis, void* workspace,
+                                         size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Paged key/value cache. "flash-attention-3" (ai.thesatyajit.com), "What is actually in the box", and
  * "FlashAttention-3 Deep Dive" (mojostudio.in), FAQ on paged KV, name it: keys and values live in
  * pages of page_size tokens, and a page table says which pages hold a sequence, in order.
