@@ -67,20 +67,28 @@ struct PagedVarlenCfg {
   static constexpr uint32_t FMT = INT4 ? kFmtF16 : kFmtBF16;
   static constexpr uint32_t IDESC_QK = make_idesc(FMT, 128, 128, false, false);
   static constexpr uint32_t IDESC_PV = make_idesc(FMT, 128, D, false, true);
-  // Warps: softmax (a warpgroup for each Q tile), then a warpgroup of PV issuers, scheduler / loader and S issuer, then
-  // (4 bits) a warpgroup that unpacks keys and values.
-  static constexpr int SOFTMAX_WARPS = 4 * NQ, WARP_PV = SOFTMAX_WARPS, WARP_LOAD = WARP_PV + 2, WARP_S = WARP_PV + 3;
-  static constexpr int WARP_UNPACK = WARP_PV + 4;
-  static constexpr int THREADS = 32 * (WARP_UNPACK + (INT4 ? 4 : 0));
-  static constexpr bool REG_SPLIT = THREADS > 256;
-  static constexpr uint32_t REGS_SOFTMAX = 200, REGS_ROLES = INT4 ? (NQ == 2 ? 48 : 64) : 96, REGS_UNPACK = NQ == 2 ? 64 : 128;
-  static constexpr int REGS_NEEDED = SOFTMAX_WARPS * 32 * REGS_SOFTMAX + 128 * REGS_ROLES + (INT4 ? 128 * REGS_UNPACK : 0);
+  // Warps: softmax (a warpgroup for each Q tile), then a warpgroup of PV issuers, scheduler and S issuer, then one that feeds
+  // the stages: bf16, two warps issue the copies of keys and two those of values (a page of 16 keys takes a copy for every 64
+  // dims, and a copy 70 cycles of a warp: one warp for all bounded the kernel); 4 bits, all unpack keys, then values.
+  static constexpr int SOFTMAX_WARPS = 4 * NQ, WARP_PV = SOFTMAX_WARPS, WARP_PLAN = WARP_PV + 2, WARP_S = WARP_PV + 3;
+  static constexpr int WARP_FEED = WARP_PV + 4, THREADS = 32 * (WARP_FEED + 4);
+  // Registers, of the launch's 512 x 128 (one Q tile: 384 x 168).
+  static constexpr uint32_t REGS_SOFTMAX = INT4 && NQ == 2 ? 184 : 200;
+  static constexpr uint32_t REGS_ROLES = NQ == 1 ? 64 : INT4 ? 48 : 56, REGS_FEED = NQ == 1 ? 120 : INT4 ? 96 : 56;
+  static constexpr int REGS_NEEDED = SOFTMAX_WARPS * 32 * REGS_SOFTMAX + 128 * REGS_ROLES + 128 * REGS_FEED;
+  static constexpr int FEEDERS = INT4 ? 4 : 2;            // warps that fill a stage
+  // Work of a key in a unit of one Q tile and of two. bf16: a tile of a decoding sequence takes 1.15 us, of a chunk 1.7. 4 bits:
+  // unpacking bounds both.
+  static constexpr int ONE = INT4 || NQ == 1 ? 3 : 2, TWO = 3;
   static constexpr int PIECES = 4;                        // pieces that the scheduler may be ahead
-  static constexpr int CONSUMERS = SOFTMAX_WARPS + NQ + 1 + (INT4 ? 4 : 0);
+  static constexpr int CONSUMERS = SOFTMAX_WARPS + NQ + 1 + 4;
+  // Tiles whose powers of two are kept, and pieces whose query rows' are: K_{j + METAS} waits for S_{j + NK}, which comes after
+  // the softmax has taken S_j from its buffer, and with it all of these; likewise the query rows QFS pieces later.
+  static constexpr int METAS = 2 * NK, QFS = NSB + 1;
 };
 
-constexpr int kUnitOverhead = 2 * 128;     // what beginning and ending a unit costs, in keys
-constexpr long long kLeastShare = 3 * 128;   // of a CTA, in keys
+constexpr int kUnitOverhead = 6 * 128;       // work (see UnitWork) of beginning and ending a unit
+constexpr long long kLeastShare = 12 * 128;   // of a CTA: a share within a unit's beginning would have nothing to do
 
 // Descriptor of an operand without swizzle: 8 x 16-byte core matrices, lbo apart along K, sbo along the rows.
 __device__ __forceinline__ uint64_t make_sdesc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
@@ -92,31 +100,39 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 x) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
 }
 
-// Keys (in 128ths of a tile) that the units of one (sequence, kv head) cost, RP positions each, off = nk - nq: unit m needs the
-// keys that its last query sees and kUnitOverhead. The sum over units 0 .. k - 1:
-struct SeqCost {
-  int nq, nk, M, RP, causal;
+// Work of the units of one (sequence, kv head), P * NQ = RP positions each, off = nk - nq: unit m needs the keys that its last query
+// sees, `one` for each if its rows fill one Q tile at most and `two` if they fill two, and kUnitOverhead.
+struct UnitWork {
+  int nq, nk, M, RP, one, two, causal;
   __device__ int keys(int m) const {
     if (!causal) return nk;
     const long long last = (long long)min((long long)(m + 1) * RP, (long long)nq) + nk - nq;
     return last > 0 ? (int)last : 0;
   }
-  __device__ long long upto(int k) const {
+  __device__ int a_key(int m) const { return nq - m * RP > RP / 2 ? two : one; }
+  __device__ long long upto(int k) const {   // of units 0 .. k - 1
     long long s = (long long)k * kUnitOverhead;
-    if (!causal) return s + (long long)k * nk;
     if (k == M && M > 0) {   // the last unit ends with the last query, which sees all keys
-      s += nk;
       --k;
+      s += (long long)a_key(k) * nk;
     }
+    if (!causal) return s + (long long)k * two * nk;
     const long long off = (long long)nk - nq;
     const long long m0 = off >= 0 ? 0 : -off / RP;   // units before see nothing
-    if (k > m0) s += (k - m0) * off + RP * ((long long)k * (k + 1) / 2 - m0 * (m0 + 1) / 2);
+    if (k > m0) s += two * ((k - m0) * off + RP * ((long long)k * (k + 1) / 2 - m0 * (m0 + 1) / 2));
     return s;
   }
 };
 
 // Wait sites of this kernel besides those of the forward (SITE_*).
-enum : uint32_t { SITE_PIECE_FULL = 16, SITE_PIECE_EMPTY = 17 };
+enum : uint32_t { SITE_PIECE_FULL = 16, SITE_PIECE_EMPTY = 17, SITE_META = 18 };
+
+// A load that is not to be moved behind a wait: what it reads is used a step later.
+__device__ __forceinline__ uint4 load_ahead(const void* p) {
+  uint4 x;
+  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
+  return x;
+}
 
 // 2^e of a float's exponent bits: 1 <= bits <= 254.
 __device__ __forceinline__ float power_of_bits(uint32_t bits) { return __uint_as_float(bits << 23); }
@@ -144,83 +160,164 @@ __device__ __forceinline__ float half_round(float x) { return __half2float(__flo
 
 // The 4-bit cache's operands. Thread r of the warpgroup has query row r of each Q tile and key r of each KV tile.
 //
-// Keys: zero + scale c = scale (c - 8) + zero', zero' = zero + 8 scale. The first term has 11 bits (8 of scale, 3 of c - 8), so
-// fp16 holds it; the second is one value a group of dims, which S takes in as a product of 16 more columns,
+// A code in the high bits of fp16's mantissa is 1 + c / 16: a shift and a three-input logic operation, and a fused multiply-add makes
+// the operand of it.
+// Keys: zero + scale c = scale (c - 8) + zero', zero' = zero + 8 scale. The first term, 16 scale (1 + c / 16) - 24 scale, has 11
+// bits (8 of scale, 3 of c - 8), so fp16 holds it; the second is one value a group of dims, which S takes in as a product of 16
+// more columns,
 //   zero' sum(q) = (zh + zl) (Qh + Ql),    zh + zl and Qh + Ql the two values in 22 bits each.
 // So S is what fp32 would give. In bf16 the keys would be 2^-8 off, and LSE with them (2e-5 of it over 1000 keys).
-// Values: zero + scale c rounded once to fp16, 2^-11 off, as P is; in bf16 the two would add as much to O's error as its own
-// rounding.
+// Values: 16 scale (1 + c / 16) + (zero - 16 scale), the sum and its second term rounded to fp16, 2^-11 off each, as P is; in bf16
+// the two would add as much to O's error as its own rounding.
 // fp16's range: every 32 keys (a warp's) of a tile are divided by a power of two that brings the greatest of them below 2^15, a
 // query row by one that brings its greatest value into [2^7, 2^8). Full precision is left to values 2^-29 of the greatest of
 // their 32 keys (query rows: 2^-21), others are off by 2^-40 (2^-33) of it. The softmax puts the keys' power back into the
 // scores, and the values' into the weights' exponents: the running maximum is over weights times those powers, and the weights
 // are summed without them.
+// Waits, with a limit, until the copies that a phase counts have landed.
+__device__ __forceinline__ void land(uint64_t* bar, uint32_t phase, unsigned long long timeout_ns) {
+  const uint64_t t = global_timer_ns();
+  while (!mbar_try_wait(smem_addr(bar), phase & 1) && global_timer_ns() - t < timeout_ns) {}
+}
+
+// The bf16 cache's keys or values, by one warp of the two that share the work. Lane i copies box 2 i + half of a tile: 64 columns
+// (box % NCH) of box_rows neighbouring keys (box / NCH), which lie in one page.
+template <class C, class F>
+__device__ __forceinline__ void load_role(const PagedVarlenParams& p, int half, bool is_v, const CUtensorMap* map, uint32_t tiles,
+                                          uint64_t* bar_full, uint64_t* bar_empty, uint64_t* bar_patch, const WaitCtl& ctl,
+                                          F& piece_of_warp) {
+  constexpr int NCH = C::NCH, NS = C::NK;
+  static_assert(C::NK == C::NV, "one count of stages for both");
+  const int lane = threadIdx.x & 31, rows = p.box_rows, boxes = 128 / rows * NCH;
+  const int box = 2 * lane + half, chunk = box % NCH, at = box / NCH * rows;
+  const bool mine = box < boxes;
+  const uint32_t dst = chunk * C::CHUNK_BYTES + at * 128, bytes = (uint32_t)((boxes + 1 - half) / 2 * rows * 128);
+  if (lane == 0) tma_prefetch_desc(map);
+  uint32_t n_t = 0, n_patch = 0;   // tiles, patched ones
+  Piece pc;
+  bool ok = true;
+  for (uint32_t it = 0; ok && piece_of_warp(it, pc); ++it) {
+    const int n = max(pc.n0, pc.n1);
+    const int* table = p.table + pc.b * p.table_stride;
+    auto look_up = [&](int t) {
+      const int key = t * 128 + at;
+      return mine && key < pc.nk ? __ldg(table + (uint32_t)key / p.div_page) : -1;
+    };
+    int page = n > 0 ? look_up(pc.t0) : -1;
+    for (int j = 0; j < n; ++j) {
+      const int key0 = (pc.t0 + j) * 128, key = key0 + at, tok = key - (int)((uint32_t)key / p.div_page) * p.c.page_size;
+      if (mine && key < pc.nk && (page < 0 || page >= p.c.num_pages)) {
+        atomicCAS(p.status, 0u, kStatusBadPage);
+        page = -1;   // outside the map: zeros, as for keys behind the last
+      }
+      const int from = page;
+      if (j + 1 < n) page = look_up(pc.t0 + j + 1);
+      const uint32_t stage = n_t % NS, tile = tiles + stage * C::TILE_BYTES;
+      bool w = n_t < (uint32_t)NS || mbar_wait(smem_addr(&bar_empty[stage]), (n_t / NS - 1) & 1, ctl, SITE_KV_EMPTY);
+      if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+      ++n_t;
+      if (p.debug_skip_load && blockIdx.x == 0 && is_v && n_t == 1) continue;
+      // Values of the last page's rows behind the sequence's end may be anything, and 0 times NaN is NaN: they are cleared.
+      const bool patch = is_v && pc.nk - key0 < 128 && pc.nk % rows != 0;
+      const uint32_t bar = smem_addr(patch ? bar_patch : &bar_full[stage]);
+      if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+      __syncwarp();
+      if (mine) tma_load_4d(tile + dst, map, bar, chunk * 64, tok, pc.kvh, from);
+      if (patch) {
+        ++n_patch;
+        w = mbar_wait(bar, (n_patch - 1) & 1, ctl, SITE_KV_FULL);
+        if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+        const int r0 = pc.nk - key0, last = r0 / rows, n_rows = (last + 1) * rows - r0;
+        for (int i = lane; i < n_rows * 8 * NCH; i += 32) {
+          const int r = i / (8 * NCH), c = i % (8 * NCH);
+          if ((last * NCH + c / 8) % 2 == half)   // of a box of mine
+            sts128(tile + c / 8 * C::CHUNK_BYTES + (r0 + r) * 128 + c % 8 * 16, make_uint4(0u, 0u, 0u, 0u));
+        }
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&bar_full[stage]));
+      }
+    }
+  }
+  if (!ok || *ctl.abort_flag) {   // unwinding: let every copy still in flight land before the CTA exits
+    for (uint32_t i = n_t > (uint32_t)NS ? n_t - NS : 0u; i < n_t; ++i) land(&bar_full[i % NS], i / NS, p.timeout_ns);
+    if (n_patch > 0) land(bar_patch, n_patch - 1, p.timeout_ns);
+  }
+}
+
 template <class C, class F>
 __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int r, int PG, uint32_t sQ, uint32_t sQx, uint32_t sK,
                                             uint32_t sKx, uint32_t sV, uint64_t* bar_q_full, uint64_t* bar_q_empty,
                                             uint64_t* bar_k_full, uint64_t* bar_k_empty, uint64_t* bar_v_full,
-                                            uint64_t* bar_v_empty, float4* s_kf, float4* s_ve, float* s_qf, const WaitCtl& ctl,
-                                            F& piece_of_warp) {
+                                            uint64_t* bar_v_empty, uint64_t* bar_meta, float4* s_kf, float4* s_ve, float* s_qf,
+                                            const WaitCtl& ctl, F& piece_of_warp) {
   constexpr int D = C::D, NQ = C::NQ, NK = C::NK, NV = C::NV, GROUPS = D / kInt4Group;
   constexpr int WORDS = D >= 128 ? 16 : 8;      // 8 codes each, of a step
   constexpr int HALVES = D / 8 / WORDS;         // steps of a row
+  constexpr int STEP_GROUPS = WORDS / 8;        // groups of dims of a step
   const int lane = r & 31, w = r >> 5;
   const uint32_t swz = (uint32_t)(r & 7), row_at = (uint32_t)r * 128, ext_at = (uint32_t)(r >> 3) * 256 + (r & 7) * 16;
-  const int pos_r = (uint32_t)r / p.div_g, g_r = r - pos_r * p.G;
-  uint32_t n_q = 0, n_k = 0;
+  uint32_t n_q = 0, n_k = 0;                    // pieces with work, tiles
   Piece pc;
   for (uint32_t it = 0; piece_of_warp(it, pc); ++it) {
-    const int n = max(pc.n0, pc.n1);
+    const int n = max(pc.n0, pc.n1), nk = pc.nk, t0 = pc.t0;
     if (n == 0) continue;
-    // My key's row: of its page in the page table, and where its codes and pairs begin (-1: nowhere).
+    // My key's page in the page table, and where its codes and pairs begin (codes -1: nowhere).
+    const int* table = p.table + pc.b * p.table_stride;
+    const long long head = pc.kvh * p.c.head_b, sz_head = pc.kvh * p.c.sz_head_b;
     auto look_up = [&](int t) {
       const int key = t * 128 + r;
-      return key < pc.nk ? __ldg(p.table + pc.b * p.table_stride + (uint32_t)key / p.div_page) : -1;
+      return key < nk ? __ldg(table + (uint32_t)key / p.div_page) : -1;
     };
-    long long at = -1, at_sz = -1;
+    uint32_t ksz[GROUPS], vsz[GROUPS];
+    auto fetch_pairs = [&](uint32_t (&x)[GROUPS], const uint8_t* from) {
+      if constexpr (GROUPS == 1) {
+        x[0] = __ldg(reinterpret_cast<const uint32_t*>(from));
+      } else if constexpr (GROUPS == 2) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(from));
+        x[0] = u.x, x[1] = u.y;
+      } else {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(from));
+        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+      }
+    };
+    long long at = -1;
     auto locate = [&](int t, int page) {
       const int key = t * 128 + r;
-      at = at_sz = -1;
-      if (key >= pc.nk) return;
+      at = -1;
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) ksz[g] = vsz[g] = 0u;
+      if (key >= nk) return;
       if (page < 0 || page >= p.c.num_pages) {
         atomicCAS(p.status, 0u, kStatusBadPage);
         return;
       }
       const int tok = key - (int)((uint32_t)key / p.div_page) * p.c.page_size;
-      at = page * p.c.page_b + tok * p.c.token_b + pc.kvh * p.c.head_b;
-      at_sz = page * p.c.sz_page_b + tok * p.c.sz_token_b + pc.kvh * p.c.sz_head_b;
+      at = page * p.c.page_b + tok * p.c.token_b + head;
+      const long long sz = page * p.c.sz_page_b + tok * p.c.sz_token_b + sz_head;
+      fetch_pairs(ksz, p.c.k_sz + sz);
+      fetch_pairs(vsz, p.c.v_sz + sz);
     };
-    uint32_t buf[2][WORDS];
-    auto fetch = [&](uint32_t (&x)[WORDS], const uint8_t* base, int half) {
+    // Codes of two steps: the one that is unpacked next and the one behind it, on its way.
+    uint32_t now[WORDS], next[WORDS];
+    auto fetch = [&](uint32_t (&x)[WORDS], long long row, bool is_v, int half) {
+      const uint8_t* from = (is_v ? p.c.v : p.c.k) + row + half * (WORDS * 4);
 #pragma unroll
       for (int i = 0; i < WORDS / 4; ++i) {
-        const uint4 u = at < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                               : __ldg(reinterpret_cast<const uint4*>(base + at + half * (WORDS * 4)) + i);
+        const uint4 u = row < 0 ? make_uint4(0u, 0u, 0u, 0u) : load_ahead(from + i * 16);
         x[4 * i] = u.x, x[4 * i + 1] = u.y, x[4 * i + 2] = u.z, x[4 * i + 3] = u.w;
       }
     };
-    auto fetch_pairs = [&](uint32_t (&x)[GROUPS], const uint8_t* base) {
-      if constexpr (GROUPS == 1) {
-        x[0] = at < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t*>(base + at_sz));
-      } else if constexpr (GROUPS == 2) {
-        const uint2 u = at < 0 ? make_uint2(0u, 0u) : __ldg(reinterpret_cast<const uint2*>(base + at_sz));
-        x[0] = u.x, x[1] = u.y;
-      } else {
-        const uint4 u = at < 0 ? make_uint4(0u, 0u, 0u, 0u) : __ldg(reinterpret_cast<const uint4*>(base + at_sz));
-        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
-      }
-    };
-    uint32_t ksz[GROUPS], vsz[GROUPS];
-    int page = look_up(pc.t0);
-    locate(pc.t0, page);
-    fetch(buf[0], p.c.k, 0);
-    fetch_pairs(ksz, p.c.k_sz);
-    fetch_pairs(vsz, p.c.v_sz);
-    page = n > 1 ? look_up(pc.t0 + 1) : -1;
+    locate(t0, look_up(t0));
+    fetch(now, at, false, 0);
+    fetch(next, at, HALVES == 1, HALVES - 1);
+    int page = n > 1 ? look_up(t0 + 1) : -1;
 
     // Query rows, once the S products of the last piece have read theirs.
     bool ok = n_q == 0 || mbar_wait(smem_addr(bar_q_empty), (n_q - 1) & 1, ctl, SITE_Q_EMPTY);
     if (!__all_sync(0xffffffffu, ok)) return;
+    const int pos_r = (uint32_t)r / p.div_g, g_r = r - pos_r * p.G;
+#pragma unroll 1
     for (int q = 0; q < NQ; ++q) {
       if ((q ? pc.n1 : pc.n0) == 0) continue;
       const int pos = q * p.P + pos_r;
@@ -234,22 +331,23 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int r, i
       }
       const uint32_t bits = max(max(most & 0xffffu, most >> 16) >> 7, 8u);   // exponent of the greatest
       const float f = valid ? power_of_bits(261u - bits) : 0.f;
-      s_qf[n_q % (C::NSB + 1) * C::ROWS + q * 128 + r] = power_of_bits(bits - 7u);
+      s_qf[n_q % C::QFS * C::ROWS + q * 128 + r] = power_of_bits(bits - 7u);
       uint32_t ext[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) ext[i] = 0u;
+      const uint32_t to = sQ + q * C::TILE_BYTES + row_at;
 #pragma unroll
       for (int ch = 0; ch < C::NCH; ++ch) {
         float sum = 0.f;
-#pragma unroll
-        for (int u8 = 0; u8 < 8; ++u8) {
+#pragma unroll 2
+        for (uint32_t u8 = 0; u8 < 8; ++u8) {
           const uint4 u = valid ? __ldg(src + ch * 8 + u8) : make_uint4(0u, 0u, 0u, 0u);
           const float d0 = __uint_as_float(u.x << 16) * f, d1 = __uint_as_float(u.x & 0xffff0000u) * f;
           const float d2 = __uint_as_float(u.y << 16) * f, d3 = __uint_as_float(u.y & 0xffff0000u) * f;
           const float d4 = __uint_as_float(u.z << 16) * f, d5 = __uint_as_float(u.z & 0xffff0000u) * f;
           const float d6 = __uint_as_float(u.w << 16) * f, d7 = __uint_as_float(u.w & 0xffff0000u) * f;
           sum += ((d0 + d1) + (d2 + d3)) + ((d4 + d5) + (d6 + d7));
-          sts128(sQ + (q * C::NCH + ch) * C::CHUNK_BYTES + row_at + ((u8 ^ swz) << 4),
+          sts128(to + ch * C::CHUNK_BYTES + ((u8 ^ (uint32_t)(r & 7)) << 4),
                  make_uint4(f16x2_pack(d0, d4), f16x2_pack(d1, d5), f16x2_pack(d2, d6), f16x2_pack(d3, d7)));
         }
         const float hi = half_round(sum), lo = sum - hi;
@@ -264,83 +362,87 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int r, i
     ++n_q;
 
     for (int j = 0; j < n; ++j, ++n_k) {
-      const uint32_t ks = n_k % NK, vs = n_k % NV;
-      uint32_t s2[GROUPS], z2[GROUPS];   // scales (and zeros) as pairs
+      const uint32_t ks = n_k % NK, vs = n_k % NV, meta = n_k % C::METAS;
+      // Powers of two of my warp's keys and values.
+      uint32_t mk = 0, mv = 0;
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) {
+        const float scale = __uint_as_float(ksz[g] << 16), zero = __uint_as_float(ksz[g] & 0xffff0000u);
+        mk = max(mk, __float_as_uint(fmaxf(fabsf(scale) * 24.f, fabsf(fmaf(8.f, scale, zero)))));
+        const float vscale = __uint_as_float(vsz[g] << 16), vzero = __uint_as_float(vsz[g] & 0xffff0000u);
+        mv = max(mv, __float_as_uint(fmaf(16.f, fabsf(vscale), fabsf(vzero))));
+      }
+      const uint32_t bk = min(max(__reduce_max_sync(0xffffffffu, mk) >> 23, 15u), 254u);
+      // Not below 2^-80: weights without their powers are summed in fp32.
+      const uint32_t bv = min(max(__reduce_max_sync(0xffffffffu, mv) >> 23, 61u), 254u);
+      const float fk = power_of_bits(268u - bk), fv = power_of_bits(268u - bv);
+      ok = n_k < (uint32_t)NK || mbar_wait(smem_addr(&bar_k_empty[ks]), (n_k / NK - 1) & 1, ctl, SITE_KV_EMPTY);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      if (lane == 0) {
+        reinterpret_cast<float*>(s_kf + meta)[w] = power_of_bits(bk - 14u);
+        reinterpret_cast<float*>(s_ve + meta)[w] = (float)((int)bv - 141);
+        mbar_arrive(smem_addr(&bar_meta[meta]));
+      }
+      // What codes are multiplied with and what is added, a pair of fp16 of each group.
+      uint32_t kpair[GROUPS], vpair[GROUPS], ext[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ext[i] = 0u;
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) {
+        const float scale = __uint_as_float(ksz[g] << 16) * fk, zero = __uint_as_float(ksz[g] & 0xffff0000u) * fk;
+        const float z = fmaf(8.f, scale, zero), hi = half_round(z);
+        kpair[g] = f16x2_pack(16.f * scale, -24.f * scale);
+        ext[2 * g] = ext[2 * g + 1] = f16x2_pack(hi, z - hi);
+        const float vscale = __uint_as_float(vsz[g] << 16) * fv, vzero = __uint_as_float(vsz[g] & 0xffff0000u) * fv;
+        vpair[g] = f16x2_pack(16.f * vscale, fmaf(-16.f, vscale, vzero));
+      }
+      sts128(sKx + ks * C::EXT_BYTES + ext_at, make_uint4(ext[0], ext[1], ext[2], ext[3]));
+      sts128(sKx + ks * C::EXT_BYTES + ext_at + 128, make_uint4(ext[4], ext[5], ext[6], ext[7]));
+      // The next tile's pairs, and its row for the codes two steps ahead.
+      const long long here = at;
+      if (j + 1 < n) {
+        locate(t0 + j + 1, page);
+        if (j + 2 < n) page = look_up(t0 + j + 2);
+      }
+      // Not unrolled over steps: the roles' code would not stay in the instruction caches (unrolled over a tile, 0.8 warps a
+      // scheduler waited for instructions at any time).
 #pragma unroll
       for (int step = 0; step < 2 * HALVES; ++step) {
         const bool is_v = step >= HALVES;
-        const int half = step % HALVES;
-        // The next step's codes, on their way while this one's are unpacked.
-        if (step + 1 < 2 * HALVES) {
-          fetch(buf[(step + 1) & 1], step + 1 >= HALVES ? p.c.v : p.c.k, (step + 1) % HALVES);
-        } else if (j + 1 < n) {
-          locate(pc.t0 + j + 1, page);
-          fetch(buf[0], p.c.k, 0);
-          fetch_pairs(ksz, p.c.k_sz);
-          fetch_pairs(vsz, p.c.v_sz);
-          if (j + 2 < n) page = look_up(pc.t0 + j + 2);
+        const int half = HALVES == 1 ? 0 : step % HALVES;
+        if (step == HALVES) {
+          ok = n_k < (uint32_t)NV || mbar_wait(smem_addr(&bar_v_empty[vs]), (n_k / NV - 1) & 1, ctl, SITE_KV_EMPTY);
+          if (!__all_sync(0xffffffffu, ok)) return;
         }
-        if (half == 0) {
-          if (!is_v) {
-            // Powers of two of my warp's keys and values.
-            uint32_t mk = 0, mv = 0;
+        uint32_t s2[STEP_GROUPS], z2[STEP_GROUPS];
 #pragma unroll
-            for (int g = 0; g < GROUPS; ++g) {
-              const float scale = __uint_as_float(ksz[g] << 16), zero = __uint_as_float(ksz[g] & 0xffff0000u);
-              mk = max(mk, __float_as_uint(fmaxf(fabsf(scale) * 8.f, fabsf(fmaf(8.f, scale, zero)))));
-              const float vscale = __uint_as_float(vsz[g] << 16), vzero = __uint_as_float(vsz[g] & 0xffff0000u);
-              mv = max(mv, __float_as_uint(fmaf(15.f, fabsf(vscale), fabsf(vzero))));
-            }
-            const uint32_t bk = min(max(__reduce_max_sync(0xffffffffu, mk) >> 23, 15u), 254u);
-            // Not below 2^-80: weights without their powers are summed in fp32.
-            const uint32_t bv = min(max(__reduce_max_sync(0xffffffffu, mv) >> 23, 61u), 254u);
-            const float nk = power_of_bits(268u - bk), nv = power_of_bits(268u - bv);
-            uint32_t ext[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ext[i] = 0u;
-            const uint32_t meta = n_k % (2 * NK);
-#pragma unroll
-            for (int g = 0; g < GROUPS; ++g) {
-              const float scale = __uint_as_float(ksz[g] << 16), zero = __uint_as_float(ksz[g] & 0xffff0000u);
-              const float z = fmaf(8.f, scale, zero) * nk, hi = half_round(z);
-              s2[g] = f16x2_pack(scale * nk, scale * nk);
-              ext[2 * g] = ext[2 * g + 1] = f16x2_pack(hi, z - hi);
-              // The values' pairs, as they are needed in the next steps.
-              const float vscale = __uint_as_float(vsz[g] << 16) * nv, vzero = __uint_as_float(vsz[g] & 0xffff0000u) * nv;
-              z2[g] = f16x2_pack(vscale, vzero);
-            }
-            ok = n_k < (uint32_t)NK || mbar_wait(smem_addr(&bar_k_empty[ks]), (n_k / NK - 1) & 1, ctl, SITE_KV_EMPTY);
-            if (!__all_sync(0xffffffffu, ok)) return;
-            if (lane == 0) {
-              reinterpret_cast<float*>(s_kf + meta)[w] = power_of_bits(bk - 14u);
-              reinterpret_cast<float*>(s_ve + meta)[w] = (float)((int)bv - 141);
-            }
-            sts128(sKx + ks * C::EXT_BYTES + ext_at, make_uint4(ext[0], ext[1], ext[2], ext[3]));
-            sts128(sKx + ks * C::EXT_BYTES + ext_at + 128, make_uint4(ext[4], ext[5], ext[6], ext[7]));
-          } else {
-#pragma unroll
-            for (int g = 0; g < GROUPS; ++g) s2[g] = __byte_perm(z2[g], 0, 0x1010), z2[g] = __byte_perm(z2[g], 0, 0x3232);
-            ok = n_k < (uint32_t)NV || mbar_wait(smem_addr(&bar_v_empty[vs]), (n_k / NV - 1) & 1, ctl, SITE_KV_EMPTY);
-            if (!__all_sync(0xffffffffu, ok)) return;
-          }
+        for (int g = 0; g < STEP_GROUPS; ++g) {
+          const uint32_t kk = HALVES > 1 && half ? kpair[(g + STEP_GROUPS) % GROUPS] : kpair[g];
+          const uint32_t vv = HALVES > 1 && half ? vpair[(g + STEP_GROUPS) % GROUPS] : vpair[g];
+          const uint32_t pair = is_v ? vv : kk;
+          s2[g] = __byte_perm(pair, 0, 0x1010), z2[g] = __byte_perm(pair, 0, 0x3232);
         }
-        const uint32_t tile = (is_v ? sV + vs * C::TILE_BYTES : sK + ks * C::TILE_BYTES) + row_at;
+        const uint32_t to = (is_v ? sV + vs * C::TILE_BYTES : sK + ks * C::TILE_BYTES) + row_at + half * (2 * C::CHUNK_BYTES);
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) {
-          const int word = half * WORDS + i, ch = word / 8, u8 = word % 8;
-          const uint32_t x = buf[step & 1][i];
-          uint32_t y[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {   // codes k and k + 4 as 1024 + c
-            const uint32_t c = ((x >> (4 * k)) & 0x000f000fu) | 0x64006400u;
-            y[k] = is_v ? half2_fma(half2_sub(c, 0x64006400u), s2[ch], z2[ch]) : half2_mul(half2_sub(c, 0x64086408u), s2[ch]);
-          }
-          sts128(tile + ch * C::CHUNK_BYTES + ((u8 ^ swz) << 4), make_uint4(y[0], y[1], y[2], y[3]));
+          // Codes m and m + 4 in the high bits of fp16's mantissa, 1 + code / 16.
+          const uint32_t x = now[i], mask = 0x03c003c0u, one = 0x3c003c00u, s = s2[i / 8], z = z2[i / 8];
+          sts128(to + i / 8 * C::CHUNK_BYTES + ((i % 8 ^ swz) << 4),
+                 make_uint4(half2_fma((x << 6 & mask) | one, s, z), half2_fma((x << 2 & mask) | one, s, z),
+                            half2_fma((x >> 2 & mask) | one, s, z), half2_fma((x >> 6 & mask) | one, s, z)));
         }
         if (half == HALVES - 1) {
           fence_async_proxy();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(is_v ? &bar_v_full[vs] : &bar_k_full[ks]));
+        }
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) now[i] = next[i];
+        // Two steps on: with one step a row the next tile's; with two the values of this, then the next tile's keys.
+        if (HALVES == 1 || is_v) {
+          if (j + 1 < n) fetch(next, at, HALVES == 1 ? is_v : false, half);
+        } else {
+          fetch(next, here, true, half);
         }
       }
     }
@@ -356,13 +458,13 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bar_q_full, bar_q_empty, bar_k_full[NK], bar_k_empty[NK], bar_v_full[NV], bar_v_empty[NV];
   __shared__ __align__(8) uint64_t bar_s_full[NQ * NSB], bar_s_free[NSB], bar_p_half[NQ][2], bar_o_done[NQ], bar_o_full[NQ];
-  __shared__ __align__(8) uint64_t bar_piece_full[C::PIECES], bar_piece_empty[C::PIECES], bar_patch, bar_drain[NQ + 1];
+  __shared__ __align__(8) uint64_t bar_piece_full[C::PIECES], bar_piece_empty[C::PIECES], bar_patch[2], bar_drain[NQ + 1];
+  __shared__ __align__(8) uint64_t bar_meta[C::METAS];
   __shared__ Piece s_pieces[C::PIECES];
   // 4 bits: powers of two of the keys (as factors of S) and values (as exponents) of every 32 keys of a tile, and of the
-  // query rows. A tile's are overwritten two rounds of the K stages later, when its softmax has long read them: K_{j + 2 NK}
-  // waits for S_{j + NK}, which comes after the softmax has taken S_j from its buffer.
-  __shared__ float4 s_kf[INT4 ? 2 * NK : 1], s_ve[INT4 ? 2 * NK : 1];
-  __shared__ float s_qf[INT4 ? (NSB + 1) * C::ROWS : 1];   // a piece's are read before its first S leaves its buffer
+  // query rows.
+  __shared__ float4 s_kf[INT4 ? C::METAS : 1], s_ve[INT4 ? C::METAS : 1];
+  __shared__ float s_qf[INT4 ? C::QFS * C::ROWS : 1];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t abort_flag;
 
@@ -376,8 +478,8 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
     abort_flag = 0u;
     mbar_init(smem_addr(&bar_q_full), INT4 ? 4 : 1);
     mbar_init(smem_addr(&bar_q_empty), 1);
-    for (int i = 0; i < NK; ++i) mbar_init(smem_addr(&bar_k_full[i]), INT4 ? 4 : 1), mbar_init(smem_addr(&bar_k_empty[i]), 1);
-    for (int i = 0; i < NV; ++i) mbar_init(smem_addr(&bar_v_full[i]), INT4 ? 4 : 1), mbar_init(smem_addr(&bar_v_empty[i]), NQ);
+    for (int i = 0; i < NK; ++i) mbar_init(smem_addr(&bar_k_full[i]), C::FEEDERS), mbar_init(smem_addr(&bar_k_empty[i]), 1);
+    for (int i = 0; i < NV; ++i) mbar_init(smem_addr(&bar_v_full[i]), C::FEEDERS), mbar_init(smem_addr(&bar_v_empty[i]), NQ);
     for (int i = 0; i < NQ * NSB; ++i) mbar_init(smem_addr(&bar_s_full[i]), 1);
     for (int i = 0; i < NSB; ++i) mbar_init(smem_addr(&bar_s_free[i]), 4);
     for (int i = 0; i < NQ; ++i) {
@@ -390,7 +492,8 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
       mbar_init(smem_addr(&bar_piece_full[i]), 1);
       mbar_init(smem_addr(&bar_piece_empty[i]), C::CONSUMERS);
     }
-    mbar_init(smem_addr(&bar_patch), 1);
+    for (int i = 0; i < C::METAS; ++i) mbar_init(smem_addr(&bar_meta[i]), 4);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&bar_patch[i]), 1);
     for (int i = 0; i < NQ + 1; ++i) mbar_init(smem_addr(&bar_drain[i]), 1);
     fence_mbar_init();
   }
@@ -406,6 +509,7 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
   __syncthreads();
   tc_fence_after();
   griddep_wait();   // launched early: what it reads may be a previous kernel's
+  griddep_launch_dependents();   // the joining kernel's CTAs may wait beside these, all of which run by now
   const uint32_t tmem = tmem_slot;
   const int PG = p.P * p.G, RP = p.P * NQ;
 
@@ -427,15 +531,11 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
     return pc.work != 0;
   };
 
-  if (warp == C::WARP_LOAD) {
-    // ------------------------------------------------------------------ scheduler, and TMA producer over a bf16 cache
-    if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REGS_ROLES>();
-    if (!INT4 && lane == 0) {
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-    }
-    uint32_t n_pieces = 0, n_k = 0, n_q = 0, n_patch = 0;   // published, K (and V) tiles, Q loads, patched V tiles
+  if (warp == C::WARP_PLAN) {
+    // ------------------------------------------------------------------ scheduler, and copies of queries over a bf16 cache
+    setmaxnreg_dec<C::REGS_ROLES>();
+    if (!INT4 && lane == 0) tma_prefetch_desc(&tm_q);
+    uint32_t n_pieces = 0, n_q = 0;   // published, Q loads
     bool ok = true;
     // Publishes a piece; its consumers are at most PIECES behind.
     auto publish = [&](const Piece& pc) {
@@ -452,78 +552,26 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
       ++n_pieces;
       return true;
     };
-    // Loads of a piece.
-    auto load = [&](const Piece& pc) {
-      if constexpr (!INT4) {
-        const int n = max(pc.n0, pc.n1);
-        if (n == 0) return true;
-        bool w = n_q == 0 || mbar_wait(smem_addr(&bar_q_empty), (n_q - 1) & 1, ctl, SITE_Q_EMPTY);
-        if (!__all_sync(0xffffffffu, w)) return false;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(smem_addr(&bar_q_full), ((pc.n0 > 0) + (pc.n1 > 0)) * NCH * PG * 128);
-          for (int q = 0; q < NQ; ++q) {
-            if ((q ? pc.n1 : pc.n0) == 0) continue;
-            for (int ch = 0; ch < NCH; ++ch)
-              tma_load_4d(sQ + (q * NCH + ch) * C::CHUNK_BYTES, &tm_q, smem_addr(&bar_q_full), ch * 64, 0,
-                          pc.q_row + q * p.P, pc.kvh);
-          }
-        }
-        ++n_q;
-        // Lane i copies 64 columns of box_rows neighbouring keys: chunk i % NCH of the tile's piece i / NCH.
-        const int rows = p.box_rows, at = lane / NCH * rows;
-        const bool mine = lane < 128 / rows * NCH;
-        const uint32_t dst = lane % NCH * C::CHUNK_BYTES + at * 128;
-        auto look_up = [&](int t) {
-          const int key = t * 128 + at;
-          return mine && key < pc.nk ? __ldg(p.table + pc.b * p.table_stride + (uint32_t)key / p.div_page) : -1;
-        };
-        int page = look_up(pc.t0);
-        for (int j = 0; j < n; ++j) {
-          const int key0 = (pc.t0 + j) * 128, key = key0 + at, tok = key - (int)((uint32_t)key / p.div_page) * p.c.page_size;
-          if (mine && key < pc.nk && (page < 0 || page >= p.c.num_pages)) {
-            atomicCAS(p.status, 0u, kStatusBadPage);
-            page = -1;   // outside the map: zeros, as for keys behind the last
-          }
-          const int from = page;
-          if (j + 1 < n) page = look_up(pc.t0 + j + 1);
-          const uint32_t ks = n_k % NK, vs = n_k % NV;
-          w = n_k < (uint32_t)NK || mbar_wait(smem_addr(&bar_k_empty[ks]), (n_k / NK - 1) & 1, ctl, SITE_KV_EMPTY);
-          if (!__all_sync(0xffffffffu, w)) return false;
-          if (lane == 0) mbar_arrive_expect_tx(smem_addr(&bar_k_full[ks]), C::TILE_BYTES);
-          __syncwarp();
-          if (mine) tma_load_4d(sK + ks * C::TILE_BYTES + dst, &tm_k, smem_addr(&bar_k_full[ks]), lane % NCH * 64, tok, pc.kvh, from);
-          w = n_k < (uint32_t)NV || mbar_wait(smem_addr(&bar_v_empty[vs]), (n_k / NV - 1) & 1, ctl, SITE_KV_EMPTY);
-          ++n_k;
-          if (!__all_sync(0xffffffffu, w)) return false;
-          if (p.debug_skip_load && blockIdx.x == 0 && n_k == 1) continue;
-          // Rows of the last page behind the sequence's end may hold anything, and 0 times NaN is NaN: they are cleared.
-          const bool patch = pc.nk - key0 < 128 && pc.nk % rows != 0;
-          const uint32_t bar = smem_addr(patch ? &bar_patch : &bar_v_full[vs]);
-          if (lane == 0) mbar_arrive_expect_tx(bar, C::TILE_BYTES);
-          __syncwarp();
-          const uint32_t tile = sV + vs * C::TILE_BYTES;
-          if (mine) tma_load_4d(tile + dst, &tm_v, bar, lane % NCH * 64, tok, pc.kvh, from);
-          if (patch) {
-            ++n_patch;
-            w = mbar_wait(bar, (n_patch - 1) & 1, ctl, SITE_KV_FULL);
-            if (!__all_sync(0xffffffffu, w)) return false;
-            const int r0 = pc.nk - key0, n_rows = (r0 + rows - 1) / rows * rows - r0;
-            for (int i = lane; i < n_rows * 8 * NCH; i += 32) {
-              const int r = i / (8 * NCH), c = i % (8 * NCH);
-              sts128(tile + c / 8 * C::CHUNK_BYTES + (r0 + r) * 128 + c % 8 * 16, make_uint4(0u, 0u, 0u, 0u));
-            }
-            fence_async_proxy();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&bar_v_full[vs]));
-          }
+    // The query rows of a piece, once the S products of the last one have read theirs.
+    auto load_queries = [&](const Piece& pc) {
+      if (INT4 || (pc.n0 == 0 && pc.n1 == 0)) return true;
+      const bool w = n_q == 0 || mbar_wait(smem_addr(&bar_q_empty), (n_q - 1) & 1, ctl, SITE_Q_EMPTY);
+      if (!__all_sync(0xffffffffu, w)) return false;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(smem_addr(&bar_q_full), ((pc.n0 > 0) + (pc.n1 > 0)) * NCH * PG * 128);
+        for (int q = 0; q < NQ; ++q) {
+          if ((q ? pc.n1 : pc.n0) == 0) continue;
+          for (int ch = 0; ch < NCH; ++ch)
+            tma_load_4d(sQ + (q * NCH + ch) * C::CHUNK_BYTES, &tm_q, smem_addr(&bar_q_full), ch * 64, 0, pc.q_row + q * p.P, pc.kvh);
         }
       }
+      ++n_q;
       return true;
     };
 
     // Sequence b as far as the offsets and lengths are sound; nq = 0 otherwise.
     auto sequence = [&](int b, int& q_base) {
-      SeqCost s{0, 0, 0, RP, p.causal};
+      UnitWork s{0, 0, 0, RP, C::ONE, C::TWO, p.causal};
       q_base = 0;
       if (b < p.B) {
         const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), n = __ldg(p.lens + b);
@@ -537,7 +585,7 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
     // Costs of 32 sequences from b0 on: mine, and of all of them up to mine.
     auto costs = [&](int b0, long long& mine) {
       int q_base;
-      const SeqCost s = sequence(b0 + lane, q_base);
+      const UnitWork s = sequence(b0 + lane, q_base);
       mine = p.c.Hkv * s.upto(s.M);
       long long upto = mine;
 #pragma unroll
@@ -547,9 +595,9 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
       }
       return upto;
     };
-    // All costs, dealt to the CTAs in equal contiguous shares: mine is [x0, x1).
-    long long W = 0, mine, x0 = 0, x1 = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) W += __shfl_sync(0xffffffffu, costs(b0, mine), 31);
+    // All work, dealt to the CTAs in equal contiguous shares: mine is [x0, x1).
+    long long W = 0, mine, upto, x0 = 0, x1 = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) upto = costs(b0, mine), W += __shfl_sync(0xffffffffu, upto, 31);
     const int shares = (int)max(1LL, min((long long)gridDim.x, W / kLeastShare)), me = blockIdx.x;
     int4 cut0 = make_int4(0, 0, 0, 0);
     if (me < shares && W > 0) {
@@ -559,7 +607,8 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
       int b = 0, kvh = 0, m = 0, q_base = 0;
       long long before = 0;
       for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const long long upto = costs(b0, mine), all = __shfl_sync(0xffffffffu, upto, 31);
+        if (p.B > 32) upto = costs(b0, mine);   // else still those of the first look
+        const long long all = __shfl_sync(0xffffffffu, upto, 31);
         if (before + all > x0) {
           const int i = __popc(__ballot_sync(0xffffffffu, before + upto <= x0));
           b = b0 + i;
@@ -568,7 +617,7 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
         }
         before += all;
       }
-      SeqCost s = sequence(b, q_base);
+      UnitWork s = sequence(b, q_base);
       {
         const long long per = s.upto(s.M), rest = x0 - before;
         kvh = (int)(rest / per);
@@ -584,13 +633,13 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
         before += kvh * per + s.upto(m);
       }
       while (ok && before < x1) {
-        const int keys = s.keys(m), n = (keys + 127) / 128;
-        // The tile that place x of all costs lies at.
+        const int keys = s.keys(m), n = (keys + 127) / 128, per = 128 * s.a_key(m);   // per: work of a tile
+        // The tile that place x of all work lies at.
         auto tile_at = [&](long long x) {
-          const long long r = x - before - kUnitOverhead + 64;
-          return r <= 0 ? 0 : (int)min((long long)n, r >> 7);
+          const long long r = x - before - kUnitOverhead + per / 2;
+          return r <= 0 ? 0 : (int)min((long long)n, r / per);
         };
-        const long long end = before + kUnitOverhead + keys;
+        const long long end = before + kUnitOverhead + keys * (long long)(per / 128);
         const int t0 = x0 > before ? tile_at(x0) : 0, t1 = x1 >= end ? n : tile_at(x1);
         if (t1 > t0 || (n == 0 && before >= x0)) {
           const bool whole = t0 == 0 && t1 == n;
@@ -611,11 +660,11 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
           pc.slot = whole ? -1 : t0 > 0 ? 2 * me : 2 * me + 1;
           if (t0 == 0 && !whole) {
             // Parts: mine, and one of each CTA whose share begins before the place where the last tile is reached.
-            const long long place = min(end, before + kUnitOverhead + 128LL * n - 64);
+            const long long place = min(end, before + kUnitOverhead + (long long)per * n - per / 2);
             const int last = (int)((place * shares + W - 1) / W) - 1;
             cut0 = make_int4(pc.q_row, pc.kvh, pc.n_pos, last - me + 1);
           }
-          ok = publish(pc) && load(pc);
+          ok = publish(pc) && load_queries(pc);
         }
         before = end;
         if (++m == s.M) {
@@ -646,20 +695,12 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
     if (ok) {
       Piece none = {};
       publish(none);
-    } else if (!INT4) {
-      // Unwinding: let every copy still in flight land before the CTA exits.
-      auto land = [&](uint64_t* bar, uint32_t phase) {
-        const uint64_t t = global_timer_ns();
-        while (!mbar_try_wait(smem_addr(bar), phase & 1) && global_timer_ns() - t < p.timeout_ns) {}
-      };
-      for (uint32_t i = n_k > (uint32_t)NK ? n_k - NK : 0u; i < n_k; ++i) land(&bar_k_full[i % NK], i / NK);
-      for (uint32_t i = n_k > (uint32_t)NV ? n_k - NV : 0u; i < n_k; ++i) land(&bar_v_full[i % NV], i / NV);
-      if (n_q > 0) land(&bar_q_full, n_q - 1);
-      if (n_patch > 0) land(&bar_patch, n_patch - 1);
+    } else if (n_q > 0) {   // unwinding: let the copies still in flight land before the CTA exits
+      land(&bar_q_full, n_q - 1, p.timeout_ns);
     }
   } else if (warp >= C::WARP_PV && warp < C::WARP_PV + NQ) {
     // ------------------------------------------------------------------ PV issuer, one per Q tile
-    if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REGS_ROLES>();
+    setmaxnreg_dec<C::REGS_ROLES>();
     if (lane == 0) {
       const int q = warp - C::WARP_PV;
       const uint32_t d_o = tmem + C::O_COL + q * D, a_p = tmem + C::P_COL + C::P_COLS * q;
@@ -695,7 +736,7 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
     }
   } else if (warp == C::WARP_S) {
     // ------------------------------------------------------------------ S issuer
-    if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REGS_ROLES>();
+    setmaxnreg_dec<C::REGS_ROLES>();
     if (lane == 0) {
       uint32_t n_k = 0, n_q = 0, k = 0, g0 = 0, g1 = 0;   // K tiles, Q loads, S products of the CTA and of each Q tile
       bool ok = true;
@@ -710,6 +751,7 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
           if (!mbar_wait(smem_addr(&bar_k_full[ks]), (n_k / NK) & 1, ctl, SITE_KV_FULL)) { ok = false; break; }
           for (int q = 0; ok && q < NQ; ++q) {
             if (j >= (q ? pc.n1 : pc.n0)) continue;
+            uint32_t& g = q ? g1 : g0;
             const uint32_t b = k % NSB;
             if (k >= (uint32_t)NSB && !mbar_wait(smem_addr(&bar_s_free[b]), (k / NSB - 1) & 1, ctl, SITE_S_FREE)) { ok = false; break; }
             tc_fence_after();
@@ -717,7 +759,6 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
             if constexpr (INT4)
               mma_f16_ss(tmem + b * 128u, make_sdesc_plain(sQx + q * C::EXT_BYTES, 128, 256),
                          make_sdesc_plain(sKx + ks * C::EXT_BYTES, 128, 256), C::IDESC_QK | p.qk_negate, 1u);
-            uint32_t& g = q ? g1 : g0;
             tc_commit(smem_addr(&bar_s_full[q * NSB + g % NSB]));
             ++g;
             ++k;
@@ -731,19 +772,21 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(smem_addr(&bar_drain[NQ]), 0) && global_timer_ns() - t0 < p.timeout_ns) {}
     }
-  } else if (INT4 && warp >= C::WARP_UNPACK) {
-    // ------------------------------------------------------------------ 4 bits: query rows, keys and values to fp16
-    if constexpr (INT4) {
-      if constexpr (C::REG_SPLIT) {
-        if constexpr (C::REGS_UNPACK > 65536 / C::THREADS) setmaxnreg_inc<C::REGS_UNPACK>();
-        else setmaxnreg_dec<C::REGS_UNPACK>();
-      }
-      unpack_role<C>(p, tid - 32 * C::WARP_UNPACK, PG, sQ, sQx, sK, sKx, sV, &bar_q_full, &bar_q_empty, bar_k_full, bar_k_empty,
-                     bar_v_full, bar_v_empty, s_kf, s_ve, s_qf, ctl, piece_of_warp);
+  } else if (warp >= C::WARP_FEED) {
+    // ------------------------------------------------------------------ bf16: copies of keys and values. 4 bits: query rows, keys and
+    // values to fp16
+    setmaxnreg_dec<C::REGS_FEED>();
+    if constexpr (!INT4) {
+      const bool is_v = warp >= C::WARP_FEED + 2;
+      load_role<C>(p, warp & 1, is_v, is_v ? &tm_v : &tm_k, is_v ? sV : sK, is_v ? bar_v_full : bar_k_full,
+                   is_v ? bar_v_empty : bar_k_empty, &bar_patch[warp & 1], ctl, piece_of_warp);
+    } else {
+      unpack_role<C>(p, tid - 32 * C::WARP_FEED, PG, sQ, sQx, sK, sKx, sV, &bar_q_full, &bar_q_empty, bar_k_full, bar_k_empty,
+                     bar_v_full, bar_v_empty, bar_meta, s_kf, s_ve, s_qf, ctl, piece_of_warp);
     }
   } else if (warp < C::SOFTMAX_WARPS) {
     // ------------------------------------------------------------------ softmax + epilogue
-    if constexpr (C::REG_SPLIT) setmaxnreg_inc<C::REGS_SOFTMAX>();
+    setmaxnreg_inc<C::REGS_SOFTMAX>();
     const int qt = warp >> 2, r = ((warp & 3) << 5) + lane;   // Q tile; row in it == TMEM lane
     const int pos_r = (uint32_t)r / p.div_g, g_r = r - pos_r * p.G;
     const uint32_t lane_base = (uint32_t)((warp & 3) << 5) << 16;
@@ -754,6 +797,9 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
     Piece pc;
     // P is 2^kUp times larger over 4-bit caches: fp16 then loses 2^-32 of a row's greatest weight times value at most.
     constexpr float kUp = INT4 ? 7.0f : 0.0f;
+    auto s_ready = [&](uint32_t n) {   // S product number n of this tile
+      return mbar_wait(smem_addr(&bar_s_full[qt * NSB + n % NSB]), (n / NSB) & 1, ctl, SITE_S_FULL);
+    };
     for (uint32_t it = 0; ok && piece_of_warp(it, pc); ++it) {
       const int n0 = pc.n0, n1 = pc.n1, n = qt ? n1 : n0;
       const uint32_t sb = sbase, gb = g, kvb = n_kv;
@@ -767,59 +813,57 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
       float s = p.scale_log2;
       if (INT4 && n > 0) {
         // The rows' powers of two come with the query rows.
-        const bool w = mbar_wait(smem_addr(&bar_s_full[qt * NSB + gb % NSB]), (gb / NSB) & 1, ctl, SITE_S_FULL);
+        const bool w = s_ready(gb);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-        s *= s_qf[n_q % (NSB + 1) * C::ROWS + qt * 128 + r];
+        s *= s_qf[n_q % C::QFS * C::ROWS + qt * 128 + r];
       }
       n_q += n0 > 0 || n1 > 0;
       float m = -INFINITY;   // running max (log2 units), the exponents' shift
       float l = 0.0f;        // running sum of exp2(s x - m)
       for (int j = 0; j < n; ++j) {
         const uint32_t gj = gb + j;
-        bool w = mbar_wait(smem_addr(&bar_s_full[qt * NSB + gj % NSB]), (gj / NSB) & 1, ctl, SITE_S_FULL);
+        float sc[4], ve[4];   // scale of the scores and, over 4 bits, exponent of the values, of 32 keys each
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[i] = s, ve[i] = 0.f;
+        if constexpr (INT4) {
+          const uint32_t t = kvb + j, meta = t % C::METAS;
+          const bool w = mbar_wait(smem_addr(&bar_meta[meta]), (t / C::METAS) & 1, ctl, SITE_META);
+          if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+          const float4 f = s_kf[meta], e = s_ve[meta];
+          // never 0, which would make NaN of a masked score; scores that small are 0 either way
+          constexpr float kLeast = 0x1p-126f;
+          sc[0] = fmaxf(s * f.x, kLeast), sc[1] = fmaxf(s * f.y, kLeast), sc[2] = fmaxf(s * f.z, kLeast), sc[3] = fmaxf(s * f.w, kLeast);
+          ve[0] = e.x, ve[1] = e.y, ve[2] = e.z, ve[3] = e.w;
+        }
+        const bool w = s_ready(gj);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
         const int key0 = (pc.t0 + j) * 128;
         const bool masked = key0 + 128 > pc.nk || (p.causal && key0 + 127 > pc.vis + qt * p.P);
         tc_fence_after();
         const uint32_t sbuf = NSB == 1 ? 0u : s_number(sb, qt, j, n0, n1) % NSB;
         const uint32_t tS = tmem + lane_base + sbuf * 128u;
-        uint32_t sr[128];
-        float mq[4];   // maxima of 32 columns each, taken on the way: the row's of an unmasked tile
-        tmem_ld_32cols_max(tS, sr, mq[0]);
-        tmem_ld_32cols_max(tS + 32, sr + 32, mq[1]);
-        tmem_ld_32cols_max(tS + 64, sr + 64, mq[2]);
-        tmem_ld_32cols_max(tS + 96, sr + 96, mq[3]);
-        float sc[4], ve[4];   // 4 bits: scale of the scores and exponent of the values, of 32 keys each
-        if constexpr (INT4) {
-          const float4 f = s_kf[(kvb + j) % (2 * NK)], e = s_ve[(kvb + j) % (2 * NK)];
-          // never 0, which would make NaN of a masked score; scores that small are 0 either way
-          constexpr float kLeast = 0x1p-126f;
-          sc[0] = fmaxf(s * f.x, kLeast), sc[1] = fmaxf(s * f.y, kLeast), sc[2] = fmaxf(s * f.z, kLeast), sc[3] = fmaxf(s * f.w, kLeast);
-          ve[0] = e.x, ve[1] = e.y, ve[2] = e.z, ve[3] = e.w;
-        } else {
+        const int lim = seen - key0;   // keys of the tile that the row sees
+        // COLS columns of S from column c0 on and the maxima of every 32 of them, which the load takes on the way (NaN ignored);
+        // columns that the row does not see are -inf.
+        auto load_scores = [&](int c0, auto& x, float* top) {
+          constexpr int COLS = sizeof(x) / 4;
+          uint32_t* bits = reinterpret_cast<uint32_t*>(x);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[i] = s, ve[i] = 0.f;
-        }
-        tmem_ld_wait();
-        reg_fence32(sr);
-        reg_fence32(sr + 32);
-        reg_fence32(sr + 64);
-        reg_fence32(sr + 96);
-        asm volatile("" : "+f"(mq[0]), "+f"(mq[1]), "+f"(mq[2]), "+f"(mq[3]));
-        // S is in registers: its buffer may take the next.
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&bar_s_free[sbuf]));
-        float x[128];
+          for (int i = 0; i < COLS / 32; ++i) tmem_ld_32cols_max(tS + c0 + 32 * i, bits + 32 * i, top[i]);
+          tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(sr[c]);
-        if (masked) {
-          const int lim = seen - key0;
+          for (int i = 0; i < COLS / 32; ++i) {
+            reg_fence32(bits + 32 * i);
+            asm volatile("" : "+f"(top[i]));
+          }
+        };
+        auto mask_scores = [&](int c0, auto& x, float* top) {
+          constexpr int COLS = sizeof(x) / 4;
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= lim) x[c] = -INFINITY;
+          for (int c = 0; c < COLS; ++c)
+            if (c0 + c >= lim) x[c] = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < COLS / 32; ++i) {
             const float* y = x + 32 * i;
             float a[4];
 #pragma unroll
@@ -830,25 +874,29 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
               for (int k = 0; k < 4; ++k) a[k] = fmax3(a[k], y[c + k], y[c + 4 + k]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) a[c] = fmaxf(a[c], y[28 + c]);
-            mq[i] = fmaxf(fmax3(a[0], a[1], a[2]), a[3]);
+            top[i] = fmaxf(fmax3(a[0], a[1], a[2]), a[3]);
           }
-        }
-        // P = exp2(s x + ve - m) in two halves of 64 keys, handed to the PV issuer one by one. The first is computed with the
-        // row's shift so far, and again where that moves (always on the first tile).
-        auto exp_half = [&](int h, float shift, uint32_t* pk) {
+        };
+        auto scores_taken = [&]() {   // S is in registers: its buffer may take the next
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&bar_s_free[sbuf]));
+        };
+        // P = exp2(s x + ve - m) of 64 keys, in pairs; their sum without the values' powers.
+        auto exp_half = [&](const float* x, float s_lo, float s_hi, float e_lo, float e_hi, uint32_t* pk) {
           float sum = 0.f;
           if constexpr (INT4) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const int c0 = h * 64 + i * 32;
-              const float add = ve[2 * h + i] - shift + kUp;
-              const uint64_t s2 = f2_pack(sc[2 * h + i], sc[2 * h + i]), a2 = f2_pack(add, add);
+              const float e = i ? e_hi : e_lo, add = e - m + kUp, f = i ? s_hi : s_lo;
+              const uint64_t s2 = f2_pack(f, f), a2 = f2_pack(add, add);
               uint64_t acc0 = 0, acc1 = 0;
 #pragma unroll
               for (int c = 0; c < 32; c += 4) {
+                const float* y = x + 32 * i + c;
                 float t0, t1, t2, t3;
-                f2_unpack(f2_fma(f2_pack(x[c0 + c], x[c0 + c + 1]), s2, a2), t0, t1);
-                f2_unpack(f2_fma(f2_pack(x[c0 + c + 2], x[c0 + c + 3]), s2, a2), t2, t3);
+                f2_unpack(f2_fma(f2_pack(y[0], y[1]), s2, a2), t0, t1);
+                f2_unpack(f2_fma(f2_pack(y[2], y[3]), s2, a2), t2, t3);
                 const float p0 = ex2(t0), p1 = ex2(t1), p2 = ex2(t2), p3 = ex2(t3);
                 acc0 = c ? f2_add(acc0, f2_pack(p0, p1)) : f2_pack(p0, p1);
                 acc1 = c ? f2_add(acc1, f2_pack(p2, p3)) : f2_pack(p2, p3);
@@ -857,20 +905,19 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
               }
               float l0, l1;
               f2_unpack(f2_add(acc0, acc1), l0, l1);
-              sum = fmaf(l0 + l1, ex2(-ve[2 * h + i]), sum);
+              sum = fmaf(l0 + l1, ex2(-e), sum);
             }
           } else {
-            const uint64_t s2 = f2_pack(s, s), a2 = f2_pack(-shift, -shift);
+            const uint64_t s2 = f2_pack(s, s), a2 = f2_pack(-m, -m);
             uint64_t acc0 = 0, acc1 = 0;
 #pragma unroll
             for (int c = 0; c < 64; c += 4) {
-              const int cc = h * 64 + c;
               float t0, t1, t2, t3;
-              f2_unpack(f2_fma(f2_pack(x[cc], x[cc + 1]), s2, a2), t0, t1);
-              f2_unpack(f2_fma(f2_pack(x[cc + 2], x[cc + 3]), s2, a2), t2, t3);
+              f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), s2, a2), t0, t1);
+              f2_unpack(f2_fma(f2_pack(x[c + 2], x[c + 3]), s2, a2), t2, t3);
               const float p0 = ex2(t0), p1 = ex2(t1), p2 = ex2(t2), p3 = ex2(t3);
-              acc0 = f2_add(acc0, f2_pack(p0, p1));
-              acc1 = f2_add(acc1, f2_pack(p2, p3));
+              acc0 = c ? f2_add(acc0, f2_pack(p0, p1)) : f2_pack(p0, p1);
+              acc1 = c ? f2_add(acc1, f2_pack(p2, p3)) : f2_pack(p2, p3);
               pk[c >> 1] = pack_bf16x2(p0, p1);
               pk[(c >> 1) + 1] = pack_bf16x2(p2, p3);
             }
@@ -887,28 +934,23 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&bar_p_half[qt][h]));
         };
-        uint32_t pk[32];
-        float sum = exp_half(0, m, pk);
-        float m_tile;
-        if constexpr (INT4)
-          m_tile = fmaxf(fmaxf(fmaf(mq[0], sc[0], ve[0]), fmaf(mq[1], sc[1], ve[1])),
-                         fmaxf(fmaf(mq[2], sc[2], ve[2]), fmaf(mq[3], sc[3], ve[3])));
-        else
-          m_tile = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * s;
-        if (j > 0) {
-          // PV_{j-1} reads the last P, and adds to O, which a rescale changes.
-          w = mbar_wait(smem_addr(&bar_o_done[qt]), (gj - 1) & 1, ctl, SITE_O_DONE);
-          if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-        }
-        float alpha = 1.0f;
-        bool rescale = false;
-        if (m_tile > m + 8.0f) {
-          alpha = ex2(m - m_tile);   // 0 on the first tile
-          m = m_tile;
-          rescale = true;
-        }
-        if (__any_sync(0xffffffffu, rescale)) {
-          if (j > 0) {
+        // PV_{j-1} reads the last P, and adds to O, which a rescale changes.
+        bool pv_done = j == 0;
+        auto wait_pv = [&]() {
+          const bool done_ = pv_done || mbar_wait(smem_addr(&bar_o_done[qt]), (gj - 1) & 1, ctl, SITE_O_DONE);
+          pv_done = true;
+          return __all_sync(0xffffffffu, done_);
+        };
+        float alpha = 1.0f, sum = 0.f;
+        auto move_max = [&](float m_tile) {
+          bool rescale = false;
+          if (m_tile > m + 8.0f) {
+            alpha = ex2(m - m_tile);   // 0 on the first tile
+            m = m_tile;
+            rescale = true;
+          }
+          if (__any_sync(0xffffffffu, rescale) && j > 0) {
+            if (!wait_pv()) return false;
             tc_fence_after();
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
@@ -921,10 +963,24 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
               tmem_st_32cols(tO + c0, ov);
             }
           }
-          sum = exp_half(0, m, pk);
-        }
+          return true;
+        };
+        uint32_t pk[32];
+        float x[128], top[4];
+        load_scores(0, x, top);
+        scores_taken();
+        if (masked) mask_scores(0, x, top);
+        float m_tile;
+        if constexpr (INT4)
+          m_tile = fmaxf(fmaxf(fmaf(top[0], sc[0], ve[0]), fmaf(top[1], sc[1], ve[1])),
+                         fmaxf(fmaf(top[2], sc[2], ve[2]), fmaf(top[3], sc[3], ve[3])));
+        else
+          m_tile = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * s;
+        if (!move_max(m_tile)) { ok = false; break; }
+        sum = exp_half(x, sc[0], sc[1], ve[0], ve[1], pk);
+        if (!wait_pv()) { ok = false; break; }
         store_half(0, pk);
-        sum += exp_half(1, m, pk);
+        sum += exp_half(x + 64, sc[2], sc[3], ve[2], ve[3], pk);
         store_half(1, pk);
         l = l * alpha + sum;
       }
@@ -995,12 +1051,11 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
       }
       tc_fence_before();
     }
-  } else {
-    if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REGS_ROLES>();
+  } else {   // one Q tile: the second PV issuer's warp
+    setmaxnreg_dec<C::REGS_ROLES>();
   }
 
   __syncwarp();
-  griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

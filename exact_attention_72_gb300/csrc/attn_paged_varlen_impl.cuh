@@ -15,12 +15,10 @@ cudaError_t launch_paged_varlen(const PagedVarlenLaunch& a, cudaStream_t stream)
   if (a.context == 0 || set_for.load(std::memory_order_relaxed) != a.context) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    if constexpr (C::REG_SPLIT) {
-      // setmaxnreg deals out the registers that the block was launched with: refuse a launch with fewer than the split needs.
-      cudaFuncAttributes fa;
-      if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
-      if (fa.numRegs * C::THREADS < C::REGS_NEEDED) return cudaErrorInvalidConfiguration;
-    }
+    // setmaxnreg deals out the registers that the block was launched with: refuse a launch with fewer than the split needs.
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
+    if (fa.numRegs * C::THREADS < C::REGS_NEEDED) return cudaErrorInvalidConfiguration;
     set_for.store(a.context, std::memory_order_relaxed);
   }
   return launch_dependent(kernel, dim3((unsigned)a.grid), dim3(C::THREADS), (size_t)C::SMEM_BYTES, stream, a.tm_q, a.tm_k, a.tm_v,

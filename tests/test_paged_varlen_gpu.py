@@ -6,7 +6,8 @@ With P_j the weights, A = sum_j P_j |v_j|, a value may be off by (units of the v
       dS = (17 (d + 16) / 16 + 8) 2^-23 scale sum |q| |k|, 4 bits 2^-21 more for a zero's and a query sum's two fp16 numbers and
       2^-31 for what fp16 loses of small values; a weight moves by dS of itself, and so does their sum: 2 dS A;
   weights: bf16, 2^-8 of themselves; over 4 bits fp16, 2^-11, and 2^-31 of the greatest weight times value of 32 keys for each key;
-  values over 4 bits: fp16, 2^-11 of the value and 2^-38 of the greatest of 32 keys;
+  values over 4 bits: fp16, 2^-11 of the value, 2^-11 of the zero - 16 scale that it is made from, and 2^-38 of the greatest of
+      32 keys;
   sums: 64 fp32 roundings and 17 * 2^-23 for each product of 16 keys, of A;
   output: bf16, 2^-8 of the value. LSE: dS and 2^-19 (1 + |LSE|).
 """
@@ -34,7 +35,7 @@ def _built(cuda_device):
 
 def write(cache, table, lens, seed, k=None, v=None):
     """Random rows (or k, v: float32 per sequence [n, Hkv, d]) at every sequence's positions; the rest of the cache stays NaN.
-    Per sequence (keys, values, terms' sizes of the keys, 32 keys' greatest |value|) in fp64 on the GPU."""
+    Per sequence (keys, values, sizes of the keys' terms and of the values', |zero - 16 scale| of the values) in fp64 on the GPU."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     out = []
     for b, n in enumerate(lens):
@@ -48,7 +49,7 @@ def write(cache, table, lens, seed, k=None, v=None):
                 x = torch.randn(shape, generator=g, device="cuda") if given is None else given[b].cuda()
                 t[pg, at] = x.bfloat16()
                 x = t[pg, at].double()
-                got.append((x, x.abs()))
+                got.append((x, x.abs(), torch.zeros_like(x)))
                 continue
             if given is None:
                 codes = torch.randint(0, 16, shape, generator=g, device="cuda", dtype=torch.uint8)
@@ -60,15 +61,15 @@ def write(cache, table, lens, seed, k=None, v=None):
             t[pg, at] = codes[..., 0::2] | (codes[..., 1::2] << 4)
             sz[pg, at] = torch.stack((scale, zero), -1)
             s, z = (y.double().repeat_interleave(64, -1) for y in (scale, zero))
-            got.append((z + s * codes.double(), (s * (codes.double() - 8)).abs() + (z + 8 * s).abs()))
-        out.append((got[0][0], got[1][0], got[0][1], got[1][1]))
+            got.append((z + s * codes.double(), (s * (codes.double() - 8)).abs() + (z + 8 * s).abs(), (z - 16 * s).abs()))
+        out.append((got[0][0], got[1][0], got[0][1], got[1][1], got[1][2]))
     return out
 
 
 def check(q, cu, o, lse, held, scale, causal, four):
     """q, o [total, H, d], lse [H, total] against what `held` (write) says, sequence by sequence."""
     H, d = q.shape[1:]
-    for b, (keys, vals, ksize, vsize) in enumerate(held):
+    for b, (keys, vals, ksize, vsize, vbase) in enumerate(held):
         lo, hi = cu[b], cu[b + 1]
         nq, (nk, Hkv) = hi - lo, keys.shape[:2]
         if nq == 0:
@@ -96,7 +97,7 @@ def check(q, cu, o, lse, held, scale, causal, four):
             room = 2.0 ** -8 * want.abs() + (rel + 2 * dS[..., None] + (64 + 17 * (nk / 16 + 1)) * 2.0 ** -23) * A
             if four:
                 pad = torch.nn.functional.pad(vsize[:, j], (0, 0, 0, -nk % 32)).view(-1, 32, d).amax((1, 2)).repeat_interleave(32)[:nk]
-                room = room + (nk * 2.0 ** -31 * (P * pad).amax(-1) + 2.0 ** -38 * (P @ pad))[..., None]
+                room = room + (nk * 2.0 ** -31 * (P * pad).amax(-1) + 2.0 ** -38 * (P @ pad))[..., None] + 2.0 ** -11 * (P @ vbase[:, j])
             err = (got - want).abs()
             bad = (err > room) & ~none[..., None]
             assert not bad.any(), (b, j, bad.nonzero()[0].tolist(), float((err / room)[~none].max()))
