@@ -88,7 +88,7 @@ struct PagedVarlenCfg {
 };
 
 constexpr int kUnitOverhead = 6 * 128;       // work (see UnitWork) of beginning and ending a unit
-constexpr long long kLeastShare = 12 * 128;   // of a CTA: a share within a unit's beginning would have nothing to do
+constexpr long long kLeastShare = 8 * 128;   // of a CTA: a share within a unit's beginning would have nothing to do
 
 // Descriptor of an operand without swizzle: 8 x 16-byte core matrices, lbo apart along K, sbo along the rows.
 __device__ __forceinline__ uint64_t make_sdesc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {

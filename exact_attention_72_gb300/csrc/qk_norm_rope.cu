@@ -17,7 +17,8 @@
 // With several axes (time, height and width of images and video) a token has a position on each, and pair i turns by the angle
 // of column i at its axis' position: cos[pos[axis(i)], i]. The axes of the pairs are 2 bits each in the launch's parameters. A
 // lane's 4 columns come as one 16-byte load where their positions agree (one axis' block of columns, or text, whose axes
-// agree), and as 4-byte loads otherwise (axes that take turns).
+// agree), and as 4-byte loads otherwise (axes that take turns). Where every lane's columns have one axis (blocks of whole fours), a
+// kernel of its own needs only that axis' position.
 //
 // Memory bounds both. At B 2, N 8192, 32 + 8 heads, d 128 on a GB300 (share of the copy bandwidth): forward 55.8 us
 // (90%; 102 with rows unpacked at the load and a CTA per 16 tasks, 70 with rows held packed, 56.7 one value an
@@ -60,7 +61,7 @@ struct NormRopeParams {
   uint32_t* status;
   // Several axes: positions [axes, T], axis_st apart, and the axis of every pair in 2 bits.
   long long axis_st;
-  uint32_t axes, axis_of[8];       // axes: those that some pair turns by, a bit each
+  uint32_t axes, axis_of[8];       // axes: an Axis
 };
 
 // A lane's 8 values of a row: pairs of neighbours, 0 and 1 of its first chunk, 2 and 3 of its second. The arithmetic works
@@ -161,52 +162,60 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// Position of token t; -1 (nothing to store) where it lies outside the tables. AXES: of its positions some that its pairs use,
-// -1 where one of those lies outside.
-template <bool AXES>
-__device__ __forceinline__ int position(const NormRopeParams& p, int t, int l) {
-  if constexpr (AXES) {
-    int pos = 0;
-    bool good = true;
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-      if (p.axes >> a & 1) {
-        pos = p.positions[a * p.axis_st + t];
-        good = good && pos >= 0 && pos < p.max_pos;
-      }
-    if (good) return pos;
+// How a token's positions are given: one; one for each axis, of which a lane's 4 pairs need one; or up to four.
+enum Axis { kOneAxis, kAxisOfLane, kAxesOfLane };
+
+template <Axis AXES>
+struct Positions {
+  int v[AXES == kAxesOfLane ? 4 : 1];   // of this lane's pairs; v[0] = -1: nothing to store
+};
+
+// Positions of token t for a lane of its row of LPR; all -1 where one that some pair turns by lies outside the tables. mine: the axes of
+// the lane's pairs. With several axes the lanes of a row agree by a vote.
+template <Axis AXES, int LPR>
+__device__ __forceinline__ Positions<AXES> position(const NormRopeParams& p, int t, uint32_t mine, int l) {
+  Positions<AXES> r;
+  if constexpr (AXES == kOneAxis) {
+    r.v[0] = 0;
+    if (!p.cos) return r;
+    const int pos = p.positions ? p.positions[t] : t - (int)((uint32_t)t / p.div_seq) * p.seq_len;
+    if (pos >= 0 && pos < p.max_pos) {
+      r.v[0] = pos;
+      return r;
+    }
     if (l == 0) atomicCAS(p.status, 0u, kStatusBadPosition);
-    return -1;
+    r.v[0] = -1;
+  } else {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < (AXES == kAxesOfLane ? 4 : 1); ++i) {
+      r.v[i] = turns(l, p.half) ? p.positions[(mine >> (2 * i) & 3u) * p.axis_st + t] : 0;
+      bad = bad || r.v[i] < 0 || r.v[i] >= p.max_pos;
+    }
+    const uint32_t row = (LPR == 32 ? 0xffffffffu : (1u << (LPR & 31)) - 1u) << (threadIdx.x & 31) / LPR * LPR;
+    if (__ballot_sync(0xffffffffu, bad) & row) {
+      if (l == 0) atomicCAS(p.status, 0u, kStatusBadPosition);
+      r.v[0] = -1;
+    }
   }
-  if (!p.cos) return 0;
-  const int pos = p.positions ? p.positions[t] : t - (int)((uint32_t)t / p.div_seq) * p.seq_len;
-  if (pos >= 0 && pos < p.max_pos) return pos;
-  if (l == 0) atomicCAS(p.status, 0u, kStatusBadPosition);
-  return -1;
+  return r;
 }
 
-// Angles of position pos (AXES: of token t's, if pos says that they lie in the tables); back: for the turn back. mine: the axes
-// of this lane's 4 pairs.
-template <bool INTERLEAVED, bool AXES>
-__device__ __forceinline__ Angles<INTERLEAVED> load_angles(const NormRopeParams& p, int pos, int t, uint32_t mine, int l, bool back) {
+// Angles at these positions; back: for the turn back.
+template <bool INTERLEAVED, Axis AXES>
+__device__ __forceinline__ Angles<INTERLEAVED> load_angles(const NormRopeParams& p, const Positions<AXES>& pos, int l, bool back) {
   float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (turns(l, p.half) && pos >= 0) {
+  if (turns(l, p.half) && pos.v[0] >= 0) {
     bool same = true;
-    int at4[4];
-    if constexpr (AXES) {   // read before, to be checked: they are in the L1 cache
-#pragma unroll
-      for (int i = 0; i < 4; ++i) at4[i] = p.positions[(mine >> (2 * i) & 3u) * p.axis_st + t];
-      pos = at4[0];
-      same = at4[1] == pos && at4[2] == pos && at4[3] == pos;
-    }
+    if constexpr (AXES == kAxesOfLane) same = pos.v[1] == pos.v[0] && pos.v[2] == pos.v[0] && pos.v[3] == pos.v[0];
     if (same) {
-      const long long at = (long long)pos * p.half + 4 * l;
+      const long long at = (long long)pos.v[0] * p.half + 4 * l;
       c = *reinterpret_cast<const float4*>(p.cos + at), s = *reinterpret_cast<const float4*>(p.sin + at);
-    } else if constexpr (AXES) {
+    } else if constexpr (AXES == kAxesOfLane) {
       float cs[4], sn[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const long long at = (long long)at4[i] * p.half + 4 * l + i;
+        const long long at = (long long)pos.v[i] * p.half + 4 * l + i;
         cs[i] = p.cos[at], sn[i] = p.sin[at];
       }
       c = make_float4(cs[0], cs[1], cs[2], cs[3]), s = make_float4(sn[0], sn[1], sn[2], sn[3]);
@@ -245,17 +254,18 @@ __device__ __forceinline__ Chunks load_weights(const float* w, int da, int db, b
 
 // CTAs walk the tasks of all tokens, one wave of them; a thread has the rows of its next task on their
 // way while it turns those of this one, so that loads are always in flight.
-template <int D, bool NORM, bool INTERLEAVED, bool PART, bool AXES>
+template <int D, bool NORM, bool INTERLEAVED, bool PART, Axis AXES>
 __global__ void __launch_bounds__(kThreads, kFwdCtasPerSm) qk_norm_rope_kernel(const NormRopeParams p) {
   griddep_wait();
   griddep_launch_dependents();   // of the next kernel only the launch may overlap: it waits for this one's end
   constexpr int LPR = D / 8, ROWS = kThreads / LPR;
   const int l = threadIdx.x % LPR;
-  const uint32_t axes = AXES ? p.axis_of[l / 4] >> (8 * (l % 4)) : 0u;
+  const uint32_t axes = AXES != kOneAxis ? p.axis_of[l / 4] >> (8 * (l % 4)) : 0u;
   int da, db;
   chunk_dims<INTERLEAVED>(l, p.half, da, db);
   struct Task {
-    int t, h0, pos;
+    int t, h0;
+    Positions<AXES> pos;
     bool is_k;
     Raw raw[kHeads];
   };
@@ -265,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtasPerSm) qk_norm_rope_kernel(c
     const uint32_t token = id / p.parts;
     const int part = id - token * p.parts.v;
     w.t = token;
-    w.pos = position<AXES>(p, w.t, l);
+    w.pos = position<AXES, LPR>(p, w.t, axes, l);
     w.is_k = part >= p.parts_q;
     w.h0 = (w.is_k ? part - p.parts_q : part) * kHeads;
     const __nv_bfloat16* x = w.is_k ? p.k + w.t * p.k_st : p.q + w.t * p.q_st;
@@ -282,10 +292,10 @@ __global__ void __launch_bounds__(kThreads, kFwdCtasPerSm) qk_norm_rope_kernel(c
   for (uint32_t first = blockIdx.x * ROWS; first < tasks; first += stride, id += stride) {
     Task next = now;
     if (first + stride < tasks) next = load(min(id + stride, tasks - 1));
-    const Angles<INTERLEAVED> r = load_angles<INTERLEAVED, AXES>(p, now.pos, now.t, axes, l, false);
+    const Angles<INTERLEAVED> r = load_angles<INTERLEAVED, AXES>(p, now.pos, l, false);
     Chunks w;
     if (NORM) w = load_weights(now.is_k ? p.wk : p.wq, da, db, p.w_vec);
-    const int heads = now.is_k ? p.Hkv : p.H, last = id < tasks && now.pos >= 0 ? heads : 0;
+    const int heads = now.is_k ? p.Hkv : p.H, last = id < tasks && now.pos.v[0] >= 0 ? heads : 0;
     __nv_bfloat16* y = (now.is_k ? p.ok : p.oq) + ((long long)now.t * heads + now.h0) * D;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
@@ -311,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtasPerSm) qk_norm_rope_kernel(c
 // The gradient. CTAs 0 .. ctas_q - 1 walk the tasks of q, the others those of k, so a thread sums the
 // weight gradient of its 8 dims in registers; a CTA adds its rows' sums in a fixed order and leaves
 // [d] in part, which dw_kernel adds up: the same bits every time.
-template <int D, bool NORM, bool INTERLEAVED, bool PART, bool AXES>
+template <int D, bool NORM, bool INTERLEAVED, bool PART, Axis AXES>
 __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kernel(const NormRopeParams p) {
   griddep_wait();
   griddep_launch_dependents();   // of the next kernel only the launch may overlap: it waits for this one's end
@@ -323,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kern
   const FastDiv parts = is_k ? p.div_k : p.div_q;
   const float* wp = is_k ? p.wk : p.wq;
   const long long sh = is_k ? p.k_sh : p.q_sh;
-  const uint32_t axes = AXES ? p.axis_of[l / 4] >> (8 * (l % 4)) : 0u;
+  const uint32_t axes = AXES != kOneAxis ? p.axis_of[l / 4] >> (8 * (l % 4)) : 0u;
   int da, db;
   chunk_dims<INTERLEAVED>(l, p.half, da, db);
   Chunks w, dw;
@@ -331,14 +341,15 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kern
 #pragma unroll
   for (int j = 0; j < 4; ++j) dw.v[j] = twice(0.f);
   struct Task {
-    int t, h0, pos;
+    int t, h0;
+    Positions<AXES> pos;
     Raw x[kHeads], g[kHeads];
   };
   auto load = [&](uint32_t id) {
     Task w;
     w.t = id / parts;
     w.h0 = (id - w.t * parts.v) * kHeads;
-    w.pos = position<AXES>(p, w.t, l);
+    w.pos = position<AXES, LPR>(p, w.t, axes, l);
     const __nv_bfloat16* x = is_k ? p.k + w.t * p.k_st : p.q + w.t * p.q_st;
     const __nv_bfloat16* dy = (is_k ? p.dyk : p.dyq) + (long long)w.t * heads * D;
 #pragma unroll
@@ -356,8 +367,8 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSm) qk_norm_rope_bwd_kern
   for (uint32_t first = (uint32_t)cta * ROWS; first < tasks; first += stride, id += stride) {
     Task next = now;
     if (first + stride < tasks) next = load(min(id + stride, tasks - 1));
-    const Angles<INTERLEAVED> r = load_angles<INTERLEAVED, AXES>(p, now.pos, now.t, axes, l, true);
-    const int last = id < tasks && now.pos >= 0 ? heads : 0;
+    const Angles<INTERLEAVED> r = load_angles<INTERLEAVED, AXES>(p, now.pos, l, true);
+    const int last = id < tasks && now.pos.v[0] >= 0 ? heads : 0;
     __nv_bfloat16* dx = (is_k ? p.ok : p.oq) + ((long long)now.t * heads + now.h0) * D;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
@@ -433,8 +444,10 @@ template <int D, class F>
 cudaError_t with_kind(const NormRopeParams& p, bool norm, bool interleaved, F&& f) {
   const bool part = 2 * p.half != D;
   auto go = [&](auto n, auto i) {
-    if (p.axes) return part ? f(n, i, std::true_type{}, std::true_type{}) : f(n, i, std::false_type{}, std::true_type{});
-    return part ? f(n, i, std::true_type{}, std::false_type{}) : f(n, i, std::false_type{}, std::false_type{});
+    auto axes = [&](auto a) { return part ? f(n, i, std::true_type{}, a) : f(n, i, std::false_type{}, a); };
+    if (p.axes == kAxisOfLane) return axes(std::integral_constant<Axis, kAxisOfLane>{});
+    if (p.axes == kAxesOfLane) return axes(std::integral_constant<Axis, kAxesOfLane>{});
+    return axes(std::integral_constant<Axis, kOneAxis>{});
   };
   if (norm) return interleaved ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
   return interleaved ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
@@ -525,8 +538,9 @@ attn_status_t put_axes(const Axes& a, int T, const float* cos, int rope_dim, con
   p.axis_st = a.n > 1 ? a.stride : 0;
   for (int i = 0; i < rope_dim / 2; ++i) {
     if (a.of[i] >= a.n) return ATTN_ERR_INVALID_ARG;
-    p.axes |= 1u << a.of[i];
     p.axis_of[i / 16] |= (uint32_t)a.of[i] << (2 * (i % 16));
+    if (i % 4 == 0 && p.axes == kOneAxis) p.axes = kAxisOfLane;
+    if (a.of[i] != a.of[i / 4 * 4]) p.axes = kAxesOfLane;   // within the 4 pairs of a lane
   }
   return ATTN_OK;
 }
