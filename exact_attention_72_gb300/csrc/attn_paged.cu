@@ -66,6 +66,7 @@
 #include "ops.h"
 #include "paged.cuh"
 #include "paged_host.h"
+#include "paged_singles.h"
 #include "ptx.cuh"
 
 namespace gb300 {
@@ -84,9 +85,10 @@ constexpr float kHeadroom = 0x1p14f;   // weights of a bf16 cache may grow to th
 // 2^15 before the next. fp16 may lose 2^-25 of each: 2^-29 of the greatest, which is 2^4 at least.
 constexpr float kTop = 6.f, kScaledHeadroom = 0x1p15f;
 
-template <int D_, bool INT4_, int NT_, bool TWIN_ = false>
+template <int D_, bool INT4_, int NT_, bool TWIN_ = false, bool PACKED_ = false>
 struct Cfg {
   static constexpr int D = D_, NT = NT_;
+  static constexpr bool PACKED = PACKED_;                // query rows are packed (Params::cu)
   static constexpr bool INT4 = INT4_, TWIN = TWIN_;      // TWIN: columns c and c + 4 hold one query row (at most 4 rows)
   static constexpr int KT = INT4 ? 32 : 16;              // keys of a tile
   static constexpr int OVERHEAD = INT4 ? 4 : 8;          // what beginning and ending a unit costs, in tiles
@@ -114,7 +116,10 @@ struct Params {
   __nv_bfloat16* o;
   float* lse;
   const int *table, *lens;
-  long long table_stride;
+  // PACKED: [B + 1], query rows are packed, total of them, and sequence b's is row cu[b]; sequences without just one are left out
+  // (Nq == 1).
+  const int* cu;
+  long long total, table_stride;
   int B, H, G, Nq, max_pages, row_blocks, causal;
   int table_lines;   // of 32 entries, of a sequence; 0 for tables of more than a line a thread, or 1 MB
   FastDiv blocks_per_page, div_g, div_blocks;   // 16-key blocks; heads of a group; row blocks of a kv head
@@ -265,10 +270,29 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return (uint32_t)(r * ROWB + ((c ^ (r / LINE & MASK)) * 16));
 }
 
+// Whether sequence b's rows are this call's.
+template <bool PACKED>
+__device__ __forceinline__ bool is_in(const Params& p, int b) {
+  if constexpr (!PACKED) return true;
+  const int row = p.cu[b];
+  return row >= 0 && row < p.total && p.cu[b + 1] - row == 1;
+}
+
+// Row of q and o of query qi of sequence b, and where head h's LSE is.
+template <bool PACKED>
+__device__ __forceinline__ long long row_of(const Params& p, int b, int qi) {
+  return PACKED ? (long long)p.cu[b] : (long long)b * p.Nq + qi;
+}
+template <bool PACKED>
+__device__ __forceinline__ long long lse_of(const Params& p, int b, int h, int qi) {
+  return PACKED ? h * p.total + p.cu[b] : ((long long)b * p.H + h) * p.Nq + qi;
+}
+
 // Keys that some row of sequence b sees at most, and its pieces of work (at least one: a unit without
 // keys still writes its zeros).
+template <bool PACKED>
 __device__ __forceinline__ int sequence_keys(const Params& p, int b) {
-  const int n = p.lens[b];
+  const int n = is_in<PACKED>(p, b) ? p.lens[b] : 0;
   return min(max(n, 0), p.max_pages * p.c.page_size);   // a call with more than kMaxKeys is refused
 }
 
@@ -308,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
   // My share of all tiles: total and, for its beginning, the sequence it lies in.
   int mine = 0;
   const int each = (p.B + kThreads - 1) / kThreads;
-  for (int b = tid * each; b < min(p.B, (tid + 1) * each); ++b) mine += (tiles_of<C>(sequence_keys(p, b)) + OV) * per_seq;
+  for (int b = tid * each; b < min(p.B, (tid + 1) * each); ++b) mine += (tiles_of<C>(sequence_keys<C::PACKED>(p, b)) + OV) * per_seq;
   // The tables are read a little later, by single lanes one entry after the other: small ones go into L2 meanwhile.
   const int line = blockIdx.x * kThreads + tid;
   if (line < p.B * p.table_lines) {
@@ -390,20 +414,20 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
       f_unit = false;
       const int at = cur.at, last = cur.last;
       if (at >= last) return;
-      int seq = cur.seq, seq_base = cur.seq_base, keys = sequence_keys(p, seq), nt = tiles_of<C>(keys);
+      int seq = cur.seq, seq_base = cur.seq_base, keys = sequence_keys<C::PACKED>(p, seq), nt = tiles_of<C>(keys);
       while (seq + 1 < p.B && at >= seq_base + (nt + OV) * per_seq) {
         seq_base += (nt + OV) * per_seq;
         ++seq;
-        keys = sequence_keys(p, seq);
+        keys = sequence_keys<C::PACKED>(p, seq);
         nt = tiles_of<C>(keys);
       }
-      if (p.lens[seq] != keys && lane == 0) atomicCAS(p.status, 0u, kStatusBadPage);
+      if (p.lens[seq] != keys && is_in<C::PACKED>(p, seq) && lane == 0) atomicCAS(p.status, 0u, kStatusBadPage);
       const int unit = (at - seq_base) / (nt + OV), base = seq_base + unit * (nt + OV) + OV;   // its first tile
       const int t0 = max(at - base, 0), t1 = min(nt, last - base), hkv = (uint32_t)unit / p.div_blocks;
       __syncwarp();
       if (lane == 0) {
         cur.at = base + nt, cur.seq = seq, cur.seq_base = seq_base, cur.b = seq, cur.hkv = hkv;
-        cur.row0 = (unit - hkv * p.row_blocks) * C::ROWS, cur.q_row = (long long)seq * p.Nq * p.H + hkv * p.G;
+        cur.row0 = (unit - hkv * p.row_blocks) * C::ROWS, cur.q_row = is_in<C::PACKED>(p, seq) ? row_of<C::PACKED>(p, seq, 0) * p.H + hkv * p.G : -1;
         s_units[warp][f_turn & 3] = Unit{seq, unit, t0, t1, nt, keys, base + nt};
       }
       __syncwarp();
@@ -421,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
           for (int i = 0; i < 8 / QRPI; ++i) {
             const int r = i * QRPI + lane / QCH;
             const uint32_t row = cur.row0 + f_q * 8 + (C::TWIN ? r & 3 : r), qi = row / p.div_g;
-            const bool in = row < (uint32_t)(p.Nq * p.G);
+            const bool in = row < (uint32_t)(p.Nq * p.G) && (!C::PACKED || cur.q_row >= 0);
             const long long from = in ? cur.q_row + (long long)qi * p.H + (row - qi * p.G) : 0;
             copy16<0>(fill + chunk_at<2 * D>(r, lane % QCH), p.q + from * D + lane % QCH * 8, in);
           }
@@ -580,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
         leave();
       }
       const volatile Unit& unit = s_units[warp][turn & 3];
-      const int keys = unit.keys, t1 = unit.t1, rows = p.Nq * p.G;
+      const int keys = unit.keys, t1 = unit.t1, rows = is_in<C::PACKED>(p, unit.b) ? p.Nq * p.G : 0;
       const int row0 = row_block(p, unit.unit) * C::ROWS;
       int limit[NT][2], least = INT_MAX;   // the column's row sees keys < limit
 #pragma unroll
@@ -936,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
               if (g == 0) p.part_lse[2 * me * C::ROWS + c] = lse2;
             } else if (row < rows) {
               const int qi = (uint32_t)row / p.div_g, h = (uint32_t)unit.unit / p.div_blocks * p.G + row - qi * p.G;
-              __nv_bfloat16* to = p.o + (((long long)unit.b * p.Nq + qi) * p.H + h) * D;
+              __nv_bfloat16* to = p.o + (row_of<C::PACKED>(p, unit.b, qi) * p.H + h) * D;
               if constexpr (INT4) {
 #pragma unroll
                 for (int i = 0; i < D / 16; i += 2) {
@@ -951,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
                   to[dim(i)] = __float2bfloat16_rn(x.x * inv), to[dim(i) + 8] = __float2bfloat16_rn(x.y * inv);
                 }
               }
-              if (g == 0) p.lse[((long long)unit.b * p.H + h) * p.Nq + qi] = lse2 * 0.69314718055994531f;
+              if (g == 0) p.lse[lse_of<C::PACKED>(p, unit.b, h, qi)] = lse2 * 0.69314718055994531f;
             }
           }
       } else {   // my share ends in this unit: joined with the CTA's other warps in it, below
@@ -993,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
     while (w1 < kWarps && s_id[w1] == s_id[w0]) ++w1;
     if (s_id[w0] >= 0) {
       const Unit unit = s_units[w0][0];
-      const int first = blockIdx.x * kWarps + w0, rows = p.Nq * p.G, row0 = row_block(p, unit.unit) * C::ROWS;
+      const int first = blockIdx.x * kWarps + w0, rows = is_in<C::PACKED>(p, unit.b) ? p.Nq * p.G : 0, row0 = row_block(p, unit.unit) * C::ROWS;
       const bool head = s_open[w0] & 1, whole = head && (s_open[w1 - 1] & 2);
 #pragma unroll
       for (int n = 0; n < C::ROWS * (D / 4) / kThreads; ++n) {
@@ -1019,9 +1043,9 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
           if (c == 0) p.part_lse[to] = lse2;
         } else if (row < rows) {
           const int qi = (uint32_t)row / p.div_g, h = (uint32_t)unit.unit / p.div_blocks * p.G + row - qi * p.G;
-          *reinterpret_cast<uint2*>(p.o + (((long long)unit.b * p.Nq + qi) * p.H + h) * D + c) =
+          *reinterpret_cast<uint2*>(p.o + (row_of<C::PACKED>(p, unit.b, qi) * p.H + h) * D + c) =
               make_uint2(pack_bf162(x.x, x.y), pack_bf162(x.z, x.w));
-          if (c == 0) p.lse[((long long)unit.b * p.H + h) * p.Nq + qi] = lse2 * 0.69314718055994531f;
+          if (c == 0) p.lse[lse_of<C::PACKED>(p, unit.b, h, qi)] = lse2 * 0.69314718055994531f;
         }
       }
       if (head && !whole && tid == 0) {
@@ -1042,7 +1066,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) attn_paged_kernel(const Par
 constexpr int kFewParts = 8;
 constexpr int kManyWarps = 16;   // of a CTA when units have many parts
 
-template <int D, int WARPS>
+template <int D, int WARPS, bool PACKED>
 __global__ void __launch_bounds__(32 * WARPS) attn_paged_join_kernel(const Params p, int rows_per_unit, int span, int records) {
   griddep_wait();
   const bool alone = WARPS == kWarps && span == kWarps;   // a record a warp
@@ -1104,11 +1128,11 @@ __global__ void __launch_bounds__(32 * WARPS) attn_paged_join_kernel(const Param
     if (way == 0) {
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        *reinterpret_cast<uint2*>(p.o + (((long long)cut.x * p.Nq + qi) * p.H + h) * D + v * 128 + c) =
+        *reinterpret_cast<uint2*>(p.o + (row_of<PACKED>(p, cut.x, qi) * p.H + h) * D + v * 128 + c) =
             make_uint2(pack_bf162(s.x[v].x * inv, s.x[v].y * inv), pack_bf162(s.x[v].z * inv, s.x[v].w * inv));
     }
     if (lane == 0)
-      p.lse[((long long)cut.x * p.H + h) * p.Nq + qi] = s.sum != 0.f ? (s.top + log2f(s.sum)) * 0.69314718055994531f : -INFINITY;
+      p.lse[lse_of<PACKED>(p, cut.x, h, qi)] = s.sum != 0.f ? (s.top + log2f(s.sum)) * 0.69314718055994531f : -INFINITY;
   };
   // A few parts: everything is loaded at once.
   auto gather_few = [&](const Cut& cut) {
@@ -1234,26 +1258,27 @@ cudaError_t launch(const Params& p, int grid, unsigned long long context, cudaSt
   // 32 parts a unit and more: 16 warps (one sequence of 60871 keys, d 256 in bf16, one kv head: 25.5 us, with 4 warps 32.4;
   // at 16 parts, B 28 of up to 1166 keys, 17 against 10.4).
   const bool many = grid >= 32 * units;
-  auto join = many ? attn_paged_join_kernel<C::D, kManyWarps> : attn_paged_join_kernel<C::D, kWarps>;
+  auto join = many ? attn_paged_join_kernel<C::D, kManyWarps, C::PACKED> : attn_paged_join_kernel<C::D, kWarps, C::PACKED>;
   return launch_dependent(join, dim3((unsigned)((records + span - 1) / span), (unsigned)std::min(C::ROWS, p.Nq * p.G)),
                           dim3(many ? 32 * kManyWarps : kThreads), 0, s, p, (int)C::ROWS, span, records);
 }
 
-template <int D, bool INT4>
+template <int D, bool INT4, bool PACKED>
 cudaError_t launch_rows(const Params& p, int rows_per_unit, int grid, unsigned long long context, cudaStream_t s) {
   if constexpr (D <= 128) {
-    if (rows_per_unit == 16) return launch<Cfg<D, INT4, 2>>(p, grid, context, s);
+    if (rows_per_unit == 16) return launch<Cfg<D, INT4, 2, false, PACKED>>(p, grid, context, s);
   }
   if constexpr (INT4) {
-    if (p.Nq * p.G <= 4) return launch<Cfg<D, true, 1, true>>(p, grid, context, s);
+    if (p.Nq * p.G <= 4) return launch<Cfg<D, true, 1, true, PACKED>>(p, grid, context, s);
   }
-  return launch<Cfg<D, INT4, 1>>(p, grid, context, s);
+  return launch<Cfg<D, INT4, 1, false, PACKED>>(p, grid, context, s);
 }
 
 template <int D>
 cudaError_t launch_dim(const Params& p, bool bits4, int rows_per_unit, int grid, unsigned long long context, cudaStream_t s) {
-  return bits4 ? launch_rows<D, true>(p, rows_per_unit, grid, context, s)
-               : launch_rows<D, false>(p, rows_per_unit, grid, context, s);
+  if (p.cu) return launch_rows<D, true, true>(p, rows_per_unit, grid, context, s);   // 4 bits only
+  return bits4 ? launch_rows<D, true, false>(p, rows_per_unit, grid, context, s)
+               : launch_rows<D, false, false>(p, rows_per_unit, grid, context, s);
 }
 
 size_t pad(size_t x) { return (x + 255) / 256 * 256; }
@@ -1264,6 +1289,31 @@ void workspace_parts(const Plan& pl, int d, size_t (&n)[3]) {
   n[0] = pad(2 * warps * pl.rows_per_unit * d * 4);
   n[1] = pad(2 * warps * pl.rows_per_unit * 4);
   n[2] = pad(warps * sizeof(int4));
+}
+
+// What follows from p's sizes, and the parts of the workspace.
+void put_sizes(Params& p, const Plan& pl, void* workspace, const size_t (&n)[3]) {
+  p.row_blocks = pl.row_blocks;
+  p.blocks_per_page = fast_div((uint32_t)p.c.page_size / 16);
+  p.div_g = fast_div((uint32_t)p.G), p.div_blocks = fast_div((uint32_t)pl.row_blocks);
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + n[0]);
+  p.cut = reinterpret_cast<::int4*>(static_cast<uint8_t*>(workspace) + n[0] + n[1]);
+}
+
+// Launches the call that p describes but for its grid.
+attn_status_t run(Params& p, const Plan& pl, int d, bool bits4, unsigned long long context, cudaStream_t stream) {
+  // No more warps than tiles there can be; tiles are counted in 32 bits.
+  const long long most = (long long)p.B * p.c.Hkv * pl.row_blocks *
+                         (((long long)p.max_pages * p.c.page_size - 1) / pl.tile + 1 + pl.overhead);
+  if (most > INT_MAX) return ATTN_ERR_UNSUPPORTED;
+  const int grid = (int)std::min<long long>(pl.grid, (most + kWarps - 1) / kWarps);
+  const long long lines = (p.max_pages + 31LL) / 32;
+  p.table_lines = lines * p.B <= std::min(8192, grid * kThreads) ? (int)lines : 0;
+  const cudaError_t e = d == 64    ? launch_dim<64>(p, bits4, pl.rows_per_unit, grid, context, stream)
+                        : d == 128 ? launch_dim<128>(p, bits4, pl.rows_per_unit, grid, context, stream)
+                                   : launch_dim<256>(p, bits4, pl.rows_per_unit, grid, context, stream);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 bool shape_ok(int B, int H, int Hkv, int Nq) { return B >= 1 && H >= 1 && Hkv >= 1 && Nq >= 1 && H % Hkv == 0; }
@@ -1327,23 +1377,32 @@ extern "C" attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t*
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   p.table = page_table, p.table_stride = table_stride, p.lens = seqlens;
-  p.B = B, p.H = H, p.G = H / Hkv, p.Nq = Nq, p.max_pages = max_pages, p.row_blocks = pl.row_blocks;
+  p.B = B, p.H = H, p.G = H / Hkv, p.Nq = Nq, p.max_pages = max_pages;
   p.causal = causal != 0;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.blocks_per_page = fast_div((uint32_t)cache->page_size / 16);
-  p.div_g = fast_div((uint32_t)p.G), p.div_blocks = fast_div((uint32_t)pl.row_blocks);
-  p.part_o = static_cast<float*>(workspace);
-  p.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + n[0]);
-  p.cut = reinterpret_cast<::int4*>(static_cast<uint8_t*>(workspace) + n[0] + n[1]);
-  // No more warps than tiles there can be; tiles are counted in 32 bits.
-  const long long most = (long long)B * Hkv * pl.row_blocks *
-                         (((long long)max_pages * cache->page_size - 1) / pl.tile + 1 + pl.overhead);
-  if (most > INT_MAX) return ATTN_ERR_UNSUPPORTED;
-  const int grid = (int)std::min<long long>(pl.grid, (most + kWarps - 1) / kWarps);
-  const long long lines = (max_pages + 31LL) / 32;
-  p.table_lines = lines * B <= std::min(8192, grid * kThreads) ? (int)lines : 0;
-  const cudaError_t e = d == 64    ? launch_dim<64>(p, bits4, pl.rows_per_unit, grid, context, stream)
-                        : d == 128 ? launch_dim<128>(p, bits4, pl.rows_per_unit, grid, context, stream)
-                                   : launch_dim<256>(p, bits4, pl.rows_per_unit, grid, context, stream);
-  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  put_sizes(p, pl, workspace, n);
+  return run(p, pl, d, bits4, context, stream);
+}
+
+// The sequences of one query token of a packed batch over a 4-bit cache (attn_paged_varlen.cu): what attn_fwd_paged does with them.
+attn_status_t gb300::launch_paged_singles(const PagedSingles& a, cudaStream_t stream) {
+  Params p = {};
+  p.c = a.c;
+  p.q = a.q, p.o = a.o, p.lse = a.lse;
+  p.table = a.table, p.lens = a.lens, p.cu = a.cu;
+  p.total = a.total, p.table_stride = a.table_stride;
+  p.B = a.B, p.H = a.H, p.G = a.H / a.c.Hkv, p.Nq = 1, p.max_pages = a.max_pages;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.status = a.status;
+  const Plan pl = make_plan(a.d, true, p.G, a.sms);
+  size_t n[3];
+  workspace_parts(pl, a.d, n);
+  put_sizes(p, pl, a.workspace, n);
+  return run(p, pl, a.d, true, a.context, stream);
+}
+
+size_t gb300::paged_singles_workspace_bytes(int G, int d, int sms) {
+  size_t n[3];
+  workspace_parts(make_plan(d, true, G, sms), d, n);
+  return n[0] + n[1] + n[2];
 }

@@ -7,6 +7,7 @@
 #include "attn.h"
 #include "attn_paged_varlen.h"
 #include "paged_host.h"
+#include "paged_singles.h"
 
 namespace gb300 {
 namespace {
@@ -73,6 +74,12 @@ cudaError_t launch(const PagedVarlenLaunch& a, cudaStream_t s) {
                           0, s, a.params);
 }
 
+// Over 4-bit caches a chunk's kernel unpacks every key for its tensor cores, 2.7 us a tile of 128 whatever its rows, where the
+// kernel of attn_fwd_paged multiplies the codes as they are. It takes sequences of one token (of at most kSinglesRows rows a kv
+// head, which read the cache once) in batches of kSinglesBatch and more; in smaller ones its two launches, 4 us if there is no such
+// sequence, may cost more than they save. B 30, up to 16384 keys, H 32, Hkv 8, d 128: 413 us unpacked, 97 so.
+constexpr int kSinglesRows = 16, kSinglesBatch = 8;
+
 int unit_rows(int d) { return d <= 128 ? 256 : 128; }
 size_t pad(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -81,6 +88,14 @@ void workspace_parts(int sms, int d, size_t (&n)[3]) {
   n[0] = pad((size_t)2 * sms * unit_rows(d) * d * 4);
   n[1] = pad((size_t)2 * sms * unit_rows(d) * 4);
   n[2] = pad((size_t)sms * sizeof(int4));
+}
+
+// Bytes of a call's workspace: the kernels that share it run one after the other.
+size_t workspace_need(int sms, int d, int G, attn_cache_type_t type) {
+  size_t n[3];
+  workspace_parts(sms, d, n);
+  const size_t parts = n[0] + n[1] + n[2];
+  return type == ATTN_CACHE_INT4 ? std::max(parts, paged_singles_workspace_bytes(std::min(G, kSinglesRows), d, sms)) : parts;
 }
 
 // bf16 cache -> 4-D map (d, token of a page, kv head, page), box 64 columns of `rows` tokens. The stride of a single page,
@@ -103,9 +118,7 @@ extern "C" size_t attn_fwd_paged_varlen_workspace_bytes(int B, int H, int Hkv, i
   int sms = 152;
   uint32_t* status;
   device_state(&sms, &status);
-  size_t n[3];
-  workspace_parts(sms, d, n);
-  return n[0] + n[1] + n[2];
+  return workspace_need(sms, d, H / Hkv, type);
 }
 
 extern "C" attn_status_t attn_fwd_paged_varlen(const void* q, const attn_paged_cache_t* cache, void* o, float* lse,
@@ -135,11 +148,12 @@ extern "C" attn_status_t attn_fwd_paged_varlen(const void* q, const attn_paged_c
   if (!device_state(&a.grid, &p.status, &a.context)) return ATTN_ERR_CUDA;
   size_t n[3];
   workspace_parts(a.grid, d, n);
-  if (workspace_bytes < n[0] + n[1] + n[2]) return ATTN_ERR_INVALID_ARG;
+  const size_t need = workspace_need(a.grid, d, G, cache->type);
+  if (workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
   struct {
     const void* b;
     size_t n;
-  } x[4] = {{o, (size_t)total_q * H * d * 2}, {lse, (size_t)total_q * H * 4}, {workspace, n[0] + n[1] + n[2]}, {q, (size_t)total_q * H * d * 2}};
+  } x[4] = {{o, (size_t)total_q * H * d * 2}, {lse, (size_t)total_q * H * 4}, {workspace, need}, {q, (size_t)total_q * H * d * 2}};
   for (int i = 0; i < 3; ++i)
     for (int j = i + 1; j < 4; ++j) {
       const uintptr_t u = (uintptr_t)x[i].b, v = (uintptr_t)x[j].b;
@@ -162,8 +176,11 @@ extern "C" attn_status_t attn_fwd_paged_varlen(const void* q, const attn_paged_c
   p.debug_skip_load = debug_skip_load();
   p.box_rows = 16;
   while (p.box_rows < 128 && cache->page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
-  a.grid = (int)std::clamp<double>(most / kLeastShare, 1., a.grid);
   const bool int4 = cache->type == ATTN_CACHE_INT4;
+  // (that kernel counts its tiles of 32 keys, and 4 more, of at most two blocks of rows, in 32 bits)
+  p.skip_singles = int4 && B >= kSinglesBatch && G <= kSinglesRows && 2LL * B * Hkv * (keys / 32 + 5) <= INT_MAX;
+  const int sms = a.grid;
+  a.grid = (int)std::clamp<double>(most / kLeastShare, 1., a.grid);
   if (!int4) {
     const uint64_t dims[4] = {(uint64_t)d, (uint64_t)G, (uint64_t)total_q, (uint64_t)Hkv};
     const uint64_t strides[3] = {(uint64_t)2 * d, (uint64_t)2 * H * d, (uint64_t)2 * G * d};
@@ -178,5 +195,9 @@ extern "C" attn_status_t attn_fwd_paged_varlen(const void* q, const attn_paged_c
     case 128: e = int4 ? launch<128, true>(a, stream) : launch<128, false>(a, stream); break;
     default: e = int4 ? launch<256, true>(a, stream) : launch<256, false>(a, stream); break;
   }
-  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  if (e != cudaSuccess) return ATTN_ERR_CUDA;
+  if (!p.skip_singles) return ATTN_OK;
+  return launch_paged_singles({p.c, p.q, p.o, lse, page_table, seqlens, cu_seqlens_q, total_q, table_stride, B, H, d, max_pages, sms,
+                               scale, workspace, p.status, a.context},
+                              stream);
 }

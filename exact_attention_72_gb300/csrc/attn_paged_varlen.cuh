@@ -20,6 +20,7 @@ struct PagedVarlenParams {
   long long table_stride;
   int B, H, G, P;           // G query heads a kv head, P = 128 / G positions a Q tile
   int total_q, max_pages, box_rows, causal;
+  int skip_singles;         // sequences of one query are another kernel's
   FastDiv div_g, div_page;  // by G and by the page size
   float scale_log2;         // |scale| log2(e)
   uint32_t qk_negate;       // as AttnParams
@@ -578,7 +579,7 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
         const int nk = min(max(n, 0), p.max_pages * p.c.page_size);   // the host refuses tables of more
         const bool good = c0 >= 0 && c1 >= c0 && c1 <= p.total_q;
         if (!good || nk != n) atomicCAS(p.status, 0u, kStatusBadPage);
-        if (good) q_base = c0, s.nq = c1 - c0, s.nk = nk, s.M = (s.nq + RP - 1) / RP;
+        if (good && !(p.skip_singles && c1 - c0 == 1)) q_base = c0, s.nq = c1 - c0, s.nk = nk, s.M = (s.nq + RP - 1) / RP;
       }
       return s;
     };

@@ -537,14 +537,15 @@ attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t* cache, voi
  *   causal: query i of n sees keys j <= i + seqlens[b] - n (bottom-right aligned, as attn_fwd_varlen); otherwise all.
  *      Rows that see no key get O = 0, LSE = -inf.
  *   scale as in attn_fwd (finite, nonzero).
- *   workspace: DEVICE, 256-byte aligned, at least attn_fwd_paged_varlen_workspace_bytes(...) bytes (which depend on d and
- *      the device alone); needs no initialisation. Calls that may overlap on the GPU (captured graphs included) need one
+ *   workspace: DEVICE, 256-byte aligned, at least attn_fwd_paged_varlen_workspace_bytes(...) bytes, which do not depend on
+ *      the lengths; needs no initialisation. Calls that may overlap on the GPU (captured graphs included) need one
  *      each. q, o, lse and workspace must not overlap each other or the cache.
  * Offsets and lengths stay on the device: the call can be captured and replayed with others. A sequence whose offsets do
  * not ascend or pass total_q has no rows; pages and lengths out of range as above; each is reported by attn_get_status.
  * Over 4-bit caches q, keys and values are held in fp16 times powers of two (of a query row; of 32 neighbouring keys):
- * below 2^-21 of a row's, or 2^-29 of 32 keys', greatest value they lose bits. Deterministic. Two programmatic dependent
- * launches; allocates nothing; total_q == 0 returns ATTN_OK at once.
+ * below 2^-21 of a row's, or 2^-29 of 32 keys', greatest value they lose bits. Sequences of one token in a
+ * batch of 8 and more go to attn_fwd_paged's kernel there (H / Hkv <= 16). Deterministic. Two programmatic dependent launches, four
+ * with those; allocates nothing; total_q == 0 returns ATTN_OK at once.
  * UNSUPPORTED as for the cache, for scale == 0, H / Hkv > 128, total_q or max_pages * page_size >= 2^31 - 1023, strides
  * of a bf16 cache that tensor maps do not take (2^40 bytes and more, or 0 between two rows), and for more than 2^52 / Hkv
  * keys over all blocks of queries.

@@ -139,6 +139,10 @@ CASES = [
     (128, 96, 1, 16, [3, 1], [200, 50]),                         # one position a tile
     (128, 8, 2, 16, [1] * 40, list(range(0, 1200, 30))),         # decoding
     (64, 128, 1, 16, [2], [300]),
+    (128, 8, 2, 16, [1, 0, 33, 1, 1, 70, 0, 1, 1], [500, 3, 40, -1, 0, 300, 0, 3000, 31]),     # single tokens among chunks, one without keys
+    (64, 24, 2, 32, [1, 1, 5, 1, 1, 1, 1, 2], [9, 2000, 40, 64, 0, 31, 32, 7]),
+    (256, 32, 2, 16, [1, 1, 1, 1, 9, 1, 1, 1], [9, 700, 40, 64, 0, 31, 32, 7]),                # sixteen heads: two blocks of rows
+    (128, 34, 2, 16, [1] * 8 + [3], [100] * 9),                                                # seventeen: not theirs
 ]
 
 
@@ -320,6 +324,40 @@ def test_bad_pages_lengths_and_offsets(kind):
     out, lse, st, detail = run(table, cu, [200, -3, 90])
     assert st == binding.ATTN_ERR_INVALID_ARG
     check(q, cu, out, lse, [held[0], tuple(x[:0] for x in held[1]), held[2]], d ** -0.5, True, kind == "int4")
+
+
+def test_bad_singles():
+    """Single tokens of a larger batch over 4 bits: bad pages count as zeros, unsound offsets leave rows, others are as before."""
+    d, lens = 128, [200, 150, 90, 40, 64, 1, 17, 300, 0]
+    table, pages = make_table(lens, 16, 1)
+    cache = make_cache("int4", pages, 16, 2, d)
+    held = write(cache, table, lens, 4)
+    q = randn((9, 4, d), 5)
+
+    def run(table, cu):
+        out, lse = torch.full_like(q, 7.0), torch.full((4, 9), 7.0, device="cuda")
+        binding.attn_fwd_paged_varlen(q, cache, i32(table), i32(cu), i32(lens), out=out, lse=lse)
+        st, detail = binding.attn_get_status()
+        binding.attn_clear_status()
+        return out, lse, st, detail
+
+    cu = list(range(10))
+    out, lse, st, _ = run(table, cu)
+    assert st == binding.ATTN_OK
+    check(q, cu, out, lse, held, d ** -0.5, True, True)
+    bad = table.copy()
+    bad[1, 2], bad[1, 5] = pages, -1
+    got, gotl, st, detail = run(bad, cu)
+    assert st == binding.ATTN_ERR_INVALID_ARG and detail == 0x2000000D
+    keep = [0, 2, 3, 4, 5, 6, 7, 8]
+    assert torch.equal(got[keep], out[keep]) and torch.equal(gotl[:, keep], lse[:, keep])
+    for x in held[1]:
+        x[32:48], x[80:96] = 0, 0
+    check(q, cu, got, gotl, held, d ** -0.5, True, True)
+    got, gotl, st, detail = run(table, [0, 1, 2, 3, 4, 5, 6, 7, 10, 11])     # the last two sequences pass the rows
+    assert st == binding.ATTN_ERR_INVALID_ARG and detail == 0x2000000D
+    check(q, cu, got, gotl, write(cache, table, lens, 4)[:7], d ** -0.5, True, True)
+    assert (got[7:] == 7).all() and (gotl[:, 7:] == 7).all()
 
 
 def test_a_missing_copy_is_reported():
