@@ -75,7 +75,7 @@ struct PagedVarlenCfg {
   static constexpr int WARP_FEED = WARP_PV + 4, THREADS = 32 * (WARP_FEED + 4);
   // Registers, of the launch's 512 x 128 (one Q tile: 384 x 168).
   static constexpr uint32_t REGS_SOFTMAX = INT4 && NQ == 2 ? 184 : 200;
-  static constexpr uint32_t REGS_ROLES = NQ == 1 ? 64 : INT4 ? 48 : 56, REGS_FEED = NQ == 1 ? 120 : INT4 ? 96 : 56;
+  static constexpr uint32_t REGS_ROLES = NQ == 1 ? 64 : 56, REGS_FEED = NQ == 1 ? 120 : INT4 ? 88 : 56;
   static constexpr int REGS_NEEDED = SOFTMAX_WARPS * 32 * REGS_SOFTMAX + 128 * REGS_ROLES + 128 * REGS_FEED;
   static constexpr int FEEDERS = INT4 ? 4 : 2;            // warps that fill a stage
   // Work of a key in a unit of one Q tile and of two. bf16: a tile of a decoding sequence takes 1.15 us, of a chunk 1.7. 4 bits:
@@ -263,7 +263,8 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int r, i
   for (uint32_t it = 0; piece_of_warp(it, pc); ++it) {
     const int n = max(pc.n0, pc.n1), nk = pc.nk, t0 = pc.t0;
     if (n == 0) continue;
-    // My key's page in the page table, and where its codes and pairs begin (codes -1: nowhere).
+    // My key's page in the page table, and where its codes and pairs begin. A key behind the last, or without a page, has scale and
+    // zero 0 and any codes.
     const int* table = p.table + pc.b * p.table_stride;
     const long long head = pc.kvh * p.c.head_b, sz_head = pc.kvh * p.c.sz_head_b;
     auto look_up = [&](int t) {
@@ -282,10 +283,10 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int r, i
         x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
       }
     };
-    long long at = -1;
+    long long at = 0;
     auto locate = [&](int t, int page) {
       const int key = t * 128 + r;
-      at = -1;
+      at = 0;
 #pragma unroll
       for (int g = 0; g < GROUPS; ++g) ksz[g] = vsz[g] = 0u;
       if (key >= nk) return;
@@ -305,7 +306,7 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int r, i
       const uint8_t* from = (is_v ? p.c.v : p.c.k) + row + half * (WORDS * 4);
 #pragma unroll
       for (int i = 0; i < WORDS / 4; ++i) {
-        const uint4 u = row < 0 ? make_uint4(0u, 0u, 0u, 0u) : load_ahead(from + i * 16);
+        const uint4 u = load_ahead(from + i * 16);
         x[4 * i] = u.x, x[4 * i + 1] = u.y, x[4 * i + 2] = u.z, x[4 * i + 3] = u.w;
       }
     };
@@ -407,7 +408,7 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int r, i
       }
       // Not unrolled over steps: the roles' code would not stay in the instruction caches (unrolled over a tile, 0.8 warps a
       // scheduler waited for instructions at any time).
-#pragma unroll
+#pragma unroll 1
       for (int step = 0; step < 2 * HALVES; ++step) {
         const bool is_v = step >= HALVES;
         const int half = HALVES == 1 ? 0 : step % HALVES;
@@ -423,12 +424,12 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int r, i
           const uint32_t pair = is_v ? vv : kk;
           s2[g] = __byte_perm(pair, 0, 0x1010), z2[g] = __byte_perm(pair, 0, 0x3232);
         }
-        const uint32_t to = (is_v ? sV + vs * C::TILE_BYTES : sK + ks * C::TILE_BYTES) + row_at + half * (2 * C::CHUNK_BYTES);
+        const uint32_t to = ((is_v ? sV + vs * C::TILE_BYTES : sK + ks * C::TILE_BYTES) + row_at + half * (2 * C::CHUNK_BYTES)) | swz << 4;
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) {
           // Codes m and m + 4 in the high bits of fp16's mantissa, 1 + code / 16.
           const uint32_t x = now[i], mask = 0x03c003c0u, one = 0x3c003c00u, s = s2[i / 8], z = z2[i / 8];
-          sts128(to + i / 8 * C::CHUNK_BYTES + ((i % 8 ^ swz) << 4),
+          sts128((to ^ i % 8 << 4) + i / 8 * C::CHUNK_BYTES,
                  make_uint4(half2_fma((x << 6 & mask) | one, s, z), half2_fma((x << 2 & mask) | one, s, z),
                             half2_fma((x >> 2 & mask) | one, s, z), half2_fma((x >> 6 & mask) | one, s, z)));
         }
@@ -522,14 +523,20 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
     mbar_arrive(smem_addr(&bar_piece_empty[i]));
     return pc.work != 0;
   };
-  auto piece_of_warp = [&](uint32_t it, Piece& pc) {
+  auto wait_piece = [&](uint32_t it) {
     const uint32_t i = it % C::PIECES;
     const bool w = mbar_wait(smem_addr(&bar_piece_full[i]), (it / C::PIECES) & 1, ctl, SITE_PIECE_FULL);
-    if (!__all_sync(0xffffffffu, w)) return false;
-    pc = s_pieces[i];
+    return __all_sync(0xffffffffu, w) && s_pieces[i].work != 0;
+  };
+  auto release_piece = [&](uint32_t it) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_addr(&bar_piece_empty[i]));
-    return pc.work != 0;
+    if (lane == 0) mbar_arrive(smem_addr(&bar_piece_empty[it % C::PIECES]));
+  };
+  auto piece_of_warp = [&](uint32_t it, Piece& pc) {
+    if (!wait_piece(it)) return false;
+    pc = s_pieces[it % C::PIECES];
+    release_piece(it);
+    return true;
   };
 
   if (warp == C::WARP_PLAN) {
@@ -789,28 +796,25 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
     // ------------------------------------------------------------------ softmax + epilogue
     setmaxnreg_inc<C::REGS_SOFTMAX>();
     const int qt = warp >> 2, r = ((warp & 3) << 5) + lane;   // Q tile; row in it == TMEM lane
-    const int pos_r = (uint32_t)r / p.div_g, g_r = r - pos_r * p.G;
     const uint32_t lane_base = (uint32_t)((warp & 3) << 5) << 16;
     const uint32_t tP = tmem + lane_base + C::P_COL + C::P_COLS * qt, tO = tmem + lane_base + C::O_COL + qt * D;
     // S products of the CTA, of this tile; KV tiles; pieces with work, of the CTA and of this tile
     uint32_t sbase = 0, g = 0, n_kv = 0, n_q = 0, done = 0;
     bool ok = true;
-    Piece pc;
     // P is 2^kUp times larger over 4-bit caches: fp16 then loses 2^-32 of a row's greatest weight times value at most.
     constexpr float kUp = INT4 ? 7.0f : 0.0f;
     auto s_ready = [&](uint32_t n) {   // S product number n of this tile
       return mbar_wait(smem_addr(&bar_s_full[qt * NSB + n % NSB]), (n / NSB) & 1, ctl, SITE_S_FULL);
     };
-    for (uint32_t it = 0; ok && piece_of_warp(it, pc); ++it) {
-      const int n0 = pc.n0, n1 = pc.n1, n = qt ? n1 : n0;
+    for (uint32_t it = 0; ok && wait_piece(it); ++it) {
+      const Piece& pc = s_pieces[it % C::PIECES];   // read where it is: registers are short
+      const int n0 = pc.n0, n1 = pc.n1, n = qt ? n1 : n0, key_first = pc.t0 * 128, nk = pc.nk;
       const uint32_t sb = sbase, gb = g, kvb = n_kv;
       sbase += (uint32_t)(n0 + n1);
       g += (uint32_t)n;
       n_kv += (uint32_t)max(n0, n1);
-      const int pos = qt * p.P + pos_r;                    // position in the unit
-      const bool valid = r < PG && pos < pc.n_pos;
-      const int seen = p.causal ? min(pc.nk, pc.vis + pos + 1) : pc.nk;   // keys that this row sees: the first so many
-      const bool empty = seen <= pc.t0 * 128;              // none in this piece
+      const int vis_first = pc.vis + qt * p.P;   // keys that the tile's first query sees, less one
+      const int seen = p.causal ? min(nk, vis_first + (int)((uint32_t)r / p.div_g) + 1) : nk;   // this row: the first so many
       float s = p.scale_log2;
       if (INT4 && n > 0) {
         // The rows' powers of two come with the query rows.
@@ -838,8 +842,8 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
         }
         const bool w = s_ready(gj);
         if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-        const int key0 = (pc.t0 + j) * 128;
-        const bool masked = key0 + 128 > pc.nk || (p.causal && key0 + 127 > pc.vis + qt * p.P);
+        const int key0 = key_first + j * 128;
+        const bool masked = key0 + 128 > nk || (p.causal && key0 + 127 > vis_first);
         tc_fence_after();
         const uint32_t sbuf = NSB == 1 ? 0u : s_number(sb, qt, j, n0, n1) % NSB;
         const uint32_t tS = tmem + lane_base + sbuf * 128u;
@@ -993,7 +997,9 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
         ++done;
         tc_fence_after();
       }
-      const bool none = empty || n == 0;
+      const int pos_r = (uint32_t)r / p.div_g, g_r = r - pos_r * p.G, pos = qt * p.P + pos_r;   // position in the unit, head
+      const bool valid = r < PG && pos < pc.n_pos;
+      const bool none = seen <= key_first || n == 0;   // no key of the piece
       const float inv_l = 1.0f / l, lse2 = none ? -INFINITY : m + log2f(l) - kUp;
       // Column of dim i of a group of 8: 4-bit codes are unpacked in the order 0 4 1 5 2 6 3 7.
       auto col = [](int c) { return INT4 ? (c & ~7) | ((c & 3) << 1) | ((c >> 2) & 1) : c; };
@@ -1051,6 +1057,7 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
         if (valid) p.part_lse[row] = lse2;
       }
       tc_fence_before();
+      release_piece(it);
     }
   } else {   // one Q tile: the second PV issuer's warp
     setmaxnreg_dec<C::REGS_ROLES>();
