@@ -72,17 +72,18 @@ struct PagedVarlenCfg {
   // the stages: bf16, two warps issue the copies of keys and two those of values (a page of 16 keys takes a copy for every 64
   // dims, and a copy 70 cycles of a warp: one warp for all bounded the kernel); 4 bits, all unpack keys, then values.
   static constexpr int SOFTMAX_WARPS = 4 * NQ, WARP_PV = SOFTMAX_WARPS, WARP_PLAN = WARP_PV + 2, WARP_S = WARP_PV + 3;
-  static constexpr int WARP_FEED = WARP_PV + 4, THREADS = 32 * (WARP_FEED + 4);
-  // Registers, of the launch's 512 x 128 (one Q tile: 384 x 168).
+  static constexpr int FEED_WARPS = INT4 && D == 256 ? 8 : 4;   // 8: four for keys, four for values
+  static constexpr int WARP_FEED = WARP_PV + 4, THREADS = 32 * (WARP_FEED + FEED_WARPS);
+  // Registers, of the launch's 512 x 128 (one Q tile over bf16: 384 x 168).
   static constexpr uint32_t REGS_SOFTMAX = INT4 && NQ == 2 ? 184 : 200;
-  static constexpr uint32_t REGS_ROLES = NQ == 1 ? 64 : 56, REGS_FEED = NQ == 1 ? 120 : INT4 ? 88 : 56;
-  static constexpr int REGS_NEEDED = SOFTMAX_WARPS * 32 * REGS_SOFTMAX + 128 * REGS_ROLES + 128 * REGS_FEED;
+  static constexpr uint32_t REGS_ROLES = NQ == 1 ? 64 : 56, REGS_FEED = NQ == 1 ? 96 : INT4 ? 88 : 56;
+  static constexpr int REGS_NEEDED = SOFTMAX_WARPS * 32 * REGS_SOFTMAX + 128 * REGS_ROLES + 32 * FEED_WARPS * REGS_FEED;
   static constexpr int FEEDERS = INT4 ? 4 : 2;            // warps that fill a stage
   // Work of a key in a unit of one Q tile and of two. bf16: a tile of a decoding sequence takes 1.15 us, of a chunk 1.7. 4 bits:
   // unpacking bounds both.
   static constexpr int ONE = INT4 || NQ == 1 ? 3 : 2, TWO = 3;
   static constexpr int PIECES = 4;                        // pieces that the scheduler may be ahead
-  static constexpr int CONSUMERS = SOFTMAX_WARPS + NQ + 1 + 4;
+  static constexpr int CONSUMERS = SOFTMAX_WARPS + NQ + 1 + FEED_WARPS;
   // Tiles whose powers of two are kept, and pieces whose query rows' are: K_{j + METAS} waits for S_{j + NK}, which comes after
   // the softmax has taken S_j from its buffer, and with it all of these; likewise the query rows QFS pieces later.
   static constexpr int METAS = 2 * NK, QFS = NSB + 1;
@@ -159,7 +160,9 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ float half_round(float x) { return __half2float(__float2half_rn(x)); }
 
-// The 4-bit cache's operands. Thread r of the warpgroup has query row r of each Q tile and key r of each KV tile.
+// The 4-bit cache's operands. Thread r of the warpgroup has query row r of each Q tile and key r of each KV tile; at d = 256 one
+// warpgroup has the keys and one the values, and each half of the query rows: with one stage of each, values that wait for their stage
+// must not hold up the next keys (5 sequences of up to 777 over 5000 tokens, 16 heads on 4: %%, in turns 292).
 //
 // A code in the high bits of fp16's mantissa is 1 + c / 16: a shift and a three-input logic operation, and a fused multiply-add makes
 // the operand of it.
@@ -175,6 +178,30 @@ __device__ __forceinline__ float half_round(float x) { return __half2float(__flo
 // their 32 keys (query rows: 2^-21), others are off by 2^-40 (2^-33) of it. The softmax puts the keys' power back into the
 // scores, and the values' into the weights' exponents: the running maximum is over weights times those powers, and the weights
 // are summed without them.
+// tcgen05 operations that a warp runs as one, of which the one lane with `on` issues them: what they take is then the same for the
+// warp and stays in uniform registers (in a branch of one lane every descriptor was moved there anew).
+__device__ __forceinline__ void warp_mma_ss(bool on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"((uint32_t)on)
+      : "memory");
+}
+__device__ __forceinline__ void warp_mma_ts(bool on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"((uint32_t)on)
+      : "memory");
+}
+__device__ __forceinline__ void warp_commit(bool on, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"((uint32_t)on)
+      : "memory");
+}
+
 // Waits, with a limit, until the copies that a phase counts have landed.
 __device__ __forceinline__ void land(uint64_t* bar, uint32_t phase, unsigned long long timeout_ns) {
   const uint64_t t = global_timer_ns();
@@ -247,16 +274,16 @@ __device__ __forceinline__ void load_role(const PagedVarlenParams& p, int half, 
 }
 
 template <class C, class F>
-__device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int r, int PG, uint32_t sQ, uint32_t sQx, uint32_t sK,
+__device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int thread, int PG, uint32_t sQ, uint32_t sQx, uint32_t sK,
                                             uint32_t sKx, uint32_t sV, uint64_t* bar_q_full, uint64_t* bar_q_empty,
                                             uint64_t* bar_k_full, uint64_t* bar_k_empty, uint64_t* bar_v_full,
                                             uint64_t* bar_v_empty, uint64_t* bar_meta, float4* s_kf, float4* s_ve, float* s_qf,
                                             const WaitCtl& ctl, F& piece_of_warp) {
   constexpr int D = C::D, NQ = C::NQ, NK = C::NK, NV = C::NV, GROUPS = D / kInt4Group;
-  constexpr int WORDS = D >= 128 ? 16 : 8;      // 8 codes each, of a step
-  constexpr int HALVES = D / 8 / WORDS;         // steps of a row
+  constexpr bool SPLIT = D == 256;              // keys and values have a warpgroup each
+  constexpr int WORDS = D >= 128 ? 16 : 8;      // 8 codes each, of a step: a key's or a value's, or with SPLIT half of them
   constexpr int STEP_GROUPS = WORDS / 8;        // groups of dims of a step
-  const int lane = r & 31, w = r >> 5;
+  const int r = thread & 127, role = thread >> 7, lane = r & 31, w = r >> 5;   // role: 1 for the values' warpgroup
   const uint32_t swz = (uint32_t)(r & 7), row_at = (uint32_t)r * 128, ext_at = (uint32_t)(r >> 3) * 256 + (r & 7) * 16;
   uint32_t n_q = 0, n_k = 0;                    // pieces with work, tiles
   Piece pc;
@@ -297,13 +324,13 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int r, i
       const int tok = key - (int)((uint32_t)key / p.div_page) * p.c.page_size;
       at = page * p.c.page_b + tok * p.c.token_b + head;
       const long long sz = page * p.c.sz_page_b + tok * p.c.sz_token_b + sz_head;
-      fetch_pairs(ksz, p.c.k_sz + sz);
-      fetch_pairs(vsz, p.c.v_sz + sz);
+      if (!SPLIT || role == 0) fetch_pairs(ksz, p.c.k_sz + sz);
+      if (!SPLIT || role == 1) fetch_pairs(vsz, p.c.v_sz + sz);
     };
-    // Codes of two steps: the one that is unpacked next and the one behind it, on its way.
+    // Codes of two steps, which make a tile: those that are unpacked next, and the ones behind them, on their way.
     uint32_t now[WORDS], next[WORDS];
-    auto fetch = [&](uint32_t (&x)[WORDS], long long row, bool is_v, int half) {
-      const uint8_t* from = (is_v ? p.c.v : p.c.k) + row + half * (WORDS * 4);
+    auto fetch = [&](uint32_t (&x)[WORDS], int step) {
+      const uint8_t* from = ((SPLIT ? role : step) ? p.c.v : p.c.k) + at + (SPLIT ? step * (WORDS * 4) : 0);
 #pragma unroll
       for (int i = 0; i < WORDS / 4; ++i) {
         const uint4 u = load_ahead(from + i * 16);
@@ -311,8 +338,8 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int r, i
       }
     };
     locate(t0, look_up(t0));
-    fetch(now, at, false, 0);
-    fetch(next, at, HALVES == 1, HALVES - 1);
+    fetch(now, 0);
+    fetch(next, 1);
     int page = n > 1 ? look_up(t0 + 1) : -1;
 
     // Query rows, once the S products of the last piece have read theirs.
@@ -334,12 +361,11 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int r, i
       const uint32_t bits = max(max(most & 0xffffu, most >> 16) >> 7, 8u);   // exponent of the greatest
       const float f = valid ? power_of_bits(261u - bits) : 0.f;
       s_qf[n_q % C::QFS * C::ROWS + q * 128 + r] = power_of_bits(bits - 7u);
-      uint32_t ext[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ext[i] = 0u;
+      uint32_t ext[4] = {0u, 0u, 0u, 0u};
       const uint32_t to = sQ + q * C::TILE_BYTES + row_at;
 #pragma unroll
-      for (int ch = 0; ch < C::NCH; ++ch) {
+      for (int g = 0; g < STEP_GROUPS; ++g) {
+        const int ch = role * STEP_GROUPS + g;
         float sum = 0.f;
 #pragma unroll 2
         for (uint32_t u8 = 0; u8 < 8; ++u8) {
@@ -353,10 +379,11 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int r, i
                  make_uint4(f16x2_pack(d0, d4), f16x2_pack(d1, d5), f16x2_pack(d2, d6), f16x2_pack(d3, d7)));
         }
         const float hi = half_round(sum), lo = sum - hi;
-        ext[2 * ch] = f16x2_pack(hi, hi), ext[2 * ch + 1] = f16x2_pack(lo, lo);
+        ext[2 * g] = f16x2_pack(hi, hi), ext[2 * g + 1] = f16x2_pack(lo, lo);
       }
-      sts128(sQx + q * C::EXT_BYTES + ext_at, make_uint4(ext[0], ext[1], ext[2], ext[3]));
-      sts128(sQx + q * C::EXT_BYTES + ext_at + 128, make_uint4(ext[4], ext[5], ext[6], ext[7]));
+      // 4 more columns of each group, 16 in two core matrices; with SPLIT a thread has one of them
+      sts128(sQx + q * C::EXT_BYTES + ext_at + role * 128, make_uint4(ext[0], ext[1], ext[2], ext[3]));
+      if (!SPLIT) sts128(sQx + q * C::EXT_BYTES + ext_at + 128, make_uint4(0u, 0u, 0u, 0u));
     }
     fence_async_proxy();
     __syncwarp();
@@ -378,13 +405,21 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int r, i
       // Not below 2^-80: weights without their powers are summed in fp32.
       const uint32_t bv = min(max(__reduce_max_sync(0xffffffffu, mv) >> 23, 61u), 254u);
       const float fk = power_of_bits(268u - bk), fv = power_of_bits(268u - bv);
-      ok = n_k < (uint32_t)NK || mbar_wait(smem_addr(&bar_k_empty[ks]), (n_k / NK - 1) & 1, ctl, SITE_KV_EMPTY);
-      if (!__all_sync(0xffffffffu, ok)) return;
-      if (lane == 0) {
-        reinterpret_cast<float*>(s_kf + meta)[w] = power_of_bits(bk - 14u);
-        reinterpret_cast<float*>(s_ve + meta)[w] = (float)((int)bv - 141);
+      auto publish = [&](bool keys, bool values) {
+        if (lane != 0) return;
+        if (keys) reinterpret_cast<float*>(s_kf + meta)[w] = power_of_bits(bk - 14u);
+        if (values) reinterpret_cast<float*>(s_ve + meta)[w] = (float)((int)bv - 141);
         mbar_arrive(smem_addr(&bar_meta[meta]));
+      };
+      // The softmax needs the values' powers before their stage is free. (It has read this slot's last: that tile's PV is done.)
+      if (SPLIT && role) publish(false, true);
+      {
+        const bool values = SPLIT && role;
+        uint64_t* bar = values ? &bar_v_empty[vs] : &bar_k_empty[ks];
+        ok = n_k < (uint32_t)NK || mbar_wait(smem_addr(bar), (n_k / NK - 1) & 1, ctl, SITE_KV_EMPTY);
+        if (!__all_sync(0xffffffffu, ok)) return;
       }
+      if (!SPLIT || !role) publish(true, !SPLIT);
       // What codes are multiplied with and what is added, a pair of fp16 of each group.
       uint32_t kpair[GROUPS], vpair[GROUPS], ext[8];
 #pragma unroll
@@ -398,33 +433,34 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int r, i
         const float vscale = __uint_as_float(vsz[g] << 16) * fv, vzero = __uint_as_float(vsz[g] & 0xffff0000u) * fv;
         vpair[g] = f16x2_pack(16.f * vscale, fmaf(-16.f, vscale, vzero));
       }
-      sts128(sKx + ks * C::EXT_BYTES + ext_at, make_uint4(ext[0], ext[1], ext[2], ext[3]));
-      sts128(sKx + ks * C::EXT_BYTES + ext_at + 128, make_uint4(ext[4], ext[5], ext[6], ext[7]));
-      // The next tile's pairs, and its row for the codes two steps ahead.
-      const long long here = at;
+      if (!SPLIT || !role) {
+        sts128(sKx + ks * C::EXT_BYTES + ext_at, make_uint4(ext[0], ext[1], ext[2], ext[3]));
+        sts128(sKx + ks * C::EXT_BYTES + ext_at + 128, make_uint4(ext[4], ext[5], ext[6], ext[7]));
+      }
+      // The next tile's pairs, and its row for the codes.
       if (j + 1 < n) {
         locate(t0 + j + 1, page);
         if (j + 2 < n) page = look_up(t0 + j + 2);
       }
-      // Not unrolled over steps: the roles' code would not stay in the instruction caches (unrolled over a tile, 0.8 warps a
+      // One loop for keys and values: the roles' code would not stay in the instruction caches (with both unrolled, 0.8 warps a
       // scheduler waited for instructions at any time).
 #pragma unroll 1
-      for (int step = 0; step < 2 * HALVES; ++step) {
-        const bool is_v = step >= HALVES;
-        const int half = HALVES == 1 ? 0 : step % HALVES;
-        if (step == HALVES) {
+      for (int step = 0; step < 2; ++step) {
+        const bool is_v = (SPLIT ? role : step) != 0;
+        if (!SPLIT && is_v) {
           ok = n_k < (uint32_t)NV || mbar_wait(smem_addr(&bar_v_empty[vs]), (n_k / NV - 1) & 1, ctl, SITE_KV_EMPTY);
           if (!__all_sync(0xffffffffu, ok)) return;
         }
         uint32_t s2[STEP_GROUPS], z2[STEP_GROUPS];
 #pragma unroll
         for (int g = 0; g < STEP_GROUPS; ++g) {
-          const uint32_t kk = HALVES > 1 && half ? kpair[(g + STEP_GROUPS) % GROUPS] : kpair[g];
-          const uint32_t vv = HALVES > 1 && half ? vpair[(g + STEP_GROUPS) % GROUPS] : vpair[g];
+          const int at_g = (g + STEP_GROUPS) % GROUPS;   // SPLIT: of the second half
+          const uint32_t kk = SPLIT && step ? kpair[at_g] : kpair[g], vv = SPLIT && step ? vpair[at_g] : vpair[g];
           const uint32_t pair = is_v ? vv : kk;
           s2[g] = __byte_perm(pair, 0, 0x1010), z2[g] = __byte_perm(pair, 0, 0x3232);
         }
-        const uint32_t to = ((is_v ? sV + vs * C::TILE_BYTES : sK + ks * C::TILE_BYTES) + row_at + half * (2 * C::CHUNK_BYTES)) | swz << 4;
+        const uint32_t stage = is_v ? sV + vs * C::TILE_BYTES : sK + ks * C::TILE_BYTES;
+        const uint32_t to = (stage + row_at + (SPLIT ? step * (STEP_GROUPS * C::CHUNK_BYTES) : 0)) | swz << 4;
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) {
           // Codes m and m + 4 in the high bits of fp16's mantissa, 1 + code / 16.
@@ -433,19 +469,14 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int r, i
                  make_uint4(half2_fma((x << 6 & mask) | one, s, z), half2_fma((x << 2 & mask) | one, s, z),
                             half2_fma((x >> 2 & mask) | one, s, z), half2_fma((x >> 6 & mask) | one, s, z)));
         }
-        if (half == HALVES - 1) {
+        if (!SPLIT || step) {
           fence_async_proxy();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(is_v ? &bar_v_full[vs] : &bar_k_full[ks]));
         }
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) now[i] = next[i];
-        // Two steps on: with one step a row the next tile's; with two the values of this, then the next tile's keys.
-        if (HALVES == 1 || is_v) {
-          if (j + 1 < n) fetch(next, at, HALVES == 1 ? is_v : false, half);
-        } else {
-          fetch(next, here, true, half);
-        }
+        if (j + 1 < n) fetch(next, step);   // of the next tile
       }
     }
   }
@@ -478,7 +509,7 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
 
   if (tid == 0) {
     abort_flag = 0u;
-    mbar_init(smem_addr(&bar_q_full), INT4 ? 4 : 1);
+    mbar_init(smem_addr(&bar_q_full), INT4 ? C::FEED_WARPS : 1);
     mbar_init(smem_addr(&bar_q_empty), 1);
     for (int i = 0; i < NK; ++i) mbar_init(smem_addr(&bar_k_full[i]), C::FEEDERS), mbar_init(smem_addr(&bar_k_empty[i]), 1);
     for (int i = 0; i < NV; ++i) mbar_init(smem_addr(&bar_v_full[i]), C::FEEDERS), mbar_init(smem_addr(&bar_v_empty[i]), NQ);
@@ -494,7 +525,7 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
       mbar_init(smem_addr(&bar_piece_full[i]), 1);
       mbar_init(smem_addr(&bar_piece_empty[i]), C::CONSUMERS);
     }
-    for (int i = 0; i < C::METAS; ++i) mbar_init(smem_addr(&bar_meta[i]), 4);
+    for (int i = 0; i < C::METAS; ++i) mbar_init(smem_addr(&bar_meta[i]), C::FEED_WARPS);
     for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&bar_patch[i]), 1);
     for (int i = 0; i < NQ + 1; ++i) mbar_init(smem_addr(&bar_drain[i]), 1);
     fence_mbar_init();
@@ -515,14 +546,11 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
   const uint32_t tmem = tmem_slot;
   const int PG = p.P * p.G, RP = p.P * NQ;
 
-  // Pieces as their consumers see them; `it` counts those taken. A single lane's and a whole warp's way to take one.
-  auto piece_of_lane = [&](uint32_t it, Piece& pc) {
-    const uint32_t i = it % C::PIECES;
-    if (!mbar_wait(smem_addr(&bar_piece_full[i]), (it / C::PIECES) & 1, ctl, SITE_PIECE_FULL)) return false;
-    pc = s_pieces[i];
-    mbar_arrive(smem_addr(&bar_piece_empty[i]));
-    return pc.work != 0;
+  auto wait = [&](uint32_t bar, uint32_t parity, uint32_t site) {   // by a whole warp
+    const bool w = mbar_wait(bar, parity, ctl, site);
+    return __all_sync(0xffffffffu, w) != 0;
   };
+  // Pieces as their consumers see them; `it` counts those taken.
   auto wait_piece = [&](uint32_t it) {
     const uint32_t i = it % C::PIECES;
     const bool w = mbar_wait(smem_addr(&bar_piece_full[i]), (it / C::PIECES) & 1, ctl, SITE_PIECE_FULL);
@@ -709,77 +737,85 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
   } else if (warp >= C::WARP_PV && warp < C::WARP_PV + NQ) {
     // ------------------------------------------------------------------ PV issuer, one per Q tile
     setmaxnreg_dec<C::REGS_ROLES>();
-    if (lane == 0) {
-      const int q = warp - C::WARP_PV;
-      const uint32_t d_o = tmem + C::O_COL + q * D, a_p = tmem + C::P_COL + C::P_COLS * q;
-      uint32_t n_v = 0, g = 0;   // V tiles of the CTA, products of this Q tile
-      bool ok = true;
-      Piece pc;
-      for (uint32_t it = 0; ok && piece_of_lane(it, pc); ++it) {
-        const int n = q ? pc.n1 : pc.n0, n_all = max(pc.n0, pc.n1);
-        for (int j = 0; ok && j < n_all; ++j, ++n_v) {
-          const uint32_t vs = n_v % NV;
-          if (!mbar_wait(smem_addr(&bar_v_full[vs]), (n_v / NV) & 1, ctl, SITE_KV_FULL)) { ok = false; break; }
-          if (j < n) {
-            const uint32_t b_v = sV + vs * C::TILE_BYTES;
-            if (!mbar_wait(smem_addr(&bar_p_half[q][0]), g & 1, ctl, SITE_P_FULL)) { ok = false; break; }
+    const bool on = elect_one();
+    const int q = warp - C::WARP_PV;
+    const uint32_t d_o = tmem + C::O_COL + q * D, a_p = tmem + C::P_COL + C::P_COLS * q;
+    uint32_t n_v = 0, g = 0;   // V tiles of the CTA, products of this Q tile
+    bool ok = true;
+    Piece pc;
+    for (uint32_t it = 0; ok && piece_of_warp(it, pc); ++it) {
+      const int n = q ? pc.n1 : pc.n0, n_all = max(pc.n0, pc.n1);
+      for (int j = 0; ok && j < n_all; ++j, ++n_v) {
+        const uint32_t vs = n_v % NV;
+        if (!wait(smem_addr(&bar_v_full[vs]), (n_v / NV) & 1, SITE_KV_FULL)) { ok = false; break; }
+        if (j < n) {
+          const uint64_t b_v = make_sdesc_swz(sV + vs * C::TILE_BYTES, C::CHUNK_BYTES, C::SBO, C::SWZ);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {   // as the softmax hands P over
+            if (!wait(smem_addr(&bar_p_half[q][h]), g & 1, SITE_P_FULL)) { ok = false; break; }
             tc_fence_after();
-            issue_pv_half<C, 0>(d_o, a_p, b_v, j > 0);
-            if (!mbar_wait(smem_addr(&bar_p_half[q][1]), g & 1, ctl, SITE_P_FULL)) { ok = false; break; }
-            tc_fence_after();
-            issue_pv_half<C, 1>(d_o, a_p, b_v, true);
-            tc_commit(smem_addr(&bar_o_done[q]));
-            if (j + 1 == n) tc_commit(smem_addr(&bar_o_full[q]));
-            tc_commit(smem_addr(&bar_v_empty[vs]));
-            ++g;
-          } else {
-            mbar_arrive(smem_addr(&bar_v_empty[vs]));
+#pragma unroll
+            for (int i = 0; i < C::KSTEPS_PV / 2; ++i) {
+              const int k = h * (C::KSTEPS_PV / 2) + i;
+              warp_mma_ts(on, d_o, a_p + k * 8, b_v + (uint64_t)((k * C::PV_ROWS * C::SWZ) >> 4), C::IDESC_PV, k > 0 || j > 0 ? 1u : 0u);
+            }
           }
+          if (!ok) break;
+          warp_commit(on, smem_addr(&bar_o_done[q]));
+          if (j + 1 == n) warp_commit(on, smem_addr(&bar_o_full[q]));
+          warp_commit(on, smem_addr(&bar_v_empty[vs]));
+          ++g;
+        } else if (lane == 0) {
+          mbar_arrive(smem_addr(&bar_v_empty[vs]));
         }
       }
-      // Every MMA this warp issued must finish before TMEM is released.
-      tc_commit(smem_addr(&bar_drain[q]));
-      const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(smem_addr(&bar_drain[q]), 0) && global_timer_ns() - t0 < p.timeout_ns) {}
     }
+    // Every MMA this warp issued must finish before TMEM is released.
+    warp_commit(on, smem_addr(&bar_drain[q]));
+    land(&bar_drain[q], 0, p.timeout_ns);
   } else if (warp == C::WARP_S) {
     // ------------------------------------------------------------------ S issuer
     setmaxnreg_dec<C::REGS_ROLES>();
-    if (lane == 0) {
-      uint32_t n_k = 0, n_q = 0, k = 0, g0 = 0, g1 = 0;   // K tiles, Q loads, S products of the CTA and of each Q tile
-      bool ok = true;
-      Piece pc;
-      for (uint32_t it = 0; ok && piece_of_lane(it, pc); ++it) {
-        const int n_all = max(pc.n0, pc.n1);
-        if (n_all == 0) continue;
-        if (!mbar_wait(smem_addr(&bar_q_full), n_q & 1, ctl, SITE_Q_FULL)) { ok = false; break; }
-        ++n_q;
-        for (int j = 0; ok && j < n_all; ++j, ++n_k) {
-          const uint32_t ks = n_k % NK;
-          if (!mbar_wait(smem_addr(&bar_k_full[ks]), (n_k / NK) & 1, ctl, SITE_KV_FULL)) { ok = false; break; }
-          for (int q = 0; ok && q < NQ; ++q) {
-            if (j >= (q ? pc.n1 : pc.n0)) continue;
-            uint32_t& g = q ? g1 : g0;
-            const uint32_t b = k % NSB;
-            if (k >= (uint32_t)NSB && !mbar_wait(smem_addr(&bar_s_free[b]), (k / NSB - 1) & 1, ctl, SITE_S_FREE)) { ok = false; break; }
-            tc_fence_after();
-            issue_qk<C>(tmem + b * 128u, sQ + q * C::TILE_BYTES, sK + ks * C::TILE_BYTES, C::IDESC_QK | p.qk_negate);
-            if constexpr (INT4)
-              mma_f16_ss(tmem + b * 128u, make_sdesc_plain(sQx + q * C::EXT_BYTES, 128, 256),
-                         make_sdesc_plain(sKx + ks * C::EXT_BYTES, 128, 256), C::IDESC_QK | p.qk_negate, 1u);
-            tc_commit(smem_addr(&bar_s_full[q * NSB + g % NSB]));
-            ++g;
-            ++k;
+    const bool on = elect_one();
+    const uint32_t idesc = C::IDESC_QK | p.qk_negate;
+    uint32_t n_k = 0, n_q = 0, k = 0, g0 = 0, g1 = 0;   // K tiles, Q loads, S products of the CTA and of each Q tile
+    bool ok = true;
+    Piece pc;
+    for (uint32_t it = 0; ok && piece_of_warp(it, pc); ++it) {
+      const int n_all = max(pc.n0, pc.n1);
+      if (n_all == 0) continue;
+      if (!wait(smem_addr(&bar_q_full), n_q & 1, SITE_Q_FULL)) { ok = false; break; }
+      ++n_q;
+      for (int j = 0; ok && j < n_all; ++j, ++n_k) {
+        const uint32_t ks = n_k % NK;
+        if (!wait(smem_addr(&bar_k_full[ks]), (n_k / NK) & 1, SITE_KV_FULL)) { ok = false; break; }
+        for (int q = 0; ok && q < NQ; ++q) {
+          if (j >= (q ? pc.n1 : pc.n0)) continue;
+          uint32_t& g = q ? g1 : g0;
+          const uint32_t b = k % NSB;
+          if (k >= (uint32_t)NSB && !wait(smem_addr(&bar_s_free[b]), (k / NSB - 1) & 1, SITE_S_FREE)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t dq = make_sdesc_swz(sQ + q * C::TILE_BYTES, 16, C::SBO, C::SWZ);
+          const uint64_t dk = make_sdesc_swz(sK + ks * C::TILE_BYTES, 16, C::SBO, C::SWZ);
+#pragma unroll
+          for (int i = 0; i < C::KSTEPS_QK; ++i) {   // 4 steps of 32 bytes to a swizzle row
+            const uint64_t off = (uint64_t)(((i / 4) * C::CHUNK_BYTES + (i % 4) * 32) >> 4);
+            warp_mma_ss(on, tmem + b * 128u, dq + off, dk + off, idesc, i > 0 ? 1u : 0u);
           }
-          if (!ok) break;
-          tc_commit(smem_addr(&bar_k_empty[ks]));
-          if (j + 1 == n_all) tc_commit(smem_addr(&bar_q_empty));
+          if constexpr (INT4)
+            warp_mma_ss(on, tmem + b * 128u, make_sdesc_plain(sQx + q * C::EXT_BYTES, 128, 256),
+                        make_sdesc_plain(sKx + ks * C::EXT_BYTES, 128, 256), idesc, 1u);
+          warp_commit(on, smem_addr(&bar_s_full[q * NSB + g % NSB]));
+          ++g;
+          ++k;
         }
+        if (!ok) break;
+        warp_commit(on, smem_addr(&bar_k_empty[ks]));
+        if (j + 1 == n_all) warp_commit(on, smem_addr(&bar_q_empty));
       }
-      tc_commit(smem_addr(&bar_drain[NQ]));
-      const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(smem_addr(&bar_drain[NQ]), 0) && global_timer_ns() - t0 < p.timeout_ns) {}
     }
+    warp_commit(on, smem_addr(&bar_drain[NQ]));
+    land(&bar_drain[NQ], 0, p.timeout_ns);
   } else if (warp >= C::WARP_FEED) {
     // ------------------------------------------------------------------ bf16: copies of keys and values. 4 bits: query rows, keys and
     // values to fp16
