@@ -44,7 +44,6 @@ struct Piece {
   int nk;                   // keys of the sequence
   int t0, n0, n1;           // first KV tile; tiles that Q tile 0 and 1 visit from there
   int slot;                 // of its part; -1: the piece is the whole unit
-  int pad;
 };
 
 template <int D_, bool INT4_>
@@ -89,6 +88,7 @@ struct PagedVarlenCfg {
   static constexpr int METAS = 2 * NK, QFS = NSB + 1;
 };
 
+constexpr long long kMostWork = 1LL << 52;   // of a call: 64 bits hold it times the number of CTAs
 constexpr int kUnitOverhead = 6 * 128;       // work (see UnitWork) of beginning and ending a unit
 constexpr long long kLeastShare = 8 * 128;   // of a CTA: a share within a unit's beginning would have nothing to do
 
@@ -138,16 +138,6 @@ __device__ __forceinline__ uint4 load_ahead(const void* p) {
 
 // 2^e of a float's exponent bits: 1 <= bits <= 254.
 __device__ __forceinline__ float power_of_bits(uint32_t bits) { return __uint_as_float(bits << 23); }
-__device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 __device__ __forceinline__ uint32_t half2_fma(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -160,24 +150,6 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ float half_round(float x) { return __half2float(__float2half_rn(x)); }
 
-// The 4-bit cache's operands. Thread r of the warpgroup has query row r of each Q tile and key r of each KV tile; at d = 256 one
-// warpgroup has the keys and one the values, and each half of the query rows: with one stage of each, values that wait for their stage
-// must not hold up the next keys (5 sequences of up to 777 over 5000 tokens, 16 heads on 4: %%, in turns 292).
-//
-// A code in the high bits of fp16's mantissa is 1 + c / 16: a shift and a three-input logic operation, and a fused multiply-add makes
-// the operand of it.
-// Keys: zero + scale c = scale (c - 8) + zero', zero' = zero + 8 scale. The first term, 16 scale (1 + c / 16) - 24 scale, has 11
-// bits (8 of scale, 3 of c - 8), so fp16 holds it; the second is one value a group of dims, which S takes in as a product of 16
-// more columns,
-//   zero' sum(q) = (zh + zl) (Qh + Ql),    zh + zl and Qh + Ql the two values in 22 bits each.
-// So S is what fp32 would give. In bf16 the keys would be 2^-8 off, and LSE with them (2e-5 of it over 1000 keys).
-// Values: 16 scale (1 + c / 16) + (zero - 16 scale), the sum and its second term rounded to fp16, 2^-11 off each, as P is; in bf16
-// the two would add as much to O's error as its own rounding.
-// fp16's range: every 32 keys (a warp's) of a tile are divided by a power of two that brings the greatest of them below 2^15, a
-// query row by one that brings its greatest value into [2^7, 2^8). Full precision is left to values 2^-29 of the greatest of
-// their 32 keys (query rows: 2^-21), others are off by 2^-40 (2^-33) of it. The softmax puts the keys' power back into the
-// scores, and the values' into the weights' exponents: the running maximum is over weights times those powers, and the weights
-// are summed without them.
 // tcgen05 operations that a warp runs as one, of which the one lane with `on` issues them: what they take is then the same for the
 // warp and stays in uniform registers (in a branch of one lane every descriptor was moved there anew).
 __device__ __forceinline__ void warp_mma_ss(bool on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -210,12 +182,11 @@ __device__ __forceinline__ void land(uint64_t* bar, uint32_t phase, unsigned lon
 
 // The bf16 cache's keys or values, by one warp of the two that share the work. Lane i copies box 2 i + half of a tile: 64 columns
 // (box % NCH) of box_rows neighbouring keys (box / NCH), which lie in one page.
-template <class C, class F>
-__device__ __forceinline__ void load_role(const PagedVarlenParams& p, int half, bool is_v, const CUtensorMap* map, uint32_t tiles,
+template <class C, bool IS_V, class F>
+__device__ __forceinline__ void load_role(const PagedVarlenParams& p, int half, const CUtensorMap* map, uint32_t tiles,
                                           uint64_t* bar_full, uint64_t* bar_empty, uint64_t* bar_patch, const WaitCtl& ctl,
                                           F& piece_of_warp) {
-  constexpr int NCH = C::NCH, NS = C::NK;
-  static_assert(C::NK == C::NV, "one count of stages for both");
+  constexpr int NCH = C::NCH, NS = IS_V ? C::NV : C::NK;
   const int lane = threadIdx.x & 31, rows = p.box_rows, boxes = 128 / rows * NCH;
   const int box = 2 * lane + half, chunk = box % NCH, at = box / NCH * rows;
   const bool mine = box < boxes;
@@ -244,9 +215,9 @@ __device__ __forceinline__ void load_role(const PagedVarlenParams& p, int half, 
       bool w = n_t < (uint32_t)NS || mbar_wait(smem_addr(&bar_empty[stage]), (n_t / NS - 1) & 1, ctl, SITE_KV_EMPTY);
       if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
       ++n_t;
-      if (p.debug_skip_load && blockIdx.x == 0 && is_v && n_t == 1) continue;
+      if (IS_V && p.debug_skip_load && blockIdx.x == 0 && n_t == 1) continue;
       // Values of the last page's rows behind the sequence's end may be anything, and 0 times NaN is NaN: they are cleared.
-      const bool patch = is_v && pc.nk - key0 < 128 && pc.nk % rows != 0;
+      const bool patch = IS_V && pc.nk - key0 < 128 && pc.nk % rows != 0;
       const uint32_t bar = smem_addr(patch ? bar_patch : &bar_full[stage]);
       if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
       __syncwarp();
@@ -273,6 +244,24 @@ __device__ __forceinline__ void load_role(const PagedVarlenParams& p, int half, 
   }
 }
 
+// The 4-bit cache's operands. Thread r of the warpgroup has query row r of each Q tile and key r of each KV tile; at d = 256 one
+// warpgroup has the keys and one the values, and each half of the query rows: with one stage of each, values that wait for their stage
+// must not hold up the next keys (5 sequences of up to 777 over 5000 tokens, 16 heads on 4: 237 us, in turns 292).
+//
+// A code in the high bits of fp16's mantissa is 1 + c / 16: a shift and a three-input logic operation, and a fused multiply-add makes
+// the operand of it.
+// Keys: zero + scale c = scale (c - 8) + zero', zero' = zero + 8 scale. The first term, 16 scale (1 + c / 16) - 24 scale, has 11
+// bits (8 of scale, 3 of c - 8), so fp16 holds it; the second is one value a group of dims, which S takes in as a product of 16
+// more columns,
+//   zero' sum(q) = (zh + zl) (Qh + Ql),    zh + zl and Qh + Ql the two values in 22 bits each.
+// So S is what fp32 would give. In bf16 the keys would be 2^-8 off, and LSE with them (2e-5 of it over 1000 keys).
+// Values: 16 scale (1 + c / 16) + (zero - 16 scale), the sum and its second term rounded to fp16, 2^-11 off each, as P is; in bf16
+// the two would add as much to O's error as its own rounding.
+// fp16's range: every 32 keys (a warp's) of a tile are divided by a power of two that brings the greatest of them below 2^15, a
+// query row by one that brings its greatest value into [2^7, 2^8). Full precision is left to values 2^-29 of the greatest of
+// their 32 keys (query rows: 2^-21), others are off by 2^-40 (2^-33) of it. The softmax puts the keys' power back into the
+// scores, and the values' into the weights' exponents: the running maximum is over weights times those powers, and the weights
+// are summed without them.
 template <class C, class F>
 __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int thread, int PG, uint32_t sQ, uint32_t sQx, uint32_t sK,
                                             uint32_t sKx, uint32_t sV, uint64_t* bar_q_full, uint64_t* bar_q_empty,
@@ -633,7 +622,11 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
     };
     // All work, dealt to the CTAs in equal contiguous shares: mine is [x0, x1).
     long long W = 0, mine, upto, x0 = 0, x1 = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) upto = costs(b0, mine), W += __shfl_sync(0xffffffffu, upto, 31);
+    for (int b0 = 0; b0 < p.B; b0 += 32) upto = costs(b0, mine), W = min(W + __shfl_sync(0xffffffffu, upto, 31), 2 * kMostWork);
+    if (W > kMostWork) {   // the host refuses calls of more: offsets whose sequences share rows
+      if (lane == 0) atomicCAS(p.status, 0u, kStatusBadPage);
+      W = 0;
+    }
     const int shares = (int)max(1LL, min((long long)gridDim.x, W / kLeastShare)), me = blockIdx.x;
     int4 cut0 = make_int4(0, 0, 0, 0);
     if (me < shares && W > 0) {
@@ -821,9 +814,10 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
     // values to fp16
     setmaxnreg_dec<C::REGS_FEED>();
     if constexpr (!INT4) {
-      const bool is_v = warp >= C::WARP_FEED + 2;
-      load_role<C>(p, warp & 1, is_v, is_v ? &tm_v : &tm_k, is_v ? sV : sK, is_v ? bar_v_full : bar_k_full,
-                   is_v ? bar_v_empty : bar_k_empty, &bar_patch[warp & 1], ctl, piece_of_warp);
+      if (warp < C::WARP_FEED + 2)
+        load_role<C, false>(p, warp & 1, &tm_k, sK, bar_k_full, bar_k_empty, &bar_patch[warp & 1], ctl, piece_of_warp);
+      else
+        load_role<C, true>(p, warp & 1, &tm_v, sV, bar_v_full, bar_v_empty, &bar_patch[warp & 1], ctl, piece_of_warp);
     } else {
       unpack_role<C>(p, tid - 32 * C::WARP_FEED, PG, sQ, sQx, sK, sKx, sV, &bar_q_full, &bar_q_empty, bar_k_full, bar_k_empty,
                      bar_v_full, bar_v_empty, bar_meta, s_kf, s_ve, s_qf, ctl, piece_of_warp);
