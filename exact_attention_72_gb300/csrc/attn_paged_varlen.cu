@@ -143,7 +143,7 @@ extern "C" attn_status_t attn_fwd_paged_varlen(const void* q, const attn_paged_c
   if (G > 128 || total_q > kMaxKeys || keys > kMaxKeys) return ATTN_ERR_UNSUPPORTED;
   const int P = 128 / G, RP = P * (unit_rows(d) / 128);
   // Work of all units, as the kernel adds it up.
-  const double most = ((double)total_q / RP + std::min(B, total_q)) * Hkv * (3. * keys + kUnitOverhead);
+  const double most = ((double)total_q / RP + std::min(B, total_q)) * Hkv * (4. * keys + kUnitOverhead);
   if (most > (double)kMostWork) return ATTN_ERR_UNSUPPORTED;
   if (!device_state(&a.grid, &p.status, &a.context)) return ATTN_ERR_CUDA;
   size_t n[3];

@@ -78,9 +78,9 @@ struct PagedVarlenCfg {
   static constexpr uint32_t REGS_ROLES = NQ == 1 ? 64 : 56, REGS_FEED = NQ == 1 ? 96 : INT4 ? 88 : 56;
   static constexpr int REGS_NEEDED = SOFTMAX_WARPS * 32 * REGS_SOFTMAX + 128 * REGS_ROLES + 32 * FEED_WARPS * REGS_FEED;
   static constexpr int FEEDERS = INT4 ? 4 : 2;            // warps that fill a stage
-  // Work of a key in a unit of one Q tile and of two. bf16: a tile of a decoding sequence takes 1.15 us, of a chunk 1.7. 4 bits:
+  // Work of a key in a unit of one Q tile and of two. bf16: a tile of a decoding sequence takes 1.2 us, of a chunk 1.65. 4 bits:
   // unpacking bounds both.
-  static constexpr int ONE = INT4 || NQ == 1 ? 3 : 2, TWO = 3;
+  static constexpr int ONE = 3, TWO = INT4 || NQ == 1 ? 3 : 4;
   static constexpr int PIECES = 4;                        // pieces that the scheduler may be ahead
   static constexpr int CONSUMERS = SOFTMAX_WARPS + NQ + 1 + FEED_WARPS;
   // Tiles whose powers of two are kept, and pieces whose query rows' are: K_{j + METAS} waits for S_{j + NK}, which comes after
@@ -630,8 +630,10 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
     const int shares = (int)max(1LL, min((long long)gridDim.x, W / kLeastShare)), me = blockIdx.x;
     int4 cut0 = make_int4(0, 0, 0, 0);
     if (me < shares && W > 0) {
-      x0 = me * W / shares;
-      x1 = (me + 1) * W / shares;
+      // Divisions in 64 bits, some 500 cycles each, go to lanes that do them at once.
+      x0 = (me + (lane & 1)) * W / shares;
+      x1 = __shfl_sync(0xffffffffu, x0, 1);
+      x0 = __shfl_sync(0xffffffffu, x0, 0);
       // The sequence, kv head and unit that x0 lies in.
       int b = 0, kvh = 0, m = 0, q_base = 0;
       long long before = 0;
@@ -663,13 +665,15 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
       }
       while (ok && before < x1) {
         const int keys = s.keys(m), n = (keys + 127) / 128, per = 128 * s.a_key(m);   // per: work of a tile
-        // The tile that place x of all work lies at.
-        auto tile_at = [&](long long x) {
-          const long long r = x - before - kUnitOverhead + per / 2;
-          return r <= 0 ? 0 : (int)min((long long)n, r / per);
-        };
         const long long end = before + kUnitOverhead + keys * (long long)(per / 128);
-        const int t0 = x0 > before ? tile_at(x0) : 0, t1 = x1 >= end ? n : tile_at(x1);
+        // The tiles that places x0 and x1 of all work lie at, by lanes 0 and 1. Lane 2: the share that begins at or behind the place
+        // where the last tile is reached.
+        const long long place = min(end, before + kUnitOverhead + (long long)per * n - per / 2);
+        const long long from = (lane == 1 ? x1 : x0) - before - kUnitOverhead + per / 2;
+        const long long quotient = (lane == 2 ? place * shares + W - 1 : max(from, 0LL)) / (lane == 2 ? W : (long long)per);
+        const int at = (int)min(quotient, (long long)(lane == 2 ? shares : n));
+        const int at0 = __shfl_sync(0xffffffffu, at, 0), at1 = __shfl_sync(0xffffffffu, at, 1), at2 = __shfl_sync(0xffffffffu, at, 2);
+        const int t0 = x0 > before ? at0 : 0, t1 = x1 >= end ? n : at1;
         if (t1 > t0 || (n == 0 && before >= x0)) {
           const bool whole = t0 == 0 && t1 == n;
           Piece pc = {};
@@ -689,9 +693,7 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
           pc.slot = whole ? -1 : t0 > 0 ? 2 * me : 2 * me + 1;
           if (t0 == 0 && !whole) {
             // Parts: mine, and one of each CTA whose share begins before the place where the last tile is reached.
-            const long long place = min(end, before + kUnitOverhead + (long long)per * n - per / 2);
-            const int last = (int)((place * shares + W - 1) / W) - 1;
-            cut0 = make_int4(pc.q_row, pc.kvh, pc.n_pos, last - me + 1);
+            cut0 = make_int4(pc.q_row, pc.kvh, pc.n_pos, at2 - me);
           }
           ok = publish(pc) && load_queries(pc);
         }
@@ -1029,12 +1031,14 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
       }
       const int pos_r = (uint32_t)r / p.div_g, g_r = r - pos_r * p.G, pos = qt * p.P + pos_r;   // position in the unit, head
       const bool valid = r < PG && pos < pc.n_pos;
+      const int slot = pc.slot, q_row = pc.q_row, head = pc.kvh * p.G + g_r;
+      release_piece(it);   // before the stores, which a later arrival would wait for
       const bool none = seen <= key_first || n == 0;   // no key of the piece
       const float inv_l = 1.0f / l, lse2 = none ? -INFINITY : m + log2f(l) - kUp;
       // Column of dim i of a group of 8: 4-bit codes are unpacked in the order 0 4 1 5 2 6 3 7.
       auto col = [](int c) { return INT4 ? (c & ~7) | ((c & 3) << 1) | ((c >> 2) & 1) : c; };
-      if (pc.slot < 0) {
-        const long long row = ((long long)(pc.q_row + pos) * p.H + pc.kvh * p.G + g_r);
+      if (slot < 0) {
+        const long long row = (long long)(q_row + pos) * p.H + head;
         __nv_bfloat16* orow = p.o + row * D;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 64) {
@@ -1065,9 +1069,9 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
             }
           }
         }
-        if (valid) p.lse[(long long)(pc.kvh * p.G + g_r) * p.total_q + pc.q_row + pos] = lse2 * 0.69314718055994531f;
+        if (valid) p.lse[(long long)head * p.total_q + q_row + pos] = lse2 * 0.69314718055994531f;
       } else {
-        const long long row = (long long)pc.slot * C::ROWS + qt * 128 + r;
+        const long long row = (long long)slot * C::ROWS + qt * 128 + r;
         float* orow = p.part_o + row * D;
         if (n > 0) {
 #pragma unroll 1
@@ -1087,7 +1091,6 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
         if (valid) p.part_lse[row] = lse2;
       }
       tc_fence_before();
-      release_piece(it);
     }
   } else {   // one Q tile: the second PV issuer's warp
     setmaxnreg_dec<C::REGS_ROLES>();
