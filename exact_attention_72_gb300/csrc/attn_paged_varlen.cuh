@@ -1,6 +1,26 @@
 // Attention of chunks of new tokens over a paged key/value cache in bf16 or 4 bits, any ragged batch:
 //   S = scale q k^T over the keys a row sees,  O = softmax(S) V,  LSE,
 // with the queries of sequence b packed from row cu[b] on and its keys, the new ones among them, in pages.
+//
+// The G query heads of a kv head share its keys, so 128 rows of a tile are P = 128 / G positions times G heads: a decoding sequence
+// reads its cache once. A CTA has two such tiles (one at d = 256, where O fills tensor memory), tcgen05 for both products, P in
+// tensor memory, the scores' buffer shared by both tiles, and a softmax warpgroup for each.
+//
+// Work: units of (sequence, kv head, tiles of positions) times KV tiles. Lengths are known on the GPU only, and differ by orders:
+// so all work, in weighted keys, is dealt to the CTAs, one an SM, in equal contiguous shares, whatever unit their ends fall into. A unit
+// that is cut leaves normalised parts in fp32, at most two a CTA, which a second kernel joins. A chunk of 300 tokens over 65k keys
+// fills the GPU like 34 sequences, and the workspace depends on neither. Finding its share takes a CTA some 3 us.
+//
+// What bounds it (GB300, H 32, Hkv 8, d 128, times of a call in a graph):
+//   bf16, 4 chunks of up to 4096 tokens over 8192: 1195 us, 1620 TFLOP/s (84% of measured). A tile of 2 x 128 rows takes 1.65 us,
+//     in which the tensor core waits for the softmax of the one buffer of scores; 1509 us at first: copies issued by four warps,
+//     MMAs by warps that run as one, and maxima taken by the loads of the scores made it so.
+//   bf16, 30 decoding sequences of up to 16k keys: 245 us, 6150 GB/s (90%). A CTA by itself takes 1.2 us a tile, 64 KB that come 2 us after
+//     their copy was issued; with fewer CTAs at it neither a fifth stage, tiles fetched into the L2 ahead (they take the copies' turns: 20%
+//     slower), nor both tiles' warps on one unit made it faster.
+//   bf16, d 256: 5 sequences, 777 tokens over 5000, H 16, Hkv 4: 149 us. 128 KB of keys and values for 128 rows come out of the
+//     L2 at 40 bytes a cycle and SM, 11.5 TB/s in all. Halves of keys in more stages: 155 us.
+//   4 bits, the first case: 1840 us. Unpacking, 2.5 us a tile of 128 keys and values by 4 warps; see unpack_role.
 #pragma once
 #include <cuda_fp16.h>
 

@@ -547,8 +547,8 @@ attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t* cache, voi
  * batch of 8 and more go to attn_fwd_paged's kernel there (H / Hkv <= 16). Deterministic. Two programmatic dependent launches, four
  * with those; allocates nothing; total_q == 0 returns ATTN_OK at once.
  * UNSUPPORTED as for the cache, for scale == 0, H / Hkv > 128, total_q or max_pages * page_size >= 2^31 - 1023, strides
- * of a bf16 cache that tensor maps do not take (2^40 bytes and more, or 0 between two rows), and for more than 2^52 / Hkv
- * keys over all blocks of queries.
+ * of a bf16 cache that tensor maps do not take (2^40 bytes and more, or 0 between two rows), and for more than 2^50 / Hkv
+ * keys over all blocks of 128 or 256 query rows.
  */
 size_t attn_fwd_paged_varlen_workspace_bytes(int B, int H, int Hkv, int total_q, int d, attn_cache_type_t type);
 attn_status_t attn_fwd_paged_varlen(const void* q, const attn_paged_cache_t* cache, void* o, float* lse,
@@ -569,8 +569,8 @@ attn_status_t attn_get_status(cudaStream_t stream);
  * attn_get_status_detail — attn_get_status that also stores the raw device status word in
  * `detail` (may be NULL): 0, 0x40000000 | the code of the wait site that gave up, 0x2000000C
  * for a rejected varlen plan, 0x2000000D for a page, length, offset or position of a paged-cache call out of
- * range (attn_paged_append: the tables of angles included), or 0x2000000E for a position of attn_qk_norm_rope or
- * attn_qk_norm_rope_bwd outside their tables. 0 is stored when the synchronization fails.
+ * range (attn_paged_append: the tables of angles included), or 0x2000000E for a position of attn_qk_norm_rope,
+ * attn_qk_norm_rope_axes or their gradients outside their tables. 0 is stored when the synchronization fails.
  */
 attn_status_t attn_get_status_detail(cudaStream_t stream, uint32_t* detail);
 

@@ -66,6 +66,26 @@ def write(cache, table, lens, seed, k=None, v=None):
     return out
 
 
+def read(cache, table, lens):
+    """What the cache holds of every sequence, as `write` returns it."""
+    out = []
+    for b, n in enumerate(lens):
+        pos = np.arange(n)
+        pg = torch.tensor(table[b][pos // cache.page_size].astype(np.int64)).cuda()
+        at = torch.tensor(pos % cache.page_size).cuda()
+        got = []
+        for t, sz in ((cache.k, cache.k_sz), (cache.v, cache.v_sz)):
+            x = t[pg, at]
+            if sz is None:
+                got.append((x.double(), x.double().abs(), torch.zeros(x.shape, dtype=torch.float64, device="cuda")))
+                continue
+            codes = torch.stack((x & 15, x >> 4), -1).flatten(-2).double()
+            s, z = (y.double().repeat_interleave(64, -1) for y in sz[pg, at].unbind(-1))
+            got.append((z + s * codes, (s * (codes - 8)).abs() + (z + 8 * s).abs(), (z - 16 * s).abs()))
+        out.append((got[0][0], got[1][0], got[0][1], got[1][1], got[1][2]))
+    return out
+
+
 def check(q, cu, o, lse, held, scale, causal, four):
     """q, o [total, H, d], lse [H, total] against what `held` (write) says, sequence by sequence."""
     H, d = q.shape[1:]
@@ -439,38 +459,49 @@ def test_refusals():
     ok()
 
 
-def test_a_step_of_a_multimodal_server():
-    """Norm and rotation, append, attention of the chunk, as they are used together: two steps of prompts and decoding over both
-    caches give what one prefill of everything gives."""
+@pytest.mark.parametrize("kind", ["bf16", "int4"])
+def test_a_step_of_a_multimodal_server(kind):
+    """Norm and rotation with three axes, append, attention of the chunk, as they are used together: two steps of prompts (text,
+    an image of 5 x 8 patches, text) and decoding, against what the cache holds after each; and q and k as all tokens at once give
+    them."""
     H, Hkv, d, ps = 8, 2, 128, 16
     steps = [[70, 33, 1], [1, 64, 200]]
     total = [sum(x) for x in zip(*steps)]
     table, pages = make_table(total, ps, 1)
-    cache = binding.PagedKVCache.allocate(pages, ps, Hkv, d)
-    half = d // 2
+    cache = binding.PagedKVCache.allocate(pages, ps, Hkv, d, kind)
+    half, text, rows, cols = d // 2, 20, 5, 8
     a = torch.arange(400, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(half, dtype=torch.float64) / half)
     cos, sin = a.cos().float().cuda(), a.sin().float().cuda()
     wq, wk = 1 + 0.1 * torch.rand(d, device="cuda"), 1 + 0.1 * torch.rand(d, device="cuda")
-    past = [0, 0, 0]
-    rows = {"q": [[] for _ in total], "k": [[] for _ in total], "v": [[] for _ in total], "o": [[] for _ in total]}
+    sections = binding.rope_pair_axes((16, 24, 24), turns=kind == "int4")
+
+    def place(p):   # of a sequence's token p: time, row and column
+        if p < text:
+            return p, p, p
+        if p < text + rows * cols:
+            return text, text + (p - text) // cols, text + (p - text) % cols
+        return (p - text - rows * cols + text + cols,) * 3
+
+    def turned(qkv, pos):
+        where = i32(np.array([place(p) for p in pos]).T.copy())
+        return binding.attn_qk_norm_rope_axes(qkv[:, :H], qkv[:, H:H + Hkv], cos, sin, where, sections, wq=wq, wk=wk)
+
+    past, seen = [0, 0, 0], []
     for i, new in enumerate(steps):
         qkv = randn((sum(new), H + 2 * Hkv, d), 9 + i)
-        pos = i32([p + j for p, n in zip(past, new) for j in range(n)])
-        q, k = binding.attn_qk_norm_rope(qkv[:, :H], qkv[:, H:H + Hkv], cos, sin, positions=pos, wq=wq, wk=wk)
-        cu = i32(np.concatenate(([0], np.cumsum(new))))
-        v = qkv[:, H + Hkv:]
-        binding.attn_paged_append(cache, k, v, cu, i32(past), i32(table))
+        pos = [p + j for p, n in zip(past, new) for j in range(n)]
+        q, k = turned(qkv, pos)
+        seen.append((qkv, pos, q, k))
+        cu = np.concatenate(([0], np.cumsum(new)))
+        binding.attn_paged_append(cache, k, qkv[:, H + Hkv:], i32(cu), i32(past), i32(table))
         past = [p + n for p, n in zip(past, new)]
-        o, _ = binding.attn_fwd_paged_varlen(q, cache, i32(table), cu, i32(past))
+        o, lse = binding.attn_fwd_paged_varlen(q, cache, i32(table), i32(cu), i32(past))
         ok()
-        for name, x in (("q", q), ("k", k), ("v", v), ("o", o)):
-            for b, part in enumerate(x.split(new)):
-                rows[name][b].append(part)
-    for b in range(3):
-        q, k, v, o = (torch.cat(rows[x][b]).double() for x in "qkvo")
-        keys, vals = (x.repeat_interleave(H // Hkv, 1) for x in (k, v))
-        S = torch.einsum("ihd,jhd->hij", q, keys) / d ** 0.5
-        S = S.masked_fill(torch.ones(S.shape[1:], device="cuda").triu(1).bool(), -math.inf)
-        P = S.softmax(-1)
-        want, A = torch.einsum("hij,jhd->ihd", P, vals), torch.einsum("hij,jhd->ihd", P, vals.abs())
-        assert ((o - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -11) * A).all()
+        check(q, cu, o, lse, read(cache, table, past), d ** -0.5, True, kind == "int4")
+    q, k = turned(torch.cat([x[0] for x in seen]), [p for x in seen for p in x[1]])
+    assert torch.equal(q, torch.cat([x[2] for x in seen])) and torch.equal(k, torch.cat([x[3] for x in seen]))
+    if kind == "bf16":
+        lo = 0
+        for b, n in enumerate(steps[0]):   # what was appended is what was turned
+            assert torch.equal(read(cache, table, past)[b][0][:n], seen[0][3][lo:lo + n].double())
+            lo += n
