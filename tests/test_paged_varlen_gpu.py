@@ -422,6 +422,89 @@ def test_captured_and_replayed_with_other_lengths():
 
 
 @pytest.mark.parametrize("kind", ["bf16", "int4"])
+def test_pages_beyond_32_bits(kind):
+    """Pages whose bytes lie more than 2^32 from the first one's, for chunks and (4 bits, a batch of 8) single tokens."""
+    d, Hkv, ps, lens, new = 256, 8, 64, [300, 77, 128, 1, 40, 500, 16, 333], [30, 1, 100, 1, 1, 1, 1, 50]
+    row = 2 * d if kind == "bf16" else d // 2
+    first = 2 ** 32 // (ps * Hkv * row) + 3
+    table, pages = make_table(lens, ps, 1)
+    table = np.where(table >= 0, table + first, table)
+    cache = binding.PagedKVCache.allocate(first + pages, ps, Hkv, d, kind)
+    held = write(cache, table, lens, 4)
+    q = randn((sum(new), 2 * Hkv, d), 5)
+    cu = np.concatenate(([0], np.cumsum(new)))
+    o, lse = binding.attn_fwd_paged_varlen(q, cache, i32(table), i32(cu), i32(lens))
+    ok()
+    check(q, cu, o, lse, held, d ** -0.5, True, kind == "int4")
+
+
+def test_captured_with_single_tokens_that_come_and_go():
+    """4 bits, a batch of which some sequences have one token: which ones is known on the GPU only."""
+    lens, d = [300, 77, 128, 1, 40, 500, 16, 33], 64
+    table, pages = make_table(lens, 16, 1)
+    cache = make_cache("int4", pages, 16, 2, d)
+    held = write(cache, table, lens, 4)
+    q = randn((60, 8, d), 5)
+    cu, n, t = i32([0] * 9), i32(lens), i32(table)
+    ws = torch.empty(binding.attn_fwd_paged_varlen_workspace_bytes(cache, 8, 8, 60), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty((8, 60), device="cuda")
+    binding.attn_fwd_paged_varlen(q, cache, t, cu, n, workspace=ws, out=out, lse=lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        binding.attn_fwd_paged_varlen(q, cache, t, cu, n, workspace=ws, out=out, lse=lse)
+    for new in ([1] * 8, [1, 0, 30, 1, 2, 1, 16, 1], [40, 1, 1, 1, 1, 1, 1, 1], [0, 0, 0, 1, 0, 0, 0, 0], [7] * 8):
+        ends = np.concatenate(([0], np.cumsum(new)))
+        cu.copy_(i32(ends))
+        out.fill_(7.0), lse.fill_(7.0)
+        graph.replay()
+        ok()
+        check(q, ends, out, lse, held, d ** -0.5, True, True)
+        assert (out[ends[-1]:] == 7).all() and (lse[:, ends[-1]:] == 7).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int4"])
+def test_two_calls_at_once(kind):
+    """On two streams, each with its own workspace: the bits of each alone."""
+    d, lens, new = 128, [3000, 5, 700, 64, 1, 900, 257, 33, 2000], [200, 1, 70, 1, 1, 130, 1, 9, 1]
+    table, pages = make_table(lens, 16, 1)
+    cache = make_cache(kind, pages, 16, 2, d)
+    write(cache, table, lens, 4)
+    cu, n, t = i32(np.concatenate(([0], np.cumsum(new)))), i32(lens), i32(table)
+    qs = [randn((sum(new), 8, d), 5 + i) for i in range(2)]
+    alone = [binding.attn_fwd_paged_varlen(q, cache, t, cu, n) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    size = binding.attn_fwd_paged_varlen_workspace_bytes(cache, len(new), 8, sum(new))
+    ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in qs]
+    out = [(torch.empty_like(q), torch.empty((8, sum(new)), device="cuda")) for q in qs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, q in enumerate(qs):
+            binding.attn_fwd_paged_varlen(q, cache, t, cu, n, workspace=ws[i], out=out[i][0], lse=out[i][1], stream=streams[i])
+    torch.cuda.synchronize()
+    ok()
+    for got, want in zip(out, alone):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_offsets_of_more_work_than_a_call_may_have():
+    """4096 sequences of the same 65536 rows (and as many whose offsets descend) over 2^31 keys each: nothing is computed, and
+    the status says so."""
+    total, pages = 1 << 16, ((1 << 31) - 1024) // 16
+    cache = make_cache("bf16", 1, 16, 1, 64)
+    q = torch.zeros((total, 1, 64), dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros((1, pages), dtype=torch.int32, device="cuda").expand(8191, -1)
+    cu = torch.tensor([0, total] * 4096, dtype=torch.int32, device="cuda")
+    lens = torch.full((8191,), pages * 16, dtype=torch.int32, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((1, total), 7.0, device="cuda")
+    binding.attn_fwd_paged_varlen(q, cache, table, cu, lens, out=out, lse=lse)
+    st, detail = binding.attn_get_status()
+    binding.attn_clear_status()
+    assert st == binding.ATTN_ERR_INVALID_ARG and detail == 0x2000000D
+    assert (out == 7).all() and (lse == 7).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int4"])
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_as_decode(kind, d):
     """One token of each sequence: what attn_fwd_paged gives, within both calls' bounds."""
