@@ -627,22 +627,24 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
       }
       return s;
     };
-    // Costs of 32 sequences from b0 on: mine, and of all of them up to mine.
-    auto costs = [&](int b0, long long& mine) {
-      int q_base;
-      const UnitWork s = sequence(b0 + lane, q_base);
-      mine = p.c.Hkv * s.upto(s.M);
-      long long upto = mine;
+    // Sequence b0 + lane; work of a kv head of it, of all its heads, and of all 32 sequences up to it.
+    UnitWork s;
+    int q_base;
+    long long per, mine, upto;
+    auto costs = [&](int b0) {
+      s = sequence(b0 + lane, q_base);
+      per = s.upto(s.M);
+      mine = p.c.Hkv * per;
+      upto = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += x;
       }
-      return upto;
     };
     // All work, dealt to the CTAs in equal contiguous shares: mine is [x0, x1).
-    long long W = 0, mine, upto, x0 = 0, x1 = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) upto = costs(b0, mine), W = min(W + __shfl_sync(0xffffffffu, upto, 31), 2 * kMostWork);
+    long long W = 0, x0 = 0, x1 = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) costs(b0), W = min(W + __shfl_sync(0xffffffffu, upto, 31), 2 * kMostWork);
     if (W > kMostWork) {   // the host refuses calls of more: offsets whose sequences share rows
       if (lane == 0) atomicCAS(p.status, 0u, kStatusBadPage);
       W = 0;
@@ -655,23 +657,28 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
       x1 = __shfl_sync(0xffffffffu, x0, 1);
       x0 = __shfl_sync(0xffffffffu, x0, 0);
       // The sequence, kv head and unit that x0 lies in.
-      int b = 0, kvh = 0, m = 0, q_base = 0;
+      int b = 0, kvh = 0, m = 0;
       long long before = 0;
       for (int b0 = 0; b0 < p.B; b0 += 32) {
-        if (p.B > 32) upto = costs(b0, mine);   // else still those of the first look
+        if (p.B > 32) costs(b0);   // else still those of the first look
         const long long all = __shfl_sync(0xffffffffu, upto, 31);
         if (before + all > x0) {
           const int i = __popc(__ballot_sync(0xffffffffu, before + upto <= x0));
           b = b0 + i;
           before += __shfl_sync(0xffffffffu, upto - mine, i);
+          per = __shfl_sync(0xffffffffu, per, i);
+          q_base = __shfl_sync(0xffffffffu, q_base, i);
+          s.nq = __shfl_sync(0xffffffffu, s.nq, i), s.nk = __shfl_sync(0xffffffffu, s.nk, i), s.M = __shfl_sync(0xffffffffu, s.M, i);
           break;
         }
         before += all;
       }
-      UnitWork s = sequence(b, q_base);
       {
-        const long long per = s.upto(s.M), rest = x0 - before;
-        kvh = (int)(rest / per);
+        const long long rest = x0 - before;
+        for (int ended = 32, k0 = 0; ended == 32; k0 += 32) {   // kv heads that end at x0 or before
+          ended = __popc(__ballot_sync(0xffffffffu, (k0 + lane + 1) * per <= rest));
+          kvh += ended;
+        }
         const long long in = rest - kvh * per;
         int n = s.M;   // the last unit that begins at `in` or before
         while (n > 1) {
