@@ -9,7 +9,7 @@
 // Work: units of (sequence, kv head, tiles of positions) times KV tiles. Lengths are known on the GPU only, and differ by orders:
 // so all work, in weighted keys, is dealt to the CTAs, one an SM, in equal contiguous shares, whatever unit their ends fall into. A unit
 // that is cut leaves normalised parts in fp32, at most two a CTA, which a second kernel joins. A chunk of 300 tokens over 65k keys
-// fills the GPU like 34 sequences, and the workspace depends on neither. Finding its share takes a CTA some 3 us.
+// fills the GPU like 34 sequences, and the workspace depends on neither. Finding its share takes a CTA some 2 us.
 //
 // What bounds it (GB300, H 32, Hkv 8, d 128, times of a call in a graph):
 //   bf16, 4 chunks of up to 4096 tokens over 8192: 1195 us, 1620 TFLOP/s (84% of measured). A tile of 2 x 128 rows takes 1.65 us,
@@ -110,7 +110,9 @@ struct PagedVarlenCfg {
 
 constexpr long long kMostWork = 1LL << 52;   // of a call: 64 bits hold it times the number of CTAs
 constexpr int kUnitOverhead = 6 * 128;       // work (see UnitWork) of beginning and ending a unit
-constexpr long long kLeastShare = 8 * 128;   // of a CTA: a share within a unit's beginning would have nothing to do
+// Least work of a CTA: about a tile, since less might lie within a unit's beginning and have nothing to do. 61 tokens over 1000, H 16,
+// Hkv 4, d 64: 13.8 us, with 12 * 128 14.6, with 24 * 128 17.8.
+constexpr long long kLeastShare = 8 * 128;
 
 // Descriptor of an operand without swizzle: 8 x 16-byte core matrices, lbo apart along K, sbo along the rows.
 __device__ __forceinline__ uint64_t make_sdesc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
