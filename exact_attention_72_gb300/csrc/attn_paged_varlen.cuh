@@ -196,6 +196,15 @@ __device__ __forceinline__ void warp_commit(bool on, uint32_t bar) {
       : "memory");
 }
 
+// One lane's arrival, as above.
+__device__ __forceinline__ void warp_arrive(bool on, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n .reg .b64 state;\n setp.ne.b32 q, %1, 0;\n"
+      " @q mbarrier.arrive.shared::cta.b64 state, [%0];\n}\n" ::"r"(bar),
+      "r"((uint32_t)on)
+      : "memory");
+}
+
 // Waits, with a limit, until the copies that a phase counts have landed.
 __device__ __forceinline__ void land(uint64_t* bar, uint32_t phase, unsigned long long timeout_ns) {
   const uint64_t t = global_timer_ns();
@@ -417,10 +426,10 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int thre
       const uint32_t bv = min(max(__reduce_max_sync(0xffffffffu, mv) >> 23, 61u), 254u);
       const float fk = power_of_bits(268u - bk), fv = power_of_bits(268u - bv);
       auto publish = [&](bool keys, bool values) {
-        if (lane != 0) return;
+        // by all lanes: the same value
         if (keys) reinterpret_cast<float*>(s_kf + meta)[w] = power_of_bits(bk - 14u);
         if (values) reinterpret_cast<float*>(s_ve + meta)[w] = (float)((int)bv - 141);
-        mbar_arrive(smem_addr(&bar_meta[meta]));
+        warp_arrive(lane == 0, smem_addr(&bar_meta[meta]));
       };
       // The softmax needs the values' powers before their stage is free. (It has read this slot's last: that tile's PV is done.)
       if (SPLIT && role) publish(false, true);
@@ -483,7 +492,7 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int thre
         if (!SPLIT || step) {
           fence_async_proxy();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(is_v ? &bar_v_full[vs] : &bar_k_full[ks]));
+          warp_arrive(lane == 0, smem_addr(is_v ? &bar_v_full[vs] : &bar_k_full[ks]));
         }
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) now[i] = next[i];
