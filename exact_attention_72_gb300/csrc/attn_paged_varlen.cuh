@@ -199,8 +199,8 @@ __device__ __forceinline__ void warp_commit(bool on, uint32_t bar) {
 // One lane's arrival, as above.
 __device__ __forceinline__ void warp_arrive(bool on, uint32_t bar) {
   asm volatile(
-      "{\n .reg .pred q;\n .reg .b64 state;\n setp.ne.b32 q, %1, 0;\n"
-      " @q mbarrier.arrive.shared::cta.b64 state, [%0];\n}\n" ::"r"(bar),
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar),
       "r"((uint32_t)on)
       : "memory");
 }
@@ -407,7 +407,7 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int thre
     }
     fence_async_proxy();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_addr(bar_q_full));
+    warp_arrive(lane == 0, smem_addr(bar_q_full));
     ++n_q;
 
     for (int j = 0; j < n; ++j, ++n_k) {
@@ -578,7 +578,7 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
   };
   auto release_piece = [&](uint32_t it) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_addr(&bar_piece_empty[it % C::PIECES]));
+    warp_arrive(lane == 0, smem_addr(&bar_piece_empty[it % C::PIECES]));
   };
   auto piece_of_warp = [&](uint32_t it, Piece& pc) {
     if (!wait_piece(it)) return false;
@@ -798,8 +798,8 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
           if (j + 1 == n) warp_commit(on, smem_addr(&bar_o_full[q]));
           warp_commit(on, smem_addr(&bar_v_empty[vs]));
           ++g;
-        } else if (lane == 0) {
-          mbar_arrive(smem_addr(&bar_v_empty[vs]));
+        } else {
+          warp_arrive(lane == 0, smem_addr(&bar_v_empty[vs]));
         }
       }
     }
@@ -955,7 +955,7 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
         auto scores_taken = [&]() {   // S is in registers: its buffer may take the next
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&bar_s_free[sbuf]));
+          warp_arrive(lane == 0, smem_addr(&bar_s_free[sbuf]));
         };
         // P = exp2(s x + ve - m) of 64 keys, in pairs; their sum without the values' powers.
         auto exp_half = [&](const float* x, float s_lo, float s_hi, float e_lo, float e_hi, uint32_t* pk) {
@@ -1007,7 +1007,7 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&bar_p_half[qt][h]));
+          warp_arrive(lane == 0, smem_addr(&bar_p_half[qt][h]));
         };
         // PV_{j-1} reads the last P, and adds to O, which a rescale changes.
         bool pv_done = j == 0;
