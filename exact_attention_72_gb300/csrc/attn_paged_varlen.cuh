@@ -314,11 +314,17 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int thre
     // zero 0 and any codes.
     const int* table = p.table + pc.b * p.table_stride;
     const long long head = pc.kvh * p.c.head_b, sz_head = pc.kvh * p.c.sz_head_b;
+    int page = 0, tok = 0;   // of my key in the tile behind the one that is located; tok < 0: no key
     auto look_up = [&](int t) {
-      const int key = t * 128 + r;
-      return key < nk ? __ldg(table + (uint32_t)key / p.div_page) : -1;
+      const int key = t * 128 + r, i = (uint32_t)min(key, nk - 1) / p.div_page;
+      page = __ldg(table + i);
+      tok = key < nk ? key - i * p.c.page_size : -1;
     };
     uint32_t ksz[GROUPS], vsz[GROUPS];
+    if (SPLIT) {   // a role has one of them
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) ksz[g] = vsz[g] = 0u;
+    }
     auto fetch_pairs = [&](uint32_t (&x)[GROUPS], const uint8_t* from) {
       if constexpr (GROUPS == 1) {
         x[0] = __ldg(reinterpret_cast<const uint32_t*>(from));
@@ -331,19 +337,14 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int thre
       }
     };
     long long at = 0;
-    auto locate = [&](int t, int page) {
-      const int key = t * 128 + r;
-      at = 0;
-#pragma unroll
-      for (int g = 0; g < GROUPS; ++g) ksz[g] = vsz[g] = 0u;
-      if (key >= nk) return;
-      if (page < 0 || page >= p.c.num_pages) {
-        atomicCAS(p.status, 0u, kStatusBadPage);
-        return;
-      }
-      const int tok = key - (int)((uint32_t)key / p.div_page) * p.c.page_size;
-      at = page * p.c.page_b + tok * p.c.token_b + head;
-      const long long sz = page * p.c.sz_page_b + tok * p.c.sz_token_b + sz_head;
+    bool held = false;   // my key of the located tile is there
+    auto locate = [&]() {
+      const bool sound = (uint32_t)page < (uint32_t)p.c.num_pages;
+      if (tok >= 0 && !sound) atomicCAS(p.status, 0u, kStatusBadPage);
+      held = tok >= 0 && sound;
+      const int pg = held ? page : 0, tk = held ? tok : 0;   // else the cache's first row
+      at = pg * p.c.page_b + tk * p.c.token_b + head;
+      const long long sz = pg * p.c.sz_page_b + tk * p.c.sz_token_b + sz_head;
       if (!SPLIT || role == 0) fetch_pairs(ksz, p.c.k_sz + sz);
       if (!SPLIT || role == 1) fetch_pairs(vsz, p.c.v_sz + sz);
     };
@@ -357,10 +358,11 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int thre
         x[4 * i] = u.x, x[4 * i + 1] = u.y, x[4 * i + 2] = u.z, x[4 * i + 3] = u.w;
       }
     };
-    locate(t0, look_up(t0));
+    look_up(t0);
+    locate();
     fetch(now, 0);
     fetch(next, 1);
-    int page = n > 1 ? look_up(t0 + 1) : -1;
+    if (n > 1) look_up(t0 + 1);
 
     // Query rows, once the S products of the last piece have read theirs.
     bool ok = n_q == 0 || mbar_wait(smem_addr(bar_q_empty), (n_q - 1) & 1, ctl, SITE_Q_EMPTY);
@@ -416,6 +418,8 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int thre
       uint32_t mk = 0, mv = 0;
 #pragma unroll
       for (int g = 0; g < GROUPS; ++g) {
+        if (!SPLIT || role == 0) ksz[g] = held ? ksz[g] : 0u;
+        if (!SPLIT || role == 1) vsz[g] = held ? vsz[g] : 0u;
         const float scale = __uint_as_float(ksz[g] << 16), zero = __uint_as_float(ksz[g] & 0xffff0000u);
         mk = max(mk, __float_as_uint(fmaxf(fabsf(scale) * 24.f, fabsf(fmaf(8.f, scale, zero)))));
         const float vscale = __uint_as_float(vsz[g] << 16), vzero = __uint_as_float(vsz[g] & 0xffff0000u);
@@ -459,8 +463,8 @@ __device__ __forceinline__ void unpack_role(const PagedVarlenParams& p, int thre
       }
       // The next tile's pairs, and its row for the codes.
       if (j + 1 < n) {
-        locate(t0 + j + 1, page);
-        if (j + 2 < n) page = look_up(t0 + j + 2);
+        locate();
+        if (j + 2 < n) look_up(t0 + j + 2);
       }
       // One loop for keys and values: the roles' code would not stay in the instruction caches (with both unrolled, 0.8 warps a
       // scheduler waited for instructions at any time).
