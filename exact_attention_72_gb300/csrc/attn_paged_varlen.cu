@@ -74,10 +74,10 @@ cudaError_t launch(const PagedVarlenLaunch& a, cudaStream_t s) {
                           0, s, a.params);
 }
 
-// Over 4-bit caches a chunk's kernel unpacks every key for its tensor cores, 2.5 us a tile of 128 whatever its rows, where the
+// Over 4-bit caches a chunk's kernel unpacks every key for its tensor cores, 2.3 us a tile of 128 whatever its rows, where the
 // kernel of attn_fwd_paged multiplies the codes as they are. It takes sequences of one token (of at most kSinglesRows rows a kv
 // head, which read the cache once) in batches of kSinglesBatch and more; in smaller ones its two launches, 4 us if there is no such
-// sequence, may cost more than they save. B 30, up to 16384 keys, H 32, Hkv 8, d 128: 413 us unpacked, 97 so.
+// sequence, may cost more than they save. B 30, up to 16384 keys, H 32, Hkv 8, d 128: 376 us unpacked, 106 so.
 constexpr int kSinglesRows = 16, kSinglesBatch = 8;
 
 int unit_rows(int d) { return d <= 128 ? 256 : 128; }

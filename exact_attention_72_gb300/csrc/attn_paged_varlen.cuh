@@ -12,7 +12,7 @@
 // fills the GPU like 34 sequences, and the workspace depends on neither. Finding its share takes a CTA some 2 us.
 //
 // What bounds it (GB300, H 32, Hkv 8, d 128, times of a call in a graph):
-//   bf16, 4 chunks of up to 4096 tokens over 8192: 1195 us, 1620 TFLOP/s (84% of measured). A tile of 2 x 128 rows takes 1.65 us,
+//   bf16, 4 chunks of up to 4096 tokens over 8192: 1183 us, 1640 TFLOP/s (85% of measured). A tile of 2 x 128 rows takes 1.65 us,
 //     in which the tensor core waits for the softmax of the one buffer of scores; 1509 us at first: copies issued by four warps,
 //     MMAs by warps that run as one, and maxima taken by the loads of the scores made it so.
 //   bf16, 30 decoding sequences of up to 16k keys: 245 us, 6150 GB/s (90%). A CTA by itself takes 1.2 us a tile, 64 KB that come 2 us after
@@ -20,7 +20,8 @@
 //     slower), nor both tiles' warps on one unit made it faster.
 //   bf16, d 256: 5 sequences, 777 tokens over 5000, H 16, Hkv 4: 149 us. 128 KB of keys and values for 128 rows come out of the
 //     L2 at 40 bytes a cycle and SM, 11.5 TB/s in all. Halves of keys in more stages: 155 us.
-//   4 bits, the first case: 1840 us. Unpacking, 2.5 us a tile of 128 keys and values by 4 warps; see unpack_role.
+//   4 bits, the first case: 1676 us. Unpacking, 2.3 us a tile of 128 keys and values by 4 warps; see unpack_role. (1833 us with a
+//     branch around each arrival, which only one lane makes.)
 #pragma once
 #include <cuda_fp16.h>
 
@@ -277,7 +278,7 @@ __device__ __forceinline__ void load_role(const PagedVarlenParams& p, int half, 
 
 // The 4-bit cache's operands. Thread r of the warpgroup has query row r of each Q tile and key r of each KV tile; at d = 256 one
 // warpgroup has the keys and one the values, and each half of the query rows: with one stage of each, values that wait for their stage
-// must not hold up the next keys (5 sequences of up to 777 over 5000 tokens, 16 heads on 4: 237 us, in turns 292).
+// must not hold up the next keys (5 sequences of up to 777 over 5000 tokens, 16 heads on 4: 219 us; in turns, with branches, 292, each for itself 237).
 //
 // A code in the high bits of fp16's mantissa is 1 + c / 16: a shift and a three-input logic operation, and a fused multiply-add makes
 // the operand of it.
