@@ -581,6 +581,11 @@ def rope_pair_axes(sections, turns: bool = False) -> bytes:
     return bytes(a for i in range(max(sections, default=0)) for a, n in enumerate(sections) if i < n)
 
 
+def _pair_axis(x) -> bytes:
+    """The axis of every pair, element by element: bytes() of a whole number would be as many zeros, and of an array its memory."""
+    return x if type(x) is bytes else bytes(iter(x))
+
+
 def attn_qk_norm_rope_axes(q, k, cos, sin, positions, pair_axis, wq=None, wk=None, eps: float = 1e-6, norm: bool = True,
                            interleaved: bool = False, q_out=None, k_out=None, stream=None):
     """attn_qk_norm_rope with positions on several axes (time, height, width): (q_out, k_out).
@@ -590,7 +595,7 @@ def attn_qk_norm_rope_axes(q, k, cos, sin, positions, pair_axis, wq=None, wk=Non
     of pairs of each axis. The rest as attn_qk_norm_rope; k may be None.
     """
     call = (_CALLS or _calls()).qk_norm_rope
-    axes = pair_axis if type(pair_axis) is bytes else bytes(pair_axis)
+    axes = _pair_axis(pair_axis)
     if stream is not None:
         return _on(stream, call, q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, axes, q_out, k_out)
     return call(q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, axes, q_out, k_out)
@@ -601,7 +606,7 @@ def attn_qk_norm_rope_axes_bwd(q, k, dq_out, dk_out, cos, sin, positions, pair_a
                                workspace=None, stream=None):
     """Gradients (dq, dk, dwq, dwk) of attn_qk_norm_rope_axes, as attn_qk_norm_rope_bwd gives them."""
     call = (_CALLS or _calls()).qk_norm_rope_bwd
-    axes = pair_axis if type(pair_axis) is bytes else bytes(pair_axis)
+    axes = _pair_axis(pair_axis)
     if stream is not None:
         return _on(stream, call, q, k, cos, sin, positions, wq, wk, eps, norm, interleaved, axes, dq_out, dk_out, dq, dk, dwq,
                    dwk, workspace)

@@ -1,8 +1,11 @@
 """Refusals of norm and rotation with several axes and of attention of chunks over the paged cache that need no GPU: every bad
 argument is turned away before any CUDA call. Addresses are made up and never read."""
 import ctypes
+import types
 
+import numpy as np
 import pytest
+import torch
 
 from exact_attention_72_gb300 import binding, build
 
@@ -107,3 +110,23 @@ def test_workspace_sizes(lib):
     for bad in ((0, 8, 2, 10, 128, 0), (1, 7, 2, 10, 128, 0), (1, 8, 0, 10, 128, 0), (1, 8, 2, -1, 128, 0), (1, 8, 2, 10, 96, 0),
                 (1, 8, 2, 10, 128, 2)):
         assert n(*bad) == 0
+
+
+@pytest.mark.parametrize("bad", [64, 3, True, 1.5, None, "0" * 64, [0.0] * 64, np.zeros(64)])
+def test_pair_axis_is_a_sequence_of_whole_numbers(bad, monkeypatch):
+    """bytes(64) would be 64 pairs of axis 0."""
+    monkeypatch.setattr(binding, "_CALLS", types.SimpleNamespace(qk_norm_rope=None, qk_norm_rope_bwd=None))
+    with pytest.raises(TypeError, match="iterable|interpreted as an integer"):
+        binding.attn_qk_norm_rope_axes(None, None, None, None, None, bad)
+    with pytest.raises(TypeError, match="iterable|interpreted as an integer"):
+        binding.attn_qk_norm_rope_axes_bwd(None, None, None, None, None, None, None, bad)
+
+
+@pytest.mark.parametrize("kind", [bytes, bytearray, list, tuple, iter, np.array, lambda x: np.array(x, np.uint8), torch.tensor])
+def test_pair_axis_by_elements(kind, monkeypatch):
+    """Arrays count by their elements, not by the bytes that hold them: 8 numbers of 64 bits are not 64 axes."""
+    axes = [0, 1, 2, 0, 1, 2, 1, 0]
+    calls = types.SimpleNamespace(qk_norm_rope=lambda *a: a[10], qk_norm_rope_bwd=lambda *a: a[10])
+    monkeypatch.setattr(binding, "_CALLS", calls)
+    assert binding.attn_qk_norm_rope_axes(None, None, None, None, None, kind(axes)) == bytes(axes)
+    assert binding.attn_qk_norm_rope_axes_bwd(None, None, None, None, None, None, None, kind(axes)) == bytes(axes)
