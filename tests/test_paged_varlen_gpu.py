@@ -588,3 +588,46 @@ def test_a_step_of_a_multimodal_server(kind):
         for b, n in enumerate(steps[0]):   # what was appended is what was turned
             assert torch.equal(read(cache, table, past)[b][0][:n], seen[0][3][lo:lo + n].double())
             lo += n
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int4"])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("d,H,Hkv,new", [(64, 32, 2, 1225), (128, 32, 2, 1225), (256, 32, 2, 1225), (256, 128, 1, 1030)])
+def test_many_units_of_a_head(kind, causal, d, H, Hkv, new):
+    """More units of a (sequence, kv head) than a warp has lanes, and than the square of that: 77 units of 16 positions (step 3 of
+    the search, which 77 is no multiple of), 154 of 8 (step 5), 1030 of one (33, then 2). Shares begin in all of them."""
+    case_of(kind, d, H, Hkv, 16, [new], [10], causal=causal)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int4"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_kv_heads(kind, d):
+    """Shares that begin in kv heads behind the 32nd and the 64th; single tokens of such a batch."""
+    case_of(kind, d, 134, 67, 16, [5, 40], [300, 20])
+    case_of(kind, d, 40, 40, 16, [1, 1, 30, 1, 0, 2, 1, 1, 1], [700, 5, 90, 33, 8, 0, 1200, 31, 0])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int4"])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("d,G", [(64, 3), (128, 3), (256, 3), (64, 6), (128, 6), (256, 6), (64, 12), (128, 12), (256, 12)])
+def test_masks_and_scales_of_single_tokens_among_chunks(kind, causal, d, G):
+    """Over 4 bits the two kernels of one call agree on the sign of the scale and on the mask. Single tokens' scores there are
+    sums of |zero| and scale times code apart: their dS is of |q| times the two."""
+    new, past = [1, 70, 1, 3, 1, 1, 0, 1, 130, 1], [60, 0, 500, 9, -1, 0, 40, 1100, 333, 31]
+    ends = [n + p for n, p in zip(new, past)]
+    table, pages = make_table(ends, 16, 3)
+    cache = make_cache(kind, pages, 16, 2, d)
+    held = write(cache, table, ends, 4)
+    if kind == "int4":
+        for b, (keys, vals, ksize, vsize, vbase) in enumerate(held):
+            if new[b] == 1 and ends[b]:
+                pos = np.arange(ends[b])
+                pg, at = torch.tensor(table[b][pos // 16].astype(np.int64)).cuda(), torch.tensor(pos % 16).cuda()
+                zero = cache.k_sz[pg, at][..., 1].double().repeat_interleave(64, -1)
+                held[b] = keys, vals, torch.maximum(ksize, zero.abs() + (keys - zero).abs()), vsize, vbase
+    cu = np.concatenate(([0], np.cumsum(new)))
+    q = randn((int(cu[-1]), 2 * G, d), 5, 2.0)
+    for scale in (d ** -0.5, -0.05, 1.5):
+        o, lse = binding.attn_fwd_paged_varlen(q, cache, i32(table), i32(cu), i32(ends), causal=causal, scale=scale)
+        ok()
+        check(q, cu, o, lse, held, scale, causal, kind == "int4")
