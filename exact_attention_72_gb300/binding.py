@@ -726,7 +726,8 @@ def attn_fwd_paged_varlen(q, cache: PagedKVCache, page_table, cu_seqlens_q, seql
 
     ``seqlens`` (int32 [B]) counts each sequence's keys, its new tokens' own among them (append them first); with
     ``causal`` query i of n sees keys j <= i + seqlens[b] - n. Chunks may have any length, one token (a decoding
-    sequence) or none. Rows that see no key give 0 and -inf; rows from cu_seqlens_q[B] on are left as they were.
+    sequence) or none. Rows that see no key give 0 and -inf; rows from cu_seqlens_q[B] on are left as they were. The same
+    call gives the same bits; a sequence's last bits may change with the other lengths of its batch.
     ``workspace`` (CUDA uint8, at least attn_fwd_paged_varlen_workspace_bytes(...)) is allocated here with torch if not
     given; where every chunk is one or a few tokens of a short row, attn_fwd_paged is faster.
     """

@@ -76,8 +76,12 @@ cudaError_t launch(const PagedVarlenLaunch& a, cudaStream_t s) {
 
 // Over 4-bit caches a chunk's kernel unpacks every key for its tensor cores, 2.3 us a tile of 128 whatever its rows, where the
 // kernel of attn_fwd_paged multiplies the codes as they are. It takes sequences of one token (of at most kSinglesRows rows a kv
-// head, which read the cache once) in batches of kSinglesBatch and more; in smaller ones its two launches, 4 us if there is no such
-// sequence, may cost more than they save. B 30, up to 16384 keys, H 32, Hkv 8, d 128: 376 us unpacked, 106 so.
+// head, which read the cache once) in batches of kSinglesBatch and more. Which sequences have one token is known on the GPU only, and
+// its two launches cost 8 to 10 us if there is none: so a rule on the size of the batch, where single tokens are likely, and neither
+// side of it is always right. H 32, Hkv 8, d 128, us unpacked and so:
+//   all single tokens:  B 30, up to 16384 keys 367, 106;  B 8, 8000 keys 69, 36, 500 keys 24 to 26, 26
+//     below the rule:   B 4, 65536 keys 224, 73;  B 7 384, 110;  B 4, 8000 keys 42, 32;  up to 2000 keys 24 to 32, 24 to 30
+//   no single token:    8 chunks of 4 over 500 keys 28, 36;  of 60 over 2000 58, 67;  30 of 100 over 8000 443, 454
 constexpr int kSinglesRows = 16, kSinglesBatch = 8;
 
 int unit_rows(int d) { return d <= 128 ? 256 : 128; }

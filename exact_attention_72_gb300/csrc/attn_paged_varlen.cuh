@@ -12,10 +12,13 @@
 // fills the GPU like 34 sequences, and the workspace depends on neither. Finding its share takes a CTA some 2 us.
 //
 // What bounds it (GB300, H 32, Hkv 8, d 128, times of a call in a graph):
-//   bf16, 4 chunks of up to 4096 tokens over 8192: 1183 us, 1640 TFLOP/s (85% of measured). A tile of 2 x 128 rows takes 1.65 us,
-//     in which the tensor core waits for the softmax of the one buffer of scores; 1509 us at first: copies issued by four warps,
-//     MMAs by warps that run as one, and maxima taken by the loads of the scores made it so.
-//   bf16, 30 decoding sequences of up to 16k keys: 245 us, 6150 GB/s (90%). A CTA by itself takes 1.2 us a tile, 64 KB that come 2 us after
+//   bf16, 4 chunks of up to 4096 tokens over 8192: 1183 us, 1640 TFLOP/s (85% of measured; another card 1230), and 1380 in calls
+//     without a pause, at the power cap. A tile of 2 x 128 rows takes 1.65 us, in which the tensor core waits for the softmax of the
+//     one buffer of scores; 1509 us at first: copies issued by four warps, MMAs by warps that run as one, and maxima taken by the
+//     loads of the scores made it so.
+//   the same at d 64: 923 us, 1050 TFLOP/s (54%). Exponentials take 46% of the special-function units and products as much of the
+//     tensor pipe; 54% of the issue slots are taken: as many scores a tile as at d = 128, for half the products.
+//   bf16, 30 decoding sequences of up to 16k keys: 243 us, 6200 GB/s (91%). A CTA by itself takes 1.2 us a tile, 64 KB that come 2 us after
 //     their copy was issued; with fewer CTAs at it neither a fifth stage, tiles fetched into the L2 ahead (they take the copies' turns: 20%
 //     slower), nor both tiles' warps on one unit made it faster.
 //   bf16, d 256: 5 sequences, 777 tokens over 5000, H 16, Hkv 4: 149 us. 128 KB of keys and values for 128 rows come out of the
@@ -48,7 +51,7 @@ struct PagedVarlenParams {
   // Parts of cut units: slot 2c the one that CTA c continues, 2c + 1 the one that it begins and does not end.
   float* part_o;            // [2 CTAs, ROWS, D] normalised O
   float* part_lse;          // [2 CTAs, ROWS] log2-sum-exp2
-  int4* cut;                // [CTAs, 2]: (first packed row, kv head, positions, parts) of the unit that CTA c begins; parts 0: none
+  int4* cut;                // [CTAs]: (first packed row, kv head, positions, parts) of the unit that CTA c begins; parts 0: none
   int o_v8;                 // rows of o are 32-byte aligned
   uint32_t* status;
   unsigned long long timeout_ns;
@@ -70,7 +73,7 @@ struct Piece {
 template <int D_, bool INT4_>
 struct PagedVarlenCfg {
   static constexpr int D = D_;
-  static constexpr bool INT4 = INT4_, FP8 = false;
+  static constexpr bool INT4 = INT4_;
   static constexpr int NQ = D <= 128 ? 2 : 1;             // 128-row Q tiles of a CTA
   static constexpr int ROWS = 128 * NQ;                   // rows of a unit
   // Operands: 16-bit, K-major (V: MN-major) tiles of 128 rows in chunks of 64 columns with the 128-byte swizzle.
@@ -287,8 +290,10 @@ __device__ __forceinline__ void load_role(const PagedVarlenParams& p, int half, 
 // more columns,
 //   zero' sum(q) = (zh + zl) (Qh + Ql),    zh + zl and Qh + Ql the two values in 22 bits each.
 // So S is what fp32 would give. In bf16 the keys would be 2^-8 off, and LSE with them (2e-5 of it over 1000 keys).
-// Values: 16 scale (1 + c / 16) + (zero - 16 scale), the sum and its second term rounded to fp16, 2^-11 off each, as P is; in bf16
-// the two would add as much to O's error as its own rounding.
+// Values: 16 scale (1 + c / 16) + (zero - 16 scale), the sum and its second term rounded to fp16: off by 2^-11 of the value and by
+// 2^-11 |zero - 16 scale|, which for a group around zero (zero = -7.5 scale) is 3 * 2^-11 of its greatest value, and the same for all
+// values of a group, whatever their size. With P's 2^-11, O's error is 0.0017 of its norm, as that of its own rounding alone; in
+// bf16 the two would add as much again.
 // fp16's range: every 32 keys (a warp's) of a tile are divided by a power of two that brings the greatest of them below 2^15, a
 // query row by one that brings its greatest value into [2^7, 2^8). Full precision is left to values 2^-29 of the greatest of
 // their 32 keys (query rows: 2^-21), others are off by 2^-40 (2^-33) of it. The softmax puts the keys' power back into the
@@ -567,7 +572,7 @@ attn_paged_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
   __syncthreads();
   tc_fence_after();
   griddep_wait();   // launched early: what it reads may be a previous kernel's
-  griddep_launch_dependents();   // the joining kernel's CTAs may wait beside these, all of which run by now
+  griddep_launch_dependents();   // the joining kernel's CTAs come where these end (each has nearly all registers of its SM)
   const uint32_t tmem = tmem_slot;
   const int PG = p.P * p.G, RP = p.P * NQ;
 

@@ -170,8 +170,8 @@ struct Positions {
   int v[AXES == kAxesOfLane ? 4 : 1];   // of this lane's pairs; v[0] = -1: nothing to store
 };
 
-// Positions of token t for a lane of its row of LPR; all -1 where one that some pair turns by lies outside the tables. mine: the axes of
-// the lane's pairs. With several axes the lanes of a row agree by a vote.
+// Positions of token t for a lane of its row of LPR; v[0] = -1 in every lane of the row where one that some pair turns by lies
+// outside the tables. mine: the axes of the lane's pairs. With several axes the lanes of a row agree by a vote.
 template <Axis AXES, int LPR>
 __device__ __forceinline__ Positions<AXES> position(const NormRopeParams& p, int t, uint32_t mine, int l) {
   Positions<AXES> r;

@@ -516,7 +516,8 @@ attn_status_t attn_paged_gather(const attn_paged_cache_t* cache, void* k, void* 
  *      graphs included) need one each. q, o, lse and workspace must not overlap each other or the cache.
  * Lengths stay on the device: the call can be captured and replayed while they grow. Every call reads
  * its keys and values ceil(Nq (H / Hkv) / R) times, R = 8 query rows, or 16 when there are more than 8
- * and d <= 128. Deterministic. Two programmatic dependent launches; allocates nothing.
+ * and d <= 128. Deterministic: the same call gives the same bits; where work is cut follows from all lengths, so that a
+ * sequence's last bits may change with the others' lengths. Two programmatic dependent launches; allocates nothing.
  * UNSUPPORTED as for the cache, for scale == 0, and for max_pages * page_size >= 2^31 - 1023 or
  * B * Hkv * row blocks * (tiles of 16 keys + 8; in 4 bits, of 32 keys + 4) >= 2^31.
  */
@@ -543,9 +544,12 @@ attn_status_t attn_fwd_paged(const void* q, const attn_paged_cache_t* cache, voi
  * Offsets and lengths stay on the device: the call can be captured and replayed with others. A sequence whose offsets do
  * not ascend or pass total_q has no rows; pages and lengths out of range as above; each is reported by attn_get_status.
  * Over 4-bit caches q, keys and values are held in fp16 times powers of two (of a query row; of 32 neighbouring keys):
- * below 2^-21 of a row's, or 2^-29 of 32 keys', greatest value they lose bits. Sequences of one token in a
- * batch of 8 and more go to attn_fwd_paged's kernel there (H / Hkv <= 16). Deterministic. Two programmatic dependent launches, four
- * with those; allocates nothing; total_q == 0 returns ATTN_OK at once.
+ * below 2^-21 of a row's, or 2^-29 of 32 keys', greatest value they lose bits. Keys are otherwise off by
+ * 2^-22 |zero + 8 scale|, values by 2^-11 of themselves and 2^-11 |zero - 16 scale|. In batches of 8 and more sequences those of
+ * one token are computed by attn_fwd_paged's kernel there (H / Hkv <= 16; unless their tiles would pass 2^31).
+ * Deterministic: the same call gives the same bits; where work is cut follows from all lengths, and who computes a single token
+ * from B, so that a sequence's last bits may change with the batch it is in. Two programmatic dependent launches (one
+ * where the sizes leave the work of one CTA), two more in such batches; allocates nothing; total_q == 0 returns ATTN_OK at once.
  * UNSUPPORTED as for the cache, for scale == 0, H / Hkv > 128, total_q or max_pages * page_size >= 2^31 - 1023, strides
  * of a bf16 cache that tensor maps do not take (2^40 bytes and more, or 0 between two rows), and for more than 2^50 / Hkv
  * keys over all blocks of 128 or 256 query rows.
